@@ -105,7 +105,7 @@ def _groups(x):
 
 def _quantise(x, bits, wide=torch.float32):
     """lo and step (as fp16 numbers) and codes of x [..., hd], each by group of 32, in `wide` arithmetic."""
-    x = _groups(x.to(wide)).clamp(-65504.0, 65504.0)
+    x = _groups(x.to(wide)).clamp(-60000.0, 60000.0)
     lo = x.amin(-1, keepdim=True).half().to(wide)
     step = ((x.amax(-1, keepdim=True) - lo) / (2 ** bits - 1)).half().to(wide)
     code = torch.where(step > 0, (x - lo) / step, torch.zeros_like(x)).round().clamp(0, 2 ** bits - 1)
