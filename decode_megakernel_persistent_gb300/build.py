@@ -1,6 +1,6 @@
 """Build libll.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Five translation units are compiled in parallel and linked into
+Its translation units are compiled in parallel and linked into
 ``decode_megakernel_persistent_gb300/libll.so`` with the CUDA runtime linked
 statically, so the library needs nothing but the driver at run time.
 """
@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libll.so")
 SOURCES = ("mk_cuda_cores.cu", "mk_tensor_cores.cu", "mk_geo.cu", "chain.cu", "schedule.cpp", "api.cpp",
-           "static_step.cu", "prefill.cu")
+           "static_step.cu", "prefill.cu", "kvq.cu", "kvq_attn.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

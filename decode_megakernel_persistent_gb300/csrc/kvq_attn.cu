@@ -1,0 +1,926 @@
+// kvq_attn.cu -- attention over the packed KV cache.
+//
+// One pass over the positions with the running maximum and sum of a softmax: a
+// tile of keys gives scores S = Q K^T, the maximum m grows where they pass it,
+// P = exp(S - m) adds to the sum l and to O = P V, and O / l is the output. K and
+// V rows come packed; they become fp16 numbers in registers, exactly the values
+// the format defines, on their way to the tensor cores.
+//
+// Two kernels share the work by the number of query rows a KV head has (its
+// query heads times the call's tokens): k_kvq_decode for up to 16, where the
+// packed bytes bound the time, and k_kvq_chunk for more.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kvq.cuh"
+#include "kvq.h"
+#include "ll_internal.h"
+
+namespace ll {
+namespace {
+
+namespace cg = cooperative_groups;
+
+struct AttnArgs {
+    const uint8_t *kc, *vc;
+    const uint32_t *kp, *vp;
+    int64_t seq_rows;
+    int32_t max_seq, group;
+    KvqLens l;
+    const void *q;
+    int64_t q_seq, q_tok, q_head;
+    float scale_log2;  // scale * log2(e): scores in log2 units, probabilities by exp2
+    KvqOut out;
+};
+
+// The running maximum of a row moves only once a score passes it by this (log2
+// units): until then probabilities are taken against the held maximum, at most
+// 2^8, well inside fp16, and neither l nor O needs rescaling.
+constexpr float HOLD = 8.f;
+
+__device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// BYTES (16 or 8) to shared memory, or zeros when !ok.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool ok) {
+    const int n = ok ? BYTES : 0;
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D += A B: A 16 x 16 (row), B 16 x 8 (col), fp16 in, fp32 sums.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values held as an mma fragment, transposed.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return kvq_u32(__floats2half2_rn(lo, hi)); }
+
+__device__ __forceinline__ float q_at(const float *p) { return *p; }
+__device__ __forceinline__ float q_at(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// The power of two that brings a row whose largest magnitude is mx into [1, 2)
+// (fp16 then holds 11 bits of every value that matters to a product; a bf16 q is
+// exact but for values 2^-14 of the largest), and its inverse.
+__device__ __forceinline__ void row_scale(float mx, float &down, float &up) {
+    int e = int((__float_as_uint(mx) >> 23) & 255u) - 127;
+    e = mx > 0.f ? min(max(e, -126), 126) : 0;
+    down = __uint_as_float(uint32_t(127 - e) << 23);
+    up = __uint_as_float(uint32_t(127 + e) << 23);
+}
+
+// Two neighbouring values (dims d, d + 1) of a token's head.
+__device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head, int d, float a, float b) {
+    const int64_t at = s * o.seq + j * o.token + head * o.head + d;
+    if (o.f32) {
+        *reinterpret_cast<float2 *>(o.f32 + at) = make_float2(a, b);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        if (!o.t[i]) break;
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        *reinterpret_cast<__nv_bfloat162 *>(o.t[i] + at) = v;
+        a -= __low2float(v);
+        b -= __high2float(v);
+    }
+}
+
+// ---- few query rows: one warp per run of keys --------------------------------------
+//
+// Grid (splits, KV heads, sequences), the splits of a (sequence, KV head) one
+// cluster. A block's keys are cut into tiles; its warps take them in turn, each
+// with a ring of its own in shared memory (cp.async, no block barriers), and
+// its own m, l and O. At the end the warps of a block, then the blocks of the
+// cluster (through distributed shared memory), merge.
+//
+// A tile of 16 keys is the A operand of S^T = K Q^T (keys x rows, 8 query rows per
+// product) and, transposed, of O^T = V^T P^T (dims x rows): with the keys as the
+// operand's 16 rows, every code is unpacked once whatever the number of query
+// rows, and few rows cost few products. A group of 4 dims by 8 lanes is how the
+// format lays a row out: lane (g, t) finds the dims of its K fragment (k = 2t, 2t +
+// 1, 2t + 8, 2t + 9 of each product, in an order of our own that Q's fragment
+// shares) in cells 2t and 2t + 1, and those of its V fragment in cell g.
+template <int BITS, int HD>
+struct DecodeShape {
+    static constexpr int NW = 8;
+    static constexpr int RB = HD * BITS / 8, PB = HD / 8;        // bytes of a row's codes and parameters
+    static constexpr int TILE = RB == 128 ? 16 : 32;             // keys
+    static constexpr int STAGE = TILE * 2 * (RB + PB);
+    static constexpr int STAGES = 104 * 1024 / (NW * STAGE) < 4 ? 104 * 1024 / (NW * STAGE) : 4;  // two blocks per SM
+    static constexpr int SMEM = NW * STAGES * STAGE;
+    static_assert(STAGES >= 2, "a ring needs two stages");
+};
+
+// The key of a block of 8 that is row r of the operand: rows 2t are keys 0..3 and
+// rows 2t + 1 keys 7..4, which spreads both the K reads (rows g) and the V reads
+// (rows 2t, then 2t + 1) over all banks.
+__device__ __forceinline__ int key_of(int r) { return r & 1 ? 7 - (r >> 1) : r >> 1; }
+
+// 16-byte chunk c of row r in a ring stage.
+template <int RB>
+__device__ __forceinline__ int swz(int r, int c) {
+    return RB == 32 ? c : RB == 64 ? c ^ (r & 2) : c ^ (((r & 3) << 1) | ((r >> 2) & 1));
+}
+
+template <int BITS, int HD, int NC, typename QT>
+__global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ AttnArgs a) {
+    using S = DecodeShape<BITS, HD>;
+    constexpr int NW = S::NW, RB = S::RB, PB = S::PB, TILE = S::TILE, NT = TILE / 16, GR = HD / 32, COLS = 8 * NC;
+    constexpr int CH = RB / 16;
+    static_assert(NW * COLS * HD * 4 <= S::SMEM, "the merge fits in the ring's memory");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float s_ml[NW][COLS][2];  // the warps' m and l
+    __shared__ float s_cml[COLS][2];     // the block's
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int s = blockIdx.z, h = blockIdx.y, C = gridDim.x, rank = blockIdx.x;
+    const int n = a.l.n(s), len = a.l.len(s);
+    if (n == 0) return;
+    const int rows = n * a.group, first = len - n;  // query rows, and the first token's position
+    const int limit = min(len, a.max_seq);          // no token sees a position from here on
+    const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
+
+    // this block's tiles
+    const int tiles = (limit + TILE - 1) / TILE;
+    const int t0 = int(int64_t(tiles) * rank / C), t1 = int(int64_t(tiles) * (rank + 1) / C);
+    uint8_t *const ring = smem + warp * (S::STAGES * S::STAGE);
+    auto load = [&](int ti, int stage) {
+        const int k0 = ti * TILE, valid = limit - k0;
+        const uint32_t dst = sptr(ring + stage * S::STAGE);
+        const uint8_t *kc = a.kc + (row0 + k0) * RB, *vc = a.vc + (row0 + k0) * RB;
+#pragma unroll
+        for (int i = lane; i < TILE * CH; i += 32) {
+            const int r = i / CH, c = i % CH;
+            const bool ok = r < valid;
+            const int64_t src = ok ? i * 16 : 0;
+            const uint32_t to = dst + r * RB + swz<RB>(r, c) * 16;
+            cp_async<16>(to, kc + src, ok);
+            cp_async<16>(to + TILE * RB, vc + src, ok);
+        }
+        if (lane < TILE) {
+            const bool ok = lane < valid;
+            const int64_t src = (row0 + k0 + (ok ? lane : 0)) * GR;
+            cp_async<PB>(dst + 2 * TILE * RB + lane * PB, a.kp + src, ok);
+            cp_async<PB>(dst + 2 * TILE * RB + TILE * PB + lane * PB, a.vp + src, ok);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < S::STAGES - 1; i++) {
+        if (t0 + warp + i * NW < t1) load(t0 + warp + i * NW, i);
+        cp_commit();
+    }
+
+    // q as B fragments: k-step (gr, ks), row col = 8 nc + g: its dims 32 gr + 8 t + 2 ks (+ 4, + 1, + 5)
+    uint32_t qf[NC][GR][2][2];
+    float fac[NC][2];  // log2 score units per product unit, of rows 8 nc + 2 t and + 1
+    int last[NC][2];   // the last position those rows see
+#pragma unroll
+    for (int nc = 0; nc < NC; nc++) {
+        const int r = 8 * nc + g;
+        float v[GR][8], mx = 0.f;
+        if (r < rows) {
+            const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + (r / a.group) * a.q_tok +
+                          (h * a.group + r % a.group) * a.q_head + 8 * t;
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[gr][i] = q_at(q + 32 * gr + i);
+        } else {
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[gr][i] = 0.f;
+        }
+#pragma unroll
+        for (int gr = 0; gr < GR; gr++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) mx = fmaxf(mx, fabsf(v[gr][i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float down, up;
+        row_scale(mx, down, up);
+        up *= a.scale_log2;
+        fac[nc][0] = __shfl_sync(0xffffffffu, up, 8 * t);
+        fac[nc][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+        last[nc][0] = first + (8 * nc + 2 * t) / a.group;
+        last[nc][1] = first + (8 * nc + 2 * t + 1) / a.group;
+#pragma unroll
+        for (int gr = 0; gr < GR; gr++)
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                qf[nc][gr][ks][0] = pack_h2(v[gr][2 * ks] * down, v[gr][2 * ks + 4] * down);
+                qf[nc][gr][ks][1] = pack_h2(v[gr][2 * ks + 1] * down, v[gr][2 * ks + 5] * down);
+            }
+    }
+
+    float o[NC][2 * GR][4], m[NC][2], l[NC][2];
+#pragma unroll
+    for (int nc = 0; nc < NC; nc++) {
+#pragma unroll
+        for (int i = 0; i < 2 * GR; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[nc][i][e] = 0.f;
+        m[nc][0] = m[nc][1] = -INFINITY;
+        l[nc][0] = l[nc][1] = 0.f;
+    }
+
+    int stage = 0;
+    for (int ti = t0 + warp; ti < t1; ti += NW) {
+        cp_wait<S::STAGES - 2>();
+        __syncwarp();  // the tile is here for every lane, and every lane is done with the tile before
+        {
+            const int ahead = ti + (S::STAGES - 1) * NW;
+            if (ahead < t1) load(ahead, stage == 0 ? S::STAGES - 1 : stage - 1);
+            cp_commit();
+        }
+        const uint8_t *kt = ring + stage * S::STAGE, *vt = kt + TILE * RB;
+        const uint32_t *kpar = reinterpret_cast<const uint32_t *>(vt + TILE * RB), *vpar = kpar + TILE * GR;
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+
+        // A tile in which some row's last position lies (or the tile's zeros begin).
+        // V rows holding a NaN there must reach only the rows that see them: they
+        // enter the product as zeros, and the rows that see them get NaN below.
+        const int k0 = ti * TILE;
+        const bool edge = k0 + TILE > min(first + 1, limit);
+        uint32_t v_nan[GR];
+        if (edge) {
+            uint32_t *const vp = const_cast<uint32_t *>(vpar);
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++) {
+                const bool nan = lane < TILE && kvq_is_nan(vp[lane * GR + gr]);
+                v_nan[gr] = __ballot_sync(0xffffffffu, nan);
+                if (nan) vp[lane * GR + gr] = 0u;
+            }
+            __syncwarp();
+        }
+
+        float sc[NT][NC][4];
+#pragma unroll
+        for (int mt = 0; mt < NT; mt++) {
+#pragma unroll
+            for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[mt][nc][e] = 0.f;
+            // this lane's quarter of rows g and g + 8: cells 2t and 2t + 1, GR groups each
+            uint32_t w[2][RB / 16], par[2][GR];
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                const int r = 16 * mt + 8 * hf + key_of(g);
+                if (RB == 32) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(kt + r * RB + 8 * t);
+                    w[hf][0] = u.x;
+                    w[hf][1] = u.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RB / 64; i++) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(kt + r * RB + swz<RB>(r, RB / 64 * t + i) * 16);
+                        w[hf][4 * i] = u.x;
+                        w[hf][4 * i + 1] = u.y;
+                        w[hf][4 * i + 2] = u.z;
+                        w[hf][4 * i + 3] = u.w;
+                    }
+                }
+#pragma unroll
+                for (int gr = 0; gr < GR; gr++) par[hf][gr] = kpar[r * GR + gr];
+            }
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++) {
+                __half2 c[2][4];
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    if (BITS == 4)  // two groups to a word: cell 2t in word gr / 2, cell 2t + 1 GR / 2 words on
+                        kvq_codes4(kvq_prmt(w[hf][gr / 2], w[hf][GR / 2 + gr / 2], gr & 1 ? 0x7632 : 0x5410), c[hf]);
+                    else
+                        kvq_codes8(w[hf][gr], w[hf][GR + gr], c[hf]);
+                    const __half2 lo = kvq_h2(kvq_prmt(par[hf][gr], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[hf][gr], 0, 0x3232));
+#pragma unroll
+                    for (int i = 0; i < 4; i++) c[hf][i] = __hfma2(st, c[hf][i], lo);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    const uint32_t af[4] = {kvq_u32(c[0][2 * ks]), kvq_u32(c[1][2 * ks]), kvq_u32(c[0][2 * ks + 1]),
+                                            kvq_u32(c[1][2 * ks + 1])};
+#pragma unroll
+                    for (int nc = 0; nc < NC; nc++) mma(sc[mt][nc], af, qf[nc][gr][ks][0], qf[nc][gr][ks][1]);
+                }
+            }
+        }
+        // scores of keys past a row's last position leave (the tile's tail holds zeros)
+        if (edge) {
+#pragma unroll
+            for (int mt = 0; mt < NT; mt++)
+#pragma unroll
+                for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int k = k0 + 16 * mt + 8 * (e >> 1) + key_of(g);
+                        if (k > last[nc][e & 1] || k >= limit) sc[mt][nc][e] = -INFINITY;
+                    }
+        }
+        bool grow = false;
+        float top[NC][2];
+#pragma unroll
+        for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                float x = sc[0][nc][b];
+                x = fmaxf(x, sc[0][nc][2 + b]);
+#pragma unroll
+                for (int mt = 1; mt < NT; mt++) x = fmaxf(x, fmaxf(sc[mt][nc][b], sc[mt][nc][2 + b]));
+                top[nc][b] = x * fac[nc][b];
+                grow |= top[nc][b] > m[nc][b] + HOLD;
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+                for (int b = 0; b < 2; b++) {
+                    float x = top[nc][b];
+#pragma unroll
+                    for (int d = 4; d <= 16; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    x = fmaxf(m[nc][b], x);
+                    const float al = m[nc][b] == -INFINITY ? 0.f : ex2(m[nc][b] - x);
+                    m[nc][b] = x;
+                    l[nc][b] *= al;
+#pragma unroll
+                    for (int i = 0; i < 2 * GR; i++) {
+                        o[nc][i][b] *= al;
+                        o[nc][i][2 + b] *= al;
+                    }
+                }
+        }
+        uint32_t pf[NT][NC][2];  // P^T as B fragments
+#pragma unroll
+        for (int nc = 0; nc < NC; nc++) {
+            const float m0 = m[nc][0] == -INFINITY ? 0.f : m[nc][0], m1 = m[nc][1] == -INFINITY ? 0.f : m[nc][1];
+#pragma unroll
+            for (int mt = 0; mt < NT; mt++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const float p0 = ex2(fmaf(sc[mt][nc][2 * hf], fac[nc][0], -m0));
+                    const float p1 = ex2(fmaf(sc[mt][nc][2 * hf + 1], fac[nc][1], -m1));
+                    l[nc][0] += p0;
+                    l[nc][1] += p1;
+                    pf[mt][nc][hf] = movmatrix(pack_h2(p0, p1));
+                }
+        }
+#pragma unroll
+        for (int mt = 0; mt < NT; mt++) {
+            // cell g of keys 2t, 2t + 1 (first half) and 2t + 8, 2t + 9 of the operand's order
+            uint32_t w[4][RB / 32], par[4][GR];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 16 * mt + 8 * (i >> 1) + key_of(2 * t + (i & 1));
+                const uint8_t *p = vt + r * RB;
+                if (RB == 32) {
+                    w[i][0] = *reinterpret_cast<const uint32_t *>(p + 4 * g);
+                } else if (RB == 64) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(p + swz<RB>(r, g >> 1) * 16 + 8 * (g & 1));
+                    w[i][0] = u.x;
+                    w[i][1 % (RB / 32)] = u.y;
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(p + swz<RB>(r, g) * 16);
+                    w[i][0] = u.x;
+                    w[i][1 % (RB / 32)] = u.y;
+                    w[i][2 % (RB / 32)] = u.z;
+                    w[i][3 % (RB / 32)] = u.w;
+                }
+#pragma unroll
+                for (int gr = 0; gr < GR; gr++) par[i][gr] = vpar[r * GR + gr];
+            }
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++) {
+                __half2 c[2][4];
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    if (BITS == 4)
+                        kvq_codes4(kvq_prmt(w[2 * hf][gr / 2], w[2 * hf + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), c[hf]);
+                    else
+                        kvq_codes8(w[2 * hf][gr], w[2 * hf + 1][gr], c[hf]);
+                    const __half2 lo = kvq_h2(kvq_prmt(par[2 * hf][gr], par[2 * hf + 1][gr], 0x5410));
+                    const __half2 st = kvq_h2(kvq_prmt(par[2 * hf][gr], par[2 * hf + 1][gr], 0x7632));
+#pragma unroll
+                    for (int i = 0; i < 4; i++) c[hf][i] = __hfma2(st, c[hf][i], lo);
+                }
+#pragma unroll
+                for (int b = 0; b < 2; b++) {  // dims 32 gr + 4 g + 2 b and + 1
+                    const uint32_t af[4] = {kvq_u32(c[0][2 * b]), kvq_u32(c[0][2 * b + 1]), kvq_u32(c[1][2 * b]),
+                                            kvq_u32(c[1][2 * b + 1])};
+#pragma unroll
+                    for (int nc = 0; nc < NC; nc++) mma(o[nc][2 * gr + b], af, pf[mt][nc][0], pf[mt][nc][1]);
+                }
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++)
+                if (v_nan[gr]) {  // (the first such key of the tile decides: later ones are seen by fewer rows)
+                    const int k = k0 + __ffs(v_nan[gr]) - 1;
+#pragma unroll
+                    for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+                        for (int b = 0; b < 2; b++)
+                            if (k <= last[nc][b]) {
+#pragma unroll
+                                for (int i = 2 * gr; i < 2 * gr + 2; i++)
+                                    o[nc][i][b] = o[nc][i][2 + b] = __uint_as_float(0x7fffffffu);
+                            }
+                }
+        }
+    }
+    cp_wait<0>();
+    __syncthreads();  // every ring is read: its memory takes the warps' results
+
+    float *const red = reinterpret_cast<float *>(smem);  // [NW][COLS][HD]
+#pragma unroll
+    for (int nc = 0; nc < NC; nc++) {
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            float x = l[nc][b];
+#pragma unroll
+            for (int d = 4; d <= 16; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+            const int col = 8 * nc + 2 * t + b;
+            if (g == 0) {
+                s_ml[warp][col][0] = m[nc][b];
+                s_ml[warp][col][1] = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * GR; i++)
+                *reinterpret_cast<float2 *>(&red[(warp * COLS + col) * HD + 32 * (i >> 1) + 4 * g + 2 * (i & 1)]) =
+                    make_float2(o[nc][i][b], o[nc][i][2 + b]);
+        }
+    }
+    __syncthreads();
+    // the block's warps: pairs of dims, NW partial sums each, against the largest m
+    const int head0 = h * a.group;
+    for (int i = threadIdx.x; i < rows * (HD / 2); i += blockDim.x) {
+        const int col = i / (HD / 2), d = 2 * (i % (HD / 2));
+        float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) M = fmaxf(M, s_ml[w][col][0]);
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            // (a warp that saw nothing adds its zeros; a NaN in it stays one)
+            const float mw = s_ml[w][col][0], f = mw == -INFINITY ? 0.f : ex2(mw - M);
+            const float2 v = *reinterpret_cast<const float2 *>(&red[(w * COLS + col) * HD + d]);
+            L = fmaf(s_ml[w][col][1], f, L);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+        }
+        if (C == 1) {
+            const float inv = M == -INFINITY ? 0.f : 1.f / L;
+            put_out(a.out, s, col / a.group, head0 + col % a.group, d, x * inv, y * inv);
+        } else {  // (each element is read and written by this thread alone)
+            *reinterpret_cast<float2 *>(&red[col * HD + d]) = make_float2(x, y);
+            if (d == 0) {
+                s_cml[col][0] = M;
+                s_cml[col][1] = L;
+            }
+        }
+    }
+    if (C == 1) return;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    // the cluster's blocks: each merges its share of the outputs from all of them
+    for (int i = rank * int(blockDim.x) + int(threadIdx.x); i < rows * (HD / 2); i += C * blockDim.x) {
+        const int col = i / (HD / 2), d = 2 * (i % (HD / 2));
+        float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
+        for (int c = 0; c < C; c++) {
+            const float *ml = cl.map_shared_rank(&s_cml[col][0], c);
+            const float mc = ml[0], lc = ml[1];
+            const float2 v = *reinterpret_cast<const float2 *>(cl.map_shared_rank(&red[col * HD + d], c));
+            const float Mn = fmaxf(M, mc);
+            const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn), f1 = mc == -INFINITY ? 0.f : ex2(mc - Mn);
+            L = L * f0 + lc * f1;
+            x = x * f0 + v.x * f1;
+            y = y * f0 + v.y * f1;
+            M = Mn;
+        }
+        const float inv = M == -INFINITY ? 0.f : 1.f / L;
+        put_out(a.out, s, col / a.group, head0 + col % a.group, d, x * inv, y * inv);
+    }
+    cl.sync();  // no block leaves while another reads its memory
+}
+
+// ---- many query rows ---------------------------------------------------------------
+//
+// Grid (splits x row tiles, KV heads, sequences). A block takes 64 query rows of
+// a KV head (row = token * group + head), 16 to a warp, and walks the keys in
+// tiles of 64: all four warps unpack a tile of K and V into fp16 in shared
+// memory, then each takes it to the tensor cores as B operands (S = Q K^T, O = P V).
+// A packed word (pair of cells of neighbouring groups) becomes one 16-byte chunk
+// of a shared-memory row, its dims in the order the unpacking leaves them; q is
+// read in the same order, and O leaves through it.
+constexpr int CK_ROWS = 64, CK_KEYS = 64, CK_THREADS = 128;
+
+// dim of element p (0..HD) of a shared-memory row
+template <int HD>
+__device__ __forceinline__ int dim_of(int p) {
+    constexpr int GP = HD / 64;  // pairs of groups
+    const int q = p >> 3;
+    return 32 * (2 * (q % GP) + (p & 1)) + 4 * (q / GP) + ((p & 7) >> 1);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <int BITS, int HD, typename QT>
+__global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant__ AttnArgs a, int C) {
+    constexpr int GR = HD / 32, GP = HD / 64, CH = HD / 8, KS = HD / 16;  // 16-byte chunks of a row, k-steps
+    constexpr int PER = CK_KEYS * CH / CK_THREADS;                        // chunks a thread unpacks, of K and of V
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *const ks = smem, *const vs = smem + CK_KEYS * HD * 2;  // [key][HD] fp16, chunk c of row r at c ^ (r & 7)
+    __shared__ float s_ml[CK_ROWS][2];
+    __shared__ uint32_t s_nan[GR][2];  // keys of the tile whose V holds a NaN, per group
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int s = blockIdx.z, h = blockIdx.y, rank = blockIdx.x % C;
+    const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group, first = len - n;
+    // the row tiles with the most keys come first
+    const int r0 = (int(gridDim.x) / C - 1 - int(blockIdx.x) / C) * CK_ROWS;
+    if (r0 >= rows) return;
+    const int row_hi = min(r0 + CK_ROWS, rows) - 1;
+    const int limit = max(0, min(min(len, a.max_seq), first + row_hi / a.group + 1));  // the tile's rows see keys below
+    const int first_last = first + r0 / a.group;                                       // the last position the first row sees
+    const int64_t krow = s * a.seq_rows + int64_t(h) * a.max_seq;
+    const int tiles = (limit + CK_KEYS - 1) / CK_KEYS;
+    const int t0 = int(int64_t(tiles) * rank / C), t1 = int(int64_t(tiles) * (rank + 1) / C);
+
+    // q as A fragments of this warp's rows g and g + 8
+    uint32_t qf[KS][4];
+    float fac[2];
+    int last[2];
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+        const int r = r0 + warp * 16 + 8 * b + g;
+        const int j = r / a.group;
+        last[b] = first + j;
+        float v[KS][4], mx = 0.f;
+        const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + int64_t(j) * a.q_tok + int64_t(h * a.group + r % a.group) * a.q_head;
+#pragma unroll
+        for (int k = 0; k < KS; k++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                v[k][e] = r < rows ? q_at(q + dim_of<HD>(16 * k + 2 * t + (e & 1) + 8 * (e >> 1))) : 0.f;
+                mx = fmaxf(mx, fabsf(v[k][e]));
+            }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float down, up;
+        row_scale(mx, down, up);
+        fac[b] = up * a.scale_log2;
+#pragma unroll
+        for (int k = 0; k < KS; k++) {
+            qf[k][b] = pack_h2(v[k][0] * down, v[k][1] * down);
+            qf[k][2 + b] = pack_h2(v[k][2] * down, v[k][3] * down);
+        }
+    }
+    float o[HD / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < HD / 8; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[d][e] = 0.f;
+
+    // a tile's packed words, in registers one tile ahead
+    uint2 w[2][PER];
+    uint32_t par[2][PER][2];
+    auto fetch = [&](int ti) {
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int at = threadIdx.x + i * CK_THREADS, r = at / CH, c = at % CH, key = ti * CK_KEYS + r;
+            const bool ok = key < limit;
+            const int64_t row = krow + (ok ? key : 0);
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                const uint8_t *codes = kv ? a.vc : a.kc;
+                const uint32_t *pp = (kv ? a.vp : a.kp) + row * GR + 2 * (c % GP);
+                w[kv][i] = make_uint2(0, 0);
+                par[kv][i][0] = par[kv][i][1] = 0;
+                if (ok) {
+                    if (BITS == 4)
+                        w[kv][i].x = reinterpret_cast<const uint32_t *>(codes)[row * CH + c];
+                    else
+                        w[kv][i] = reinterpret_cast<const uint2 *>(codes)[row * CH + c];
+                    const uint2 u = *reinterpret_cast<const uint2 *>(pp);
+                    par[kv][i][0] = u.x;
+                    par[kv][i][1] = u.y;
+                }
+            }
+        }
+    };
+    if (t0 < t1) fetch(t0);
+    for (int ti = t0; ti < t1; ti++) {
+        const int k0 = ti * CK_KEYS;
+        const bool edge = k0 + CK_KEYS > min(first_last + 1, limit);
+        __syncthreads();  // every warp is done with the tile before
+        if (edge && threadIdx.x < 2 * GR) s_nan[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+        if (edge) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int at = threadIdx.x + i * CK_THREADS, r = at / CH, c = at % CH;
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                uint32_t p0 = par[kv][i][0], p1 = par[kv][i][1];
+                if (kv && edge) {  // (see k_kvq_decode: a NaN of V reaches only the rows that see it)
+                    if (kvq_is_nan(p0)) {
+                        atomicOr(&s_nan[2 * (c % GP)][r >> 5], 1u << (r & 31));
+                        p0 = 0;
+                    }
+                    if (kvq_is_nan(p1)) {
+                        atomicOr(&s_nan[2 * (c % GP) + 1][r >> 5], 1u << (r & 31));
+                        p1 = 0;
+                    }
+                }
+                __half2 v[4];
+                if (BITS == 4)
+                    kvq_codes4(w[kv][i].x, v);
+                else
+                    kvq_codes8(w[kv][i].x, w[kv][i].y, v);
+                const __half2 lo = kvq_h2(kvq_prmt(p0, p1, 0x5410)), st = kvq_h2(kvq_prmt(p0, p1, 0x7632));
+                uint4 u;
+                u.x = kvq_u32(__hfma2(st, v[0], lo));
+                u.y = kvq_u32(__hfma2(st, v[1], lo));
+                u.z = kvq_u32(__hfma2(st, v[2], lo));
+                u.w = kvq_u32(__hfma2(st, v[3], lo));
+                *reinterpret_cast<uint4 *>((kv ? vs : ks) + (r * CH + (c ^ (r & 7))) * 16) = u;
+            }
+        }
+        if (ti + 1 < t1) fetch(ti + 1);
+        __syncthreads();
+
+        float sc[CK_KEYS / 8][4];
+#pragma unroll
+        for (int nb = 0; nb < CK_KEYS / 8; nb++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sc[nb][e] = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < CK_KEYS / 16; nb++) {
+            const int r = 16 * nb + 8 * (lane >> 4) + (lane & 7);
+#pragma unroll
+            for (int k = 0; k < KS; k++) {
+                uint32_t b[4];
+                const int c = 2 * k + ((lane >> 3) & 1);
+                ldsm4(sptr(ks + (r * CH + (c ^ (r & 7))) * 16), b);
+                mma(sc[2 * nb], qf[k], b[0], b[1]);
+                mma(sc[2 * nb + 1], qf[k], b[2], b[3]);
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int nb = 0; nb < CK_KEYS / 8; nb++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int k = k0 + 8 * nb + 2 * t + (e & 1);
+                    if (k > last[e >> 1] || k >= limit) sc[nb][e] = -INFINITY;
+                }
+        }
+        bool grow = false;
+        float top[2];
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int nb = 0; nb < CK_KEYS / 8; nb++) x = fmaxf(x, fmaxf(sc[nb][2 * b], sc[nb][2 * b + 1]));
+            top[b] = x * fac[b];
+            grow |= top[b] > m[b] + HOLD;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+                float x = top[b];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                x = fmaxf(m[b], x);
+                const float al = m[b] == -INFINITY ? 0.f : ex2(m[b] - x);
+                m[b] = x;
+                l[b] *= al;
+#pragma unroll
+                for (int d = 0; d < HD / 8; d++) {
+                    o[d][2 * b] *= al;
+                    o[d][2 * b + 1] *= al;
+                }
+            }
+        }
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+        for (int nb = 0; nb < CK_KEYS / 8; nb++) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                sc[nb][e] = ex2(fmaf(sc[nb][e], fac[e >> 1], e < 2 ? -m0 : -m1));
+                l[e >> 1] += sc[nb][e];
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < CK_KEYS / 16; nb++) {
+            const uint32_t pf[4] = {pack_h2(sc[2 * nb][0], sc[2 * nb][1]), pack_h2(sc[2 * nb][2], sc[2 * nb][3]),
+                                    pack_h2(sc[2 * nb + 1][0], sc[2 * nb + 1][1]), pack_h2(sc[2 * nb + 1][2], sc[2 * nb + 1][3])};
+            const int r = 16 * nb + 8 * ((lane >> 3) & 1) + (lane & 7);
+#pragma unroll
+            for (int d = 0; d < HD / 16; d++) {
+                uint32_t b[4];
+                const int c = 2 * d + (lane >> 4);
+                ldsm4t(sptr(vs + (r * CH + (c ^ (r & 7))) * 16), b);
+                mma(o[2 * d], pf, b[0], b[1]);
+                mma(o[2 * d + 1], pf, b[2], b[3]);
+            }
+        }
+        if (edge) {  // element 8 d + 2 t + e of a row belongs to group 2 (d % GP) + e
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++) {
+                const uint32_t lo = s_nan[gr][0], hi = s_nan[gr][1];
+                if (!(lo | hi)) continue;
+                const int k = k0 + (lo ? __ffs(lo) - 1 : 31 + __ffs(hi));
+#pragma unroll
+                for (int d = gr / 2; d < HD / 8; d += GP)
+#pragma unroll
+                    for (int b = 0; b < 2; b++)
+                        if (k <= last[b]) o[d][2 * b + (gr & 1)] = __uint_as_float(0x7fffffffu);
+            }
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+        l[b] += __shfl_xor_sync(0xffffffffu, l[b], 1);
+        l[b] += __shfl_xor_sync(0xffffffffu, l[b], 2);
+    }
+    const int head0 = h * a.group;
+    float *const red = reinterpret_cast<float *>(smem);  // [CK_ROWS][HD], dims in their own order
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+        const int r = warp * 16 + 8 * b + g;
+        const float f = C > 1 ? 1.f : m[b] == -INFINITY ? 0.f : 1.f / l[b];
+#pragma unroll
+        for (int d = 0; d < HD / 8; d++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) red[r * HD + dim_of<HD>(8 * d + 2 * t + e)] = o[d][2 * b + e] * f;
+        if (t == 0) {
+            s_ml[r][0] = m[b];
+            s_ml[r][1] = l[b];
+        }
+    }
+    const int live = min(CK_ROWS, rows - r0) * (HD / 2);
+    if (C == 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < live; i += CK_THREADS) {
+            const int r = i / (HD / 2), d = 2 * (i % (HD / 2)), R = r0 + r;
+            put_out(a.out, s, R / a.group, head0 + R % a.group, d, red[r * HD + d], red[r * HD + d + 1]);
+        }
+        return;
+    }
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int i = rank * CK_THREADS + int(threadIdx.x); i < live; i += C * CK_THREADS) {
+        const int r = i / (HD / 2), d = 2 * (i % (HD / 2)), R = r0 + r;
+        float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
+        for (int c = 0; c < C; c++) {
+            const float *ml = cl.map_shared_rank(&s_ml[r][0], c);
+            const float mc = ml[0], lc = ml[1];
+            const float2 v = *reinterpret_cast<const float2 *>(cl.map_shared_rank(&red[r * HD + d], c));
+            const float Mn = fmaxf(M, mc);
+            const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn), f1 = mc == -INFINITY ? 0.f : ex2(mc - Mn);
+            L = L * f0 + lc * f1;
+            x = x * f0 + v.x * f1;
+            y = y * f0 + v.y * f1;
+            M = Mn;
+        }
+        const float inv = M == -INFINITY ? 0.f : 1.f / L;
+        put_out(a.out, s, R / a.group, head0 + R % a.group, d, x * inv, y * inv);
+    }
+    cl.sync();
+}
+
+// ---- launches ----------------------------------------------------------------------
+
+// Once per kernel and device: its shared memory, and clusters of up to 16.
+template <auto kernel>
+bool prepared(int smem) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return true;
+}
+
+template <typename K, typename... Args>
+int launch_cluster(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+// Splits of one unit of work (a power of two, at most 16: a cluster): as many as
+// fill the device with `units` units, while each split keeps at least `least` of
+// the longest walk's `steps` steps.
+int splits_for(int64_t units, int64_t slots, int64_t steps, int64_t least) {
+    int c = 1;
+    while (c < 16 && units * c * 2 <= slots && steps >= 2 * c * least) c *= 2;
+    return c;
+}
+
+}  // namespace
+
+int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
+                         int max_len, float scale, const KvqOut &out, int nsm, cudaStream_t st) {
+    AttnArgs a;
+    a.kc = c.k_codes;
+    a.vc = c.v_codes;
+    a.kp = reinterpret_cast<const uint32_t *>(c.k_params);
+    a.vp = reinterpret_cast<const uint32_t *>(c.v_params);
+    a.seq_rows = c.seq_rows;
+    a.max_seq = c.max_seq;
+    a.group = n_q_heads / c.n_kv_heads;
+    a.l = l;
+    a.q = q.data;
+    a.q_seq = q.seq;
+    a.q_tok = q.token;
+    a.q_head = q.head;
+    a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(float(c.head_dim))) * 1.4426950408889634f;
+    a.out = out;
+    const int longest = max_len > 0 ? std::min(max_len, c.max_seq) : c.max_seq;
+    const int rows = l.n_tok * a.group;
+    const int64_t pairs = int64_t(c.n_seq) * c.n_kv_heads;
+    int rc = LL_OK;
+    kvq_dispatch(c, [&](auto bits, auto hd) {
+        constexpr int B = bits.value, H = hd.value;
+        auto typed = [&](auto qt) {
+            using QT = decltype(qt);
+            if (rows <= 16) {
+                using S = DecodeShape<B, H>;
+                const int C = splits_for(pairs, 2 * nsm, longest / (S::NW * S::TILE), 1);
+                auto go = [&](auto nc) {
+                    constexpr auto kernel = k_kvq_decode<B, H, nc.value, QT>;
+                    rc = prepared<kernel>(S::SMEM) ? launch_cluster(kernel, dim3(C, c.n_kv_heads, c.n_seq), 256, S::SMEM, C, st, a)
+                                                   : LL_ERR_CUDA;
+                };
+                if (rows <= 8)
+                    go(KvqConst<1>{});
+                else
+                    go(KvqConst<2>{});
+            } else {
+                constexpr int SMEM = 2 * CK_KEYS * H * 2;
+                static_assert(CK_ROWS * H * 4 <= SMEM, "the merge fits in the tiles' memory");
+                const int rt = (rows + CK_ROWS - 1) / CK_ROWS;
+                const int C = splits_for(pairs * rt, 2 * nsm, longest / CK_KEYS, 2);
+                constexpr auto kernel = k_kvq_chunk<B, H, QT>;
+                rc = prepared<kernel>(SMEM)
+                         ? launch_cluster(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
+                         : LL_ERR_CUDA;
+            }
+        };
+        if (type == LL_F32)
+            typed(float{});
+        else
+            typed(__nv_bfloat16{});
+    });
+    return rc;
+}
+
+}  // namespace ll

@@ -36,6 +36,9 @@ LL_Q_BATCH_CC = 12
 LL_Q_BATCH = 10
 LL_MAX_BATCH = 8
 
+LL_BF16 = 0
+LL_F32 = 1
+
 LL_STATIC_SCRATCH_BYTES = 4194304
 LL_STATIC_MAX_LAYERS = 256
 
@@ -49,7 +52,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libll.so")
 EXPORTS = ("ll_init", "ll_init_error", "ll_decode_step", "ll_decode_step_async", "ll_decode_steps", "ll_synchronize",
            "ll_set_trace", "ll_set_timeout_ns", "ll_query", "ll_debug_inject", "ll_plan", "ll_last_error",
            "ll_free", "ll_decode_step_static", "ll_init_batch", "ll_decode_steps_batch", "ll_handle_plan",
-           "ll_prefill")
+           "ll_prefill", "ll_kvq_write", "ll_kvq_read", "ll_kvq_attention")
 
 
 class LLError(RuntimeError):
@@ -72,6 +75,16 @@ LAYER_KEYS = ("attn_norm", "wq", "wk", "wv", "wo", "mlp_norm", "wg", "wu", "wd")
 class ll_weights(ctypes.Structure):
     _fields_ = [("embed", _P16), ("lm_head", _P16), ("final_norm", _P16)] + [
         (k, _PP16) for k in LAYER_KEYS]
+
+
+class ll_kvq_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_params", "v_params")] + [
+        ("seq_rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+            "n_seq", "n_kv_heads", "head_dim", "max_seq", "bits")]
+
+
+class ll_kvq_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("seq", "token", "head")]
 
 
 _lib = None
@@ -126,6 +139,13 @@ def lib() -> ctypes.CDLL:
     L.ll_handle_plan.restype = ctypes.c_int
     L.ll_prefill.argtypes = [vp, vp, i32, i32, vp, vp]
     L.ll_prefill.restype = ctypes.c_int
+    cachep, rowsp, err = ctypes.POINTER(ll_kvq_cache), ctypes.POINTER(ll_kvq_rows), [ctypes.c_char_p, ctypes.c_size_t]
+    L.ll_kvq_write.argtypes = [cachep, rowsp, rowsp, i32, i32, vp, vp, vp] + err
+    L.ll_kvq_write.restype = ctypes.c_int
+    L.ll_kvq_read.argtypes = [cachep, rowsp, rowsp, i32, vp, vp, vp] + err
+    L.ll_kvq_read.restype = ctypes.c_int
+    L.ll_kvq_attention.argtypes = [cachep, rowsp, i32, i32, vp, vp, i32, ctypes.c_float, rowsp, vp] + err
+    L.ll_kvq_attention.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -290,6 +310,59 @@ def ll_init_batch(cfg: ll_config, weights: dict, k_caches, v_caches, stream=None
 def ll_decode_steps_batch(h, tokens_in_dev, positions, n_steps: int, logits, tokens_dev) -> None:
     pos = (ctypes.c_int32 * max(1, len(positions)))(*[int(x) for x in positions])
     _check(h, lib().ll_decode_steps_batch(h, _ptr(tokens_in_dev), pos, int(n_steps), _ptr(logits), _ptr(tokens_dev)))
+
+
+def _kvq_call(fn, device, *args) -> None:
+    """One packed-cache call on torch's current stream of ``device``."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _kvq_call(fn, device, *args)
+    err = ctypes.create_string_buffer(256)
+    rc = fn(*args, torch.cuda.current_stream().cuda_stream, err, 256)
+    if rc != LL_OK:
+        raise LLError(rc, err.value.decode())
+
+
+def ll_kvq_write(cache: "KVQCache", k, v, lens, n_toks=None) -> None:
+    """Quantise k and v [n_seq, n_tok, n_kv_heads, head_dim] (bf16 or fp32, any strides
+    but the last) into ``cache`` as the last tokens of sequences ``lens`` long."""
+    import torch
+    if getattr(k, "dtype", None) not in (torch.bfloat16, torch.float32):
+        raise LLError(LL_ERR_ARG, f"k must be bfloat16 or float32, not {getattr(k, 'dtype', None)}")
+    kr, n_tok = cache._rows(k, "k", k.dtype, cache.n_kv_heads)
+    vr, _ = cache._rows(v, "v", k.dtype, cache.n_kv_heads, n_tok)
+    _kvq_call(lib().ll_kvq_write, cache.device, cache.ref, kr, vr, LL_F32 if k.dtype == torch.float32 else LL_BF16,
+              n_tok, cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks", True))
+
+
+def ll_kvq_read(cache: "KVQCache", k_out, v_out, lens, n_toks=None) -> None:
+    """The last tokens' rows of ``cache`` read back into k_out and v_out
+    [n_seq, n_tok, n_kv_heads, head_dim] (bf16)."""
+    import torch
+    kr, n_tok = cache._rows(k_out, "k_out", torch.bfloat16, cache.n_kv_heads, written=True)
+    vr, _ = cache._rows(v_out, "v_out", torch.bfloat16, cache.n_kv_heads, n_tok, written=True)
+    _kvq_call(lib().ll_kvq_read, cache.device, cache.ref, kr, vr, n_tok, cache._lens(lens, "lens"),
+              cache._lens(n_toks, "n_toks", True))
+
+
+def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=None, max_len: int = 0):
+    """Causal attention of the last tokens' queries q [n_seq, n_tok, n_q_heads, head_dim]
+    (bf16) over ``cache``; out like q (made if None: rows of padded tokens then hold zeros)."""
+    import torch
+    if getattr(q, "ndim", 0) != 4:
+        raise LLError(LL_ERR_ARG, "q must be [n_seq, n_tok, n_q_heads, head_dim]")
+    heads = q.shape[2]
+    qr, n_tok = cache._rows(q, "q", torch.bfloat16, heads)
+    if scale is not None and not scale > 0:
+        raise LLError(LL_ERR_ARG, f"scale must be positive, not {scale}")
+    lp, np_ = cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks", True)
+    if out is None:
+        out = (torch.zeros if np_ else torch.empty)(q.shape, dtype=q.dtype, device=q.device)
+    o, _ = cache._rows(out, "out", torch.bfloat16, heads, n_tok, written=True)
+    _kvq_call(lib().ll_kvq_attention, cache.device, cache.ref, qr, heads, n_tok, lp, np_, int(max_len),
+              0.0 if scale is None else float(scale), o)
+    return out
 
 
 def ll_last_error(h) -> str:
@@ -482,3 +555,97 @@ class BatchDecoder(Decoder):
         _need(logits, "logits", torch.float32, steps * self.n * int(self.shape.vocab), self.device)
         _need(tokens_dev, "tokens_dev", torch.int32, steps * self.n, self.device, optional=False)
         ll_decode_steps_batch(self.handle, tokens_in_dev, positions, n_steps, logits, tokens_dev)
+
+
+class KVQCache:
+    """A packed KV cache (the format in include/ll.h) over the caller's tensors:
+    codes uint8 [n_seq, n_kv_heads, max_seq, head_dim * bits / 8] and parameters
+    float16 [n_seq, n_kv_heads, max_seq, head_dim / 32, 2] of K and of V, contiguous
+    within a sequence. Its calls are ll_kvq_write, ll_kvq_read and
+    ll_kvq_attention; ``lens`` (int32 [n_seq], on the device) counts each sequence's positions with
+    the call's own tokens as the last, ``n_toks`` (alike, or None for all) how many
+    of the call's tokens each sequence has."""
+
+    def __init__(self, k_codes, k_params, v_codes, v_params, bits: int):
+        import torch
+        if bits not in (4, 8):
+            raise LLError(LL_ERR_SHAPE, f"bits must be 4 or 8, not {bits}")
+        dev = getattr(k_codes, "device", None)
+        for t, name, dtype, dims in ((k_codes, "k_codes", torch.uint8, 4), (v_codes, "v_codes", torch.uint8, 4),
+                                     (k_params, "k_params", torch.float16, 5), (v_params, "v_params", torch.float16, 5)):
+            if not getattr(t, "is_cuda", False):
+                raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor")
+            if t.dtype != dtype or t.dim() != dims or t.device != dev:
+                raise LLError(LL_ERR_ARG, f"{name} must be {dtype} of {dims} dims on {dev}")
+        S, KV, M, row = k_codes.shape
+        hd = row * 8 // bits
+        if hd not in (64, 128) or row * 8 != hd * bits:
+            raise LLError(LL_ERR_SHAPE, f"a row of {row} bytes in {bits} bits is {row * 8 / bits:g} dims: 64 or 128 are held")
+        if min(S, KV, M) < 1:
+            raise LLError(LL_ERR_SHAPE, "every size must be positive")
+        rows = {KV * M}
+        for t, name, shape in ((k_codes, "k_codes", (S, KV, M, row)), (v_codes, "v_codes", (S, KV, M, row)),
+                               (k_params, "k_params", (S, KV, M, hd // 32, 2)), (v_params, "v_params", (S, KV, M, hd // 32, 2))):
+            if tuple(t.shape) != shape or not t[0].is_contiguous():
+                raise LLError(LL_ERR_ARG, f"{name} must be {shape}, contiguous within a sequence, not {tuple(t.shape)}")
+        if S > 1:  # rows from one sequence to the next
+            rows = {t.stride(0) / t[0, 0, 0].numel() for t in (k_codes, v_codes, k_params, v_params)}
+            if len(rows) > 1 or min(rows) < KV * M or min(rows) % 1:
+                raise LLError(LL_ERR_ARG, "the four arrays must be the same number of whole rows, at least "
+                                          "n_kv_heads * max_seq, apart from sequence to sequence")
+        self.k_codes, self.k_params, self.v_codes, self.v_params = k_codes, k_params, v_codes, v_params
+        self.n_seq, self.n_kv_heads, self.max_seq, self.head_dim, self.bits = S, KV, M, hd, bits
+        self.device = dev
+        self.struct = ll_kvq_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), int(rows.pop()), S, KV, hd, M,
+                                   bits)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, n_seq: int, n_kv_heads: int, max_seq: int, head_dim: int, bits: int, device="cuda"):
+        """A cache of new tensors (all zeros)."""
+        import torch
+        if bits not in (4, 8) or head_dim not in (64, 128):
+            raise LLError(LL_ERR_SHAPE, f"bits must be 4 or 8 and head_dim 64 or 128, not {bits} and {head_dim}")
+        lead = (n_seq, n_kv_heads, max_seq)
+        codes = [torch.zeros(*lead, head_dim * bits // 8, dtype=torch.uint8, device=device) for _ in range(2)]
+        params = [torch.zeros(*lead, head_dim // 32, 2, dtype=torch.float16, device=device) for _ in range(2)]
+        return cls(codes[0], params[0], codes[1], params[1], bits)
+
+    def _rows(self, t, name: str, dtype, heads: int, n_tok=None, written: bool = False):
+        """t as an ll_kvq_rows reference, and its tokens."""
+        if not getattr(t, "is_cuda", False):
+            raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise LLError(LL_ERR_ARG, f"{name} must be {dtype}, not {t.dtype}")
+        if t.device != self.device:
+            raise LLError(LL_ERR_ARG, f"{name} is on {t.device}, the cache on {self.device}")
+        shape, st = t.shape, t.stride()
+        if len(shape) != 4 or shape[0] != self.n_seq or shape[2] != heads or shape[3] != self.head_dim or (
+                n_tok is not None and shape[1] != n_tok):
+            raise LLError(LL_ERR_ARG, f"{name} is {tuple(shape)}, the call needs "
+                                      f"[{self.n_seq}, {n_tok or 'n_tok'}, {heads}, {self.head_dim}]")
+        if st[3] != 1:
+            raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
+        if written:  # no two rows of an output may share memory
+            reach = self.head_dim
+            for stride, size in sorted((st[i], shape[i]) for i in range(3) if shape[i] > 1):
+                if stride < reach:
+                    raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
+                reach += stride * (size - 1)
+        return ctypes.byref(ll_kvq_rows(t.data_ptr(), st[0], st[1], st[2])), shape[1]
+
+    def _lens(self, t, name: str, optional: bool = False) -> int:
+        import torch
+        if t is None and optional:
+            return 0
+        _need(t, name, torch.int32, self.n_seq, self.device, optional=False)
+        return t.data_ptr()
+
+    def write(self, k, v, lens, n_toks=None) -> None:
+        ll_kvq_write(self, k, v, lens, n_toks)
+
+    def read(self, k_out, v_out, lens, n_toks=None) -> None:
+        ll_kvq_read(self, k_out, v_out, lens, n_toks)
+
+    def attention(self, q, lens, n_toks=None, out=None, scale=None, max_len: int = 0):
+        return ll_kvq_attention(self, q, lens, n_toks, out, scale, max_len)

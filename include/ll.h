@@ -297,6 +297,89 @@ int ll_decode_step_static(const ll_config *cfg, const ll_weights *w, uint16_t *k
                           int32_t token, int32_t pos, float *logits_dev, int32_t *next_token_host, void *stream,
                           char *err, size_t err_len);
 
+/* ---- Packed KV cache: K and V rows in 4 or 8 bits ----------------------------
+ *
+ * A row is the K (or V) vector of one (sequence, KV head, position). It is held
+ * as groups of 32 dims; a group has two fp16 parameters, lo and step, and one
+ * code of `bits` bits per dim, which stands for the value
+ *     fp16(lo + step * code)                      (one rounding).
+ * Writing takes, over the group's values x (each clamped to +-60000):
+ *     lo = fp16(min x),  step = fp16((max x - lo) / (2^bits - 1)),
+ *     code = (x - lo) / step rounded to the nearest integer, ties to even, and
+ *            clamped to [0, 2^bits - 1]; 0 where step is 0 (it is never below),
+ * in fp32 arithmetic, so a value is read back within half a step of itself, up
+ * to the fp16 roundings of lo, step and the value. A group holding a NaN reads
+ * back as NaN.
+ *
+ * Codes of a row: head_dim * bits / 8 bytes. Dim d = 32 gr + 4 g + i (group gr,
+ * g < 8, i < 4) is element (g * (head_dim / 32) + gr) * 4 + i; 4-bit elements sit
+ * two to a byte, the even element in the low half. Parameters of a row: head_dim
+ * / 32 pairs (lo, step). Row (s, h, p) is number s * seq_rows + h * max_seq + p
+ * of each array. At 64 dims a row takes 40 bytes in 4 bits and 72 in 8, against
+ * 128 in bf16; at 128 dims 80 and 144 against 256.
+ *
+ * The calls below need no handle. They enqueue on `stream` (cudaStream_t as
+ * void*, of the device that is current at the call), allocate nothing, keep
+ * nothing between calls, and may be captured into CUDA graphs. They return LL_OK,
+ * LL_ERR_ARG / LL_ERR_SHAPE (nothing was launched), LL_ERR_DEVICE or LL_ERR_CUDA,
+ * with a one-line reason in err (err_len bytes; NULL for none).
+ *
+ * Every call is about the LAST tokens of its sequences: sequence s holds
+ * len_dev[s] positions (device int32, the call's own tokens among them), and the
+ * call handles its last n tokens, n = n_tok_dev[s] held within [0, n_tok] (device
+ * int32), or n_tok for every sequence when n_tok_dev is NULL. Token j < n is at
+ * position len - n + j. Tokens outside [0, max_seq) and padded tokens j >= n are
+ * skipped: nothing is read or written for them. */
+#define LL_BF16 0
+#define LL_F32 1
+
+typedef struct {
+    uint8_t *k_codes, *v_codes;    /* device, 16-byte aligned */
+    uint16_t *k_params, *v_params; /* device, 16-byte aligned, fp16 bit patterns */
+    int64_t seq_rows;              /* rows from one sequence to the next, at least n_kv_heads * max_seq */
+    int32_t n_seq;                 /* 1 to 65535 */
+    int32_t n_kv_heads;
+    int32_t head_dim;              /* 64 or 128 */
+    int32_t max_seq;               /* positions a sequence holds at most */
+    int32_t bits;                  /* 4 or 8 */
+} ll_kvq_cache;
+
+/* Rows of head_dim contiguous elements: (sequence s, token j, head h) starts at
+ * data + s * seq + j * token + h * head (strides in elements). data and every
+ * stride in use must be multiples of 16 bytes; the stride of an extent of 1 is
+ * not looked at. */
+typedef struct {
+    void *data;
+    int64_t seq, token, head;
+} ll_kvq_rows;
+
+/* Quantise the tokens' K and V rows ([n_seq][n_tok][n_kv_heads][head_dim] by the
+ * strides of k and v; type LL_BF16 or LL_F32) into the cache. */
+int ll_kvq_write(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *v, int32_t type, int32_t n_tok,
+                 const int32_t *len_dev, const int32_t *n_tok_dev, void *stream, char *err, size_t err_len);
+
+/* The tokens' rows read back as bf16 (each value rounded to it) into k and v, laid
+ * out as ll_kvq_write's inputs, whose strides in use must not be 0. */
+int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *v, int32_t n_tok,
+                const int32_t *len_dev, const int32_t *n_tok_dev, void *stream, char *err, size_t err_len);
+
+/* Attention over the cache: for each token at position p and each query head,
+ *     out = sum_i softmax_i(scale * q . k_i) v_i   over the positions i in [0, p]
+ * (those below max_seq), with query head h reading KV head h / (n_q_heads /
+ * n_kv_heads), at most 8 query heads to a KV head. q and out: bf16 rows
+ * [n_seq][n_tok][n_q_heads][head_dim] by their strides (out's not 0 in use). A
+ * token at a position below 0 (a sequence of length 0, say) has nothing to look
+ * at and gives zeros; rows of padded tokens j >= n keep what they hold. The
+ * tokens' own K and V rows must have been written before. scale: finite and
+ * positive, or 0 for 1 / sqrt(head_dim). max_len: a bound on the lengths that the
+ * launch is laid out for, 0 for max_seq; longer lengths give the same results,
+ * more slowly. Products run on tensor cores in fp16 (q scaled by a power of two
+ * per row, the probabilities rounded to fp16) with fp32 sums; the softmax is fp32.
+ * The same call on the same data repeats bit for bit. */
+int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_heads, int32_t n_tok,
+                     const int32_t *len_dev, const int32_t *n_tok_dev, int32_t max_len, float scale,
+                     const ll_kvq_rows *out, void *stream, char *err, size_t err_len);
+
 #ifdef __cplusplus
 }
 #endif
