@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "kvq.h"
 #include "ll_internal.h"
 
 using ll::Instr;
@@ -36,6 +37,7 @@ struct ll_handle {
     uint32_t epoch = 0;
     int nb = 1;                 // sequences decoded together (batched handles)
     bool batch_api = false;     // made by ll_init_batch: only ll_decode_steps_batch steps it
+    ll_kvq_cache kvq{};         // the packed cache (bits 0: none) of a handle made by ll_init_kvq
     bool bcc = false;           // a batch of two on CUDA-core pages (mv_shape_bc geometry)
     int32_t *pinned = nullptr;  // [0, nb) next tokens, [nb] status
     uint8_t *tagged = nullptr;  // the megakernel's tagged activation words (cleared on reset)
@@ -273,9 +275,10 @@ int attn_splits(int max_seq, int n_kv_heads, int nsm, int nb) {
 namespace {
 
 // ll_init (nb = 1, one cache pair) and ll_init_batch (nb sequences, batch_api):
-// one handle, one library allocation, the schedule for nb sequences.
+// one handle, one library allocation, the schedule for nb sequences. ll_init_kvq:
+// a packed cache kvq in place of the one cache pair (whose pointers are null).
 int init_handle(const ll_config *cfg, const ll_weights *w, uint16_t *const *k_caches, uint16_t *const *v_caches,
-                int nb, bool batch_api, void *stream, ll_handle **out) {
+                int nb, bool batch_api, void *stream, ll_handle **out, const ll_kvq_cache *kvq = nullptr) {
     g_init_error.clear();
     auto bad = [&](int code, const std::string &msg) {
         g_init_error = msg;
@@ -313,10 +316,19 @@ int init_handle(const ll_config *cfg, const ll_weights *w, uint16_t *const *k_ca
     if (nb < 1 || nb > ll::MAX_B || (nb & (nb - 1)) != 0)
         return bad(LL_ERR_ARG, "the batch must be 1, 2, 4 or 8 sequences");
     if (!k_caches || !v_caches) return bad(LL_ERR_ARG, "KV cache arrays are NULL");
-    for (int b = 0; b < nb; b++)
+    for (int b = 0; b < nb && !kvq; b++)
         if (!aligned16(k_caches[b]) || !aligned16(v_caches[b])) return bad(LL_ERR_ARG, "KV caches must be 16-byte aligned");
     uint16_t *const k_cache = k_caches[0], *const v_cache = v_caches[0];
     if (batch_api && c.backend != LL_BACKEND_MEGAKERNEL) return bad(LL_ERR_ARG, "batched decode runs on the megakernel backend");
+    if (kvq) {
+        const char *msg = "";
+        if (const int rc = ll::kvq_check_cache(kvq, msg)) return bad(rc, msg);
+        if (kvq->n_seq != c.n_layers || kvq->n_kv_heads != c.n_kv_heads || kvq->head_dim != c.head_dim ||
+            kvq->max_seq != c.max_seq)
+            return bad(LL_ERR_ARG, "the packed cache is not laid out for this model (n_seq = n_layers, n_kv_heads, "
+                                   "head_dim and max_seq as in cfg)");
+        if (c.backend != LL_BACKEND_CHAIN) return bad(LL_ERR_ARG, "a packed cache is decoded by LL_BACKEND_CHAIN");
+    }
     if (!aligned16(w->embed) || !aligned16(w->final_norm)) return bad(LL_ERR_ARG, "embed/final_norm not 16-byte aligned");
     if (!c.tied && !aligned16(w->lm_head)) return bad(LL_ERR_ARG, "lm_head not 16-byte aligned");
     const uint16_t *const *lp[9] = {w->attn_norm, w->wq, w->wk, w->wv, w->wo, w->mlp_norm, w->wg, w->wu, w->wd};
@@ -544,7 +556,7 @@ int init_handle(const ll_config *cfg, const ll_weights *w, uint16_t *const *k_ca
         if (const char *e = std::getenv("LL_ATTN_FLASH")) p.attn_flash = std::atoi(e) ? 1 : 0;
         // its KV pages come through TMA tensor maps (each sequence's, for the
         // tensor-core kernel, in library memory); without them, the block variant
-        if (!encode_kv_maps(c, k_cache, v_cache, p.kv_maps)) p.attn_flash = 0;
+        if (kvq || !encode_kv_maps(c, k_cache, v_cache, p.kv_maps)) p.attn_flash = 0;
         std::vector<ll::TensorMap> kvm(size_t(nb) * ll::TM_COUNT);
         for (int b = 0; b < nb && p.attn_flash; b++) {
             ll::TensorMap one[ll::TM_COUNT];
@@ -628,6 +640,10 @@ int init_handle(const ll_config *cfg, const ll_weights *w, uint16_t *const *k_ca
     cb.logits = logits;
     cb.splits = h->splits;
     cb.rope_row = nullptr;
+    if (kvq) {
+        h->kvq = *kvq;
+        cb.kvq = &h->kvq;
+    }
 
     bool ok = cudaMemcpy(d_layers, layers.data(), layers.size() * sizeof(ll::LayerW), cudaMemcpyHostToDevice) ==
                   cudaSuccess &&
@@ -663,6 +679,16 @@ int ll_init(const ll_config *cfg, const ll_weights *w, uint16_t *k_cache, uint16
 int ll_init_batch(const ll_config *cfg, const ll_weights *w, uint16_t *const *k_caches, uint16_t *const *v_caches,
                   int32_t n_seq, void *stream, ll_handle **out) {
     return init_handle(cfg, w, k_caches, v_caches, n_seq, true, stream, out);
+}
+
+int ll_init_kvq(const ll_config *cfg, const ll_weights *w, const ll_kvq_cache *cache, void *stream, ll_handle **out) {
+    uint16_t *none = nullptr;
+    if (!cache) {
+        if (out) *out = nullptr;
+        g_init_error = "the packed cache is NULL";
+        return LL_ERR_ARG;
+    }
+    return init_handle(cfg, w, &none, &none, 1, false, stream, out, cache);
 }
 
 #ifdef LL_DEBUG_CHECKS
@@ -717,7 +743,7 @@ int ll_prefill(ll_handle *h, const int32_t *tokens_dev, int32_t n, int32_t pos0,
     if (!ll::prefill_prepare(h->kp, h->host_layers.data(), n, h->pf))
         return fail(h, LL_ERR_OOM, "prefill buffers for " + std::to_string(n) + " positions could not be made");
     const int rc = ll::launch_prefill(h->kp, h->host_layers.data(), h->pf, tokens_dev, n, pos0, logits_dev,
-                                      next_token_dev, h->stream);
+                                      next_token_dev, h->kvq.bits ? &h->kvq : nullptr, h->stream);
     if (rc != LL_OK) {
         cudaError_t e = cudaGetLastError();
         return fail(h, rc, std::string("prefill launch failed: ") + cudaGetErrorString(e));
@@ -794,6 +820,7 @@ int ll_query(const ll_handle *h, int what, int64_t *value) {
         case LL_Q_SMEM_BYTES: *value = h->smem_bytes; break;
         case LL_Q_MV_TC: *value = (h->kp.mv_h.tc ? 1 : 0) | (h->kp.mv_q.tc ? 2 : 0) | (h->kp.mv_i.tc ? 4 : 0); break;
         case LL_Q_BATCH: *value = h->nb; break;
+        case LL_Q_KV_BITS: *value = h->kvq.bits ? h->kvq.bits : 16; break;
         case LL_Q_BATCH_CC: *value = h->bcc ? 1 : 0; break;
         case LL_Q_TRACE_BYTES:
             *value = (int64_t(h->nsm) * h->max_instr * ll::TRACE_WORDS + int64_t(h->nsm) * ll::PTRACE_PAGES * 3) *

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kvq.h"
 #include "ll_internal.h"
 
 namespace ll {
@@ -110,7 +111,8 @@ __global__ void k_matvec(const uint16_t *__restrict__ W, const float *__restrict
 }
 
 // RoPE on q (in place) and k; k and v rounded to bf16 and stored at pos. c is
-// the (cos, sin) row of position pos, hd / 2 entries.
+// the (cos, sin) row of position pos, hd / 2 entries. Without a cache (kc null:
+// a packed one is written from the fp32 rows) k stays in place and v as it is.
 __global__ void k_rope_kv(float *qkv, const float2 *c, int pos, int nq, int nkv, int hd,
                           uint16_t *kc, uint16_t *vc, size_t layer_base, int max_seq) {
     const int half = hd / 2;
@@ -122,7 +124,7 @@ __global__ void k_rope_kv(float *qkv, const float2 *c, int pos, int nq, int nkv,
             const float a = v[i], b = v[i + half];
             const float2 r = c[i];
             const float ra = a * r.x - b * r.y, rb = a * r.y + b * r.x;
-            if (h < nq) {
+            if (h < nq || !kc) {
                 v[i] = ra;
                 v[i + half] = rb;
             } else {
@@ -130,7 +132,7 @@ __global__ void k_rope_kv(float *qkv, const float2 *c, int pos, int nq, int nkv,
                 kc[dst + i] = to_bf(ra);
                 kc[dst + i + half] = to_bf(rb);
             }
-        } else {
+        } else if (kc) {
             const int u = t - total, g = u / hd, d = u % hd;
             const float val = qkv[size_t(nq + nkv) * hd + u];
             vc[layer_base + (size_t(g) * max_seq + pos) * hd + d] = to_bf(val);
@@ -337,9 +339,21 @@ int launch_chain_step(const KParams &p, const ChainBufs &b, void *stream_) {
         mv(w.wv, b.h, kd, H, b.qkv + qd + kd, 0);
         k_rope_kv<<<((p.nq + p.nkv) * p.hd / 2 + kd + 255) / 256, 256, 0, st>>>(
             b.qkv, rope_row, p.pos, p.nq, p.nkv, p.hd, p.k_cache, p.v_cache, lb, p.max_seq);
-        k_attn_partial<<<dim3(p.nkv, b.splits), 256, 0, st>>>(b.qkv, p.k_cache, p.v_cache, lb, p.pos,
-                                                             p.max_seq, G, p.hd, b.splits, b.part);
-        k_attn_combine<<<(qd + 255) / 256, 256, 0, st>>>(b.part, p.nq, p.hd, b.splits, b.o);
+        if (b.kvq) {
+            const ll_kvq_cache c = kvq_sequence(*b.kvq, l);
+            const ll_kvq_rows q = {b.qkv, 0, 0, p.hd}, k = {b.qkv + qd, 0, 0, p.hd}, v = {b.qkv + qd + kd, 0, 0, p.hd};
+            const KvqLens lens = {nullptr, nullptr, p.pos + 1, 1};
+            KvqOut o = {};
+            o.f32 = b.o;
+            o.head = p.hd;
+            int rc = launch_kvq_write(c, k, v, LL_F32, lens, st);
+            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, p.pos + 1, 0.f, o, p.nsm, st);
+            if (rc != LL_OK) return rc;
+        } else {
+            k_attn_partial<<<dim3(p.nkv, b.splits), 256, 0, st>>>(b.qkv, p.k_cache, p.v_cache, lb, p.pos,
+                                                                 p.max_seq, G, p.hd, b.splits, b.part);
+            k_attn_combine<<<(qd + 255) / 256, 256, 0, st>>>(b.part, p.nq, p.hd, b.splits, b.o);
+        }
         mv(w.wo, b.o, H, qd, b.x, 1);
         k_rmsnorm<<<1, 1024, 0, st>>>(b.x, w.mlp_norm, H, p.eps, b.h);
         mv(w.wg, b.h, I, H, b.gate, 0);

@@ -155,7 +155,7 @@ struct KParams {
     // model
     const LayerW *layers;     // [L] (device)
     const uint16_t *embed, *lm_head, *final_norm;
-    uint16_t *k_cache, *v_cache;
+    uint16_t *k_cache, *v_cache;  // null in a handle with a packed cache
     const float2 *rope_cs;    // [max_seq][hd/2] (cos, sin)
     int32_t L, H, nq, nkv, hd, I, V, max_seq;
     float eps;
@@ -226,6 +226,7 @@ struct ChainBufs {
     // the (cos, sin) row of the step's position, or null to take row pos of the
     // KParams table (rope_cs)
     const float2 *rope_row;
+    const ll_kvq_cache *kvq = nullptr;  // the packed cache (layers as its sequences) of an ll_init_kvq handle
 };
 
 // KV splits per KV head: about ATTN_SPLIT_POS cached positions each at the
@@ -257,8 +258,9 @@ struct PrefillBufs {
 // Allocates (or grows) the buffers and encodes the maps; false on failure.
 bool prefill_prepare(const KParams &p, const LayerW *host_layers, int n, PrefillBufs &b);
 void prefill_release(PrefillBufs &b);
+// kvq: the packed cache of an ll_init_kvq handle, or null.
 int launch_prefill(const KParams &p, const LayerW *host_layers, PrefillBufs &b, const int32_t *tokens_dev, int n,
-                   int pos0, float *logits, int32_t *next_dev, void *stream);
+                   int pos0, float *logits, int32_t *next_dev, const ll_kvq_cache *kvq, void *stream);
 
 // Host-side schedule construction (schedule.cpp). nb sequences (attention items
 // per sequence); an SM's LM-head rows in instructions of at most lm_rows rows.

@@ -34,6 +34,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "kvq.h"
 #include "ll_internal.h"
 
 namespace ll {
@@ -520,7 +521,8 @@ __global__ void k_pf_norm_split(const float *x, const uint16_t *g, int H, float 
 // One block per position t: RoPE ("rotate half") on its q heads in place and on
 // its k heads, k and v rounded to bf16 (nearest even) into the cache at pos0 + t.
 // A thread takes four consecutive pairs (i, i + hd / 2) of a head: 16-byte loads
-// and stores of q, 8-byte stores into the cache.
+// and stores of q, 8-byte stores into the cache. Without a cache (kc null: a packed
+// one is written from the fp32 rows) k stays in place and v as it is.
 __device__ __forceinline__ uint2 bf16x4(float a, float b, float c, float d) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
@@ -543,7 +545,7 @@ __global__ void k_pf_rope_kv(float *qkv, const float2 *rope, int pos0, int nq, i
                                       a.w * c23.z - b.w * c23.w);
         const float4 rb = make_float4(a.x * c01.y + b.x * c01.x, a.y * c01.w + b.y * c01.z, a.z * c23.y + b.z * c23.x,
                                       a.w * c23.w + b.w * c23.z);
-        if (h < nq) {
+        if (h < nq || !kc) {
             *reinterpret_cast<float4 *>(v + i) = ra;
             *reinterpret_cast<float4 *>(v + i + half) = rb;
         } else {
@@ -552,7 +554,7 @@ __global__ void k_pf_rope_kv(float *qkv, const float2 *rope, int pos0, int nq, i
             *reinterpret_cast<uint2 *>(kc + dst + i + half) = bf16x4(rb.x, rb.y, rb.z, rb.w);
         }
     }
-    for (int u = 4 * int(threadIdx.x); u < kd; u += 4 * int(blockDim.x)) {
+    for (int u = 4 * int(threadIdx.x); kc && u < kd; u += 4 * int(blockDim.x)) {
         const int g = u / hd, d = u % hd;
         const float4 x = *reinterpret_cast<const float4 *>(row + qd + kd + u);
         *reinterpret_cast<uint2 *>(vc + layer_base + (size_t(g) * max_seq + pos) * hd + d) = bf16x4(x.x, x.y, x.z, x.w);
@@ -1019,7 +1021,7 @@ bool prefill_prepare(const KParams &p, const LayerW *host_layers, int n, Prefill
     for (int q = 0; q < NTERMS && ok; q++)
         ok = encode_operand(b.h[q], int64_t(na), p.H, b.m_h[q]) && encode_operand(b.o[q], int64_t(na), int(qd), b.m_o[q]) &&
              encode_operand(b.a[q], int64_t(na), p.I, b.m_a[q]);
-    {  // the caches, [L * n_kv * max_seq][hd], in tiles of 16 rows x 64 columns
+    if (p.k_cache) {  // the caches, [L * n_kv * max_seq][hd], in tiles of 16 rows x 64 columns
         EncodeTiled enc = encoder();
         const int64_t rows = int64_t(p.L) * p.nkv * p.max_seq;
         const cuuint64_t dims[2] = {cuuint64_t(p.hd), cuuint64_t(rows)};
@@ -1053,7 +1055,7 @@ void prefill_release(PrefillBufs &b) {
 }
 
 int launch_prefill(const KParams &p, const LayerW *host_layers, PrefillBufs &b, const int32_t *tokens_dev, int n,
-                   int pos0, float *logits, int32_t *next_dev, void *stream_) {
+                   int pos0, float *logits, int32_t *next_dev, const ll_kvq_cache *kvq, void *stream_) {
     cudaStream_t st = static_cast<cudaStream_t>(stream_);
     const int H = p.H, qd = p.nq * p.hd, kd = p.nkv * p.hd, I = p.I;
     const size_t per_layer = size_t(p.nkv) * p.max_seq * p.hd;
@@ -1085,7 +1087,19 @@ int launch_prefill(const KParams &p, const LayerW *host_layers, PrefillBufs &b, 
         if (rc == LL_OK)
             rc = ok(launch_pdl(k_pf_rope_kv, dim3(n), dim3(256), 0, st, b.qkv, (const float2 *)p.rope_cs, pos0, p.nq,
                                p.nkv, p.hd, p.k_cache, p.v_cache, lb, p.max_seq));
-        if (rc == LL_OK) rc = launch_attention(p, b, l, pos0, n, to, st);
+        if (rc == LL_OK && kvq) {
+            const ll_kvq_cache c = kvq_sequence(*kvq, l);
+            const ll_kvq_rows q = {b.qkv, 0, ld, p.hd}, k = {b.qkv + qd, 0, ld, p.hd}, v = {b.qkv + qd + kd, 0, ld, p.hd};
+            const KvqLens lens = {nullptr, nullptr, pos0 + n, n};
+            KvqOut o = {};
+            for (int i = 0; i < NTERMS; i++) o.t[i] = b.o[i];
+            o.token = qd;
+            o.head = p.hd;
+            rc = launch_kvq_write(c, k, v, LL_F32, lens, st);
+            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, pos0 + n, 0.f, o, p.nsm, st);
+        } else if (rc == LL_OK) {
+            rc = launch_attention(p, b, l, pos0, n, to, st);
+        }
         if (rc == LL_OK) rc = gemm<EPI_ADD>(b.m_o, m + 3, 1, 0, 0, n, H, qd, b.x, H, nullptr, p, st);
         if (rc == LL_OK)
             rc = ok(launch_pdl(k_pf_norm_split, dim3(n), dim3(norm_threads), 0, st, (const float *)b.x,

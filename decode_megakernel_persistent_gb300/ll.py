@@ -34,6 +34,7 @@ LL_Q_TRACE_BYTES = 8
 LL_Q_MV_TC = 9
 LL_Q_BATCH_CC = 12
 LL_Q_BATCH = 10
+LL_Q_KV_BITS = 13
 LL_MAX_BATCH = 8
 
 LL_BF16 = 0
@@ -52,7 +53,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libll.so")
 EXPORTS = ("ll_init", "ll_init_error", "ll_decode_step", "ll_decode_step_async", "ll_decode_steps", "ll_synchronize",
            "ll_set_trace", "ll_set_timeout_ns", "ll_query", "ll_debug_inject", "ll_plan", "ll_last_error",
            "ll_free", "ll_decode_step_static", "ll_init_batch", "ll_decode_steps_batch", "ll_handle_plan",
-           "ll_prefill", "ll_kvq_write", "ll_kvq_read", "ll_kvq_attention")
+           "ll_prefill", "ll_kvq_write", "ll_kvq_read", "ll_kvq_attention", "ll_init_kvq")
 
 
 class LLError(RuntimeError):
@@ -146,6 +147,8 @@ def lib() -> ctypes.CDLL:
     L.ll_kvq_read.restype = ctypes.c_int
     L.ll_kvq_attention.argtypes = [cachep, rowsp, i32, i32, vp, vp, i32, ctypes.c_float, rowsp, vp] + err
     L.ll_kvq_attention.restype = ctypes.c_int
+    L.ll_init_kvq.argtypes = [ctypes.POINTER(ll_config), ctypes.POINTER(ll_weights), cachep, vp, ctypes.POINTER(vp)]
+    L.ll_init_kvq.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -312,6 +315,20 @@ def ll_decode_steps_batch(h, tokens_in_dev, positions, n_steps: int, logits, tok
     _check(h, lib().ll_decode_steps_batch(h, _ptr(tokens_in_dev), pos, int(n_steps), _ptr(logits), _ptr(tokens_dev)))
 
 
+def ll_init_kvq(cfg: ll_config, weights: dict, cache: "KVQCache", stream=None):
+    """A handle whose KV cache is packed: ``cache`` has the model's layers as its sequences."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    w, keep = _weights_struct(weights)
+    h = ctypes.c_void_p()
+    rc = lib().ll_init_kvq(ctypes.byref(cfg), ctypes.byref(w), cache.ref, ctypes.c_void_p(stream.cuda_stream),
+                           ctypes.byref(h))
+    if rc != LL_OK:
+        raise LLError(rc, lib().ll_init_error().decode())
+    return h
+
+
 def _kvq_call(fn, device, *args) -> None:
     """One packed-cache call on torch's current stream of ``device``."""
     import torch
@@ -395,12 +412,11 @@ def _need(t, name: str, dtype, min_numel: int, device, optional: bool = True) ->
         raise LLError(LL_ERR_ARG, f"{name} holds {t.numel()} elements, the call needs {min_numel}")
 
 
-def check_model(shape, weights: dict, k_cache, v_cache, max_seq: int) -> None:
-    """The weights and caches ll_init will read, against the shape: every tensor a
-    contiguous CUDA bf16 tensor on the embedding's device with exactly the
-    elements of its matrix or vector (per-layer lists n_layers long), and the
-    caches room for [n_layers][n_kv_heads][max_seq][head_dim] (raises
-    LLError(LL_ERR_ARG) naming the first misfit)."""
+def check_weights(shape, weights: dict) -> None:
+    """The weights a handle will read, against the shape: every tensor a contiguous
+    CUDA bf16 tensor on the embedding's device with exactly the elements of its
+    matrix or vector, per-layer lists n_layers long (raises LLError(LL_ERR_ARG)
+    naming the first misfit)."""
     import torch
     H, V, I, L = int(shape.hidden), int(shape.vocab), int(shape.inter), int(shape.n_layers)
     q, kv = int(shape.n_q_heads) * int(shape.head_dim), int(shape.n_kv_heads) * int(shape.head_dim)
@@ -423,7 +439,16 @@ def check_model(shape, weights: dict, k_cache, v_cache, max_seq: int) -> None:
             raise LLError(LL_ERR_ARG, f"{key} must list one tensor per layer ({L})")
         for i, t in enumerate(ts):
             exact(t, f"{key}[{i}]", n)
-    cache = L * kv * int(max_seq)
+
+
+def check_model(shape, weights: dict, k_cache, v_cache, max_seq: int) -> None:
+    """check_weights, and the caches ll_init will read: contiguous CUDA bf16 tensors
+    on the embedding's device with room for [n_layers][n_kv_heads][max_seq][head_dim]
+    (raises LLError(LL_ERR_ARG))."""
+    import torch
+    check_weights(shape, weights)
+    dev = getattr(weights.get("embed"), "device", None)
+    cache = int(shape.n_layers) * int(shape.n_kv_heads) * int(shape.head_dim) * int(max_seq)
     _need(k_cache, "k_cache", torch.bfloat16, cache, dev, optional=False)
     _need(v_cache, "v_cache", torch.bfloat16, cache, dev, optional=False)
 
@@ -555,6 +580,30 @@ class BatchDecoder(Decoder):
         _need(logits, "logits", torch.float32, steps * self.n * int(self.shape.vocab), self.device)
         _need(tokens_dev, "tokens_dev", torch.int32, steps * self.n, self.device, optional=False)
         ll_decode_steps_batch(self.handle, tokens_in_dev, positions, n_steps, logits, tokens_dev)
+
+
+class KVQDecoder(Decoder):
+    """A decoder whose KV cache is packed (ll_init_kvq): ``cache`` is a KVQCache with the
+    model's layers as its sequences, holding max_seq positions. Steps and prefill as
+    Decoder's, one kernel per operation."""
+
+    def __init__(self, shape, weights: dict, cache: "KVQCache", stream=None):
+        import torch
+        self.handle = None
+        check_weights(shape, weights)
+        want = (int(shape.n_layers), int(shape.n_kv_heads), int(shape.head_dim))
+        if (cache.n_seq, cache.n_kv_heads, cache.head_dim) != want:
+            raise LLError(LL_ERR_ARG, f"the cache is {(cache.n_seq, cache.n_kv_heads, cache.head_dim)} "
+                                      f"(sequences as layers, KV heads, dims), the model {want}")
+        if cache.device != weights["embed"].device:
+            raise LLError(LL_ERR_ARG, f"the cache is on {cache.device}, the weights on {weights['embed'].device}")
+        self.shape = shape
+        self.weights = weights
+        self.cache = cache
+        self.stream = stream if stream is not None else torch.cuda.current_stream()
+        self.cfg = make_config(shape, cache.max_seq, LL_BACKEND_CHAIN)
+        self.device = weights["embed"].device
+        self.handle = ll_init_kvq(self.cfg, weights, cache, self.stream)
 
 
 class KVQCache:

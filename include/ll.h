@@ -233,6 +233,7 @@ int ll_set_trace(ll_handle *h, uint64_t *trace_dev, size_t bytes);
 #define LL_Q_TRACE_BYTES 8      /* size of the buffer ll_set_trace needs */
 #define LL_Q_BATCH 10           /* sequences a handle decodes together */
 #define LL_Q_MV_TC 9            /* matrix-vector widths on tensor-core pages: bit 0 hidden, bit 1 n_q*head_dim, bit 2 inter */
+#define LL_Q_KV_BITS 13         /* bits of a cached K or V value: 16, or a packed cache's 4 or 8 */
 #define LL_Q_BATCH_CC 12        /* 1: a batch of two on CUDA-core pages (each page read once for both sequences) */
 int ll_query(const ll_handle *h, int what, int64_t *value);
 
@@ -379,6 +380,17 @@ int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *
 int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_heads, int32_t n_tok,
                      const int32_t *len_dev, const int32_t *n_tok_dev, int32_t max_len, float scale,
                      const ll_kvq_rows *out, void *stream, char *err, size_t err_len);
+
+/* A decoder whose KV cache is packed: as ll_init, with the cache's sequences as
+ * the model's layers (cache->n_seq = n_layers, one sequence of each layer;
+ * n_kv_heads, head_dim and max_seq as in cfg). The struct is copied, the arrays
+ * stay the caller's. Steps run one kernel per operation, so cfg->backend must be
+ * LL_BACKEND_CHAIN (LL_ERR_ARG otherwise). ll_decode_step, _async, ll_decode_steps and
+ * ll_prefill work as on any handle: position pos's K and V are written as
+ * ll_kvq_write writes them (from fp32 values, after RoPE) and attention reads the
+ * packed rows 0..pos as ll_kvq_attention does, with fp32 queries (scaled and rounded
+ * to fp16's 11 bits) and fp32 outputs. */
+int ll_init_kvq(const ll_config *cfg, const ll_weights *w, const ll_kvq_cache *cache, void *stream, ll_handle **out);
 
 #ifdef __cplusplus
 }
