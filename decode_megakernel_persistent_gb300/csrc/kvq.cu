@@ -42,8 +42,7 @@ struct RwArgs {
     uint32_t *params[2];   // (lo, step) as fp16 pairs
     int64_t seq_rows;
     int32_t max_seq, nkv, n_rows;  // n_rows = n_tok * nkv
-    int32_t token_fast;    // row index r: 1 = head * n_tok + token, 0 = token * nkv + head
-    FastDiv inner;         // n_tok or nkv
+    FastDiv heads;  // nkv
     KvqLens l;
 };
 
@@ -58,155 +57,236 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// A thread's 8 values of a row, as they are stored.
+__device__ __forceinline__ void load8(const float *p, uint32_t (&w)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p), b = *reinterpret_cast<const uint4 *>(p + 4);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, uint32_t (&w)[4]) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+}
+__device__ __forceinline__ void widen8(const uint32_t (&w)[8], float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void widen8(const uint32_t (&w)[4], float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
 }
 
-// A thread's row of the call: token and head of row number r, and its position,
-// or -1 where there is nothing to do.
-__device__ __forceinline__ int row_of(const RwArgs &a, int r, int n, int len, int &j, int &h) {
-    if (r >= a.n_rows) return -1;
-    const int o = int(a.inner.div(uint32_t(r))), i = r - o * int(a.inner.d);
-    j = a.token_fast ? i : o;
-    h = a.token_fast ? o : i;
-    const int pos = len - n + j;
-    return j < n && pos >= 0 && pos < a.max_seq ? pos : -1;
+// Smallest and largest of the four lanes' 8 values each; NaN if any is.
+__device__ __forceinline__ void group_range(const uint32_t (&w)[8], float &mn, float &mx) {
+    mn = mx = __uint_as_float(w[0]);
+#pragma unroll
+    for (int i = 1; i < 8; i++) {
+        mn = min_nan(mn, __uint_as_float(w[i]));
+        mx = max_nan(mx, __uint_as_float(w[i]));
+    }
+#pragma unroll
+    for (int o = 1; o <= 2; o *= 2) {
+        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
 }
+// (bf16, two at a time; in the end (min, -max) as one pair, so that one shuffle carries both)
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void group_range(const uint32_t (&w)[4], float &mn, float &mx) {
+    const uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
+    const uint32_t hi = max2_nan(max2_nan(w[0], w[1]), max2_nan(w[2], w[3])) ^ 0x80008000u;
+    uint32_t r = min2_nan(kvq_prmt(lo, hi, 0x5410), kvq_prmt(lo, hi, 0x7632));
+    r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, 1));
+    r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, 2));
+    mn = __uint_as_float(r << 16);
+    mx = -__uint_as_float(r & 0xffff0000u);
+}
+
+// The integer nearest to each t[i] / step, ties to even, within [0, TOP], as floats.
+// The product with 1 / step (inv, approximate) is within 2^-13 of the quotient, so
+// its nearest integer n is the quotient's, or a neighbour of it where the quotient
+// lies within that of the border between the two. The residue t - n step says
+// which: it is exact in one multiply-add (step has 11 bits, n 8, and where n is not
+// 0 the last bit of t is no finer than 2^-24 of step), so n is nearest if it is
+// below half a step, and past half a step, or at it with n odd, the neighbour is.
+// inside: no t is far enough outside for a code outside [0, TOP].
+template <int TOP>
+__device__ __forceinline__ void nearest8(const float (&t)[8], float step, float inv, bool inside, float (&n)[8]) {
+    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
+    const float half = 0.5f * step;
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        n[i] = __fadd_rn(__fmaf_rn(t[i], inv, MAGIC), -MAGIC);
+        worst = fmaxf(worst, fabsf(__fmaf_rn(-n[i], step, t[i])));
+    }
+    if (!inside || worst >= half) {  // (ties, values past the range's ends)
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            n[i] = fminf(fmaxf(n[i], 0.f), float(TOP));
+            const float r = __fmaf_rn(-n[i], step, t[i]), e = fabsf(r);
+            const bool odd = int(n[i]) & 1;
+            if (e > half || (e == half && odd)) n[i] = fminf(fmaxf(n[i] + copysignf(1.f, r), 0.f), float(TOP));
+        }
+    }
+}
+
+// Where a thread's rows are. FAR (many tokens): a block takes one head, K or V, and
+// neighbouring rows are neighbouring positions (the packed rows of a head are one
+// run). Otherwise the heads of a token are neighbours.
+__host__ __device__ constexpr int rw_rows(bool far) { return far ? 4 : 2; }  // rows a thread has in flight
+
+template <bool FAR, int RPB, int U>
+struct RowWalk {
+    int kv, h[U], j[U], pos[U];  // pos: -1 where there is nothing to do
+    __device__ __forceinline__ RowWalk(const RwArgs &a, int n, int len, int row) {
+        kv = FAR ? blockIdx.y & 1 : blockIdx.y;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int r = blockIdx.x * (RPB * U) + row + u * RPB;
+            bool ok = true;
+            if (FAR) {
+                j[u] = r;
+                h[u] = blockIdx.y >> 1;
+            } else {
+                ok = r < a.n_rows;
+                j[u] = int(a.heads.div(uint32_t(ok ? r : 0)));
+                h[u] = (ok ? r : 0) - j[u] * a.nkv;
+            }
+            const int p = len - n + j[u];
+            pos[u] = ok && j[u] < n && p >= 0 && p < a.max_seq ? p : -1;
+        }
+    }
+};
 
 // Lanes of a row: lane e takes dims 8 e .. 8 e + 7, which is cells g = 2 a and 2 a
 // + 1 (a = e % 4) of group gr = e / 4; the four lanes of a group share its min
 // and max by shuffles. Cells of one g and neighbouring groups are neighbours in
 // the row, so lanes e and e ^ 4 exchange a cell and each stores a whole word (two
 // cells): the row leaves the warp as one run of bytes.
-template <typename T, int BITS, int HD>
+template <typename T, int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant__ RwArgs a) {
-    constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = 2;
-    const int s = blockIdx.z, kv = blockIdx.y, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
-    const int n = a.l.n(s), len = a.l.len(s);
-    const ll_kvq_rows &in = a.rows[kv];
-    const int r0 = blockIdx.x * (RPB * U) + threadIdx.x / LPR;
-    float x[U][8];
-    int pos[U], h[U];
+    constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);
+    const int s = blockIdx.z, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
+    const RowWalk<FAR, RPB, U> w(a, a.l.n(s), a.l.len(s), threadIdx.x / LPR);
+    const ll_kvq_rows &in = a.rows[w.kv];
+    uint32_t raw[U][2 * sizeof(T)];
+    const T *src = static_cast<const T *>(in.data) + s * in.seq + 8 * e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        int j = 0;
-        h[u] = 0;
-        pos[u] = row_of(a, r0 + u * RPB, n, len, j, h[u]);
-        if (pos[u] >= 0) {
-            load8(static_cast<const T *>(in.data) + s * in.seq + j * in.token + h[u] * in.head + 8 * e, x[u]);
+        if (w.pos[u] >= 0) {
+            load8(src + w.j[u] * in.token + w.h[u] * in.head, raw[u]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) x[u][i] = 0.f;
+            for (int i = 0; i < int(2 * sizeof(T)); i++) raw[u][i] = 0;
         }
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        float mn = x[u][0], mx = x[u][0];
-#pragma unroll
-        for (int i = 1; i < 8; i++) {
-            mn = min_nan(mn, x[u][i]);
-            mx = max_nan(mx, x[u][i]);
-        }
-#pragma unroll
-        for (int o = 1; o <= 2; o *= 2) {
-            mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        }
+        float mn, mx, x[8];
+        group_range(raw[u], mn, mx);
+        widen8(raw[u], x);
         // (values past the bound need no clamp of their own: their codes are clamped)
-        mn = min_nan(max_nan(mn, -BOUND), BOUND);
-        mx = min_nan(max_nan(mx, -BOUND), BOUND);
-        constexpr float TOP = float((1 << BITS) - 1);
-        const __half lo = __float2half_rn(mn);
-        const float lof = __half2float(lo);
-        const __half step = __float2half_rn(max_nan(__fdiv_rn(mx - lof, TOP), 0.f));
+        const float low = min_nan(max_nan(mn, -BOUND), BOUND), high = min_nan(max_nan(mx, -BOUND), BOUND);
+        constexpr int TOP = (1 << BITS) - 1;
+        const __half lo = __float2half_rn(low);
+        const float lof = __half2float(lo), d = __fsub_rn(high, lof);
+        // d / TOP, rounded once: the product with the rounded 1 / TOP, corrected by its residue (Markstein)
+        constexpr float R = 1.f / float(TOP);
+        const float y = __fmul_rn(d, R), quo = __fmaf_rn(__fmaf_rn(-float(TOP), y, d), R, y);
+        const __half step = __float2half_rn(max_nan(quo, 0.f));
         const float stf = __half2float(step);
         uint32_t c[2] = {0, 0};  // cells 2 ga, 2 ga + 1
         if (stf > 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float q = fminf(fmaxf(rintf(__fdiv_rn(x[u][i] - lof, stf)), 0.f), TOP);
-                c[i / 4] |= uint32_t(int(q)) << (BITS * (i % 4));
+            for (int i = 0; i < 8; i++) x[i] = __fsub_rn(x[i], lof);
+            float q[8], inv;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(stf));
+            const bool inside = (mn - lof) * inv > -0.25f && (mx - lof) * inv < float(TOP) + 0.25f;
+            nearest8<TOP>(x, stf, inv, inside, q);
+            // the codes of a cell as one number (two, in 8 bits), each below 2^16: exact in fp32
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const float *v = q + 4 * i;
+                if (BITS == 4)
+                    c[i] = uint32_t(fmaf(fmaf(fmaf(v[3], 16.f, v[2]), 16.f, v[1]), 16.f, v[0]));
+                else
+                    c[i] = kvq_prmt(uint32_t(fmaf(v[1], 256.f, v[0])), uint32_t(fmaf(v[3], 256.f, v[2])), 0x5410);
             }
         }
         const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? c[0] : c[1], 4);
-        if (pos[u] < 0) continue;
-        const int64_t row = s * a.seq_rows + int64_t(h[u]) * a.max_seq + pos[u];
+        if (w.pos[u] < 0) continue;
+        const int64_t row = s * a.seq_rows + int64_t(w.h[u]) * a.max_seq + w.pos[u];
         const int word = (2 * ga + (gr & 1)) * (GR / 2) + gr / 2;
         const uint32_t first = gr & 1 ? got : c[0], second = gr & 1 ? c[1] : got;  // groups gr & ~1, gr | 1
         if (BITS == 4)
-            reinterpret_cast<uint32_t *>(a.codes[kv])[row * (HD / 8) + word] = first | second << 16;
+            reinterpret_cast<uint32_t *>(a.codes[w.kv])[row * (HD / 8) + word] = kvq_prmt(first, second, 0x5410);
         else
-            reinterpret_cast<uint2 *>(a.codes[kv])[row * (HD / 8) + word] = make_uint2(first, second);
+            reinterpret_cast<uint2 *>(a.codes[w.kv])[row * (HD / 8) + word] = make_uint2(first, second);
         if (ga == 0)
-            a.params[kv][row * GR + gr] = uint32_t(__half_as_ushort(lo)) | uint32_t(__half_as_ushort(step)) << 16;
+            a.params[w.kv][row * GR + gr] = uint32_t(__half_as_ushort(lo)) | uint32_t(__half_as_ushort(step)) << 16;
     }
 }
 
 // The same walk backwards: each lane loads a word (two cells), exchanges one with
 // its partner and stores 8 dims as bf16.
-template <int BITS, int HD>
+template <int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__ RwArgs a) {
-    constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = 2;
-    const int s = blockIdx.z, kv = blockIdx.y, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
-    const int n = a.l.n(s), len = a.l.len(s);
-    const ll_kvq_rows &out = a.rows[kv];
-    const int r0 = blockIdx.x * (RPB * U) + threadIdx.x / LPR;
+    constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);
+    const int s = blockIdx.z, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
+    const RowWalk<FAR, RPB, U> at(a, a.l.n(s), a.l.len(s), threadIdx.x / LPR);
+    const ll_kvq_rows &out = a.rows[at.kv];
     const int word = (2 * ga + (gr & 1)) * (GR / 2) + gr / 2;
     uint2 w[U];
     uint32_t par[U];
-    int pos[U], h[U], j[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        j[u] = h[u] = 0;
-        pos[u] = row_of(a, r0 + u * RPB, n, len, j[u], h[u]);
         w[u] = make_uint2(0, 0);
         par[u] = 0;
-        if (pos[u] >= 0) {
-            const int64_t row = s * a.seq_rows + int64_t(h[u]) * a.max_seq + pos[u];
-            if (BITS == 4) {
-                const uint32_t v = reinterpret_cast<const uint32_t *>(a.codes[kv])[row * (HD / 8) + word];
-                w[u] = make_uint2(v & 0xffffu, v >> 16);
-            } else {
-                w[u] = reinterpret_cast<const uint2 *>(a.codes[kv])[row * (HD / 8) + word];
-            }
-            par[u] = a.params[kv][row * GR + gr];
+        if (at.pos[u] >= 0) {
+            const int64_t row = s * a.seq_rows + int64_t(at.h[u]) * a.max_seq + at.pos[u];
+            if (BITS == 4)
+                w[u].x = reinterpret_cast<const uint32_t *>(a.codes[at.kv])[row * (HD / 8) + word];
+            else
+                w[u] = reinterpret_cast<const uint2 *>(a.codes[at.kv])[row * (HD / 8) + word];
+            par[u] = a.params[at.kv][row * GR + gr];
         }
     }
+    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(out.data) + s * out.seq + 8 * e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        // the word is cell (2 ga + gr % 2) of groups gr & ~1 (x) and gr | 1 (y): keep
-        // this lane's group, hand the partner its own
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? w[u].x : w[u].y, 4);
-        if (pos[u] < 0) continue;
-        const uint32_t c0 = gr & 1 ? got : w[u].x, c1 = gr & 1 ? w[u].y : got;  // cells 2 ga, 2 ga + 1
-        __half2 v[4];  // (dim i, dim 4 + i)
-        if (BITS == 4)
-            kvq_codes4(c0 | c1 << 16, v);
-        else
-            kvq_codes8(c0, c1, v);
-        const __half2 lo = kvq_h2(kvq_prmt(par[u], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[u], 0, 0x3232));
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 p = __half22float2(__hfma2(st, v[i], lo));
-            f[i] = p.x;
-            f[4 + i] = p.y;
+        // the word is cell (2 ga + gr % 2) of groups gr & ~1 (first) and gr | 1: keep
+        // this lane's group, hand the partner its own; v = pairs (dim i, dim 4 + i)
+        __half2 v[4];
+        if (BITS == 4) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, w[u].x, 4);
+            kvq_codes4(gr & 1 ? kvq_prmt(got, w[u].x, 0x7632) : kvq_prmt(w[u].x, got, 0x5410), v);
+        } else {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? w[u].x : w[u].y, 4);
+            kvq_codes8(gr & 1 ? got : w[u].x, gr & 1 ? w[u].y : got, v);
         }
+        if (at.pos[u] < 0) continue;
+        const __half2 lo = kvq_h2(kvq_prmt(par[u], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[u], 0, 0x3232));
+        float2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) f[i] = __half22float2(__hfma2(st, v[i], lo));
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t *>(&b);
+        for (int i = 0; i < 2; i++) {
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(f[2 * i].x, f[2 * i + 1].x);
+            const __nv_bfloat162 b1 = __floats2bfloat162_rn(f[2 * i].y, f[2 * i + 1].y);
+            o[i] = *reinterpret_cast<const uint32_t *>(&b0);
+            o[2 + i] = *reinterpret_cast<const uint32_t *>(&b1);
         }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out.data) + s * out.seq + j[u] * out.token +
-                                   h[u] * out.head + 8 * e) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + at.j[u] * out.token + at.h[u] * out.head) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -222,17 +302,17 @@ RwArgs rw_args(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_rows &v
     a.max_seq = c.max_seq;
     a.nkv = c.n_kv_heads;
     a.n_rows = l.n_tok * c.n_kv_heads;
-    // many tokens: neighbouring threads take neighbouring positions of one head (the
-    // packed rows of a head are one run); few: the heads of a token
-    a.token_fast = l.n_tok >= 32;
-    a.inner = FastDiv(uint32_t(a.token_fast ? l.n_tok : c.n_kv_heads));
+    a.heads = FastDiv(uint32_t(c.n_kv_heads));
     a.l = l;
     return a;
 }
 
-dim3 rw_grid(const ll_kvq_cache &c, const RwArgs &a) {
-    const int per_block = RW_THREADS / (c.head_dim / 8) * 2;
-    return dim3((a.n_rows + per_block - 1) / per_block, 2, c.n_seq);
+// The walk by whole heads pays once a head's tokens fill a block's rows.
+bool rw_far(const ll_kvq_cache &c, const KvqLens &l) { return l.n_tok >= RW_THREADS / (c.head_dim / 8); }
+
+dim3 rw_grid(const ll_kvq_cache &c, const KvqLens &l, bool far) {
+    const int rows = far ? l.n_tok : l.n_tok * c.n_kv_heads, per_block = RW_THREADS / (c.head_dim / 8) * rw_rows(far);
+    return dim3((rows + per_block - 1) / per_block, far ? 2 * c.n_kv_heads : 2, c.n_seq);
 }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
@@ -242,20 +322,28 @@ int launched() { return cudaGetLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 int launch_kvq_write(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_rows &v, int type, const KvqLens &l,
                      cudaStream_t st) {
     const RwArgs a = rw_args(c, k, v, l);
-    const dim3 g = rw_grid(c, a);
+    const bool far = rw_far(c, l);
+    const dim3 g = rw_grid(c, l, far);
     kvq_dispatch(c, [&](auto bits, auto hd) {
+        constexpr int B = bits.value, H = hd.value;
         if (type == LL_F32)
-            k_kvq_write<float, bits.value, hd.value><<<g, RW_THREADS, 0, st>>>(a);
+            far ? k_kvq_write<float, B, H, true><<<g, RW_THREADS, 0, st>>>(a)
+                : k_kvq_write<float, B, H, false><<<g, RW_THREADS, 0, st>>>(a);
         else
-            k_kvq_write<__nv_bfloat16, bits.value, hd.value><<<g, RW_THREADS, 0, st>>>(a);
+            far ? k_kvq_write<__nv_bfloat16, B, H, true><<<g, RW_THREADS, 0, st>>>(a)
+                : k_kvq_write<__nv_bfloat16, B, H, false><<<g, RW_THREADS, 0, st>>>(a);
     });
     return launched();
 }
 
 int launch_kvq_read(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_rows &v, const KvqLens &l, cudaStream_t st) {
     const RwArgs a = rw_args(c, k, v, l);
-    const dim3 g = rw_grid(c, a);
-    kvq_dispatch(c, [&](auto bits, auto hd) { k_kvq_read<bits.value, hd.value><<<g, RW_THREADS, 0, st>>>(a); });
+    const bool far = rw_far(c, l);
+    const dim3 g = rw_grid(c, l, far);
+    kvq_dispatch(c, [&](auto bits, auto hd) {
+        constexpr int B = bits.value, H = hd.value;
+        far ? k_kvq_read<B, H, true><<<g, RW_THREADS, 0, st>>>(a) : k_kvq_read<B, H, false><<<g, RW_THREADS, 0, st>>>(a);
+    });
     return launched();
 }
 

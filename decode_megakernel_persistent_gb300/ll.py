@@ -329,14 +329,16 @@ def ll_init_kvq(cfg: ll_config, weights: dict, cache: "KVQCache", stream=None):
     return h
 
 
-def _kvq_call(fn, device, *args) -> None:
-    """One packed-cache call on torch's current stream of ``device``."""
+def _kvq_call(fn, device: int, *args) -> None:
+    """One packed-cache call on torch's current stream of ``device``. (A call's GPU work
+    takes a few microseconds, so its checks here are kept to as few lookups as they
+    need.)"""
     import torch
-    if device.index != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _kvq_call(fn, device, *args)
     err = ctypes.create_string_buffer(256)
-    rc = fn(*args, torch.cuda.current_stream().cuda_stream, err, 256)
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), err, 256)
     if rc != LL_OK:
         raise LLError(rc, err.value.decode())
 
@@ -344,41 +346,41 @@ def _kvq_call(fn, device, *args) -> None:
 def ll_kvq_write(cache: "KVQCache", k, v, lens, n_toks=None) -> None:
     """Quantise k and v [n_seq, n_tok, n_kv_heads, head_dim] (bf16 or fp32, any strides
     but the last) into ``cache`` as the last tokens of sequences ``lens`` long."""
-    import torch
-    if getattr(k, "dtype", None) not in (torch.bfloat16, torch.float32):
-        raise LLError(LL_ERR_ARG, f"k must be bfloat16 or float32, not {getattr(k, 'dtype', None)}")
-    kr, n_tok = cache._rows(k, "k", k.dtype, cache.n_kv_heads)
-    vr, _ = cache._rows(v, "v", k.dtype, cache.n_kv_heads, n_tok)
-    _kvq_call(lib().ll_kvq_write, cache.device, cache.ref, kr, vr, LL_F32 if k.dtype == torch.float32 else LL_BF16,
-              n_tok, cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks", True))
+    dtype = getattr(k, "dtype", None)
+    if dtype not in cache.in_types:
+        raise LLError(LL_ERR_ARG, f"k must be bfloat16 or float32, not {dtype}")
+    kr, n_tok = cache._rows(k, "k", dtype, cache.n_kv_heads)
+    vr, _ = cache._rows(v, "v", dtype, cache.n_kv_heads, n_tok)
+    _kvq_call(cache.lib.ll_kvq_write, cache.index, cache.ref, kr, vr, cache.in_types[dtype], n_tok,
+              cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks") if n_toks is not None else None)
 
 
 def ll_kvq_read(cache: "KVQCache", k_out, v_out, lens, n_toks=None) -> None:
     """The last tokens' rows of ``cache`` read back into k_out and v_out
     [n_seq, n_tok, n_kv_heads, head_dim] (bf16)."""
-    import torch
-    kr, n_tok = cache._rows(k_out, "k_out", torch.bfloat16, cache.n_kv_heads, written=True)
-    vr, _ = cache._rows(v_out, "v_out", torch.bfloat16, cache.n_kv_heads, n_tok, written=True)
-    _kvq_call(lib().ll_kvq_read, cache.device, cache.ref, kr, vr, n_tok, cache._lens(lens, "lens"),
-              cache._lens(n_toks, "n_toks", True))
+    kr, n_tok = cache._rows(k_out, "k_out", cache.bf16, cache.n_kv_heads, None, True)
+    vr, _ = cache._rows(v_out, "v_out", cache.bf16, cache.n_kv_heads, n_tok, True)
+    _kvq_call(cache.lib.ll_kvq_read, cache.index, cache.ref, kr, vr, n_tok, cache._lens(lens, "lens"),
+              cache._lens(n_toks, "n_toks") if n_toks is not None else None)
 
 
 def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=None, max_len: int = 0):
     """Causal attention of the last tokens' queries q [n_seq, n_tok, n_q_heads, head_dim]
     (bf16) over ``cache``; out like q (made if None: rows of padded tokens then hold zeros)."""
-    import torch
     if getattr(q, "ndim", 0) != 4:
         raise LLError(LL_ERR_ARG, "q must be [n_seq, n_tok, n_q_heads, head_dim]")
     heads = q.shape[2]
-    qr, n_tok = cache._rows(q, "q", torch.bfloat16, heads)
-    if scale is not None and not scale > 0:
+    qr, n_tok = cache._rows(q, "q", cache.bf16, heads)
+    if scale is None:
+        scale = 0.0
+    elif not scale > 0:
         raise LLError(LL_ERR_ARG, f"scale must be positive, not {scale}")
-    lp, np_ = cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks", True)
+    lp, np_ = cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks") if n_toks is not None else None
     if out is None:
+        import torch
         out = (torch.zeros if np_ else torch.empty)(q.shape, dtype=q.dtype, device=q.device)
-    o, _ = cache._rows(out, "out", torch.bfloat16, heads, n_tok, written=True)
-    _kvq_call(lib().ll_kvq_attention, cache.device, cache.ref, qr, heads, n_tok, lp, np_, int(max_len),
-              0.0 if scale is None else float(scale), o)
+    o, _ = cache._rows(out, "out", cache.bf16, heads, n_tok, True)
+    _kvq_call(cache.lib.ll_kvq_attention, cache.index, cache.ref, qr, heads, n_tok, lp, np_, max_len, scale, o)
     return out
 
 
@@ -648,6 +650,10 @@ class KVQCache:
         self.struct = ll_kvq_cache(_ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), int(rows.pop()), S, KV, hd, M,
                                    bits)
         self.ref = ctypes.byref(self.struct)
+        # what every call looks up
+        self.lib, self.index = lib(), dev.index
+        self.bf16, self.int32 = torch.bfloat16, torch.int32
+        self.in_types = {torch.bfloat16: LL_BF16, torch.float32: LL_F32}
 
     @classmethod
     def empty(cls, n_seq: int, n_kv_heads: int, max_seq: int, head_dim: int, bits: int, device="cuda"):
@@ -662,32 +668,30 @@ class KVQCache:
 
     def _rows(self, t, name: str, dtype, heads: int, n_tok=None, written: bool = False):
         """t as an ll_kvq_rows reference, and its tokens."""
-        if not getattr(t, "is_cuda", False):
-            raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor")
+        if getattr(t, "device", None) != self.device:
+            raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor on {self.device}, the cache's device")
         if t.dtype != dtype:
             raise LLError(LL_ERR_ARG, f"{name} must be {dtype}, not {t.dtype}")
-        if t.device != self.device:
-            raise LLError(LL_ERR_ARG, f"{name} is on {t.device}, the cache on {self.device}")
-        shape, st = t.shape, t.stride()
-        if len(shape) != 4 or shape[0] != self.n_seq or shape[2] != heads or shape[3] != self.head_dim or (
-                n_tok is not None and shape[1] != n_tok):
+        shape = t.shape
+        tokens = n_tok if n_tok is not None else shape[1] if len(shape) == 4 else 0
+        if shape != (self.n_seq, tokens, heads, self.head_dim):
             raise LLError(LL_ERR_ARG, f"{name} is {tuple(shape)}, the call needs "
-                                      f"[{self.n_seq}, {n_tok or 'n_tok'}, {heads}, {self.head_dim}]")
-        if st[3] != 1:
+                                      f"[{self.n_seq}, {tokens or 'n_tok'}, {heads}, {self.head_dim}]")
+        seq, token, head, last = t.stride()
+        if last != 1:
             raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
         if written:  # no two rows of an output may share memory
             reach = self.head_dim
-            for stride, size in sorted((st[i], shape[i]) for i in range(3) if shape[i] > 1):
-                if stride < reach:
-                    raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
-                reach += stride * (size - 1)
-        return ctypes.byref(ll_kvq_rows(t.data_ptr(), st[0], st[1], st[2])), shape[1]
+            for stride, size in sorted(((seq, self.n_seq), (token, tokens), (head, heads))):
+                if size > 1:
+                    if stride < reach:
+                        raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
+                    reach += stride * (size - 1)
+        return ctypes.byref(ll_kvq_rows(t.data_ptr(), seq, token, head)), tokens
 
-    def _lens(self, t, name: str, optional: bool = False) -> int:
-        import torch
-        if t is None and optional:
-            return 0
-        _need(t, name, torch.int32, self.n_seq, self.device, optional=False)
+    def _lens(self, t, name: str) -> int:
+        if getattr(t, "device", None) != self.device or t.dtype != self.int32 or t.shape != (self.n_seq,) or not t.is_contiguous():
+            raise LLError(LL_ERR_ARG, f"{name} must be a contiguous int32 tensor [{self.n_seq}] on {self.device}")
         return t.data_ptr()
 
     def write(self, k, v, lens, n_toks=None) -> None:

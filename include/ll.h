@@ -306,11 +306,11 @@ int ll_decode_step_static(const ll_config *cfg, const ll_weights *w, uint16_t *k
  *     fp16(lo + step * code)                      (one rounding).
  * Writing takes, over the group's values x (each clamped to +-60000):
  *     lo = fp16(min x),  step = fp16((max x - lo) / (2^bits - 1)),
- *     code = (x - lo) / step rounded to the nearest integer, ties to even, and
- *            clamped to [0, 2^bits - 1]; 0 where step is 0 (it is never below),
- * in fp32 arithmetic, so a value is read back within half a step of itself, up
- * to the fp16 roundings of lo, step and the value. A group holding a NaN reads
- * back as NaN.
+ *     code = the integer nearest to (x - lo) / step, ties to even, clamped to
+ *            [0, 2^bits - 1]; 0 where step is 0 (it is never below),
+ * the differences and step's quotient in fp32. So a value is read back within half
+ * a step of itself, up to the fp16 roundings of lo, step and the value. A group
+ * holding a NaN reads back as NaN.
  *
  * Codes of a row: head_dim * bits / 8 bytes. Dim d = 32 gr + 4 g + i (group gr,
  * g < 8, i < 4) is element (g * (head_dim / 32) + gr) * 4 + i; 4-bit elements sit

@@ -16,8 +16,10 @@ def quantise(x, bits):
     x = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32).clamp(-BOUND, BOUND)  # (keeps NaN)
     lo = x.amin(-1).half()  # (NaN if any is)
     step = ((x.amax(-1) - lo.float()) / top).clamp(min=0).half()
-    lf, sf = lo.float()[..., None], step.float()[..., None]
-    code = torch.where(sf > 0, ((x - lf) / sf).round().clamp(0, top), torch.zeros_like(x))
+    # the integer nearest to (x - lo) / step: the difference in fp32, its quotient in fp64, where
+    # 24 bits by 11 cannot round onto a border between two integers
+    t, sf = (x - lo.float()[..., None]).double(), step.double()[..., None]
+    code = torch.where(sf > 0, (t / sf).round().clamp(0, top), torch.zeros_like(t))
     return lo, step, torch.nan_to_num(code, nan=0.0).long()
 
 

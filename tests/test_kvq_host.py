@@ -210,6 +210,12 @@ def test_binding_rows_checks():
               torch.zeros(2, dtype=torch.int32)):
         with pytest.raises(ll.LLError):
             c._lens(t, "lens")
+        with pytest.raises(ll.LLError):
+            ll.ll_kvq_write(c, good, good, t)
+        with pytest.raises(ll.LLError):
+            ll.ll_kvq_read(c, good, good, t)
+        with pytest.raises(ll.LLError):
+            ll.ll_kvq_attention(c, good, t)
     with pytest.raises(ll.LLError):
         ll.ll_kvq_attention(c, None, lens)
     with pytest.raises(ll.LLError):
