@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
     const int s = blockIdx.z, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
     const RowWalk<FAR, RPB, U> at(a, a.l.n(s), a.l.len(s), threadIdx.x / LPR);
     const ll_kvq_rows &out = a.rows[at.kv];
+    const KvqConsts consts;
     const int word = (2 * ga + (gr & 1)) * (GR / 2) + gr / 2;
     uint2 w[U];
     uint32_t par[U];
@@ -268,10 +269,10 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
         __half2 v[4];
         if (BITS == 4) {
             const uint32_t got = __shfl_xor_sync(0xffffffffu, w[u].x, 4);
-            kvq_codes4(gr & 1 ? kvq_prmt(got, w[u].x, 0x7632) : kvq_prmt(w[u].x, got, 0x5410), v);
+            kvq_codes4(gr & 1 ? kvq_prmt(got, w[u].x, 0x7632) : kvq_prmt(w[u].x, got, 0x5410), consts, v);
         } else {
             const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? w[u].x : w[u].y, 4);
-            kvq_codes8(gr & 1 ? got : w[u].x, gr & 1 ? w[u].y : got, v);
+            kvq_codes8(gr & 1 ? got : w[u].x, gr & 1 ? w[u].y : got, consts, v);
         }
         if (at.pos[u] < 0) continue;
         const __half2 lo = kvq_h2(kvq_prmt(par[u], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[u], 0, 0x3232));

@@ -46,19 +46,41 @@ constexpr float HOLD = 8.f;
 
 __device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
-// BYTES (16 or 8) to shared memory, or zeros when !ok.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool ok) {
-    const int n = ok ? BYTES : 0;
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// A run of bytes to shared memory by the copy engine (both addresses and the size
+// multiples of 16), counted by an mbarrier.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits for a phase for at most a second: false when it has not come by then.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        for (int i = 0; i < 64; i++)
+            if (bar_try(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < 1000000000ull);
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    return bar_try(bar, parity) || bar_wait_long(bar, parity);
 }
 
 // D += A B: A 16 x 16 (row), B 16 x 8 (col), fp16 in, fp32 sums.
@@ -115,9 +137,10 @@ __device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head,
 //
 // Grid (splits, KV heads, sequences), the splits of a (sequence, KV head) one
 // cluster. A block's keys are cut into tiles; its warps take them in turn, each
-// with a ring of its own in shared memory (cp.async, no block barriers), and
-// its own m, l and O. At the end the warps of a block, then the blocks of the
-// cluster (through distributed shared memory), merge.
+// with a ring of its own in shared memory, which one lane fills by bulk copies
+// (a tile of a head's codes is one run of bytes, its parameters another), and its
+// own m, l and O: no block barriers. At the end the warps of a block, then the blocks
+// of the cluster (through distributed shared memory), merge.
 //
 // A tile of 16 keys is the A operand of S^T = K Q^T (keys x rows, 8 query rows per
 // product) and, transposed, of O^T = V^T P^T (dims x rows): with the keys as the
@@ -125,13 +148,16 @@ __device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head,
 // rows, and few rows cost few products. A group of 4 dims by 8 lanes is how the
 // format lays a row out: lane (g, t) finds the dims of its K fragment (k = 2t, 2t +
 // 1, 2t + 8, 2t + 9 of each product, in an order of our own that Q's fragment
-// shares) in cells 2t and 2t + 1, and those of its V fragment in cell g.
+// shares) in cells 2t and 2t + 1, and those of its V fragment in cell g. What a
+// pair of a K fragment holds are the same dim of two neighbouring groups, which
+// share a packed word; of a V fragment, one dim of two keys.
 template <int BITS, int HD>
 struct DecodeShape {
     static constexpr int NW = 8;
     static constexpr int RB = HD * BITS / 8, PB = HD / 8;        // bytes of a row's codes and parameters
     static constexpr int TILE = RB == 128 ? 16 : 32;             // keys
-    static constexpr int STAGE = TILE * 2 * (RB + PB);
+    static constexpr int PAR = TILE * PB + 16;                   // a tile's parameters, from an even row on
+    static constexpr int STAGE = 2 * (TILE * RB + PAR);
     static constexpr int STAGES = 104 * 1024 / (NW * STAGE) < 4 ? 104 * 1024 / (NW * STAGE) : 4;  // two blocks per SM
     static constexpr int SMEM = NW * STAGES * STAGE;
     static_assert(STAGES >= 2, "a ring needs two stages");
@@ -139,25 +165,22 @@ struct DecodeShape {
 
 // The key of a block of 8 that is row r of the operand: rows 2t are keys 0..3 and
 // rows 2t + 1 keys 7..4, which spreads both the K reads (rows g) and the V reads
-// (rows 2t, then 2t + 1) over all banks.
+// (rows 2t, then 2t + 1) over the banks (32-byte rows: no conflicts; 64: K none, V
+// two to a bank; 128: two and four, with the shared-memory pipe half idle).
 __device__ __forceinline__ int key_of(int r) { return r & 1 ? 7 - (r >> 1) : r >> 1; }
-
-// 16-byte chunk c of row r in a ring stage.
-template <int RB>
-__device__ __forceinline__ int swz(int r, int c) {
-    return RB == 32 ? c : RB == 64 ? c ^ (r & 2) : c ^ (((r & 3) << 1) | ((r >> 2) & 1));
-}
 
 template <int BITS, int HD, int NC, typename QT>
 __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ AttnArgs a) {
     using S = DecodeShape<BITS, HD>;
     constexpr int NW = S::NW, RB = S::RB, PB = S::PB, TILE = S::TILE, NT = TILE / 16, GR = HD / 32, COLS = 8 * NC;
-    constexpr int CH = RB / 16;
+    constexpr int GP = GR / 2, PAR = S::PAR;  // pairs of groups
     static_assert(NW * COLS * HD * 4 <= S::SMEM, "the merge fits in the ring's memory");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[NW][COLS][2];  // the warps' m and l
     __shared__ float s_cml[COLS][2];     // the block's
+    __shared__ uint64_t s_full[NW][S::STAGES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, C = gridDim.x, rank = blockIdx.x;
     const int n = a.l.n(s), len = a.l.len(s);
     if (n == 0) return;
@@ -169,34 +192,44 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
     const int tiles = (limit + TILE - 1) / TILE;
     const int t0 = int(int64_t(tiles) * rank / C), t1 = int(int64_t(tiles) * (rank + 1) / C);
     uint8_t *const ring = smem + warp * (S::STAGES * S::STAGE);
-    auto load = [&](int ti, int stage) {
-        const int k0 = ti * TILE, valid = limit - k0;
-        const uint32_t dst = sptr(ring + stage * S::STAGE);
-        const uint8_t *kc = a.kc + (row0 + k0) * RB, *vc = a.vc + (row0 + k0) * RB;
-#pragma unroll
-        for (int i = lane; i < TILE * CH; i += 32) {
-            const int r = i / CH, c = i % CH;
-            const bool ok = r < valid;
-            const int64_t src = ok ? i * 16 : 0;
-            const uint32_t to = dst + r * RB + swz<RB>(r, c) * 16;
-            cp_async<16>(to, kc + src, ok);
-            cp_async<16>(to + TILE * RB, vc + src, ok);
+    const uint32_t full = sptr(s_full[warp]);
+    // rows of 8 bytes of parameters are copied from an even row on (skew: the first one's place); the
+    // row behind the last position of all may not exist, so an odd last one is fetched when its tile is used
+    const int skew = PB == 8 ? int(row0 & 1) : 0;
+    const bool odd_end = PB == 8 && limit == a.max_seq && ((skew + limit) & 1);
+    const int edge_from = min(first + 1, limit) - int(odd_end);
+    // (lane 0; tiles come in order, NW apart: the addresses move by constants)
+    const uint8_t *kc = a.kc + (row0 + (t0 + warp) * TILE) * RB, *vc = a.vc + (row0 + (t0 + warp) * TILE) * RB;
+    const uint32_t *kp = a.kp + (row0 + (t0 + warp) * TILE - skew) * GR, *vp = a.vp + (row0 + (t0 + warp) * TILE - skew) * GR;
+    auto load = [&](int ti, uint32_t dst, uint32_t bar) {
+        const int count = min(TILE, limit - ti * TILE);
+        uint32_t par = (count + skew) * PB;
+        if (PB == 8) par = (odd_end && ti * TILE + count == limit ? par : par + 8) & ~15u;
+        bar_expect(bar, 2 * (count * RB + par));
+        bulk_copy(dst, kc, count * RB, bar);
+        bulk_copy(dst + TILE * RB, vc, count * RB, bar);
+        if (PB != 8 || par) {
+            bulk_copy(dst + 2 * TILE * RB, kp, par, bar);
+            bulk_copy(dst + 2 * TILE * RB + PAR, vp, par, bar);
         }
-        if (lane < TILE) {
-            const bool ok = lane < valid;
-            const int64_t src = (row0 + k0 + (ok ? lane : 0)) * GR;
-            cp_async<PB>(dst + 2 * TILE * RB + lane * PB, a.kp + src, ok);
-            cp_async<PB>(dst + 2 * TILE * RB + TILE * PB + lane * PB, a.vp + src, ok);
-        }
+        kc += NW * TILE * RB;
+        vc += NW * TILE * RB;
+        kp += NW * TILE * GR;
+        vp += NW * TILE * GR;
     };
+    const uint32_t ring0 = sptr(ring);
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < S::STAGES - 1; i++) {
-        if (t0 + warp + i * NW < t1) load(t0 + warp + i * NW, i);
-        cp_commit();
+        for (int i = 0; i < S::STAGES; i++) bar_init(full + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < S::STAGES - 1; i++)
+            if (t0 + warp + i * NW < t1) load(t0 + warp + i * NW, ring0 + i * S::STAGE, full + 8 * i);
     }
+    __syncwarp();
 
-    // q as B fragments: k-step (gr, ks), row col = 8 nc + g: its dims 32 gr + 8 t + 2 ks (+ 4, + 1, + 5)
-    uint32_t qf[NC][GR][2][2];
+    // q as B fragments: (gp, b, i) the pair of dims 64 gp + 4 (2 t + b) + i and 32 on, of row 8 nc + g
+    uint32_t qf[NC][GP][2][4];
     float fac[NC][2];  // log2 score units per product unit, of rows 8 nc + 2 t and + 1
     int last[NC][2];   // the last position those rows see
 #pragma unroll
@@ -230,12 +263,9 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
         last[nc][0] = first + (8 * nc + 2 * t) / a.group;
         last[nc][1] = first + (8 * nc + 2 * t + 1) / a.group;
 #pragma unroll
-        for (int gr = 0; gr < GR; gr++)
+        for (int gp = 0; gp < GP; gp++)
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                qf[nc][gr][ks][0] = pack_h2(v[gr][2 * ks] * down, v[gr][2 * ks + 4] * down);
-                qf[nc][gr][ks][1] = pack_h2(v[gr][2 * ks + 1] * down, v[gr][2 * ks + 5] * down);
-            }
+            for (int i = 0; i < 8; i++) qf[nc][gp][i >> 2][i & 3] = pack_h2(v[2 * gp][i] * down, v[2 * gp + 1][i] * down);
     }
 
     float o[NC][2 * GR][4], m[NC][2], l[NC][2];
@@ -250,32 +280,52 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
     }
 
     int stage = 0;
+    uint32_t phase = 0;  // the parity that the ring's stages complete next
+    bool lost = false;
     for (int ti = t0 + warp; ti < t1; ti += NW) {
-        cp_wait<S::STAGES - 2>();
-        __syncwarp();  // the tile is here for every lane, and every lane is done with the tile before
-        {
-            const int ahead = ti + (S::STAGES - 1) * NW;
-            if (ahead < t1) load(ahead, stage == 0 ? S::STAGES - 1 : stage - 1);
-            cp_commit();
+        __syncwarp();  // every lane is done with the tile before: its stage is free
+        if (lane == 0 && ti + (S::STAGES - 1) * NW < t1) {
+            const int to = stage == 0 ? S::STAGES - 1 : stage - 1;
+            load(ti + (S::STAGES - 1) * NW, ring0 + to * S::STAGE, full + 8 * to);
+        }
+        if (!bar_wait(full + 8 * stage, phase)) {  // (then the other copies in flight are waited for as long)
+            for (int i = 1; i < S::STAGES && ti + i * NW < t1; i++) {
+                const int at = stage + i;
+                bar_wait(full + 8 * (at % S::STAGES), at < S::STAGES ? phase : phase ^ 1);
+            }
+            lost = true;
+            break;
         }
         const uint8_t *kt = ring + stage * S::STAGE, *vt = kt + TILE * RB;
-        const uint32_t *kpar = reinterpret_cast<const uint32_t *>(vt + TILE * RB), *vpar = kpar + TILE * GR;
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+        const uint32_t *kpar = reinterpret_cast<const uint32_t *>(vt + TILE * RB) + skew * GR, *vpar = kpar + PAR / 4;
+        if (++stage == S::STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
 
-        // A tile in which some row's last position lies (or the tile's zeros begin).
-        // V rows holding a NaN there must reach only the rows that see them: they
-        // enter the product as zeros, and the rows that see them get NaN below.
+        // A tile in which some row's last position lies (or the sequence ends). Its keys
+        // past the end become zeros. V rows holding a NaN there must reach only the rows
+        // that see them: they enter the product as zeros, and the rows that see them
+        // get NaN below.
         const int k0 = ti * TILE;
-        const bool edge = k0 + TILE > min(first + 1, limit);
+        const bool edge = k0 + TILE > edge_from;
         uint32_t v_nan[GR];
         if (edge) {
-            uint32_t *const vp = const_cast<uint32_t *>(vpar);
+            uint32_t *const ks = const_cast<uint32_t *>(kpar), *const vs = const_cast<uint32_t *>(vpar);
+            const int valid = limit - k0;
+            if (odd_end && valid <= TILE && lane < GR) {
+                ks[(valid - 1) * GR + lane] = a.kp[(row0 + limit - 1) * GR + lane];
+                vs[(valid - 1) * GR + lane] = a.vp[(row0 + limit - 1) * GR + lane];
+            }
+            __syncwarp();
 #pragma unroll
             for (int gr = 0; gr < GR; gr++) {
-                const bool nan = lane < TILE && kvq_is_nan(vp[lane * GR + gr]);
+                const bool nan = lane < TILE && lane < valid && kvq_is_nan(vs[lane * GR + gr]);
                 v_nan[gr] = __ballot_sync(0xffffffffu, nan);
-                if (nan) vp[lane * GR + gr] = 0u;
+                if (lane < TILE && lane >= valid) ks[lane * GR + gr] = 0u;
+                if (nan || (lane < TILE && lane >= valid)) vs[lane * GR + gr] = 0u;
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the stage is copied into again)
             __syncwarp();
         }
 
@@ -298,7 +348,7 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
                 } else {
 #pragma unroll
                     for (int i = 0; i < RB / 64; i++) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(kt + r * RB + swz<RB>(r, RB / 64 * t + i) * 16);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(kt + r * RB + RB / 4 * t + 16 * i);
                         w[hf][4 * i] = u.x;
                         w[hf][4 * i + 1] = u.y;
                         w[hf][4 * i + 2] = u.z;
@@ -309,24 +359,32 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
                 for (int gr = 0; gr < GR; gr++) par[hf][gr] = kpar[r * GR + gr];
             }
 #pragma unroll
-            for (int gr = 0; gr < GR; gr++) {
-                __half2 c[2][4];
+            for (int gp = 0; gp < GP; gp++) {
+                __half2 lo[2], st[2];
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    if (BITS == 4)  // two groups to a word: cell 2t in word gr / 2, cell 2t + 1 GR / 2 words on
-                        kvq_codes4(kvq_prmt(w[hf][gr / 2], w[hf][GR / 2 + gr / 2], gr & 1 ? 0x7632 : 0x5410), c[hf]);
-                    else
-                        kvq_codes8(w[hf][gr], w[hf][GR + gr], c[hf]);
-                    const __half2 lo = kvq_h2(kvq_prmt(par[hf][gr], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[hf][gr], 0, 0x3232));
-#pragma unroll
-                    for (int i = 0; i < 4; i++) c[hf][i] = __hfma2(st, c[hf][i], lo);
+                    lo[hf] = kvq_h2(kvq_prmt(par[hf][2 * gp], par[hf][2 * gp + 1], 0x5410));
+                    st[hf] = kvq_h2(kvq_prmt(par[hf][2 * gp], par[hf][2 * gp + 1], 0x7632));
                 }
 #pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
-                    const uint32_t af[4] = {kvq_u32(c[0][2 * ks]), kvq_u32(c[1][2 * ks]), kvq_u32(c[0][2 * ks + 1]),
-                                            kvq_u32(c[1][2 * ks + 1])};
+                for (int b = 0; b < 2; b++) {
+                    __half2 c[2][4];
 #pragma unroll
-                    for (int nc = 0; nc < NC; nc++) mma(sc[mt][nc], af, qf[nc][gr][ks][0], qf[nc][gr][ks][1]);
+                    for (int hf = 0; hf < 2; hf++) {
+                        if (BITS == 4)
+                            kvq_codes4(w[hf][b * GP + gp], consts, c[hf]);
+                        else
+                            kvq_codes8(w[hf][b * GR + 2 * gp], w[hf][b * GR + 2 * gp + 1], consts, c[hf]);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) c[hf][i] = __hfma2(st[hf], c[hf][i], lo[hf]);
+                    }
+#pragma unroll
+                    for (int ks = 0; ks < 2; ks++) {
+                        const uint32_t af[4] = {kvq_u32(c[0][2 * ks]), kvq_u32(c[1][2 * ks]), kvq_u32(c[0][2 * ks + 1]),
+                                                kvq_u32(c[1][2 * ks + 1])};
+#pragma unroll
+                        for (int nc = 0; nc < NC; nc++) mma(sc[mt][nc], af, qf[nc][gp][b][2 * ks], qf[nc][gp][b][2 * ks + 1]);
+                    }
                 }
             }
         }
@@ -400,11 +458,11 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
                 if (RB == 32) {
                     w[i][0] = *reinterpret_cast<const uint32_t *>(p + 4 * g);
                 } else if (RB == 64) {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(p + swz<RB>(r, g >> 1) * 16 + 8 * (g & 1));
+                    const uint2 u = *reinterpret_cast<const uint2 *>(p + 8 * g);
                     w[i][0] = u.x;
                     w[i][1 % (RB / 32)] = u.y;
                 } else {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(p + swz<RB>(r, g) * 16);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(p + 16 * g);
                     w[i][0] = u.x;
                     w[i][1 % (RB / 32)] = u.y;
                     w[i][2 % (RB / 32)] = u.z;
@@ -419,9 +477,9 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
                     if (BITS == 4)
-                        kvq_codes4(kvq_prmt(w[2 * hf][gr / 2], w[2 * hf + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), c[hf]);
+                        kvq_codes4(kvq_prmt(w[2 * hf][gr / 2], w[2 * hf + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), consts, c[hf]);
                     else
-                        kvq_codes8(w[2 * hf][gr], w[2 * hf + 1][gr], c[hf]);
+                        kvq_codes8(w[2 * hf][gr], w[2 * hf + 1][gr], consts, c[hf]);
                     const __half2 lo = kvq_h2(kvq_prmt(par[2 * hf][gr], par[2 * hf + 1][gr], 0x5410));
                     const __half2 st = kvq_h2(kvq_prmt(par[2 * hf][gr], par[2 * hf + 1][gr], 0x7632));
 #pragma unroll
@@ -453,7 +511,14 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
                 }
         }
     }
-    cp_wait<0>();
+    if (lost) {  // a copy that never came: the rows have no result
+#pragma unroll
+        for (int nc = 0; nc < NC; nc++)
+#pragma unroll
+            for (int i = 0; i < 2 * GR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[nc][i][e] = __uint_as_float(0x7fffffffu);
+    }
     __syncthreads();  // every ring is read: its memory takes the warps' results
 
     float *const red = reinterpret_cast<float *>(smem);  // [NW][COLS][HD]
@@ -568,6 +633,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
     __shared__ float s_ml[CK_ROWS][2];
     __shared__ uint32_t s_nan[GR][2];  // keys of the tile whose V holds a NaN, per group
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, rank = blockIdx.x % C;
     const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group, first = len - n;
     // the row tiles with the most keys come first
@@ -667,9 +733,9 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
                 }
                 __half2 v[4];
                 if (BITS == 4)
-                    kvq_codes4(w[kv][i].x, v);
+                    kvq_codes4(w[kv][i].x, consts, v);
                 else
-                    kvq_codes8(w[kv][i].x, w[kv][i].y, v);
+                    kvq_codes8(w[kv][i].x, w[kv][i].y, consts, v);
                 const __half2 lo = kvq_h2(kvq_prmt(p0, p1, 0x5410)), st = kvq_h2(kvq_prmt(p0, p1, 0x7632));
                 uint4 u;
                 u.x = kvq_u32(__hfma2(st, v[0], lo));
