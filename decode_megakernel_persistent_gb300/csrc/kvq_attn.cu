@@ -103,6 +103,16 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return kvq_u32(__floats2half2_rn(lo, hi)); }
 
+__device__ __forceinline__ void load_q8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load_q8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
 __device__ __forceinline__ float q_at(const float *p) { return *p; }
 __device__ __forceinline__ float q_at(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
@@ -139,8 +149,9 @@ __device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head,
 // cluster. A block's keys are cut into tiles; its warps take them in turn, each
 // with a ring of its own in shared memory, which one lane fills by bulk copies
 // (a tile of a head's codes is one run of bytes, its parameters another), and its
-// own m, l and O: no block barriers. At the end the warps of a block, then the blocks
-// of the cluster (through distributed shared memory), merge.
+// own m, l and O: no block barriers. At the end the warps of a block merge, then the
+// blocks of the cluster: each owns a share of the outputs, and sends the others their
+// shares of its own (stores into their shared memory, one cluster barrier).
 //
 // A tile of 16 keys is the A operand of S^T = K Q^T (keys x rows, 8 query rows per
 // product) and, transposed, of O^T = V^T P^T (dims x rows): with the keys as the
@@ -177,16 +188,35 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
     static_assert(NW * COLS * HD * 4 <= S::SMEM, "the merge fits in the ring's memory");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[NW][COLS][2];  // the warps' m and l
-    __shared__ float s_cml[COLS][2];     // the block's
+    __shared__ float s_recv[COLS * HD];  // the cluster's sums of this block's share of the outputs, by rank
+    __shared__ float s_rml[16][COLS][2]; // and the ranks' m and l
     __shared__ uint64_t s_full[NW][S::STAGES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, C = gridDim.x, rank = blockIdx.x;
+    // q first, while the lengths are on their way: (nc) row 8 nc + g, this lane's dims 32 gr + 8 t ..
+    float qv[NC][GR][8];
+#pragma unroll
+    for (int nc = 0; nc < NC; nc++) {
+        const int r = 8 * nc + g;
+        const bool ok = r < a.l.n_tok * a.group;
+        const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + (ok ? r / a.group : 0) * a.q_tok +
+                      (h * a.group + (ok ? r % a.group : 0)) * a.q_head + 8 * t;
+#pragma unroll
+        for (int gr = 0; gr < GR; gr++) load_q8(q + 32 * gr, qv[nc][gr]);
+        if (!ok) {
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) qv[nc][gr][i] = 0.f;
+        }
+    }
     const int n = a.l.n(s), len = a.l.len(s);
     if (n == 0) return;
     const int rows = n * a.group, first = len - n;  // query rows, and the first token's position
     const int limit = min(len, a.max_seq);          // no token sees a position from here on
     const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first remote store)
 
     // this block's tiles
     const int tiles = (limit + TILE - 1) / TILE;
@@ -234,21 +264,8 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
     int last[NC][2];   // the last position those rows see
 #pragma unroll
     for (int nc = 0; nc < NC; nc++) {
-        const int r = 8 * nc + g;
-        float v[GR][8], mx = 0.f;
-        if (r < rows) {
-            const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + (r / a.group) * a.q_tok +
-                          (h * a.group + r % a.group) * a.q_head + 8 * t;
-#pragma unroll
-            for (int gr = 0; gr < GR; gr++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[gr][i] = q_at(q + 32 * gr + i);
-        } else {
-#pragma unroll
-            for (int gr = 0; gr < GR; gr++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[gr][i] = 0.f;
-        }
+        const float(&v)[GR][8] = qv[nc];
+        float mx = 0.f;
 #pragma unroll
         for (int gr = 0; gr < GR; gr++)
 #pragma unroll
@@ -542,8 +559,10 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
     }
     __syncthreads();
     // the block's warps: pairs of dims, NW partial sums each, against the largest m
-    const int head0 = h * a.group;
-    for (int i = threadIdx.x; i < rows * (HD / 2); i += blockDim.x) {
+    const int head0 = h * a.group, pairs = rows * (HD / 2), share = (pairs + C - 1) / C;
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the cluster's blocks have all begun
+    cg::cluster_group cl = cg::this_cluster();
+    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
         const int col = i / (HD / 2), d = 2 * (i % (HD / 2));
         float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
@@ -560,36 +579,39 @@ __global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ A
         if (C == 1) {
             const float inv = M == -INFINITY ? 0.f : 1.f / L;
             put_out(a.out, s, col / a.group, head0 + col % a.group, d, x * inv, y * inv);
-        } else {  // (each element is read and written by this thread alone)
-            *reinterpret_cast<float2 *>(&red[col * HD + d]) = make_float2(x, y);
-            if (d == 0) {
-                s_cml[col][0] = M;
-                s_cml[col][1] = L;
-            }
+        } else {
+            const int owner = i / share;
+            float2 *to = reinterpret_cast<float2 *>(s_recv) + rank * share + (i - owner * share);
+            *cl.map_shared_rank(to, owner) = make_float2(x, y);
         }
     }
     if (C == 1) return;
-    cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
-    // the cluster's blocks: each merges its share of the outputs from all of them
-    for (int i = rank * int(blockDim.x) + int(threadIdx.x); i < rows * (HD / 2); i += C * blockDim.x) {
-        const int col = i / (HD / 2), d = 2 * (i % (HD / 2));
+    for (int i = threadIdx.x; i < rows * C; i += blockDim.x) {  // every block gets every row's m and l
+        const int col = i / C;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; w++) M = fmaxf(M, s_ml[w][col][0]);
+#pragma unroll
+        for (int w = 0; w < NW; w++)
+            L = fmaf(s_ml[w][col][1], s_ml[w][col][0] == -INFINITY ? 0.f : ex2(s_ml[w][col][0] - M), L);
+        *reinterpret_cast<float2 *>(cl.map_shared_rank(&s_rml[rank][col][0], i % C)) = make_float2(M, L);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int k = threadIdx.x; k < share && rank * share + k < pairs; k += blockDim.x) {
+        const int i = rank * share + k, col = i / (HD / 2), d = 2 * (i % (HD / 2));
         float M = -INFINITY, L = 0.f, x = 0.f, y = 0.f;
+        for (int c = 0; c < C; c++) M = fmaxf(M, s_rml[c][col][0]);
+#pragma unroll 4
         for (int c = 0; c < C; c++) {
-            const float *ml = cl.map_shared_rank(&s_cml[col][0], c);
-            const float mc = ml[0], lc = ml[1];
-            const float2 v = *reinterpret_cast<const float2 *>(cl.map_shared_rank(&red[col * HD + d], c));
-            const float Mn = fmaxf(M, mc);
-            const float f0 = M == -INFINITY ? 0.f : ex2(M - Mn), f1 = mc == -INFINITY ? 0.f : ex2(mc - Mn);
-            L = L * f0 + lc * f1;
-            x = x * f0 + v.x * f1;
-            y = y * f0 + v.y * f1;
-            M = Mn;
+            const float mc = s_rml[c][col][0], f = mc == -INFINITY ? 0.f : ex2(mc - M);
+            const float2 v = reinterpret_cast<const float2 *>(s_recv)[c * share + k];
+            L = fmaf(s_rml[c][col][1], f, L);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
         }
         const float inv = M == -INFINITY ? 0.f : 1.f / L;
         put_out(a.out, s, col / a.group, head0 + col % a.group, d, x * inv, y * inv);
     }
-    cl.sync();  // no block leaves while another reads its memory
 }
 
 // ---- many query rows ---------------------------------------------------------------
@@ -922,13 +944,21 @@ int launch_cluster(K kernel, dim3 grid, int threads, int smem, int cluster, cuda
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
-// Splits of one unit of work (a power of two, at most 16: a cluster): as many as
-// fill the device with `units` units, while each split keeps at least `least` of
-// the longest walk's `steps` steps.
-int splits_for(int64_t units, int64_t slots, int64_t steps, int64_t least) {
-    int c = 1;
-    while (c < 16 && units * c * 2 <= slots && steps >= 2 * c * least) c *= 2;
-    return c;
+// Splits of one unit of work (a power of two, at most 16: a cluster) for `units`
+// units whose longest walk has `steps` steps, on `slots` blocks at a time: the
+// number that gives the fewest steps in a row, a block's start and merge counted
+// as `extra` steps.
+int splits_for(int64_t units, int64_t slots, int64_t steps, int64_t extra) {
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int c = 1; c <= 16; c *= 2) {
+        const int64_t rounds = (units * c + slots - 1) / slots, time = rounds * ((steps + c - 1) / c + extra);
+        if (time < least) {
+            least = time;
+            best = c;
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -960,7 +990,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
             using QT = decltype(qt);
             if (rows <= 16) {
                 using S = DecodeShape<B, H>;
-                const int C = splits_for(pairs, 2 * nsm, longest / (S::NW * S::TILE), 1);
+                const int C = splits_for(pairs, 2 * nsm, (longest + S::NW * S::TILE - 1) / (S::NW * S::TILE), 4);
                 auto go = [&](auto nc) {
                     constexpr auto kernel = k_kvq_decode<B, H, nc.value, QT>;
                     rc = prepared<kernel>(S::SMEM) ? launch_cluster(kernel, dim3(C, c.n_kv_heads, c.n_seq), 256, S::SMEM, C, st, a)
@@ -974,7 +1004,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
                 constexpr int SMEM = 2 * CK_KEYS * H * 2;
                 static_assert(CK_ROWS * H * 4 <= SMEM, "the merge fits in the tiles' memory");
                 const int rt = (rows + CK_ROWS - 1) / CK_ROWS;
-                const int C = splits_for(pairs * rt, 2 * nsm, longest / CK_KEYS, 2);
+                const int C = splits_for(pairs * rt, 2 * nsm, (longest + CK_KEYS - 1) / CK_KEYS, 4);
                 constexpr auto kernel = k_kvq_chunk<B, H, QT>;
                 rc = prepared<kernel>(SMEM)
                          ? launch_cluster(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
