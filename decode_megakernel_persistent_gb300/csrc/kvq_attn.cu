@@ -164,12 +164,14 @@ __device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head,
 // share a packed word; of a V fragment, one dim of two keys.
 template <int BITS, int HD>
 struct DecodeShape {
-    static constexpr int NW = 8;
+    // Four small blocks per SM: one's start and merge run under the others' tiles. Against two blocks of 8
+    // warps: 32 sequences at 32768 positions of 128 dims 271 -> 266 us, 8 ragged ones up to 8192 21.6 -> 19.9.
+    static constexpr int NW = 4, PER_SM = 4;
     static constexpr int RB = HD * BITS / 8, PB = HD / 8;        // bytes of a row's codes and parameters
     static constexpr int TILE = RB == 128 ? 16 : 32;             // keys
     static constexpr int PAR = TILE * PB + 16;                   // a tile's parameters, from an even row on
     static constexpr int STAGE = 2 * (TILE * RB + PAR);
-    static constexpr int STAGES = 104 * 1024 / (NW * STAGE) < 4 ? 104 * 1024 / (NW * STAGE) : 4;  // two blocks per SM
+    static constexpr int ROOM = 208 * 1024 / PER_SM / (NW * STAGE), STAGES = ROOM < 4 ? ROOM : 4;
     static constexpr int SMEM = NW * STAGES * STAGE;
     static_assert(STAGES >= 2, "a ring needs two stages");
 };
@@ -181,7 +183,7 @@ struct DecodeShape {
 __device__ __forceinline__ int key_of(int r) { return r & 1 ? 7 - (r >> 1) : r >> 1; }
 
 template <int BITS, int HD, int NC, typename QT>
-__global__ void __launch_bounds__(256, 2) k_kvq_decode(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(DecodeShape<BITS, HD>::NW * 32, DecodeShape<BITS, HD>::PER_SM) k_kvq_decode(const __grid_constant__ AttnArgs a) {
     using S = DecodeShape<BITS, HD>;
     constexpr int NW = S::NW, RB = S::RB, PB = S::PB, TILE = S::TILE, NT = TILE / 16, GR = HD / 32, COLS = 8 * NC;
     constexpr int GP = GR / 2, PAR = S::PAR;  // pairs of groups
@@ -945,15 +947,20 @@ int launch_cluster(K kernel, dim3 grid, int threads, int smem, int cluster, cuda
 }
 
 // Splits of one unit of work (a power of two, at most 16: a cluster) for `units`
-// units whose longest walk has `steps` steps, on `slots` blocks at a time: the
-// number that gives the fewest steps in a row, a block's start and merge counted
-// as `extra` steps.
-int splits_for(int64_t units, int64_t slots, int64_t steps, int64_t extra) {
+// units whose longest walk has `steps` steps, with `slots` blocks on the device:
+// the fewest of a block's own steps and the device's share of all blocks' steps
+// together. A block's start and merge take as long as EXTRA steps, and a step on
+// a full SM twice as long as on one that holds a single block (measured with 4-bit
+// rows of 64 dims: 0.67 us a step alone, 2.7 us for start and merge). Over lengths
+// from 1024 to 32768 and 8 to 512 units the splits that it takes are within 2 % of
+// the best of 1, 2, 4, 8 and 16.
+int splits_for(int64_t units, int slots, double steps) {
+    constexpr double EXTRA = 4;
     int best = 1;
-    int64_t least = INT64_MAX;
+    double least = 0;
     for (int c = 1; c <= 16; c *= 2) {
-        const int64_t rounds = (units * c + slots - 1) / slots, time = rounds * ((steps + c - 1) / c + extra);
-        if (time < least) {
+        const double time = steps / c + EXTRA + 2.0 * double(units) * (steps + EXTRA * c) / slots;
+        if (c == 1 || time < least) {
             least = time;
             best = c;
         }
@@ -990,10 +997,10 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
             using QT = decltype(qt);
             if (rows <= 16) {
                 using S = DecodeShape<B, H>;
-                const int C = splits_for(pairs, 2 * nsm, (longest + S::NW * S::TILE - 1) / (S::NW * S::TILE), 4);
+                const int C = splits_for(pairs, S::PER_SM * nsm, double(longest) / (S::NW * S::TILE));
                 auto go = [&](auto nc) {
                     constexpr auto kernel = k_kvq_decode<B, H, nc.value, QT>;
-                    rc = prepared<kernel>(S::SMEM) ? launch_cluster(kernel, dim3(C, c.n_kv_heads, c.n_seq), 256, S::SMEM, C, st, a)
+                    rc = prepared<kernel>(S::SMEM) ? launch_cluster(kernel, dim3(C, c.n_kv_heads, c.n_seq), S::NW * 32, S::SMEM, C, st, a)
                                                    : LL_ERR_CUDA;
                 };
                 if (rows <= 8)
@@ -1004,7 +1011,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
                 constexpr int SMEM = 2 * CK_KEYS * H * 2;
                 static_assert(CK_ROWS * H * 4 <= SMEM, "the merge fits in the tiles' memory");
                 const int rt = (rows + CK_ROWS - 1) / CK_ROWS;
-                const int C = splits_for(pairs * rt, 2 * nsm, (longest + CK_KEYS - 1) / CK_KEYS, 4);
+                const int C = splits_for(pairs * rt, 2 * nsm, double(longest) / CK_KEYS);
                 constexpr auto kernel = k_kvq_chunk<B, H, QT>;
                 rc = prepared<kernel>(SMEM)
                          ? launch_cluster(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
