@@ -16,72 +16,14 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 
-#include "kvq.cuh"
-#include "kvq.h"
+#include "kvq_attn.cuh"
 #include "ll_internal.h"
 
 namespace ll {
 namespace {
 
 namespace cg = cooperative_groups;
-
-struct AttnArgs {
-    const uint8_t *kc, *vc;
-    const uint32_t *kp, *vp;
-    int64_t seq_rows;
-    int32_t max_seq, group;
-    KvqLens l;
-    const void *q;
-    int64_t q_seq, q_tok, q_head;
-    float scale_log2;  // scale * log2(e): scores in log2 units, probabilities by exp2
-    KvqOut out;
-};
-
-// The running maximum of a row moves only once a score passes it by this (log2
-// units): until then probabilities are taken against the held maximum, at most
-// 2^8, well inside fp16, and neither l nor O needs rescaling.
-constexpr float HOLD = 8.f;
-
-__device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-// A run of bytes to shared memory by the copy engine (both addresses and the size
-// multiples of 16), counted by an mbarrier.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-                 "r"(bytes), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-// Waits for a phase for at most a second: false when it has not come by then.
-__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    do {
-        for (int i = 0; i < 64; i++)
-            if (bar_try(bar, parity)) return true;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (t - t0 < 1000000000ull);
-    return false;
-}
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    return bar_try(bar, parity) || bar_wait_long(bar, parity);
-}
 
 // D += A B: A 16 x 16 (row), B 16 x 8 (col), fp16 in, fp32 sums.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -96,53 +38,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return kvq_u32(__floats2half2_rn(lo, hi)); }
-
-__device__ __forceinline__ void load_q8(const float *p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load_q8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-}
-__device__ __forceinline__ float q_at(const float *p) { return *p; }
-__device__ __forceinline__ float q_at(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-
-// The power of two that brings a row whose largest magnitude is mx into [1, 2)
-// (fp16 then holds 11 bits of every value that matters to a product; a bf16 q is
-// exact but for values 2^-14 of the largest), and its inverse.
-__device__ __forceinline__ void row_scale(float mx, float &down, float &up) {
-    int e = int((__float_as_uint(mx) >> 23) & 255u) - 127;
-    e = mx > 0.f ? min(max(e, -126), 126) : 0;
-    down = __uint_as_float(uint32_t(127 - e) << 23);
-    up = __uint_as_float(uint32_t(127 + e) << 23);
-}
-
-// Two neighbouring values (dims d, d + 1) of a token's head.
-__device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head, int d, float a, float b) {
-    const int64_t at = s * o.seq + j * o.token + head * o.head + d;
-    if (o.f32) {
-        *reinterpret_cast<float2 *>(o.f32 + at) = make_float2(a, b);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 3; i++) {
-        if (!o.t[i]) break;
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        *reinterpret_cast<__nv_bfloat162 *>(o.t[i] + at) = v;
-        a -= __low2float(v);
-        b -= __high2float(v);
-    }
-}
-
 // ---- few query rows: one warp per run of keys --------------------------------------
 //
 // Grid (splits, KV heads, sequences), the splits of a (sequence, KV head) one
@@ -183,7 +78,7 @@ struct DecodeShape {
 __device__ __forceinline__ int key_of(int r) { return r & 1 ? 7 - (r >> 1) : r >> 1; }
 
 template <int BITS, int HD, int NC, typename QT>
-__global__ void __launch_bounds__(DecodeShape<BITS, HD>::NW * 32, DecodeShape<BITS, HD>::PER_SM) k_kvq_decode(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(DecodeShape<BITS, HD>::NW * 32, DecodeShape<BITS, HD>::PER_SM) k_kvq_decode(const __grid_constant__ KvqAttnArgs a) {
     using S = DecodeShape<BITS, HD>;
     constexpr int NW = S::NW, RB = S::RB, PB = S::PB, TILE = S::TILE, NT = TILE / 16, GR = HD / 32, COLS = 8 * NC;
     constexpr int GP = GR / 2, PAR = S::PAR;  // pairs of groups
@@ -430,7 +325,7 @@ __global__ void __launch_bounds__(DecodeShape<BITS, HD>::NW * 32, DecodeShape<BI
 #pragma unroll
                 for (int mt = 1; mt < NT; mt++) x = fmaxf(x, fmaxf(sc[mt][nc][b], sc[mt][nc][2 + b]));
                 top[nc][b] = x * fac[nc][b];
-                grow |= top[nc][b] > m[nc][b] + HOLD;
+                grow |= top[nc][b] > m[nc][b] + KVQ_HOLD;
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -649,7 +544,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 template <int BITS, int HD, typename QT>
-__global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant__ AttnArgs a, int C) {
+__global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant__ KvqAttnArgs a, int C) {
     constexpr int GR = HD / 32, GP = HD / 64, CH = HD / 8, KS = HD / 16;  // 16-byte chunks of a row, k-steps
     constexpr int PER = CK_KEYS * CH / CK_THREADS;                        // chunks a thread unpacks, of K and of V
     extern __shared__ __align__(128) uint8_t smem[];
@@ -806,7 +701,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
 #pragma unroll
             for (int nb = 0; nb < CK_KEYS / 8; nb++) x = fmaxf(x, fmaxf(sc[nb][2 * b], sc[nb][2 * b + 1]));
             top[b] = x * fac[b];
-            grow |= top[b] > m[b] + HOLD;
+            grow |= top[b] > m[b] + KVQ_HOLD;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -916,20 +811,6 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
 
 // ---- launches ----------------------------------------------------------------------
 
-// Once per kernel and device: its shared memory, and clusters of up to 16.
-template <auto kernel>
-bool prepared(int smem) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return false;
-    if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
-    return true;
-}
-
 template <typename K, typename... Args>
 int launch_cluster(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
@@ -972,7 +853,7 @@ int splits_for(int64_t units, int slots, double steps) {
 
 int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
                          int max_len, float scale, const KvqOut &out, int nsm, cudaStream_t st) {
-    AttnArgs a;
+    KvqAttnArgs a;
     a.kc = c.k_codes;
     a.vc = c.v_codes;
     a.kp = reinterpret_cast<const uint32_t *>(c.k_params);
@@ -990,6 +871,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     const int longest = max_len > 0 ? std::min(max_len, c.max_seq) : c.max_seq;
     const int rows = l.n_tok * a.group;
     const int64_t pairs = int64_t(c.n_seq) * c.n_kv_heads;
+    if (rows > 128) return launch_kvq_prompt(c, a, type, st);
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         constexpr int B = bits.value, H = hd.value;

@@ -1,0 +1,165 @@
+// kvq_attn.cuh -- what the attention kernels over the packed KV cache share
+// (kvq_attn.cu: few query rows and chunks; kvq_prompt.cu: prompts).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "kvq.cuh"
+#include "kvq.h"
+
+namespace ll {
+
+struct KvqAttnArgs {
+    const uint8_t *kc, *vc;
+    const uint32_t *kp, *vp;
+    int64_t seq_rows;
+    int32_t max_seq, group;
+    KvqLens l;
+    const void *q;
+    int64_t q_seq, q_tok, q_head;
+    float scale_log2;  // scale * log2(e): scores in log2 units, probabilities by exp2
+    KvqOut out;
+};
+
+// The running maximum of a row moves only once a score passes it by this (log2
+// units): until then probabilities are taken against the held maximum, at most
+// 2^8, well inside fp16, and neither l nor O needs rescaling.
+constexpr float KVQ_HOLD = 8.f;
+
+__device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// A run of bytes to shared memory by the copy engine (both addresses and the size
+// multiples of 16), counted by an mbarrier.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits for a phase for at most a second: false when it has not come by then.
+static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        for (int i = 0; i < 64; i++)
+            if (bar_try(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < 1000000000ull);
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    return bar_try(bar, parity) || bar_wait_long(bar, parity);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return kvq_u32(__floats2half2_rn(lo, hi)); }
+
+__device__ __forceinline__ void load_q8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load_q8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+__device__ __forceinline__ float4 load_q4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load_q4(const __nv_bfloat16 *p) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float q_at(const float *p) { return *p; }
+__device__ __forceinline__ float q_at(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+// The power of two that brings a row whose largest magnitude is mx into [1, 2)
+// (fp16 then holds 11 bits of every value that matters to a product; a bf16 q is
+// exact but for values 2^-14 of the largest), and its inverse.
+__device__ __forceinline__ void row_scale(float mx, float &down, float &up) {
+    int e = int((__float_as_uint(mx) >> 23) & 255u) - 127;
+    e = mx > 0.f ? min(max(e, -126), 126) : 0;
+    down = __uint_as_float(uint32_t(127 - e) << 23);
+    up = __uint_as_float(uint32_t(127 + e) << 23);
+}
+
+// Two neighbouring values (dims d, d + 1) of a token's head.
+__device__ __forceinline__ void put_out(const KvqOut &o, int s, int j, int head, int d, float a, float b) {
+    const int64_t at = s * o.seq + j * o.token + head * o.head + d;
+    if (o.f32) {
+        *reinterpret_cast<float2 *>(o.f32 + at) = make_float2(a, b);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        if (!o.t[i]) break;
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        *reinterpret_cast<__nv_bfloat162 *>(o.t[i] + at) = v;
+        a -= __low2float(v);
+        b -= __high2float(v);
+    }
+}
+
+// 32 values from dim d on, each times f.
+__device__ __forceinline__ void put_out32(const KvqOut &o, int s, int j, int head, int d, const uint32_t (&x)[32], float f) {
+    if (o.f32 || o.t[1]) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) put_out(o, s, j, head, d + i, __uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f);
+        return;
+    }
+    uint4 *const to = reinterpret_cast<uint4 *>(o.t[0] + s * o.seq + j * o.token + head * o.head + d);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[8 * i + 2 * k]) * f, __uint_as_float(x[8 * i + 2 * k + 1]) * f);
+            w[k] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        to[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Once per kernel and device: its shared memory, and clusters of up to 16.
+template <auto kernel>
+bool prepared(int smem) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    if (dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return true;
+}
+
+// The kernel for prompts (kvq_prompt.cu): 256 query rows of a KV head to a block.
+constexpr int KVQ_PROMPT_ROWS = 256;
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cudaStream_t st);
+
+}  // namespace ll

@@ -1,0 +1,527 @@
+// kvq_prompt.cu -- attention of many query rows over the packed KV cache, on the
+// fifth-generation tensor cores.
+//
+// A block takes 256 query rows of a KV head (row = token * group + head), as two
+// tiles A and B of 128, and walks the keys in tiles of 128. Four warps unpack a
+// tile of K and V into fp16 in shared memory, two stages deep (once for both row
+// tiles: unpacking costs about as much as one row tile's softmax); one thread
+// issues tcgen05.mma, S = Q K^T and O += P V, both in tensor memory; and four warps
+// per row tile, a row to a thread, read S, take P = exp(S - m) back into the first
+// half of S's columns as fp16 (the A operand of P V), and move the running
+// maximum where a score passes it. While one row tile is in its softmax, the
+// other is in its products.
+//
+// What bounds it: at 128 dims the products of a key tile take 2,048 cycles of the
+// tensor cores for the two row tiles, the softmax and unpacking about 1,800 issue
+// slots per scheduler; at 64 dims the products are half of that, and the softmax
+// bounds.
+#include "kvq_attn.cuh"
+#include "ll_internal.h"
+
+namespace ll {
+namespace {
+
+constexpr int THREADS = 13 * 32;  // softmax A, softmax B, unpacking (4 warps each), products
+constexpr int KEYS = 128;
+
+template <int HD>
+struct Shape {
+    static constexpr uint32_t QT = 128 * HD * 2, KT = KEYS * HD * 2;  // a row tile; a K or V tile
+    static constexpr uint32_t SMEM = 2 * QT + 2 * 2 * KT + 1024;      // two row tiles, two stages (from a 1,024-byte border)
+    static constexpr uint32_t TM_S = 0, TM_O = 256;                   // tensor memory columns: S of A and B, O of A and B
+};
+
+// Shared-memory matrix descriptor of a K-major tile in the 128-byte swizzle (rows
+// of 128 bytes, 8-row groups 1,024 bytes apart); 16 elements along K are 32 bytes.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1u) << 16 | uint64_t(1024u >> 4) << 32 | uint64_t(1u) << 46 |
+           uint64_t(2u) << 61;
+}
+// Instruction descriptor of kind::f16: fp16 A and B, both K-major, fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+    return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(add)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(add)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {  // arrives once all products issued so far are done
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Bounded wait: false, with *err set for the other warps, once a second passes.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *err) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        for (int i = 0; i < 64; i++)
+            if (bar_try(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (!*err && t - t0 < 1000000000ull);
+    *err = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *err) {
+    return bar_try(bar, parity) || wait_long(bar, parity, err);
+}
+
+// 32 columns of this thread's tensor-memory lane; the values are there after tm_wait.
+__device__ __forceinline__ void tm_load(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+// (the values pass through the statement, so that no use of them can come before it)
+__device__ __forceinline__ void tm_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The dim of element p of a K or Q row in shared memory: a packed word (cells g of
+// groups 2 gp and 2 gp + 1) becomes one 16-byte chunk, in the order its
+// unpacking leaves it.
+template <int HD>
+__device__ __forceinline__ int dim_at(int p) {
+    constexpr int GP = HD / 64;
+    const int q = p >> 3;
+    return 32 * (2 * (q % GP) + (p & 1)) + 4 * (q / GP) + ((p & 7) >> 1);
+}
+
+// Byte of 16-byte chunk c (8 fp16) of row r in a K-major tile of `rows` rows: 64
+// columns (8 chunks) after 64 columns, each in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t chunk_at(int rows, int r, int c) {
+    return uint32_t((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <int BITS, int HD, typename QT>
+__global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant__ KvqAttnArgs a) {
+    using S = Shape<HD>;
+    constexpr int GR = HD / 32, GP = HD / 64, RB = HD * BITS / 8;
+    extern __shared__ uint8_t raw[];
+    uint8_t *const smem = raw + ((1024u - (sptr(raw) & 1023u)) & 1023u);
+    __shared__ uint64_t bars[10];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_err;
+    __shared__ __align__(16) uint8_t s_nan[2][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
+    const uint32_t bar0 = sptr(bars);
+    // kv_full[2], kv_empty[2], s_full[A, B], p_full[A, B], o_full[A, B]
+    const uint32_t kv_full = bar0, kv_empty = bar0 + 16, s_full = bar0 + 32, p_full = bar0 + 48, o_full = bar0 + 64;
+    volatile int *const err = &s_err;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.z, h = blockIdx.y;
+    const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group, first = len - n;
+    const int r0 = (int(gridDim.x) - 1 - int(blockIdx.x)) * KVQ_PROMPT_ROWS;  // the most keys first
+    if (r0 >= rows) return;
+    // keys that a row tile's last row sees, in tiles; a row tile past the last row sees none
+    auto seen = [&](int t) {
+        const int lo = r0 + 128 * t, hi = min(lo + 128, rows) - 1;
+        return lo < rows ? max(0, min(min(len, a.max_seq), first + hi / a.group + 1)) : 0;
+    };
+    const int seen_a = seen(0), seen_b = seen(1), limit = max(seen_a, seen_b);
+    const int na = (seen_a + KEYS - 1) / KEYS, nb = (seen_b + KEYS - 1) / KEYS, tiles = max(na, nb);
+    const int first_last = first + r0 / a.group;           // the last position that the block's first row sees
+    const int edge_from = min(first_last + 1, limit);      // tiles that reach past it are masked
+    const uint32_t q_at0 = sptr(smem), kv0 = q_at0 + 2 * S::QT;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            bar_init(kv_full + 8 * i, 4);
+            bar_init(kv_empty + 8 * i, 1);
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_full + 8 * i, 4);
+            bar_init(o_full + 8 * i, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_err = 0;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sptr(&s_tmem)), "n"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    float fac = 0.f;
+    if (warp < 8) {  // this thread's row of Q: scaled to fp16, in the order of K's unpacking
+        const int r = r0 + int(threadIdx.x), row = threadIdx.x & 127;
+        float mx = 0.f, down, up;
+        const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + int64_t(r / a.group) * a.q_tok +
+                      int64_t(h * a.group + r % a.group) * a.q_head;
+        if (r < rows)
+            for (int d = 0; d < HD; d += 8) {
+                float v[8];
+                load_q8(q + d, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) mx = fmaxf(mx, fabsf(v[i]));
+            }
+        row_scale(mx, down, up);
+        fac = up * a.scale_log2;
+        uint8_t *const qs = smem + (threadIdx.x >> 7) * S::QT;
+        for (int gp = 0; gp < GP; gp++)
+            for (int g = 0; g < 8; g++) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+                if (r < rows) {
+                    x = load_q4(q + 64 * gp + 4 * g);
+                    y = load_q4(q + 64 * gp + 32 + 4 * g);
+                }
+                *reinterpret_cast<uint4 *>(qs + chunk_at(128, row, g * GP + gp)) =
+                    make_uint4(pack_h2(x.x * down, y.x * down), pack_h2(x.y * down, y.y * down),
+                               pack_h2(x.z * down, y.z * down), pack_h2(x.w * down, y.w * down));
+            }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp == 12) {
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
+            auto scores = [&](int t, int i) {  // S of row tile t with key tile i
+                const uint32_t q = q_at0 + t * S::QT, k = kv0 + (i & 1) * 2 * S::KT;
+#pragma unroll
+                for (int d = 0; d < HD / 16; d++)
+                    mma_ss(tmem + S::TM_S + 128 * t, desc_sw128(q + (d >> 2) * 128 * 128) + 2 * (d & 3),
+                           desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
+                commit(s_full + 8 * t);
+            };
+            auto values = [&](int t, int i) {  // O += P V
+                const uint32_t v = kv0 + (i & 1) * 2 * S::KT + S::KT;
+#pragma unroll
+                for (int k = 0; k < KEYS / 16; k++)
+                    mma_ts(tmem + S::TM_O + HD * t, tmem + S::TM_S + 128 * t + 8 * k,
+                           desc_sw128(v + (k >> 2) * HD * 128) + 2 * (k & 3), id_o, (i | k) != 0);
+            };
+            bool ok = tiles == 0 || wait(kv_full, 0, err);
+            if (ok && tiles) {
+                fence_after();
+                if (na) scores(0, 0);
+                if (nb) scores(1, 0);
+            }
+            for (int i = 0; i < tiles && ok; i++) {
+                if (i < na) {
+                    if (!(ok = wait(p_full, i & 1, err))) break;
+                    fence_after();
+                    values(0, i);
+                    if (i + 1 == na) commit(o_full);
+                }
+                if (i + 1 < tiles) {
+                    if (!(ok = wait(kv_full + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1, err))) break;
+                    fence_after();
+                    if (i + 1 < na) scores(0, i + 1);
+                }
+                if (i < nb) {
+                    if (!(ok = wait(p_full + 8, i & 1, err))) break;
+                    fence_after();
+                    values(1, i);
+                    if (i + 1 == nb) commit(o_full + 8);
+                }
+                commit(kv_empty + 8 * (i & 1));
+                if (i + 1 < nb) scores(1, i + 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // unpacking: for K a thread is a key; for V it is 8 keys of a cell, which leave as
+        // 16-byte runs of the transposed tile's rows (a row a dim). Lanes 0..7 take 8
+        // runs of 8 keys: their stores fall in different banks.
+        const KvqConsts consts;
+        const int t = threadIdx.x - 256, w = t >> 5;
+        const int oct = (lane & 7) | (w & 1) << 3, g = lane >> 3 | (w >> 1) << 2;
+        const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
+        constexpr int VW = GR * BITS / 8;  // words of a cell's groups: 4-bit cells sit two groups to a word
+        for (int i = 0; i < tiles; i++) {
+            const int k0 = i * KEYS;
+            const bool edge = k0 + KEYS > edge_from;
+            uint32_t kw[RB / 4], kpar[GR], vw[8][VW], vpar[8][GR];
+            auto words = [](const void *p, auto &to) {
+                constexpr int N = sizeof(to) / 4;
+                if constexpr (N >= 4) {
+#pragma unroll
+                    for (int j = 0; j < N / 4; j++) {
+                        const uint4 u = static_cast<const uint4 *>(p)[j];
+                        to[4 * j] = u.x;
+                        to[4 * j + 1] = u.y;
+                        to[4 * j + 2] = u.z;
+                        to[4 * j + 3] = u.w;
+                    }
+                } else if constexpr (N == 2) {
+                    const uint2 u = *static_cast<const uint2 *>(p);
+                    to[0] = u.x;
+                    to[1] = u.y;
+                } else {
+                    to[0] = *static_cast<const uint32_t *>(p);
+                }
+            };
+            auto zero = [](auto &to) {
+#pragma unroll
+                for (int j = 0; j < int(sizeof(to) / 4); j++) to[j] = 0;
+            };
+            if (k0 + t < limit) {
+                words(a.kc + (row0 + k0 + t) * RB, kw);
+                words(a.kp + (row0 + k0 + t) * GR, kpar);
+            } else {
+                zero(kw);
+                zero(kpar);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int key = k0 + 8 * oct + j;
+                if (key < limit) {
+                    words(a.vc + (row0 + key) * RB + g * (RB / 8), vw[j]);
+                    words(a.vp + (row0 + key) * GR, vpar[j]);
+                } else {
+                    zero(vw[j]);
+                    zero(vpar[j]);
+                }
+            }
+            const int stage = i & 1;
+            if (i >= 2 && !wait(kv_empty + 8 * stage, ((i >> 1) - 1) & 1, err)) break;
+            uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT, *const vs = ks + S::KT;
+#pragma unroll
+            for (int gp = 0; gp < GP; gp++) {
+                const __half2 lo = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x5410));
+                const __half2 st = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x7632));
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    const int q = c * GP + gp;  // the chunk: cell c of this pair of groups
+                    __half2 v[4];
+                    if (BITS == 4)
+                        kvq_codes4(kw[q], consts, v);
+                    else
+                        kvq_codes8(kw[(2 * q) % (RB / 4)], kw[(2 * q + 1) % (RB / 4)], consts, v);
+                    *reinterpret_cast<uint4 *>(ks + chunk_at(KEYS, t, q)) =
+                        make_uint4(kvq_u32(__hfma2(st, v[0], lo)), kvq_u32(__hfma2(st, v[1], lo)),
+                                   kvq_u32(__hfma2(st, v[2], lo)), kvq_u32(__hfma2(st, v[3], lo)));
+                }
+            }
+            if (edge) {  // a NaN of V must reach only the rows that see it: it enters as zero, the rows are told
+#pragma unroll
+                for (int gr = 0; gr < GR; gr++) {
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (kvq_is_nan(vpar[j][gr])) {
+                            bits |= 1u << j;
+                            vpar[j][gr] = 0;
+                        }
+                    if (g == 0) s_nan[stage][gr][oct] = uint8_t(bits);
+                }
+            }
+#pragma unroll
+            for (int gr = 0; gr < GR; gr++) {
+                uint32_t x[4][4];  // [dim][pair of keys]
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    __half2 v[4];
+                    if (BITS == 4)
+                        kvq_codes4(kvq_prmt(vw[2 * p][gr / 2], vw[2 * p + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), consts, v);
+                    else
+                        kvq_codes8(vw[2 * p][gr % VW], vw[2 * p + 1][gr % VW], consts, v);
+                    const __half2 lo = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x5410));
+                    const __half2 st = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x7632));
+#pragma unroll
+                    for (int d = 0; d < 4; d++) x[d][p] = kvq_u32(__hfma2(st, v[d], lo));
+                }
+#pragma unroll
+                for (int d = 0; d < 4; d++)
+                    *reinterpret_cast<uint4 *>(vs + chunk_at(HD, 32 * gr + 4 * g + d, oct)) =
+                        make_uint4(x[d][0], x[d][1], x[d][2], x[d][3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive(kv_full + 8 * stage);
+        }
+    } else {
+        const int t = warp >> 2, r = r0 + int(threadIdx.x), mine = t ? nb : na;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 tensor-memory lanes
+        const uint32_t ts = tmem + lanes + S::TM_S + 128 * t, to = tmem + lanes + S::TM_O + HD * t;
+        const int last = r < rows ? min(first + r / a.group, limit - 1) : -1;  // the last key this row sees
+        float m = -INFINITY, l = 0.f;
+        uint32_t poison = 0;  // groups of V in which this row sees a NaN
+        bool ok = true;
+        for (int i = 0; i < mine; i++) {
+            if (!(ok = wait(s_full + 8 * t, i & 1, err))) break;
+            fence_after();
+            const int k0 = i * KEYS;
+            const bool edge = k0 + KEYS > edge_from;
+            const int valid = last - k0 + 1;  // keys of the tile that this row sees
+            uint32_t p[64];                   // P, fp16 pairs
+            float top, sum;
+            auto pass = [&](float m_use, auto masked) {  // P against m_use, its sum, the largest score
+                const uint64_t f2 = pair2(fac, fac), m2 = pair2(-m_use, -m_use);
+                uint64_t acc = pair2(0.f, 0.f);
+                uint32_t c[2][32];
+                float mx = -INFINITY;
+                tm_load(ts, c[0]);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    uint32_t(&x)[32] = c[q & 1];
+                    tm_wait(x);
+                    if (q < 3) tm_load(ts + 32 * (q + 1), c[(q + 1) & 1]);
+                    if (masked.value) {
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (32 * q + j >= valid) x[j] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
+                        mx = fmaxf(mx, fmaxf(s0, s1));
+                        float e0, e1;
+                        split2(fma2(pair2(s0, s1), f2, m2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        acc = add2(acc, pair2(e0, e1));
+                        p[16 * q + j / 2] = pack_h2(e0, e1);
+                    }
+                }
+                float u, v;
+                split2(acc, u, v);
+                sum = u + v;
+                top = mx * fac;
+            };
+            auto both = [&](float m_use) {
+                if (edge)
+                    pass(m_use, KvqConst<1>{});
+                else
+                    pass(m_use, KvqConst<0>{});
+            };
+            both(m == -INFINITY ? 0.f : m);
+            const bool grow = top > m + KVQ_HOLD;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float to_m = grow ? top : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
+                m = to_m;
+                both(m == -INFINITY ? 0.f : m);
+                l *= al;
+                if (i > 0) {  // (the products so far are done: S came after them)
+#pragma unroll 1
+                    for (int q = 0; q < HD / 32; q++) {
+                        uint32_t x[32];
+                        tm_load(to + 32 * q, x);
+                        tm_wait(x);
+#pragma unroll
+                        for (int j = 0; j < 32; j++) x[j] = __float_as_uint(__uint_as_float(x[j]) * al);
+                        tm_store(to + 32 * q, x);
+                    }
+                }
+            }
+            l += sum;
+            tm_store(ts, p);
+            tm_store(ts + 32, p + 32);
+            tm_store_wait();
+            if (edge) {
+                wait(kv_full + 8 * (i & 1), (i >> 1) & 1, err);  // (it is complete: S was made from it)
+#pragma unroll
+                for (int gr = 0; gr < GR; gr++) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i & 1][gr]);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) poison |= 1u << gr;
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(p_full + 8 * t);
+        }
+        if (mine > 0 && ok) ok = wait(o_full + 8 * t, 0, err);
+        fence_after();
+        // (every lane takes part in the loads; a tile without keys has no O)
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        const int j = r / a.group, head = h * a.group + r % a.group;
+#pragma unroll 1
+        for (int q = 0; q < HD / 32; q++) {
+            uint32_t x[32];
+#pragma unroll
+            for (int e = 0; e < 32; e++) x[e] = 0;
+            if (mine > 0) {
+                tm_load(to + 32 * q, x);
+                tm_wait(x);
+            }
+            if (r >= rows) continue;
+            const float f = !ok || (poison >> q & 1) ? __uint_as_float(0x7fffffffu) : inv;
+            put_out32(a.out, s, j, head, 32 * q, x, f);
+        }
+        fence_before();
+    }
+    __syncthreads();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+}  // namespace
+
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cudaStream_t st) {
+    const int64_t rows = int64_t(a.l.n_tok) * a.group;
+    const dim3 grid(unsigned((rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS), c.n_kv_heads, c.n_seq);
+    int rc = LL_OK;
+    kvq_dispatch(c, [&](auto bits, auto hd) {
+        auto go = [&](auto qt) {
+            constexpr auto kernel = k_kvq_prompt<bits.value, hd.value, decltype(qt)>;
+            constexpr int SMEM = Shape<hd.value>::SMEM;
+            if (!prepared<kernel>(SMEM)) {
+                rc = LL_ERR_CUDA;
+                return;
+            }
+            kernel<<<grid, THREADS, SMEM, st>>>(a);
+            if (cudaGetLastError() != cudaSuccess) rc = LL_ERR_CUDA;
+        };
+        if (type == LL_F32)
+            go(float{});
+        else
+            go(__nv_bfloat16{});
+    });
+    return rc;
+}
+
+}  // namespace ll
