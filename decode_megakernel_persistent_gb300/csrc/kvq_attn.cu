@@ -861,6 +861,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     a.seq_rows = c.seq_rows;
     a.max_seq = c.max_seq;
     a.group = n_q_heads / c.n_kv_heads;
+    a.nkv = c.n_kv_heads;
     a.l = l;
     a.q = q.data;
     a.q_seq = q.seq;

@@ -19,7 +19,7 @@ struct KvqAttnArgs {
     const uint8_t *kc, *vc;
     const uint32_t *kp, *vp;
     int64_t seq_rows;
-    int32_t max_seq, group;
+    int32_t max_seq, group, nkv;
     KvqLens l;
     const void *q;
     int64_t q_seq, q_tok, q_head;

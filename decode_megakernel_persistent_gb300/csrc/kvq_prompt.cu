@@ -41,18 +41,29 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
     return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
+// The products are issued by a whole warp, of which one elected lane (the same at every
+// call) carries them out: in a branch for one lane the compiler has to move every
+// operand into a uniform register first, which took as long as the products
+// (prompt of 8192: 617 against 000 us).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(add)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(add)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {  // arrives once all products issued so far are done
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -160,9 +171,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     const uint32_t kv_full = bar0, kv_empty = bar0 + 16, s_full = bar0 + 32, p_full = bar0 + 48, o_full = bar0 + 64;
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.z, h = blockIdx.y;
+    // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
+    const int nkv = a.nkv, s = blockIdx.z, h = int(blockIdx.x) % nkv;
     const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group, first = len - n;
-    const int r0 = (int(gridDim.x) - 1 - int(blockIdx.x)) * KVQ_PROMPT_ROWS;  // the most keys first
+    const int r0 = (int(gridDim.x) - 1 - int(blockIdx.x)) / nkv * KVQ_PROMPT_ROWS;
     if (r0 >= rows) return;
     // keys that a row tile's last row sees, in tiles; a row tile past the last row sees none
     auto seen = [&](int t) {
@@ -222,10 +234,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
     if (warp == 12) {
-        if (lane == 0) {
+        {
             constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
             auto scores = [&](int t, int i) {  // S of row tile t with key tile i
                 const uint32_t q = q_at0 + t * S::QT, k = kv0 + (i & 1) * 2 * S::KT;
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
 
 int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cudaStream_t st) {
     const int64_t rows = int64_t(a.l.n_tok) * a.group;
-    const dim3 grid(unsigned((rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS), c.n_kv_heads, c.n_seq);
+    const dim3 grid(unsigned((rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS * c.n_kv_heads), 1, c.n_seq);
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         auto go = [&](auto qt) {
