@@ -27,8 +27,24 @@ constexpr int KEYS = 128;
 template <int HD>
 struct Shape {
     static constexpr uint32_t QT = 128 * HD * 2, KT = KEYS * HD * 2;  // a row tile; a K or V tile
-    static constexpr uint32_t SMEM = 2 * QT + 2 * 2 * KT + 1024;      // two row tiles, two stages (from a 1,024-byte border)
-    static constexpr uint32_t TM_S = 0, TM_O = 256;                   // tensor memory columns: S of A and B, O of A and B
+    // K/V stages and S buffers: at 64 dims there is room for three S (512 columns of tensor memory with the two O),
+    // so that a row tile's next scores are there when its softmax ends; the products then run two steps ahead,
+    // which takes four stages.
+    static constexpr int ST = HD == 64 ? 4 : 2, NB = HD == 64 ? 3 : 2;
+    static constexpr uint32_t SMEM = 2 * QT + ST * 2 * KT + 1024;     // (from a 1,024-byte border)
+    static constexpr uint32_t TM_O = 128 * NB;                        // tensor memory: S buffers, O of A and B
+    static_assert(TM_O + 2 * HD <= 512, "tensor memory");
+};
+
+// The order of the block's steps (row tile t, key tile i): A and B in turn, then
+// what the longer walk has left. Step j uses S buffer j % NB.
+struct Steps {
+    int na, nb;
+    __device__ __forceinline__ int both() const { return min(na, nb); }
+    __device__ __forceinline__ int count() const { return na + nb; }
+    __device__ __forceinline__ int tile(int j) const { return j < 2 * both() ? j >> 1 : j - both(); }
+    __device__ __forceinline__ int row(int j) const { return j < 2 * both() ? j & 1 : int(nb > na); }
+    __device__ __forceinline__ int step(int t, int i) const { return i < both() ? 2 * i + t : both() + i; }
 };
 
 // Shared-memory matrix descriptor of a K-major tile in the 128-byte swizzle (rows
@@ -162,13 +178,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     constexpr int GR = HD / 32, GP = HD / 64, RB = HD * BITS / 8;
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (sptr(raw) & 1023u)) & 1023u);
-    __shared__ uint64_t bars[10];
+    constexpr int ST = S::ST, NB = S::NB;
+    __shared__ uint64_t bars[2 * ST + 2 * NB + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
-    __shared__ __align__(16) uint8_t s_nan[2][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
+    __shared__ __align__(16) uint8_t s_nan[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
     const uint32_t bar0 = sptr(bars);
-    // kv_full[2], kv_empty[2], s_full[A, B], p_full[A, B], o_full[A, B]
-    const uint32_t kv_full = bar0, kv_empty = bar0 + 16, s_full = bar0 + 32, p_full = bar0 + 48, o_full = bar0 + 64;
+    // per K/V stage, per S buffer, and per row tile (its products with V so far are done)
+    const uint32_t kv_full = bar0, kv_empty = kv_full + 8 * ST, s_full = kv_empty + 8 * ST, p_full = s_full + 8 * NB,
+                   o_done = p_full + 8 * NB;
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
@@ -182,19 +200,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         return lo < rows ? max(0, min(min(len, a.max_seq), first + hi / a.group + 1)) : 0;
     };
     const int seen_a = seen(0), seen_b = seen(1), limit = max(seen_a, seen_b);
-    const int na = (seen_a + KEYS - 1) / KEYS, nb = (seen_b + KEYS - 1) / KEYS, tiles = max(na, nb);
+    const Steps steps = {(seen_a + KEYS - 1) / KEYS, (seen_b + KEYS - 1) / KEYS};
+    const int tiles = max(steps.na, steps.nb);
     const int first_last = first + r0 / a.group;           // the last position that the block's first row sees
     const int edge_from = min(first_last + 1, limit);      // tiles that reach past it are masked
     const uint32_t q_at0 = sptr(smem), kv0 = q_at0 + 2 * S::QT;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < ST; i++) {
             bar_init(kv_full + 8 * i, 4);
             bar_init(kv_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < NB; i++) {
             bar_init(s_full + 8 * i, 1);
             bar_init(p_full + 8 * i, 4);
-            bar_init(o_full + 8 * i, 1);
         }
+        for (int i = 0; i < 2; i++) bar_init(o_done + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_err = 0;
     }
@@ -237,52 +258,39 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
     if (warp == 12) {
-        {
-            constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
-            auto scores = [&](int t, int i) {  // S of row tile t with key tile i
-                const uint32_t q = q_at0 + t * S::QT, k = kv0 + (i & 1) * 2 * S::KT;
-#pragma unroll
-                for (int d = 0; d < HD / 16; d++)
-                    mma_ss(tmem + S::TM_S + 128 * t, desc_sw128(q + (d >> 2) * 128 * 128) + 2 * (d & 3),
-                           desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
-                commit(s_full + 8 * t);
-            };
-            auto values = [&](int t, int i) {  // O += P V
-                const uint32_t v = kv0 + (i & 1) * 2 * S::KT + S::KT;
-#pragma unroll
-                for (int k = 0; k < KEYS / 16; k++)
-                    mma_ts(tmem + S::TM_O + HD * t, tmem + S::TM_S + 128 * t + 8 * k,
-                           desc_sw128(v + (k >> 2) * HD * 128) + 2 * (k & 3), id_o, (i | k) != 0);
-            };
-            bool ok = tiles == 0 || wait(kv_full, 0, err);
-            if (ok && tiles) {
+        constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
+        const int count = steps.count();
+        int ready = 0;  // key tiles that are known to be unpacked
+        auto scores = [&](int j) {  // S of step j
+            const int i = steps.tile(j), b = j % NB;
+            if (i >= ready) {
+                if (!wait(kv_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
+                ready = i + 1;
                 fence_after();
-                if (na) scores(0, 0);
-                if (nb) scores(1, 0);
             }
-            for (int i = 0; i < tiles && ok; i++) {
-                if (i < na) {
-                    if (!(ok = wait(p_full, i & 1, err))) break;
-                    fence_after();
-                    values(0, i);
-                    if (i + 1 == na) commit(o_full);
-                }
-                if (i + 1 < tiles) {
-                    if (!(ok = wait(kv_full + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1, err))) break;
-                    fence_after();
-                    if (i + 1 < na) scores(0, i + 1);
-                }
-                if (i < nb) {
-                    if (!(ok = wait(p_full + 8, i & 1, err))) break;
-                    fence_after();
-                    values(1, i);
-                    if (i + 1 == nb) commit(o_full + 8);
-                }
-                commit(kv_empty + 8 * (i & 1));
-                if (i + 1 < nb) scores(1, i + 1);
-            }
+            const uint32_t q = q_at0 + steps.row(j) * S::QT, k = kv0 + (i % ST) * 2 * S::KT;
+#pragma unroll
+            for (int d = 0; d < HD / 16; d++)
+                mma_ss(tmem + 128 * b, desc_sw128(q + (d >> 2) * 128 * 128) + 2 * (d & 3),
+                       desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
+            commit(s_full + 8 * b);
+            return true;
+        };
+        bool ok = true;
+        for (int j = 0; j < min(NB, count) && ok; j++) ok = scores(j);
+        for (int j = 0; j < count && ok; j++) {
+            const int i = steps.tile(j), t = steps.row(j), b = j % NB;
+            if (!(ok = wait(p_full + 8 * b, (j / NB) & 1, err))) break;
+            fence_after();
+            const uint32_t v = kv0 + (i % ST) * 2 * S::KT + S::KT;
+#pragma unroll
+            for (int k = 0; k < KEYS / 16; k++)  // O += P V
+                mma_ts(tmem + S::TM_O + HD * t, tmem + 128 * b + 8 * k, desc_sw128(v + (k >> 2) * HD * 128) + 2 * (k & 3), id_o,
+                       (i | k) != 0);
+            commit(o_done + 8 * t);
+            if (j + 1 == count || steps.tile(j + 1) != i) commit(kv_empty + 8 * (i % ST));
+            if (j + NB < count) ok = scores(j + NB);
         }
-        __syncwarp();
     } else if (warp >= 8) {
         // unpacking: for K a thread is a key; for V it is 8 keys of a cell, which leave as
         // 16-byte runs of the transposed tile's rows (a row a dim). Lanes 0..7 take 8
@@ -292,33 +300,31 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         const int oct = (lane & 7) | (w & 1) << 3, g = lane >> 3 | (w >> 1) << 2;
         const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
         constexpr int VW = GR * BITS / 8;  // words of a cell's groups: 4-bit cells sit two groups to a word
-        for (int i = 0; i < tiles; i++) {
-            const int k0 = i * KEYS;
-            const bool edge = k0 + KEYS > edge_from;
-            uint32_t kw[RB / 4], kpar[GR], vw[8][VW], vpar[8][GR];
-            auto words = [](const void *p, auto &to) {
-                constexpr int N = sizeof(to) / 4;
-                if constexpr (N >= 4) {
+        uint32_t kw[RB / 4], kpar[GR], vw[8][VW], vpar[8][GR];
+        auto words = [](const void *p, auto &to) {
+            constexpr int N = sizeof(to) / 4;
+            if constexpr (N >= 4) {
 #pragma unroll
-                    for (int j = 0; j < N / 4; j++) {
-                        const uint4 u = static_cast<const uint4 *>(p)[j];
-                        to[4 * j] = u.x;
-                        to[4 * j + 1] = u.y;
-                        to[4 * j + 2] = u.z;
-                        to[4 * j + 3] = u.w;
-                    }
-                } else if constexpr (N == 2) {
-                    const uint2 u = *static_cast<const uint2 *>(p);
-                    to[0] = u.x;
-                    to[1] = u.y;
-                } else {
-                    to[0] = *static_cast<const uint32_t *>(p);
+                for (int j = 0; j < N / 4; j++) {
+                    const uint4 u = static_cast<const uint4 *>(p)[j];
+                    to[4 * j] = u.x;
+                    to[4 * j + 1] = u.y;
+                    to[4 * j + 2] = u.z;
+                    to[4 * j + 3] = u.w;
                 }
-            };
-            auto zero = [](auto &to) {
+            } else if constexpr (N == 2) {
+                const uint2 u = *static_cast<const uint2 *>(p);
+                to[0] = u.x;
+                to[1] = u.y;
+            } else {
+                to[0] = *static_cast<const uint32_t *>(p);
+            }
+        };
+        auto zero = [](auto &to) {
 #pragma unroll
-                for (int j = 0; j < int(sizeof(to) / 4); j++) to[j] = 0;
-            };
+            for (int j = 0; j < int(sizeof(to) / 4); j++) to[j] = 0;
+        };
+        auto load_k = [&](int k0) {
             if (k0 + t < limit) {
                 words(a.kc + (row0 + k0 + t) * RB, kw);
                 words(a.kp + (row0 + k0 + t) * GR, kpar);
@@ -326,6 +332,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 zero(kw);
                 zero(kpar);
             }
+        };
+        // (V's words are on their way while K is unpacked, the next tile's K while V is)
+        if (tiles > 0) load_k(0);
+        for (int i = 0; i < tiles; i++) {
+            const int k0 = i * KEYS, stage = i % ST;
+            const bool edge = k0 + KEYS > edge_from;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 const int key = k0 + 8 * oct + j;
@@ -337,8 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                     zero(vpar[j]);
                 }
             }
-            const int stage = i & 1;
-            if (i >= 2 && !wait(kv_empty + 8 * stage, ((i >> 1) - 1) & 1, err)) break;
+            if (i >= ST && !wait(kv_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
             uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT, *const vs = ks + S::KT;
 #pragma unroll
             for (int gp = 0; gp < GP; gp++) {
@@ -357,6 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                                    kvq_u32(__hfma2(st, v[2], lo)), kvq_u32(__hfma2(st, v[3], lo)));
                 }
             }
+            if (i + 1 < tiles) load_k(k0 + KEYS);
             if (edge) {  // a NaN of V must reach only the rows that see it: it enters as zero, the rows are told
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
@@ -395,15 +407,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             if (lane == 0) arrive(kv_full + 8 * stage);
         }
     } else {
-        const int t = warp >> 2, r = r0 + int(threadIdx.x), mine = t ? nb : na;
+        const int t = warp >> 2, r = r0 + int(threadIdx.x), mine = t ? steps.nb : steps.na;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 tensor-memory lanes
-        const uint32_t ts = tmem + lanes + S::TM_S + 128 * t, to = tmem + lanes + S::TM_O + HD * t;
+        const uint32_t to = tmem + lanes + S::TM_O + HD * t;
         const int last = r < rows ? min(first + r / a.group, limit - 1) : -1;  // the last key this row sees
         float m = -INFINITY, l = 0.f;
         uint32_t poison = 0;  // groups of V in which this row sees a NaN
         bool ok = true;
         for (int i = 0; i < mine; i++) {
-            if (!(ok = wait(s_full + 8 * t, i & 1, err))) break;
+            const int j = steps.step(t, i), b = j % NB;
+            const uint32_t ts = tmem + lanes + 128 * b;
+            if (!(ok = wait(s_full + 8 * b, (j / NB) & 1, err))) break;
             fence_after();
             const int k0 = i * KEYS;
             const bool edge = k0 + KEYS > edge_from;
@@ -450,13 +464,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                     pass(m_use, KvqConst<0>{});
             };
             both(m == -INFINITY ? 0.f : m);
+            // O is this thread's once the products of its tile before are done. (Waited for at
+            // every tile: a phase that nobody waits for could be taken for the one after next.)
+            if (i > 0) {
+                if (!(ok = wait(o_done + 8 * t, (i - 1) & 1, err))) break;
+                fence_after();
+            }
             const bool grow = top > m + KVQ_HOLD;
             if (__any_sync(0xffffffffu, grow)) {
                 const float to_m = grow ? top : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
                 m = to_m;
                 both(m == -INFINITY ? 0.f : m);
                 l *= al;
-                if (i > 0) {  // (the products so far are done: S came after them)
+                if (i > 0) {
 #pragma unroll 1
                     for (int q = 0; q < HD / 32; q++) {
                         uint32_t x[32];
@@ -473,10 +493,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             tm_store(ts + 32, p + 32);
             tm_store_wait();
             if (edge) {
-                wait(kv_full + 8 * (i & 1), (i >> 1) & 1, err);  // (it is complete: S was made from it)
+                wait(kv_full + 8 * (i % ST), (i / ST) & 1, err);  // (it is complete: S was made from it)
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i & 1][gr]);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i % ST][gr]);
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int q = 0; q < 4; q++)
@@ -485,9 +505,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) arrive(p_full + 8 * t);
+            if (lane == 0) arrive(p_full + 8 * b);
         }
-        if (mine > 0 && ok) ok = wait(o_full + 8 * t, 0, err);
+        if (mine > 0 && ok) ok = wait(o_done + 8 * t, (mine - 1) & 1, err);
         fence_after();
         // (every lane takes part in the loads; a tile without keys has no O)
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
