@@ -2,10 +2,10 @@
 // fifth-generation tensor cores.
 //
 // A block takes 256 query rows of a KV head (row = token * group + head), as two
-// tiles A and B of 128, and walks the keys in tiles of 128. Four warps unpack a
-// tile of K and V into fp16 in shared memory, two stages deep (once for both row
-// tiles: unpacking costs about as much as one row tile's softmax); one thread
-// issues tcgen05.mma, S = Q K^T and O += P V, both in tensor memory; and four warps
+// tiles A and B of 128, and walks the keys in tiles of 128. Four warps unpack
+// tiles of K and four tiles of V into fp16 in shared memory, two stages deep or
+// more (once for both row tiles: unpacking costs about as much as one row
+// tile's softmax); one warp issues tcgen05.mma, S = Q K^T and O += P V, both in tensor memory; and four warps
 // per row tile, a row to a thread, read S, take P = exp(S - m) back into the first
 // half of S's columns as fp16 (the A operand of P V), and move the running
 // maximum where a score passes it. While one row tile is in its softmax, the
@@ -21,7 +21,21 @@
 namespace ll {
 namespace {
 
-constexpr int THREADS = 13 * 32;  // softmax A, softmax B, unpacking (4 warps each), products
+constexpr int THREADS = 20 * 32;  // softmax A, softmax B, K, V (4 warps each), products (a warp of four)
+constexpr int W_MMA = 16;
+// Registers a thread: 96 at launch, then as the roles need them (a softmax thread
+// holds P of its row, 64, beside the scores on their way; a V thread up to 64 packed
+// words). The groups' shares add up to the launch's.
+constexpr int R_LAUNCH = 96, R_SOFTMAX = 136, R_K = 64, R_V = 104, R_MMA = 40;
+static_assert(2 * R_SOFTMAX + R_K + R_V + R_MMA == 5 * R_LAUNCH && 5 * 128 * R_LAUNCH <= 65536, "registers");
+template <int N>
+__device__ __forceinline__ void more_regs() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr int KEYS = 128;
 
 template <int HD>
@@ -88,7 +102,7 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
 // Bounded wait: false, with *err set for the other warps, once a second passes.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *err) {
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *err) {
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     do {
@@ -114,6 +128,23 @@ __device__ __forceinline__ void tm_load(uint32_t addr, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr)
         : "memory");
+}
+// (16 columns)
+__device__ __forceinline__ void tm_load16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 // (the values pass through the statement, so that no use of them can come before it)
 __device__ __forceinline__ void tm_wait(uint32_t (&r)[32]) {
@@ -179,14 +210,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (sptr(raw) & 1023u)) & 1023u);
     constexpr int ST = S::ST, NB = S::NB;
-    __shared__ uint64_t bars[2 * ST + 2 * NB + 2];
+    __shared__ uint64_t bars[4 * ST + 2 * NB + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     __shared__ __align__(16) uint8_t s_nan[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
     const uint32_t bar0 = sptr(bars);
     // per K/V stage, per S buffer, and per row tile (its products with V so far are done)
-    const uint32_t kv_full = bar0, kv_empty = kv_full + 8 * ST, s_full = kv_empty + 8 * ST, p_full = s_full + 8 * NB,
-                   o_done = p_full + 8 * NB;
+    const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
+                   s_full = v_empty + 8 * ST, p_full = s_full + 8 * NB, o_done = p_full + 8 * NB;
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
@@ -208,8 +239,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; i++) {
-            bar_init(kv_full + 8 * i, 4);
-            bar_init(kv_empty + 8 * i, 1);
+            bar_init(k_full + 8 * i, 4);
+            bar_init(k_empty + 8 * i, 1);
+            bar_init(v_full + 8 * i, 4);
+            bar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < NB; i++) {
             bar_init(s_full + 8 * i, 1);
@@ -219,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_err = 0;
     }
-    if (warp == 12) {
+    if (warp == W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sptr(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -257,14 +290,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
-    if (warp == 12) {
+    if (warp >= W_MMA) {
+        fewer_regs<R_MMA>();
+    }
+    if (warp > W_MMA) {
+    } else if (warp == W_MMA) {
         constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
         const int count = steps.count();
-        int ready = 0;  // key tiles that are known to be unpacked
+        int ready = 0, vready = 0;  // key tiles whose K, whose V is known to be unpacked
         auto scores = [&](int j) {  // S of step j
             const int i = steps.tile(j), b = j % NB;
             if (i >= ready) {
-                if (!wait(kv_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
+                if (!wait(k_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
                 ready = i + 1;
                 fence_after();
             }
@@ -274,12 +311,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 mma_ss(tmem + 128 * b, desc_sw128(q + (d >> 2) * 128 * 128) + 2 * (d & 3),
                        desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
             commit(s_full + 8 * b);
+            if (j + 1 == count || steps.tile(j + 1) != i) commit(k_empty + 8 * (i % ST));
             return true;
         };
         bool ok = true;
         for (int j = 0; j < min(NB, count) && ok; j++) ok = scores(j);
         for (int j = 0; j < count && ok; j++) {
             const int i = steps.tile(j), t = steps.row(j), b = j % NB;
+            if (i >= vready) {
+                if (!(ok = wait(v_full + 8 * (i % ST), (i / ST) & 1, err))) break;
+                vready = i + 1;
+            }
             if (!(ok = wait(p_full + 8 * b, (j / NB) & 1, err))) break;
             fence_after();
             const uint32_t v = kv0 + (i % ST) * 2 * S::KT + S::KT;
@@ -288,19 +330,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 mma_ts(tmem + S::TM_O + HD * t, tmem + 128 * b + 8 * k, desc_sw128(v + (k >> 2) * HD * 128) + 2 * (k & 3), id_o,
                        (i | k) != 0);
             commit(o_done + 8 * t);
-            if (j + 1 == count || steps.tile(j + 1) != i) commit(kv_empty + 8 * (i % ST));
+            if (j + 1 == count || steps.tile(j + 1) != i) commit(v_empty + 8 * (i % ST));
             if (j + NB < count) ok = scores(j + NB);
         }
     } else if (warp >= 8) {
-        // unpacking: for K a thread is a key; for V it is 8 keys of a cell, which leave as
-        // 16-byte runs of the transposed tile's rows (a row a dim). Lanes 0..7 take 8
-        // runs of 8 keys: their stores fall in different banks.
         const KvqConsts consts;
-        const int t = threadIdx.x - 256, w = t >> 5;
-        const int oct = (lane & 7) | (w & 1) << 3, g = lane >> 3 | (w >> 1) << 2;
+        const int t = threadIdx.x & 127, w = t >> 5;
         const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
-        constexpr int VW = GR * BITS / 8;  // words of a cell's groups: 4-bit cells sit two groups to a word
-        uint32_t kw[RB / 4], kpar[GR], vw[8][VW], vpar[8][GR];
         auto words = [](const void *p, auto &to) {
             constexpr int N = sizeof(to) / 4;
             if constexpr (N >= 4) {
@@ -324,89 +360,109 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
 #pragma unroll
             for (int j = 0; j < int(sizeof(to) / 4); j++) to[j] = 0;
         };
-        auto load_k = [&](int k0) {
-            if (k0 + t < limit) {
-                words(a.kc + (row0 + k0 + t) * RB, kw);
-                words(a.kp + (row0 + k0 + t) * GR, kpar);
-            } else {
-                zero(kw);
-                zero(kpar);
-            }
-        };
-        // (V's words are on their way while K is unpacked, the next tile's K while V is)
-        if (tiles > 0) load_k(0);
-        for (int i = 0; i < tiles; i++) {
-            const int k0 = i * KEYS, stage = i % ST;
-            const bool edge = k0 + KEYS > edge_from;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int key = k0 + 8 * oct + j;
+        if (warp < 12) {  // K: a thread is a key
+            fewer_regs<R_K>();
+            uint32_t kw[RB / 4], kpar[GR];
+            auto load = [&](int i) {
+                const int key = i * KEYS + t;
                 if (key < limit) {
-                    words(a.vc + (row0 + key) * RB + g * (RB / 8), vw[j]);
-                    words(a.vp + (row0 + key) * GR, vpar[j]);
+                    words(a.kc + (row0 + key) * RB, kw);
+                    words(a.kp + (row0 + key) * GR, kpar);
                 } else {
-                    zero(vw[j]);
-                    zero(vpar[j]);
+                    zero(kw);
+                    zero(kpar);
                 }
-            }
-            if (i >= ST && !wait(kv_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
-            uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT, *const vs = ks + S::KT;
+            };
+            for (int i = 0; i < tiles; i++) {
+                const int stage = i % ST;
+                load(i);
+                if (i >= ST && !wait(k_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
+                uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT;
 #pragma unroll
-            for (int gp = 0; gp < GP; gp++) {
-                const __half2 lo = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x5410));
-                const __half2 st = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x7632));
+                for (int gp = 0; gp < GP; gp++) {
+                    const __half2 lo = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x5410));
+                    const __half2 st = kvq_h2(kvq_prmt(kpar[2 * gp], kpar[2 * gp + 1], 0x7632));
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    const int q = c * GP + gp;  // the chunk: cell c of this pair of groups
-                    __half2 v[4];
-                    if (BITS == 4)
-                        kvq_codes4(kw[q], consts, v);
-                    else
-                        kvq_codes8(kw[(2 * q) % (RB / 4)], kw[(2 * q + 1) % (RB / 4)], consts, v);
-                    *reinterpret_cast<uint4 *>(ks + chunk_at(KEYS, t, q)) =
-                        make_uint4(kvq_u32(__hfma2(st, v[0], lo)), kvq_u32(__hfma2(st, v[1], lo)),
-                                   kvq_u32(__hfma2(st, v[2], lo)), kvq_u32(__hfma2(st, v[3], lo)));
+                    for (int c = 0; c < 8; c++) {
+                        const int q = c * GP + gp;  // the chunk: cell c of this pair of groups
+                        __half2 v[4];
+                        if (BITS == 4)
+                            kvq_codes4(kw[q], consts, v);
+                        else
+                            kvq_codes8(kw[(2 * q) % (RB / 4)], kw[(2 * q + 1) % (RB / 4)], consts, v);
+                        *reinterpret_cast<uint4 *>(ks + chunk_at(KEYS, t, q)) =
+                            make_uint4(kvq_u32(__hfma2(st, v[0], lo)), kvq_u32(__hfma2(st, v[1], lo)),
+                                       kvq_u32(__hfma2(st, v[2], lo)), kvq_u32(__hfma2(st, v[3], lo)));
+                    }
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive(k_full + 8 * stage);
             }
-            if (i + 1 < tiles) load_k(k0 + KEYS);
-            if (edge) {  // a NaN of V must reach only the rows that see it: it enters as zero, the rows are told
+        } else {
+            more_regs<R_V>();
+            // V: a thread is 8 keys of a cell, which leave as 16-byte runs of the transposed
+            // tile's rows (a row a dim). Lanes 0..7 take 8 runs of 8 keys: their stores
+            // fall in different banks.
+            const int oct = (lane & 7) | (w & 1) << 3, g = lane >> 3 | (w >> 1) << 2;
+            constexpr int VW = GR * BITS / 8;  // words of a cell's groups: 4-bit cells sit two groups to a word
+            uint32_t vw[8][VW], vpar[8][GR];
+            for (int i = 0; i < tiles; i++) {
+                const int k0 = i * KEYS, stage = i % ST;
+                const bool edge = k0 + KEYS > edge_from;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int key = k0 + 8 * oct + j;
+                    if (key < limit) {
+                        words(a.vc + (row0 + key) * RB + g * (RB / 8), vw[j]);
+                        words(a.vp + (row0 + key) * GR, vpar[j]);
+                    } else {
+                        zero(vw[j]);
+                        zero(vpar[j]);
+                    }
+                }
+                if (i >= ST && !wait(v_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
+                uint8_t *const vs = smem + 2 * S::QT + stage * 2 * S::KT + S::KT;
+                if (edge) {  // a NaN of V must reach only the rows that see it: it enters as zero, the rows are told
+#pragma unroll
+                    for (int gr = 0; gr < GR; gr++) {
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            if (kvq_is_nan(vpar[j][gr])) {
+                                bits |= 1u << j;
+                                vpar[j][gr] = 0;
+                            }
+                        if (g == 0) s_nan[stage][gr][oct] = uint8_t(bits);
+                    }
+                }
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
-                    uint32_t bits = 0;
+                    uint32_t x[4][4];  // [dim][pair of keys]
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (kvq_is_nan(vpar[j][gr])) {
-                            bits |= 1u << j;
-                            vpar[j][gr] = 0;
-                        }
-                    if (g == 0) s_nan[stage][gr][oct] = uint8_t(bits);
+                    for (int p = 0; p < 4; p++) {
+                        __half2 v[4];
+                        if (BITS == 4)
+                            kvq_codes4(kvq_prmt(vw[2 * p][gr / 2], vw[2 * p + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), consts, v);
+                        else
+                            kvq_codes8(vw[2 * p][gr % VW], vw[2 * p + 1][gr % VW], consts, v);
+                        const __half2 lo = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x5410));
+                        const __half2 st = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x7632));
+#pragma unroll
+                        for (int d = 0; d < 4; d++) x[d][p] = kvq_u32(__hfma2(st, v[d], lo));
+                    }
+#pragma unroll
+                    for (int d = 0; d < 4; d++)
+                        *reinterpret_cast<uint4 *>(vs + chunk_at(HD, 32 * gr + 4 * g + d, oct)) =
+                            make_uint4(x[d][0], x[d][1], x[d][2], x[d][3]);
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive(v_full + 8 * stage);
             }
-#pragma unroll
-            for (int gr = 0; gr < GR; gr++) {
-                uint32_t x[4][4];  // [dim][pair of keys]
-#pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    __half2 v[4];
-                    if (BITS == 4)
-                        kvq_codes4(kvq_prmt(vw[2 * p][gr / 2], vw[2 * p + 1][gr / 2], gr & 1 ? 0x7632 : 0x5410), consts, v);
-                    else
-                        kvq_codes8(vw[2 * p][gr % VW], vw[2 * p + 1][gr % VW], consts, v);
-                    const __half2 lo = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x5410));
-                    const __half2 st = kvq_h2(kvq_prmt(vpar[2 * p][gr], vpar[2 * p + 1][gr], 0x7632));
-#pragma unroll
-                    for (int d = 0; d < 4; d++) x[d][p] = kvq_u32(__hfma2(st, v[d], lo));
-                }
-#pragma unroll
-                for (int d = 0; d < 4; d++)
-                    *reinterpret_cast<uint4 *>(vs + chunk_at(HD, 32 * gr + 4 * g + d, oct)) =
-                        make_uint4(x[d][0], x[d][1], x[d][2], x[d][3]);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) arrive(kv_full + 8 * stage);
         }
     } else {
+        more_regs<R_SOFTMAX>();
         const int t = warp >> 2, r = r0 + int(threadIdx.x), mine = t ? steps.nb : steps.na;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 tensor-memory lanes
         const uint32_t to = tmem + lanes + S::TM_O + HD * t;
@@ -427,21 +483,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             auto pass = [&](float m_use, auto masked) {  // P against m_use, its sum, the largest score
                 const uint64_t f2 = pair2(fac, fac), m2 = pair2(-m_use, -m_use);
                 uint64_t acc = pair2(0.f, 0.f);
-                uint32_t c[2][32];
+                uint32_t c[2][16];
                 float mx = -INFINITY;
-                tm_load(ts, c[0]);
+                tm_load16(ts, c[0]);
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    uint32_t(&x)[32] = c[q & 1];
-                    tm_wait(x);
-                    if (q < 3) tm_load(ts + 32 * (q + 1), c[(q + 1) & 1]);
+                for (int q = 0; q < 8; q++) {
+                    uint32_t(&x)[16] = c[q & 1];
+                    tm_wait16(x);
+                    if (q < 7) tm_load16(ts + 16 * (q + 1), c[(q + 1) & 1]);
                     if (masked.value) {
 #pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            if (32 * q + j >= valid) x[j] = 0xff800000u;
+                        for (int j = 0; j < 16; j++)
+                            if (16 * q + j >= valid) x[j] = 0xff800000u;
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
+                    for (int j = 0; j < 16; j += 2) {
                         const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
                         mx = fmaxf(mx, fmaxf(s0, s1));
                         float e0, e1;
@@ -449,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                         e0 = ex2(e0);
                         e1 = ex2(e1);
                         acc = add2(acc, pair2(e0, e1));
-                        p[16 * q + j / 2] = pack_h2(e0, e1);
+                        p[8 * q + j / 2] = pack_h2(e0, e1);
                     }
                 }
                 float u, v;
@@ -493,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             tm_store(ts + 32, p + 32);
             tm_store_wait();
             if (edge) {
-                wait(kv_full + 8 * (i % ST), (i / ST) & 1, err);  // (it is complete: S was made from it)
+                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (what its V's NaNs are)
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i % ST][gr]);
@@ -528,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         fence_before();
     }
     __syncthreads();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+    if (warp == W_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
 }  // namespace
