@@ -22,11 +22,11 @@ namespace ll {
 namespace {
 
 constexpr int THREADS = 20 * 32;  // softmax A, softmax B, K, V (4 warps each), products (a warp of four)
-constexpr int W_MMA = 16;
+constexpr int W_MMA = 16;  // the warp, or two, that issue products
 // Registers a thread: 96 at launch, then as the roles need them (a softmax thread
 // holds P of its row, 64, beside the scores on their way; a V thread up to 64 packed
 // words). The groups' shares add up to the launch's.
-constexpr int R_LAUNCH = 96, R_SOFTMAX = 136, R_K = 64, R_V = 104, R_MMA = 40;
+constexpr int R_LAUNCH = 96, R_SOFTMAX = 112, R_K = 72, R_V = 136, R_MMA = 48;
 static_assert(2 * R_SOFTMAX + R_K + R_V + R_MMA == 5 * R_LAUNCH && 5 * 128 * R_LAUNCH <= 65536, "registers");
 template <int N>
 __device__ __forceinline__ void more_regs() {
@@ -45,6 +45,11 @@ struct Shape {
     // so that a row tile's next scores are there when its softmax ends; the products then run two steps ahead,
     // which takes four stages.
     static constexpr int ST = HD == 64 ? 4 : 2, NB = HD == 64 ? 3 : 2;
+    // With three buffers two warps issue the products, one S and one P V, so that one's waits and address work lie under
+    // the other's products (a prompt of 8192 at 64 dims 404 -> 357 us). With two, S has to follow the P V of its
+    // buffer, and one warp issues them in an order that keeps the two row tiles out of step (two warps at 128 dims, one
+    // for S and one for P V or one per row tile: 537 -> 611 and 635 us).
+    static constexpr bool ONE_WARP = NB == 2;
     static constexpr uint32_t SMEM = 2 * QT + ST * 2 * KT + 1024;     // (from a 1,024-byte border)
     static constexpr uint32_t TM_O = 128 * NB;                        // tensor memory: S buffers, O of A and B
     static_assert(TM_O + 2 * HD <= 512, "tensor memory");
@@ -167,6 +172,14 @@ __device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t *r) {
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two fp32 operations at once.
@@ -210,14 +223,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (sptr(raw) & 1023u)) & 1023u);
     constexpr int ST = S::ST, NB = S::NB;
-    __shared__ uint64_t bars[4 * ST + 2 * NB + 2];
+    __shared__ uint64_t bars[4 * ST + 4 * NB + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     __shared__ __align__(16) uint8_t s_nan[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
     const uint32_t bar0 = sptr(bars);
-    // per K/V stage, per S buffer, and per row tile (its products with V so far are done)
+    // per K/V stage; per S buffer (p_full for the two halves of its keys); per row tile (its products with the first
+    // half of a tile's V, and with all of it, are done)
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
-                   s_full = v_empty + 8 * ST, p_full = s_full + 8 * NB, o_done = p_full + 8 * NB;
+                   s_full = v_empty + 8 * ST, p_full = s_full + 8 * NB, s_free = p_full + 16 * NB, o_half = s_free + 8 * NB, o_done = o_half + 16;
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
@@ -246,9 +260,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         }
         for (int i = 0; i < NB; i++) {
             bar_init(s_full + 8 * i, 1);
-            bar_init(p_full + 8 * i, 4);
+            bar_init(p_full + 16 * i, 4);
+            bar_init(p_full + 16 * i + 8, 4);
+            bar_init(s_free + 8 * i, 1);
         }
-        for (int i = 0; i < 2; i++) bar_init(o_done + 8 * i, 1);
+        for (int i = 0; i < 4; i++) bar_init(o_half + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_err = 0;
     }
@@ -293,45 +309,69 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     if (warp >= W_MMA) {
         fewer_regs<R_MMA>();
     }
-    if (warp > W_MMA) {
-    } else if (warp == W_MMA) {
+    if (warp > W_MMA + (S::ONE_WARP ? 0 : 1)) {
+    } else if (warp >= W_MMA) {
         constexpr uint32_t id_s = idesc_f16(128, KEYS), id_o = idesc_f16(128, HD);
         const int count = steps.count();
-        int ready = 0, vready = 0;  // key tiles whose K, whose V is known to be unpacked
+        int kready = 0, vready = 0;  // key tiles whose K, V is known to be unpacked
+        // the last of the steps that use a key tile
+        auto last = [&](int j, int i) { return j + 1 == count || steps.tile(j + 1) != i; };
         auto scores = [&](int j) {  // S of step j
             const int i = steps.tile(j), b = j % NB;
-            if (i >= ready) {
+            const uint32_t q = q_at0 + steps.row(j) * S::QT, k = kv0 + (i % ST) * 2 * S::KT;
+            if (i >= kready) {
                 if (!wait(k_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
-                ready = i + 1;
+                kready = i + 1;
                 fence_after();
             }
-            const uint32_t q = q_at0 + steps.row(j) * S::QT, k = kv0 + (i % ST) * 2 * S::KT;
 #pragma unroll
             for (int d = 0; d < HD / 16; d++)
                 mma_ss(tmem + 128 * b, desc_sw128(q + (d >> 2) * 128 * 128) + 2 * (d & 3),
                        desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
             commit(s_full + 8 * b);
-            if (j + 1 == count || steps.tile(j + 1) != i) commit(k_empty + 8 * (i % ST));
+            if (last(j, i)) commit(k_empty + 8 * (i % ST));
             return true;
         };
-        bool ok = true;
-        for (int j = 0; j < min(NB, count) && ok; j++) ok = scores(j);
-        for (int j = 0; j < count && ok; j++) {
+        auto values = [&](int j) {  // O += P V of step j, in two halves of the keys
             const int i = steps.tile(j), t = steps.row(j), b = j % NB;
+            const uint32_t v = kv0 + (i % ST) * 2 * S::KT + S::KT;
             if (i >= vready) {
-                if (!(ok = wait(v_full + 8 * (i % ST), (i / ST) & 1, err))) break;
+                if (!wait(v_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
                 vready = i + 1;
             }
-            if (!(ok = wait(p_full + 8 * b, (j / NB) & 1, err))) break;
-            fence_after();
-            const uint32_t v = kv0 + (i % ST) * 2 * S::KT + S::KT;
 #pragma unroll
-            for (int k = 0; k < KEYS / 16; k++)  // O += P V
-                mma_ts(tmem + S::TM_O + HD * t, tmem + 128 * b + 8 * k, desc_sw128(v + (k >> 2) * HD * 128) + 2 * (k & 3), id_o,
-                       (i | k) != 0);
-            commit(o_done + 8 * t);
-            if (j + 1 == count || steps.tile(j + 1) != i) commit(v_empty + 8 * (i % ST));
-            if (j + NB < count) ok = scores(j + NB);
+            for (int f = 0; f < 2; f++) {
+                if (!wait(p_full + 16 * b + 8 * f, (j / NB) & 1, err)) return false;
+                fence_after();
+#pragma unroll
+                for (int k = 4 * f; k < 4 * f + 4; k++)
+                    mma_ts(tmem + S::TM_O + HD * t, tmem + 128 * b + 8 * k, desc_sw128(v + f * HD * 128) + 2 * (k & 3), id_o,
+                           (i | k) != 0);
+                commit((f ? o_done : o_half) + 8 * t);
+            }
+            if (last(j, i)) commit(v_empty + 8 * (i % ST));
+            return true;
+        };
+        if (S::ONE_WARP) {
+            bool ok = true;
+            for (int j = 0; j < min(NB, count) && ok; j++) ok = scores(j);
+            for (int j = 0; j < count && ok; j++) {
+                ok = values(j);
+                if (ok && j + NB < count) ok = scores(j + NB);
+            }
+        } else if (warp == W_MMA) {
+            for (int j = 0; j < count; j++) {
+                if (j >= NB) {
+                    if (!wait(s_free + 8 * (j % NB), (j / NB - 1) & 1, err)) break;
+                    fence_after();
+                }
+                if (!scores(j)) break;
+            }
+        } else {
+            for (int j = 0; j < count; j++) {
+                if (!values(j)) break;
+                commit(s_free + 8 * (j % NB));
+            }
         }
     } else if (warp >= 8) {
         const KvqConsts consts;
@@ -478,78 +518,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             const int k0 = i * KEYS;
             const bool edge = k0 + KEYS > edge_from;
             const int valid = last - k0 + 1;  // keys of the tile that this row sees
-            uint32_t p[64];                   // P, fp16 pairs
-            float top, sum;
-            auto pass = [&](float m_use, auto masked) {  // P against m_use, its sum, the largest score
-                const uint64_t f2 = pair2(fac, fac), m2 = pair2(-m_use, -m_use);
-                uint64_t acc = pair2(0.f, 0.f);
-                uint32_t c[2][16];
-                float mx = -INFINITY;
-                tm_load16(ts, c[0]);
-#pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    uint32_t(&x)[16] = c[q & 1];
-                    tm_wait16(x);
-                    if (q < 7) tm_load16(ts + 16 * (q + 1), c[(q + 1) & 1]);
-                    if (masked.value) {
-#pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            if (16 * q + j >= valid) x[j] = 0xff800000u;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
-                        mx = fmaxf(mx, fmaxf(s0, s1));
-                        float e0, e1;
-                        split2(fma2(pair2(s0, s1), f2, m2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        acc = add2(acc, pair2(e0, e1));
-                        p[8 * q + j / 2] = pack_h2(e0, e1);
-                    }
-                }
-                float u, v;
-                split2(acc, u, v);
-                sum = u + v;
-                top = mx * fac;
-            };
-            auto both = [&](float m_use) {
-                if (edge)
-                    pass(m_use, KvqConst<1>{});
-                else
-                    pass(m_use, KvqConst<0>{});
-            };
-            both(m == -INFINITY ? 0.f : m);
             // O is this thread's once the products of its tile before are done. (Waited for at
             // every tile: a phase that nobody waits for could be taken for the one after next.)
-            if (i > 0) {
-                if (!(ok = wait(o_done + 8 * t, (i - 1) & 1, err))) break;
-                fence_after();
-            }
-            const bool grow = top > m + KVQ_HOLD;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float to_m = grow ? top : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
-                m = to_m;
-                both(m == -INFINITY ? 0.f : m);
-                l *= al;
-                if (i > 0) {
-#pragma unroll 1
-                    for (int q = 0; q < HD / 32; q++) {
-                        uint32_t x[32];
-                        tm_load(to + 32 * q, x);
-                        tm_wait(x);
-#pragma unroll
-                        for (int j = 0; j < 32; j++) x[j] = __float_as_uint(__uint_as_float(x[j]) * al);
-                        tm_store(to + 32 * q, x);
-                    }
-                }
-            }
-            l += sum;
-            tm_store(ts, p);
-            tm_store(ts + 32, p + 32);
-            tm_store_wait();
+            if (i > 0 && !(ok = wait(o_done + 8 * t, (i - 1) & 1, err))) break;
             if (edge) {
-                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (what its V's NaNs are)
+                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (V is unpacked: what its NaNs are is known)
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i % ST][gr]);
@@ -559,9 +532,80 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                         if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) poison |= 1u << gr;
                 }
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(p_full + 8 * b);
+            // The keys in two halves, each with its own look at the maximum: the products with
+            // the first half of V run under the softmax of the second.
+#pragma unroll 1
+            for (int f = 0; f < 2; f++) {
+                uint32_t p[32];  // P, fp16 pairs
+                float top, sum;
+                auto pass = [&](float m_use, auto masked) {  // P against m_use, its sum, the largest score
+                    const uint64_t f2 = pair2(fac, fac), m2 = pair2(-m_use, -m_use);
+                    uint64_t acc = pair2(0.f, 0.f);
+                    uint32_t c[2][16];
+                    float mx = -INFINITY;
+                    tm_load16(ts + 64 * f, c[0]);
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        uint32_t(&x)[16] = c[q & 1];
+                        tm_wait16(x);
+                        if (q < 3) tm_load16(ts + 64 * f + 16 * (q + 1), c[(q + 1) & 1]);
+                        if (masked.value) {
+#pragma unroll
+                            for (int j = 0; j < 16; j++)
+                                if (64 * f + 16 * q + j >= valid) x[j] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
+                            mx = fmaxf(mx, fmaxf(s0, s1));
+                            float e0, e1;
+                            split2(fma2(pair2(s0, s1), f2, m2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            acc = add2(acc, pair2(e0, e1));
+                            p[8 * q + j / 2] = pack_h2(e0, e1);
+                        }
+                    }
+                    float u, v;
+                    split2(acc, u, v);
+                    sum = u + v;
+                    top = mx * fac;
+                };
+                auto both = [&](float m_use) {
+                    if (edge)
+                        pass(m_use, KvqConst<1>{});
+                    else
+                        pass(m_use, KvqConst<0>{});
+                };
+                both(m == -INFINITY ? 0.f : m);
+                const bool grow = top > m + KVQ_HOLD;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float to_m = grow ? top : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
+                    m = to_m;
+                    both(m == -INFINITY ? 0.f : m);
+                    l *= al;
+                    if (f && !(ok = wait(o_half + 8 * t, i & 1, err))) break;
+                    fence_after();
+                    if (i + f > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < HD / 16; q++) {
+                            uint32_t x[16];
+                            tm_load16(to + 16 * q, x);
+                            tm_wait16(x);
+#pragma unroll
+                            for (int j = 0; j < 16; j++) x[j] = __float_as_uint(__uint_as_float(x[j]) * al);
+                            tm_store16(to + 16 * q, x);
+                        }
+                    }
+                }
+                l += sum;
+                tm_store(ts + 32 * f, p);
+                tm_store_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(p_full + 16 * b + 8 * f);
+            }
+            if (!ok) break;
         }
         if (mine > 0 && ok) ok = wait(o_done + 8 * t, (mine - 1) & 1, err);
         fence_after();
