@@ -811,22 +811,6 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
 
 // ---- launches ----------------------------------------------------------------------
 
-template <typename K, typename... Args>
-int launch_cluster(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
-}
-
 // Splits of one unit of work (a power of two, at most 16: a cluster) for `units`
 // units whose longest walk has `steps` steps, with `slots` blocks on the device:
 // the fewest of a block's own steps and the device's share of all blocks' steps
@@ -872,7 +856,11 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     const int longest = max_len > 0 ? std::min(max_len, c.max_seq) : c.max_seq;
     const int rows = l.n_tok * a.group;
     const int64_t pairs = int64_t(c.n_seq) * c.n_kv_heads;
-    if (rows > 128) return launch_kvq_prompt(c, a, type, st);
+    // The prompt kernel does a pair of row and key in a quarter of the chunk kernel's time but takes 7 us longer to start
+    // and merge: at 64 dims 4 to 16 million pairs take as long either way (8 heads, 128 rows by 4096 keys: 15.5 us and
+    // 15.8; 512 by 4096: 37 and 25), at 128 dims half as many.
+    if (rows > 16 && double(pairs) * rows * longest * (c.head_dim / 64) >= double(8 << 20))
+        return launch_kvq_prompt(c, a, type, longest, nsm, st);
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         constexpr int B = bits.value, H = hd.value;
@@ -883,7 +871,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
                 const int C = splits_for(pairs, S::PER_SM * nsm, double(longest) / (S::NW * S::TILE));
                 auto go = [&](auto nc) {
                     constexpr auto kernel = k_kvq_decode<B, H, nc.value, QT>;
-                    rc = prepared<kernel>(S::SMEM) ? launch_cluster(kernel, dim3(C, c.n_kv_heads, c.n_seq), S::NW * 32, S::SMEM, C, st, a)
+                    rc = prepared<kernel>(S::SMEM) ? kvq_launch(kernel, dim3(C, c.n_kv_heads, c.n_seq), S::NW * 32, S::SMEM, C, st, a)
                                                    : LL_ERR_CUDA;
                 };
                 if (rows <= 8)
@@ -897,7 +885,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
                 const int C = splits_for(pairs * rt, 2 * nsm, double(longest) / CK_KEYS);
                 constexpr auto kernel = k_kvq_chunk<B, H, QT>;
                 rc = prepared<kernel>(SMEM)
-                         ? launch_cluster(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
+                         ? kvq_launch(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
                          : LL_ERR_CUDA;
             }
         };

@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "kvq.cuh"
 #include "kvq.h"
@@ -158,8 +159,62 @@ bool prepared(int smem) {
     return true;
 }
 
+template <typename K, typename... Args>
+int kvq_launch(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+// Blocks of `kernel` that are resident at once in clusters of 1, 2, 4, 8 and 16 (a
+// cluster's blocks have to fit in one group of SMs, so larger clusters leave some
+// SMs out), asked once per device.
+struct KvqSlots {
+    int n[5];
+};
+template <auto kernel>
+const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
+    static KvqSlots slots[64];
+    static std::atomic<uint64_t> known{0};
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = 0;
+    if (known.load(std::memory_order_acquire) >> dev & 1) return slots[dev];
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < 5; i++) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1u << i);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = size_t(smem);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            clusters = i ? 0 : nsm;
+        }
+        slots[dev].n[i] = clusters << i;
+    }
+    known.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    return slots[dev];
+}
+
 // The kernel for prompts (kvq_prompt.cu): 256 query rows of a KV head to a block.
 constexpr int KVQ_PROMPT_ROWS = 256;
-int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cudaStream_t st);
+// longest: the longest length it is laid out for.
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, cudaStream_t st);
 
 }  // namespace ll

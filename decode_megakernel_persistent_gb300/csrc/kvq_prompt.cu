@@ -11,10 +11,16 @@
 // maximum where a score passes it. While one row tile is in its softmax, the
 // other is in its products.
 //
+// Where there are too few blocks for the device, a cluster of them shares the keys
+// of its rows: each keeps O, m and l of its part in its own shared memory, and
+// merges a share of the rows from all of them.
+//
 // What bounds it: at 128 dims the products of a key tile take 2,048 cycles of the
 // tensor cores for the two row tiles, the softmax and unpacking about 1,800 issue
 // slots per scheduler; at 64 dims the products are half of that, and the softmax
 // bounds.
+#include <cooperative_groups.h>
+
 #include "kvq_attn.cuh"
 #include "ll_internal.h"
 
@@ -182,6 +188,11 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void cluster_sync() {  // (by whole warps)
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Two fp32 operations at once.
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
     uint64_t r;
@@ -217,7 +228,7 @@ __device__ __forceinline__ uint32_t chunk_at(int rows, int r, int c) {
 }
 
 template <int BITS, int HD, typename QT>
-__global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant__ KvqAttnArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant__ KvqAttnArgs a, int C) {
     using S = Shape<HD>;
     constexpr int GR = HD / 32, GP = HD / 64, RB = HD * BITS / 8;
     extern __shared__ uint8_t raw[];
@@ -226,6 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     __shared__ uint64_t bars[4 * ST + 4 * NB + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
+    __shared__ float2 s_ml[256];
     __shared__ __align__(16) uint8_t s_nan[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
     const uint32_t bar0 = sptr(bars);
     // per K/V stage; per S buffer (p_full for the two halves of its keys); per row tile (its products with the first
@@ -235,9 +247,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
-    const int nkv = a.nkv, s = blockIdx.z, h = int(blockIdx.x) % nkv;
+    const int nkv = a.nkv, s = blockIdx.z, unit = int(blockIdx.x) / C, rank = int(blockIdx.x) % C, h = unit % nkv;
     const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group, first = len - n;
-    const int r0 = (int(gridDim.x) - 1 - int(blockIdx.x)) / nkv * KVQ_PROMPT_ROWS;
+    const int r0 = (int(gridDim.x) / C - 1 - unit) / nkv * KVQ_PROMPT_ROWS;
     if (r0 >= rows) return;
     // keys that a row tile's last row sees, in tiles; a row tile past the last row sees none
     auto seen = [&](int t) {
@@ -245,8 +257,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         return lo < rows ? max(0, min(min(len, a.max_seq), first + hi / a.group + 1)) : 0;
     };
     const int seen_a = seen(0), seen_b = seen(1), limit = max(seen_a, seen_b);
-    const Steps steps = {(seen_a + KEYS - 1) / KEYS, (seen_b + KEYS - 1) / KEYS};
-    const int tiles = max(steps.na, steps.nb);
+    // this block's key tiles: `tiles` of them from tile0 on, of which row tile A or B may see fewer
+    const int all = (limit + KEYS - 1) / KEYS, tile0 = int(int64_t(all) * rank / C);
+    const int tiles = int(int64_t(all) * (rank + 1) / C) - tile0;
+    const Steps steps = {min(max((seen_a + KEYS - 1) / KEYS - tile0, 0), tiles), min(max((seen_b + KEYS - 1) / KEYS - tile0, 0), tiles)};
     const int first_last = first + r0 / a.group;           // the last position that the block's first row sees
     const int edge_from = min(first_last + 1, limit);      // tiles that reach past it are masked
     const uint32_t q_at0 = sptr(smem), kv0 = q_at0 + 2 * S::QT;
@@ -415,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             };
             for (int i = 0; i < tiles; i++) {
                 const int stage = i % ST;
-                load(i);
+                load(tile0 + i);
                 if (i >= ST && !wait(k_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
                 uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT;
 #pragma unroll
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             constexpr int VW = GR * BITS / 8;  // words of a cell's groups: 4-bit cells sit two groups to a word
             uint32_t vw[8][VW], vpar[8][GR];
             for (int i = 0; i < tiles; i++) {
-                const int k0 = i * KEYS, stage = i % ST;
+                const int k0 = (tile0 + i) * KEYS, stage = i % ST;
                 const bool edge = k0 + KEYS > edge_from;
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
@@ -515,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             const uint32_t ts = tmem + lanes + 128 * b;
             if (!(ok = wait(s_full + 8 * b, (j / NB) & 1, err))) break;
             fence_after();
-            const int k0 = i * KEYS;
+            const int k0 = (tile0 + i) * KEYS;
             const bool edge = k0 + KEYS > edge_from;
             const int valid = last - k0 + 1;  // keys of the tile that this row sees
             // O is this thread's once the products of its tile before are done. (Waited for at
@@ -610,8 +624,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         if (mine > 0 && ok) ok = wait(o_done + 8 * t, (mine - 1) & 1, err);
         fence_after();
         // (every lane takes part in the loads; a tile without keys has no O)
-        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        const float inv = C > 1 ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
         const int j = r / a.group, head = h * a.group + r % a.group;
+        float *const part = reinterpret_cast<float *>(smem + 2 * S::QT);  // [256][HD], 16-byte chunk c of row x at c ^ x
+        if (C > 1) {
+            // the block's products are done, so its K and V stages are free
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            s_ml[threadIdx.x] = make_float2(m, l);
+        }
 #pragma unroll 1
         for (int q = 0; q < HD / 32; q++) {
             uint32_t x[32];
@@ -621,11 +641,46 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 tm_load(to + 32 * q, x);
                 tm_wait(x);
             }
-            if (r >= rows) continue;
             const float f = !ok || (poison >> q & 1) ? __uint_as_float(0x7fffffffu) : inv;
-            put_out32(a.out, s, j, head, 32 * q, x, f);
+            if (C > 1) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    *reinterpret_cast<float4 *>(part + threadIdx.x * HD + 4 * ((8 * q + e) ^ (threadIdx.x & (HD / 4 - 1)))) =
+                        make_float4(__uint_as_float(x[4 * e]) * f, __uint_as_float(x[4 * e + 1]) * f,
+                                    __uint_as_float(x[4 * e + 2]) * f, __uint_as_float(x[4 * e + 3]) * f);
+            } else if (r < rows) {
+                put_out32(a.out, s, j, head, 32 * q, x, f);
+            }
         }
         fence_before();
+        if (C > 1) {
+            cluster_sync();
+            const cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+            const int share = 256 / C, live = min(share, rows - r0 - rank * share);
+            for (int e = threadIdx.x; e < live * (HD / 4); e += 256) {
+                const int row = rank * share + e / (HD / 4), c = e % (HD / 4), R = r0 + row;
+                float M = -INFINITY, L = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < C; k++) M = fmaxf(M, cl.map_shared_rank(&s_ml[row], k)->x);
+#pragma unroll 4
+                for (int k = 0; k < C; k++) {
+                    const float2 ml = *cl.map_shared_rank(&s_ml[row], k);
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        cl.map_shared_rank(part + row * HD + 4 * (c ^ (row & (HD / 4 - 1))), k));
+                    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                    L = fmaf(ml.y, f, L);
+                    o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+                }
+                const float g = M == -INFINITY ? 0.f : 1.f / L;
+                put_out(a.out, s, R / a.group, h * a.group + R % a.group, 4 * c, o.x * g, o.y * g);
+                put_out(a.out, s, R / a.group, h * a.group + R % a.group, 4 * c + 2, o.z * g, o.w * g);
+            }
+            cluster_sync();  // no block leaves while another reads its memory
+        }
+    }
+    if (C > 1 && warp >= 8) {
+        cluster_sync();
+        cluster_sync();
     }
     __syncthreads();
     if (warp == W_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
@@ -633,9 +688,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
 
 }  // namespace
 
-int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cudaStream_t st) {
-    const int64_t rows = int64_t(a.l.n_tok) * a.group;
-    const dim3 grid(unsigned((rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS * c.n_kv_heads), 1, c.n_seq);
+namespace {
+
+// Blocks that share the keys of a block's rows: for `units` blocks whose longest
+// walk has `steps` key tiles, the number with the fewest steps in a row. A block's
+// start and end take as long as 6 steps, the merge of a cluster 4 more.
+int prompt_splits(int64_t units, const KvqSlots &slots, double steps) {
+    int best = 1;
+    double least = 0;
+    for (int i = 0, c = 1; i < 5 && (c == 1 || slots.n[i] > 0); i++, c *= 2) {
+        const int64_t rounds = (units * c + slots.n[i] - 1) / slots.n[i];
+        const double time = double(rounds) * (steps / c + 6 + (c > 1 ? 4 : 0));
+        if (c == 1 || time < least) {
+            least = time;
+            best = c;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, cudaStream_t st) {
+    const int64_t rows = int64_t(a.l.n_tok) * a.group, tiles = (rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS * c.n_kv_heads;
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         auto go = [&](auto qt) {
@@ -645,8 +720,8 @@ int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, cud
                 rc = LL_ERR_CUDA;
                 return;
             }
-            kernel<<<grid, THREADS, SMEM, st>>>(a);
-            if (cudaGetLastError() != cudaSuccess) rc = LL_ERR_CUDA;
+            const int C = prompt_splits(tiles * c.n_seq, kvq_slots<kernel>(THREADS, SMEM, nsm), double(longest) / KEYS);
+            rc = kvq_launch(kernel, dim3(unsigned(tiles * C), 1, c.n_seq), THREADS, SMEM, C, st, a, C);
         };
         if (type == LL_F32)
             go(float{});

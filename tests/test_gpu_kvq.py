@@ -148,17 +148,18 @@ def test_write_special_values(bits, dtype):
     assert torch.equal(ko.view(torch.int16), vo.view(torch.int16))
 
 
-def make_cache(seed, S, KV, M, hd, bits, lens):
-    """A cache of random rows; what lies past a sequence's length is NaN. Also its values [S, KV, M, hd], float64."""
+def make_cache(seed, S, KV, M, hd, bits, lens, cap=None):
+    """A cache (of cap positions, M unless given) of M random rows; what lies past a sequence's length is NaN. Also the
+    rows' values [S, KV, M, hd], float64."""
     g = gen(seed)
     k = torch.randn(S, M, KV, hd, generator=g, device="cuda").bfloat16()
     k[..., ::16] *= 4
     v = torch.randn(S, M, KV, hd, generator=g, device="cuda").bfloat16()
-    c = filled_cache(S, KV, M, hd, bits)
+    c = filled_cache(S, KV, cap or M, hd, bits)
     full = i32([M] * S)
     c.write(k, v, full)
     vals = []
-    for params, codes in ((c.k_params, c.k_codes), (c.v_params, c.v_codes)):
+    for params, codes in ((c.k_params[:, :, :M], c.k_codes[:, :, :M]), (c.v_params[:, :, :M], c.v_codes[:, :, :M])):
         el = codes.long() if bits == 8 else torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()
         code = el[..., kvq_ref.place(hd).cuda()].unflatten(-1, (hd // 32, 32))
         vals.append(kvq_ref.values(params[..., 0].cpu(), params[..., 1].cpu(), code.cpu()).cuda())
@@ -209,13 +210,15 @@ def test_decode_attention(bits, hd, group, KV, max_len):
 
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("cap", [460, 60000])  # laid out for short lengths (few splits), and for long ones (many, most empty)
 @pytest.mark.parametrize("T,group", [(2, 4), (3, 3), (2, 8), (4, 4), (16, 1), (5, 4), (17, 1), (33, 2), (70, 4), (129, 3), (150, 8)])
-def test_chunk_attention(bits, hd, T, group):
+def test_chunk_attention(bits, hd, T, group, cap):
     KV, M = 2, 460
-    lens = [T, T + 1, 460, 300, 0, 64 + T, T // 2, 461]
-    n = [T, 1, T, T // 2, T, 0, T, T]  # (the last two reach before the start and past the end)
+    # (the last two reach before the start, and past the end where there is one)
+    lens = [T, T + 1, 460, 300, 0, 64 + T, T // 2, 461 if cap == M else 459]
+    n = [T, 1, T, T // 2, T, 0, T, T]
     S = len(lens)
-    c, kv, vv = make_cache(5 + T, S, KV, M, hd, bits, lens)
+    c, kv, vv = make_cache(5 + T, S, KV, M, hd, bits, lens, cap)
     q = torch.randn(S, T, KV * group, hd, generator=gen(4), device="cuda").bfloat16()
     out = torch.full_like(q, 9.0)
     c.attention(q, i32(lens), i32(n), out=out)
@@ -226,11 +229,12 @@ def test_chunk_attention(bits, hd, T, group):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("T,group,M", [(300, 4, 2100), (513, 2, 600), (1000, 1, 1000)])
+@pytest.mark.parametrize("T,group,M,cap", [(300, 4, 2100, 2100), (513, 2, 600, 600), (1000, 1, 1000, 1000), (600, 4, 2100, 2100),
+                                           (1000, 1, 1000, 9000), (1025, 8, 1100, 1100), (70, 4, 5000, 5000), (64, 2, 9001, 70001)])
 @pytest.mark.parametrize("hd", [64, 128])
-def test_long_chunk_attention(bits, hd, T, group, M):
+def test_long_chunk_attention(bits, hd, T, group, M, cap):
     lens = [M, M - 3]
-    c, kv, vv = make_cache(8, 2, 1, M, hd, bits, lens)
+    c, kv, vv = make_cache(8, 2, 1, M, hd, bits, lens, cap)
     q = torch.randn(2, T, group, hd, generator=gen(6), device="cuda").bfloat16()
     out = c.attention(q, i32(lens), scale=0.21)
     check_attention(c, kv, vv, q, lens, [T, T], out, scale=0.21)
@@ -245,12 +249,12 @@ def test_long_decode(hd, bits):
     check_attention(c, kv, vv, q, lens, [1, 1], c.attention(q, i32(lens)))
 
 
-@pytest.mark.parametrize("T,group", [(1, 4), (3, 4), (40, 2)])
+@pytest.mark.parametrize("T,group,cap", [(1, 4, 200), (3, 4, 200), (40, 2, 200), (40, 2, 70000)])
 @pytest.mark.parametrize("mag", [1e-30, 1e-3, 60.0, 1e30])
-def test_query_magnitudes(T, group, mag):
+def test_query_magnitudes(T, group, cap, mag):
     """Queries far outside fp16's range: each row is scaled by a power of two."""
     M, KV, hd = 200, 2, 64
-    c, kv, vv = make_cache(10, 1, KV, M, hd, 4, [M])
+    c, kv, vv = make_cache(10, 1, KV, M, hd, 4, [M], cap)
     q = (torch.randn(1, T, KV * group, hd, generator=gen(6), device="cuda") * mag).bfloat16()
     q[0, 0, 0] = 0  # a row of zeros attends evenly
     scale = 0.125 if mag < 1e3 else 1e-31
@@ -258,12 +262,13 @@ def test_query_magnitudes(T, group, mag):
     check_attention(c, kv, vv, q, [M], [T], out, scale=scale)
 
 
-@pytest.mark.parametrize("T,group", [(1, 4), (4, 4), (5, 1), (24, 4), (200, 2)])
+@pytest.mark.parametrize("T,group,cap", [(1, 4, 333), (4, 4, 333), (5, 1, 333), (24, 4, 333), (200, 2, 333), (24, 4, 60000),
+                                         (200, 2, 60000), (200, 4, 20000)])
 @pytest.mark.parametrize("bits", [4, 8])
-def test_nan_reaches_only_rows_that_see_it(T, group, bits):
+def test_nan_reaches_only_rows_that_see_it(T, group, cap, bits):
     KV, hd, M = 1, 128, 333
     lens = [M]
-    c, kv, vv = make_cache(12, 1, KV, M, hd, bits, lens)
+    c, kv, vv = make_cache(12, 1, KV, M, hd, bits, lens, cap)
     q = torch.randn(1, T, group, hd, generator=gen(6), device="cuda").bfloat16()
     at = M - (T + 1) // 2  # seen by the later half of the tokens
     base = c.attention(q, i32(lens))
@@ -306,12 +311,12 @@ def test_strided_sequences_past_32_bits():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
-@pytest.mark.parametrize("T", [1, 3, 30])
-def test_strided_queries_and_outputs(T):
+@pytest.mark.parametrize("T,cap", [(1, 100), (3, 100), (30, 100), (30, 20000)])
+def test_strided_queries_and_outputs(T, cap):
     """q as columns of a fused projection, out as columns of a wider buffer: the rest of it stays."""
     S, KV, group, hd, M = 3, 2, 4, 64, 100
     lens = [100, 37, 64]
-    c, kv, vv = make_cache(15, S, KV, M, hd, 4, lens)
+    c, kv, vv = make_cache(15, S, KV, M, hd, 4, lens, cap)
     H = KV * group
     q = torch.randn(S, T, H + 2 * KV, hd, generator=gen(1), device="cuda").bfloat16()[:, :, :H]
     wide = torch.full((S, T, H + 3, hd), 5.0, dtype=torch.bfloat16, device="cuda")
