@@ -110,32 +110,36 @@ __device__ __forceinline__ void group_range(const uint32_t (&w)[4], float &mn, f
     mx = -__uint_as_float(r & 0xffff0000u);
 }
 
-// The integer nearest to each t[i] / step, ties to even, within [0, TOP], as floats.
-// The product with 1 / step (inv, approximate) is within 2^-13 of the quotient, so
-// its nearest integer n is the quotient's, or a neighbour of it where the quotient
-// lies within that of the border between the two. The residue t - n step says
-// which: it is exact in one multiply-add (step has 11 bits, n 8, and where n is not
-// 0 the last bit of t is no finer than 2^-24 of step), so n is nearest if it is
-// below half a step, and past half a step, or at it with n odd, the neighbour is.
-// inside: no t is far enough outside for a code outside [0, TOP].
+// The integer nearest to each t / step, t = x[i] - lo in fp32, ties to even, within
+// [0, TOP], as floats. inv is 1 / step less one part in 2^21, so the product t inv
+// lies below the quotient by less than 2^-12, and its nearest integer n is the
+// quotient's or, where the quotient is at the border to the next integer or just past
+// it, one less. The residue r = t - n step says which: it is exact in one multiply-add
+// (step has 11 bits, n 8, and where n is not 0 the last bit of t is no finer than 2^-24
+// of step). Past half a step, or at it with n odd, the next integer is it; as bits of
+// floats, r + odd > half. inside: no t is far enough outside for a code outside [0, TOP].
+// (16 layers of 32768 positions, 8 heads of 64 dims, written in 4 bits and read again: 1,257
+// us with an IEEE division for every value, 802 in the same kernel with the product;
+// later 569 with single and 539 with two-wide fp32 operations.)
 template <int TOP>
-__device__ __forceinline__ void nearest8(const float (&t)[8], float step, float inv, bool inside, float (&n)[8]) {
-    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, ties to even
-    const float half = 0.5f * step;
-    float worst = 0.f;
+__device__ __forceinline__ void nearest8(const float (&x)[8], float lo, float step, float inv, bool inside, float (&n)[8]) {
+    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, whose lowest bit is the float's
+    const int half = __float_as_int(0.5f * step);
+    const uint64_t magic = kvq_pair(MAGIC, MAGIC), back = kvq_pair(-MAGIC, -MAGIC), l = kvq_pair(-lo, -lo);
+    const uint64_t inv2 = kvq_pair(inv, inv), step2 = kvq_pair(-step, -step);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        n[i] = __fadd_rn(__fmaf_rn(t[i], inv, MAGIC), -MAGIC);
-        worst = fmaxf(worst, fabsf(__fmaf_rn(-n[i], step, t[i])));
+    for (int i = 0; i < 8; i += 2) {
+        const uint64_t t = kvq_add2(kvq_pair(x[i], x[i + 1]), l), m = kvq_fma2(t, inv2, magic), k = kvq_add2(m, back);
+        float m0, m1, r0, r1;
+        kvq_split(m, m0, m1);
+        kvq_split(k, n[i], n[i + 1]);
+        kvq_split(kvq_fma2(k, step2, t), r0, r1);
+        if (__float_as_int(r0) + (__float_as_int(m0) & 1) > half) n[i] += 1.f;
+        if (__float_as_int(r1) + (__float_as_int(m1) & 1) > half) n[i + 1] += 1.f;
     }
-    if (!inside || worst >= half) {  // (ties, values past the range's ends)
+    if (!inside) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            n[i] = fminf(fmaxf(n[i], 0.f), float(TOP));
-            const float r = __fmaf_rn(-n[i], step, t[i]), e = fabsf(r);
-            const bool odd = int(n[i]) & 1;
-            if (e > half || (e == half && odd)) n[i] = fminf(fmaxf(n[i] + copysignf(1.f, r), 0.f), float(TOP));
-        }
+        for (int i = 0; i < 8; i++) n[i] = fminf(fmaxf(n[i], 0.f), float(TOP));
     }
 }
 
@@ -146,25 +150,38 @@ __host__ __device__ constexpr int rw_rows(bool far) { return far ? 4 : 2; }  // 
 
 template <bool FAR, int RPB, int U>
 struct RowWalk {
-    int kv, h[U], j[U], pos[U];  // pos: -1 where there is nothing to do
-    __device__ __forceinline__ RowWalk(const RwArgs &a, int n, int len, int row) {
-        kv = FAR ? blockIdx.y & 1 : blockIdx.y;
+    int kv;
+    uint32_t valid = 0;    // bit u: there is something to do
+    int64_t row[U], at[U]; // row in the cache, and the token's row in the call's tensor
+    __device__ __forceinline__ RowWalk(const RwArgs &a, int s, int row0) {
+        const int n = a.l.n(s), first = a.l.len(s) - n;
+        if (FAR) {  // neighbouring rows in both: one address each, and steps from it
+            kv = blockIdx.y & 1;
+            const int h = blockIdx.y >> 1, j = blockIdx.x * (RPB * U) + row0;
+            const ll_kvq_rows &t = a.rows[kv];
+            row[0] = s * a.seq_rows + int64_t(h) * a.max_seq + first + j;
+            at[0] = s * t.seq + h * t.head + j * t.token;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int r = blockIdx.x * (RPB * U) + row + u * RPB;
-            bool ok = true;
-            if (FAR) {
-                j[u] = r;
-                h[u] = blockIdx.y >> 1;
-            } else {
-                ok = r < a.n_rows;
-                j[u] = int(a.heads.div(uint32_t(ok ? r : 0)));
-                h[u] = (ok ? r : 0) - j[u] * a.nkv;
+            for (int u = 0; u < U; u++) {
+                row[u] = row[0] + u * RPB;
+                at[u] = at[0] + u * (RPB * t.token);
+                // (j < n, and the position first + j in [0, max_seq))
+                if (j + u * RPB < n && uint32_t(first + j + u * RPB) < uint32_t(a.max_seq)) valid |= 1u << u;
             }
-            const int p = len - n + j[u];
-            pos[u] = ok && j[u] < n && p >= 0 && p < a.max_seq ? p : -1;
+        } else {
+            kv = blockIdx.y;
+            const ll_kvq_rows &t = a.rows[kv];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int r = blockIdx.x * (RPB * U) + row0 + u * RPB;
+                const int j = int(a.heads.div(uint32_t(min(r, a.n_rows)))), h = min(r, a.n_rows) - j * a.nkv;
+                row[u] = s * a.seq_rows + int64_t(h) * a.max_seq + first + j;
+                at[u] = s * t.seq + h * t.head + j * t.token;
+                if (r < a.n_rows && j < n && uint32_t(first + j) < uint32_t(a.max_seq)) valid |= 1u << u;
+            }
         }
     }
+    __device__ __forceinline__ bool has(int u) const { return valid >> u & 1; }
 };
 
 // Lanes of a row: lane e takes dims 8 e .. 8 e + 7, which is cells g = 2 a and 2 a
@@ -172,18 +189,21 @@ struct RowWalk {
 // and max by shuffles. Cells of one g and neighbouring groups are neighbours in
 // the row, so lanes e and e ^ 4 exchange a cell and each stores a whole word (two
 // cells): the row leaves the warp as one run of bytes.
+//
+// What bounds it: instructions (about 180 for a lane's 8 values; the schedulers issue
+// in 85 % of the cycles). 4 layers of 32768 positions, 8 heads of 64 dims, bf16 to 4 bits:
+// 90 us for 352 MB, 57 % of the copy rate; one token: 3 us, a launch.
 template <typename T, int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant__ RwArgs a) {
     constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);
     const int s = blockIdx.z, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
-    const RowWalk<FAR, RPB, U> w(a, a.l.n(s), a.l.len(s), threadIdx.x / LPR);
-    const ll_kvq_rows &in = a.rows[w.kv];
+    const RowWalk<FAR, RPB, U> w(a, s, threadIdx.x / LPR);
     uint32_t raw[U][2 * sizeof(T)];
-    const T *src = static_cast<const T *>(in.data) + s * in.seq + 8 * e;
+    const T *src = static_cast<const T *>(a.rows[w.kv].data) + 8 * e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        if (w.pos[u] >= 0) {
-            load8(src + w.j[u] * in.token + w.h[u] * in.head, raw[u]);
+        if (w.has(u)) {
+            load8(src + w.at[u], raw[u]);
         } else {
 #pragma unroll
             for (int i = 0; i < int(2 * sizeof(T)); i++) raw[u][i] = 0;
@@ -206,25 +226,26 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
         const float stf = __half2float(step);
         uint32_t c[2] = {0, 0};  // cells 2 ga, 2 ga + 1
         if (stf > 0.f) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) x[i] = __fsub_rn(x[i], lof);
             float q[8], inv;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(stf));
+            inv = fmaf(inv, -4.76837158203125e-7f, inv);  // (2^-21)
             const bool inside = (mn - lof) * inv > -0.25f && (mx - lof) * inv < float(TOP) + 0.25f;
-            nearest8<TOP>(x, stf, inv, inside, q);
+            nearest8<TOP>(x, lof, stf, inv, inside, q);
             // the codes of a cell as one number (two, in 8 bits), each below 2^16: exact in fp32
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 const float *v = q + 4 * i;
+                // (2^23 added: the number is then the low half of the bits)
                 if (BITS == 4)
-                    c[i] = uint32_t(fmaf(fmaf(fmaf(v[3], 16.f, v[2]), 16.f, v[1]), 16.f, v[0]));
+                    c[i] = __float_as_uint(fmaf(fmaf(fmaf(v[3], 16.f, v[2]), 16.f, v[1]), 16.f, v[0] + 8388608.f));
                 else
-                    c[i] = kvq_prmt(uint32_t(fmaf(v[1], 256.f, v[0])), uint32_t(fmaf(v[3], 256.f, v[2])), 0x5410);
+                    c[i] = kvq_prmt(__float_as_uint(fmaf(v[1], 256.f, v[0] + 8388608.f)),
+                                    __float_as_uint(fmaf(v[3], 256.f, v[2] + 8388608.f)), 0x5410);
             }
         }
         const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? c[0] : c[1], 4);
-        if (w.pos[u] < 0) continue;
-        const int64_t row = s * a.seq_rows + int64_t(w.h[u]) * a.max_seq + w.pos[u];
+        if (!w.has(u)) continue;
+        const int64_t row = w.row[u];
         const int word = (2 * ga + (gr & 1)) * (GR / 2) + gr / 2;
         const uint32_t first = gr & 1 ? got : c[0], second = gr & 1 ? c[1] : got;  // groups gr & ~1, gr | 1
         if (BITS == 4)
@@ -237,13 +258,13 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
 }
 
 // The same walk backwards: each lane loads a word (two cells), exchanges one with
-// its partner and stores 8 dims as bf16.
+// its partner and stores 8 dims as bf16. Bound by the memory: the cache of the write
+// above in 53 us, 98 % of the copy rate.
 template <int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__ RwArgs a) {
     constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);
     const int s = blockIdx.z, e = threadIdx.x % LPR, gr = e / 4, ga = e % 4;
-    const RowWalk<FAR, RPB, U> at(a, a.l.n(s), a.l.len(s), threadIdx.x / LPR);
-    const ll_kvq_rows &out = a.rows[at.kv];
+    const RowWalk<FAR, RPB, U> at(a, s, threadIdx.x / LPR);
     const KvqConsts consts;
     const int word = (2 * ga + (gr & 1)) * (GR / 2) + gr / 2;
     uint2 w[U];
@@ -252,8 +273,8 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
     for (int u = 0; u < U; u++) {
         w[u] = make_uint2(0, 0);
         par[u] = 0;
-        if (at.pos[u] >= 0) {
-            const int64_t row = s * a.seq_rows + int64_t(at.h[u]) * a.max_seq + at.pos[u];
+        if (at.has(u)) {
+            const int64_t row = at.row[u];
             if (BITS == 4)
                 w[u].x = reinterpret_cast<const uint32_t *>(a.codes[at.kv])[row * (HD / 8) + word];
             else
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
             par[u] = a.params[at.kv][row * GR + gr];
         }
     }
-    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(out.data) + s * out.seq + 8 * e;
+    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.rows[at.kv].data) + 8 * e;
 #pragma unroll
     for (int u = 0; u < U; u++) {
         // the word is cell (2 ga + gr % 2) of groups gr & ~1 (first) and gr | 1: keep
@@ -274,7 +295,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
             const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? w[u].x : w[u].y, 4);
             kvq_codes8(gr & 1 ? got : w[u].x, gr & 1 ? w[u].y : got, consts, v);
         }
-        if (at.pos[u] < 0) continue;
+        if (!at.has(u)) continue;
         const __half2 lo = kvq_h2(kvq_prmt(par[u], 0, 0x1010)), st = kvq_h2(kvq_prmt(par[u], 0, 0x3232));
         float2 f[4];
 #pragma unroll
@@ -287,7 +308,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__
             o[i] = *reinterpret_cast<const uint32_t *>(&b0);
             o[2 + i] = *reinterpret_cast<const uint32_t *>(&b1);
         }
-        *reinterpret_cast<uint4 *>(dst + at.j[u] * out.token + at.h[u] * out.head) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + at.at[u]) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 

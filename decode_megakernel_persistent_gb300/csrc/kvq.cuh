@@ -14,6 +14,24 @@ __device__ __forceinline__ uint32_t kvq_prmt(uint32_t a, uint32_t b, uint32_t se
 __device__ __forceinline__ __half2 kvq_h2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
 __device__ __forceinline__ uint32_t kvq_u32(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t kvq_pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void kvq_split(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t kvq_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t kvq_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // A group's parameters (lo, step) that stand for NaN.
 __device__ __forceinline__ bool kvq_is_nan(uint32_t par) {
     return (par & 0x7fffu) > 0x7c00u || (par >> 16 & 0x7fffu) > 0x7c00u;

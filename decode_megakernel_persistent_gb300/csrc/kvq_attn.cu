@@ -6,9 +6,10 @@
 // V rows come packed; they become fp16 numbers in registers, exactly the values
 // the format defines, on their way to the tensor cores.
 //
-// Two kernels share the work by the number of query rows a KV head has (its
+// Three kernels share the work by the number of query rows a KV head has (its
 // query heads times the call's tokens): k_kvq_decode for up to 16, where the
-// packed bytes bound the time, and k_kvq_chunk for more.
+// packed bytes bound the time; for more, k_kvq_chunk, and k_kvq_prompt (a file of its own)
+// once there is enough to compute for blocks of 256 rows.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

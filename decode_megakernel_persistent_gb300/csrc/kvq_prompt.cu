@@ -85,7 +85,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
 // The products are issued by a whole warp, of which one elected lane (the same at every
 // call) carries them out: in a branch for one lane the compiler has to move every
 // operand into a uniform register first, which took as long as the products
-// (prompt of 8192: 617 against 000 us).
+// (prompt of 8192: 617 us, and 564 this way).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
         "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -191,24 +191,6 @@ __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st
 __device__ __forceinline__ void cluster_sync() {  // (by whole warps)
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Two fp32 operations at once.
-__device__ __forceinline__ uint64_t pair2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split2(uint64_t p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // The dim of element p of a K or Q row in shared memory: a packed word (cells g of
@@ -553,8 +535,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 uint32_t p[32];  // P, fp16 pairs
                 float top, sum;
                 auto pass = [&](float m_use, auto masked) {  // P against m_use, its sum, the largest score
-                    const uint64_t f2 = pair2(fac, fac), m2 = pair2(-m_use, -m_use);
-                    uint64_t acc = pair2(0.f, 0.f);
+                    const uint64_t f2 = kvq_pair(fac, fac), m2 = kvq_pair(-m_use, -m_use);
+                    uint64_t acc = kvq_pair(0.f, 0.f);
                     uint32_t c[2][16];
                     float mx = -INFINITY;
                     tm_load16(ts + 64 * f, c[0]);
@@ -573,15 +555,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                             const float s0 = __uint_as_float(x[j]), s1 = __uint_as_float(x[j + 1]);
                             mx = fmaxf(mx, fmaxf(s0, s1));
                             float e0, e1;
-                            split2(fma2(pair2(s0, s1), f2, m2), e0, e1);
+                            kvq_split(kvq_fma2(kvq_pair(s0, s1), f2, m2), e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
-                            acc = add2(acc, pair2(e0, e1));
+                            acc = kvq_add2(acc, kvq_pair(e0, e1));
                             p[8 * q + j / 2] = pack_h2(e0, e1);
                         }
                     }
                     float u, v;
-                    split2(acc, u, v);
+                    kvq_split(acc, u, v);
                     sum = u + v;
                     top = mx * fac;
                 };
