@@ -58,11 +58,12 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 // shares) in cells 2t and 2t + 1, and those of its V fragment in cell g. What a
 // pair of a K fragment holds are the same dim of two neighbouring groups, which
 // share a packed word; of a V fragment, one dim of two keys.
-template <int BITS, int HD>
+template <int BITS, int HD, int WARPS>
 struct DecodeShape {
-    // Four small blocks per SM: one's start and merge run under the others' tiles. Against two blocks of 8
-    // warps: 32 sequences at 32768 positions of 128 dims 271 -> 266 us, 8 ragged ones up to 8192 21.6 -> 19.9.
-    static constexpr int NW = 4, PER_SM = 4;
+    // Blocks of 4, 8 or 16 warps, 16 to an SM: many units of work run best as small blocks (one's start and merge run
+    // under the others' tiles: 32 sequences at 32768 positions of 128 dims 266 us, in blocks of 8 warps 271), few as large
+    // ones, whose warps a cluster cannot otherwise bring to an SM (decode_plan has the figures).
+    static constexpr int NW = WARPS, PER_SM = 16 / WARPS;
     static constexpr int RB = HD * BITS / 8, PB = HD / 8;        // bytes of a row's codes and parameters
     static constexpr int TILE = RB == 128 ? 16 : 32;             // keys
     static constexpr int PAR = TILE * PB + 16;                   // a tile's parameters, from an even row on
@@ -78,15 +79,15 @@ struct DecodeShape {
 // two to a bank; 128: two and four, with the shared-memory pipe half idle).
 __device__ __forceinline__ int key_of(int r) { return r & 1 ? 7 - (r >> 1) : r >> 1; }
 
-template <int BITS, int HD, int NC, typename QT>
-__global__ void __launch_bounds__(DecodeShape<BITS, HD>::NW * 32, DecodeShape<BITS, HD>::PER_SM) k_kvq_decode(const __grid_constant__ KvqAttnArgs a) {
-    using S = DecodeShape<BITS, HD>;
+template <int BITS, int HD, int WARPS, int NC, typename QT>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __grid_constant__ KvqAttnArgs a) {
+    using S = DecodeShape<BITS, HD, WARPS>;
     constexpr int NW = S::NW, RB = S::RB, PB = S::PB, TILE = S::TILE, NT = TILE / 16, GR = HD / 32, COLS = 8 * NC;
     constexpr int GP = GR / 2, PAR = S::PAR;  // pairs of groups
     static_assert(NW * COLS * HD * 4 <= S::SMEM, "the merge fits in the ring's memory");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[NW][COLS][2];  // the warps' m and l
-    __shared__ float s_recv[COLS * HD];  // the cluster's sums of this block's share of the outputs, by rank
+    __shared__ float s_recv[COLS * HD + 32];  // the cluster's sums of this block's share of the outputs, by rank (16 shares, rounded up)
     __shared__ float s_rml[16][COLS][2]; // and the ranks' m and l
     __shared__ uint64_t s_full[NW][S::STAGES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -834,6 +835,65 @@ int splits_for(int64_t units, int slots, double steps) {
     return best;
 }
 
+// How the decode kernel cuts `seqs` x `heads` units of up to `keys` keys: warps of a
+// block, and blocks that share a unit. slots: the blocks that the device holds at once
+// with one, two and four of them (of 16, 8 and 4 warps) to an SM.
+//
+// Where 16 splits of each unit fill the device, small blocks do, and balance ragged lengths.
+// Otherwise the fewest microseconds, by what was measured: a warp's step (a tile)
+// takes 0.45 + 0.06 x the warps that its SM holds where it is 32 keys of 64 dims or 16
+// of 128, 0.62 + 0.107 x for 32 of 128; start and merge 3.4 + 0.07 a warp, and 0.9
+// more where SMs hold several blocks. As lengths may differ, the time of one long
+// sequence alone counts as much as that of all as long. A sequence of 32768 keys, 8 heads of
+// 64 dims in 4 bits: 12.6 us in 12 splits of 16 warps (18.1 in 16 of 4: a device of 152 SMs holds only
+// seven clusters of 16 without two blocks on an SM); of 131072, 34 us (58); 2 sequences of 32768, 19.9 (22.5).
+struct DecodePlan {
+    int warps, splits;
+};
+DecodePlan decode_plan(int seqs, int heads, const KvqSlots *const (&slots)[3], int keys, int tile, int tile_values) {
+    DecodePlan best = {4, 1};
+    const KvqSlots &small = *slots[2];
+    const int64_t units = int64_t(seqs) * heads;
+    if (units * 16 > small.n[KVQ_CLUSTER_SIZES - 1]) {
+        best.splits = splits_for(units, small.n[0], double(keys) / (4 * tile));
+        return best;
+    }
+    const double fixed = tile_values > 2048 ? 0.62 : 0.45, per_warp = tile_values > 2048 ? 0.107 : 0.06;
+    const int tiles = (keys + tile - 1) / tile;
+    double least = 0;
+    for (int v = 2; v >= 0; v--)
+        for (int i = 0; i < KVQ_CLUSTER_SIZES; i++) {
+            const int c = KVQ_CLUSTERS[i], warps = 16 >> v, one = slots[0]->n[i], two = slots[1]->n[i], four = small.n[i];
+            if (units * c > slots[v]->n[i]) continue;
+            const int steps = ((tiles + c - 1) / c + warps - 1) / warps;
+            auto time = [&](int n) {
+                const int blocks = n * c, per_sm = blocks <= one ? 1 : blocks <= two ? 2 : 4 * blocks <= 3 * four ? 3 : 4;
+                return 3.4 + 0.07 * warps + (per_sm > 1 ? 0.9 : 0.) + steps * (fixed + per_warp * warps * per_sm);
+            };
+            const double t = time(int(units)) + time(heads);
+            if (least == 0 || t < least) {
+                least = t;
+                best = {warps, c};
+            }
+        }
+    return best;
+}
+
+template <int BITS, int HD, int WARPS, int NC, typename QT>
+const KvqSlots &decode_slots(int nsm) {
+    constexpr auto kernel = k_kvq_decode<BITS, HD, WARPS, NC, QT>;
+    constexpr int SMEM = DecodeShape<BITS, HD, WARPS>::SMEM;
+    static const KvqSlots none = {};
+    return prepared<kernel>(SMEM) ? kvq_slots<kernel>(WARPS * 32, SMEM, nsm) : none;
+}
+template <int BITS, int HD, int WARPS, int NC, typename QT>
+int decode_launch(const ll_kvq_cache &c, const KvqAttnArgs &a, int splits, cudaStream_t st) {
+    constexpr auto kernel = k_kvq_decode<BITS, HD, WARPS, NC, QT>;
+    constexpr int SMEM = DecodeShape<BITS, HD, WARPS>::SMEM;
+    if (!prepared<kernel>(SMEM)) return LL_ERR_CUDA;
+    return kvq_launch(kernel, dim3(splits, c.n_kv_heads, c.n_seq), WARPS * 32, SMEM, splits, st, a);
+}
+
 }  // namespace
 
 int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
@@ -868,12 +928,17 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
         auto typed = [&](auto qt) {
             using QT = decltype(qt);
             if (rows <= 16) {
-                using S = DecodeShape<B, H>;
-                const int C = splits_for(pairs, S::PER_SM * nsm, double(longest) / (S::NW * S::TILE));
                 auto go = [&](auto nc) {
-                    constexpr auto kernel = k_kvq_decode<B, H, nc.value, QT>;
-                    rc = prepared<kernel>(S::SMEM) ? kvq_launch(kernel, dim3(C, c.n_kv_heads, c.n_seq), S::NW * 32, S::SMEM, C, st, a)
-                                                   : LL_ERR_CUDA;
+                    constexpr int tile = DecodeShape<B, H, 4>::TILE;
+                    const KvqSlots *const slots[3] = {&decode_slots<B, H, 16, nc.value, QT>(nsm), &decode_slots<B, H, 8, nc.value, QT>(nsm),
+                                                &decode_slots<B, H, 4, nc.value, QT>(nsm)};
+                    const DecodePlan plan = decode_plan(c.n_seq, c.n_kv_heads, slots, longest, tile, H * tile);
+                    if (plan.warps == 16)
+                        rc = decode_launch<B, H, 16, nc.value, QT>(c, a, plan.splits, st);
+                    else if (plan.warps == 8)
+                        rc = decode_launch<B, H, 8, nc.value, QT>(c, a, plan.splits, st);
+                    else
+                        rc = decode_launch<B, H, 4, nc.value, QT>(c, a, plan.splits, st);
                 };
                 if (rows <= 8)
                     go(KvqConst<1>{});

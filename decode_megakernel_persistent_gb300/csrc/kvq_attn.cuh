@@ -175,11 +175,12 @@ int kvq_launch(K kernel, dim3 grid, int threads, int smem, int cluster, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
-// Blocks of `kernel` that are resident at once in clusters of 1, 2, 4, 8 and 16 (a
-// cluster's blocks have to fit in one group of SMs, so larger clusters leave some
-// SMs out), asked once per device.
+// Blocks of `kernel` that are resident at once in clusters of each size (a cluster's
+// blocks have to fit in one group of SMs, so larger clusters leave some SMs out: with
+// one block to an SM, 152 of them in ones and 112 in sixteens), asked once per device.
+constexpr int KVQ_CLUSTERS[] = {1, 2, 4, 6, 8, 12, 16}, KVQ_CLUSTER_SIZES = 7;
 struct KvqSlots {
-    int n[5];
+    int n[KVQ_CLUSTER_SIZES];
 };
 template <auto kernel>
 const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
@@ -190,14 +191,15 @@ const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = 0;
     if (known.load(std::memory_order_acquire) >> dev & 1) return slots[dev];
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < 5; i++) {
+    for (int i = 0; i < KVQ_CLUSTER_SIZES; i++) {
+        const unsigned size = unsigned(KVQ_CLUSTERS[i]);
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(1u << i);
+        cfg.gridDim = dim3(size);
         cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = size_t(smem);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 1u << i;
+        attr[0].val.clusterDim.x = size;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -206,7 +208,7 @@ const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
             cudaGetLastError();
             clusters = i ? 0 : nsm;
         }
-        slots[dev].n[i] = clusters << i;
+        slots[dev].n[i] = clusters * int(size);
     }
     known.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     return slots[dev];

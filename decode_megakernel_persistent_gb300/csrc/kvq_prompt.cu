@@ -678,7 +678,9 @@ namespace {
 int prompt_splits(int64_t units, const KvqSlots &slots, double steps) {
     int best = 1;
     double least = 0;
-    for (int i = 0, c = 1; i < 5 && (c == 1 || slots.n[i] > 0); i++, c *= 2) {
+    for (int i = 0; i < KVQ_CLUSTER_SIZES; i++) {
+        const int c = KVQ_CLUSTERS[i];
+        if (KVQ_PROMPT_ROWS % c || slots.n[i] < 1) continue;  // (the merge's shares are whole)
         const int64_t rounds = (units * c + slots.n[i] - 1) / slots.n[i];
         const double time = double(rounds) * (steps / c + 6 + (c > 1 ? 4 : 0));
         if (c == 1 || time < least) {
