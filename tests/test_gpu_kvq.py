@@ -249,6 +249,21 @@ def test_long_decode(hd, bits):
     check_attention(c, kv, vv, q, lens, [1, 1], c.attention(q, i32(lens)))
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,group", [(1, 4), (2, 5), (2, 8)])
+@pytest.mark.parametrize("KV,lens,cap", [(8, [1], 32768), (8, [385], 32768), (8, [4099], 32767), (8, [2000], 8192), (1, [3001], 60001),
+                                         (2, [777], 9000), (8, [1500, 64], 32768), (3, [3000, 1, 0], 20001), (7, [5003], 5003)])
+def test_decode_attention_of_few_sequences(bits, hd, T, group, KV, lens, cap):
+    """Laid out for few units of long rows: blocks of 8 and 16 warps, 6 and 12 splits, most of them with little to do."""
+    S, M = len(lens), max(lens)
+    c, kv, vv = make_cache(21 + KV, S, KV, M, hd, bits, lens, cap)
+    q = torch.randn(S, T, KV * group, hd, generator=gen(2), device="cuda").bfloat16() * 2
+    out = c.attention(q, i32(lens))
+    check_attention(c, kv, vv, q, lens, [T] * S, out)
+    assert torch.equal(out, c.attention(q, i32(lens)))
+
+
 @pytest.mark.parametrize("T,group,cap", [(1, 4, 200), (3, 4, 200), (40, 2, 200), (40, 2, 70000)])
 @pytest.mark.parametrize("mag", [1e-30, 1e-3, 60.0, 1e30])
 def test_query_magnitudes(T, group, cap, mag):
