@@ -381,6 +381,46 @@ def test_decode_loop_captured_and_on_a_side_stream():
             check_attention(c, kq, vq, q, [i + 1, i + 1, 0], [1] * S, out)
 
 
+def test_first_calls_of_a_process_may_be_captured():
+    """No call needs one before it outside a graph: a new process captures its first write, read and attention (of
+    one token, a few and many), replays them and gets what the plain calls give."""
+    code = """
+import torch
+from decode_megakernel_persistent_gb300 import ll
+c = ll.KVQCache.empty(1, 2, 5000, 64, 4)
+x = torch.randn(1, 2200, 2, 64, device="cuda").bfloat16()
+qs = [torch.randn(1, t, 16, 64, device="cuda").bfloat16() for t in (1, 12, 2200)]
+outs = [torch.full_like(q, 7.0) for q in qs]
+back = [torch.empty_like(x) for _ in range(2)]
+lens = torch.tensor([2200], dtype=torch.int32, device="cuda")
+def run():
+    c.write(x, x, lens)
+    c.read(back[0], back[1], lens)
+    for q, o in zip(qs, outs):
+        c.attention(q, lens, out=o)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs + back]
+for t in outs + back:
+    t.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs + back))
+assert all(bool((t != 7).any()) and bool(torch.isfinite(t.float()).all()) for t in got)
+print("same")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_prompt_then_tokens_equals_one_chunk():
     """A prompt written and attended in pieces gives what the whole prompt gives."""
     KV, group, hd, n = 2, 4, 64, 90
