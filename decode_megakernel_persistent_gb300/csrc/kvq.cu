@@ -379,7 +379,7 @@ int kvq_check_cache(const ll_kvq_cache *c, const char *&msg) {
     if (c->head_dim != 64 && c->head_dim != 128) return bad(LL_ERR_SHAPE, "head_dim must be 64 or 128");
     if (c->n_seq < 1 || c->n_seq > 65535) return bad(LL_ERR_SHAPE, "n_seq must be 1 to 65535");
     if (c->n_kv_heads < 1 || c->n_kv_heads > 32767) return bad(LL_ERR_SHAPE, "n_kv_heads must be 1 to 32767");
-    if (c->max_seq < 1) return bad(LL_ERR_SHAPE, "max_seq must be positive");
+    if (c->max_seq < 1 || c->max_seq > 1 << 30) return bad(LL_ERR_SHAPE, "max_seq must be 1 to 2^30");
     if (c->n_seq > 1 && c->seq_rows < int64_t(c->n_kv_heads) * c->max_seq)
         return bad(LL_ERR_ARG, "seq_rows is less than n_kv_heads * max_seq");
     const void *p[4] = {c->k_codes, c->v_codes, c->k_params, c->v_params};

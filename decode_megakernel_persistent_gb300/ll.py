@@ -373,8 +373,8 @@ def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=No
     qr, n_tok = cache._rows(q, "q", cache.bf16, heads)
     if scale is None:
         scale = 0.0
-    elif not scale > 0:
-        raise LLError(LL_ERR_ARG, f"scale must be positive, not {scale}")
+    elif not ctypes.c_float(scale).value > 0:  # (as the call gets it: a smaller one would be 0, the default)
+        raise LLError(LL_ERR_ARG, f"scale must be positive in fp32, not {scale}")
     lp, np_ = cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks") if n_toks is not None else None
     if out is None:
         import torch

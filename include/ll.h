@@ -339,9 +339,9 @@ typedef struct {
     uint16_t *k_params, *v_params; /* device, 16-byte aligned, fp16 bit patterns */
     int64_t seq_rows;              /* rows from one sequence to the next, at least n_kv_heads * max_seq */
     int32_t n_seq;                 /* 1 to 65535 */
-    int32_t n_kv_heads;
+    int32_t n_kv_heads;            /* 1 to 32767 */
     int32_t head_dim;              /* 64 or 128 */
-    int32_t max_seq;               /* positions a sequence holds at most */
+    int32_t max_seq;               /* positions a sequence holds at most, 1 to 2^30 */
     int32_t bits;                  /* 4 or 8 */
 } ll_kvq_cache;
 

@@ -117,6 +117,49 @@ def test_write_and_attention_refusals(lib):
     assert call(lib, "attention", c, max_len=-1)[0] == ll.LL_ERR_ARG
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_longest_cache(lib, name):
+    """Positions are 32-bit numbers in the kernels, rounded up to tiles: 2^30 is the last size that is taken."""
+    rc, msg = call(lib, name, cache(max_seq=(1 << 30) + 1, seq_rows=1 << 40))
+    assert rc == ll.LL_ERR_SHAPE and "max_seq" in msg
+    if not torch.cuda.is_available():
+        assert call(lib, name, cache(max_seq=1 << 30, seq_rows=1 << 40))[0] == ll.LL_ERR_CUDA
+
+
+def init_kvq(lib, c, out=True, **k):
+    d = dict(n_layers=2, hidden=256, n_q_heads=4, n_kv_heads=2, head_dim=64, inter=512, vocab=64, max_seq=32, tied=1,
+             backend=ll.LL_BACKEND_CHAIN, rms_eps=1e-5, rope_theta=1e4)
+    d.update(k)
+    cfg, w, h = ll.ll_config(**d), ll.ll_weights(), ctypes.c_void_p(1)
+    rc = lib.ll_init_kvq(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(c) if c is not None else None, None,
+                         ctypes.byref(h) if out else None)
+    return rc, h.value, lib.ll_init_error().decode()
+
+
+def test_handles_that_are_refused(lib):
+    """The packed cache is checked before the weights' pointers (NULL here) are looked at."""
+    rc, h, msg = init_kvq(lib, None)
+    assert rc == ll.LL_ERR_ARG and h is None and "cache" in msg
+    assert init_kvq(lib, cache(), out=False)[0] == ll.LL_ERR_ARG
+    for k in (dict(bits=3), dict(max_seq=0), dict(n_seq=0)):
+        rc, h, msg = init_kvq(lib, cache(**k))
+        assert rc == ll.LL_ERR_SHAPE and h is None and msg, k
+    for k in (dict(n_seq=3), dict(n_kv_heads=1), dict(head_dim=128), dict(max_seq=31), dict(seq_rows=63), dict(v_codes=None)):
+        rc, h, msg = init_kvq(lib, cache(**k))
+        assert rc == ll.LL_ERR_ARG and h is None and msg, k
+    rc, h, msg = init_kvq(lib, cache(), backend=ll.LL_BACKEND_MEGAKERNEL)
+    assert rc == ll.LL_ERR_ARG and h is None and "LL_BACKEND_CHAIN" in msg
+    rc, h, msg = init_kvq(lib, cache())  # the cache is taken, the weights are not
+    assert rc == ll.LL_ERR_ARG and h is None and "embed" in msg
+
+
+def test_scale_as_the_call_gets_it():
+    c, q, lens = fake_cache(), _Fake((2, 1, 2, 64), torch.bfloat16, "cuda:0"), _Fake((2,), torch.int32, "cuda:0")
+    for scale in (0.0, -0.5, float("nan"), 1e-60):
+        with pytest.raises(ll.LLError, match="scale"):
+            ll.ll_kvq_attention(c, q, lens, scale=scale)
+
+
 def test_binding_refuses_host_tensors_and_bits():
     codes = torch.zeros(1, 1, 8, 32, dtype=torch.uint8)
     params = torch.zeros(1, 1, 8, 2, 2, dtype=torch.float16)
