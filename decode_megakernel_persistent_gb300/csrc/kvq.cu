@@ -110,37 +110,36 @@ __device__ __forceinline__ void group_range(const uint32_t (&w)[4], float &mn, f
     mx = -__uint_as_float(r & 0xffff0000u);
 }
 
-// The integer nearest to each t / step, t = x[i] - lo in fp32, ties to even, within
-// [0, TOP], as floats. inv is 1 / step less one part in 2^21, so the product t inv
-// lies below the quotient by less than 2^-12, and its nearest integer n is the
-// quotient's or, where the quotient is at the border to the next integer or just past
-// it, one less. The residue r = t - n step says which: it is exact in one multiply-add
-// (step has 11 bits, n 8, and where n is not 0 the last bit of t is no finer than 2^-24
-// of step). Past half a step, or at it with n odd, the next integer is it; as bits of
-// floats, r | odd > half (half a step has its lowest bits zero). inside: no t is far enough outside for a code outside [0, TOP].
+// The integer n nearest to each t / step, t = x[i] - lo in fp32, ties to even, within
+// [0, TOP], as the bits of 1.5 * 2^23 + n (whose lowest 16 are n).
+//
+// It is the rounded quotient rounded again: a border b between two integers has 9 bits
+// and step 11, so b step is an fp32 number, and a t that is not b step differs from it by
+// so much that the quotient misses b by more than half of b's last place (times 1 +
+// 2^-11 or more): rounding to fp32 cannot take it onto or past the border. The
+// quotient is t inv, corrected once by its residue times inv (Markstein), with inv
+// within 2^-22 of 1 / step: then it is off by 2^-43 of itself before its rounding, which
+// is within that margin. inside: no t is so far outside that n might be outside [0, TOP].
+//
 // (16 layers of 32768 positions, 8 heads of 64 dims, written in 4 bits and read again: 1,257
-// us with an IEEE division for every value, 802 in the same kernel with the product;
-// later 569 with single and 539 with two-wide fp32 operations.)
+// us with an IEEE division for every value; 534 with the product t inv rounded to an integer and
+// compared with half a step, whose comparisons kept the ALU pipe busy; 518 this way.)
 template <int TOP>
-__device__ __forceinline__ void nearest8(const float (&x)[8], float lo, float step, float inv, bool inside, float (&n)[8]) {
-    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, whose lowest bit is the float's
-    const int half = __float_as_int(0.5f * step);
-    const uint64_t magic = kvq_pair(MAGIC, MAGIC), back = kvq_pair(-MAGIC, -MAGIC), l = kvq_pair(-lo, -lo);
-    const uint64_t inv2 = kvq_pair(inv, inv), step2 = kvq_pair(-step, -step);
+__device__ __forceinline__ void nearest8(float (&x)[8], float lo, float step, float inv, bool inside, uint32_t (&n)[8]) {
+    constexpr float MAGIC = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+    if (!inside) {  // (finite, so that the quotients are)
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = fminf(fmaxf(x[i], -BOUND), BOUND);
+    }
+    const uint64_t magic = kvq_pair(MAGIC, MAGIC), l = kvq_pair(-lo, -lo), inv2 = kvq_pair(inv, inv), step2 = kvq_pair(-step, -step);
+    float m[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const uint64_t t = kvq_add2(kvq_pair(x[i], x[i + 1]), l), m = kvq_fma2(t, inv2, magic), k = kvq_add2(m, back);
-        float m0, m1, r0, r1;
-        kvq_split(m, m0, m1);
-        kvq_split(k, n[i], n[i + 1]);
-        kvq_split(kvq_fma2(k, step2, t), r0, r1);
-        if ((__float_as_int(r0) | (__float_as_int(m0) & 1)) > half) n[i] += 1.f;
-        if ((__float_as_int(r1) | (__float_as_int(m1) & 1)) > half) n[i + 1] += 1.f;
+        const uint64_t t = kvq_add2(kvq_pair(x[i], x[i + 1]), l), q = kvq_mul2(t, inv2);
+        kvq_split(kvq_add2(kvq_fma2(kvq_fma2(q, step2, t), inv2, q), magic), m[i], m[i + 1]);
     }
-    if (!inside) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) n[i] = fminf(fmaxf(n[i], 0.f), float(TOP));
-    }
+    for (int i = 0; i < 8; i++) n[i] = __float_as_uint(inside ? m[i] : fminf(fmaxf(m[i], MAGIC), MAGIC + float(TOP)));
 }
 
 // Where a thread's rows are. FAR (many tokens): a block takes one head, K or V, and
@@ -226,21 +225,19 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
         const float stf = __half2float(step);
         uint32_t c[2] = {0, 0};  // cells 2 ga, 2 ga + 1
         if (stf > 0.f) {
-            float q[8], inv;
+            float inv;
+            uint32_t q[8];
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(stf));
-            inv = fmaf(inv, -4.76837158203125e-7f, inv);  // (2^-21)
             const bool inside = (mn - lof) * inv > -0.25f && (mx - lof) * inv < float(TOP) + 0.25f;
             nearest8<TOP>(x, lof, stf, inv, inside, q);
-            // the codes of a cell as one number (two, in 8 bits), each below 2^16: exact in fp32
+            // the codes of a cell as one number (two, in 8 bits), the low 16 bits of a sum: those of 1.5 * 2^23 are zero
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                const float *v = q + 4 * i;
-                // (2^23 added: the number is then the low half of the bits)
+                const uint32_t *v = q + 4 * i;
                 if (BITS == 4)
-                    c[i] = __float_as_uint(fmaf(fmaf(fmaf(v[3], 16.f, v[2]), 16.f, v[1]), 16.f, v[0] + 8388608.f));
+                    c[i] = ((v[3] * 16 + v[2]) * 16 + v[1]) * 16 + v[0];
                 else
-                    c[i] = kvq_prmt(__float_as_uint(fmaf(v[1], 256.f, v[0] + 8388608.f)),
-                                    __float_as_uint(fmaf(v[3], 256.f, v[2] + 8388608.f)), 0x5410);
+                    c[i] = kvq_prmt(v[1] * 256 + v[0], v[3] * 256 + v[2], 0x5410);
             }
         }
         const uint32_t got = __shfl_xor_sync(0xffffffffu, gr & 1 ? c[0] : c[1], 4);
