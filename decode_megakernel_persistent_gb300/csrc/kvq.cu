@@ -75,21 +75,28 @@ __device__ __forceinline__ void widen8(const uint32_t (&w)[4], float (&x)[8]) {
     for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
 }
 
-// Smallest and largest of the four lanes' 8 values each; NaN if any is.
-__device__ __forceinline__ void group_range(const uint32_t (&w)[8], float &mn, float &mx) {
-    mn = mx = __uint_as_float(w[0]);
+// Smallest and largest of values as (min, -max), so that one kind of minimum joins
+// ranges; NaN if any value is. bf16: both in a word.
+struct Range32 {
+    float mn, neg_mx;
+};
+__device__ __forceinline__ Range32 join(Range32 a, Range32 b) { return {min_nan(a.mn, b.mn), min_nan(a.neg_mx, b.neg_mx)}; }
+__device__ __forceinline__ Range32 from_lane(Range32 a, int o) {
+    return {__shfl_xor_sync(0xffffffffu, a.mn, o), __shfl_xor_sync(0xffffffffu, a.neg_mx, o)};
+}
+__device__ __forceinline__ float2 ends(Range32 a) { return make_float2(a.mn, -a.neg_mx); }
+__device__ __forceinline__ Range32 range8(const uint32_t (&w)[8]) {
+    float mn = __uint_as_float(w[0]), mx = mn;
 #pragma unroll
     for (int i = 1; i < 8; i++) {
         mn = min_nan(mn, __uint_as_float(w[i]));
         mx = max_nan(mx, __uint_as_float(w[i]));
     }
-#pragma unroll
-    for (int o = 1; o <= 2; o *= 2) {
-        mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
+    return {mn, -mx};
 }
-// (bf16, two at a time; in the end (min, -max) as one pair, so that one shuffle carries both)
+struct Range16 {
+    uint32_t v;
+};
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -100,14 +107,26 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ void group_range(const uint32_t (&w)[4], float &mn, float &mx) {
+__device__ __forceinline__ Range16 join(Range16 a, Range16 b) { return {min2_nan(a.v, b.v)}; }
+__device__ __forceinline__ Range16 from_lane(Range16 a, int o) { return {__shfl_xor_sync(0xffffffffu, a.v, o)}; }
+__device__ __forceinline__ float2 ends(Range16 a) { return make_float2(__uint_as_float(a.v << 16), -__uint_as_float(a.v & 0xffff0000u)); }
+__device__ __forceinline__ Range16 range8(const uint32_t (&w)[4]) {
     const uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
     const uint32_t hi = max2_nan(max2_nan(w[0], w[1]), max2_nan(w[2], w[3])) ^ 0x80008000u;
-    uint32_t r = min2_nan(kvq_prmt(lo, hi, 0x5410), kvq_prmt(lo, hi, 0x7632));
-    r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, 1));
-    r = min2_nan(r, __shfl_xor_sync(0xffffffffu, r, 2));
-    mn = __uint_as_float(r << 16);
-    mx = -__uint_as_float(r & 0xffff0000u);
+    return {min2_nan(kvq_prmt(lo, hi, 0x5410), kvq_prmt(lo, hi, 0x7632))};
+}
+// The ranges of U rows over the four lanes of a group (lane a of them): of row a % U.
+// Lanes that differ in a bit hand each other the rows that are not theirs.
+template <typename R>
+__device__ __forceinline__ R group_range(const R (&r)[4], int a) {
+    const R x = join(a & 1 ? r[1] : r[0], from_lane(a & 1 ? r[0] : r[1], 1));
+    const R y = join(a & 1 ? r[3] : r[2], from_lane(a & 1 ? r[2] : r[3], 1));
+    return join(a & 2 ? y : x, from_lane(a & 2 ? x : y, 2));
+}
+template <typename R>
+__device__ __forceinline__ R group_range(const R (&r)[2], int a) {
+    const R x = join(a & 1 ? r[1] : r[0], from_lane(a & 1 ? r[0] : r[1], 1));
+    return join(x, from_lane(x, 2));
 }
 
 // The integer n nearest to each t / step, t = x[i] - lo in fp32, ties to even, within
@@ -181,6 +200,14 @@ struct RowWalk {
         }
     }
     __device__ __forceinline__ bool has(int u) const { return valid >> u & 1; }
+    __device__ __forceinline__ int64_t row_of(int u) const {  // (u not a constant)
+        if (FAR) return row[0] + u * RPB;
+        int64_t r = row[0];
+#pragma unroll
+        for (int i = 1; i < U; i++)
+            if (u == i) r = row[i];
+        return r;
+    }
 };
 
 // Lanes of a row: lane e takes dims 8 e .. 8 e + 7, which is cells g = 2 a and 2 a
@@ -189,9 +216,9 @@ struct RowWalk {
 // the row, so lanes e and e ^ 4 exchange a cell and each stores a whole word (two
 // cells): the row leaves the warp as one run of bytes.
 //
-// What bounds it: instructions (about 180 for a lane's 8 values; the schedulers issue
-// in 85 % of the cycles). 4 layers of 32768 positions, 8 heads of 64 dims, bf16 to 4 bits:
-// 90 us for 352 MB, 57 % of the copy rate; one token: 3 us, a launch.
+// What bounds it: from bf16 the instructions, from fp32 the memory. 4 layers of 32768 positions, 8
+// heads of 64 dims to 4 bits: 79 us from bf16 (352 MB, 66 % of the copy rate), 97 us from fp32
+// (621 MB, 95 %); one token: 3 us, a launch.
 template <typename T, int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant__ RwArgs a) {
     constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);
@@ -208,14 +235,19 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
             for (int i = 0; i < int(2 * sizeof(T)); i++) raw[u][i] = 0;
         }
     }
+    // lo and step of a group's rows, a row to a lane (all four lanes computing every row's: 518 us where this is
+    // 494); handed round as one word, whose top bit (step is not negative) says that a value lies far outside
+    // of lo .. lo + TOP step
+    constexpr int TOP = (1 << BITS) - 1;
+    decltype(range8(raw[0])) ranges[U];
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-        float mn, mx, x[8];
-        group_range(raw[u], mn, mx);
-        widen8(raw[u], x);
+    for (int u = 0; u < U; u++) ranges[u] = range8(raw[u]);
+    uint32_t par;
+    {
+        const int mine = ga % U;
+        const float2 e2 = ends(group_range(ranges, ga));
         // (values past the bound need no clamp of their own: their codes are clamped)
-        const float low = min_nan(max_nan(mn, -BOUND), BOUND), high = min_nan(max_nan(mx, -BOUND), BOUND);
-        constexpr int TOP = (1 << BITS) - 1;
+        const float low = min_nan(max_nan(e2.x, -BOUND), BOUND), high = min_nan(max_nan(e2.y, -BOUND), BOUND);
         const __half lo = __float2half_rn(low);
         const float lof = __half2float(lo), d = __fsub_rn(high, lof);
         // d / TOP, rounded once: the product with the rounded 1 / TOP, corrected by its residue (Markstein)
@@ -223,12 +255,23 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
         const float y = __fmul_rn(d, R), quo = __fmaf_rn(__fmaf_rn(-float(TOP), y, d), R, y);
         const __half step = __float2half_rn(max_nan(quo, 0.f));
         const float stf = __half2float(step);
+        const bool inside = e2.x - lof > -0.25f * stf && e2.y - lof < (float(TOP) + 0.25f) * stf;
+        par = uint32_t(__half_as_ushort(lo)) | uint32_t(__half_as_ushort(step)) << 16;
+        if (ga < U && (w.valid >> mine & 1)) a.params[w.kv][w.row_of(mine) * GR + gr] = par;
+        par = (par & 0x7fffffffu) | (inside ? 0u : 0x80000000u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        float x[8];
+        widen8(raw[u], x);
+        const uint32_t p = __shfl_sync(0xffffffffu, par, (threadIdx.x & 28) + u);
+        const float lof = __half2float(__ushort_as_half(uint16_t(p))), stf = __half2float(__ushort_as_half(uint16_t(p >> 16 & 0x7fffu)));
+        const bool inside = int32_t(p) >= 0;
         uint32_t c[2] = {0, 0};  // cells 2 ga, 2 ga + 1
         if (stf > 0.f) {
             float inv;
             uint32_t q[8];
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(stf));
-            const bool inside = (mn - lof) * inv > -0.25f && (mx - lof) * inv < float(TOP) + 0.25f;
             nearest8<TOP>(x, lof, stf, inv, inside, q);
             // the codes of a cell as one number (two, in 8 bits), the low 16 bits of a sum: those of 1.5 * 2^23 are zero
 #pragma unroll
@@ -249,8 +292,6 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
             reinterpret_cast<uint32_t *>(a.codes[w.kv])[row * (HD / 8) + word] = kvq_prmt(first, second, 0x5410);
         else
             reinterpret_cast<uint2 *>(a.codes[w.kv])[row * (HD / 8) + word] = make_uint2(first, second);
-        if (ga == 0)
-            a.params[w.kv][row * GR + gr] = uint32_t(__half_as_ushort(lo)) | uint32_t(__half_as_ushort(step)) << 16;
     }
 }
 
