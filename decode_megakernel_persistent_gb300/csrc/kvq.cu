@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
 
 // The same walk backwards: each lane loads a word (two cells), exchanges one with
 // its partner and stores 8 dims as bf16. Bound by the memory: the cache of the write
-// above in 53 us, 98 % of the copy rate.
+// above in 58 us, 89 % of the copy rate (rows of 128 dims: 96 %).
 template <int BITS, int HD, bool FAR>
 __global__ void __launch_bounds__(RW_THREADS) k_kvq_read(const __grid_constant__ RwArgs a) {
     constexpr int LPR = HD / 8, GR = HD / 32, RPB = RW_THREADS / LPR, U = rw_rows(FAR);

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 LL_OK = 0
 LL_ERR_ARG = -1
@@ -329,16 +330,27 @@ def ll_init_kvq(cfg: ll_config, weights: dict, cache: "KVQCache", stream=None):
     return h
 
 
-def _kvq_call(fn, device: int, *args) -> None:
-    """One packed-cache call on torch's current stream of ``device``. (A call's GPU work
-    takes a few microseconds, so its checks here are kept to as few lookups as they
-    need.)"""
-    import torch
-    if device != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _kvq_call(fn, device, *args)
-    err = ctypes.create_string_buffer(256)
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(device), err, 256)
+class _KVQThread(threading.local):
+    """A thread's buffer for the reason of a refusal."""
+
+    def __init__(self):
+        self.err = ctypes.create_string_buffer(256)
+
+
+_kvq_thread = _KVQThread()
+
+
+def _kvq_call(fn, cache: "KVQCache", *args) -> None:
+    """One packed-cache call on torch's current stream of the cache's device. (A call's GPU
+    work takes a few microseconds, so its checks here are kept to as few lookups as
+    they need.)"""
+    index, torch_c = cache.index, cache.torch_c
+    if index != torch_c._cuda_getDevice():
+        import torch
+        with torch.cuda.device(index):
+            return _kvq_call(fn, cache, *args)
+    err = _kvq_thread.err
+    rc = fn(cache.ref, *args, torch_c._cuda_getCurrentRawStream(index), err, 256)
     if rc != LL_OK:
         raise LLError(rc, err.value.decode())
 
@@ -351,7 +363,7 @@ def ll_kvq_write(cache: "KVQCache", k, v, lens, n_toks=None) -> None:
         raise LLError(LL_ERR_ARG, f"k must be bfloat16 or float32, not {dtype}")
     kr, n_tok = cache._rows(k, "k", dtype, cache.n_kv_heads)
     vr, _ = cache._rows(v, "v", dtype, cache.n_kv_heads, n_tok)
-    _kvq_call(cache.lib.ll_kvq_write, cache.index, cache.ref, kr, vr, cache.in_types[dtype], n_tok,
+    _kvq_call(cache.lib.ll_kvq_write, cache, kr, vr, cache.in_types[dtype], n_tok,
               cache._lens(lens, "lens"), cache._lens(n_toks, "n_toks") if n_toks is not None else None)
 
 
@@ -360,7 +372,7 @@ def ll_kvq_read(cache: "KVQCache", k_out, v_out, lens, n_toks=None) -> None:
     [n_seq, n_tok, n_kv_heads, head_dim] (bf16)."""
     kr, n_tok = cache._rows(k_out, "k_out", cache.bf16, cache.n_kv_heads, None, True)
     vr, _ = cache._rows(v_out, "v_out", cache.bf16, cache.n_kv_heads, n_tok, True)
-    _kvq_call(cache.lib.ll_kvq_read, cache.index, cache.ref, kr, vr, n_tok, cache._lens(lens, "lens"),
+    _kvq_call(cache.lib.ll_kvq_read, cache, kr, vr, n_tok, cache._lens(lens, "lens"),
               cache._lens(n_toks, "n_toks") if n_toks is not None else None)
 
 
@@ -380,7 +392,7 @@ def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=No
         import torch
         out = (torch.zeros if np_ else torch.empty)(q.shape, dtype=q.dtype, device=q.device)
     o, _ = cache._rows(out, "out", cache.bf16, heads, n_tok, True)
-    _kvq_call(cache.lib.ll_kvq_attention, cache.index, cache.ref, qr, heads, n_tok, lp, np_, max_len, scale, o)
+    _kvq_call(cache.lib.ll_kvq_attention, cache, qr, heads, n_tok, lp, np_, max_len, scale, o)
     return out
 
 
@@ -651,7 +663,7 @@ class KVQCache:
                                    bits)
         self.ref = ctypes.byref(self.struct)
         # what every call looks up
-        self.lib, self.index = lib(), dev.index
+        self.lib, self.index, self.torch_c = lib(), dev.index, torch._C
         self.bf16, self.int32 = torch.bfloat16, torch.int32
         self.in_types = {torch.bfloat16: LL_BF16, torch.float32: LL_F32}
 
@@ -680,7 +692,7 @@ class KVQCache:
         seq, token, head, last = t.stride()
         if last != 1:
             raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
-        if written:  # no two rows of an output may share memory
+        if written and not t.is_contiguous():  # no two rows of an output may share memory
             reach = self.head_dim
             for stride, size in sorted(((seq, self.n_seq), (token, tokens), (head, heads))):
                 if size > 1:
