@@ -880,17 +880,17 @@ DecodePlan decode_plan(int seqs, int heads, const KvqSlots *const (&slots)[3], i
 }
 
 template <int BITS, int HD, int WARPS, int NC, typename QT>
-const KvqSlots &decode_slots(int nsm) {
+const KvqSlots &decode_slots(int nsm, int dev) {
     constexpr auto kernel = k_kvq_decode<BITS, HD, WARPS, NC, QT>;
     constexpr int SMEM = DecodeShape<BITS, HD, WARPS>::SMEM;
     static const KvqSlots none = {};
-    return prepared<kernel>(SMEM) ? kvq_slots<kernel>(WARPS * 32, SMEM, nsm) : none;
+    return prepared<kernel>(SMEM, dev) ? kvq_slots<kernel>(WARPS * 32, SMEM, nsm, dev) : none;
 }
 template <int BITS, int HD, int WARPS, int NC, typename QT>
-int decode_launch(const ll_kvq_cache &c, const KvqAttnArgs &a, int splits, cudaStream_t st) {
+int decode_launch(const ll_kvq_cache &c, const KvqAttnArgs &a, int splits, int dev, cudaStream_t st) {
     constexpr auto kernel = k_kvq_decode<BITS, HD, WARPS, NC, QT>;
     constexpr int SMEM = DecodeShape<BITS, HD, WARPS>::SMEM;
-    if (!prepared<kernel>(SMEM)) return LL_ERR_CUDA;
+    if (!prepared<kernel>(SMEM, dev)) return LL_ERR_CUDA;
     return kvq_launch(kernel, dim3(splits, c.n_kv_heads, c.n_seq), WARPS * 32, SMEM, splits, st, a);
 }
 
@@ -914,6 +914,8 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     a.q_head = q.head;
     a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(float(c.head_dim))) * 1.4426950408889634f;
     a.out = out;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LL_ERR_CUDA;
     const int longest = max_len > 0 ? std::min(max_len, c.max_seq) : c.max_seq;
     const int rows = l.n_tok * a.group;
     const int64_t pairs = int64_t(c.n_seq) * c.n_kv_heads;
@@ -921,7 +923,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     // and merge: at 64 dims 4 to 16 million pairs take as long either way (8 heads, 128 rows by 4096 keys: 15.5 us and
     // 15.8; 512 by 4096: 37 and 25), at 128 dims half as many.
     if (rows > 16 && double(pairs) * rows * longest * (c.head_dim / 64) >= double(8 << 20))
-        return launch_kvq_prompt(c, a, type, longest, nsm, st);
+        return launch_kvq_prompt(c, a, type, longest, nsm, dev, st);
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         constexpr int B = bits.value, H = hd.value;
@@ -930,15 +932,15 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
             if (rows <= 16) {
                 auto go = [&](auto nc) {
                     constexpr int tile = DecodeShape<B, H, 4>::TILE;
-                    const KvqSlots *const slots[3] = {&decode_slots<B, H, 16, nc.value, QT>(nsm), &decode_slots<B, H, 8, nc.value, QT>(nsm),
-                                                &decode_slots<B, H, 4, nc.value, QT>(nsm)};
+                    const KvqSlots *const slots[3] = {&decode_slots<B, H, 16, nc.value, QT>(nsm, dev), &decode_slots<B, H, 8, nc.value, QT>(nsm, dev),
+                                                &decode_slots<B, H, 4, nc.value, QT>(nsm, dev)};
                     const DecodePlan plan = decode_plan(c.n_seq, c.n_kv_heads, slots, longest, tile, H * tile);
                     if (plan.warps == 16)
-                        rc = decode_launch<B, H, 16, nc.value, QT>(c, a, plan.splits, st);
+                        rc = decode_launch<B, H, 16, nc.value, QT>(c, a, plan.splits, dev, st);
                     else if (plan.warps == 8)
-                        rc = decode_launch<B, H, 8, nc.value, QT>(c, a, plan.splits, st);
+                        rc = decode_launch<B, H, 8, nc.value, QT>(c, a, plan.splits, dev, st);
                     else
-                        rc = decode_launch<B, H, 4, nc.value, QT>(c, a, plan.splits, st);
+                        rc = decode_launch<B, H, 4, nc.value, QT>(c, a, plan.splits, dev, st);
                 };
                 if (rows <= 8)
                     go(KvqConst<1>{});
@@ -950,7 +952,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
                 const int rt = (rows + CK_ROWS - 1) / CK_ROWS;
                 const int C = splits_for(pairs * rt, 2 * nsm, double(longest) / CK_KEYS);
                 constexpr auto kernel = k_kvq_chunk<B, H, QT>;
-                rc = prepared<kernel>(SMEM)
+                rc = prepared<kernel>(SMEM, dev)
                          ? kvq_launch(kernel, dim3(rt * C, c.n_kv_heads, c.n_seq), CK_THREADS, SMEM, C, st, a, C)
                          : LL_ERR_CUDA;
             }

@@ -145,12 +145,10 @@ __device__ __forceinline__ void put_out32(const KvqOut &o, int s, int j, int hea
     }
 }
 
-// Once per kernel and device: its shared memory, and clusters of up to 16.
+// Once per kernel and device (the current one): its shared memory, and clusters of up to 16.
 template <auto kernel>
-bool prepared(int smem) {
+bool prepared(int smem, int dev) {
     static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return true;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
@@ -183,12 +181,11 @@ struct KvqSlots {
     int n[KVQ_CLUSTER_SIZES];
 };
 template <auto kernel>
-const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
+const KvqSlots &kvq_slots(int threads, int smem, int nsm, int dev) {
     static KvqSlots slots[64];
     static std::atomic<uint64_t> known{0};
     static std::mutex mu;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = 0;
+    dev &= 63;
     if (known.load(std::memory_order_acquire) >> dev & 1) return slots[dev];
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < KVQ_CLUSTER_SIZES; i++) {
@@ -216,7 +213,7 @@ const KvqSlots &kvq_slots(int threads, int smem, int nsm) {
 
 // The kernel for prompts (kvq_prompt.cu): 256 query rows of a KV head to a block.
 constexpr int KVQ_PROMPT_ROWS = 256;
-// longest: the longest length it is laid out for.
-int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, cudaStream_t st);
+// longest: the longest length it is laid out for; dev: the current device.
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, int dev, cudaStream_t st);
 
 }  // namespace ll

@@ -693,18 +693,18 @@ int prompt_splits(int64_t units, const KvqSlots &slots, double steps) {
 
 }  // namespace
 
-int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, cudaStream_t st) {
+int launch_kvq_prompt(const ll_kvq_cache &c, const KvqAttnArgs &a, int type, int longest, int nsm, int dev, cudaStream_t st) {
     const int64_t rows = int64_t(a.l.n_tok) * a.group, tiles = (rows + KVQ_PROMPT_ROWS - 1) / KVQ_PROMPT_ROWS * c.n_kv_heads;
     int rc = LL_OK;
     kvq_dispatch(c, [&](auto bits, auto hd) {
         auto go = [&](auto qt) {
             constexpr auto kernel = k_kvq_prompt<bits.value, hd.value, decltype(qt)>;
             constexpr int SMEM = Shape<hd.value>::SMEM;
-            if (!prepared<kernel>(SMEM)) {
+            if (!prepared<kernel>(SMEM, dev)) {
                 rc = LL_ERR_CUDA;
                 return;
             }
-            const int C = prompt_splits(tiles * c.n_seq, kvq_slots<kernel>(THREADS, SMEM, nsm), double(longest) / KEYS);
+            const int C = prompt_splits(tiles * c.n_seq, kvq_slots<kernel>(THREADS, SMEM, nsm, dev), double(longest) / KEYS);
             rc = kvq_launch(kernel, dim3(unsigned(tiles * C), 1, c.n_seq), THREADS, SMEM, C, st, a, C);
         };
         if (type == LL_F32)
