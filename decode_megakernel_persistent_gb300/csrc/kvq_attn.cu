@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     static_assert(NW * COLS * HD * 4 <= S::SMEM, "the merge fits in the ring's memory");
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float s_ml[NW][COLS][2];  // the warps' m and l
-    __shared__ float s_recv[COLS * HD + 32];  // the cluster's sums of this block's share of the outputs, by rank (16 shares, rounded up)
-    __shared__ float s_rml[16][COLS][2]; // and the ranks' m and l
+    __shared__ __align__(8) float s_recv[COLS * HD + 32];  // the cluster's sums of this block's share of the outputs, by rank (16 shares, rounded up)
+    __shared__ __align__(8) float s_rml[16][COLS][2]; // and the ranks' m and l
     __shared__ uint64_t s_full[NW][S::STAGES];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const KvqConsts consts;
