@@ -821,14 +821,13 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
 
 // ---- launches ----------------------------------------------------------------------
 
-// Splits of one unit of work (a power of two, at most 16: a cluster) for `units`
-// units whose longest walk has `steps` steps, with `slots` blocks on the device:
+// The chunk kernel's splits of one unit of work (a power of two, at most 16: a cluster) for
+// `units` units whose longest walk has `steps` key tiles, with `slots` blocks on the device:
 // the fewest of a block's own steps and the device's share of all blocks' steps
 // together. A block's start and merge take as long as EXTRA steps, and a step on
-// a full SM twice as long as on one that holds a single block (measured with 4-bit
-// rows of 64 dims: 0.67 us a step alone, 2.7 us for start and merge). Over lengths
-// from 1024 to 32768 and 8 to 512 units the splits that it takes are within 2 % of
-// the best of 1, 2, 4, 8 and 16.
+// a full SM twice as long as on one that holds a single block. Of 22 layouts measured (64 to
+// 256 rows by 512 to 20000 keys) it was within 13 % of the best of 1, 2, 4, 8 and 16 in all,
+// within 5 % in 17.
 int splits_for(int64_t units, int slots, double steps) {
     constexpr double EXTRA = 4;
     int best = 1;
@@ -847,38 +846,39 @@ int splits_for(int64_t units, int slots, double steps) {
 // block, and blocks that share a unit. slots: the blocks that the device holds at once
 // with one, two and four of them (of 16, 8 and 4 warps) to an SM.
 //
-// Where 16 splits of each unit fill the device, small blocks do, and balance ragged lengths.
-// Otherwise the fewest microseconds, by what was measured: a warp's step (a tile)
-// takes 0.45 + 0.06 x the warps that its SM holds where it is 32 keys of 64 dims or 16
-// of 128, 0.62 + 0.107 x for 32 of 128; start and merge 3.4 + 0.07 a warp, and 0.9
-// more where SMs hold several blocks. As lengths may differ, the time of one long
-// sequence alone counts as much as that of all as long. A sequence of 32768 keys, 8 heads of
-// 64 dims in 4 bits: 12.6 us in 12 splits of 16 warps (18.1 in 16 of 4: a device of 152 SMs holds only
-// seven clusters of 16 without two blocks on an SM); of 131072, 34 us (58); 2 sequences of 32768, 19.9 (22.5).
+// The fewest microseconds, by what was measured: a warp's step (a tile) takes 0.45 +
+// 0.06 x the warps that its SM holds where it is 32 keys of 64 dims or 16 of 128, 0.62 +
+// 0.107 x for 32 of 128; start and merge 3.4 + 0.07 a warp, and 0.9 more where SMs hold
+// several blocks; more blocks than fit run in rounds, the last of them with what is left. As
+// lengths may differ, half of that is added, or the time of one long sequence alone if that is
+// more. Of 128 layouts measured (2 to 1024 units of 512 to 131072 keys, uniform and ragged, one
+// token and a few) it was within 10 % of the best of all warps and splits in 123, 18 % off at worst. A sequence of 32768 keys, 8 heads of 64 dims in 4
+// bits: 12.6 us in 12 splits of 16 warps (18.1 in 16 of 4: a device of 152 SMs holds only
+// seven clusters of 16 without two blocks on an SM); 32 of them, 128 dims in 8 bits: 373 us in 4 splits
+// of 4 warps (397 in 16, 481 in one).
 struct DecodePlan {
     int warps, splits;
 };
 DecodePlan decode_plan(int seqs, int heads, const KvqSlots *const (&slots)[3], int keys, int tile, int tile_values) {
-    DecodePlan best = {4, 1};
-    const KvqSlots &small = *slots[2];
-    const int64_t units = int64_t(seqs) * heads;
-    if (units * 16 > small.n[KVQ_CLUSTER_SIZES - 1]) {
-        best.splits = splits_for(units, small.n[0], double(keys) / (4 * tile));
-        return best;
-    }
     const double fixed = tile_values > 2048 ? 0.62 : 0.45, per_warp = tile_values > 2048 ? 0.107 : 0.06;
+    const int64_t units = int64_t(seqs) * heads;
     const int tiles = (keys + tile - 1) / tile;
+    DecodePlan best = {4, 1};
     double least = 0;
     for (int v = 2; v >= 0; v--)
         for (int i = 0; i < KVQ_CLUSTER_SIZES; i++) {
-            const int c = KVQ_CLUSTERS[i], warps = 16 >> v, one = slots[0]->n[i], two = slots[1]->n[i], four = small.n[i];
-            if (units * c > slots[v]->n[i]) continue;
+            const int c = KVQ_CLUSTERS[i], warps = 16 >> v, room = slots[v]->n[i];
+            if (room < 1) continue;
             const int steps = ((tiles + c - 1) / c + warps - 1) / warps;
-            auto time = [&](int n) {
-                const int blocks = n * c, per_sm = blocks <= one ? 1 : blocks <= two ? 2 : 4 * blocks <= 3 * four ? 3 : 4;
-                return 3.4 + 0.07 * warps + (per_sm > 1 ? 0.9 : 0.) + steps * (fixed + per_warp * warps * per_sm);
+            const double start = 3.4 + 0.07 * warps, full = start + steps * (fixed + per_warp * 16);
+            auto time = [&](int64_t n) {
+                const int64_t rounds = n * c / room;
+                const int rest = int(n * c - rounds * room);
+                if (!rest) return rounds * full;
+                const int per_sm = rest <= slots[0]->n[i] ? 1 : rest <= slots[1]->n[i] ? 2 : 4 * rest <= 3 * slots[2]->n[i] ? 3 : 4;
+                return rounds * full + start + (per_sm > 1 ? 0.9 : 0.) + steps * (fixed + per_warp * warps * per_sm);
             };
-            const double t = time(int(units)) + time(heads);
+            const double all = time(units), t = all + std::max(all / 2, time(heads));
             if (least == 0 || t < least) {
                 least = t;
                 best = {warps, c};
