@@ -250,10 +250,8 @@ __global__ void __launch_bounds__(RW_THREADS) k_kvq_write(const __grid_constant_
         const float low = min_nan(max_nan(e2.x, -BOUND), BOUND), high = min_nan(max_nan(e2.y, -BOUND), BOUND);
         const __half lo = __float2half_rn(low);
         const float lof = __half2float(lo), d = __fsub_rn(high, lof);
-        // d / TOP, rounded once: the product with the rounded 1 / TOP, corrected by its residue (Markstein)
         constexpr float R = 1.f / float(TOP);
-        const float y = __fmul_rn(d, R), quo = __fmaf_rn(__fmaf_rn(-float(TOP), y, d), R, y);
-        const __half step = __float2half_rn(max_nan(quo, 0.f));
+        const __half step = __float2half_rn(max_nan(__fmul_rn(d, R), 0.f));
         const float stf = __half2float(step);
         const bool inside = e2.x - lof > -0.25f * stf && e2.y - lof < (float(TOP) + 0.25f) * stf;
         par = uint32_t(__half_as_ushort(lo)) | uint32_t(__half_as_ushort(step)) << 16;

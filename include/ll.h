@@ -305,10 +305,10 @@ int ll_decode_step_static(const ll_config *cfg, const ll_weights *w, uint16_t *k
  * code of `bits` bits per dim, which stands for the value
  *     fp16(lo + step * code)                      (one rounding).
  * Writing takes, over the group's values x (each clamped to +-60000):
- *     lo = fp16(min x),  step = fp16((max x - lo) / (2^bits - 1)),
+ *     lo = fp16(min x),  step = fp16((max x - lo) * fp32(1 / (2^bits - 1))),
  *     code = the integer nearest to (x - lo) / step, ties to even, clamped to
  *            [0, 2^bits - 1]; 0 where step is 0 (it is never below),
- * the differences and step's quotient in fp32. So a value is read back within half
+ * the differences and step's product in fp32. So a value is read back within half
  * a step of itself, up to the fp16 roundings of lo, step and the value. A group
  * holding a NaN reads back as NaN.
  *

@@ -15,7 +15,7 @@ def quantise(x, bits):
     x = x.detach().float().cpu()
     x = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32).clamp(-BOUND, BOUND)  # (keeps NaN)
     lo = x.amin(-1).half()  # (NaN if any is)
-    step = ((x.amax(-1) - lo.float()) / top).clamp(min=0).half()
+    step = ((x.amax(-1) - lo.float()) * torch.tensor(1.0 / top)).clamp(min=0).half()  # (1 / top rounded to fp32)
     # the integer nearest to (x - lo) / step: the difference in fp32, its quotient in fp64, where
     # 24 bits by 11 cannot round onto a border between two integers
     t, sf = (x - lo.float()[..., None]).double(), step.double()[..., None]
