@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 //
 // What bounds it: where blocks fill the device, the unpacking (8 sequences of 32768, 128 dims in
 // 4 bits: the schedulers issue in 63 % of the cycles, the ALU pipe is busy in 51 %); 32 of
-// them take 271 us for 1.34 GB, 73 % of the copy rate. Where few do, each
+// them take 266 us for 1.34 GB, 74 % of the copy rate. Where few do, each
 // warp's chain of a tile (0.7 us alone) and start and merge (3 to 5 us): one
 // sequence of 32768 positions of 64 dims 12.6 us, of 1024 4.4 us.
 template <int BITS, int HD, int WARPS>
