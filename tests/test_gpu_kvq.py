@@ -326,6 +326,60 @@ def test_strided_sequences_past_32_bits():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
+def test_rows_past_32_bits():
+    """One sequence whose codes reach past 2^31 bytes. Every position holds the same K and V row but three (the first, one in
+    the middle, the last), whose K rows win by far in turn: each query row gives its key's V."""
+    M, hd, bits = (1 << 24) + 5, 128, 8
+    c = ll.KVQCache.empty(1, 1, M, hd, bits)
+    g = gen(31)
+    k = torch.randn(1, 1, 1, hd, generator=g, device="cuda").bfloat16() * 0.01
+    v = torch.randn(1, 1, 1, hd, generator=g, device="cuda").bfloat16()
+    c.write(k.expand(1, M, 1, hd), v.expand(1, M, 1, hd), i32([M]))
+    at = [0, M // 2 + 1, M - 1 - 400]
+    rows = torch.zeros(3, hd, device="cuda")
+    for i, p in enumerate(at):
+        rows[i, 32 * i:32 * i + 32] = 16.0 * torch.randn(32, generator=g, device="cuda").sign()
+        vi = torch.randn(1, 1, 1, hd, generator=g, device="cuda").bfloat16()
+        c.write(rows[i].bfloat16().view(1, 1, 1, hd), vi, i32([p + 1]))
+    back = [torch.empty(1, 1, 1, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = []
+    for p in at:
+        c.read(back[0], back[1], i32([p + 1]))
+        want.append(back[1].flatten().clone())
+    for T in (1, 4, 40, 400):
+        q = rows.bfloat16()[torch.arange(4 * T, device="cuda") % 3].view(1, T, 4, hd)
+        out = c.attention(q, i32([M])).view(4 * T, hd)
+        for r in range(4 * T):
+            # (its key's score is 16 * 16 * 32 / sqrt(128) = 724 above the others': their weights are zeros; the product with
+            # q is exact but for the K codes, whose group is +-16 alone, and V comes back as it is read)
+            assert torch.equal(out[r], want[r % 3]), (T, r)
+
+
+@pytest.mark.parametrize("S,KV", [(65535, 1), (1, 32767), (300, 200)])
+@pytest.mark.parametrize("T", [1, 17])
+def test_many_sequences_and_heads(S, KV, T):
+    """The largest counts of sequences and heads. With one position per token, each row attends to those before it."""
+    M, hd, bits = 17, 64, 4
+    c = ll.KVQCache.empty(S, KV, M, hd, bits)
+    k, v = (torch.randn(S, T, KV, hd, generator=gen(i), device="cuda").bfloat16() for i in (1, 2))
+    q = torch.randn(S, T, KV, hd, generator=gen(3), device="cuda").bfloat16()
+    lens = torch.full((S,), T, dtype=torch.int32, device="cuda")
+    c.write(k, v, lens)
+    kb, vb = torch.empty_like(k), torch.empty_like(v)
+    c.read(kb, vb, lens)
+    out = c.attention(q, lens)
+    for s, h in ((0, 0), (S - 1, KV - 1), (S // 2, KV // 3), (S // 3, KV // 2)):
+        one = ll.KVQCache(c.k_codes[s:s + 1, h:h + 1], c.k_params[s:s + 1, h:h + 1], c.v_codes[s:s + 1, h:h + 1],
+                          c.v_params[s:s + 1, h:h + 1], bits)
+        vals = []
+        for x, codes, params, b in ((k, one.k_codes, one.k_params, kb), (v, one.v_codes, one.v_params, vb)):
+            wc, wp, val = expect_rows(x[s, :, h], bits)
+            assert torch.equal(codes[0, 0, :T].cpu(), wc) and same_params(params[0, 0, :T].cpu(), wp)
+            assert torch.equal(b[s, :, h].cpu(), val.float().bfloat16())
+            vals.append(val.cuda()[None, None])
+        check_attention(one, vals[0], vals[1], q[s:s + 1, :, h:h + 1], [T], [T], out[s:s + 1, :, h:h + 1])
+
+
 @pytest.mark.parametrize("T,cap", [(1, 100), (3, 100), (30, 100), (30, 20000)])
 def test_strided_queries_and_outputs(T, cap):
     """q as columns of a fused projection, out as columns of a wider buffer: the rest of it stays."""
