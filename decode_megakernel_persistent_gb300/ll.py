@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 LL_OK = 0
@@ -89,6 +90,9 @@ class ll_kvq_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("seq", "token", "head")]
 
 
+_rows_bytes = struct.Struct("@Pqqq").pack  # an ll_kvq_rows, a fifth of the time that the ctypes object takes
+
+
 _lib = None
 
 
@@ -141,7 +145,8 @@ def lib() -> ctypes.CDLL:
     L.ll_handle_plan.restype = ctypes.c_int
     L.ll_prefill.argtypes = [vp, vp, i32, i32, vp, vp]
     L.ll_prefill.restype = ctypes.c_int
-    cachep, rowsp, err = ctypes.POINTER(ll_kvq_cache), ctypes.POINTER(ll_kvq_rows), [ctypes.c_char_p, ctypes.c_size_t]
+    # (rows: an ll_kvq_rows by reference, or its bytes)
+    cachep, rowsp, err = ctypes.POINTER(ll_kvq_cache), vp, [ctypes.c_char_p, ctypes.c_size_t]
     L.ll_kvq_write.argtypes = [cachep, rowsp, rowsp, i32, i32, vp, vp, vp] + err
     L.ll_kvq_write.restype = ctypes.c_int
     L.ll_kvq_read.argtypes = [cachep, rowsp, rowsp, i32, vp, vp, vp] + err
@@ -679,7 +684,7 @@ class KVQCache:
         return cls(codes[0], params[0], codes[1], params[1], bits)
 
     def _rows(self, t, name: str, dtype, heads: int, n_tok=None, written: bool = False):
-        """t as an ll_kvq_rows reference, and its tokens."""
+        """t as an ll_kvq_rows' bytes, and its tokens."""
         if getattr(t, "device", None) != self.device:
             raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor on {self.device}, the cache's device")
         if t.dtype != dtype:
@@ -699,7 +704,7 @@ class KVQCache:
                     if stride < reach:
                         raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
                     reach += stride * (size - 1)
-        return ctypes.byref(ll_kvq_rows(t.data_ptr(), seq, token, head)), tokens
+        return _rows_bytes(t.data_ptr(), seq, token, head), tokens
 
     def _lens(self, t, name: str) -> int:
         if getattr(t, "device", None) != self.device or t.dtype != self.int32 or t.shape != (self.n_seq,) or not t.is_contiguous():

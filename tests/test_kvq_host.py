@@ -40,6 +40,8 @@ int main(void) {
     want = [ctypes.sizeof(ll.ll_kvq_cache), ll.ll_kvq_cache.seq_rows.offset, ll.ll_kvq_cache.bits.offset,
             ctypes.sizeof(ll.ll_kvq_rows), ll.ll_kvq_rows.head.offset]
     assert got == want
+    want = ll.ll_kvq_rows(4096, 3, -5, 1 << 40)  # as the binding packs it
+    assert ll._rows_bytes(4096, 3, -5, 1 << 40) == ctypes.string_at(ctypes.addressof(want), ctypes.sizeof(want))
 
 
 def cache(**k):
