@@ -872,7 +872,7 @@ DecodePlan decode_plan(int seqs, int heads, const KvqSlots *const (&slots)[3], i
             const int steps = ((tiles + c - 1) / c + warps - 1) / warps;
             const double start = 3.4 + 0.07 * warps, full = start + steps * (fixed + per_warp * 16);
             auto time = [&](int64_t n) {
-                const int64_t rounds = n * c / room;
+                const int64_t rounds = n * c < room ? 0 : n * c / room;
                 const int rest = int(n * c - rounds * room);
                 if (!rest) return rounds * full;
                 const int per_sm = rest <= slots[0]->n[i] ? 1 : rest <= slots[1]->n[i] ? 2 : 4 * rest <= 3 * slots[2]->n[i] ? 3 : 4;
