@@ -326,6 +326,24 @@ def test_strided_sequences_past_32_bits():
     assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
 
 
+@pytest.mark.parametrize("T,cap", [(1, 400), (4, 400), (40, 400), (300, 400), (1, 40000), (300, 40000)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_bad_queries_stay_in_their_rows(T, cap, hd, value):
+    """A query row with a NaN or an infinity has no softmax: NaN, and the other rows as they are without it."""
+    M, KV, group = 400, 2, 4
+    c, kv, vv = make_cache(17, 1, KV, M, hd, 4, [M], cap)
+    q = torch.randn(1, T, KV * group, hd, generator=gen(6), device="cuda").bfloat16()
+    base = c.attention(q, i32([M]))
+    bad = torch.zeros(1, T, KV * group, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 0), (T // 2, 3), (T - 1, KV * group - 1)):
+        q[0, t, h, (7 * t + h) % hd] = value
+        bad[0, t, h] = True
+    out = c.attention(q, i32([M]))
+    assert bool(torch.isnan(out[bad]).all())
+    assert torch.equal(out[~bad], base[~bad])
+
+
 def test_rows_past_32_bits():
     """One sequence whose codes reach past 2^31 bytes. Every position holds the same K and V row but three (the first, one in
     the middle, the last), whose K rows win by far in turn: each query row gives its key's V."""
