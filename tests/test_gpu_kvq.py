@@ -453,6 +453,45 @@ def test_decode_loop_captured_and_on_a_side_stream():
             check_attention(c, kq, vq, q, [i + 1, i + 1, 0], [1] * S, out)
 
 
+def test_calls_at_once_on_two_streams():
+    """Single tokens, chunks and prompts over one cache, on two streams at once and as two graphs replayed at once,
+    while a third writes another cache."""
+    KV, M, hd = 4, 3000, 64
+    c, kv, vv = make_cache(23, 2, KV, M, hd, 4, [M, M - 7])
+    other = ll.KVQCache.empty(2, KV, M, hd, 8)
+    rows = torch.randn(2, M, KV, hd, generator=gen(1), device="cuda").bfloat16()
+    lens = i32([M, M - 7])
+    qs = [[torch.randn(2, t, 4 * KV, hd, generator=gen(40 + i), device="cuda").bfloat16() for t in (1, 9, 700)] for i in range(2)]
+    want = [[c.attention(q, lens) for q in x] for x in qs]
+    outs = [[torch.zeros_like(q) for q in x] for x in qs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+
+    def run(i):
+        for q, o in zip(qs[i], outs[i]):
+            c.attention(q, lens, out=o)
+
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            run(i)
+    for how in range(2):
+        for x in outs:
+            for o in x:
+                o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    graphs[i].replay() if how else run(i)
+            with torch.cuda.stream(streams[2]):
+                other.write(rows, rows, lens)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(outs, want) for a, b in zip(x, y))
+    last = ll.KVQCache.empty(2, KV, M, hd, 8)
+    last.write(rows, rows, lens)
+    assert torch.equal(other.k_codes, last.k_codes) and torch.equal(other.v_params, last.v_params)
+
+
 def test_first_calls_of_a_process_may_be_captured():
     """No call needs one before it outside a graph: a new process captures its first write, read and attention (of
     one token, a few and many), replays them and gets what the plain calls give."""
