@@ -53,7 +53,7 @@ int launch_kvq_read(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_ro
 int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
                          int max_len, float scale, const KvqOut &out, int nsm, cudaStream_t st);
 
-// Sequence s of the cache alone.
+// Sequence s of the cache alone. Its parameters may begin 8 bytes off a 16-byte border (64 dims, an odd row).
 inline ll_kvq_cache kvq_sequence(const ll_kvq_cache &c, int s) {
     ll_kvq_cache one = c;
     const int64_t row = s * c.seq_rows, codes = row * (c.head_dim * c.bits / 8), params = row * (c.head_dim / 16);

@@ -128,9 +128,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     const int t0 = int(int64_t(tiles) * rank / C), t1 = int(int64_t(tiles) * (rank + 1) / C);
     uint8_t *const ring = smem + warp * (S::STAGES * S::STAGE);
     const uint32_t full = sptr(s_full[warp]);
-    // rows of 8 bytes of parameters are copied from an even row on (skew: the first one's place); the
-    // row behind the last position of all may not exist, so an odd last one is fetched when its tile is used
-    const int skew = PB == 8 ? int(row0 & 1) : 0;
+    // rows of 8 bytes of parameters are copied from a 16-byte border on (skew: the first one's place. By its address, as
+    // the arrays of one layer of a handle's cache may begin at an odd row); the row behind the last position of all
+    // may not exist, so one in the middle of 16 bytes is fetched when its tile is used
+    const int skew = PB == 8 ? int((row0 + int64_t(reinterpret_cast<uintptr_t>(a.kp) / 8)) & 1) : 0;
     const bool odd_end = PB == 8 && limit == a.max_seq && ((skew + limit) & 1);
     const int edge_from = min(first + 1, limit) - int(odd_end);
     // (lane 0; tiles come in order, NW apart: the addresses move by constants)
