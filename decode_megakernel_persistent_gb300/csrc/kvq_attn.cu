@@ -99,12 +99,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, C = gridDim.x, rank = blockIdx.x;
-    // q first, while the lengths are on their way: (nc) row 8 nc + g, this lane's dims 32 gr + 8 t ..
+    // q first, while the lengths are on their way: (nc) row 8 nc + g, this lane's dims 32 gr + 8 t .. (Rows of padded
+    // tokens may not exist, so with counts of tokens q waits for its sequence's.)
+    const int n = a.l.n(s), rows = n * a.group;  // query rows
+    if (n == 0) return;
     float qv[NC][GR][8];
 #pragma unroll
     for (int nc = 0; nc < NC; nc++) {
         const int r = 8 * nc + g;
-        const bool ok = r < a.l.n_tok * a.group;
+        const bool ok = r < rows;
         const QT *q = static_cast<const QT *>(a.q) + s * a.q_seq + (ok ? r / a.group : 0) * a.q_tok +
                       (h * a.group + (ok ? r % a.group : 0)) * a.q_head + 8 * t;
 #pragma unroll
@@ -116,9 +119,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                 for (int i = 0; i < 8; i++) qv[nc][gr][i] = 0.f;
         }
     }
-    const int n = a.l.n(s), len = a.l.len(s);
-    if (n == 0) return;
-    const int rows = n * a.group, first = len - n;  // query rows, and the first token's position
+    const int len = a.l.len(s), first = len - n;    // (first: the first token's position)
     const int limit = min(len, a.max_seq);          // no token sees a position from here on
     const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first remote store)

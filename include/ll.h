@@ -329,8 +329,9 @@ int ll_decode_step_static(const ll_config *cfg, const ll_weights *w, uint16_t *k
  * len_dev[s] positions (device int32, the call's own tokens among them), and the
  * call handles its last n tokens, n = n_tok_dev[s] held within [0, n_tok] (device
  * int32), or n_tok for every sequence when n_tok_dev is NULL. Token j < n is at
- * position len - n + j. Tokens outside [0, max_seq) and padded tokens j >= n are
- * skipped: nothing is read or written for them. */
+ * position len - n + j. Padded tokens j >= n are skipped: nothing is read or
+ * written for them, so their rows need not exist. So are, by ll_kvq_write and
+ * ll_kvq_read, tokens outside [0, max_seq). */
 #define LL_BF16 0
 #define LL_F32 1
 
@@ -370,7 +371,8 @@ int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *
  * n_kv_heads), at most 8 query heads to a KV head. q and out: bf16 rows
  * [n_seq][n_tok][n_q_heads][head_dim] by their strides (out's not 0 in use). A
  * token at a position below 0 (a sequence of length 0, say) has nothing to look
- * at and gives zeros; rows of padded tokens j >= n keep what they hold. The
+ * at and gives zeros, one at max_seq or behind sees the whole cache; rows of
+ * padded tokens j >= n keep what they hold. The
  * tokens' own K and V rows must have been written before. scale: finite and
  * positive, or 0 for 1 / sqrt(head_dim). max_len: a bound on the lengths that the
  * launch is laid out for, 0 for max_seq; longer lengths give the same results,
