@@ -1,7 +1,7 @@
 // kvq_attn.cu -- attention over the packed KV cache.
 //
 // One pass over the positions with the running maximum and sum of a softmax: a
-// tile of keys gives scores S = Q K^T, the maximum m grows where they pass it,
+// tile of keys gives scores S = Q K^T, the reference m grows where they pass it (KVQ_HOLD),
 // P = exp(S - m) adds to the sum l and to O = P V, and O / l is the output. K and
 // V rows come packed; they become fp16 numbers in registers, exactly the values
 // the format defines, on their way to the tensor cores.
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
 #pragma unroll
                 for (int mt = 1; mt < NT; mt++) x = fmaxf(x, fmaxf(sc[mt][nc][b], sc[mt][nc][2 + b]));
                 top[nc][b] = x * fac[nc][b];
-                grow |= top[nc][b] > m[nc][b] + KVQ_HOLD;
+                grow |= top[nc][b] > m[nc][b] + (KVQ_ROOM + KVQ_HOLD);
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                     float x = top[nc][b];
 #pragma unroll
                     for (int d = 4; d <= 16; d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    x = fmaxf(m[nc][b], x);
+                    x = fmaxf(m[nc][b], x - KVQ_ROOM);
                     const float al = m[nc][b] == -INFINITY ? 0.f : ex2(m[nc][b] - x);
                     m[nc][b] = x;
                     l[nc][b] *= al;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
 #pragma unroll
             for (int nb = 0; nb < CK_KEYS / 8; nb++) x = fmaxf(x, fmaxf(sc[nb][2 * b], sc[nb][2 * b + 1]));
             top[b] = x * fac[b];
-            grow |= top[b] > m[b] + KVQ_HOLD;
+            grow |= top[b] > m[b] + (KVQ_ROOM + KVQ_HOLD);
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
                 float x = top[b];
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                x = fmaxf(m[b], x);
+                x = fmaxf(m[b], x - KVQ_ROOM);
                 const float al = m[b] == -INFINITY ? 0.f : ex2(m[b] - x);
                 m[b] = x;
                 l[b] *= al;

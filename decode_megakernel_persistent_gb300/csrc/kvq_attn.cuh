@@ -28,10 +28,13 @@ struct KvqAttnArgs {
     KvqOut out;
 };
 
-// The running maximum of a row moves only once a score passes it by this (log2
-// units): until then probabilities are taken against the held maximum, at most
-// 2^8, well inside fp16, and neither l nor O needs rescaling.
-constexpr float KVQ_HOLD = 8.f;
+// A row's reference m is its running maximum less KVQ_ROOM (log2 units), and moves only once
+// a score passes it by KVQ_ROOM + KVQ_HOLD: until then neither l nor O needs rescaling.
+// Probabilities are taken against m, so the largest score's is 2^7 to 2^15. They enter the products as
+// fp16 (the matrix rate of its 11 bits; K and V themselves come with 4 or 8), whose range
+// that uses up: the smallest that is not lost is 2^-32 of the largest or less, where
+// it would be 2^-25 with the maximum itself as the reference.
+constexpr float KVQ_HOLD = 8.f, KVQ_ROOM = 7.f;
 
 __device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 

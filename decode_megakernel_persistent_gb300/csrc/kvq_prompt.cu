@@ -576,9 +576,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                         pass(m_use, KvqConst<0>{});
                 };
                 both(m == -INFINITY ? 0.f : m);
-                const bool grow = top > m + KVQ_HOLD;
+                const bool grow = top > m + (KVQ_ROOM + KVQ_HOLD);
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float to_m = grow ? top : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
+                    const float to_m = grow ? top - KVQ_ROOM : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
                     m = to_m;
                     both(m == -INFINITY ? 0.f : m);
                     l *= al;

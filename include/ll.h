@@ -377,7 +377,8 @@ int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *
  * positive, or 0 for 1 / sqrt(head_dim). max_len: a bound on the lengths that the
  * launch is laid out for, 0 for max_seq; longer lengths give the same results,
  * more slowly. Products run on tensor cores in fp16 (q scaled by a power of two
- * per row, the probabilities rounded to fp16) with fp32 sums; the softmax is fp32.
+ * per row, the probabilities rounded to fp16, those below 2^-32 of a row's largest
+ * to 0) with fp32 sums; the softmax is fp32.
  * The same call on the same data repeats bit for bit. */
 int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_heads, int32_t n_tok,
                      const int32_t *len_dev, const int32_t *n_tok_dev, int32_t max_len, float scale,

@@ -47,3 +47,27 @@ def test_query_storage_that_ends_with_the_last_token(T, group, cap, hd):
         out[s, :n[s]] = got[at:at + n[s] * row].view(n[s], H, hd)
     check_attention(c, kv, vv, q, lens, n, out, mark=9.0)
     assert bool((got[:first] == 5).all()) and bool((got[end:] == 5).all())
+
+
+@pytest.mark.parametrize("T,group,L,cap", [(1, 4, 1, 32), (1, 4, 40, 40), (1, 4, 5000, 5000), (2, 8, 600, 600), (40, 2, 700, 700), (24, 4, 900, 60000),
+                                           (300, 4, 5000, 5000), (300, 4, 5000, 40000)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("x", [12, 20, 26, 30])
+def test_many_small_weights_behind_a_dominant_key(T, group, L, cap, hd, x):
+    """The first key outweighs each of the others 2^x times, and only the others have a V: the output is
+    what they add up to. K and V are values that the packed rows hold exactly, the scores 0 and x log2 units."""
+    KV, M = 2, L + T
+    c = ll.KVQCache.empty(1, KV, max(M, cap), hd, 4)
+    k, v = torch.zeros(1, M, KV, hd, device="cuda"), torch.ones(1, M, KV, hd, device="cuda")
+    k[0, 0, :, :32] = 1.0
+    v[0, 0] = 0.0
+    c.write(k, v, i32([M]))
+    q = torch.ones(1, T, KV * group, hd, device="cuda").bfloat16()
+    out = c.attention(q, i32([M]), scale=x * 0.6931471805599453 / 32).double()
+    others = (L + torch.arange(T, device="cuda", dtype=torch.float64)) * 2.0 ** -x  # (token t sees L + t of them)
+    want = (others / (1 + others))[None, :, None, None]
+    # bf16's rounding; a probability's to fp16, 2^-11 of it or half of fp16's smallest step, where the first key's is
+    # 2^7 at least; scores (exact products, one fp32 factor) and exp2 within 2^-18 at 30 log2 units
+    tol = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** (x - 32) + 2.0 ** -18
+    off = (out - want).abs() / want
+    assert float(off.max()) <= tol, float(off.max())
