@@ -37,9 +37,53 @@ __device__ __forceinline__ uint64_t kvq_add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A group's parameters (lo, step) that stand for NaN.
-__device__ __forceinline__ bool kvq_is_nan(uint32_t par) {
-    return (par & 0x7fffu) > 0x7c00u || (par >> 16 & 0x7fffu) > 0x7c00u;
+// Whether a group's parameters (lo, step) stand for a NaN or an infinity at some code: values
+// grow or fall with the code and a lo that is not finite reaches every one, so the largest code tells.
+template <int BITS>
+__device__ __forceinline__ bool kvq_not_finite(uint32_t par) {
+    const __half v = __hfma(__ushort_as_half(uint16_t(par >> 16)), __int2half_rn((1 << BITS) - 1), __ushort_as_half(uint16_t(par)));
+    return (__half_as_ushort(v) & 0x7c00u) == 0x7c00u;
+}
+// The value of dim d (of 32) of a row's group gr.
+template <int BITS, int HD>
+__device__ __forceinline__ __half kvq_value(const uint8_t *codes, uint32_t par, int gr, int d) {
+    const int el = ((d >> 2) * (HD / 32) + gr) * 4 + (d & 3);
+    const int code = BITS == 8 ? codes[el] : codes[el >> 1] >> (4 * (el & 1)) & 15;
+    return __hfma(__ushort_as_half(uint16_t(par >> 16)), __int2half_rn(code), __ushort_as_half(uint16_t(par)));
+}
+// A pair of values, those that are not finite as zeros.
+__device__ __forceinline__ uint32_t kvq_finite2(uint32_t v) {
+    if ((v & 0x7c00u) == 0x7c00u) v &= 0xffff0000u;
+    if ((v & 0x7c000000u) == 0x7c000000u) v &= 0xffffu;
+    return v;
+}
+// Bit d: dim d of a row's group gr is not finite. (Rows like that are rare: a loop, of few registers.)
+template <int BITS, int HD>
+__device__ __forceinline__ uint32_t kvq_not_finite_dims(const uint8_t *codes, uint32_t par, int gr) {
+    uint32_t dims = 0;
+#pragma unroll 1
+    for (int d = 0; d < 32; d++) {
+        const __half v = kvq_value<BITS, HD>(codes, par, gr, d);
+        if ((__half_as_ushort(v) & 0x7c00u) == 0x7c00u) dims |= 1u << d;
+    }
+    return dims;
+}
+// The values of a row's group gr that are not finite become finite ones: by code 0 where lo and step are
+// finite, otherwise (all of them are not) by the parameters that are returned.
+template <int BITS, int HD>
+__device__ __forceinline__ uint32_t kvq_make_finite(uint8_t *codes, uint32_t par, int gr) {
+    if ((par & 0x7c00u) == 0x7c00u || (par & 0x7c000000u) == 0x7c000000u) return 0;
+    const uint32_t dims = kvq_not_finite_dims<BITS, HD>(codes, par, gr);
+#pragma unroll 1
+    for (int d = 0; d < 32; d++) {
+        const int el = ((d >> 2) * (HD / 32) + gr) * 4 + (d & 3);
+        if (!(dims >> d & 1)) continue;
+        if (BITS == 8)
+            codes[el] = 0;
+        else
+            codes[el >> 1] &= el & 1 ? 0x0f : 0xf0;
+    }
+    return par;
 }
 
 // Constants of the unpacking, held in registers: an instruction takes one immediate

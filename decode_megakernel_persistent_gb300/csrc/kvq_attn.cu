@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
 
     int stage = 0;
     uint32_t phase = 0;  // the parity that the ring's stages complete next
-    bool lost = false;
+    bool lost = false, bad_seen = false;
     for (int ti = t0 + warp; ti < t1; ti += NW) {
         __syncwarp();  // every lane is done with the tile before: its stage is free
         if (lane == 0 && ti + (S::STAGES - 1) * NW < t1) {
@@ -228,14 +228,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
         }
 
         // A tile in which some row's last position lies (or the sequence ends). Its keys
-        // past the end become zeros. V rows holding a NaN there must reach only the rows
-        // that see them: they enter the product as zeros, and the rows that see them
-        // get NaN below.
+        // past the end become zeros. V values there that are not finite must reach only the
+        // rows that see them: others enter the product in their place, and the rows that
+        // see them get NaN behind the walk.
         const int k0 = ti * TILE;
         const bool edge = k0 + TILE > edge_from;
-        uint32_t v_nan[GR];
         if (edge) {
             uint32_t *const ks = const_cast<uint32_t *>(kpar), *const vs = const_cast<uint32_t *>(vpar);
+            uint8_t *const vr = const_cast<uint8_t *>(vt) + lane * RB;
             const int valid = limit - k0;
             if (odd_end && valid <= TILE && lane < GR) {
                 ks[(valid - 1) * GR + lane] = a.kp[(row0 + limit - 1) * GR + lane];
@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
             __syncwarp();
 #pragma unroll
             for (int gr = 0; gr < GR; gr++) {
-                const bool nan = lane < TILE && lane < valid && kvq_is_nan(vs[lane * GR + gr]);
-                v_nan[gr] = __ballot_sync(0xffffffffu, nan);
-                if (lane < TILE && lane >= valid) ks[lane * GR + gr] = 0u;
-                if (nan || (lane < TILE && lane >= valid)) vs[lane * GR + gr] = 0u;
+                const bool bad = lane < TILE && lane < valid && kvq_not_finite<BITS>(vs[lane * GR + gr]);
+                bad_seen |= __any_sync(0xffffffffu, bad);
+                if (lane < TILE && lane >= valid) ks[lane * GR + gr] = vs[lane * GR + gr] = 0u;
+                if (bad) vs[lane * GR + gr] = kvq_make_finite<BITS, HD>(vr, vs[lane * GR + gr], gr);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the stage is copied into again)
             __syncwarp();
@@ -418,21 +418,28 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                 }
             }
         }
-        if (edge) {
+    }
+    if (bad_seen) {  // NaN in the rows that see them (once, behind the walk: in it, 32 sequences of 32768 took 282 us for 272)
+#pragma unroll 1
+        for (int ti = t0 + warp; ti < t1; ti += NW) {
+            if ((ti + 1) * TILE <= edge_from) continue;
+            const int k0 = ti * TILE, k_mine = k0 + lane;
 #pragma unroll
-            for (int gr = 0; gr < GR; gr++)
-                if (v_nan[gr]) {  // (the first such key of the tile decides: later ones are seen by fewer rows)
-                    const int k = k0 + __ffs(v_nan[gr]) - 1;
+            for (int gr = 0; gr < GR; gr++) {
+                const bool bad = lane < TILE && k_mine < limit && kvq_not_finite<BITS>(a.vp[(row0 + k_mine) * GR + gr]);
+#pragma unroll 1
+                for (uint32_t keys = __ballot_sync(0xffffffffu, bad); keys; keys &= keys - 1) {
+                    const int k = k0 + __ffs(keys) - 1;
+                    const uint32_t dims = kvq_not_finite_dims<BITS, HD>(a.vc + (row0 + k) * RB, a.vp[(row0 + k) * GR + gr], gr) >> (4 * g);
 #pragma unroll
                     for (int nc = 0; nc < NC; nc++)
 #pragma unroll
                         for (int b = 0; b < 2; b++)
-                            if (k <= last[nc][b]) {
 #pragma unroll
-                                for (int i = 2 * gr; i < 2 * gr + 2; i++)
-                                    o[nc][i][b] = o[nc][i][2 + b] = __uint_as_float(0x7fffffffu);
-                            }
+                            for (int i = 0; i < 4; i++)  // dim 32 gr + 4 g + i
+                                if (k <= last[nc][b] && (dims >> i & 1)) o[nc][2 * gr + (i >> 1)][2 * (i & 1) + b] = __uint_as_float(0x7fffffffu);
                 }
+            }
         }
     }
     if (lost) {  // a copy that never came: the rows have no result
@@ -562,7 +569,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *const ks = smem, *const vs = smem + CK_KEYS * HD * 2;  // [key][HD] fp16, chunk c of row r at c ^ (r & 7)
     __shared__ float s_ml[CK_ROWS][2];
-    __shared__ uint32_t s_nan[GR][2];  // keys of the tile whose V holds a NaN, per group
+    __shared__ uint32_t s_bad[GR][2];  // keys of the tile whose V may not be finite, per group
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, rank = blockIdx.x % C;
@@ -644,23 +651,20 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
         const int k0 = ti * CK_KEYS;
         const bool edge = k0 + CK_KEYS > min(first_last + 1, limit);
         __syncthreads();  // every warp is done with the tile before
-        if (edge && threadIdx.x < 2 * GR) s_nan[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+        if (edge && threadIdx.x < 2 * GR) s_bad[threadIdx.x >> 1][threadIdx.x & 1] = 0;
         if (edge) __syncthreads();
 #pragma unroll
         for (int i = 0; i < PER; i++) {
             const int at = threadIdx.x + i * CK_THREADS, r = at / CH, c = at % CH;
 #pragma unroll
             for (int kv = 0; kv < 2; kv++) {
-                uint32_t p0 = par[kv][i][0], p1 = par[kv][i][1];
-                if (kv && edge) {  // (see k_kvq_decode: a NaN of V reaches only the rows that see it)
-                    if (kvq_is_nan(p0)) {
-                        atomicOr(&s_nan[2 * (c % GP)][r >> 5], 1u << (r & 31));
-                        p0 = 0;
-                    }
-                    if (kvq_is_nan(p1)) {
-                        atomicOr(&s_nan[2 * (c % GP) + 1][r >> 5], 1u << (r & 31));
-                        p1 = 0;
-                    }
+                const uint32_t p0 = par[kv][i][0], p1 = par[kv][i][1];
+                bool bad = false;
+                if (kv && edge) {  // (see k_kvq_decode: V that is not finite reaches only the rows that see it)
+                    const bool b0 = kvq_not_finite<BITS>(p0), b1 = kvq_not_finite<BITS>(p1);
+                    if (b0) atomicOr(&s_bad[2 * (c % GP)][r >> 5], 1u << (r & 31));
+                    if (b1) atomicOr(&s_bad[2 * (c % GP) + 1][r >> 5], 1u << (r & 31));
+                    bad = b0 || b1;
                 }
                 __half2 v[4];
                 if (BITS == 4)
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
                 u.y = kvq_u32(__hfma2(st, v[1], lo));
                 u.z = kvq_u32(__hfma2(st, v[2], lo));
                 u.w = kvq_u32(__hfma2(st, v[3], lo));
+                if (bad) u = make_uint4(kvq_finite2(u.x), kvq_finite2(u.y), kvq_finite2(u.z), kvq_finite2(u.w));
                 *reinterpret_cast<uint4 *>((kv ? vs : ks) + (r * CH + (c ^ (r & 7))) * 16) = u;
             }
         }
@@ -755,18 +760,18 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
                 mma(o[2 * d + 1], pf, b[2], b[3]);
             }
         }
-        if (edge) {  // element 8 d + 2 t + e of a row belongs to group 2 (d % GP) + e
+        if (edge) {  // element 8 d + 2 t + e of a row is dim 4 (d / GP) + t of group 2 (d % GP) + e
 #pragma unroll
-            for (int gr = 0; gr < GR; gr++) {
-                const uint32_t lo = s_nan[gr][0], hi = s_nan[gr][1];
-                if (!(lo | hi)) continue;
-                const int k = k0 + (lo ? __ffs(lo) - 1 : 31 + __ffs(hi));
+            for (int gr = 0; gr < GR; gr++)
+                for (uint64_t keys = uint64_t(s_bad[gr][1]) << 32 | s_bad[gr][0]; keys; keys &= keys - 1) {
+                    const int k = k0 + __ffsll(keys) - 1;
+                    const uint32_t dims = kvq_not_finite_dims<BITS, HD>(a.vc + (krow + k) * (HD * BITS / 8), a.vp[(krow + k) * GR + gr], gr) >> t;
 #pragma unroll
-                for (int d = gr / 2; d < HD / 8; d += GP)
+                    for (int d = gr / 2; d < HD / 8; d += GP)
 #pragma unroll
-                    for (int b = 0; b < 2; b++)
-                        if (k <= last[b]) o[d][2 * b + (gr & 1)] = __uint_as_float(0x7fffffffu);
-            }
+                        for (int b = 0; b < 2; b++)
+                            if (k <= last[b] && (dims >> (4 * (d / GP)) & 1)) o[d][2 * b + (gr & 1)] = __uint_as_float(0x7fffffffu);
+                }
         }
     }
 #pragma unroll

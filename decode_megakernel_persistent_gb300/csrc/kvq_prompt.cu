@@ -211,6 +211,43 @@ __device__ __forceinline__ uint32_t chunk_at(int rows, int r, int c) {
     return uint32_t((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// Adds to O (tensor memory, a row to a thread of whole warps) what the walk left out of it: the V groups of
+// `groups` of keys k .. last that may not be finite. NaN where a value is not. qs: the row's tile of Q as
+// it is multiplied; scores take fac and m as in the walk. (A function of its own, and its
+// arguments by value: a prompt of 8192 554 us, 558 to 564 as part of the kernel or with the arguments' address.)
+template <int BITS, int HD>
+__device__ __noinline__ void add_left_out(const uint8_t *kc, const uint8_t *vc, const uint32_t *kp, const uint32_t *vp, int64_t row0, int k,
+                                          int last, uint32_t groups, const uint8_t *qs, int row, float fac, float m, uint32_t to) {
+    constexpr int GR = HD / 32, RB = HD * BITS / 8;
+#pragma unroll 1
+    for (int gr = 0; gr < GR; gr++) {
+        uint32_t x[32];
+        tm_load(to + 32 * gr, x);
+        tm_wait(x);
+#pragma unroll 1
+        for (int i = groups >> gr & 1 ? k : last + 1; i <= last; i++) {
+            const uint32_t par = vp[(row0 + i) * GR + gr];
+            if (!kvq_not_finite<BITS>(par)) continue;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int e = 0; e < HD; e++) {
+                const int d = dim_at<HD>(e), kg = d / 32;
+                const __half q = *reinterpret_cast<const __half *>(qs + chunk_at(128, row, e >> 3) + 2 * (e & 7));
+                sum = fmaf(__half2float(q), __half2float(kvq_value<BITS, HD>(kc + (row0 + i) * RB, kp[(row0 + i) * GR + kg], kg, d % 32)), sum);
+            }
+            const float p = ex2(fmaf(sum, fac, -m));
+#pragma unroll
+            for (int d = 0; d < 32; d++) {
+                const float v = __half2float(kvq_value<BITS, HD>(vc + (row0 + i) * RB, par, gr, d));
+                x[d] = __float_as_uint(isfinite(v) ? fmaf(p, v, __uint_as_float(x[d])) : __uint_as_float(0x7fffffffu));
+            }
+        }
+        __syncwarp();
+        tm_store(to + 32 * gr, x);
+    }
+    tm_store_wait();
+}
+
 template <int BITS, int HD, typename QT>
 __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant__ KvqAttnArgs a, int C) {
     using S = Shape<HD>;
@@ -222,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     __shared__ float2 s_ml[256];
-    __shared__ __align__(16) uint8_t s_nan[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V holds a NaN
+    __shared__ __align__(16) uint8_t s_bad[ST][GR][16];  // [stage][group][keys of 8]: keys of the tile whose V may not be finite
     const uint32_t bar0 = sptr(bars);
     // per K/V stage; per S buffer (p_full for the two halves of its keys); per row tile (its products with the first
     // half of a tile's V, and with all of it, are done)
@@ -461,17 +498,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 }
                 if (i >= ST && !wait(v_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
                 uint8_t *const vs = smem + 2 * S::QT + stage * 2 * S::KT + S::KT;
-                if (edge) {  // a NaN of V must reach only the rows that see it: it enters as zero, the rows are told
+                if (edge) {  // V that is not finite must reach only the rows that see it: its group enters as zeros, the rows
+                             // are told (taking out single values here cost a prompt of 8192 1 to 2 %)
 #pragma unroll
                     for (int gr = 0; gr < GR; gr++) {
                         uint32_t bits = 0;
 #pragma unroll
                         for (int j = 0; j < 8; j++)
-                            if (kvq_is_nan(vpar[j][gr])) {
+                            if (kvq_not_finite<BITS>(vpar[j][gr])) {
                                 bits |= 1u << j;
                                 vpar[j][gr] = 0;
                             }
-                        if (g == 0) s_nan[stage][gr][oct] = uint8_t(bits);
+                        if (g == 0) s_bad[stage][gr][oct] = uint8_t(bits);
                     }
                 }
 #pragma unroll
@@ -506,7 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         const uint32_t to = tmem + lanes + S::TM_O + HD * t;
         const int last = r < rows ? min(first + r / a.group, limit - 1) : -1;  // the last key this row sees
         float m = -INFINITY, l = 0.f;
-        uint32_t poison = 0;  // groups of V in which this row sees a NaN
+        uint32_t seen_bad = 0;  // groups of V of which this row sees one that may not be finite
         bool ok = true;
         for (int i = 0; i < mine; i++) {
             const int j = steps.step(t, i), b = j % NB;
@@ -520,14 +558,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             // every tile: a phase that nobody waits for could be taken for the one after next.)
             if (i > 0 && !(ok = wait(o_done + 8 * t, (i - 1) & 1, err))) break;
             if (edge) {
-                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (V is unpacked: what its NaNs are is known)
+                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (V is unpacked: what of it may not be finite is known)
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(s_nan[i % ST][gr]);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(s_bad[i % ST][gr]);
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) poison |= 1u << gr;
+                        if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) seen_bad |= 1u << gr;
                 }
             }
             // The keys in two halves, each with its own look at the maximum: the products with
@@ -607,6 +645,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         }
         if (mine > 0 && ok) ok = wait(o_done + 8 * t, (mine - 1) & 1, err);
         fence_after();
+        if (__any_sync(0xffffffffu, seen_bad))  // (keys of the tiles that were masked: this block's from edge_from on)
+            add_left_out<BITS, HD>(a.kc, a.vc, a.kp, a.vp, s * a.seq_rows + int64_t(h) * a.max_seq, max(tile0, edge_from / KEYS) * KEYS,
+                                   min(last, (tile0 + mine) * KEYS - 1), seen_bad, smem + t * S::QT, threadIdx.x & 127, fac, m, to);
         // (every lane takes part in the loads; a tile without keys has no O)
         const float inv = C > 1 ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
         const int j = r / a.group, head = h * a.group + r % a.group;
@@ -625,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 tm_load(to + 32 * q, x);
                 tm_wait(x);
             }
-            const float f = !ok || (poison >> q & 1) ? __uint_as_float(0x7fffffffu) : inv;
+            const float f = ok ? inv : __uint_as_float(0x7fffffffu);
             if (C > 1) {
 #pragma unroll
                 for (int e = 0; e < 8; e++)

@@ -379,6 +379,8 @@ int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *
  * more slowly. Products run on tensor cores in fp16 (q scaled by a power of two
  * per row, the probabilities rounded to fp16, those below 2^-32 of a row's largest
  * to 0) with fp32 sums; the softmax is fp32.
+ * A K row holding a NaN or an infinity concerns only the tokens that see it, a V
+ * value that is not finite only their outputs in its dim (infinite or NaN there).
  * The same call on the same data repeats bit for bit. */
 int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_heads, int32_t n_tok,
                      const int32_t *len_dev, const int32_t *n_tok_dev, int32_t max_len, float scale,

@@ -71,3 +71,48 @@ def test_many_small_weights_behind_a_dominant_key(T, group, L, cap, hd, x):
     tol = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** (x - 32) + 2.0 ** -18
     off = (out - want).abs() / want
     assert float(off.max()) <= tol, float(off.max())
+
+
+@pytest.mark.parametrize("T,group,cap", [(1, 4, 333), (4, 4, 333), (5, 1, 333), (24, 4, 333), (200, 2, 333), (24, 4, 60000),
+                                         (200, 2, 60000), (200, 4, 20000), (300, 4, 9000)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("lo,step", [(float("inf"), 0.5), (-1.0, float("inf")), (float("-inf"), 0.0), (60000.0, None), (-60000.0, None)])
+def test_infinite_values_reach_only_rows_that_see_them(T, group, cap, hd, bits, lo, step):
+    """V groups of the caller's own whose parameters are infinite, or whose larger codes pass fp16's range
+    (step None: from about the middle code on): such a value makes its dim infinite or NaN where it
+    is seen. Its group's finite values count as any others, and rows that do not see it are as before."""
+    KV, M = 1, 333
+    lens = [M]
+    c, kv, vv = make_cache(12, 1, KV, M, hd, bits, lens, cap)
+    q = torch.randn(1, T, group, hd, generator=gen(6), device="cuda").bfloat16()
+    base = c.attention(q, i32(lens))
+    if step is None:
+        step = (1 if lo > 0 else -1) * 11000.0 / 2 ** bits
+    gr = hd // 32 - 1
+    codes = c.v_codes[0, 0].long() if bits == 8 else torch.stack([c.v_codes[0, 0] & 15, c.v_codes[0, 0] >> 4], -1).flatten(-2).long()
+    codes = codes[:, kvq_ref.place(hd).cuda()].unflatten(-1, (hd // 32, 32))[:, gr]  # [positions, 32]
+    # one seen by the later half of the tokens, two by the last alone
+    places = [M - (T + 1) // 2, M - 1] if T > 1 else [M - 1]
+    bad = torch.zeros(M, 32, dtype=torch.bool, device="cuda")
+    vv = vv.clone()
+    for at in places:
+        c.v_params[0, 0, at, gr, 0], c.v_params[0, 0, at, gr, 1] = lo, step
+        p = c.v_params[0, 0, at, gr].cpu()
+        val = kvq_ref.values(p[None, 0], p[None, 1], codes[at].cpu()[None])  # (numpy's infinities past fp16's range)
+        bad[at] = ~torch.isfinite(val).cuda()
+        vv[0, 0, at, 32 * gr:32 * gr + 32] = torch.where(bad[at], torch.zeros_like(bad[at], dtype=torch.float64), val.cuda())
+    assert bool(bad[places[-1]].any()) and (lo in (60000.0, -60000.0)) == (not bool(bad[places[-1]].all()))
+    out = c.attention(q, i32(lens))
+    last = M - T + torch.arange(T, device="cuda")
+    blind = last < min(places)
+    assert torch.equal(out[0, blind], base[0, blind])
+    assert torch.equal(out[0, :, :, :32 * gr], base[0, :, :, :32 * gr])
+    seen = torch.stack([bad[:p + 1].any(0) for p in last.tolist()])  # [tokens, 32]: a value that is not finite is seen
+    got = out[0, :, :, 32 * gr:]
+    assert torch.equal(~torch.isfinite(got.float()), seen[:, None].expand_as(got))
+    # the finite ones: the formula's, with zeros in the places that it leaves out
+    o, tol = kvq_ref.attend(q[0].double().reshape(-1, hd), kv[0, 0], vv[0, 0], last.repeat_interleave(group))
+    o, tol = (x.view(T, group, hd)[..., 32 * gr:] for x in (o, tol))
+    fin = ~seen[:, None].expand_as(got)
+    assert bool(((got.double() - o).abs() <= tol)[fin].all())
