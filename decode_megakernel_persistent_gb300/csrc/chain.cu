@@ -347,7 +347,7 @@ int launch_chain_step(const KParams &p, const ChainBufs &b, void *stream_) {
             o.f32 = b.o;
             o.head = p.hd;
             int rc = launch_kvq_write(c, k, v, LL_F32, lens, st);
-            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, p.pos + 1, 0.f, o, p.nsm, st);
+            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, p.pos + 1, 0.f, o, {p.timeout_ns, p.status}, p.nsm, st);
             if (rc != LL_OK) return rc;
         } else {
             k_attn_partial<<<dim3(p.nkv, b.splits), 256, 0, st>>>(b.qkv, p.k_cache, p.v_cache, lb, p.pos,

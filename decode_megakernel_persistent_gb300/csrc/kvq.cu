@@ -547,7 +547,7 @@ int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_he
     o.seq = out->seq;
     o.token = out->token;
     o.head = out->head;
-    return finish(ll::launch_kvq_attention(*c, *q, LL_BF16, n_q_heads, l, max_len, scale, o, nsm,
+    return finish(ll::launch_kvq_attention(*c, *q, LL_BF16, n_q_heads, l, max_len, scale, o, {}, nsm,
                                            static_cast<cudaStream_t>(stream)),
                   err, err_len);
 }

@@ -32,6 +32,13 @@ struct KvqOut {
     float *f32;  // fp32 rows instead, or null
 };
 
+// How long a kernel waits for a copy or a product of its own, and the handle's status word that
+// records LL_ERR_DEP_TIMEOUT when one has not come by then (null: the rows' NaN are all that tells).
+struct KvqWaits {
+    uint64_t timeout_ns = 1000000000ull;
+    int32_t *status = nullptr;
+};
+
 // f(bits, head_dim) with both as compile-time constants.
 template <int V>
 struct KvqConst {
@@ -51,7 +58,7 @@ int launch_kvq_write(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_r
 int launch_kvq_read(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_rows &v, const KvqLens &l, cudaStream_t st);
 // q: bf16 (type LL_BF16) or fp32 rows. max_len: the longest length the launch is laid out for.
 int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
-                         int max_len, float scale, const KvqOut &out, int nsm, cudaStream_t st);
+                         int max_len, float scale, const KvqOut &out, const KvqWaits &waits, int nsm, cudaStream_t st);
 
 // Sequence s of the cache alone. Its parameters may begin 8 bytes off a 16-byte border (64 dims, an odd row).
 inline ll_kvq_cache kvq_sequence(const ll_kvq_cache &c, int s) {

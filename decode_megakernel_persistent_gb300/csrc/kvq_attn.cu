@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     __shared__ __align__(8) float s_recv[COLS * HD + 32];  // the cluster's sums of this block's share of the outputs, by rank (16 shares, rounded up)
     __shared__ __align__(8) float s_rml[16][COLS][2]; // and the ranks' m and l
     __shared__ uint64_t s_full[NW][S::STAGES];
+    __shared__ int s_lost[NW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const KvqConsts consts;
     const int s = blockIdx.z, h = blockIdx.y, C = gridDim.x, rank = blockIdx.x;
     // q first, while the lengths are on their way: (nc) row 8 nc + g, this lane's dims 32 gr + 8 t .. (Rows of padded
     // tokens may not exist, so with counts of tokens q waits for its sequence's.)
-    const int n = a.l.n(s), rows = n * a.group;  // query rows
+    const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group;  // rows: of queries
     if (n == 0) return;
     float qv[NC][GR][8];
 #pragma unroll
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                 for (int i = 0; i < 8; i++) qv[nc][gr][i] = 0.f;
         }
     }
-    const int len = a.l.len(s), first = len - n;    // (first: the first token's position)
+    const int first = len - n;                      // the first token's position
     const int limit = min(len, a.max_seq);          // no token sees a position from here on
     const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before the first remote store)
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < S::STAGES; i++) bar_init(full + 8 * i, 1);
+        s_lost[warp] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < S::STAGES - 1; i++)
@@ -205,21 +207,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
 
     int stage = 0;
     uint32_t phase = 0;  // the parity that the ring's stages complete next
-    bool lost = false, bad_seen = false;
+    int load_end = t1;
+    bool bad_seen = false;
     for (int ti = t0 + warp; ti < t1; ti += NW) {
         __syncwarp();  // every lane is done with the tile before: its stage is free
-        if (lane == 0 && ti + (S::STAGES - 1) * NW < t1) {
+        if (lane == 0 && ti + (S::STAGES - 1) * NW < load_end) {
             const int to = stage == 0 ? S::STAGES - 1 : stage - 1;
             load(ti + (S::STAGES - 1) * NW, ring0 + to * S::STAGE, full + 8 * to);
         }
-        if (!bar_wait(full + 8 * stage, phase)) {  // (then the other copies in flight are waited for as long)
-            for (int i = 1; i < S::STAGES && ti + i * NW < t1; i++) {
-                const int at = stage + i;
-                bar_wait(full + 8 * (at % S::STAGES), at < S::STAGES ? phase : phase ^ 1);
-            }
-            lost = true;
-            break;
-        }
+        if (!bar_try(full + 8 * stage, phase) && !copy_wait(full + 8 * stage, phase, a.waits.timeout_ns, &s_lost[warp]))
+            load_end = min(load_end, ti + (S::STAGES - 1) * NW + 1);  // (no more copies are made)
         const uint8_t *kt = ring + stage * S::STAGE, *vt = kt + TILE * RB;
         const uint32_t *kpar = reinterpret_cast<const uint32_t *>(vt + TILE * RB) + skew * GR, *vpar = kpar + PAR / 4;
         if (++stage == S::STAGES) {
@@ -442,7 +439,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
             }
         }
     }
-    if (lost) {  // a copy that never came: the rows have no result
+    __syncwarp();
+    if (s_lost[warp]) {  // a copy that did not come in time: the rows have no result, and what is in flight lands first
+        if (lane == 0) {
+            const int end = (load_end - t0 - warp + NW - 1) / NW;  // copies that were made, of this warp's tiles
+            for (int i = max(0, end - S::STAGES); i < end; i++) bar_wait_long(full + 8 * (i % S::STAGES), i / S::STAGES & 1, KVQ_DRAIN_NS);
+            if (a.waits.status) atomicCAS(a.waits.status, 0, LL_ERR_DEP_TIMEOUT);
+        }
 #pragma unroll
         for (int nc = 0; nc < NC; nc++)
 #pragma unroll
@@ -912,7 +915,7 @@ int decode_launch(const ll_kvq_cache &c, const KvqAttnArgs &a, int splits, int d
 }  // namespace
 
 int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, int n_q_heads, const KvqLens &l,
-                         int max_len, float scale, const KvqOut &out, int nsm, cudaStream_t st) {
+                         int max_len, float scale, const KvqOut &out, const KvqWaits &waits, int nsm, cudaStream_t st) {
     KvqAttnArgs a;
     a.kc = c.k_codes;
     a.vc = c.v_codes;
@@ -929,6 +932,7 @@ int launch_kvq_attention(const ll_kvq_cache &c, const ll_kvq_rows &q, int type, 
     a.q_head = q.head;
     a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(float(c.head_dim))) * 1.4426950408889634f;
     a.out = out;
+    a.waits = waits;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LL_ERR_CUDA;
     const int longest = max_len > 0 ? std::min(max_len, c.max_seq) : c.max_seq;

@@ -26,6 +26,7 @@ struct KvqAttnArgs {
     int64_t q_seq, q_tok, q_head;
     float scale_log2;  // scale * log2(e): scores in log2 units, probabilities by exp2
     KvqOut out;
+    KvqWaits waits;
 };
 
 // A row's reference m is its running maximum less KVQ_ROOM (log2 units), and moves only once
@@ -60,20 +61,26 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-// Waits for a phase for at most a second: false when it has not come by then.
-static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
+// Waits for a phase for at most timeout_ns: false when it has not come by then.
+static __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     do {
         for (int i = 0; i < 64; i++)
             if (bar_try(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (t - t0 < 1000000000ull);
+    } while (t - t0 < timeout_ns);
     return false;
 }
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    return bar_try(bar, parity) || bar_wait_long(bar, parity);
+// The same for a warp's copies, with what a lane found in *lost: false when this or an earlier one has not come. Each lane looks
+// at its own clock, so a limit may pass for some lanes alone; the warp goes on whole all the same, with what the memory
+// holds and without further waits (its rows become NaN).
+static __device__ __noinline__ bool copy_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns, volatile int *lost) {
+    if (!*lost && bar_wait_long(bar, parity, timeout_ns)) return true;
+    *lost = 1;
+    return false;
 }
+constexpr uint64_t KVQ_DRAIN_NS = 1000000000ull;  // what is in flight when a wait has run out is given this long to land
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -114,20 +114,22 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// Bounded wait: false, with *err set for the other warps, once a second passes.
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *err) {
+// Bounded wait: once the limit passes, with *err and the status word set, or once another's has, the block goes on without
+// waits to its end, as if all had come: its loops and whole-warp instructions stay together, and its rows become NaN.
+__device__ __forceinline__ void wait_long(uint32_t bar, uint32_t parity, volatile int *err, const KvqWaits &w) {
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     do {
+        if (*err) return;
         for (int i = 0; i < 64; i++)
-            if (bar_try(bar, parity)) return true;
+            if (bar_try(bar, parity)) return;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (!*err && t - t0 < 1000000000ull);
+    } while (t - t0 < w.timeout_ns);
     *err = 1;
-    return false;
+    if (w.status) atomicCAS(w.status, 0, LL_ERR_DEP_TIMEOUT);
 }
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int *err) {
-    return bar_try(bar, parity) || wait_long(bar, parity, err);
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *err, const KvqWaits &w) {
+    if (!bar_try(bar, parity)) wait_long(bar, parity, err, w);
 }
 
 // 32 columns of this thread's tensor-memory lane; the values are there after tm_wait.
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     extern __shared__ uint8_t raw[];
     uint8_t *const smem = raw + ((1024u - (sptr(raw) & 1023u)) & 1023u);
     constexpr int ST = S::ST, NB = S::NB;
-    __shared__ uint64_t bars[4 * ST + 4 * NB + 4];
+    __shared__ uint64_t bars[4 * ST + 4 * NB + 6];
     __shared__ uint32_t s_tmem;
     __shared__ int s_err;
     __shared__ float2 s_ml[256];
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
     // per K/V stage; per S buffer (p_full for the two halves of its keys); per row tile (its products with the first
     // half of a tile's V, and with all of it, are done)
     const uint32_t k_full = bar0, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
-                   s_full = v_empty + 8 * ST, p_full = s_full + 8 * NB, s_free = p_full + 16 * NB, o_half = s_free + 8 * NB, o_done = o_half + 16;
+                   s_full = v_empty + 8 * ST, p_full = s_full + 8 * NB, s_free = p_full + 16 * NB, o_half = s_free + 8 * NB, o_done = o_half + 16, drained = o_done + 16;
     volatile int *const err = &s_err;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (row tiles slowest, last ones first: the blocks with the most keys of every head start first)
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             bar_init(p_full + 16 * i + 8, 4);
             bar_init(s_free + 8 * i, 1);
         }
-        for (int i = 0; i < 4; i++) bar_init(o_half + 8 * i, 1);
+        for (int i = 0; i < 6; i++) bar_init(o_half + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_err = 0;
     }
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             const int i = steps.tile(j), b = j % NB;
             const uint32_t q = q_at0 + steps.row(j) * S::QT, k = kv0 + (i % ST) * 2 * S::KT;
             if (i >= kready) {
-                if (!wait(k_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
+                wait(k_full + 8 * (i % ST), (i / ST) & 1, err, a.waits);
                 kready = i + 1;
                 fence_after();
             }
@@ -365,18 +367,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                        desc_sw128(k + (d >> 2) * KEYS * 128) + 2 * (d & 3), id_s, d != 0);
             commit(s_full + 8 * b);
             if (last(j, i)) commit(k_empty + 8 * (i % ST));
-            return true;
         };
         auto values = [&](int j) {  // O += P V of step j, in two halves of the keys
             const int i = steps.tile(j), t = steps.row(j), b = j % NB;
             const uint32_t v = kv0 + (i % ST) * 2 * S::KT + S::KT;
             if (i >= vready) {
-                if (!wait(v_full + 8 * (i % ST), (i / ST) & 1, err)) return false;
+                wait(v_full + 8 * (i % ST), (i / ST) & 1, err, a.waits);
                 vready = i + 1;
             }
 #pragma unroll
             for (int f = 0; f < 2; f++) {
-                if (!wait(p_full + 16 * b + 8 * f, (j / NB) & 1, err)) return false;
+                wait(p_full + 16 * b + 8 * f, (j / NB) & 1, err, a.waits);
                 fence_after();
 #pragma unroll
                 for (int k = 4 * f; k < 4 * f + 4; k++)
@@ -385,26 +386,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 commit((f ? o_done : o_half) + 8 * t);
             }
             if (last(j, i)) commit(v_empty + 8 * (i % ST));
-            return true;
         };
         if (S::ONE_WARP) {
-            bool ok = true;
-            for (int j = 0; j < min(NB, count) && ok; j++) ok = scores(j);
-            for (int j = 0; j < count && ok; j++) {
-                ok = values(j);
-                if (ok && j + NB < count) ok = scores(j + NB);
+            for (int j = 0; j < min(NB, count); j++) scores(j);
+            for (int j = 0; j < count; j++) {
+                values(j);
+                if (j + NB < count) scores(j + NB);
             }
         } else if (warp == W_MMA) {
             for (int j = 0; j < count; j++) {
                 if (j >= NB) {
-                    if (!wait(s_free + 8 * (j % NB), (j / NB - 1) & 1, err)) break;
+                    wait(s_free + 8 * (j % NB), (j / NB - 1) & 1, err, a.waits);
                     fence_after();
                 }
-                if (!scores(j)) break;
+                scores(j);
             }
         } else {
             for (int j = 0; j < count; j++) {
-                if (!values(j)) break;
+                values(j);
                 commit(s_free + 8 * (j % NB));
             }
         }
@@ -451,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
             for (int i = 0; i < tiles; i++) {
                 const int stage = i % ST;
                 load(tile0 + i);
-                if (i >= ST && !wait(k_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
+                if (i >= ST) wait(k_empty + 8 * stage, (i / ST - 1) & 1, err, a.waits);
                 uint8_t *const ks = smem + 2 * S::QT + stage * 2 * S::KT;
 #pragma unroll
                 for (int gp = 0; gp < GP; gp++) {
@@ -496,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                         zero(vpar[j]);
                     }
                 }
-                if (i >= ST && !wait(v_empty + 8 * stage, (i / ST - 1) & 1, err)) break;
+                if (i >= ST) wait(v_empty + 8 * stage, (i / ST - 1) & 1, err, a.waits);
                 uint8_t *const vs = smem + 2 * S::QT + stage * 2 * S::KT + S::KT;
                 if (edge) {  // V that is not finite must reach only the rows that see it: its group enters as zeros, the rows
                              // are told (taking out single values here cost a prompt of 8192 1 to 2 %)
@@ -545,20 +544,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         const int last = r < rows ? min(first + r / a.group, limit - 1) : -1;  // the last key this row sees
         float m = -INFINITY, l = 0.f;
         uint32_t seen_bad = 0;  // groups of V of which this row sees one that may not be finite
-        bool ok = true;
         for (int i = 0; i < mine; i++) {
             const int j = steps.step(t, i), b = j % NB;
             const uint32_t ts = tmem + lanes + 128 * b;
-            if (!(ok = wait(s_full + 8 * b, (j / NB) & 1, err))) break;
+            wait(s_full + 8 * b, (j / NB) & 1, err, a.waits);
             fence_after();
             const int k0 = (tile0 + i) * KEYS;
             const bool edge = k0 + KEYS > edge_from;
             const int valid = last - k0 + 1;  // keys of the tile that this row sees
             // O is this thread's once the products of its tile before are done. (Waited for at
             // every tile: a phase that nobody waits for could be taken for the one after next.)
-            if (i > 0 && !(ok = wait(o_done + 8 * t, (i - 1) & 1, err))) break;
+            if (i > 0) wait(o_done + 8 * t, (i - 1) & 1, err, a.waits);
             if (edge) {
-                wait(v_full + 8 * (i % ST), (i / ST) & 1, err);  // (V is unpacked: what of it may not be finite is known)
+                wait(v_full + 8 * (i % ST), (i / ST) & 1, err, a.waits);  // (V is unpacked: what of it may not be finite is known)
 #pragma unroll
                 for (int gr = 0; gr < GR; gr++) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(s_bad[i % ST][gr]);
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                     m = to_m;
                     both(m == -INFINITY ? 0.f : m);
                     l *= al;
-                    if (f && !(ok = wait(o_half + 8 * t, i & 1, err))) break;
+                    if (f) wait(o_half + 8 * t, i & 1, err, a.waits);
                     fence_after();
                     if (i + f > 0) {
 #pragma unroll 1
@@ -641,15 +639,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 __syncwarp();
                 if (lane == 0) arrive(p_full + 16 * b + 8 * f);
             }
-            if (!ok) break;
         }
-        if (mine > 0 && ok) ok = wait(o_done + 8 * t, (mine - 1) & 1, err);
+        if (mine > 0) wait(o_done + 8 * t, (mine - 1) & 1, err, a.waits);
         fence_after();
         if (__any_sync(0xffffffffu, seen_bad))  // (keys of the tiles that were masked: this block's from edge_from on)
             add_left_out<BITS, HD>(a.kc, a.vc, a.kp, a.vp, s * a.seq_rows + int64_t(h) * a.max_seq, max(tile0, edge_from / KEYS) * KEYS,
                                    min(last, (tile0 + mine) * KEYS - 1), seen_bad, smem + t * S::QT, threadIdx.x & 127, fac, m, to);
         // (every lane takes part in the loads; a tile without keys has no O)
-        const float inv = C > 1 ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
+        const float inv = *err ? __uint_as_float(0x7fffffffu) : C > 1 ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
         const int j = r / a.group, head = h * a.group + r % a.group;
         float *const part = reinterpret_cast<float *>(smem + 2 * S::QT);  // [256][HD], 16-byte chunk c of row x at c ^ x
         if (C > 1) {
@@ -666,15 +663,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                 tm_load(to + 32 * q, x);
                 tm_wait(x);
             }
-            const float f = ok ? inv : __uint_as_float(0x7fffffffu);
             if (C > 1) {
 #pragma unroll
                 for (int e = 0; e < 8; e++)
                     *reinterpret_cast<float4 *>(part + threadIdx.x * HD + 4 * ((8 * q + e) ^ (threadIdx.x & (HD / 4 - 1)))) =
-                        make_float4(__uint_as_float(x[4 * e]) * f, __uint_as_float(x[4 * e + 1]) * f,
-                                    __uint_as_float(x[4 * e + 2]) * f, __uint_as_float(x[4 * e + 3]) * f);
+                        make_float4(__uint_as_float(x[4 * e]) * inv, __uint_as_float(x[4 * e + 1]) * inv,
+                                    __uint_as_float(x[4 * e + 2]) * inv, __uint_as_float(x[4 * e + 3]) * inv);
             } else if (r < rows) {
-                put_out32(a.out, s, j, head, 32 * q, x, f);
+                put_out32(a.out, s, j, head, 32 * q, x, inv);
             }
         }
         fence_before();
@@ -708,6 +704,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         cluster_sync();
     }
     __syncthreads();
+    if (*err) {  // a wait has run out: products in flight end before their memory goes
+        if (warp == W_MMA || warp == W_MMA + 1) {
+            commit(drained + 8 * (warp - W_MMA));
+            bar_wait_long(drained + 8 * (warp - W_MMA), 0, KVQ_DRAIN_NS);
+        }
+        __syncthreads();
+    }
     if (warp == W_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 

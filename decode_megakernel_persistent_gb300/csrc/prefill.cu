@@ -1096,7 +1096,7 @@ int launch_prefill(const KParams &p, const LayerW *host_layers, PrefillBufs &b, 
             o.token = qd;
             o.head = p.hd;
             rc = launch_kvq_write(c, k, v, LL_F32, lens, st);
-            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, pos0 + n, 0.f, o, p.nsm, st);
+            if (rc == LL_OK) rc = launch_kvq_attention(c, q, LL_F32, p.nq, lens, pos0 + n, 0.f, o, {p.timeout_ns, p.status}, p.nsm, st);
         } else if (rc == LL_OK) {
             rc = launch_attention(p, b, l, pos0, n, to, st);
         }

@@ -381,7 +381,9 @@ int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *
  * to 0) with fp32 sums; the softmax is fp32.
  * A K row holding a NaN or an infinity concerns only the tokens that see it, a V
  * value that is not finite only their outputs in its dim (infinite or NaN there).
- * The same call on the same data repeats bit for bit. */
+ * The same call on the same data repeats bit for bit. Every wait inside (for its own
+ * copies and products) ends after a second; should one run out, the rows concerned
+ * are NaN. */
 int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_heads, int32_t n_tok,
                      const int32_t *len_dev, const int32_t *n_tok_dev, int32_t max_len, float scale,
                      const ll_kvq_rows *out, void *stream, char *err, size_t err_len);
@@ -394,7 +396,8 @@ int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_he
  * ll_prefill work as on any handle: position pos's K and V are written as
  * ll_kvq_write writes them (from fp32 values, after RoPE) and attention reads the
  * packed rows 0..pos as ll_kvq_attention does, with fp32 queries (scaled and rounded
- * to fp16's 11 bits) and fp32 outputs. */
+ * to fp16's 11 bits) and fp32 outputs; its waits end after the handle's limit
+ * (ll_set_timeout_ns) and then record LL_ERR_DEP_TIMEOUT. */
 int ll_init_kvq(const ll_config *cfg, const ll_weights *w, const ll_kvq_cache *cache, void *stream, ll_handle **out);
 
 #ifdef __cplusplus
