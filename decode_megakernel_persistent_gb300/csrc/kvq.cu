@@ -373,7 +373,8 @@ dim3 rw_grid(const ll_kvq_cache &c, const KvqLens &l, bool far) {
     return dim3((rows + per_block - 1) / per_block, far ? 2 * c.n_kv_heads : 2, c.n_seq);
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
+// (The error stays for whoever reports it.)
+int launched() { return cudaPeekAtLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
 
 }  // namespace
 

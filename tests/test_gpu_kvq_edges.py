@@ -116,3 +116,45 @@ def test_infinite_values_reach_only_rows_that_see_them(T, group, cap, hd, bits, 
     o, tol = (x.view(T, group, hd)[..., 32 * gr:] for x in (o, tol))
     fin = ~seen[:, None].expand_as(got)
     assert bool(((got.double() - o).abs() <= tol)[fin].all())
+
+
+def test_a_launch_that_fails_says_why():
+    """A stream whose capture was made invalid (by waiting for it while it captures) takes no launches: each call reports
+    LL_ERR_CUDA with CUDA's reason, and works again once the capture has ended. In a process of its own."""
+    code = """
+import ctypes, torch
+from decode_megakernel_persistent_gb300 import ll
+c = ll.KVQCache.empty(1, 2, 5000, 64, 4)
+x = torch.randn(1, 600, 2, 64, device="cuda").bfloat16()
+qs = [torch.randn(1, t, 16, 64, device="cuda").bfloat16() for t in (1, 12, 600)]
+outs = [torch.empty_like(q) for q in qs]
+back = [torch.empty_like(x) for _ in range(2)]
+lens = torch.tensor([600], dtype=torch.int32, device="cuda")
+calls = [lambda: c.write(x, x, lens), lambda: c.read(back[0], back[1], lens)]
+calls += [lambda q=q, o=o: c.attention(q, lens, out=o) for q, o in zip(qs, outs)]
+torch.cuda.synchronize()
+st = torch.cuda.Stream()
+cu = ctypes.CDLL("libcuda.so.1")
+s, graph = ctypes.c_void_p(st.cuda_stream), ctypes.c_void_p()
+assert cu.cuStreamBeginCapture_v2(s, 2) == 0  # (relaxed: the first calls of the process may look things up)
+assert cu.cuStreamSynchronize(s) != 0
+with torch.cuda.stream(st):
+    for f in calls:
+        try:
+            f()
+        except ll.LLError as e:
+            assert e.code == ll.LL_ERR_CUDA and "captur" in str(e) and "no error" not in str(e), str(e)
+        else:
+            raise AssertionError("launched into an invalid capture")
+cu.cuStreamEndCapture(s, ctypes.byref(graph))
+for f in calls:
+    f()
+torch.cuda.synchronize()
+print("told")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "told" in r.stdout, r.stderr[-2000:]
