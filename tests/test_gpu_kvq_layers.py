@@ -9,6 +9,7 @@ torch = pytest.importorskip("torch")
 
 from decode_megakernel_persistent_gb300 import ll, synth
 from helpers import check_token, compare_logits
+import kvq_ref
 from test_gpu_kvq_model import Reference
 
 pytestmark = pytest.mark.gpu
@@ -75,4 +76,115 @@ def test_layers_an_odd_number_of_rows_apart(shape, max_seq, gap, bits, n):
         check_token(got, want, f"pos {pos}")
         tok = int(np.argmax(want))
     gaps_are_marked(shape, max_seq, gap, flat)
+    dec.close()
+
+
+WIDE = synth.ModelShape("wide-64", 2, 512, 32, 8, 64, 512, 1000, True)
+WIDE_128 = synth.ModelShape("wide-128", 2, 512, 32, 8, 128, 512, 1000, True)
+
+
+class Forward:
+    """Reference's forward pass of many positions at once, over the rows that the cache holds, checked as there."""
+
+    def __init__(self, ref):
+        self.s, self.c, self.w = ref.s, ref.cache, ref.w
+
+    def held(self, which, l, pos0, x):
+        """The rows of layer l up to those of x [n, n_kv, hd] (positions pos0 on), which are right roundings of it."""
+        c, end = self.c, pos0 + x.shape[0]
+        codes, params = (getattr(c, f"{which}_{kind}")[l, :, :end] for kind in ("codes", "params"))
+        el = codes.long() if c.bits == 8 else torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()
+        code = el[..., kvq_ref.place(c.head_dim).cuda()].unflatten(-1, (c.head_dim // 32, 32))
+        val = kvq_ref.values(params[..., 0].cpu(), params[..., 1].cpu(), code.cpu()).cuda()  # [n_kv, end, hd]
+        lo, step = (params[:, pos0:, :, i].double().repeat_interleave(32, -1)[:, :x.shape[0]] for i in (0, 1))
+        x, got = x.transpose(0, 1), val[:, pos0:]
+        # (as Reference.held bounds it; the noise by the position's own largest value)
+        tol = step * (0.5 + 2 ** c.bits * 2.0 ** -11) + (lo.abs() + got.abs()) * 2.0 ** -11 + 2e-3 * x.abs().amax((0, 2), keepdim=True)
+        off = (got - x).abs()
+        assert bool((off <= tol).all()), (which, l, float((off / tol).max()))
+        return val
+
+    def norm(self, x, g):
+        return x / torch.sqrt((x * x).mean(-1, keepdim=True) + self.s.rms_eps) * g
+
+    def rope(self, x, pos0):
+        half = self.s.head_dim // 2
+        pos = pos0 + torch.arange(x.shape[0], dtype=torch.float64, device="cuda")
+        a = pos[:, None, None] * self.s.rope_theta ** (-2.0 * torch.arange(half, dtype=torch.float64, device="cuda") / self.s.head_dim)
+        p, q = x[..., :half], x[..., half:]
+        return torch.cat([p * a.cos() - q * a.sin(), q * a.cos() + p * a.sin()], -1)
+
+    def logits(self, tokens, pos0):
+        """Those of the last of `tokens`, at positions pos0 on, once the handle has run them."""
+        s, w, n = self.s, self.w, len(tokens)
+        x = w["embed"][torch.tensor(tokens, device="cuda")]
+        G = s.n_q_heads // s.n_kv_heads
+        unseen = torch.arange(pos0 + n, device="cuda") > pos0 + torch.arange(n, device="cuda")[:, None]
+        for l in range(s.n_layers):
+            h = self.norm(x, w["attn_norm"][l])
+            q, k, v = ((h @ w[m][l].view(-1, s.hidden).T).view(n, -1, s.head_dim) for m in ("wq", "wk", "wv"))
+            k, v = self.held("k", l, pos0, self.rope(k, pos0)), self.held("v", l, pos0, v)
+            q = self.rope(q, pos0).view(n, s.n_kv_heads, G, s.head_dim).permute(1, 2, 0, 3)  # [n_kv, G, n, hd]
+            p = torch.softmax((q @ k[:, None].transpose(-1, -2) / s.head_dim ** 0.5).masked_fill_(unseen, float("-inf")), -1)
+            x = x + (p @ v[:, None]).permute(2, 0, 1, 3).reshape(n, -1) @ w["wo"][l].view(s.hidden, -1).T
+            h = self.norm(x, w["mlp_norm"][l])
+            g, u = (h @ w[m][l].view(-1, s.hidden).T for m in ("wg", "wu"))
+            x = x + (torch.nn.functional.silu(g) * u) @ w["wd"][l].view(s.hidden, -1).T
+        head = (w["embed"] if s.tied else w["lm_head"]).view(s.vocab, s.hidden)
+        return (head @ self.norm(x[-1], w["final_norm"])).cpu().numpy()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("shape,calls", [(WIDE, (530,)), (WIDE, (200, 600)), (WIDE_128, (400,)), (WIDE_128, (130, 401)), (synth.TINY, (1500,)),
+                                         (synth.TINY, (700, 1301)), (ONE_KV_128, (1101,)), (ONE_KV_128, (300, 1001))],
+                         ids=lambda x: x.name if hasattr(x, "name") else "+".join(map(str, x)))
+def test_prefill_of_prompts(shape, calls, bits):
+    """Prompts long enough for the kernel of 256 query rows to a block (rows x positions x KV heads past 8 million at 64 dims,
+    half as many at 128): blocks on their own (the wide shapes) and clusters that share the keys, fp32 queries, outputs
+    as three bf16 terms, behind a prefix too. What attention gives shows in the next layer's rows, and in the logits."""
+    n = sum(calls)
+    dec, ref, flat = pair(shape, bits, n + 3, gap=1)
+    fwd = Forward(ref)
+    prompt = synth.make_tokens(shape.vocab, n, seed=3)
+    dev = torch.tensor(prompt, dtype=torch.int32, device="cuda")
+    logits, nxt = torch.empty(shape.vocab, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = 0
+    for m in calls:
+        dec.prefill(dev[at:at + m], at, logits, nxt)
+        dec.synchronize()
+        want = fwd.logits(prompt[at:at + m], at)
+        compare_logits(logits.cpu().numpy(), want, f"prefill up to {at + m}")
+        check_token(int(nxt), want, f"prefill up to {at + m}")
+        at += m
+    tok = int(np.argmax(want))
+    for pos in range(n, n + 3):
+        got = dec.step(tok, pos, logits)
+        want = fwd.logits([tok], pos)
+        compare_logits(logits.cpu().numpy(), want, f"pos {pos}")
+        check_token(got, want, f"pos {pos}")
+        tok = int(np.argmax(want))
+    gaps_are_marked(shape, n + 3, 1, flat)
+    dec.close()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("shape", [synth.TINY, ONE_KV_128], ids=lambda s: s.name)
+def test_steps_at_long_contexts(shape, bits):
+    """fp32 queries over rows enough for many splits and large blocks."""
+    n, M = 3000, 20001
+    dec, ref, flat = pair(shape, bits, M, gap=3)
+    fwd = Forward(ref)
+    prompt = synth.make_tokens(shape.vocab, n, seed=4)
+    logits, nxt = torch.empty(shape.vocab, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    dec.prefill(torch.tensor(prompt, dtype=torch.int32, device="cuda"), 0, logits, nxt)
+    dec.synchronize()
+    want = fwd.logits(prompt, 0)
+    tok = int(np.argmax(want))
+    for pos in range(n, n + 4):
+        got = dec.step(tok, pos, logits)
+        want = fwd.logits([tok], pos)
+        compare_logits(logits.cpu().numpy(), want, f"pos {pos}")
+        check_token(got, want, f"pos {pos}")
+        tok = int(np.argmax(want))
+    gaps_are_marked(shape, M, 3, flat)
     dec.close()
