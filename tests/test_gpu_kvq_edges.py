@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from decode_megakernel_persistent_gb300 import ll
+import kvq_keys
 import kvq_ref
 from test_gpu_kvq import check_attention, gen, i32, make_cache
 
@@ -158,3 +159,38 @@ print("told")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
     assert r.returncode == 0 and "told" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("T,group,KV,lens,cap", [
+    (1, 4, 1, [70001], 70001), (1, 4, 8, [32768], 32768), (1, 8, 2, [4099, 32768, 1000], 32768), (1, 1, 1, [333] * 300, 333), (1, 4, 1, [333], 60000),
+    (4, 4, 1, [70001, 4099], 70001), (2, 8, 8, [1000], 32768), (3, 4, 2, [333, 40], 333),
+    (17, 1, 1, [32768], 32768), (32, 4, 1, [4099, 333], 4099), (5, 4, 2, [32768], 32768),
+    (64, 4, 1, [70001], 70001), (300, 4, 1, [32768, 4099], 32768), (600, 2, 2, [4099], 4099), (300, 4, 1, [1000], 9000)])
+def test_every_run_of_keys_counts(T, group, KV, lens, cap, bits, hd):
+    """Keys that all weigh alike, each run of 16 in a dim of its own (as far as the dims go): a tile or a split
+    left out, or counted twice, is far outside of the bound (the CPU tests of the bound show it)."""
+    S, M = len(lens), max(lens)
+    g = torch.Generator()
+    g.manual_seed(T + M)
+    c = ll.KVQCache.empty(S, KV, max(M, cap), hd, bits)
+    k, v = (torch.zeros(S, M, KV, hd) for _ in range(2))
+    for s, n in enumerate(lens):
+        for h in range(KV):
+            k[s, :n, h], v[s, :n, h] = kvq_keys.key_values(n, hd, g)
+    c.write(k.cuda(), v.cuda(), i32(lens), i32(lens))
+    q = torch.randn(S, T, KV * group, hd, generator=gen(2), device="cuda").bfloat16()
+    out = c.attention(q, i32(lens))
+    for s in range(S) if S < 10 else (0, 151, S - 1):
+        last = (lens[s] - T + torch.arange(T, device="cuda")).repeat_interleave(group)
+        for h in range(KV):
+            vals = []
+            for codes, params in ((c.k_codes, c.k_params), (c.v_codes, c.v_params)):
+                codes, params = codes[s, h, :lens[s]], params[s, h, :lens[s]].cpu()
+                el = codes.long() if bits == 8 else torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()
+                code = el[:, kvq_ref.place(hd).cuda()].unflatten(-1, (hd // 32, 32)).cpu()
+                vals.append(kvq_ref.values(params[..., 0], params[..., 1], code).cuda())
+            o, tol = kvq_keys.attend(q[s, :, h * group:(h + 1) * group].double().reshape(-1, hd), vals[0], vals[1], last)
+            off = (out[s, :, h * group:(h + 1) * group].double().reshape(-1, hd) - o).abs()
+            assert bool((off <= tol).all()), (s, h, float((off / tol).max()))
