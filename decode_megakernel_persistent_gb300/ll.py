@@ -377,6 +377,8 @@ def ll_kvq_read(cache: "KVQCache", k_out, v_out, lens, n_toks=None) -> None:
     [n_seq, n_tok, n_kv_heads, head_dim] (bf16)."""
     kr, n_tok = cache._rows(k_out, "k_out", cache.bf16, cache.n_kv_heads, None, True)
     vr, _ = cache._rows(v_out, "v_out", cache.bf16, cache.n_kv_heads, n_tok, True)
+    if kr == vr:
+        raise LLError(LL_ERR_ARG, "k_out and v_out are the same rows")
     _kvq_call(cache.lib.ll_kvq_read, cache, kr, vr, n_tok, cache._lens(lens, "lens"),
               cache._lens(n_toks, "n_toks") if n_toks is not None else None)
 

@@ -356,12 +356,14 @@ typedef struct {
 } ll_kvq_rows;
 
 /* Quantise the tokens' K and V rows ([n_seq][n_tok][n_kv_heads][head_dim] by the
- * strides of k and v; type LL_BF16 or LL_F32) into the cache. */
+ * strides of k and v; type LL_BF16 or LL_F32) into the cache, whose four arrays must
+ * not overlap. */
 int ll_kvq_write(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *v, int32_t type, int32_t n_tok,
                  const int32_t *len_dev, const int32_t *n_tok_dev, void *stream, char *err, size_t err_len);
 
 /* The tokens' rows read back as bf16 (each value rounded to it) into k and v, laid
- * out as ll_kvq_write's inputs, whose strides in use must not be 0. */
+ * out as ll_kvq_write's inputs, whose strides in use must not be 0; k and v must not
+ * overlap. */
 int ll_kvq_read(const ll_kvq_cache *c, const ll_kvq_rows *k, const ll_kvq_rows *v, int32_t n_tok,
                 const int32_t *len_dev, const int32_t *n_tok_dev, void *stream, char *err, size_t err_len);
 
