@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
     // q first, while the lengths are on their way: (nc) row 8 nc + g, this lane's dims 32 gr + 8 t .. (Rows of padded
     // tokens may not exist, so with counts of tokens q waits for its sequence's.)
     const int n = a.l.n(s), len = a.l.len(s), rows = n * a.group;  // rows: of queries
-    if (n == 0) return;
+    if (a.l.n_dev && n == 0) return;
     float qv[NC][GR][8];
 #pragma unroll
     for (int nc = 0; nc < NC; nc++) {
@@ -239,12 +239,21 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                 vs[(valid - 1) * GR + lane] = a.vp[(row0 + limit - 1) * GR + lane];
             }
             __syncwarp();
+            bool bad = false;
+            if (lane < TILE) {
 #pragma unroll
-            for (int gr = 0; gr < GR; gr++) {
-                const bool bad = lane < TILE && lane < valid && kvq_not_finite<BITS>(vs[lane * GR + gr]);
-                bad_seen |= __any_sync(0xffffffffu, bad);
-                if (lane < TILE && lane >= valid) ks[lane * GR + gr] = vs[lane * GR + gr] = 0u;
-                if (bad) vs[lane * GR + gr] = kvq_make_finite<BITS, HD>(vr, vs[lane * GR + gr], gr);
+                for (int gr = 0; gr < GR; gr++) {
+                    if (lane < valid)
+                        bad |= kvq_not_finite<BITS>(vs[lane * GR + gr]);
+                    else
+                        ks[lane * GR + gr] = vs[lane * GR + gr] = 0u;
+                }
+            }
+            if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
+                bad_seen = true;
+#pragma unroll 1
+                for (int gr = 0; gr < GR && bad; gr++)
+                    if (kvq_not_finite<BITS>(vs[lane * GR + gr])) vs[lane * GR + gr] = kvq_make_finite<BITS, HD>(vr, vs[lane * GR + gr], gr);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the stage is copied into again)
             __syncwarp();
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
             }
         }
     }
-    if (bad_seen) {  // NaN in the rows that see them (once, behind the walk: in it, 32 sequences of 32768 took 282 us for 272)
+    if (__builtin_expect(bad_seen, 0)) {  // NaN in the rows that see them (once, behind the walk: in it, 32 sequences of 32768 took 282 us for 271)
 #pragma unroll 1
         for (int ti = t0 + warp; ti < t1; ti += NW) {
             if ((ti + 1) * TILE <= edge_from) continue;
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
         }
     }
     __syncwarp();
-    if (s_lost[warp]) {  // a copy that did not come in time: the rows have no result, and what is in flight lands first
+    if (__builtin_expect(s_lost[warp], 0)) {  // a copy that did not come in time: the rows have no result, and what is in flight lands first
         if (lane == 0) {
             const int end = (load_end - t0 - warp + NW - 1) / NW;  // copies that were made, of this warp's tiles
             for (int i = max(0, end - S::STAGES); i < end; i++) bar_wait_long(full + 8 * (i % S::STAGES), i / S::STAGES & 1, KVQ_DRAIN_NS);
