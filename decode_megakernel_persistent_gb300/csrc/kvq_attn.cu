@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
                 x = fmaxf(x, sc[0][nc][2 + b]);
 #pragma unroll
                 for (int mt = 1; mt < NT; mt++) x = fmaxf(x, fmaxf(sc[mt][nc][b], sc[mt][nc][2 + b]));
-                top[nc][b] = x * fac[nc][b];
-                grow |= top[nc][b] > m[nc][b] + (KVQ_ROOM + KVQ_HOLD);
+                top[nc][b] = __fmul_rn(x, fac[nc][b]);
+                grow |= kvq_passes(top[nc][b], m[nc][b]);
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_kvq_decode(const __g
             for (int mt = 0; mt < NT; mt++)
 #pragma unroll
                 for (int hf = 0; hf < 2; hf++) {
-                    const float p0 = ex2(fmaf(sc[mt][nc][2 * hf], fac[nc][0], -m0));
-                    const float p1 = ex2(fmaf(sc[mt][nc][2 * hf + 1], fac[nc][1], -m1));
+                    const float p0 = ex2(kvq_above(sc[mt][nc][2 * hf], fac[nc][0], m0));
+                    const float p1 = ex2(kvq_above(sc[mt][nc][2 * hf + 1], fac[nc][1], m1));
                     l[nc][0] += p0;
                     l[nc][1] += p1;
                     pf[mt][nc][hf] = movmatrix(pack_h2(p0, p1));
@@ -731,8 +731,8 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
             float x = -INFINITY;
 #pragma unroll
             for (int nb = 0; nb < CK_KEYS / 8; nb++) x = fmaxf(x, fmaxf(sc[nb][2 * b], sc[nb][2 * b + 1]));
-            top[b] = x * fac[b];
-            grow |= top[b] > m[b] + (KVQ_ROOM + KVQ_HOLD);
+            top[b] = __fmul_rn(x, fac[b]);
+            grow |= kvq_passes(top[b], m[b]);
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(CK_THREADS) k_kvq_chunk(const __grid_constant_
         for (int nb = 0; nb < CK_KEYS / 8; nb++) {
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                sc[nb][e] = ex2(fmaf(sc[nb][e], fac[e >> 1], e < 2 ? -m0 : -m1));
+                sc[nb][e] = ex2(kvq_above(sc[nb][e], fac[e >> 1], e < 2 ? m0 : m1));
                 l[e >> 1] += sc[nb][e];
             }
         }

@@ -36,6 +36,13 @@ struct KvqAttnArgs {
 // that uses up: the smallest that is not lost is 2^-32 of the largest or less, where
 // it would be 2^-25 with the maximum itself as the reference.
 constexpr float KVQ_HOLD = 8.f, KVQ_ROOM = 7.f;
+// A score (a product s times its row's factor) above m, rounded before m is taken off, as m was. With one rounding for
+// s * fac - m, scores past 2^25 log2 units stood above the largest of them by their own last place, and their
+// probabilities past fp16's range (one rounding: 32 sequences of 32768 positions 1 % faster, a prompt of 8192 5 %; the
+// prompt kernel takes it and does such rows again).
+__device__ __forceinline__ float kvq_above(float s, float fac, float m) { return __fsub_rn(__fmul_rn(s, fac), m); }
+// Whether a row's largest score (rounded) moves m.
+__device__ __forceinline__ bool kvq_passes(float top, float m) { return __fsub_rn(top, m) > KVQ_ROOM + KVQ_HOLD; }
 
 __device__ __forceinline__ uint32_t sptr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 

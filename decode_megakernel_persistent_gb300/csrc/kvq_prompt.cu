@@ -213,34 +213,54 @@ __device__ __forceinline__ uint32_t chunk_at(int rows, int r, int c) {
     return uint32_t((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Adds to O (tensor memory, a row to a thread of whole warps) what the walk left out of it: the V groups of
-// `groups` of keys k .. last that may not be finite. NaN where a value is not. qs: the row's tile of Q as
-// it is multiplied; scores take fac and m as in the walk. (A function of its own, and its
-// arguments by value: a prompt of 8192 554 us, 558 to 564 as part of the kernel or with the arguments' address.)
+// The product of a row of Q (in shared memory, as it is multiplied) and a K row of the cache.
 template <int BITS, int HD>
-__device__ __noinline__ void add_left_out(const uint8_t *kc, const uint8_t *vc, const uint32_t *kp, const uint32_t *vp, int64_t row0, int k,
-                                          int last, uint32_t groups, const uint8_t *qs, int row, float fac, float m, uint32_t to) {
+__device__ __forceinline__ float product(const uint8_t *qs, int row, const uint8_t *codes, const uint32_t *params) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int e = 0; e < HD; e++) {
+        const int d = dim_at<HD>(e), gr = d / 32;
+        const __half q = *reinterpret_cast<const __half *>(qs + chunk_at(128, row, e >> 3) + 2 * (e & 7));
+        sum = fmaf(__half2float(q), __half2float(kvq_value<BITS, HD>(codes, params[gr], gr, d % 32)), sum);
+    }
+    return sum;
+}
+
+// What the walk could not do, for rows like that are rare: a row to a thread of whole warps, its O in tensor memory (to) and its
+// m and l, over the keys k0 .. last. `flags`: REDO, scores so large that the walk's one rounding may have lost them
+// (kvq_above): all of it again, by the row itself. A group's bit: O lacks those keys from k on whose V in the group may not be
+// finite; they are added, NaN where a value is not. (A function of its own, and its arguments by value: a prompt of 8192 554 us,
+// 558 to 564 as part of the kernel or with the arguments' address.)
+constexpr uint32_t REDO = 0x80000000u;
+template <int BITS, int HD>
+__device__ __noinline__ float2 finish_rows(const uint8_t *kc, const uint8_t *vc, const uint32_t *kp, const uint32_t *vp, int k0, int k, int last,
+                                           uint32_t flags, const uint8_t *qs, int row, float fac, float2 ml, uint32_t to) {
     constexpr int GR = HD / 32, RB = HD * BITS / 8;
+    const bool redo = flags & REDO;
+    if (redo) {
+        ml = make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+        for (int i = k0; i <= last; i++) ml.x = fmaxf(ml.x, __fmul_rn(product<BITS, HD>(qs, row, kc + int64_t(i) * RB, kp + int64_t(i) * GR), fac));
+    }
 #pragma unroll 1
     for (int gr = 0; gr < GR; gr++) {
         uint32_t x[32];
         tm_load(to + 32 * gr, x);
         tm_wait(x);
+        if (redo) {
+            ml.y = 0.f;
+#pragma unroll
+            for (int d = 0; d < 32; d++) x[d] = 0;
+        }
 #pragma unroll 1
-        for (int i = groups >> gr & 1 ? k : last + 1; i <= last; i++) {
-            const uint32_t par = vp[(row0 + i) * GR + gr];
-            if (!kvq_not_finite<BITS>(par)) continue;
-            float sum = 0.f;
-#pragma unroll 1
-            for (int e = 0; e < HD; e++) {
-                const int d = dim_at<HD>(e), kg = d / 32;
-                const __half q = *reinterpret_cast<const __half *>(qs + chunk_at(128, row, e >> 3) + 2 * (e & 7));
-                sum = fmaf(__half2float(q), __half2float(kvq_value<BITS, HD>(kc + (row0 + i) * RB, kp[(row0 + i) * GR + kg], kg, d % 32)), sum);
-            }
-            const float p = ex2(fmaf(sum, fac, -m));
+        for (int i = redo ? k0 : flags >> gr & 1 ? k : last + 1; i <= last; i++) {
+            const uint32_t par = vp[int64_t(i) * GR + gr];
+            if (!redo && !kvq_not_finite<BITS>(par)) continue;
+            const float p = ex2(kvq_above(product<BITS, HD>(qs, row, kc + int64_t(i) * RB, kp + int64_t(i) * GR), fac, ml.x));
+            if (redo) ml.y += p;
 #pragma unroll
             for (int d = 0; d < 32; d++) {
-                const float v = __half2float(kvq_value<BITS, HD>(vc + (row0 + i) * RB, par, gr, d));
+                const float v = __half2float(kvq_value<BITS, HD>(vc + int64_t(i) * RB, par, gr, d));
                 x[d] = __float_as_uint(isfinite(v) ? fmaf(p, v, __uint_as_float(x[d])) : __uint_as_float(0x7fffffffu));
             }
         }
@@ -248,6 +268,7 @@ __device__ __noinline__ void add_left_out(const uint8_t *kc, const uint8_t *vc, 
         tm_store(to + 32 * gr, x);
     }
     tm_store_wait();
+    return ml;
 }
 
 template <int BITS, int HD, typename QT>
@@ -543,7 +564,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         const uint32_t to = tmem + lanes + S::TM_O + HD * t;
         const int last = r < rows ? min(first + r / a.group, limit - 1) : -1;  // the last key this row sees
         float m = -INFINITY, l = 0.f;
-        uint32_t seen_bad = 0;  // groups of V of which this row sees one that may not be finite
+        uint32_t flags = 0;  // groups of V of which this row sees one that may not be finite, and REDO
         for (int i = 0; i < mine; i++) {
             const int j = steps.step(t, i), b = j % NB;
             const uint32_t ts = tmem + lanes + 128 * b;
@@ -563,7 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) seen_bad |= 1u << gr;
+                        if (u[q] && 32 * q + __ffs(u[q]) - 1 < valid) flags |= 1u << gr;
                 }
             }
             // The keys in two halves, each with its own look at the maximum: the products with
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                     float u, v;
                     kvq_split(acc, u, v);
                     sum = u + v;
-                    top = mx * fac;
+                    top = __fmul_rn(mx, fac);
                 };
                 auto both = [&](float m_use) {
                     if (edge)
@@ -612,10 +633,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
                         pass(m_use, KvqConst<0>{});
                 };
                 both(m == -INFINITY ? 0.f : m);
-                const bool grow = top > m + (KVQ_ROOM + KVQ_HOLD);
+                const bool grow = kvq_passes(top, m);
                 if (__any_sync(0xffffffffu, grow)) {
                     const float to_m = grow ? top - KVQ_ROOM : m, al = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - to_m);
                     m = to_m;
+                    if (fabsf(m) > 8388608.f && fabsf(m) < INFINITY) flags |= REDO;  // (up to 2^23 no place is more than 1/2)
                     both(m == -INFINITY ? 0.f : m);
                     l *= al;
                     if (f) wait(o_half + 8 * t, i & 1, err, a.waits);
@@ -642,9 +664,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kvq_prompt(const __grid_constant
         }
         if (mine > 0) wait(o_done + 8 * t, (mine - 1) & 1, err, a.waits);
         fence_after();
-        if (__any_sync(0xffffffffu, seen_bad))  // (keys of the tiles that were masked: this block's from edge_from on)
-            add_left_out<BITS, HD>(a.kc, a.vc, a.kp, a.vp, s * a.seq_rows + int64_t(h) * a.max_seq, max(tile0, edge_from / KEYS) * KEYS,
-                                   min(last, (tile0 + mine) * KEYS - 1), seen_bad, smem + t * S::QT, threadIdx.x & 127, fac, m, to);
+        if (__any_sync(0xffffffffu, flags)) {
+            const int64_t row0 = s * a.seq_rows + int64_t(h) * a.max_seq;
+            const float2 ml = finish_rows<BITS, HD>(a.kc + row0 * RB, a.vc + row0 * RB, a.kp + row0 * GR, a.vp + row0 * GR, tile0 * KEYS,
+                                                    max(tile0, edge_from / KEYS) * KEYS, min(last, (tile0 + mine) * KEYS - 1), flags,
+                                                    smem + t * S::QT, threadIdx.x & 127, fac, make_float2(m, l), to);
+            m = ml.x;
+            l = ml.y;
+        }
         // (every lane takes part in the loads; a tile without keys has no O)
         const float inv = *err ? __uint_as_float(0x7fffffffu) : C > 1 ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
         const int j = r / a.group, head = h * a.group + r % a.group;

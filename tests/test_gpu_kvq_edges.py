@@ -194,3 +194,39 @@ def test_every_run_of_keys_counts(T, group, KV, lens, cap, bits, hd):
             o, tol = kvq_keys.attend(q[s, :, h * group:(h + 1) * group].double().reshape(-1, hd), vals[0], vals[1], last)
             off = (out[s, :, h * group:(h + 1) * group].double().reshape(-1, hd) - o).abs()
             assert bool((off <= tol).all()), (s, h, float((off / tol).max()))
+
+
+@pytest.mark.parametrize("T,group,M,cap", [(1, 4, 333, 333), (1, 1, 3000, 40000), (4, 4, 333, 333), (40, 2, 333, 333), (24, 4, 500, 60000), (300, 4, 2000, 2000),
+                                           (300, 4, 2000, 9000)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("mag", [1e4, 1e6, 3e7, 1e8, 1e9, 1e12, 1e25])
+def test_scores_far_apart(T, group, M, cap, hd, mag):
+    """Queries so large that the largest score wins outright, at any magnitude: what a row gives is its best key's V. The keys
+    are whole numbers that the packed rows hold exactly, and queries small whole numbers times a power of
+    two, so that the scores of a row (before scale) are exact, and the best and the next far apart or equal."""
+    KV = 2
+    g = gen(T + M)
+    k = torch.randint(-7, 9, (1, M, KV, hd), generator=g, device="cuda").float()
+    k[..., ::32], k[..., 1::32] = -7.0, 8.0  # every group's codes 0 and 15, step 1
+    v = torch.randint(0, 16, (1, M, KV, hd), generator=g, device="cuda").float()
+    v[..., ::32], v[..., 1::32] = 0.0, 15.0
+    c = ll.KVQCache.empty(1, KV, max(M, cap), hd, 4)
+    c.write(k, v, i32([M]))
+    q = torch.randint(-3, 4, (1, T, KV * group, hd), generator=g, device="cuda").float()
+    e = int(torch.log2(torch.tensor(mag)))
+    out = c.attention((q * 2.0 ** e).bfloat16(), i32([M]), scale=1.0)
+    for h in range(KV):
+        s = q[0, :, h * group:(h + 1) * group].double() @ k[0, :, h].double().T  # [T, group, M]
+        s.masked_fill_(torch.arange(M, device="cuda") > M - T + torch.arange(T, device="cuda")[:, None, None], float("-inf"))
+        best = (s == s.amax(-1, keepdim=True)).double()  # (the others are 2^13 log2 units and more behind)
+        want = (best @ v[0, :, h].double()) / best.sum(-1, keepdim=True)
+        got = out[0, :, h * group:(h + 1) * group].double()
+        # bf16's rounding, the weights' to fp16 and sums of few of them; and, where several keys are best, their weights against each
+        # other: a score is s * fac - m in fp32, in one rounding or in two of 2^-24 of it each (kvq_above), so that equal
+        # scores of different blocks or tiles may come out u = |score| 2^-23 log2 units apart. Weights that are off by factors of
+        # at most 2^u move a mean by at most 2^u - 1 of the values' spread, and never out of it.
+        vb = torch.where(best[..., None] > 0, v[0, :, h].double(), torch.nan)
+        spread = torch.nan_to_num(vb, nan=-1e9).amax(-2) - torch.nan_to_num(vb, nan=1e9).amin(-2)
+        u = s.amax(-1, keepdim=True).abs() * 2.0 ** e * 1.4427 * 2.0 ** -23
+        tol = want.abs() * (2.0 ** -8 + 2.0 ** -11) + 2.0 ** -20 + spread * (2.0 ** u.clamp(max=1.0) - 1.0)
+        assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / tol).max())
