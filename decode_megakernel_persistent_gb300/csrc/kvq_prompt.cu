@@ -18,9 +18,9 @@
 // What bounds it: at 128 dims the products of a key tile take 2,048 cycles of the
 // tensor cores for the two row tiles, the softmax and unpacking about 1,800 issue
 // slots per scheduler; at 64 dims the products are half of that, and the softmax
-// bounds. A prompt of 8192 with 32 query heads over 8 packed in 4 bits: 537 us at 128
+// bounds. A prompt of 8192 with 32 query heads over 8 packed in 4 bits: 538 us at 128
 // dims (1.02 PFLOP/s of causal products, 54 % of the measured matrix rate; the products
-// alone, without softmax and unpacking, took 420 us), 372 us at 64.
+// alone, without softmax and unpacking, took 420 us), 380 us at 64.
 #include <cooperative_groups.h>
 
 #include "kvq_attn.cuh"
