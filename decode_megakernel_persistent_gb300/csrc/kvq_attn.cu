@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 // share a packed word; of a V fragment, one dim of two keys.
 //
 // What bounds it: where blocks fill the device, the unpacking (8 sequences of 32768, 128 dims in
-// 4 bits: the schedulers issue in 58 % of the cycles, the ALU pipe is busy in 49 %); 32 of
+// 4 bits: the schedulers issue in 58 % of the cycles, the ALU pipe is busy in 48 %); 32 of
 // them take 270 us for 1.34 GB, 73 % of the copy rate. Where few do, each
 // warp's chain of a tile (0.7 us alone) and start and merge (3 to 5 us): one
 // sequence of 32768 positions of 64 dims 12.9 us, of 1024 4.8 us. With two blocks of query
