@@ -1,0 +1,86 @@
+// call.cpp -- the shared parts of the C entries without a handle (call.h).
+#include "call.h"
+
+#include <cstdarg>
+#include <cstdio>
+#include <mutex>
+
+namespace ll {
+
+namespace {
+
+struct Dev {
+    int state = 0;  // 0 unknown, 1 fits, 2 another architecture
+    int nsm = 0, sm = 0;
+};
+constexpr int MAX_DEVICES = 64;
+std::mutex g_dev_mu;
+Dev g_dev[MAX_DEVICES];
+
+}  // namespace
+
+int report(char *err, size_t err_len, int code, const char *fmt, ...) {
+    if (err && err_len) {
+        va_list ap;
+        va_start(ap, fmt);
+        std::vsnprintf(err, err_len, fmt, ap);
+        va_end(ap);
+    }
+    return code;
+}
+
+int check_device(int &nsm, char *err, size_t err_len) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return report(err, err_len, LL_ERR_CUDA, "no CUDA device");
+    if (dev < 0 || dev >= MAX_DEVICES) return report(err, err_len, LL_ERR_DEVICE, "device ordinal %d out of range", dev);
+    std::lock_guard<std::mutex> lock(g_dev_mu);
+    Dev &d = g_dev[dev];
+    if (!d.state) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return report(err, err_len, LL_ERR_CUDA, "cannot query device %d", dev);
+        d.sm = 10 * major + minor;
+        d.state = d.sm == 103 ? 1 : 2;
+    }
+    if (d.state == 2) return report(err, err_len, LL_ERR_DEVICE, "device is sm_%d, this library is built for sm_103a", d.sm);
+    nsm = d.nsm;
+    return LL_OK;
+}
+
+int check_rows(const ll_kvq_rows *r, const char *name, int64_t n_seq, int64_t n_tok, int64_t heads, int size, bool written,
+               char *err, size_t err_len) {
+    if (!r || !r->data) return report(err, err_len, LL_ERR_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(r->data) & 15u) return report(err, err_len, LL_ERR_ARG, "%s is not 16-byte aligned", name);
+    const int64_t stride[3] = {r->seq, r->token, r->head}, extent[3] = {n_seq, n_tok, heads};
+    for (int i = 0; i < 3; i++) {
+        if (extent[i] <= 1) continue;
+        if ((stride[i] * size) % 16) return report(err, err_len, LL_ERR_ARG, "a stride of %s is not a multiple of 16 bytes", name);
+        if (written && stride[i] == 0) return report(err, err_len, LL_ERR_ARG, "%s is written and has a stride of 0", name);
+    }
+    return LL_OK;
+}
+
+int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t width, bool e4m3, bool written, char *err,
+                      size_t err_len) {
+    if (!r || !r->data) return report(err, err_len, LL_ERR_ARG, "%s is NULL", name);
+    if (r->type != LL_BF16 && r->type != LL_F32 && !(e4m3 && r->type == LL_E4M3))
+        return report(err, err_len, LL_ERR_ARG, "%s must be LL_BF16%s", name, e4m3 ? ", LL_F32 or LL_E4M3" : " or LL_F32");
+    const int size = r->type == LL_F32 ? 4 : r->type == LL_BF16 ? 2 : 1;
+    if (reinterpret_cast<uintptr_t>(r->data) % size) return report(err, err_len, LL_ERR_ARG, "%s is not aligned to its type", name);
+    if (written && n > 1 && r->stride < width) return report(err, err_len, LL_ERR_ARG, "%s is written and its rows overlap", name);
+    if (r->type == LL_E4M3) {
+        if (r->group != 0 && r->group != 128) return report(err, err_len, LL_ERR_ARG, "%s must have scales of 128 columns or of a row", name);
+        if (!r->scale || reinterpret_cast<uintptr_t>(r->scale) % 4) return report(err, err_len, LL_ERR_ARG, "%s has no scales, or not aligned ones", name);
+    }
+    return LL_OK;
+}
+
+int finish(int rc, char *err, size_t err_len) {
+    if (rc == LL_OK) return rc;
+    const cudaError_t e = cudaGetLastError();
+    return report(err, err_len, rc, "kernel launch failed: %s", cudaGetErrorString(e));
+}
+
+}  // namespace ll

@@ -1,0 +1,35 @@
+// call.h -- what the C entries without a handle share: reporting a reason, the device's
+// check, the checks of rows (call.cpp).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/ll.h"
+
+namespace ll {
+
+// The code, with a one-line reason in err.
+int report(char *err, size_t err_len, int code, const char *fmt, ...);
+
+// Once per device: is it the one this library is built for, and its SM count.
+int check_device(int &nsm, char *err, size_t err_len);
+
+// Rows of head_dim elements of `size` bytes each over (n_seq, n_tok, heads);
+// written: they are outputs, so no two may share their place by a stride of 0.
+int check_rows(const ll_kvq_rows *r, const char *name, int64_t n_seq, int64_t n_tok, int64_t heads, int size, bool written,
+               char *err, size_t err_len);
+
+// n rows of a matrix operand of `width` columns: pointers, alignment, type (e4m3: whether it may be
+// LL_E4M3), strides (written: rows must not overlap).
+int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t width, bool e4m3, bool written, char *err,
+                      size_t err_len);
+
+// rc, with CUDA's reason where a launch failed.
+int finish(int rc, char *err, size_t err_len);
+
+// (The error stays for whoever reports it.)
+inline int launched() { return cudaPeekAtLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
+
+}  // namespace ll

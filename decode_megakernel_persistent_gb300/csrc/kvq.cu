@@ -6,10 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <cstdarg>
-#include <cstdio>
-#include <mutex>
-
+#include "call.h"
 #include "kvq.cuh"
 #include "kvq.h"
 #include "ll_internal.h"
@@ -373,9 +370,6 @@ dim3 rw_grid(const ll_kvq_cache &c, const KvqLens &l, bool far) {
     return dim3((rows + per_block - 1) / per_block, far ? 2 * c.n_kv_heads : 2, c.n_seq);
 }
 
-// (The error stays for whoever reports it.)
-int launched() { return cudaPeekAtLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
-
 }  // namespace
 
 int launch_kvq_write(const ll_kvq_cache &c, const ll_kvq_rows &k, const ll_kvq_rows &v, int type, const KvqLens &l,
@@ -429,59 +423,10 @@ int kvq_check_cache(const ll_kvq_cache *c, const char *&msg) {
 
 namespace {
 
-int report(char *err, size_t err_len, int code, const char *fmt, ...) {
-    if (err && err_len) {
-        va_list ap;
-        va_start(ap, fmt);
-        std::vsnprintf(err, err_len, fmt, ap);
-        va_end(ap);
-    }
-    return code;
-}
-
-// Once per device: is it the one this library is built for, and its SM count.
-struct Dev {
-    int state = 0;  // 0 unknown, 1 fits, 2 another architecture
-    int nsm = 0, sm = 0;
-};
-constexpr int MAX_DEVICES = 64;
-std::mutex g_dev_mu;
-Dev g_dev[MAX_DEVICES];
-
-int check_device(int &nsm, char *err, size_t err_len) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return report(err, err_len, LL_ERR_CUDA, "no CUDA device");
-    if (dev < 0 || dev >= MAX_DEVICES) return report(err, err_len, LL_ERR_DEVICE, "device ordinal %d out of range", dev);
-    std::lock_guard<std::mutex> lock(g_dev_mu);
-    Dev &d = g_dev[dev];
-    if (!d.state) {
-        int major = 0, minor = 0;
-        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&d.nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return report(err, err_len, LL_ERR_CUDA, "cannot query device %d", dev);
-        d.sm = 10 * major + minor;
-        d.state = d.sm == 103 ? 1 : 2;
-    }
-    if (d.state == 2) return report(err, err_len, LL_ERR_DEVICE, "device is sm_%d, this library is built for sm_103a", d.sm);
-    nsm = d.nsm;
-    return LL_OK;
-}
-
-// Rows of head_dim elements of `size` bytes each over (n_seq, n_tok, heads);
-// written: they are outputs, so no two may share their place by a stride of 0.
-int check_rows(const ll_kvq_rows *r, const char *name, int64_t n_seq, int64_t n_tok, int64_t heads, int size, bool written,
-               char *err, size_t err_len) {
-    if (!r || !r->data) return report(err, err_len, LL_ERR_ARG, "%s is NULL", name);
-    if (reinterpret_cast<uintptr_t>(r->data) & 15u) return report(err, err_len, LL_ERR_ARG, "%s is not 16-byte aligned", name);
-    const int64_t stride[3] = {r->seq, r->token, r->head}, extent[3] = {n_seq, n_tok, heads};
-    for (int i = 0; i < 3; i++) {
-        if (extent[i] <= 1) continue;
-        if ((stride[i] * size) % 16) return report(err, err_len, LL_ERR_ARG, "a stride of %s is not a multiple of 16 bytes", name);
-        if (written && stride[i] == 0) return report(err, err_len, LL_ERR_ARG, "%s is written and has a stride of 0", name);
-    }
-    return LL_OK;
-}
+using ll::check_device;
+using ll::check_rows;
+using ll::finish;
+using ll::report;
 
 int check_call(const ll_kvq_cache *c, int32_t n_tok, const int32_t *len_dev, const int32_t *n_tok_dev, int64_t heads, char *err,
                size_t err_len) {
@@ -494,12 +439,6 @@ int check_call(const ll_kvq_cache *c, int32_t n_tok, const int32_t *len_dev, con
     if ((reinterpret_cast<uintptr_t>(len_dev) & 3u) || (reinterpret_cast<uintptr_t>(n_tok_dev) & 3u))
         return report(err, err_len, LL_ERR_ARG, "len_dev or n_tok_dev is not 4-byte aligned");
     return LL_OK;
-}
-
-int finish(int rc, char *err, size_t err_len) {
-    if (rc == LL_OK) return rc;
-    const cudaError_t e = cudaGetLastError();
-    return report(err, err_len, rc, "kernel launch failed: %s", cudaGetErrorString(e));
 }
 
 }  // namespace

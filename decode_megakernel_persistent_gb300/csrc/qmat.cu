@@ -1,0 +1,288 @@
+// qmat.cu -- matrices in 4 bits: quantising one, reading it back, and the C entries of the
+// 4-bit calls. The format stands in include/ll.h, the products in qmat_mul.cu.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "call.h"
+#include "kvq.h"
+#include "qmat.cuh"
+#include "qmat.h"
+
+namespace ll {
+namespace {
+
+constexpr int RW_THREADS = 256;
+constexpr float BOUND = 60000.f;  // below fp16's largest, as in the packed cache
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 8 values of a row from column k on, those past the matrix as `none`.
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int64_t k, int64_t cols, bool vec, float none, float (&x)[8]) {
+    if (vec && k + 8 <= cols) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(row + k), b = *reinterpret_cast<const float4 *>(row + k + 4);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(row + k);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = k + i < cols ? widen(row[k + i]) : none;
+    }
+}
+
+// Quantise. A lane is row g or g + 8 of a tile and the columns 32 j + 8 t .. + 7 (lane 4 g + t), as the
+// products read a tile: four words, 16 bytes a lane, a half warp's rows in one 512-byte store. A group's range
+// goes over the lane's words of the group and the four lanes of a row.
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w, int64_t stride, bool vec) {
+    const int KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;
+    const int64_t half = (int64_t(blockIdx.x) * RW_THREADS + threadIdx.x) >> 5;  // (a warp's half tile)
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t tile = half >> 1;
+    const int64_t R = tile / KT, K = tile % KT;
+    if (R >= (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS) return;
+    const int in_tile = int(half & 1) * 8 + g;
+    const int64_t r = R * QM_TILE_ROWS + in_tile;
+    const bool held = r < m.rows;
+    float x[4][8];
+    float mn[4], mx[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int64_t k = K * QM_TILE_COLS + 32 * j + 8 * t;
+        if (held) {
+            load8(w + r * stride, k, m.cols, vec, 0.f, x[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) x[j][i] = 0.f;
+        }
+        mn[j] = INFINITY;
+        mx[j] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            // (a NaN stays one: the comparisons are false for it)
+            x[j][i] = x[j][i] > BOUND ? BOUND : x[j][i] < -BOUND ? -BOUND : x[j][i];
+            if (k + i < m.cols) {
+                mn[j] = min_nan(mn[j], x[j][i]);
+                mx[j] = max_nan(mx[j], x[j][i]);
+            }
+        }
+    }
+    constexpr int PER = GROUP / 32;  // words of a group
+    uint32_t words[4];
+#pragma unroll
+    for (int j0 = 0; j0 < 4; j0 += PER) {
+        float lo = mn[j0], hi = mx[j0];
+#pragma unroll
+        for (int j = j0 + 1; j < j0 + PER; j++) {
+            lo = min_nan(lo, mn[j]);
+            hi = max_nan(hi, mx[j]);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) {
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        const int64_t first = K * QM_TILE_COLS + 32 * j0;
+        if (!held || first >= m.cols) lo = hi = 0.f;
+        const __half lo_h = __float2half_rn(lo);
+        const float base = __half2float(lo_h);
+        const __half step_h = __float2half_rn(__fdiv_rn(hi - base, 15.f));
+        const float step = __half2float(step_h);
+#pragma unroll
+        for (int j = j0; j < j0 + PER; j++) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float q = step > 0.f ? rintf(__fdiv_rn(x[j][i] - base, step)) : 0.f;
+                const uint32_t c = uint32_t(fminf(fmaxf(q, 0.f), 15.f));  // (a NaN: 0; its group's lo is NaN)
+                word |= (first + 32 * (j - j0) + 8 * t + i < m.cols ? c : 0u) << (4 * (i / 2 + 4 * (i % 2)));
+            }
+            words[j] = __funnelshift_l(word, word, 3);
+        }
+        if (t == 0) {
+            const int64_t at = ((tile * (4 / PER)) + j0 / PER) * QM_TILE_ROWS + in_tile;
+            reinterpret_cast<__half2 *>(m.params)[at] = __halves2half2(lo_h, step_h);
+        }
+    }
+    reinterpret_cast<uint4 *>(m.codes)[half * 32 + lane] = make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+// Read back, with k_qmat_write's lanes.
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(RW_THREADS) k_qmat_read(ll_qmat m, T *w, int64_t stride, bool vec) {
+    const int KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;
+    const int64_t half = (int64_t(blockIdx.x) * RW_THREADS + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t tile = half >> 1;
+    const int64_t R = tile / KT, K = tile % KT;
+    const int in_tile = int(half & 1) * 8 + g;
+    const int64_t r = R * QM_TILE_ROWS + in_tile;
+    if (r >= m.rows) return;
+    const uint4 c = reinterpret_cast<const uint4 *>(m.codes)[half * 32 + lane];
+    const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+    constexpr int PER = GROUP / 32;
+    float2 p[4 / PER];
+#pragma unroll
+    for (int s = 0; s < 4 / PER; s++)
+        p[s] = __half22float2(reinterpret_cast<const __half2 *>(m.params)[(tile * (4 / PER) + s) * QM_TILE_ROWS + in_tile]);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int64_t k = K * QM_TILE_COLS + 32 * j + 8 * t;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = fmaf(p[j / PER].y, qm_code(words[j], i), p[j / PER].x);
+        T *dst = w + r * stride + k;
+        if (vec && k + 8 <= m.cols) {
+            if constexpr (sizeof(T) == 4) {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                    o[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (k + i < m.cols) {
+                    if constexpr (sizeof(T) == 4) dst[i] = x[i];
+                    else dst[i] = __float2bfloat16_rn(x[i]);
+                }
+        }
+    }
+}
+
+int64_t tiles_of(const ll_qmat &m) {
+    return int64_t((m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS) * ((m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS);
+}
+
+template <typename F>
+void by_group(int group, F &&f) {
+    group == 32 ? f(KvqConst<32>{}) : group == 64 ? f(KvqConst<64>{}) : f(KvqConst<128>{});
+}
+
+bool vec_rows(const void *p, int64_t stride, int size) {
+    return !(reinterpret_cast<uintptr_t>(p) & 15u) && (stride * size) % 16 == 0;
+}
+
+}  // namespace
+
+int launch_qmat_write(const ll_qmat &m, const void *w, int type, int64_t stride, cudaStream_t st) {
+    const unsigned blocks = unsigned((tiles_of(m) * 2 + RW_THREADS / 32 - 1) / (RW_THREADS / 32));
+    by_group(m.group, [&](auto g) {
+        constexpr int G = g.value;
+        if (type == LL_F32)
+            k_qmat_write<float, G><<<blocks, RW_THREADS, 0, st>>>(m, static_cast<const float *>(w), stride, vec_rows(w, stride, 4));
+        else
+            k_qmat_write<__nv_bfloat16, G><<<blocks, RW_THREADS, 0, st>>>(m, static_cast<const __nv_bfloat16 *>(w), stride, vec_rows(w, stride, 2));
+    });
+    return launched();
+}
+
+int launch_qmat_read(const ll_qmat &m, void *w, int type, int64_t stride, cudaStream_t st) {
+    const unsigned blocks = unsigned((tiles_of(m) * 2 + RW_THREADS / 32 - 1) / (RW_THREADS / 32));
+    by_group(m.group, [&](auto g) {
+        constexpr int G = g.value;
+        if (type == LL_F32)
+            k_qmat_read<float, G><<<blocks, RW_THREADS, 0, st>>>(m, static_cast<float *>(w), stride, vec_rows(w, stride, 4));
+        else
+            k_qmat_read<__nv_bfloat16, G><<<blocks, RW_THREADS, 0, st>>>(m, static_cast<__nv_bfloat16 *>(w), stride, vec_rows(w, stride, 2));
+    });
+    return launched();
+}
+
+int qmat_check(const ll_qmat *m, const char *&msg) {
+    auto bad = [&](int code, const char *why) {
+        msg = why;
+        return code;
+    };
+    if (!m) return bad(LL_ERR_ARG, "the 4-bit matrix is NULL");
+    if (m->group != 32 && m->group != 64 && m->group != 128) return bad(LL_ERR_SHAPE, "group must be 32, 64 or 128");
+    if (m->rows < 1 || m->rows > 1 << 24 || m->cols < 1 || m->cols > 1 << 24) return bad(LL_ERR_SHAPE, "rows and cols must be 1 to 2^24");
+    if (tiles_of(*m) > int64_t(1) << 30) return bad(LL_ERR_SHAPE, "a 4-bit matrix has at most 2^30 tiles of 16 by 128");
+    for (const void *p : {static_cast<const void *>(m->codes), static_cast<const void *>(m->params)})
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 15u)) return bad(LL_ERR_ARG, "a 4-bit matrix array is NULL or not 16-byte aligned");
+    return LL_OK;
+}
+
+}  // namespace ll
+
+namespace {
+
+using ll::check_device;
+using ll::finish;
+using ll::report;
+
+int check_matrix(const ll_qmat *m, char *err, size_t err_len) {
+    if (err && err_len) err[0] = '\0';
+    const char *msg = "";
+    if (const int rc = ll::qmat_check(m, msg)) return report(err, err_len, rc, "%s", msg);
+    return LL_OK;
+}
+
+int check_dense(const ll_qmat *m, const void *w, int32_t type, int64_t stride, char *err, size_t err_len) {
+    if (type != LL_BF16 && type != LL_F32) return report(err, err_len, LL_ERR_ARG, "type must be LL_BF16 or LL_F32");
+    if (!w || reinterpret_cast<uintptr_t>(w) % (type == LL_F32 ? 4 : 2)) return report(err, err_len, LL_ERR_ARG, "w is NULL or not aligned to its type");
+    if (m->rows > 1 && stride < m->cols) return report(err, err_len, LL_ERR_ARG, "stride is less than cols");
+    return LL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ll_qmat_write(const ll_qmat *m, const void *w, int32_t type, int64_t stride, void *stream, char *err, size_t err_len) {
+    if (int rc = check_matrix(m, err, err_len)) return rc;
+    if (int rc = check_dense(m, w, type, stride, err, err_len)) return rc;
+    int nsm = 0;
+    if (int rc = check_device(nsm, err, err_len)) return rc;
+    return finish(ll::launch_qmat_write(*m, w, type, stride, static_cast<cudaStream_t>(stream)), err, err_len);
+}
+
+int ll_qmat_read(const ll_qmat *m, void *w, int32_t type, int64_t stride, void *stream, char *err, size_t err_len) {
+    if (int rc = check_matrix(m, err, err_len)) return rc;
+    if (int rc = check_dense(m, w, type, stride, err, err_len)) return rc;
+    int nsm = 0;
+    if (int rc = check_device(nsm, err, err_len)) return rc;
+    return finish(ll::launch_qmat_read(*m, w, type, stride, static_cast<cudaStream_t>(stream)), err, err_len);
+}
+
+int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *add, const ll_rows *y, void *stream, char *err,
+                size_t err_len) {
+    if (int rc = check_matrix(m, err, err_len)) return rc;
+    if (n < 1) return report(err, err_len, LL_ERR_ARG, "n must be at least 1");
+    if (n > 1 << 19) return report(err, err_len, LL_ERR_SHAPE, "n must be at most 2^19");
+    if (int rc = ll::check_matrix_rows(x, "x", n, m->cols, true, false, err, err_len)) return rc;
+    if (int rc = ll::check_matrix_rows(y, "y", n, m->rows, false, true, err, err_len)) return rc;
+    if (add) {
+        if (int rc = ll::check_matrix_rows(add, "add", n, m->rows, false, false, err, err_len)) return rc;
+        if (add->type != y->type) return report(err, err_len, LL_ERR_ARG, "add must be of y's type");
+    }
+    int nsm = 0;
+    if (int rc = check_device(nsm, err, err_len)) return rc;
+    return finish(ll::launch_qmat_mul(*m, *x, n, add, *y, nsm, static_cast<cudaStream_t>(stream)), err, err_len);
+}
+
+}  // extern "C"

@@ -1,0 +1,220 @@
+// rope.cu -- rotary positions of query and key rows (ll_rope in include/ll.h).
+//
+// A pair turns by position * f_i. The table holds f_i / (2 pi) as a 64-bit fraction of a turn, so position *
+// turns modulo 2^64 is the angle's remainder, as exact as f_i itself (53 bits): no angle of a far position
+// is ever rounded, and no 64-bit floating point is needed. Its upper 32 bits, as a signed fraction of half
+// a turn, are sincospi's argument in [-1, 1).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "call.h"
+#include "kvq.h"
+#include "rows.cuh"
+
+namespace ll {
+namespace {
+
+constexpr int ROPE_THREADS = 256;
+
+struct RopeArgs {
+    ll_rope_table t;
+    ll_kvq_rows in[2], out[2];  // q, k
+    int nq, heads;              // query heads, heads in all
+    KvqLens l;
+    int units;                  // of 8 pairs, or (behind them) of 16 values that are copied
+    int pair_units, slots, tokens;  // slots: threads that share a token's unit, by heads; tokens of a block
+    bool vec, inverse;
+};
+
+// A thread has one unit of one token, its 8 angles in registers, and every slots-th head.
+template <typename T>
+__global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a) {
+    const int u = threadIdx.x % a.units, slot = threadIdx.x / a.units % a.slots, in = threadIdx.x / (a.units * a.slots);
+    const int s = blockIdx.y, j = blockIdx.x * a.tokens + in;
+    if (in >= a.tokens) return;
+    const int n = a.l.n(s);
+    const int64_t pos = int64_t(a.l.len(s)) - n + j;
+    if (j >= n || pos < 0) return;
+    const int rot = a.t.rot_dims, half = rot / 2;
+    const bool turned = u < a.pair_units;
+    float c[8], sn[8];
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int p = min(8 * u + i, half - 1);
+            const uint64_t turns = uint64_t(pos) * a.t.turns[p];
+            sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &sn[i], &c[i]);
+            c[i] *= a.t.size;
+            sn[i] *= a.inverse ? -a.t.size : a.t.size;
+        }
+    }
+    for (int h = slot; h < a.heads; h += a.slots) {
+        const int which = h >= a.nq, head = which ? h - a.nq : h;
+        const ll_kvq_rows &from = a.in[which], &to = a.out[which];
+        const T *x = static_cast<const T *>(from.data) + s * from.seq + j * from.token + head * from.head;
+        T *y = static_cast<T *>(to.data) + s * to.seq + j * to.token + head * to.head;
+        if (!turned) {  // values behind the turned ones
+            const int d0 = rot + 16 * (u - a.pair_units), d1 = min(d0 + 16, a.t.head_dim);
+            for (int d = d0; d < d1; d++) y[d] = x[d];
+            continue;
+        }
+        float p[8], q[8], v[8], w[8];
+        if (a.vec && !a.t.interleaved) {
+            load8(x, 8 * u, half, true, p);
+            load8(x + half, 8 * u, half, true, q);
+        } else if (a.vec) {
+            load8(x, 16 * u, rot, true, v);
+            load8(x, 16 * u + 8, rot, true, w);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                p[i] = v[2 * i]; q[i] = v[2 * i + 1];
+                p[4 + i] = w[2 * i]; q[4 + i] = w[2 * i + 1];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int k = min(8 * u + i, half - 1);
+                p[i] = float(x[a.t.interleaved ? 2 * k : k]);
+                q[i] = float(x[a.t.interleaved ? 2 * k + 1 : half + k]);
+            }
+        }
+        float e[8], f[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            e[i] = p[i] * c[i] - q[i] * sn[i];
+            f[i] = q[i] * c[i] + p[i] * sn[i];
+        }
+        if (a.vec && !a.t.interleaved) {
+            store8(y, 8 * u, half, true, e);
+            store8(y + half, 8 * u, half, true, f);
+        } else if (a.vec) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                v[2 * i] = e[i]; v[2 * i + 1] = f[i];
+                w[2 * i] = e[4 + i]; w[2 * i + 1] = f[4 + i];
+            }
+            store8(y, 16 * u, rot, true, v);
+            store8(y, 16 * u + 8, rot, true, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int k = 8 * u + i;
+                if (k < half) {
+                    y[a.t.interleaved ? 2 * k : k] = T(e[i]);
+                    y[a.t.interleaved ? 2 * k + 1 : half + k] = T(f[i]);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows &q_out, int nq, const ll_kvq_rows *k, const ll_kvq_rows *k_out,
+                int nk, int type, int n_seq, const KvqLens &l, bool inverse, cudaStream_t st) {
+    RopeArgs a = {};
+    a.t = t;
+    a.in[0] = q;
+    a.out[0] = q_out;
+    if (k) {
+        a.in[1] = *k;
+        a.out[1] = *k_out;
+    }
+    a.nq = nq;
+    a.heads = nq + (k ? nk : 0);
+    a.l = l;
+    a.pair_units = (t.rot_dims / 2 + 7) / 8;
+    // units of pairs are whole, and their second halves on 16-byte borders
+    a.vec = t.interleaved ? t.rot_dims % 16 == 0 : t.rot_dims / 2 % 8 == 0;
+    const bool same = q.data == q_out.data && (!k || k->data == k_out->data);
+    a.units = a.pair_units + (same ? 0 : (t.head_dim - t.rot_dims + 15) / 16);
+    const int most = ROPE_THREADS / a.units;  // (16 units at most: 256 dims)
+    a.slots = a.heads < most ? a.heads : most;
+    a.tokens = most / a.slots;
+    a.inverse = inverse;
+    const dim3 grid((l.n_tok + a.tokens - 1) / a.tokens, n_seq);
+    type == LL_F32 ? k_rope<float><<<grid, ROPE_THREADS, 0, st>>>(a) : k_rope<__nv_bfloat16><<<grid, ROPE_THREADS, 0, st>>>(a);
+    return launched();
+}
+
+}  // namespace ll
+
+extern "C" {
+
+int ll_rope_plan(ll_rope_table *r, int32_t head_dim, int32_t rot_dims, int32_t interleaved, double theta, int32_t scaling, double factor,
+                 double low, double high, double length, char *err, size_t err_len) {
+    using ll::report;
+    if (err && err_len) err[0] = '\0';
+    if (!r) return report(err, err_len, LL_ERR_ARG, "the table is NULL");
+    if (head_dim < 8 || head_dim > 256 || head_dim % 8) return report(err, err_len, LL_ERR_SHAPE, "head_dim must be a multiple of 8, at most 256");
+    if (rot_dims < 2 || rot_dims > head_dim || rot_dims % 2) return report(err, err_len, LL_ERR_SHAPE, "rot_dims must be even, 2 to head_dim");
+    if (!(theta > 1) || !std::isfinite(theta)) return report(err, err_len, LL_ERR_ARG, "theta must be finite and above 1");
+    if (scaling < LL_ROPE_PLAIN || scaling > LL_ROPE_RAMP) return report(err, err_len, LL_ERR_ARG, "unknown scaling");
+    if (scaling != LL_ROPE_PLAIN && (!(factor >= 1) || !std::isfinite(factor))) return report(err, err_len, LL_ERR_ARG, "factor must be finite and at least 1");
+    if (scaling >= LL_ROPE_BANDS && (!(length >= 1) || !std::isfinite(length) || !(low > 0) || !(high > low) || !std::isfinite(high)))
+        return report(err, err_len, LL_ERR_ARG, "length must be at least 1 and high above low, above 0");
+    const double two_pi = 6.283185307179586476925;
+    *r = {};
+    r->head_dim = head_dim;
+    r->rot_dims = rot_dims;
+    r->interleaved = interleaved ? 1 : 0;
+    r->size = scaling == LL_ROPE_RAMP ? float(0.1 * std::log(factor) + 1) : 1.f;
+    auto pair = [&](double turns) { return rot_dims * std::log(length / (two_pi * turns)) / (2 * std::log(theta)); };
+    double first = 0, last = 0;
+    if (scaling == LL_ROPE_RAMP) {
+        first = std::fmax(std::floor(pair(high)), 0);
+        last = std::fmin(std::ceil(pair(low)), rot_dims - 1);
+    }
+    for (int i = 0; i < rot_dims / 2; i++) {
+        double f = std::pow(theta, -2.0 * i / rot_dims);
+        if (scaling == LL_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == LL_ROPE_BANDS) {
+            const double s = std::fmin(std::fmax((length * f / two_pi - low) / (high - low), 0), 1);
+            f = f * s + f / factor * (1 - s);
+        } else if (scaling == LL_ROPE_RAMP) {
+            const double s = std::fmin(std::fmax((i - first) / (last != first ? last - first : 0.001), 0), 1);
+            f = f * (1 - s) + f / factor * s;
+        }
+        r->turns[i] = uint64_t(std::llrint(std::ldexp(f / two_pi, 64)));  // (below 2^62)
+    }
+    return LL_OK;
+}
+
+int ll_rope(const ll_rope_table *r, const ll_kvq_rows *q, const ll_kvq_rows *q_out, int32_t n_q_heads, const ll_kvq_rows *k,
+            const ll_kvq_rows *k_out, int32_t n_k_heads, int32_t type, int32_t n_seq, int32_t n_tok, const int32_t *len_dev,
+            const int32_t *n_tok_dev, int32_t inverse, void *stream, char *err, size_t err_len) {
+    using ll::check_rows;
+    using ll::report;
+    if (err && err_len) err[0] = '\0';
+    if (!r || r->head_dim < 8 || r->head_dim > 256 || r->head_dim % 8 || r->rot_dims < 2 || r->rot_dims > r->head_dim || r->rot_dims % 2)
+        return report(err, err_len, LL_ERR_ARG, "the table is NULL or was not made by ll_rope_plan");
+    if (type != LL_BF16 && type != LL_F32) return report(err, err_len, LL_ERR_ARG, "type must be LL_BF16 or LL_F32");
+    if (n_seq < 1 || n_seq > 65535) return report(err, err_len, LL_ERR_SHAPE, "n_seq must be 1 to 65535");
+    if (n_tok < 1) return report(err, err_len, LL_ERR_ARG, "n_tok must be at least 1");
+    if (n_q_heads < 1 || n_q_heads > 32767 || (k && (n_k_heads < 1 || n_k_heads > 32767)))
+        return report(err, err_len, LL_ERR_SHAPE, "heads must be 1 to 32767");
+    if (!k != !k_out) return report(err, err_len, LL_ERR_ARG, "k and k_out go together");
+    if (!len_dev) return report(err, err_len, LL_ERR_ARG, "len_dev is NULL");
+    if ((reinterpret_cast<uintptr_t>(len_dev) & 3u) || (reinterpret_cast<uintptr_t>(n_tok_dev) & 3u))
+        return report(err, err_len, LL_ERR_ARG, "len_dev or n_tok_dev is not 4-byte aligned");
+    const int size = type == LL_F32 ? 4 : 2;
+    if (int rc = check_rows(q, "q", n_seq, n_tok, n_q_heads, size, false, err, err_len)) return rc;
+    if (int rc = check_rows(q_out, "q_out", n_seq, n_tok, n_q_heads, size, true, err, err_len)) return rc;
+    if (k) {
+        if (int rc = check_rows(k, "k", n_seq, n_tok, n_k_heads, size, false, err, err_len)) return rc;
+        if (int rc = check_rows(k_out, "k_out", n_seq, n_tok, n_k_heads, size, true, err, err_len)) return rc;
+        if (k_out->data == q_out->data) return report(err, err_len, LL_ERR_ARG, "q_out and k_out are the same rows");
+    }
+    int nsm = 0;
+    if (int rc = ll::check_device(nsm, err, err_len)) return rc;
+    const ll::KvqLens l = {len_dev, n_tok_dev, 0, n_tok};
+    return ll::finish(ll::launch_rope(*r, *q, *q_out, n_q_heads, k, k_out, n_k_heads, type, n_seq, l, inverse != 0, static_cast<cudaStream_t>(stream)),
+                      err, err_len);
+}
+
+}  // extern "C"

@@ -1,0 +1,91 @@
+// rows.cuh -- 8 values of a row loaded to fp32 and stored from it (rmsnorm.cu, rope.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "kvq.h"
+
+namespace ll {
+
+struct e4m3 {
+    uint8_t bits;
+};
+
+int launch_rmsnorm(const ll_rows &x, const ll_rows *res, const ll_rows *res_out, const uint16_t *gain, float eps, int n, int width,
+                   const ll_rows &out, cudaStream_t st);
+int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows &q_out, int nq, const ll_kvq_rows *k, const ll_kvq_rows *k_out,
+                int nk, int type, int n_seq, const KvqLens &l, bool inverse, cudaStream_t st);
+
+#ifdef __CUDACC__
+template <typename T>
+__device__ __forceinline__ float rounded(float x) {
+    return sizeof(T) == 4 ? x : __bfloat162float(__float2bfloat16_rn(x));
+}
+
+// Columns k..k+7 of a row of `width` values, zeros past its end. vec: 16-byte (8-byte for e4m3) accesses are aligned.
+__device__ __forceinline__ void load8(const float *row, int k, int width, bool vec, float (&x)[8]) {
+    if (vec && k + 8 <= width) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + k), b = *reinterpret_cast<const float4 *>(row + k + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = k + i < width ? row[k + i] : 0.f;
+    }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int k, int width, bool vec, float (&x)[8]) {
+    if (vec && k + 8 <= width) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + k);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = k + i < width ? __bfloat162float(row[k + i]) : 0.f;
+    }
+}
+
+__device__ __forceinline__ void store8(float *row, int k, int width, bool vec, const float (&x)[8]) {
+    if (vec && k + 8 <= width) {
+        reinterpret_cast<float4 *>(row + k)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(row + k)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (k + i < width) row[k + i] = x[i];
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int k, int width, bool vec, const float (&x)[8]) {
+    if (vec && k + 8 <= width) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(row + k) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (k + i < width) row[k + i] = __float2bfloat16_rn(x[i]);
+    }
+}
+__device__ __forceinline__ void store8(e4m3 *row, int k, int width, bool vec, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint16_t h;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+        w[i] = h;
+    }
+    if (vec && k + 8 <= width) {
+        *reinterpret_cast<uint2 *>(row + k) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (k + i < width) row[k + i].bits = uint8_t(w[i / 2] >> (8 * (i & 1)));
+    }
+}
+#endif
+
+}  // namespace ll

@@ -41,6 +41,12 @@ LL_MAX_BATCH = 8
 
 LL_BF16 = 0
 LL_F32 = 1
+LL_E4M3 = 2
+
+LL_ROPE_PLAIN = 0
+LL_ROPE_LINEAR = 1
+LL_ROPE_BANDS = 2
+LL_ROPE_RAMP = 3
 
 LL_STATIC_SCRATCH_BYTES = 4194304
 LL_STATIC_MAX_LAYERS = 256
@@ -55,7 +61,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libll.so")
 EXPORTS = ("ll_init", "ll_init_error", "ll_decode_step", "ll_decode_step_async", "ll_decode_steps", "ll_synchronize",
            "ll_set_trace", "ll_set_timeout_ns", "ll_query", "ll_debug_inject", "ll_plan", "ll_last_error",
            "ll_free", "ll_decode_step_static", "ll_init_batch", "ll_decode_steps_batch", "ll_handle_plan",
-           "ll_prefill", "ll_kvq_write", "ll_kvq_read", "ll_kvq_attention", "ll_init_kvq")
+           "ll_prefill", "ll_kvq_write", "ll_kvq_read", "ll_kvq_attention", "ll_init_kvq",
+           "ll_qmat_write", "ll_qmat_read", "ll_qmat_mul", "ll_rmsnorm", "ll_rope_plan", "ll_rope", "ll_verify")
 
 
 class LLError(RuntimeError):
@@ -90,6 +97,21 @@ class ll_kvq_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("seq", "token", "head")]
 
 
+class ll_qmat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("params", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in ("rows", "cols", "group")]
+
+
+class ll_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("type", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale", ctypes.c_void_p)]
+
+
+class ll_rope_table(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "rot_dims", "interleaved")] + [
+        ("size", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+_matrix_rows_bytes = struct.Struct("@PqiiP").pack  # an ll_rows
 _rows_bytes = struct.Struct("@Pqqq").pack  # an ll_kvq_rows, a fifth of the time that the ctypes object takes
 
 
@@ -155,6 +177,21 @@ def lib() -> ctypes.CDLL:
     L.ll_kvq_attention.restype = ctypes.c_int
     L.ll_init_kvq.argtypes = [ctypes.POINTER(ll_config), ctypes.POINTER(ll_weights), cachep, vp, ctypes.POINTER(vp)]
     L.ll_init_kvq.restype = ctypes.c_int
+    L.ll_qmat_write.argtypes = [ctypes.POINTER(ll_qmat), vp, i32, ctypes.c_int64, vp] + err
+    L.ll_qmat_write.restype = ctypes.c_int
+    L.ll_qmat_read.argtypes = [ctypes.POINTER(ll_qmat), vp, i32, ctypes.c_int64, vp] + err
+    L.ll_qmat_read.restype = ctypes.c_int
+    L.ll_qmat_mul.argtypes = [ctypes.POINTER(ll_qmat), vp, i32, vp, vp, vp] + err
+    L.ll_qmat_mul.restype = ctypes.c_int
+    L.ll_rmsnorm.argtypes = [vp, vp, vp, vp, ctypes.c_float, i32, i32, vp, vp] + err
+    L.ll_rmsnorm.restype = ctypes.c_int
+    L.ll_rope_plan.argtypes = [ctypes.POINTER(ll_rope_table), i32, i32, i32, ctypes.c_double, i32] + 4 * [ctypes.c_double] + err
+    L.ll_rope_plan.restype = ctypes.c_int
+    L.ll_rope.argtypes = [ctypes.POINTER(ll_rope_table), vp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, i32, vp] + err
+    L.ll_rope.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    L.ll_verify.argtypes = [vp, i32, i64, i64, vp, vp, vp, i64, i64, vp, vp, i32, i32, i32, vp, vp, vp] + err
+    L.ll_verify.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -401,6 +438,178 @@ def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=No
     o, _ = cache._rows(out, "out", cache.bf16, heads, n_tok, True)
     _kvq_call(cache.lib.ll_kvq_attention, cache, qr, heads, n_tok, lp, np_, max_len, scale, o)
     return out
+
+
+def _device_call(fn, device, *args) -> None:
+    """One call without a handle on torch's current stream of `device`."""
+    import torch
+    index = device.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _device_call(fn, device, *args)
+    err = _kvq_thread.err
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index), err, 256)
+    if rc != LL_OK:
+        raise LLError(rc, err.value.decode())
+
+
+class _Types:
+    """torch's dtypes by the library's, looked up once."""
+    codes = None
+
+    @classmethod
+    def get(cls) -> dict:
+        if cls.codes is None:
+            import torch
+            cls.codes = {torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float8_e4m3fn: LL_E4M3}
+            cls.bf16, cls.f32, cls.e4m3, cls.int32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+        return cls.codes
+
+
+def _matrix_rows(t, name: str, shape, device, written: bool = False, scale=None, group: int = 0):
+    """t [n, width] as an ll_rows' bytes (the library checks types and strides, which it sees)."""
+    if getattr(t, "device", None) != device or device.type != "cuda":
+        raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None and device.type == "cuda" else ""))
+    code = _Types.get().get(t.dtype)
+    if code is None:
+        raise LLError(LL_ERR_ARG, f"{name} must not be {t.dtype}")
+    if t.shape != shape:
+        raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {list(shape)}")
+    stride, last = t.stride()
+    if last != 1 and shape[1] > 1:
+        raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
+    return _matrix_rows_bytes(t.data_ptr(), stride, code, group, 0 if scale is None else scale.data_ptr())
+
+
+def _scales(scale, name: str, n: int, width: int, device):
+    """The group (0: the row) that the scales [n, groups] of e4m3 rows stand for."""
+    if getattr(scale, "device", None) != device or scale.dtype != _Types.f32 or scale.dim() != 2 or not scale.is_contiguous():
+        raise LLError(LL_ERR_ARG, f"{name} must be a contiguous float32 tensor [{n}, groups] on {device}")
+    tiles = (width + 127) // 128
+    if scale.shape not in ((n, 1), (n, tiles)):
+        raise LLError(LL_ERR_ARG, f"{name} is {tuple(scale.shape)}, the call needs [{n}, 1] or [{n}, {tiles}]")
+    return 128 if scale.shape[1] == tiles and tiles > 1 else 0
+
+
+def ll_qmat_write(m: "Q4Matrix", w) -> None:
+    """Quantise w [rows, cols] (bf16 or fp32) into the matrix."""
+    _matrix_rows(w, "w", (m.rows, m.cols), m.device)
+    _kvq_call(m.lib.ll_qmat_write, m, w.data_ptr(), _Types.codes[w.dtype], w.stride(0))
+
+
+def ll_qmat_read(m: "Q4Matrix", out=None, dtype=None):
+    """The matrix's values [rows, cols], each rounded once to bf16 (or fp32)."""
+    if out is None:
+        import torch
+        out = torch.empty(m.rows, m.cols, dtype=dtype or torch.bfloat16, device=m.device)
+    _matrix_rows(out, "out", (m.rows, m.cols), m.device, True)
+    _kvq_call(m.lib.ll_qmat_read, m, out.data_ptr(), _Types.codes[out.dtype], out.stride(0))
+    return out
+
+
+def ll_qmat_mul(m: "Q4Matrix", x, scale=None, add=None, out=None, out_dtype=None):
+    """x [n, cols] times the matrix's transpose (+ add [n, rows]): [n, rows]. x is bf16, fp32, or
+    float8_e4m3fn with ``scale`` (fp32 [n, 1] or [n, ceil(cols / 128)]); out like add, or of
+    ``out_dtype`` (bf16 if None). out may be add."""
+    device = m.device
+    if getattr(x, "ndim", 0) != 2:
+        raise LLError(LL_ERR_ARG, "x must be [n, cols]")
+    n = x.shape[0]
+    types = _Types.get()
+    group = 0
+    if x.dtype == _Types.e4m3:
+        if scale is None:
+            raise LLError(LL_ERR_ARG, "x in float8_e4m3fn needs its scales")
+        group = _scales(scale, "scale", n, m.cols, device)
+    elif scale is not None:
+        raise LLError(LL_ERR_ARG, f"x in {x.dtype} has no scales")
+    xr = _matrix_rows(x, "x", (n, m.cols), device, False, scale, group)
+    shape = (n, m.rows)
+    if out is None:
+        import torch
+        out = torch.empty(shape, dtype=out_dtype or (add.dtype if add is not None else torch.bfloat16), device=device)
+    yr = _matrix_rows(out, "out", shape, device, True)
+    ar = _matrix_rows(add, "add", shape, device) if add is not None else None
+    if types[out.dtype] == LL_E4M3:
+        raise LLError(LL_ERR_ARG, "out must be bfloat16 or float32")
+    _kvq_call(m.lib.ll_qmat_mul, m, xr, n, ar, yr)
+    return out
+
+
+def ll_rmsnorm(x, gain, eps: float = 1e-5, residual=None, residual_out=None, out=None, out_dtype=None, group: int = 0, scale=None):
+    """RMS norm of the rows of x [n, width], with the residual's addition in front if there is
+    one (residual_out: where the sum goes, residual itself if None). Returns out (of x's type, or
+    ``out_dtype``); for float8_e4m3fn (out, scale), a scale for each row (group 0) or 128 columns."""
+    if getattr(x, "ndim", 0) != 2:
+        raise LLError(LL_ERR_ARG, "x must be [n, width]")
+    import torch
+    shape, device = x.shape, x.device
+    n, width = shape
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
+    xr = _matrix_rows(x, "x", shape, device)
+    e4m3 = out.dtype == _Types.e4m3
+    if group not in (0, 128) or (group and not e4m3):
+        raise LLError(LL_ERR_ARG, "group is 0, or 128 for float8_e4m3fn")
+    if e4m3:
+        groups = (n, (width + 127) // 128 if group else 1)
+        if scale is None:
+            scale = torch.empty(groups, dtype=torch.float32, device=device)
+        elif getattr(scale, "device", None) != device or scale.dtype != torch.float32 or scale.shape != groups or not scale.is_contiguous():
+            raise LLError(LL_ERR_ARG, f"scale must be a contiguous float32 tensor {list(groups)} on {device}")
+    elif scale is not None:
+        raise LLError(LL_ERR_ARG, f"out in {out.dtype} has no scales")
+    outr = _matrix_rows(out, "out", shape, device, True, scale, group)
+    if getattr(gain, "device", None) != device or gain.dtype != torch.bfloat16 or gain.shape != (width,) or not gain.is_contiguous():
+        raise LLError(LL_ERR_ARG, f"gain must be a contiguous bfloat16 tensor [{width}] on {device}")
+    rr = ro = None
+    if residual is not None:
+        rr = _matrix_rows(residual, "residual", shape, device)
+        ro = rr if residual_out is None else _matrix_rows(residual_out, "residual_out", shape, device, True)
+    elif residual_out is not None:
+        raise LLError(LL_ERR_ARG, "residual_out needs a residual")
+    _device_call(lib().ll_rmsnorm, device, xr, rr, ro, gain.data_ptr(), eps, n, width, outr)
+    return (out, scale) if e4m3 else out
+
+
+def ll_verify(logits, drafts, u, probs=None, n_drafts=None, temperature=None, tokens=None, accepted=None):
+    """Verify drafts int32 [n_seq, n_draft] against logits [n_seq, n_draft + 1, vocab] (bf16 or fp32)
+    with the random numbers u [n_seq, n_draft + 1] (include/ll.h: ll_verify); n_draft may be 0.
+    probs [n_seq, n_draft, vocab]: the drafts' own distribution, or None; n_drafts int32 [n_seq] and
+    temperature fp32 [n_seq], or None. Returns tokens int32 [n_seq, n_draft + 1] (accepted drafts, the new
+    token, then -1) and accepted int32 [n_seq]."""
+    if getattr(logits, "ndim", 0) != 3 or not logits.is_cuda:
+        raise LLError(LL_ERR_ARG, "logits must be a CUDA tensor [n_seq, n_draft + 1, vocab]")
+    device = logits.device
+    S, rows, V = logits.shape
+    D = rows - 1
+    code = _Types.get().get(logits.dtype)
+    f32, int32 = _Types.f32, _Types.int32
+    ls, lr, last = logits.stride()
+    if code not in (LL_BF16, LL_F32) or (last != 1 and V > 1):
+        raise LLError(LL_ERR_ARG, "logits must be bfloat16 or float32, contiguous in the last dim")
+    if tokens is None or accepted is None:
+        import torch
+        tokens = torch.empty((S, rows), dtype=int32, device=device) if tokens is None else tokens
+        accepted = torch.empty((S,), dtype=int32, device=device) if accepted is None else accepted
+
+    def need(t, name, dtype, shape):
+        if getattr(t, "device", None) != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise LLError(LL_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+        return t.data_ptr()
+
+    dp = need(drafts, "drafts", int32, (S, D)) if D or drafts is not None else None
+    up = need(u, "u", f32, (S, rows))
+    tp, ap = need(tokens, "tokens", int32, (S, rows)), need(accepted, "accepted", int32, (S,))
+    np_ = need(n_drafts, "n_drafts", int32, (S,)) if n_drafts is not None else None
+    temp = need(temperature, "temperature", f32, (S,)) if temperature is not None else None
+    pp, ps, pr = None, 0, 0
+    if probs is not None:
+        if getattr(probs, "device", None) != device or probs.dtype != f32 or probs.shape != (S, D, V) or (V > 1 and probs.stride(2) != 1):
+            raise LLError(LL_ERR_ARG, f"probs must be a float32 tensor {[S, D, V]} on {device}, contiguous in the last dim")
+        pp, ps, pr = probs.data_ptr(), probs.stride(0), probs.stride(1)
+    _device_call(lib().ll_verify, device, logits.data_ptr(), code, ls, lr, dp, np_, pp, ps, pr, up, temp, S, D, V, tp, ap)
+    return tokens, accepted
 
 
 def ll_last_error(h) -> str:
@@ -721,3 +930,132 @@ class KVQCache:
 
     def attention(self, q, lens, n_toks=None, out=None, scale=None, max_len: int = 0):
         return ll_kvq_attention(self, q, lens, n_toks, out, scale, max_len)
+
+
+class Q4Matrix:
+    """A matrix [rows, cols] in 4 bits (the format in include/ll.h) over the caller's tensors: codes uint8
+    [ceil(rows / 16), ceil(cols / 128), 1024] and parameters float16 [ceil(rows / 16), ceil(cols / 128),
+    128 / group, 16, 2], contiguous, with groups of 32, 64 or 128 columns. Its calls are ll_qmat_write,
+    ll_qmat_read and ll_qmat_mul."""
+
+    def __init__(self, codes, params, rows: int, cols: int):
+        import torch
+        dev = getattr(codes, "device", None)
+        for t, name, dtype, dims in ((codes, "codes", torch.uint8, 3), (params, "params", torch.float16, 5)):
+            if not getattr(t, "is_cuda", False):
+                raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor")
+            if t.dtype != dtype or t.dim() != dims or t.device != dev or not t.is_contiguous():
+                raise LLError(LL_ERR_ARG, f"{name} must be contiguous {dtype} of {dims} dims on {dev}")
+        if rows < 1 or cols < 1:
+            raise LLError(LL_ERR_SHAPE, "every size must be positive")
+        per = params.shape[2]
+        if per not in (1, 2, 4):
+            raise LLError(LL_ERR_SHAPE, f"{per} groups to 128 columns: groups are 32, 64 or 128 wide")
+        tiles = ((rows + 15) // 16, (cols + 127) // 128)
+        for t, name, shape in ((codes, "codes", (*tiles, 1024)), (params, "params", (*tiles, per, 16, 2))):
+            if tuple(t.shape) != shape:
+                raise LLError(LL_ERR_ARG, f"{name} must be {shape} for a matrix of {rows} by {cols}, not {tuple(t.shape)}")
+        self.codes, self.params = codes, params
+        self.rows, self.cols, self.group = rows, cols, 128 // per
+        self.device = dev
+        self.struct = ll_qmat(_ptr(codes), _ptr(params), rows, cols, self.group)
+        self.ref = ctypes.byref(self.struct)
+        self.lib, self.index, self.torch_c = lib(), dev.index, torch._C  # what every call looks up
+        _Types.get()
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, group: int = 128, device="cuda"):
+        """A matrix of new tensors (all zeros)."""
+        import torch
+        if group not in (32, 64, 128) or rows < 1 or cols < 1:
+            raise LLError(LL_ERR_SHAPE, "every size must be positive, and group 32, 64 or 128")
+        tiles = ((rows + 15) // 16, (cols + 127) // 128)
+        return cls(torch.zeros(*tiles, 1024, dtype=torch.uint8, device=device),
+                   torch.zeros(*tiles, 128 // group, 16, 2, dtype=torch.float16, device=device), rows, cols)
+
+    @classmethod
+    def quantised(cls, w, group: int = 128):
+        """The matrix w [rows, cols] (bf16 or fp32, on the GPU) in 4 bits."""
+        m = cls.empty(w.shape[0], w.shape[1], group, w.device)
+        m.write(w)
+        return m
+
+    def write(self, w) -> None:
+        ll_qmat_write(self, w)
+
+    def read(self, out=None, dtype=None):
+        return ll_qmat_read(self, out, dtype)
+
+    def matvec(self, x, scale=None, add=None, out=None, out_dtype=None):
+        return ll_qmat_mul(self, x, scale, add, out, out_dtype)
+
+
+class Rope:
+    """Rotary positions of head_dim-wide heads (include/ll.h: ll_rope): ``rot_dims`` of them (all if None),
+    halves or interleaved pairs, frequencies from ``theta``. scaling: None, or a dict of "kind" and its values:
+    "linear" (factor), "bands" (factor, low, high, length), "ramp" (factor, fast, slow, length; fast and slow
+    the turns over the original length that bound the ramp). apply's lens and n_toks are as KVQCache's."""
+
+    def __init__(self, head_dim: int, theta: float = 500000.0, rot_dims=None, interleaved: bool = False, scaling=None):
+        s = dict(scaling or {"kind": "plain"})
+        kind = s.pop("kind", None)
+        keys = {"plain": (), "linear": ("factor",), "bands": ("factor", "low", "high", "length"), "ramp": ("factor", "fast", "slow", "length")}
+        if kind not in keys or set(s) != set(keys[kind]):
+            raise LLError(LL_ERR_ARG, f"scaling {scaling} is not one of " + ", ".join(f"{k} {v}" for k, v in keys.items()))
+        if kind == "ramp":
+            s["low"], s["high"] = s.pop("slow"), s.pop("fast")
+        self.table = ll_rope_table()
+        self.ref = ctypes.byref(self.table)
+        self.lib, self.head_dim = lib(), head_dim
+        err = ctypes.create_string_buffer(256)
+        rc = self.lib.ll_rope_plan(self.ref, head_dim, head_dim if rot_dims is None else rot_dims, int(interleaved), theta,
+                                   list(keys).index(kind), s.get("factor", 1.0), s.get("low", 0.0), s.get("high", 0.0),
+                                   s.get("length", 0.0), err, 256)
+        if rc != LL_OK:
+            raise LLError(rc, err.value.decode())
+
+    def _rows(self, t, name: str, like, heads: int, written: bool):
+        if getattr(t, "device", None) != like.device or t.dtype != like.dtype:
+            raise LLError(LL_ERR_ARG, f"{name} must be {like.dtype} on {like.device}, as q")
+        if t.shape != (like.shape[0], like.shape[1], heads, self.head_dim):
+            raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {[*like.shape[:2], heads, self.head_dim]}")
+        seq, token, head, last = t.stride()
+        if last != 1:
+            raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
+        if written and not t.is_contiguous():  # no two rows of an output may share memory
+            reach = self.head_dim
+            for stride, size in sorted(((seq, t.shape[0]), (token, t.shape[1]), (head, heads))):
+                if size > 1:
+                    if stride < reach:
+                        raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
+                    reach += stride * (size - 1)
+        return _rows_bytes(t.data_ptr(), seq, token, head)
+
+    def apply(self, q, k, lens, n_toks=None, q_out=None, k_out=None, inverse: bool = False):
+        """Turn the last tokens' q [n_seq, n_tok, n_q_heads, head_dim] and k [n_seq, n_tok, n_k_heads, head_dim]
+        (or None), bf16 or fp32, into q_out and k_out (in place where None). Rows of padded
+        tokens keep what they hold."""
+        if getattr(q, "ndim", 0) != 4 or not q.is_cuda:
+            raise LLError(LL_ERR_ARG, "q must be a CUDA tensor [n_seq, n_tok, n_q_heads, head_dim]")
+        code = _Types.get().get(q.dtype)
+        if code not in (LL_BF16, LL_F32):
+            raise LLError(LL_ERR_ARG, f"q must be bfloat16 or float32, not {q.dtype}")
+        S, n_tok, heads, _ = q.shape
+        qo = q if q_out is None else q_out
+        qr, qor = self._rows(q, "q", q, heads, q_out is None), self._rows(qo, "q_out", q, heads, True)
+        kr = kor = None
+        k_heads = 0
+        if k is not None:
+            k_heads = k.shape[2] if getattr(k, "ndim", 0) == 4 else 0
+            kr = self._rows(k, "k", q, k_heads, k_out is None)
+            kor = kr if k_out is None else self._rows(k_out, "k_out", q, k_heads, True)
+        elif k_out is not None:
+            raise LLError(LL_ERR_ARG, "k_out needs a k")
+        for t, name in ((lens, "lens"), (n_toks, "n_toks")):
+            if t is None and name == "n_toks":
+                continue
+            if getattr(t, "device", None) != q.device or t.dtype != _Types.int32 or t.shape != (S,) or not t.is_contiguous():
+                raise LLError(LL_ERR_ARG, f"{name} must be a contiguous int32 tensor [{S}] on {q.device}")
+        _device_call(self.lib.ll_rope, q.device, self.ref, qr, qor, heads, kr, kor, k_heads, code, S, n_tok, lens.data_ptr(),
+                     n_toks.data_ptr() if n_toks is not None else None, int(inverse))
+        return qo, (k if k_out is None else k_out)

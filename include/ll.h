@@ -402,6 +402,152 @@ int ll_kvq_attention(const ll_kvq_cache *c, const ll_kvq_rows *q, int32_t n_q_he
  * (ll_set_timeout_ns) and then record LL_ERR_DEP_TIMEOUT. */
 int ll_init_kvq(const ll_config *cfg, const ll_weights *w, const ll_kvq_cache *cache, void *stream, ll_handle **out);
 
+/* ---- What a decode step does around the attention -----------------------------
+ *
+ * Products with 4-bit matrices, RMS norm, rotary positions, and the verification of
+ * drafted tokens, for callers who lay out their own steps (around the packed cache's
+ * calls, say). As those calls, they need no handle, enqueue on `stream` of the current
+ * device, allocate nothing, keep nothing between calls, may be captured into CUDA
+ * graphs, and return LL_OK, LL_ERR_ARG / LL_ERR_SHAPE (nothing was launched),
+ * LL_ERR_DEVICE or LL_ERR_CUDA with a one-line reason in err. Repeated on the same
+ * data, a call gives the same bits. Outputs must not overlap inputs or each other
+ * unless a call says so. */
+#define LL_E4M3 2 /* 8-bit floats: 1 sign, 4 exponent, 3 mantissa bits, no infinities */
+
+/* A matrix of rows x cols values in 4 bits. Each row is cut into groups of `group`
+ * columns (32, 64 or 128; the last may be short); a group has two fp16 parameters,
+ * lo and step, and a code c stands for lo + step * c (not rounded). In memory:
+ * tiles of 16 rows by 128 columns, KT = ceil(cols / 128) of them to a tile row.
+ *   codes: tile (R, K) is the 1024 bytes from codes + (R * KT + K) * 1024, as 256
+ *     words of 8 codes. The codes of row r and columns k..k+7 (k a multiple of 8) are
+ *     in word (r % 16 / 8) * 128 + (r % 8) * 16 + (k % 32 / 8) * 4 + k % 128 / 32 of
+ *     tile (r / 16, k / 128); the code of column k + i is in the 4 bits that begin at
+ *     bit (4 f + 3) % 32, f = i / 2 + 4 (i % 2) (the one at bit 31 goes on at bit 0).
+ *   params: (lo, step) of row r and group k / group are the fp16 pair number
+ *     ((R * KT + K) * (128 / group) + k % 128 / group) * 16 + r % 16.
+ * Rows and columns past the matrix, up to whole tiles, must exist; theirs are zeros
+ * where this library writes them, and any codes with finite parameters do as well. */
+typedef struct {
+    uint8_t *codes;   /* device, 16-byte aligned: ceil(rows / 16) * KT * 1024 bytes */
+    uint16_t *params; /* device, 16-byte aligned: ceil(rows / 16) * KT * (128 / group) * 32 values */
+    int32_t rows, cols; /* outputs and inputs, 1 to 2^24 each */
+    int32_t group;
+} ll_qmat;
+
+/* Quantise a matrix w (type LL_BF16 or LL_F32, row r from w + r * stride elements on;
+ * any alignment of its type) into m: over a group's values x, each clamped to +-60000,
+ * lo = fp16(min x), step = fp16((max x - lo) / 15), code = the integer nearest to
+ * (x - lo) / step, ties to even, clamped to [0, 15], 0 where step is 0. A group holding a
+ * NaN reads back as NaN. */
+int ll_qmat_write(const ll_qmat *m, const void *w, int32_t type, int64_t stride, void *stream, char *err, size_t err_len);
+
+/* The matrix that m stands for, each value rounded once to `type` (LL_BF16 or LL_F32),
+ * row r to w + r * stride elements, stride >= cols. */
+int ll_qmat_read(const ll_qmat *m, void *w, int32_t type, int64_t stride, void *stream, char *err, size_t err_len);
+
+/* Rows of a matrix operand: row i begins at data + i * stride elements. */
+typedef struct {
+    void *data;     /* device, aligned to its type */
+    int64_t stride; /* elements; not looked at when there is one row */
+    int32_t type;   /* LL_BF16, LL_F32 or (where a call takes it) LL_E4M3 */
+    int32_t group;  /* LL_E4M3: columns that share a scale: 128, or 0 for a whole row */
+    float *scale;   /* LL_E4M3: device [rows][ceil(cols / group)], row after row (one a row for group 0) */
+} ll_rows;
+
+/* y = x W^T (+ add): for each of n rows, y[i][r] = sum_k W[r][k] x[i][k] + add[i][r], one
+ * rounding to y's type. x [n][cols]: LL_BF16, LL_F32 or LL_E4M3 with scales (a value is its
+ * code times its scale). y and add [n][rows]: LL_BF16 or LL_F32, both of one type; add may
+ * be NULL, and may be y itself. n: 1 to 2^19. The codes are multiplied as integers and sums held
+ * in fp32; fp32 x enters with all its bits (as three bf16 terms). bf16 y of many rows n of bf16 or
+ * e4m3 x may be computed from W and x in fp16's 11 bits (x scaled by a power of two a
+ * row). A row of x that holds a NaN or an infinity gives infinities or NaN in its own
+ * row of y alone; finite values should be below 2^100 in size. */
+int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *add, const ll_rows *y, void *stream, char *err,
+                size_t err_len);
+
+/* RMS norm of n rows of `width` values (1 to 32768), with a residual's addition in front:
+ *   r = x                        (residual NULL)
+ *   r = x + residual, rounded to residual's type and stored to residual_out,
+ *   out = r / sqrt(mean(r^2) + eps) * gain
+ * in fp32, rounded once to out's type. x, residual: LL_BF16 or LL_F32 each; residual_out
+ * as residual, and may be residual or x itself where its type is theirs; out: LL_BF16,
+ * LL_F32 or LL_E4M3, and may be x where its type is x's. gain: bf16 [width]. In LL_E4M3 each group of
+ * out->group columns (128, or 0 for the row) gets scale = max|out| / 448, 2^-126 at least, and
+ * the codes nearest to out / scale. */
+int ll_rmsnorm(const ll_rows *x, const ll_rows *residual, const ll_rows *residual_out, const uint16_t *gain, float eps,
+               int32_t n, int32_t width, const ll_rows *out, void *stream, char *err, size_t err_len);
+
+/* Rotary positions. Of a head's head_dim values the first rot_dims are turned in pairs
+ * i < rot_dims / 2: (i, i + rot_dims / 2), or (2 i, 2 i + 1) in the interleaved layout; the
+ * others are copied. At position p pair (a, b) becomes
+ *   (a cos t - b sin t, b cos t + a sin t) * size,   t = p * f_i
+ * with f_i = theta^(-2 i / rot_dims), changed by `scaling`:
+ *   LL_ROPE_PLAIN   not at all;
+ *   LL_ROPE_LINEAR  f_i / factor;
+ *   LL_ROPE_BANDS   by the turns w = length * f_i / (2 pi) that the pair makes over the
+ *     original context length: s = (w - low) / (high - low) held within [0, 1],
+ *     f_i s + f_i / factor (1 - s);
+ *   LL_ROPE_RAMP    between the pairs that make `high` and `low` turns over it: d(b) =
+ *     rot_dims ln(length / (2 pi b)) / (2 ln theta), first = max(floor d(high), 0), last =
+ *     min(ceil d(low), rot_dims - 1), s = (i - first) / (last - first) held within [0, 1] (a
+ *     difference of 0 taken as 0.001), f_i (1 - s) + f_i / factor s, and size = 0.1 ln(factor)
+ *     + 1 (1 in the others).
+ * ll_rope_plan works the frequencies out into *r, which its caller keeps (no device
+ * memory): turns a position as 64-bit fractions, so that a position's angle is the
+ * remainder of an integer product and far positions lose nothing. */
+#define LL_ROPE_PLAIN 0
+#define LL_ROPE_LINEAR 1
+#define LL_ROPE_BANDS 2
+#define LL_ROPE_RAMP 3
+
+typedef struct {
+    int32_t head_dim, rot_dims, interleaved;
+    float size;
+    uint64_t turns[128]; /* f_i / (2 pi) * 2^64, rounded, modulo 2^64 */
+} ll_rope_table;
+
+/* head_dim: a multiple of 8, at most 256; rot_dims: even, 2 to head_dim; theta > 1; factor >= 1,
+ * length >= 1 and high > low > 0 where `scaling` uses them. Host only. */
+int ll_rope_plan(ll_rope_table *r, int32_t head_dim, int32_t rot_dims, int32_t interleaved, double theta, int32_t scaling,
+                 double factor, double low, double high, double length, char *err, size_t err_len);
+
+/* Turn the last tokens' query rows q [n_seq][n_tok][n_q_heads][head_dim] and key rows k
+ * [n_seq][n_tok][n_k_heads][head_dim] (both of type LL_BF16 or LL_F32) into q_out and k_out, as
+ * the packed cache's calls take rows, sequences and tokens: token j of a sequence's n is at
+ * position len_dev[s] - n + j. Padded tokens and positions below 0 are skipped. The outputs may be
+ * the inputs (the same rows); k and k_out may both be NULL. inverse != 0 turns backwards
+ * (with the same size): the transposed rotation, which gradients need. Computed in fp32, one rounding. */
+int ll_rope(const ll_rope_table *r, const ll_kvq_rows *q, const ll_kvq_rows *q_out, int32_t n_q_heads, const ll_kvq_rows *k,
+            const ll_kvq_rows *k_out, int32_t n_k_heads, int32_t type, int32_t n_seq, int32_t n_tok, const int32_t *len_dev,
+            const int32_t *n_tok_dev, int32_t inverse, void *stream, char *err, size_t err_len);
+
+/* Verify drafted tokens against the target model's logits, from given random numbers, and
+ * draw the token behind the last accepted one; with n_draft = 0, sample a token.
+ *   logits: [n_seq][n_draft + 1][vocab] (LL_BF16 or LL_F32; strides in elements): row j decides
+ *     draft j, and row n of a sequence with n drafts gives the token behind them all.
+ *   draft: device int32 [n_seq][n_draft]; n_draft_dev: device int32 [n_seq], each sequence's
+ *     number of drafts, held within [0, n_draft], or NULL for n_draft.
+ *   probs: device fp32 [n_seq][n_draft][vocab] by strides, the distribution q_j that draft j was
+ *     drawn from (of the same temperature), or NULL for drafts that were not drawn: q_j is then 1 at the draft.
+ *   u: device fp32 [n_seq][n_draft + 1] in [0, 1): u_j decides draft j, the last one draws.
+ *   temperature: device fp32 [n_seq], or NULL for 1. p_j = softmax(logits_j / temperature);
+ *     0 (anything not above 2^-100) is greedy: p_j is 1 at the largest logit, the lowest index of equals.
+ * Draft j is accepted if all before it were and u_j q_j(x) < p_j(x). At the first that is not, r, the
+ * new token is drawn from max(p_r - q_r, 0) (from p_r, should that be 0 everywhere); behind
+ * n accepted ones from p_n. A draw gives the lowest index whose sum of weights up to it exceeds
+ * u times the sum of all. Greedy: accepted if it is the largest, whose index the new token is.
+ *   tokens: device int32 [n_seq][n_draft + 1]: the accepted drafts, the new token, then -1.
+ *   accepted: device int32 [n_seq], how many drafts were.
+ * NaN logits are never drawn (as -infinity); +infinity takes all the weight, shared by equals. A row
+ * without any other logit ends its sequence with the token -1. A draft outside [0, vocab) is
+ * rejected. Rows behind the first rejection and behind a sequence's drafts are not read, or without effect.
+ * vocab: 1 to 393216. Weights are held to 2^-43 of the largest, sums exactly. Every wait inside is for a
+ * block of the same cluster, which runs at the same time. */
+int ll_verify(const void *logits, int32_t type, int64_t logits_seq, int64_t logits_row, const int32_t *draft,
+              const int32_t *n_draft_dev, const float *probs, int64_t probs_seq, int64_t probs_row, const float *u,
+              const float *temperature, int32_t n_seq, int32_t n_draft, int32_t vocab, int32_t *tokens, int32_t *accepted,
+              void *stream, char *err, size_t err_len);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,190 @@
+"""Matrices in 4 bits on the GPU: quantising, reading back, products."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from decode_megakernel_persistent_gb300 import ll
+import step_ref
+from step_ref import gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_megakernel_persistent_gb300 import build
+    build.build()
+
+
+def padded(shape, dtype, pad, seed):
+    """Random values in rows that are `pad` elements apart from each other more than their width."""
+    return torch.randn(shape[0], shape[1] + pad, generator=gen(seed), device="cuda").to(dtype)[:, :shape[1]]
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (16, 128), (17, 129), (5, 40), (33, 1000), (256, 512)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_write_and_read(rows, cols, group, dtype, pad):
+    w = padded((rows, cols), dtype, pad, 1)
+    m = ll.Q4Matrix.quantised(w, group)
+    code, lo, step = step_ref.unpack(m.codes, m.params, rows, cols)
+    want, steps = step_ref.quantised(w.cpu(), group)
+    got = m.read(dtype=torch.float32)
+    # the values are what codes and parameters say, to fp32's rounding
+    assert bool(((lo + step * code) - got.cpu().double()).abs().le((lo.abs() + 15 * step) * 2.0 ** -24).all())
+    assert torch.equal(lo, step_ref.unpack(m.codes, m.params, rows, cols)[1]) and torch.equal(step, steps)
+    # and the definition's, but for codes within fp32's rounding of a border (16 units of 2^-24, twice): no more than few of those
+    off = ((lo + step * code) - want).abs()
+    z = (w.cpu().double() - lo) / torch.where(step > 0, step, 1.0)
+    border = ((z - z.floor()) - 0.5).abs() < 2.0 ** -18
+    assert bool((off <= step * border).all())
+    out = torch.full((rows, cols + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+    m.read(out[:, :cols])
+    assert torch.equal(out[:, :cols], got.bfloat16()) and bool((out[:, cols:] == 7).all())
+
+
+def test_written_padding_is_zero():
+    m = ll.Q4Matrix(torch.full((2, 2, 1024), 255, dtype=torch.uint8, device="cuda"),
+                    torch.full((2, 2, 2, 16, 2), 9.0, dtype=torch.float16, device="cuda"), 17, 130)
+    m.write(padded((17, 130), torch.float32, 0, 3))
+    code, lo, step = step_ref.unpack(m.codes, m.params, 32, 256)
+    assert float(code[17:].abs().max()) == 0 and float(code[:, 130:].abs().max()) == 0
+    assert float(lo[17:].abs().max()) == 0 and float(step[17:].abs().max()) == 0 and float(lo[:, 192:].abs().max()) == 0
+
+
+def test_special_values_in_a_matrix():
+    w = torch.randn(16, 256, generator=gen(2), device="cuda")
+    w[1, 5] = float("nan")
+    w[2, 200] = float("inf")
+    w[3, 0] = -1e30
+    w[4] = 0.25
+    m = ll.Q4Matrix.quantised(w, 64)
+    got = m.read(dtype=torch.float32)
+    nan = torch.isnan(got)
+    want = torch.zeros_like(nan)
+    want[1, :64] = True
+    assert torch.equal(nan, want)
+    assert float(got[2, 200]) <= 60000 * (1 + 2.0 ** -10) and float(got[2, 200]) >= 60000 * (1 - 2.0 ** -10)
+    assert float(got[3, 0]) == float(torch.tensor(-60000.0).half())
+    assert bool((got[4] == 0.25).all())
+
+
+def integer_matrix(rows, cols, group, seed):
+    """A matrix whose values, as rows of small integers, leave nothing to round in fp32 sums."""
+    g = gen(seed, "cpu")
+    code = torch.randint(0, 16, (rows, cols), generator=g)
+    lo = torch.randint(-8, 9, (rows, -(-cols // group)), generator=g).double()
+    step = torch.randint(0, 4, lo.shape, generator=g).double()
+    codes, params = step_ref.pack(code, lo, step, group)
+    # what lies past the matrix may be anything finite
+    garbage = torch.randint(0, 256, codes.shape, generator=g, dtype=torch.uint8)
+    R, K = codes.shape[:2]
+    full, _, _ = step_ref.unpack(garbage, params, 16 * R, 128 * K)
+    full[:rows, :cols] = code.double()
+    per = 128 // group
+    p = params.permute(0, 3, 1, 2, 4).reshape(16 * R, K * per, 2).double()
+    p[rows:] = 2.0
+    p[:, lo.shape[1]:] = -3.0
+    codes, params = step_ref.pack(full.long(), p[..., 0], p[..., 1], group)
+    return ll.Q4Matrix(codes.cuda(), params.cuda(), rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (16, 128), (15, 127), (17, 300), (100, 1031), (512, 2048), (40, 4096), (2100, 384)])
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 8, 9, 16, 17, 33, 64, 70])
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "e4m3", "e4m3 groups"])
+def test_integers_are_exact(rows, cols, n, kind):
+    """Every sum below 2^24 and every value an integer: whatever the order, the result is exact, so a column or
+    row out of place shows whatever its size. fp32 x has integers of 24 bits, a few of them."""
+    group = (32, 64, 128)[(rows + n) % 3]
+    m = integer_matrix(rows, cols, group, rows * 1000 + n)
+    g = gen(n, "cpu")
+    x = torch.randint(-2, 3, (n, cols), generator=g).double()
+    scale, xs, wide = None, x, x
+    if kind == "fp32":
+        wide = x.clone()
+        wide[:, 0] = 12345.0 + torch.arange(n)
+        xs = wide.float().cuda()
+    elif kind == "bf16":
+        xs = x.bfloat16().cuda()
+    else:
+        groups = -(-cols // 128) if kind == "e4m3 groups" else 1
+        scale = 2.0 ** torch.randint(-1, 2, (n, groups), generator=g).double()
+        wide = x * (scale.repeat_interleave(128, 1)[:, :cols] if groups > 1 else scale)
+        xs, scale = x.to(torch.float8_e4m3fn).cuda(), scale.float().cuda()
+    code, lo, step = step_ref.unpack(m.codes, m.params, rows, cols)
+    want = wide @ (lo + step * code).t()
+    assert float((wide.abs() @ (lo.abs() + step * code + 16 * step).t()).max()) < 2 ** 24
+    got = m.matvec(xs, scale=scale, out_dtype=torch.float32)
+    assert torch.equal(got.cpu().double(), want)
+    add = torch.randint(-9, 9, (n, rows), generator=g).double()
+    got = m.matvec(xs, scale=scale, add=add.float().cuda())
+    assert torch.equal(got.cpu().double(), want + add)
+
+
+@pytest.mark.parametrize("rows,cols,group", [(64, 4096, 128), (300, 2048, 64), (48, 1000, 32), (2064, 14336, 128)])
+@pytest.mark.parametrize("n", [1, 4, 7, 13, 30, 64, 130])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products(rows, cols, group, n, kind, dtype):
+    m = ll.Q4Matrix.quantised(0.02 * torch.randn(rows, cols, generator=gen(rows), device="cuda") + 0.01, group)
+    x = torch.randn(n, cols, generator=gen(n), device="cuda")
+    x[:, ::37] *= 30  # outliers, as activations have them
+    scale = None
+    if kind == torch.float8_e4m3fn:
+        scale = (x.unflatten(1, (-1, 8)).abs().amax((1, 2)) / 448)[:, None].contiguous()
+        wide = (x / scale).to(kind)
+        x, wide = wide, wide.double() * scale.double()
+    else:
+        x = x.to(kind)
+        wide = x.double()
+    add = torch.randn(n, rows, generator=gen(5), device="cuda").to(dtype) if n % 2 else None
+    got = m.matvec(x, scale=scale, add=add, out_dtype=dtype)
+    want, tol = step_ref.product(m, wide.cpu(), None if add is None else add.double().cpu(), dtype)
+    off = (got.cpu().double() - want).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    again = m.matvec(x, scale=scale, add=add, out_dtype=dtype)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_strides_of_operands(n, kind):
+    """Rows that are apart, not 16-byte aligned, the same for all (stride 0); add that is the output itself."""
+    rows, cols = 70, 520
+    m = ll.Q4Matrix.quantised(torch.randn(rows, cols, generator=gen(1), device="cuda"), 64)
+    x = torch.randn(n, cols, generator=gen(2), device="cuda").to(kind)
+    want = m.matvec(x, out_dtype=torch.float32)
+    for pad, shift in ((8, 0), (3, 1), (1, 5)):
+        store = torch.full((n, cols + pad + shift), float("nan"), dtype=kind, device="cuda")
+        view = store[:, shift:shift + cols]
+        view.copy_(x)
+        out = torch.full((n, rows + pad), 3.0, device="cuda")
+        m.matvec(view, out=out[:, :rows])
+        assert torch.equal(out[:, :rows], want) and bool((out[:, rows:] == 3).all())
+    one = m.matvec(x[:1].expand(n, cols), out_dtype=torch.float32)
+    assert torch.equal(one, want[:1].expand(n, rows))
+    add = torch.randn(n, rows, generator=gen(3), device="cuda")
+    both = m.matvec(x, add=add)
+    own = add.clone()
+    m.matvec(x, add=own, out=own)
+    assert torch.equal(own, both)
+
+
+@pytest.mark.parametrize("n", [3, 20, 64])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
+def test_a_row_that_is_not_finite_stays_alone(n, kind):
+    m = ll.Q4Matrix.quantised(torch.randn(40, 300, generator=gen(1), device="cuda"), 128)
+    x = torch.randn(n, 300, generator=gen(2), device="cuda").to(kind)
+    scale = torch.ones(n, 1, device="cuda") if kind == torch.float8_e4m3fn else None
+    for dtype in (torch.bfloat16, torch.float32):
+        want = m.matvec(x, scale=scale, out_dtype=dtype)
+        y = x.float().clone()
+        y[1, 17] = float("nan")
+        y[2, 299] = float("nan") if kind == torch.float8_e4m3fn else float("inf")
+        got = m.matvec(y.to(kind), scale=scale, out_dtype=dtype)
+        assert not bool(torch.isfinite(got[1:3].float()).any())
+        keep = [i for i in range(n) if i not in (1, 2)]
+        assert torch.equal(got[keep], want[keep])

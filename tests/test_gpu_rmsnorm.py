@@ -1,0 +1,123 @@
+"""RMS norm with the residual's addition on the GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from decode_megakernel_persistent_gb300 import ll
+from step_ref import HALF_STEP, gen
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_megakernel_persistent_gb300 import build
+    build.build()
+
+
+def reference(x, gain, eps, residual):
+    """(sum as it is stored, norm) in 64 bits and the norm's bound but for its last rounding."""
+    r = x.double()
+    if residual is not None:
+        r = (x.float() + residual.float()).to(residual.dtype).double()
+    v = r / (r.square().mean(1, keepdim=True) + eps).sqrt() * gain.double()
+    # the sum of squares: 32 additions a thread, 15 over the threads, each square rounded: 48 roundings,
+    # half of it behind the root; division, eps, root, reciprocal and two products: 6 more
+    return r, v, (24 + 6) * 2.0 ** -24 * v.abs()
+
+
+def check(x, gain, eps, residual, dtype, group):
+    r, v, tol = reference(x, gain, eps, residual)
+    new = torch.full_like(residual, 5.0) if residual is not None else None
+    got = ll.ll_rmsnorm(x, gain, eps, residual=residual, residual_out=new, out_dtype=dtype, group=group)
+    if residual is not None:
+        assert torch.equal(new.double(), r)
+    if dtype != E4M3:
+        assert bool(((got.double() - v).abs() <= tol + HALF_STEP[dtype] * (v.abs() + tol) + 1e-37).all())
+        return got
+    codes, scale = got
+    n, width = x.shape
+    g = group or width
+    assert scale.shape == (n, -(-width // g))
+    most = torch.stack([v[:, a:a + g].abs().amax(1) for a in range(0, width, g)], 1)
+    want = (most / 448).clamp(min=2.0 ** -126)
+    assert bool(((scale.double() - want).abs() <= want * 33 * 2.0 ** -24).all())
+    wide = scale.double().repeat_interleave(g, 1)[:, :width]
+    # half a step of three mantissa bits, or of the smallest step (2^-9); reciprocal and product 2^-23
+    z = v / wide
+    assert bool(((codes.double() - z).abs() <= (z.abs() * 2.0 ** -4).clamp(min=2.0 ** -10) * (1 + 2.0 ** -18) + z.abs() * 34 * 2.0 ** -24).all())
+    return codes
+
+
+@pytest.mark.parametrize("n,width", [(1, 1), (3, 7), (5, 64), (1, 128), (40, 129), (2, 256), (7, 500), (3, 1000), (1, 2048), (9, 4096), (2, 4100),
+                                     (3, 8192), (2, 14336), (1, 16385), (2, 32768), (1000, 64)])
+@pytest.mark.parametrize("dtype,group", [(torch.bfloat16, 0), (torch.float32, 0), (E4M3, 0), (E4M3, 128)])
+@pytest.mark.parametrize("kinds", ["b", "f", "bb", "bf", "fb", "ff"])
+def test_norm(n, width, dtype, group, kinds):
+    t = {"b": torch.bfloat16, "f": torch.float32}
+    x = torch.randn(n, width, generator=gen(n), device="cuda").to(t[kinds[0]])
+    residual = 4 * torch.randn(n, width, generator=gen(width), device="cuda").to(t[kinds[1]]) if len(kinds) > 1 else None
+    gain = (1 + 0.2 * torch.randn(width, generator=gen(3), device="cuda")).bfloat16()
+    check(x, gain, 1e-5, residual, dtype, group)
+
+
+@pytest.mark.parametrize("dtype,group", [(torch.bfloat16, 0), (E4M3, 0), (E4M3, 128)])
+@pytest.mark.parametrize("width", [72, 513, 4096])
+def test_rows_apart_and_in_place(width, dtype, group):
+    n = 6
+    gain = (1 + 0.2 * torch.randn(width, generator=gen(3), device="cuda")).bfloat16()
+    x = torch.randn(n, width, generator=gen(1), device="cuda").bfloat16()
+    res = torch.randn(n, width, generator=gen(2), device="cuda").bfloat16()
+    base = check(x, gain, 1e-5, res, dtype, group)
+    for pad, shift in ((8, 0), (5, 1)):
+        xs, rs = (torch.full((n, width + pad + shift), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        xs[:, shift:shift + width], rs[:, shift:shift + width] = x, res
+        out = torch.full((n, width + pad), 2.0, device="cuda").to(dtype)
+        got = ll.ll_rmsnorm(xs[:, shift:shift + width], gain, 1e-5, residual=rs[:, shift:shift + width], out=out[:, :width], group=group)
+        got = got[0] if dtype == E4M3 else got
+        assert torch.equal(got.float(), base.float()) and bool((out[:, width:].float() == 2).all())
+        assert torch.equal(rs[:, shift:shift + width], (x.float() + res.float()).bfloat16())  # (in place)
+        assert bool(torch.isnan(rs[:, shift + width:]).all())
+    if dtype == torch.bfloat16:  # out may be x, and residual_out x
+        y = x.clone()
+        assert torch.equal(ll.ll_rmsnorm(y, gain, 1e-5, residual=res.clone(), out=y), base) and torch.equal(y, base)
+        y = x.clone()
+        assert torch.equal(ll.ll_rmsnorm(y, gain, 1e-5, residual=res, residual_out=y), base)
+    # the same row for all
+    row = x[:1].expand(n, width)
+    got = ll.ll_rmsnorm(row, gain, 1e-5, out_dtype=torch.float32)
+    assert torch.equal(got, got[:1].expand(n, width))
+
+
+@pytest.mark.parametrize("width", [100, 2048])
+def test_special_rows(width):
+    x = torch.randn(6, width, generator=gen(1), device="cuda")
+    x[0] = 0
+    x[1, 3] = float("nan")
+    x[2, 4] = float("inf")
+    x[3] *= 1e-30
+    x[4] *= 1e15
+    gain = torch.ones(width, dtype=torch.bfloat16, device="cuda")
+    out = ll.ll_rmsnorm(x, gain, 0.0 if width == 100 else 1e-5)
+    if width == 100:  # 0 / sqrt(0)
+        assert bool(torch.isnan(out[0]).all())
+    else:
+        assert bool((out[0] == 0).all())
+        _, v, tol = reference(x[3:], gain, 1e-5, None)
+        assert bool(((out[3:].double() - v).abs() <= tol + 2.0 ** -24 * v.abs() + 1e-37).all())
+    assert bool(torch.isnan(out[1]).all()) and bool(torch.isnan(out[2, 4]))
+    codes, scale = ll.ll_rmsnorm(x, gain, 1e-5, out_dtype=E4M3)
+    assert bool((codes[0].float() == 0).all()) and bool(torch.isfinite(scale[0]).all())
+    assert bool(torch.isnan(codes[1].float()).all())
+    tiny = (codes[3].double() * scale[3].double())
+    assert bool((tiny - x[3].double() / 1e-5 ** 0.5).abs().le(x[3].double().abs() / 1e-5 ** 0.5 * (2.0 ** -4 + 1e-4) + float(scale[3]) * 2.0 ** -10).all())
+
+
+def test_many_rows():
+    n, width = 70001, 128
+    x = torch.randn(n, width, generator=gen(1), device="cuda").bfloat16()
+    gain = torch.ones(width, dtype=torch.bfloat16, device="cuda")
+    check(x, gain, 1e-6, None, torch.bfloat16, 0)

@@ -1,0 +1,195 @@
+"""Verification of drafted tokens on the GPU: equal to the definition in 64 bits, decision by decision."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from decode_megakernel_persistent_gb300 import ll
+import step_ref
+from step_ref import gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_megakernel_persistent_gb300 import build
+    build.build()
+
+
+def make(S, D, V, seed, dtype=torch.float32, probs=True, spread=2.0, noise=0.7, temperature=1.0):
+    g = gen(seed)
+    logits = spread * torch.randn(S, D + 1, V, generator=g, device="cuda")
+    if V > 16:
+        logits.scatter_add_(2, torch.randint(0, V, (S, D + 1, 4), generator=g, device="cuda"), 8 + torch.randn(S, D + 1, 4, generator=g, device="cuda"))
+    logits = logits.to(dtype)
+    guess = (logits[:, :D].float() + noise * torch.randn(S, D, V, generator=g, device="cuda")) / temperature
+    q = torch.softmax(guess, -1) if probs else None
+    drafts = (guess - torch.rand(S, D, V, generator=g, device="cuda").clamp(min=1e-30).log().neg().log()).argmax(-1).int() if D else \
+        torch.zeros(S, 0, dtype=torch.int32, device="cuda")
+    return logits, drafts, torch.rand(S, D + 1, generator=g, device="cuda"), q
+
+
+def cpu(t):
+    return None if t is None else t.cpu()
+
+
+def check(logits, drafts, u, probs=None, n_drafts=None, temperature=None, border=1e-6):
+    tokens, accepted = ll.ll_verify(logits, drafts, u, probs=probs, n_drafts=n_drafts, temperature=temperature)
+    want = step_ref.verified(cpu(logits), cpu(drafts), cpu(u), cpu(probs), cpu(n_drafts), cpu(temperature))
+    # (acceptance compares fp32 sums: a decision within 1e-6 of its border could go either way. None is.)
+    assert border is None or want[2] > border * (1e-4 if logits.shape[2] > 1000 else 1), want[2]
+    assert torch.equal(accepted.cpu(), want[1]) and torch.equal(tokens.cpu(), want[0])
+    return tokens, accepted
+
+
+@pytest.mark.parametrize("V", [1, 2, 7, 64, 1000, 1001, 32000, 128256])
+@pytest.mark.parametrize("D", [0, 1, 4])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("probs", [True, False])
+def test_verify(V, D, dtype, probs):
+    S = 9
+    for T in (1.0, 0.6):
+        logits, drafts, u, q = make(S, D, V, V + D, dtype, probs and D > 0, temperature=T)
+        check(logits, drafts, u, q, temperature=torch.full((S,), T, device="cuda"))
+
+
+def test_ragged_and_mixed_temperatures():
+    S, D, V = 24, 6, 5003
+    logits, drafts, u, q = make(S, D, V, 5)
+    n = torch.arange(S, dtype=torch.int32, device="cuda") % (D + 3) - 1  # from -1 to D + 1: held within [0, D]
+    T = torch.tensor([0.0, 1.0, 0.5, 2.0, 1e-31, -1.0, float("nan"), 1e-3], device="cuda").repeat(3)
+    for s in range(0, S, 8):  # greedy ones draft the best, to get anywhere
+        drafts[s, :4] = logits[s, :4].argmax(-1).int()
+    tokens, accepted = check(logits, drafts, u, q, n, T)
+    assert int(accepted.max()) >= 3 and int(accepted.min()) == 0
+    assert bool((tokens.gather(1, accepted.long()[:, None]) >= 0).all())
+
+
+@pytest.mark.parametrize("probs", [True, False])
+def test_every_border_of_a_small_vocabulary(probs):
+    """512 random numbers, evenly spread, for one distribution: each token as often as its weight says, decided as the
+    definition decides."""
+    S, V = 512, 11
+    logits, drafts, u, q = make(1, 1, V, 3, probs=True)
+    logits, q = logits.expand(S, 2, V), q.expand(S, 1, V)
+    drafts = torch.full((S, 1), 4, dtype=torch.int32, device="cuda")
+    u = torch.stack([torch.full((S,), 0.999999, device="cuda"), (torch.arange(S, device="cuda") + 0.37) / S], 1)
+    logits = logits.clone()
+    logits[:, 0, 4] -= 3  # (rejected)
+    tokens, accepted = check(logits, drafts, u, q if probs else None, border=1e-7)
+    assert int(accepted.max()) == 0
+    p = torch.softmax(logits[0, 0].double(), 0)
+    w = (p - q[0, 0].double()).clamp(min=0) if probs else p * (torch.arange(V, device="cuda") != 4)
+    share = torch.bincount(tokens[:, 0], minlength=V).double() / S
+    assert float((share - w / w.sum()).abs().max()) <= 1 / S + 1e-6
+
+
+def test_output_follows_the_target():
+    """Whatever the draft's distribution, the first token out is distributed as the target's: exact over a grid of random numbers."""
+    V, N = 5, 64
+    p = torch.tensor([0.4, 0.3, 0.15, 0.1, 0.05], dtype=torch.float64)
+    q = torch.tensor([0.1, 0.2, 0.3, 0.2, 0.2], dtype=torch.float64)
+    grid = (torch.arange(N, dtype=torch.float64) + 0.5) / N
+    got = torch.zeros(V, dtype=torch.float64)
+    for x in range(V):
+        u = torch.cartesian_prod(grid, grid).float().cuda()
+        S = u.shape[0]
+        logits = p.log().float().cuda().expand(S, 2, V).contiguous()
+        tokens, _ = ll.ll_verify(logits, torch.full((S, 1), x, dtype=torch.int32, device="cuda"), u, probs=q.float().cuda().expand(S, 1, V).contiguous())
+        got += q[x] * torch.bincount(tokens[:, 0].cpu(), minlength=V).double() / S
+    assert float((got - p).abs().max()) <= 2 / N  # (a grid cell of each of the two numbers)
+
+
+def test_special_logits():
+    S, V = 10, 300
+    inf, nan = math.inf, math.nan
+    logits, drafts, u, q = make(S, 2, V, 8)
+    logits[0, 0, 5] = nan                       # never drawn
+    logits[1, 0] = -inf                         # no row at all
+    logits[2, 0] = nan
+    logits[3, 0, 7] = inf                       # takes all
+    drafts[3, 0] = 7
+    logits[4, 0, 9], logits[4, 0, 250] = inf, inf
+    drafts[4, 0] = 10
+    logits[5, 0] = -inf
+    logits[5, 0, 299] = -4.0                    # the only one
+    drafts[6] = torch.tensor([-1, 3])           # drafts that are no tokens
+    drafts[7] = torch.tensor([V, 3])
+    drafts[8, 0] = 2 ** 31 - 1
+    logits[9] = 3e38                            # large, and equal
+    logits[9, :, 100:] = -3e38
+    tokens, accepted = check(logits, drafts, u, q, border=None)
+    assert tokens[1].tolist() == [-1, -1, -1] and tokens[2].tolist() == [-1, -1, -1]
+    assert int(tokens[3, 0]) == 7 and int(tokens[4, 0]) in (9, 250) and int(tokens[5, 0]) == 299 and int(tokens[9, 0]) < 100
+    check(logits, drafts, u, None, border=None)
+    T = torch.zeros(S, device="cuda")
+    tokens, _ = check(logits, drafts, u, q, temperature=T)
+    assert int(tokens[4, 0]) == 9 and int(tokens[9, 0]) == 0  # the lowest of equals
+
+
+def test_draft_distributions_that_take_everything():
+    """q above p everywhere (not a distribution, but fp32 sums may come near that): p is drawn from itself. NaN in q takes nothing away."""
+    logits, drafts, u, q = make(4, 1, 200, 2)
+    u[:, 0] = 0.9999999
+    q[0], q[1] = 1.0, 1e30
+    q[2, 0, ::2] = float("nan")
+    q[2, 0, int(drafts[2])] = 1.0
+    q[3] = 0.0
+    q[3, 0, int(drafts[3])] = 1.0
+    tokens, accepted = ll.ll_verify(logits, drafts, u, probs=q)
+    clean = torch.nan_to_num(q.cpu(), nan=0.0)
+    want = step_ref.verified(logits.cpu(), drafts.cpu(), u.cpu(), clean)
+    assert torch.equal(tokens.cpu(), want[0]) and torch.equal(accepted.cpu(), want[1])
+
+
+def test_draws_at_the_ends():
+    V = 50000
+    logits = torch.full((3, 1, V), -1.0, device="cuda")
+    u = torch.tensor([[0.0], [1 - 2.0 ** -24], [0.5]], device="cuda")
+    tokens, _ = ll.ll_verify(logits, torch.zeros(3, 0, dtype=torch.int32, device="cuda"), u)
+    assert tokens[:, 0].tolist() == [0, V - 1, V // 2]
+    logits[:, :, 0] = -math.inf
+    logits[:, :, V - 1] = -math.inf
+    tokens, _ = ll.ll_verify(logits, torch.zeros(3, 0, dtype=torch.int32, device="cuda"), u)
+    assert tokens[:2, 0].tolist() == [1, V - 2]
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 0), (4, 4), (3, 1), (1, 0)])
+def test_strides(pad, shift):
+    S, D, V = 5, 3, 4099
+    logits, drafts, u, q = make(S, D, V, 11)
+    want = check(logits, drafts, u, q)
+    for dtype in (torch.float32,):
+        ls = torch.full((S, D + 2, V + pad + shift), 1e9, dtype=dtype, device="cuda")
+        qs = torch.full((S, D + 1, V + pad + shift), 1e9, device="cuda")
+        ls[:, :D + 1, shift:shift + V], qs[:, :D, shift:shift + V] = logits, q
+        got = ll.ll_verify(ls[:, :D + 1, shift:shift + V], drafts, u, probs=qs[:, :D, shift:shift + V])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_near_equal_distributions():
+    """A draft that is almost the target: the residual is what is left of numbers that agree to many digits, and every border
+    of it counts. Weights are held to 2^-43."""
+    S, V = 200, 20000
+    g = gen(4)
+    logits = torch.randn(S, 2, V, generator=g, device="cuda")
+    p = torch.softmax(logits[:, 0].double(), -1)
+    q = (p * (1 + 1e-3 * torch.randn(S, V, generator=g, device="cuda", dtype=torch.float64))).float()[:, None].contiguous()
+    # a draft that is rejected: q above p, u near 1
+    drafts = (q[:, 0].double() / p).argmax(-1).int()[:, None].contiguous()
+    u = torch.rand(S, 2, generator=g, device="cuda")
+    u[:, 0] = 0.9999999
+    tokens, accepted = check(logits, drafts, u, q, border=1e-5)
+    assert int(accepted.max()) == 0
+
+
+def test_largest_vocabulary():
+    V = 393216
+    logits, drafts, u, q = make(3, 1, V, 21)
+    check(logits, drafts, u, q)
+    logits[:, :, :V - 5] = -math.inf
+    check(logits, drafts, u, None)

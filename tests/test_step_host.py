@@ -1,0 +1,235 @@
+"""The operators around the attention without a GPU: structures' layout, what the C entries and the binding refuse
+before anything is launched, the rotary tables, and the 64-bit references' own closed forms."""
+import ctypes
+import math
+import os
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from decode_megakernel_persistent_gb300 import build as llbuild
+from decode_megakernel_persistent_gb300 import ll
+import step_ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    llbuild.build()
+    return ll.lib()
+
+
+def test_struct_layouts_match_c(tmp_path):
+    src = tmp_path / "layout.c"
+    src.write_text(r'''
+#include <stdio.h>
+#include <stddef.h>
+#include "ll.h"
+int main(void) {
+  printf("%zu %zu %zu %zu %zu %zu %zu %zu\n", sizeof(ll_qmat), offsetof(ll_qmat, group), sizeof(ll_rows), offsetof(ll_rows, type),
+         offsetof(ll_rows, scale), sizeof(ll_rope_table), offsetof(ll_rope_table, size), offsetof(ll_rope_table, turns));
+  return 0;
+}
+''')
+    exe = tmp_path / "layout"
+    subprocess.check_call(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)])
+    got = [int(v) for v in subprocess.check_output([str(exe)]).split()]
+    assert got == [ctypes.sizeof(ll.ll_qmat), ll.ll_qmat.group.offset, ctypes.sizeof(ll.ll_rows), ll.ll_rows.type.offset, ll.ll_rows.scale.offset,
+                   ctypes.sizeof(ll.ll_rope_table), ll.ll_rope_table.size.offset, ll.ll_rope_table.turns.offset]
+    want = ll.ll_rows(4096, -7, 2, 128, 8192)  # as the binding packs it
+    assert ll._matrix_rows_bytes(4096, -7, 2, 128, 8192) == ctypes.string_at(ctypes.addressof(want), ctypes.sizeof(want))
+
+
+def answer(fn, *args):
+    buf = ctypes.create_string_buffer(200)
+    return fn(*args, None, buf, 200), buf.value.decode()
+
+
+def mat(**k):
+    return ctypes.byref(ll.ll_qmat(**dict(dict(codes=4096, params=8192, rows=64, cols=256, group=64), **k)))
+
+
+def rows(**k):
+    return ctypes.byref(ll.ll_rows(**dict(dict(data=65536, stride=512, type=ll.LL_BF16, group=0, scale=None), **k)))
+
+
+@pytest.mark.parametrize("k,code", [(dict(codes=None), ll.LL_ERR_ARG), (dict(codes=4104), ll.LL_ERR_ARG), (dict(params=None), ll.LL_ERR_ARG),
+                                    (dict(params=8200), ll.LL_ERR_ARG), (dict(group=16), ll.LL_ERR_SHAPE), (dict(group=0), ll.LL_ERR_SHAPE),
+                                    (dict(rows=0), ll.LL_ERR_SHAPE), (dict(cols=-1), ll.LL_ERR_SHAPE), (dict(rows=(1 << 24) + 1), ll.LL_ERR_SHAPE),
+                                    (dict(rows=1 << 24, cols=1 << 24), ll.LL_ERR_SHAPE)])
+def test_matrices_that_are_refused(lib, k, code):
+    for rc, msg in (answer(lib.ll_qmat_write, mat(**k), 65536, 0, 256), answer(lib.ll_qmat_read, mat(**k), 65536, 0, 256),
+                    answer(lib.ll_qmat_mul, mat(**k), rows(), 1, None, rows(data=131072))):
+        assert rc == code and msg
+    assert answer(lib.ll_qmat_mul, None, rows(), 1, None, rows())[0] == ll.LL_ERR_ARG
+
+
+@pytest.mark.parametrize("w,kind,stride", [(None, 0, 256), (65537, 0, 256), (65538, 1, 256), (65536, 2, 256), (65536, 0, 255)])
+def test_dense_matrices_that_are_refused(lib, w, kind, stride):
+    for fn in (lib.ll_qmat_write, lib.ll_qmat_read):
+        rc, msg = answer(fn, mat(), w, kind, stride)
+        assert rc == ll.LL_ERR_ARG and msg
+
+
+def test_products_that_are_refused(lib):
+    def mul(x=None, n=3, add=None, y=None):
+        return answer(lib.ll_qmat_mul, mat(), x or rows(), n, add, y or rows(data=131072))
+    A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
+    for kw, code in ((dict(n=0), A), (dict(n=-1), A), (dict(n=(1 << 19) + 1), S), (dict(x=rows(data=None)), A), (dict(x=rows(data=65537)), A),
+                     (dict(x=rows(data=65538, type=1)), A), (dict(x=rows(type=3)), A), (dict(x=rows(type=2)), A), (dict(x=rows(type=2, scale=4098)), A),
+                     (dict(x=rows(type=2, scale=4096, group=64)), A), (dict(y=rows(type=2, scale=4096)), A), (dict(y=rows(stride=63)), A),
+                     (dict(y=rows(stride=0)), A), (dict(y=rows(data=None)), A), (dict(add=rows(type=1)), A), (dict(add=rows(data=None)), A)):
+        rc, msg = mul(**kw)
+        assert rc == code and msg, kw
+    assert lib.ll_qmat_mul(mat(), rows(), 0, None, rows(), None, None, 0) == A  # (no place for a reason)
+
+
+def test_norms_that_are_refused(lib):
+    def norm(x=None, res=None, res_out=None, gain=4096, eps=1e-5, n=3, width=256, out=None):
+        return answer(lib.ll_rmsnorm, x or rows(), res, res_out, gain, eps, n, width, out or rows(data=131072))
+    A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
+    r = rows(data=1 << 18)
+    for kw, code in ((dict(n=0), A), (dict(width=0), S), (dict(width=32769), S), (dict(eps=-1.0), A), (dict(eps=NAN), A), (dict(eps=INF), A), (dict(gain=None), A),
+                     (dict(gain=4097), A), (dict(x=rows(type=2, scale=4096)), A), (dict(out=rows(type=2)), A), (dict(out=rows(type=2, scale=4096, group=32)), A),
+                     (dict(out=rows(stride=255)), A), (dict(res=r), A), (dict(res_out=r), A), (dict(res=r, res_out=rows(data=1 << 18, type=1)), A),
+                     (dict(res=r, res_out=rows(data=131072)), A), (dict(res=r, res_out=rows(data=1 << 18, stride=3)), A), (dict(x=rows(data=None)), A)):
+        rc, msg = norm(**kw)
+        assert rc == code and msg, kw
+
+
+def kvq_rows(**k):
+    return ctypes.byref(ll.ll_kvq_rows(**dict(dict(data=65536, seq=4096, token=512, head=64), **k)))
+
+
+def plan(lib, hd=64, rot=64, inter=0, theta=1e4, kind=0, factor=1.0, low=0.0, high=0.0, length=0.0):
+    t = ll.ll_rope_table()
+    buf = ctypes.create_string_buffer(200)
+    return lib.ll_rope_plan(ctypes.byref(t), hd, rot, inter, theta, kind, factor, low, high, length, buf, 200), buf.value.decode(), t
+
+
+def test_rotary_plans_that_are_refused(lib):
+    A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
+    for kw, code in ((dict(hd=0), S), (dict(hd=60), S), (dict(hd=264), S), (dict(rot=0), S), (dict(rot=3), S), (dict(rot=66), S), (dict(theta=1.0), A),
+                     (dict(theta=NAN), A), (dict(theta=INF), A), (dict(kind=4), A), (dict(kind=-1), A), (dict(kind=1, factor=0.5), A), (dict(kind=1, factor=INF), A),
+                     (dict(kind=2, factor=8.0, low=1.0, high=1.0, length=100.0), A), (dict(kind=2, factor=8.0, low=0.0, high=1.0, length=100.0), A),
+                     (dict(kind=3, factor=8.0, low=1.0, high=4.0, length=0.0), A), (dict(kind=3, factor=8.0, low=1.0, high=NAN, length=10.0), A)):
+        rc, msg, _ = plan(lib, **kw)
+        assert rc == code and msg, kw
+    assert lib.ll_rope_plan(None, 64, 64, 0, 1e4, 0, 1.0, 0.0, 0.0, 0.0, None, 0) == A
+
+
+@pytest.mark.parametrize("hd,rot,theta", [(64, 64, 1e4), (128, 128, 5e5), (256, 256, 1e6), (96, 40, 1e4), (8, 2, 2.0)])
+@pytest.mark.parametrize("scaling", [None, dict(kind="linear", factor=4.0), dict(kind="bands", factor=32.0, low=1.0, high=4.0, length=8192),
+                                     dict(kind="ramp", factor=16.0, fast=32.0, slow=1.0, length=4096), dict(kind="ramp", factor=2.0, fast=1e9, slow=1e-9, length=64)])
+def test_rotary_tables(lib, hd, rot, theta, scaling):
+    f, size = step_ref.frequencies(rot, theta, scaling)
+    t = ll.Rope(hd, theta, rot, True, scaling).table
+    assert (t.head_dim, t.rot_dims, t.interleaved) == (hd, rot, 1) and t.size == ctypes.c_float(size).value
+    for i in range(128):
+        want = float(f[i]) / (2 * math.pi) * 2.0 ** 64 if i < rot // 2 else 0.0
+        assert abs(t.turns[i] - want) <= max(1.0, want * 2.0 ** -48)  # (pow, logarithms and sums in 64 bits)
+
+
+def test_rotary_calls_that_are_refused(lib):
+    rc, _, t = plan(lib)
+    assert rc == ll.LL_OK
+    A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
+
+    def rope(t=ctypes.byref(t), q=None, qo=None, nq=4, k=None, ko=None, nk=2, kind=0, S=2, n=3, lens=64, n_toks=None):
+        return answer(lib.ll_rope, t, q or kvq_rows(), qo or kvq_rows(), nq, k, ko, nk, kind, S, n, lens, n_toks, 0)
+    bad = ll.ll_rope_table()
+    k = kvq_rows(data=1 << 18)
+    for kw, code in ((dict(t=None), A), (dict(t=ctypes.byref(bad)), A), (dict(q=kvq_rows(data=None)), A), (dict(q=kvq_rows(data=65544)), A),
+                     (dict(qo=kvq_rows(token=4)), A), (dict(qo=kvq_rows(token=0)), A), (dict(nq=0), S), (dict(nq=40000), S), (dict(k=k), A), (dict(ko=k), A),
+                     (dict(k=k, ko=k, nk=0), S), (dict(k=k, ko=kvq_rows()), A), (dict(kind=2), A), (dict(S=0), S), (dict(S=65536), S), (dict(n=0), A),
+                     (dict(lens=None), A), (dict(lens=66), A), (dict(n_toks=65), A)):
+        rc, msg = rope(**kw)
+        assert rc == code and msg, kw
+
+
+def test_verifications_that_are_refused(lib):
+    A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
+
+    def verify(logits=65536, kind=1, draft=64, nd=None, probs=None, u=64, temp=None, S=2, D=3, V=100, tokens=64, accepted=64):
+        return answer(lib.ll_verify, logits, kind, 400, 100, draft, nd, probs, 300, 100, u, temp, S, D, V, tokens, accepted)
+    for kw, code in ((dict(logits=None), A), (dict(logits=65538), A), (dict(logits=65537, kind=0), A), (dict(kind=2), A), (dict(draft=None), A), (dict(draft=65), A),
+                     (dict(nd=66), A), (dict(probs=66), A), (dict(u=None), A), (dict(u=66), A), (dict(temp=66), A), (dict(S=0), S), (dict(S=65536), S), (dict(D=-1), S),
+                     (dict(D=(1 << 20) + 1), S), (dict(V=0), S), (dict(V=393217), S), (dict(tokens=None), A), (dict(accepted=None), A), (dict(accepted=65), A)):
+        rc, msg = verify(**kw)
+        assert rc == code and msg, kw
+
+
+# ---- the binding, with tensors on the CPU ----
+
+def test_binding_refuses_cpu_tensors(lib):
+    z = torch.zeros
+    for call in (lambda: ll.Q4Matrix(z(1, 1, 1024, dtype=torch.uint8), z(1, 1, 1, 16, 2, dtype=torch.float16), 16, 128),
+                 lambda: ll.ll_rmsnorm(z(2, 64), z(64, dtype=torch.bfloat16)), lambda: ll.ll_rmsnorm(z(64), z(64, dtype=torch.bfloat16)),
+                 lambda: ll.Rope(64).apply(z(1, 1, 1, 64), None, z(1, dtype=torch.int32)),
+                 lambda: ll.ll_verify(z(1, 1, 10), None, z(1, 1))):
+        with pytest.raises(ll.LLError) as e:
+            call()
+        assert e.value.code == ll.LL_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(head_dim=60), dict(head_dim=64, rot_dims=65), dict(head_dim=64, theta=0.5), dict(head_dim=64, scaling={"kind": "other"}),
+                                dict(head_dim=64, scaling={"kind": "linear"}), dict(head_dim=64, scaling={"kind": "linear", "factor": 2.0, "low": 1.0}),
+                                dict(head_dim=64, scaling={"kind": "bands", "factor": 2.0, "low": 4.0, "high": 1.0, "length": 100})])
+def test_binding_refuses_rotary_tables(lib, kw):
+    with pytest.raises(ll.LLError):
+        ll.Rope(**kw)
+
+
+# ---- the references ----
+
+def test_reference_pack_is_its_unpack():
+    g = step_ref.gen(1, "cpu")
+    for rows, cols, group in ((1, 1, 32), (17, 130, 64), (40, 512, 128)):
+        code = torch.randint(0, 16, (rows, cols), generator=g)
+        lo, step = torch.randn(2, rows, -(-cols // group), generator=g).half()
+        c, p = step_ref.pack(code, lo, step, group)
+        got = step_ref.unpack(c, p, rows, cols)
+        assert torch.equal(got[0], code.double())
+        assert torch.equal(got[1], lo.double().repeat_interleave(group, 1)[:, :cols]) and torch.equal(got[2], step.double().repeat_interleave(group, 1)[:, :cols])
+
+
+def test_a_word_of_codes_written_out():
+    """Inputs 0..7 of row 0 with codes 0..7: fields of 4 bits in the order 0 2 4 6 1 3 5 7, turned left by 3."""
+    c, _ = step_ref.pack(torch.arange(8)[None], torch.zeros(1, 1), torch.zeros(1, 1), 128)
+    word = 0
+    for f, code in enumerate((0, 2, 4, 6, 1, 3, 5, 7)):
+        word |= code << (4 * f)
+    word = (word << 3 | word >> 29) & 0xFFFFFFFF
+    assert int.from_bytes(bytes(c[0, 0, :4].tolist()), "little") == word
+
+
+def test_reference_verification_closed_forms():
+    log = torch.log
+    p = torch.tensor([0.5, 0.25, 0.125, 0.125], dtype=torch.float64)
+    q = torch.tensor([0.25, 0.5, 0.125, 0.125])
+    logits = log(p).expand(1, 2, 4)
+    one = lambda x, u: step_ref.verified(logits, torch.tensor([[x]]), torch.tensor([u]), q[None, None])[:2]
+    assert one(0, [0.99, 0.6])[0].tolist() == [[0, 1]]  # 0.25 < 0.5 whatever u; the next one from p
+    assert one(1, [0.49, 0.1])[0].tolist() == [[1, 0]]  # 0.49 * 0.5 < 0.25
+    assert one(1, [0.51, 0.9])[0].tolist() == [[0, -1]]  # rejected; the residual is all on 0
+    greedy = step_ref.verified(logits, torch.tensor([[0]]), torch.zeros(1, 2), None, None, torch.zeros(1))
+    assert greedy[0].tolist() == [[0, 0]] and greedy[1].tolist() == [1]
+
+
+def test_reference_rotation_is_a_rotation():
+    x = torch.randn(2, 3, 4, 64, dtype=torch.float64)
+    pos = torch.tensor([[0, 1, 2], [7, 8, 9]])
+    for inter in (False, True):
+        y, _ = step_ref.rotated(x, pos, 64, 1e4, None, inter)
+        assert torch.allclose(y.norm(dim=-1), x.norm(dim=-1)) and torch.equal(y[0, 0], x[0, 0])
+        back, _ = step_ref.rotated(y, pos, 64, 1e4, None, inter, inverse=True)
+        assert torch.allclose(back, x)
+        # scores depend on the distance alone
+        k = x[:1, :1, :1].expand(1, 2, 1, 64)
+        a, _ = step_ref.rotated(k, torch.tensor([[5, 9]]), 64, 1e4, None, inter)
+        b, _ = step_ref.rotated(k, torch.tensor([[105, 109]]), 64, 1e4, None, inter)
+        assert torch.allclose((a[0, 0] * a[0, 1]).sum(), (b[0, 0] * b[0, 1]).sum())
