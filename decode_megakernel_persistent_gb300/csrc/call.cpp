@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
+#include <vector>
 
 namespace ll {
 
@@ -16,6 +17,12 @@ struct Dev {
 constexpr int MAX_DEVICES = 64;
 std::mutex g_dev_mu;
 Dev g_dev[MAX_DEVICES];
+
+struct Allowed {
+    const void *kernel;
+    int dev;
+};
+std::vector<Allowed> g_allowed;  // (a few tens at most)
 
 }  // namespace
 
@@ -75,6 +82,17 @@ int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t wid
         if (!r->scale || reinterpret_cast<uintptr_t>(r->scale) % 4) return report(err, err_len, LL_ERR_ARG, "%s has no scales, or not aligned ones", name);
     }
     return LL_OK;
+}
+
+bool allow_smem(const void *kernel, int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    std::lock_guard<std::mutex> lock(g_dev_mu);
+    for (const Allowed &a : g_allowed)
+        if (a.kernel == kernel && a.dev == dev) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    g_allowed.push_back({kernel, dev});
+    return true;
 }
 
 int finish(int rc, char *err, size_t err_len) {

@@ -29,6 +29,9 @@ int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t wid
 // rc, with CUDA's reason where a launch failed.
 int finish(int rc, char *err, size_t err_len);
 
+// Lets a kernel have `bytes` of dynamic shared memory on the current device, once each.
+bool allow_smem(const void *kernel, int bytes);
+
 // (The error stays for whoever reports it.)
 inline int launched() { return cudaPeekAtLastError() == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
 

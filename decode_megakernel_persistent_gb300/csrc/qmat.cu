@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
     const bool held = r < m.rows;
     float x[4][8];
     float mn[4], mx[4];
+    const bool whole = (K + 1) * QM_TILE_COLS <= m.cols;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const int64_t k = K * QM_TILE_COLS + 32 * j + 8 * t;
@@ -73,13 +74,15 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
 #pragma unroll
             for (int i = 0; i < 8; i++) x[j][i] = 0.f;
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
         mn[j] = INFINITY;
         mx[j] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            // (a NaN stays one: the comparisons are false for it)
-            x[j][i] = x[j][i] > BOUND ? BOUND : x[j][i] < -BOUND ? -BOUND : x[j][i];
-            if (k + i < m.cols) {
+            x[j][i] = min_nan(max_nan(x[j][i], -BOUND), BOUND);
+            if (whole || K * QM_TILE_COLS + 32 * j + 8 * t + i < m.cols) {
                 mn[j] = min_nan(mn[j], x[j][i]);
                 mx[j] = max_nan(mx[j], x[j][i]);
             }
@@ -104,16 +107,20 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
         if (!held || first >= m.cols) lo = hi = 0.f;
         const __half lo_h = __float2half_rn(lo);
         const float base = __half2float(lo_h);
-        const __half step_h = __float2half_rn(__fdiv_rn(hi - base, 15.f));
+        const __half step_h = __float2half_rn(fmaxf(__fdiv_rn(hi - base, 15.f), 0.f));  // (lo may round past the largest)
         const float step = __half2float(step_h);
+        // A quotient by the reciprocal is off by a few units of its last place; corrected once by its residue, which is
+        // exact, it is as near the exact quotient as a division, and borders go as they do there. Step 0: a NaN, code 0.
+        const float inv = 1.f / step;
 #pragma unroll
         for (int j = j0; j < j0 + PER; j++) {
             uint32_t word = 0;
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float q = step > 0.f ? rintf(__fdiv_rn(x[j][i] - base, step)) : 0.f;
-                const uint32_t c = uint32_t(fminf(fmaxf(q, 0.f), 15.f));  // (a NaN: 0; its group's lo is NaN)
-                word |= (first + 32 * (j - j0) + 8 * t + i < m.cols ? c : 0u) << (4 * (i / 2 + 4 * (i % 2)));
+                const float d = x[j][i] - base, q0 = d * inv, q = fmaf(fmaf(-q0, step, d), inv, q0);
+                // (1.5 * 2^23 added: the nearest integer, ties to even, in the lower bits; NaN: 0, as its group's lo is one)
+                const uint32_t c = __float_as_uint(fminf(fmaxf(q, 0.f), 15.f) + 12582912.f) - 0x4b400000u;
+                word += (whole || first + 32 * (j - j0) + 8 * t + i < m.cols ? c : 0u) << (4 * (i / 2 + 4 * (i % 2)));
             }
             words[j] = __funnelshift_l(word, word, 3);
         }
@@ -148,7 +155,11 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_read(ll_qmat m, T *w, int64
         const int64_t k = K * QM_TILE_COLS + 32 * j + 8 * t;
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = fmaf(p[j / PER].y, qm_code(words[j], i), p[j / PER].x);
+        for (int i = 0; i < 4; i++) {
+            const uint32_t c = qm_codes<false>(words[j], i, 0x41804180u);
+            x[2 * i] = fmaf(p[j / PER].y, __uint_as_float(c << 16) - 16.f, p[j / PER].x);
+            x[2 * i + 1] = fmaf(p[j / PER].y, __uint_as_float(c & 0xffff0000u) - 16.f, p[j / PER].x);
+        }
         T *dst = w + r * stride + k;
         if (vec && k + 8 <= m.cols) {
             if constexpr (sizeof(T) == 4) {

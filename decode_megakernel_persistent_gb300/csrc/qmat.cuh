@@ -15,18 +15,14 @@ namespace ll {
 // one logical operation for two codes, beside the shift.
 __device__ __forceinline__ uint32_t qm_turn(uint32_t w, int p) { return p == 0 ? w : p == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * p); }
 
-// The pair (c - 8) of codes 2 p and 2 p + 1, exact in bf16.
+// Codes 2 p and 2 p + 1 as a bf16 pair, c - 8 (EXACT) or 16 + c.
+template <bool EXACT>
 __device__ __forceinline__ uint32_t qm_codes(uint32_t w, int p, uint32_t magic) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(qm_turn(w, p)), "r"(0x00780078u), "r"(magic));  // (a & b) | c
+    if (!EXACT) return r;
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&r), __float2bfloat162_rn(24.f));
     return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Code i of a word as a number.
-__device__ __forceinline__ float qm_code(uint32_t w, int i) {
-    const int f = i / 2 + 4 * (i % 2);
-    return float(__funnelshift_r(w, w, (4 * f + 3) & 31) & 15u);
 }
 
 }  // namespace ll

@@ -18,6 +18,12 @@ namespace {
 
 constexpr int MV_WARPS = 8;
 constexpr int MV_THREADS = 32 * MV_WARPS;
+// Tiles of a warp in flight, and blocks of an SM.
+template <int NT>
+struct MvGeo {
+    static constexpr int UNITS = NT == 1 ? 8 : 6, BLOCKS = NT <= 2 ? 2 : 1;
+};
+constexpr int MV_STAGE = 1024 + 4 * 16 * 4;  // a tile's codes and (4 groups') parameters in shared memory
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -25,11 +31,18 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Streamed past L1: codes are read once.
-__device__ __forceinline__ uint4 ld_codes(const uint4 *p) {
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
     uint4 u;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
     return u;
+}
+__device__ __forceinline__ float2 lds_pair(uint32_t at) {  // (lo, step)
+    uint32_t u;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
@@ -52,6 +65,7 @@ struct MvArgs {
     int64_t y_stride;
     bool y_f32;
     int n;
+    int pg;                 // parameter groups of a tile
     int splits;             // warps that share a row tile's columns, a divisor of MV_WARPS
 };
 
@@ -60,6 +74,7 @@ struct MvArgs {
 template <int XT>
 struct Column {
     static constexpr int TERMS = XT == LL_F32 ? 3 : 1;
+    static constexpr int SIZE = XT == LL_F32 ? 4 : XT == LL_BF16 ? 2 : 1;
     const char *row;
     int term;
     bool held;
@@ -67,72 +82,67 @@ struct Column {
         const int token = first + c / TERMS;
         term = c % TERMS;
         held = token < a.n;
-        constexpr int SIZE = XT == LL_F32 ? 4 : XT == LL_BF16 ? 2 : 1;
         row = static_cast<const char *>(a.x) + int64_t(held ? token : 0) * a.x_stride * SIZE;
     }
-    // The 8 values from column k on as four bf16 pairs.
-    __device__ __forceinline__ void load(const MvArgs &a, int k, uint32_t (&b)[4]) const {
-        if (!held || k >= a.cols) {
-            b[0] = b[1] = b[2] = b[3] = 0;
-            return;
-        }
-        const bool whole = a.vec && k + 8 <= a.cols;
-        if constexpr (XT == LL_BF16) {
-            const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + k;
-            if (whole) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-                b[0] = u.x; b[1] = u.y; b[2] = u.z; b[3] = u.w;
+    // The 8 values from column k on, as they lie in memory.
+    struct Raw {
+        uint32_t w[2 * SIZE];
+    };
+    __device__ __forceinline__ Raw load(const MvArgs &a, int k) const {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < 2 * SIZE; i++) r.w[i] = 0;
+        if (!held || k >= a.cols) return r;
+        const char *p = row + int64_t(k) * SIZE;
+        if (a.vec && k + 8 <= a.cols) {
+            if constexpr (SIZE == 1) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+                r.w[0] = u.x; r.w[1] = u.y;
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t lo = k + 2 * i < a.cols ? p[2 * i] : 0, hi = k + 2 * i + 1 < a.cols ? p[2 * i + 1] : 0;
-                    b[i] = lo | hi << 16;
+                for (int i = 0; i < SIZE / 2; i++) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                    r.w[4 * i] = u.x; r.w[4 * i + 1] = u.y; r.w[4 * i + 2] = u.z; r.w[4 * i + 3] = u.w;
                 }
             }
-        } else if constexpr (XT == LL_F32) {
-            const float *p = reinterpret_cast<const float *>(row) + k;
-            float v[8];
-            if (whole) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(p)), w = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-                v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w; v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
-            } else {
+        } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = k + i < a.cols ? p[i] : 0.f;
+            for (int i = 0; i < 8; i++) {
+                if (k + i >= a.cols) continue;
+                if constexpr (SIZE == 4) r.w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+                else if constexpr (SIZE == 2) r.w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t *>(p)[i]) << (16 * (i % 2));
+                else r.w[i / 4] |= uint32_t(reinterpret_cast<const uint8_t *>(p)[i]) << (8 * (i % 4));
             }
+        }
+        return r;
+    }
+    // The same as four bf16 pairs.
+    __device__ __forceinline__ void pairs(const Raw &r, uint32_t (&b)[4]) const {
+        if constexpr (XT == LL_BF16) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) b[i] = r.w[i];
+        } else if constexpr (XT == LL_F32) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 uint32_t t[2];
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    float r = v[2 * i + e];
-                    float cut = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+                    float v = __uint_as_float(r.w[2 * i + e]);
+                    float cut = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
                     if (term > 0) {
-                        r -= cut;
-                        cut = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+                        v -= cut;
+                        cut = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
                     }
-                    if (term > 1) {
-                        r -= cut;
-                        cut = r;
-                    }
+                    if (term > 1) cut = v - cut;
                     t[e] = __float_as_uint(cut);
                 }
-                b[i] = t[0] >> 16 | (t[1] & 0xffff0000u);
+                b[i] = __byte_perm(t[0], t[1], 0x7632);
             }
         } else {
-            const uint8_t *p = reinterpret_cast<const uint8_t *>(row) + k;
-            uint32_t w[2] = {0, 0};
-            if (whole) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-                w[0] = u.x;
-                w[1] = u.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) w[i / 4] |= (k + i < a.cols ? uint32_t(p[i]) : 0u) << (8 * (i % 4));
-            }
 #pragma unroll
             for (int i = 0; i < 4; i++) {  // (e4m3 is exact in fp16 and in bf16)
                 uint32_t h;
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w[i / 2] >> (16 * (i % 2)))));
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(r.w[i / 2] >> (16 * (i % 2)))));
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                 b[i] = bf16_pair(f.x, f.y);
             }
@@ -140,81 +150,120 @@ struct Column {
     }
 };
 
-// A warp takes R row tiles and the k tiles ks, ks + splits, ... of them, with up to 8 NT columns of x.
-template <int XT, int NT, int R, int PG>
-__global__ void __launch_bounds__(MV_THREADS) k_qmat_mv(const MvArgs a) {
-    constexpr int TERMS = Column<XT>::TERMS, TOKENS = 8 * NT / TERMS;
-    __shared__ float part[MV_WARPS][R * QM_TILE_ROWS][8 * NT + 1];
+// A few rows x: up to 8 NT columns. A warp takes R row tiles at a time and, of `splits` warps that share them, every
+// splits-th tile of 128 columns. Its next tiles are always on their way (cp.async into a ring of its own), across
+// its row tiles, so no latency shows but the first.
+// EXACT: the codes as c - 8 (fp32 y: 1.4e-7 of the outputs' norm off); otherwise as 16 + c, a subtraction a pair
+// less, whose sums are some six times as large, and so are their roundings (bf16 y rounds 2^-9).
+template <int XT, int NT, int R, bool EXACT>
+__global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const MvArgs a) {
+    constexpr int TERMS = Column<XT>::TERMS, TOKENS = 8 * NT / TERMS, UNITS = MvGeo<NT>::UNITS, DEPTH = UNITS / R;
+    extern __shared__ __align__(16) uint8_t ring[];  // [warp][DEPTH][R][MV_STAGE]
+    __shared__ float part[2][MV_WARPS][R * QM_TILE_ROWS][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int ks = warp % a.splits, groups = MV_WARPS / a.splits;
-    const int rt0 = (blockIdx.x * groups + warp / a.splits) * R;
+    const int ks = warp % a.splits, team = warp / a.splits, teams = MV_WARPS / a.splits;
+    const int groups = (a.RT + R - 1) / R, stride = gridDim.x * teams;
     const int first = blockIdx.y * TOKENS;
+    const int own = (a.KT - ks + a.splits - 1) / a.splits;  // (splits <= KT: 1 at least)
+    const uint32_t stages = uint32_t(__cvta_generic_to_shared(ring)) + warp * (UNITS * MV_STAGE);
     uint32_t magic;
     asm volatile("mov.b32 %0, 0x41804180;" : "=r"(magic));
-    float tot[R][NT][4];
-#pragma unroll
-    for (int r = 0; r < R; r++)
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) tot[r][nt][i] = 0.f;
-    if (rt0 < a.RT) {
-        const uint4 *codes[R];
-        const __half2 *params[R];
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            const int64_t tile = int64_t(min(rt0 + r, a.RT - 1)) * a.KT;  // (past the end: a tile twice, its rows not stored)
-            codes[r] = a.codes + tile * 64 + lane;
-            params[r] = a.params + tile * (PG * QM_TILE_ROWS) + g;
-        }
-        for (int kt = ks; kt < a.KT; kt += a.splits) {
-            uint4 c[R][2];
-            __half2 p[R][PG][2];
+    // (teams of a block are gridDim.x groups apart: with fewer groups than teams, blocks have alike many)
+    const int g0 = blockIdx.x + gridDim.x * team;
+
+    int next_group = g0, next_k = 0, next_stage = 0;
+    auto issue = [&]() {
+        if (next_group < groups) {
+            const int kt = ks + next_k * a.splits;
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                c[r][0] = ld_codes(codes[r] + int64_t(kt) * 64);
-                c[r][1] = ld_codes(codes[r] + int64_t(kt) * 64 + 32);
-#pragma unroll
-                for (int s = 0; s < PG; s++) {
-                    p[r][s][0] = __ldg(params[r] + (int64_t(kt) * PG + s) * QM_TILE_ROWS);
-                    p[r][s][1] = __ldg(params[r] + (int64_t(kt) * PG + s) * QM_TILE_ROWS + 8);
-                }
+                const int64_t tile = int64_t(min(next_group * R + r, a.RT - 1)) * a.KT + kt;  // (past the end: a tile twice, its rows not stored)
+                const uint32_t to = stages + (next_stage * R + r) * MV_STAGE;
+                copy16(to + 16 * lane, a.codes + tile * 64 + lane);
+                copy16(to + 512 + 16 * lane, a.codes + tile * 64 + 32 + lane);
+                if (lane < 4 * a.pg) copy16(to + 1024 + 16 * lane, reinterpret_cast<const uint4 *>(a.params) + tile * (4 * a.pg) + lane);
             }
+            if (++next_k == own) {
+                next_k = 0;
+                next_group += stride;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next_stage = next_stage + 1 == DEPTH ? 0 : next_stage + 1;
+    };
 #pragma unroll
-            for (int s = 0; s < PG; s++) {
-                float acc[R][NT][4], ones[NT][4];
+    for (int i = 0; i < DEPTH - 1; i++) issue();
+
+    int stage = 0, parity = 0;
+    typename Column<XT>::Raw ahead[NT][4];  // x of the next tile
+    auto load_x = [&](int kt) {
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
+        for (int nt = 0; nt < NT; nt++) {
+            const Column<XT> col(a, nt * 8 + g, first);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) ones[nt][i] = 0.f;
+            for (int j = 0; j < 4; j++) ahead[nt][j] = col.load(a, kt * QM_TILE_COLS + 32 * j + 8 * t);
+        }
+    };
+    constexpr bool AHEAD = NT == 1 && XT != LL_F32;  // (registers)
+    if (AHEAD && g0 < groups) load_x(ks);
+    for (int group = g0; group < groups; group += stride) {
+        float tot[R][NT][4];
 #pragma unroll
-                    for (int r = 0; r < R; r++)
+        for (int r = 0; r < R; r++)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) acc[r][nt][i] = 0.f;
-                }
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int jj = 0; jj < 4 / PG; jj++) {
-                    const int j = s * (4 / PG) + jj;
-                    uint32_t b[NT][4];
+                for (int i = 0; i < 4; i++) tot[r][nt][i] = 0.f;
+        for (int k = 0; k < own; k++) {
+            const int kt = ks + k * a.splits;
+            uint32_t b[NT][4][4];
+            if (!AHEAD) load_x(kt);
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        const Column<XT> col(a, nt * 8 + g, first);
-                        col.load(a, kt * QM_TILE_COLS + 32 * j + 8 * t, b[nt]);
-                    }
+            for (int nt = 0; nt < NT; nt++) {
+                const Column<XT> col(a, nt * 8 + g, first);
 #pragma unroll
-                    for (int m = 0; m < 2; m++) {
+                for (int j = 0; j < 4; j++) col.pairs(ahead[nt][j], b[nt][j]);
+            }
+            if (AHEAD) load_x(k + 1 < own ? kt + a.splits : ks);
+            issue();
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+            __syncwarp();  // (parameters come by other lanes' copies)
+            uint4 c[R][2];
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++) mma_bf16(ones[nt], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, b[nt][2 * m], b[nt][2 * m + 1]);
+            for (int r = 0; r < R; r++) {
+                c[r][0] = lds16(stages + (stage * R + r) * MV_STAGE + 16 * lane);
+                c[r][1] = lds16(stages + (stage * R + r) * MV_STAGE + 512 + 16 * lane);
+            }
+            float acc[R][NT][4], ones[NT][4];
 #pragma unroll
-                        for (int r = 0; r < R; r++) {
-                            const uint32_t lo = (&c[r][0].x)[j], hi = (&c[r][1].x)[j];
-                            const uint32_t a0 = qm_codes(lo, 2 * m, magic), a1 = qm_codes(hi, 2 * m, magic);
-                            const uint32_t a2 = qm_codes(lo, 2 * m + 1, magic), a3 = qm_codes(hi, 2 * m + 1, magic);
+            for (int j = 0; j < 4; j++) {
+                if (j == 0 || (j * a.pg) % 4 == 0) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; nt++) mma_bf16(acc[r][nt], a0, a1, a2, a3, b[nt][2 * m], b[nt][2 * m + 1]);
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            ones[nt][i] = 0.f;
+#pragma unroll
+                            for (int r = 0; r < R; r++) acc[r][nt][i] = 0.f;
                         }
+                }
+#pragma unroll
+                for (int m = 0; m < 2; m++) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        mma_bf16(ones[nt], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+#pragma unroll
+                    for (int r = 0; r < R; r++) {
+                        const uint32_t lo = (&c[r][0].x)[j], hi = (&c[r][1].x)[j];
+                        const uint32_t a0 = qm_codes<EXACT>(lo, 2 * m, magic), a1 = qm_codes<EXACT>(hi, 2 * m, magic);
+                        const uint32_t a2 = qm_codes<EXACT>(lo, 2 * m + 1, magic), a3 = qm_codes<EXACT>(hi, 2 * m + 1, magic);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) mma_bf16(acc[r][nt], a0, a1, a2, a3, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
                     }
                 }
+                if (((j + 1) * a.pg) % 4 != 0) continue;
+                // the group's end: its sums meet their parameters
+                const int s = j * a.pg / 4;
                 float sc[NT][2];
                 if constexpr (XT == LL_E4M3) {
 #pragma unroll
@@ -227,8 +276,10 @@ __global__ void __launch_bounds__(MV_THREADS) k_qmat_mv(const MvArgs a) {
                 }
 #pragma unroll
                 for (int r = 0; r < R; r++) {
-                    const float2 p0 = __half22float2(p[r][s][0]), p1 = __half22float2(p[r][s][1]);
-                    const float z0 = fmaf(8.f, p0.y, p0.x), z1 = fmaf(8.f, p1.y, p1.x);
+                    const uint32_t at = stages + (stage * R + r) * MV_STAGE + 1024 + (s * QM_TILE_ROWS + g) * 4;
+                    const float2 p0 = lds_pair(at), p1 = lds_pair(at + 32);
+                    constexpr float ZERO = EXACT ? 8.f : -16.f;
+                    const float z0 = fmaf(ZERO, p0.y, p0.x), z1 = fmaf(ZERO, p1.y, p1.x);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -241,56 +292,74 @@ __global__ void __launch_bounds__(MV_THREADS) k_qmat_mv(const MvArgs a) {
                         }
                 }
             }
+            __syncwarp();  // (before another lane's copy into this stage)
+            stage = stage + 1 == DEPTH ? 0 : stage + 1;
         }
-    }
+        // the splits' shares and an fp32 token's terms added up
 #pragma unroll
-    for (int r = 0; r < R; r++)
+        for (int r = 0; r < R; r++)
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) part[warp][r * QM_TILE_ROWS + g + 8 * (i / 2)][nt * 8 + 2 * t + (i & 1)] = tot[r][nt][i];
-    __syncthreads();
-    // the splits' shares and an fp32 token's terms added up
-    constexpr int ROWS = R * QM_TILE_ROWS;
-    for (int e = threadIdx.x; e < groups * ROWS * TOKENS; e += MV_THREADS) {
-        const int in = e % (groups * ROWS), token = e / (groups * ROWS), grp = in / ROWS;
-        const int64_t row = int64_t(blockIdx.x) * groups * ROWS + in;
-        if (row >= a.rows || first + token >= a.n) continue;
-        float y = 0.f;
-        for (int s = 0; s < a.splits; s++)
+                for (int i = 0; i < 4; i++) part[parity][warp][r * QM_TILE_ROWS + g + 8 * (i / 2)][nt * 8 + 2 * t + (i & 1)] = tot[r][nt][i];
+        // (the shares of the group before last lie in the other half: one barrier a group)
+        if (a.splits == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * a.splits) : "memory");
+        constexpr int ROWS = R * QM_TILE_ROWS;
+        for (int e = ks * 32 + lane; e < ROWS * TOKENS; e += 32 * a.splits) {
+            const int in = e % ROWS, token = e / ROWS;
+            const int64_t row = int64_t(group) * ROWS + in;
+            if (row >= a.rows || first + token >= a.n) continue;
+            float y = 0.f;
+            for (int s = 0; s < a.splits; s++)
 #pragma unroll
-            for (int u = TERMS - 1; u >= 0; u--) y += part[grp * a.splits + s][in % ROWS][token * TERMS + u];
-        const int64_t at = int64_t(first + token) * a.y_stride + row, from = int64_t(first + token) * a.add_stride + row;
-        if (a.y_f32) {
-            if (a.add) y += static_cast<const float *>(a.add)[from];
-            static_cast<float *>(a.y)[at] = y;
-        } else {
-            if (a.add) y += __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[from]);
-            static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(y);
+                for (int u = TERMS - 1; u >= 0; u--) y += part[parity][team * a.splits + s][in][token * TERMS + u];
+            const int64_t at = int64_t(first + token) * a.y_stride + row, from = int64_t(first + token) * a.add_stride + row;
+            if (a.y_f32) {
+                if (a.add) y += static_cast<const float *>(a.add)[from];
+                static_cast<float *>(a.y)[at] = y;
+            } else {
+                if (a.add) y += __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[from]);
+                static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(y);
+            }
         }
+        parity ^= 1;
     }
 }
 
-template <int XT, int NT, int R>
-void launch_mv(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
-    constexpr int TOKENS = 8 * NT / Column<XT>::TERMS;
+template <int XT, int NT, int R, bool EXACT>
+int launch_mv(const MvArgs &a, int nsm, cudaStream_t st) {
+    constexpr int TOKENS = 8 * NT / Column<XT>::TERMS, SMEM = MV_WARPS * MvGeo<NT>::UNITS * MV_STAGE;
+    if (!allow_smem(reinterpret_cast<const void *>(k_qmat_mv<XT, NT, R, EXACT>), SMEM)) return LL_ERR_CUDA;
     MvArgs b = a;
-    const int tiles = (a.RT + R - 1) / R;
-    b.splits = 1;
-    while (b.splits < MV_WARPS && int64_t(tiles) * b.splits < int64_t(nsm) * 16 && 2 * b.splits <= a.KT) b.splits *= 2;
-    const int groups = MV_WARPS / b.splits;
-    const dim3 grid((tiles + groups - 1) / groups, (a.n + TOKENS - 1) / TOKENS);
-    if (pg == 1) k_qmat_mv<XT, NT, R, 1><<<grid, MV_THREADS, 0, st>>>(b);
-    else if (pg == 2) k_qmat_mv<XT, NT, R, 2><<<grid, MV_THREADS, 0, st>>>(b);
-    else k_qmat_mv<XT, NT, R, 4><<<grid, MV_THREADS, 0, st>>>(b);
+    // splits by the steps of the busiest warp: its tiles, and 2 a group for the shares' barrier
+    const int tiles = (a.RT + R - 1) / R, blocks = MvGeo<NT>::BLOCKS * nsm;
+    int64_t best = INT64_MAX;
+    for (int splits = 1; splits <= MV_WARPS && splits <= a.KT; splits *= 2) {
+        const int64_t slots = int64_t(blocks) * (MV_WARPS / splits), rounds = (tiles + slots - 1) / slots;
+        const int64_t steps = rounds * ((a.KT + splits - 1) / splits * R + (splits > 1 ? 2 : 1));
+        if (steps < best) {
+            best = steps;
+            b.splits = splits;
+        }
+    }
+    // (fewer groups than slots: one a block before two in one)
+    const dim3 grid(tiles < blocks ? tiles : blocks, (a.n + TOKENS - 1) / TOKENS);
+    k_qmat_mv<XT, NT, R, EXACT><<<grid, MV_THREADS, SMEM, st>>>(b);
+    return launched();
 }
 
 template <int XT>
-void launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
+int launch_mv_type(const MvArgs &a, int nsm, cudaStream_t st) {
     const int columns = a.n * Column<XT>::TERMS;
-    if (columns <= 8) launch_mv<XT, 1, 2>(a, pg, nsm, st);
-    else if (columns <= 16) launch_mv<XT, 2, 2>(a, pg, nsm, st);
-    else launch_mv<XT, 4, 1>(a, pg, nsm, st);
+    // two row tiles a warp share x's fragments; one where that leaves SMs without any
+    const bool two = a.RT >= 4 * nsm;
+    if (a.y_f32) {
+        if (columns <= 8) return two ? launch_mv<XT, 1, 2, true>(a, nsm, st) : launch_mv<XT, 1, 1, true>(a, nsm, st);
+        return columns <= 16 ? launch_mv<XT, 2, 2, true>(a, nsm, st) : launch_mv<XT, 4, 1, true>(a, nsm, st);
+    }
+    if (columns <= 8) return two ? launch_mv<XT, 1, 2, false>(a, nsm, st) : launch_mv<XT, 1, 1, false>(a, nsm, st);
+    return columns <= 16 ? launch_mv<XT, 2, 2, false>(a, nsm, st) : launch_mv<XT, 4, 1, false>(a, nsm, st);
 }
 
 }  // namespace
@@ -316,11 +385,8 @@ int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *ad
     a.y_stride = y.stride;
     a.y_f32 = y.type == LL_F32;
     a.n = n;
-    const int pg = QM_TILE_COLS / m.group;
-    if (x.type == LL_BF16) launch_mv_type<LL_BF16>(a, pg, nsm, st);
-    else if (x.type == LL_F32) launch_mv_type<LL_F32>(a, pg, nsm, st);
-    else launch_mv_type<LL_E4M3>(a, pg, nsm, st);
-    return launched();
+    a.pg = QM_TILE_COLS / m.group;
+    return x.type == LL_BF16 ? launch_mv_type<LL_BF16>(a, nsm, st) : x.type == LL_F32 ? launch_mv_type<LL_F32>(a, nsm, st) : launch_mv_type<LL_E4M3>(a, nsm, st);
 }
 
 }  // namespace ll

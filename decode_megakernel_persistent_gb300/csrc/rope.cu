@@ -9,6 +9,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "call.h"
@@ -27,12 +28,29 @@ struct RopeArgs {
     KvqLens l;
     int units;                  // of 8 pairs, or (behind them) of 16 values that are copied
     int pair_units, slots, tokens;  // slots: threads that share a token's unit, by heads; tokens of a block
-    bool vec, inverse;
+    bool inverse;
 };
 
-// A thread has one unit of one token, its 8 angles in registers, and every slots-th head.
+// 8 values as they lie in memory.
 template <typename T>
+struct Unit {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); i++) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            x[i] = sizeof(T) == 4 ? __uint_as_float(u[i]) : __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+};
+
+// A thread has one unit of one token, its 8 angles in registers, and every slots-th head, BATCH of them on their way at once.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a) {
+    constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;
     const int u = threadIdx.x % a.units, slot = threadIdx.x / a.units % a.slots, in = threadIdx.x / (a.units * a.slots);
     const int s = blockIdx.y, j = blockIdx.x * a.tokens + in;
     if (in >= a.tokens) return;
@@ -40,73 +58,84 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
     const int64_t pos = int64_t(a.l.len(s)) - n + j;
     if (j >= n || pos < 0) return;
     const int rot = a.t.rot_dims, half = rot / 2;
-    const bool turned = u < a.pair_units;
-    float c[8], sn[8];
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int p = min(8 * u + i, half - 1);
-            const uint64_t turns = uint64_t(pos) * a.t.turns[p];
-            sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &sn[i], &c[i]);
-            c[i] *= a.t.size;
-            sn[i] *= a.inverse ? -a.t.size : a.t.size;
-        }
-    }
-    for (int h = slot; h < a.heads; h += a.slots) {
-        const int which = h >= a.nq, head = which ? h - a.nq : h;
-        const ll_kvq_rows &from = a.in[which], &to = a.out[which];
-        const T *x = static_cast<const T *>(from.data) + s * from.seq + j * from.token + head * from.head;
-        T *y = static_cast<T *>(to.data) + s * to.seq + j * to.token + head * to.head;
-        if (!turned) {  // values behind the turned ones
-            const int d0 = rot + 16 * (u - a.pair_units), d1 = min(d0 + 16, a.t.head_dim);
+    auto row = [&](const ll_kvq_rows (&rows)[2], int h) {
+        const int which = h >= a.nq;
+        return static_cast<T *>(rows[which].data) + s * rows[which].seq + j * rows[which].token + (which ? h - a.nq : h) * rows[which].head;
+    };
+    if (u >= a.pair_units) {  // values behind the turned ones
+        const int d0 = rot + 16 * (u - a.pair_units), d1 = min(d0 + 16, a.t.head_dim);
+        for (int h = slot; h < a.heads; h += a.slots) {
+            const T *x = row(a.in, h);
+            T *y = row(a.out, h);
             for (int d = d0; d < d1; d++) y[d] = x[d];
-            continue;
         }
-        float p[8], q[8], v[8], w[8];
-        if (a.vec && !a.t.interleaved) {
-            load8(x, 8 * u, half, true, p);
-            load8(x + half, 8 * u, half, true, q);
-        } else if (a.vec) {
-            load8(x, 16 * u, rot, true, v);
-            load8(x, 16 * u + 8, rot, true, w);
+        return;
+    }
+    float c[8], sn[8];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                p[i] = v[2 * i]; q[i] = v[2 * i + 1];
-                p[4 + i] = w[2 * i]; q[4 + i] = w[2 * i + 1];
+    for (int i = 0; i < 8; i++) {
+        const uint64_t turns = uint64_t(pos) * a.t.turns[min(8 * u + i, half - 1)];
+        sincospif(float(int32_t(turns >> 32)) * 0x1p-31f, &sn[i], &c[i]);
+        c[i] *= a.t.size;
+        sn[i] *= a.inverse ? -a.t.size : a.t.size;
+    }
+    if constexpr (VEC) {
+        const int at0 = a.t.interleaved ? 16 * u : 8 * u, at1 = a.t.interleaved ? 16 * u + 8 : half + 8 * u;
+        for (int h0 = slot; h0 < a.heads; h0 += BATCH * a.slots) {
+            Unit<T> r0[BATCH], r1[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; i++) {
+                const int h = h0 + i * a.slots;
+                if (h >= a.heads) break;
+                const T *x = row(a.in, h);
+                r0[i].load(x + at0);
+                r1[i].load(x + at1);
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const int k = min(8 * u + i, half - 1);
-                p[i] = float(x[a.t.interleaved ? 2 * k : k]);
-                q[i] = float(x[a.t.interleaved ? 2 * k + 1 : half + k]);
+            for (int i = 0; i < BATCH; i++) {
+                const int h = h0 + i * a.slots;
+                if (h >= a.heads) break;
+                T *y = row(a.out, h);
+                float p[8], q[8], v[8], w[8];
+                r0[i].get(v);
+                r1[i].get(w);
+                if (a.t.interleaved) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        p[e] = v[2 * e] * c[e] - v[2 * e + 1] * sn[e];
+                        q[e] = v[2 * e + 1] * c[e] + v[2 * e] * sn[e];
+                        p[4 + e] = w[2 * e] * c[4 + e] - w[2 * e + 1] * sn[4 + e];
+                        q[4 + e] = w[2 * e + 1] * c[4 + e] + w[2 * e] * sn[4 + e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        v[2 * e] = p[e]; v[2 * e + 1] = q[e];
+                        w[2 * e] = p[4 + e]; w[2 * e + 1] = q[4 + e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        p[e] = v[e] * c[e] - w[e] * sn[e];
+                        w[e] = w[e] * c[e] + v[e] * sn[e];
+                        v[e] = p[e];
+                    }
+                }
+                store8(y, at0, at0 + 8, true, v);
+                store8(y, at1, at1 + 8, true, w);
             }
         }
-        float e[8], f[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            e[i] = p[i] * c[i] - q[i] * sn[i];
-            f[i] = q[i] * c[i] + p[i] * sn[i];
-        }
-        if (a.vec && !a.t.interleaved) {
-            store8(y, 8 * u, half, true, e);
-            store8(y + half, 8 * u, half, true, f);
-        } else if (a.vec) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                v[2 * i] = e[i]; v[2 * i + 1] = f[i];
-                w[2 * i] = e[4 + i]; w[2 * i + 1] = f[4 + i];
-            }
-            store8(y, 16 * u, rot, true, v);
-            store8(y, 16 * u + 8, rot, true, w);
-        } else {
+    } else {  // units that are not whole or not on 16-byte borders
+        for (int h = slot; h < a.heads; h += a.slots) {
+            const T *x = row(a.in, h);
+            T *y = row(a.out, h);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const int k = 8 * u + i;
-                if (k < half) {
-                    y[a.t.interleaved ? 2 * k : k] = T(e[i]);
-                    y[a.t.interleaved ? 2 * k + 1 : half + k] = T(f[i]);
-                }
+                if (k >= half) break;
+                const int d0 = a.t.interleaved ? 2 * k : k, d1 = a.t.interleaved ? 2 * k + 1 : half + k;
+                const float p = float(x[d0]), q = float(x[d1]);
+                y[d0] = T(p * c[i] - q * sn[i]);
+                y[d1] = T(q * c[i] + p * sn[i]);
             }
         }
     }
@@ -115,7 +144,7 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
 }  // namespace
 
 int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows &q_out, int nq, const ll_kvq_rows *k, const ll_kvq_rows *k_out,
-                int nk, int type, int n_seq, const KvqLens &l, bool inverse, cudaStream_t st) {
+                int nk, int type, int n_seq, const KvqLens &l, bool inverse, int nsm, cudaStream_t st) {
     RopeArgs a = {};
     a.t = t;
     a.in[0] = q;
@@ -129,15 +158,20 @@ int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows 
     a.l = l;
     a.pair_units = (t.rot_dims / 2 + 7) / 8;
     // units of pairs are whole, and their second halves on 16-byte borders
-    a.vec = t.interleaved ? t.rot_dims % 16 == 0 : t.rot_dims / 2 % 8 == 0;
+    const bool vec = t.interleaved ? t.rot_dims % 16 == 0 : t.rot_dims / 2 % 8 == 0;
     const bool same = q.data == q_out.data && (!k || k->data == k_out->data);
     a.units = a.pair_units + (same ? 0 : (t.head_dim - t.rot_dims + 15) / 16);
-    const int most = ROPE_THREADS / a.units;  // (16 units at most: 256 dims)
-    a.slots = a.heads < most ? a.heads : most;
+    // Heads of a thread: its angles cost as much as three or four heads' turning, so as many heads as leave the SMs full,
+    // 8 at most. (A prompt of 8192 tokens of 40 heads of 128 dims: HEADS_TABLE.)
+    const int64_t items = int64_t(n_seq) * l.n_tok * a.units * a.heads;
+    const int per = int(std::min<int64_t>(8, std::max<int64_t>(1, items / (int64_t(nsm) * 1024))));
+    const int most = ROPE_THREADS / a.units;  // (17 units at most)
+    a.slots = std::min((a.heads + per - 1) / per, most);
     a.tokens = most / a.slots;
     a.inverse = inverse;
     const dim3 grid((l.n_tok + a.tokens - 1) / a.tokens, n_seq);
-    type == LL_F32 ? k_rope<float><<<grid, ROPE_THREADS, 0, st>>>(a) : k_rope<__nv_bfloat16><<<grid, ROPE_THREADS, 0, st>>>(a);
+    if (type == LL_F32) vec ? k_rope<float, true><<<grid, ROPE_THREADS, 0, st>>>(a) : k_rope<float, false><<<grid, ROPE_THREADS, 0, st>>>(a);
+    else vec ? k_rope<__nv_bfloat16, true><<<grid, ROPE_THREADS, 0, st>>>(a) : k_rope<__nv_bfloat16, false><<<grid, ROPE_THREADS, 0, st>>>(a);
     return launched();
 }
 
@@ -213,7 +247,7 @@ int ll_rope(const ll_rope_table *r, const ll_kvq_rows *q, const ll_kvq_rows *q_o
     int nsm = 0;
     if (int rc = ll::check_device(nsm, err, err_len)) return rc;
     const ll::KvqLens l = {len_dev, n_tok_dev, 0, n_tok};
-    return ll::finish(ll::launch_rope(*r, *q, *q_out, n_q_heads, k, k_out, n_k_heads, type, n_seq, l, inverse != 0, static_cast<cudaStream_t>(stream)),
+    return ll::finish(ll::launch_rope(*r, *q, *q_out, n_q_heads, k, k_out, n_k_heads, type, n_seq, l, inverse != 0, nsm, static_cast<cudaStream_t>(stream)),
                       err, err_len);
 }
 

@@ -15,7 +15,7 @@ struct e4m3 {
 int launch_rmsnorm(const ll_rows &x, const ll_rows *res, const ll_rows *res_out, const uint16_t *gain, float eps, int n, int width,
                    const ll_rows &out, cudaStream_t st);
 int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows &q_out, int nq, const ll_kvq_rows *k, const ll_kvq_rows *k_out,
-                int nk, int type, int n_seq, const KvqLens &l, bool inverse, cudaStream_t st);
+                int nk, int type, int n_seq, const KvqLens &l, bool inverse, int nsm, cudaStream_t st);
 
 #ifdef __CUDACC__
 template <typename T>

@@ -436,7 +436,7 @@ typedef struct {
 
 /* Quantise a matrix w (type LL_BF16 or LL_F32, row r from w + r * stride elements on;
  * any alignment of its type) into m: over a group's values x, each clamped to +-60000,
- * lo = fp16(min x), step = fp16((max x - lo) / 15), code = the integer nearest to
+ * lo = fp16(min x), step = fp16(max(max x - lo, 0) / 15), code = the integer nearest to
  * (x - lo) / step, ties to even, clamped to [0, 15], 0 where step is 0. A group holding a
  * NaN reads back as NaN. */
 int ll_qmat_write(const ll_qmat *m, const void *w, int32_t type, int64_t stride, void *stream, char *err, size_t err_len);

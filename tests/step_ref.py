@@ -63,7 +63,7 @@ def quantised(w, group):
     for a in range(0, w.shape[1], group):
         x = w[:, a:a + group]
         lo = x.amin(1, keepdim=True).half().double()
-        step = ((x.amax(1, keepdim=True) - lo).float() / 15).half().double()
+        step = ((x.amax(1, keepdim=True) - lo).clamp(min=0).float() / 15).half().double()  # (lo may round past the largest)
         z = (x - lo) / torch.where(step > 0, step, 1.0)
         out[:, a:a + group] = lo + step * torch.where(step > 0, z.round().clamp(0, 15), 0.0)
         steps[:, a:a + group] = step
