@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_read(ll_qmat m, T *w, int64
         float x[8];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const uint32_t c = qm_codes<false>(words[j], i, 0x41804180u);
+            const uint32_t c = qm_codes<false, false>(words[j], i, 0x41804180u);
             x[2 * i] = fmaf(p[j / PER].y, __uint_as_float(c << 16) - 16.f, p[j / PER].x);
             x[2 * i + 1] = fmaf(p[j / PER].y, __uint_as_float(c & 0xffff0000u) - 16.f, p[j / PER].x);
         }
