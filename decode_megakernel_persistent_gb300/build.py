@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libll.so")
 SOURCES = ("mk_cuda_cores.cu", "mk_tensor_cores.cu", "mk_geo.cu", "chain.cu", "schedule.cpp", "api.cpp",
-           "static_step.cu", "prefill.cu", "kvq.cu", "kvq_attn.cu", "kvq_prompt.cu", "call.cpp", "qmat.cu", "qmat_mul.cu",
+           "static_step.cu", "prefill.cu", "kvq.cu", "kvq_attn.cu", "kvq_prompt.cu", "call.cpp", "qmat.cu", "qmat_mul.cu", "qmat_tc.cu",
            "rmsnorm.cu", "rope.cu", "verify.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

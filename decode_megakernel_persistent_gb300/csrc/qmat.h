@@ -17,6 +17,9 @@ int launch_qmat_read(const ll_qmat &m, void *w, int type, int64_t stride, cudaSt
 // add: null for none.
 int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st);
 
+// The same on tcgen05 (qmat_tc.cu); LL_ERR_SHAPE where x does not fit into shared memory (nothing was launched).
+int launch_qmat_tc(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st);
+
 // The matrix's own checks (shape, pointers): LL_OK, or the code with a reason in msg.
 int qmat_check(const ll_qmat *m, const char *&msg);
 

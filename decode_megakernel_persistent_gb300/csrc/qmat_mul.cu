@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "call.h"
 #include "qmat.cuh"
@@ -357,6 +358,11 @@ int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
 }  // namespace
 
 int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st) {
+    static const char *force = getenv("QM_TC");
+    if (force && atoi(force)) {
+        const int rc = launch_qmat_tc(m, x, n, add, y, nsm, st);
+        if (rc != LL_ERR_SHAPE) return rc;
+    }
     MvArgs a = {};
     a.codes = reinterpret_cast<const uint4 *>(m.codes);
     a.params = reinterpret_cast<const uint4 *>(m.params);

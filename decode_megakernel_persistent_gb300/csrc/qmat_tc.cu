@@ -1,0 +1,695 @@
+// qmat_tc.cu -- y = x W^T (+ add) with W in 4 bits on the fifth-generation tensor cores: many rows x, or large
+// matrices (qmat_mul.cu has the other kernel, and the rule).
+//
+//   y[i][r] = sum over groups G of  step (sum_k c x) + lo (sum_k x),   k in G
+//
+// A code c needs no arithmetic to become an operand: the bits 0000cccc, read as an e4m3 number, are c / 512 (up to 7 a
+// subnormal, from 8 on a normal one), so unpacking is a shift and a mask for four codes. x enters as e4m3 too: as it
+// is; or bf16 as two terms (hi, and 32 times what is left of it), fp32 as four, of 4 bits and a sign each, scaled by a
+// power of two for a row and 128 columns. Two terms hold bf16's 8 bits exactly down to 2^-14 of the largest of the
+// 128 (what is lost below is 2^-22 of it at most), four hold 20 bits of fp32. Products are exact, sums fp32; lo, step and
+// the scales meet them in fp32, once a group.
+//
+// A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Eight warps, in two sets that
+// take units in turn, unpack 32 rows each from a ring of their own (cp.async) into tensor memory, the products' A operand,
+// a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products of a group into one
+// of several sums in tensor memory; four warps, a row to a thread, take them from there and join them in registers with
+// the group's parameters. Blocks of a cluster share the columns: each row's shares then meet through shared memory.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "call.h"
+#include "kvq_attn.cuh"
+#include "qmat.h"
+
+namespace ll {
+namespace {
+
+struct TcArgs {
+    const uint4 *codes;
+    const uint4 *params;    // (lo, step), 4 rows to 16 bytes
+    int rows, cols, KT, RT;
+    const void *x;
+    int64_t x_stride;
+    int x_type;
+    const float *scale;     // e4m3: [n][scale_row], the tile's or (scale_step 0) the row's
+    int scale_row, scale_step;
+    bool vec;               // x's rows take 8-value loads
+    const void *add;
+    int64_t add_stride;
+    void *y;
+    int64_t y_stride;
+    bool y_f32;
+    int n;
+    KvqWaits waits;
+    // the plan
+    int terms, tokens;      // columns of x's operand a token takes, tokens of a pass over the matrix
+    int cluster, slice;     // blocks that share the columns, tiles of a block
+    int depth;              // units of a warp in flight
+};
+
+constexpr int UNPACK = 8, FLUSH = 4, W_MMA = UNPACK + FLUSH, THREADS = 32 * (W_MMA + 1);
+constexpr int SA = 8;                     // A stages, 32 columns of tensor memory each
+constexpr int MAX_SMEM = 232448 - 2048, MAX_CLUSTER = 8;
+
+// What a block keeps of x, by bytes from `base` on (a 1,024-byte border):
+//   operand  [slice][N][128]      K-major rows of a tile's columns, in the 128-byte swizzle
+//   scale    [slice][NC] floats   of a tile's column
+//   sum      [slice][PG][NC]      of a group's x (in the column of its first term)
+template <int NC, int PG>
+struct XSlice {
+    static constexpr int N = NC < 16 ? 16 : NC;  // columns of a product: 16 at least
+    uint32_t operand, scale, sum;
+    __device__ __forceinline__ XSlice(uint32_t base, int slice) {
+        operand = base;
+        scale = operand + slice * N * 128;
+        sum = scale + slice * NC * 4;
+    }
+    static __host__ __device__ int bytes(int slice) { return slice * (N * 128 + NC * 4 * (1 + PG)); }
+};
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+// Until all but the last n groups of copies have landed.
+__device__ __forceinline__ void wait_copies(int n) {
+    switch (n) {
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+    return u;
+}
+__device__ __forceinline__ ulonglong2 lds_two_pairs(uint32_t at) {
+    ulonglong2 u;
+    asm volatile("ld.shared.v2.u64 {%0,%1}, [%2];" : "=l"(u.x), "=l"(u.y) : "r"(at) : "memory");
+    return u;
+}
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+__device__ __forceinline__ float2 from_e4m3(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(two)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Shared-memory descriptor of a K-major tile in the 128-byte swizzle (rows of 128 bytes, 8-row groups 1,024 bytes apart).
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1u) << 16 | uint64_t(1024u >> 4) << 32 | uint64_t(1u) << 46 | uint64_t(2u) << 61;
+}
+// kind::f8f6f4: e4m3 A and B, fp32 sums, M = 128.
+template <int N>
+constexpr uint32_t IDESC = (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+// (by a whole warp, of which one elected lane, the same at every call, carries it out)
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {  // arrives once all products issued so far are done
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Bounded wait: once the limit passes, with *err set, or once another's has, the block goes on without waits to its
+// end, as if all had come: its loops and whole-warp instructions stay together, and its outputs become NaN.
+__device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, volatile int *err, uint64_t timeout_ns) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (*err) return;
+        for (int i = 0; i < 64; i++)
+            if (bar_try(bar, parity)) return;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < timeout_ns);
+    *err = 1;
+}
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int *err, const KvqWaits &w) {
+    if (!bar_try(bar, parity)) wait_long(bar, parity, err, w.timeout_ns);
+}
+// The same for a barrier that other blocks of the cluster arrive at.
+__device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __noinline__ void wait_cluster(uint32_t bar, uint32_t parity, volatile int *err, uint64_t timeout_ns) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (*err) return;
+        for (int i = 0; i < 64; i++)
+            if (try_cluster(bar, parity)) return;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < timeout_ns);
+    *err = 1;
+}
+__device__ __forceinline__ uint32_t in_block(uint32_t at, int rank) {  // a shared address of another block of the cluster
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_in(uint32_t bar, int rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_block(bar, rank)) : "memory");
+}
+__device__ __forceinline__ float load_in(uint32_t at, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(in_block(at, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {  // (by whole warps)
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 8 columns of this thread's tensor-memory lane; the values are there after tm_wait8.
+__device__ __forceinline__ void tm_load8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
+// (the values pass through the statement, so that no use of them can come before it)
+__device__ __forceinline__ void tm_wait8(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int NC, int PG>
+__device__ __forceinline__ void stage_x(const TcArgs &a, const XSlice<NC, PG> &xs, int first, int tile0, int tiles) {
+    const int u = threadIdx.x % 16;
+    const int held = min(a.tokens, a.n - first);
+    for (int e = threadIdx.x / 16; e < tiles * held; e += blockDim.x / 16) {
+        const int kt = e / held, token = e % held;  // (16 threads alike)
+        const int k = (tile0 + kt) * QM_TILE_COLS + 8 * u;
+        const int64_t row = int64_t(first + token) * a.x_stride;
+        float v[8];
+        uint32_t raw[2] = {0, 0};  // e4m3: the codes as they are
+        const bool whole = a.vec && k + 8 <= a.cols;
+        if (a.x_type == LL_BF16) {
+            const uint16_t *p = static_cast<const uint16_t *>(a.x) + row + k;
+            if (whole) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+                const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = __uint_as_float(i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = k + i < a.cols ? __uint_as_float(uint32_t(p[i]) << 16) : 0.f;
+            }
+        } else if (a.x_type == LL_F32) {
+            const float *p = static_cast<const float *>(a.x) + row + k;
+            if (whole) {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(p)), z = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+                v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w; v[4] = z.x; v[5] = z.y; v[6] = z.z; v[7] = z.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) v[i] = k + i < a.cols ? p[i] : 0.f;
+            }
+        } else {
+            const uint8_t *p = static_cast<const uint8_t *>(a.x) + row + k;
+            if (whole) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+                raw[0] = w.x;
+                raw[1] = w.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) raw[i / 4] |= (k + i < a.cols ? uint32_t(p[i]) : 0u) << (8 * (i % 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float2 f = from_e4m3(raw[i / 2] >> (16 * (i % 2)));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+        const unsigned mates = 0xffffu << (threadIdx.x & 16);
+        float scale, sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        const int col0 = token * a.terms;
+        const uint32_t tile = xs.operand + kt * (XSlice<NC, PG>::N * 128);
+        auto store = [&](int col, uint32_t w0, uint32_t w1) {  // codes of columns 0..3 and 4..7
+            const uint32_t at = tile + col * 128 + ((u / 2 ^ (col & 7)) << 4) + u % 2 * 8;  // (the 128-byte swizzle)
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(__byte_perm(w0, w1, 0x5140)), "r"(__byte_perm(w0, w1, 0x7362)) : "memory");
+        };
+        if (a.x_type == LL_E4M3) {
+            scale = __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step);
+            store(col0, raw[0], raw[1]);
+            sum *= scale;
+        } else {
+            uint32_t top = 0;  // the largest exponent of finite values
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint32_t bits = __float_as_uint(v[i]) & 0x7fffffffu;
+                top = max(top, bits < 0x7f800000u ? bits : 0u);
+                if (bits >= 0x7f800000u) v[i] = __uint_as_float(0x7fffffffu);
+            }
+            top = __reduce_max_sync(mates, top) >> 23;
+            // largest values to [128, 256): by 2^(134 - top), held to what is a normal number (below 2^-113: all zeros)
+            const int up = 261 - int(max(top, 14u));
+            const float f = __uint_as_float(uint32_t(up) << 23);
+            scale = __uint_as_float(uint32_t(254 - up) << 23);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] *= f;
+            float s = scale;
+            for (int term = 0; term < a.terms; term++) {
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    h[i] = to_e4m3(v[2 * i], v[2 * i + 1]);
+                    const float2 b = from_e4m3(h[i]);
+                    v[2 * i] = (v[2 * i] - b.x) * 32.f;
+                    v[2 * i + 1] = (v[2 * i + 1] - b.y) * 32.f;
+                }
+                store(col0 + term, h[0] | h[1] << 16, h[2] | h[3] << 16);
+                if (u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xs.scale + (kt * NC + col0 + term) * 4), "f"(s) : "memory");
+                s *= 1.f / 32;
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 16 / PG; o *= 2) sum += __shfl_xor_sync(mates, sum, o);
+        if (a.x_type == LL_E4M3 && u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xs.scale + (kt * NC + col0) * 4), "f"(scale) : "memory");
+        if (u % (16 / PG) == 0) {
+            const uint32_t at = xs.sum + ((kt * PG + u / (16 / PG)) * NC + col0) * 4;
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sum) : "memory");
+            for (int term = 1; term < a.terms; term++) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * term), "f"(0.f) : "memory");
+        }
+    }
+}
+
+__device__ __forceinline__ void store_y(const TcArgs &a, int64_t row, int token, float y) {
+    const int64_t at = token * a.y_stride + row, from = token * a.add_stride + row;
+    if (a.y_f32) {
+        if (a.add) y += static_cast<const float *>(a.add)[from];
+        static_cast<float *>(a.y)[at] = y;
+    } else {
+        if (a.add) y += __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[from]);
+        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(y);
+    }
+}
+
+// A walk over a block's units: tile kt of its columns of its i-th row block.
+struct Units {
+    int tiles, rb, stride, kt = 0;
+    __device__ __forceinline__ Units(int tiles_, int rb0, int stride_, int skip) : tiles(tiles_), rb(rb0), stride(stride_) { next(skip); }
+    __device__ __forceinline__ void next(int by) {
+        kt += by;
+        while (kt >= tiles) {
+            kt -= tiles;
+            rb += stride;
+        }
+    }
+};
+
+// NC columns of x's operand, PG parameter groups of a tile.
+template <int NC, int PG>
+__global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ TcArgs a) {
+    constexpr int N = XSlice<NC, PG>::N, SD = N <= 32 ? 8 : 4;  // (256 columns of sums at most)
+    constexpr uint32_t TM_D = 32 * SA;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t bars[2 * SA + 2 * SD + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_err;
+    const uint32_t a_full = sptr(bars), a_empty = a_full + 8 * SA, d_full = a_empty + 8 * SA, d_empty = d_full + 8 * SD;
+    const uint32_t ready = d_empty + 8 * SD, freed = ready + 16, drained = freed + 16;  // (ready, freed: of two shares)
+    volatile int *const err = &s_err;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int C = a.cluster, rank = int(blockIdx.x) % C, clusters = int(gridDim.x) / C, first = blockIdx.y * a.tokens;
+    const int tile0 = rank * a.slice, tiles = min(a.slice, a.KT - tile0);  // (1 at least)
+    const int RB = (a.RT + 7) / 8, rb0 = int(blockIdx.x) / C, blocks = (RB - rb0 + clusters - 1) / clusters;
+    const int units = blocks * tiles;
+    const int held = min(a.tokens, a.n - first);
+    const uint32_t base = (sptr(raw) + 1023u) & ~1023u;
+    const XSlice<NC, PG> xs(base, a.slice);
+    const uint32_t rings = base + (XSlice<NC, PG>::bytes(a.slice) + 15) / 16 * 16, shares = rings + UNPACK * a.depth * 2048;
+
+    // the unpacking warps' copies
+    const int q = warp & 3;
+    const uint32_t ring = rings + warp * (a.depth * 2048);
+    Units ahead(tiles, rb0, clusters, warp >> 2);
+    int ahead_u = warp >> 2, ahead_slot = 0;
+    auto issue = [&]() {
+        if (ahead_u < units) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                // 16 bytes a lane: row (i * 32 + lane) / 4 of the warp's, piece lane % 4 of it, turned by the row so that a row's
+                // reader meets no bank twice
+                const int64_t tile = int64_t(min(ahead.rb * 8 + 2 * q + i / 2, a.RT - 1)) * a.KT + tile0 + ahead.kt;  // (rows past the end: not stored)
+                const int row = 8 * i + lane / 4;
+                copy16(ring + ahead_slot * 2048 + row * 64 + (((lane & 3) + (row >> 1)) & 3) * 16, a.codes + tile * 64 + (i & 1) * 32 + lane);
+            }
+            if (lane < 4 * PG) {  // (the parameters, for the joining warps)
+                const int64_t tile = int64_t(min(ahead.rb * 8 + 2 * q + lane / (2 * PG), a.RT - 1)) * a.KT + tile0 + ahead.kt;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.params + tile * (4 * PG) + lane % (2 * PG) * 2));
+            }
+            ahead.next(2);
+            ahead_u += 2;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ahead_slot = ahead_slot + 1 == a.depth ? 0 : ahead_slot + 1;
+    };
+    if (warp < UNPACK)
+        for (int i = 0; i < a.depth - 1; i++) issue();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < SA; i++) {
+            bar_init(a_full + 8 * i, 4);
+            bar_init(a_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < SD; i++) {
+            bar_init(d_full + 8 * i, 1);
+            bar_init(d_empty + 8 * i, FLUSH);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(ready + 8 * i, FLUSH * C);
+            bar_init(freed + 8 * i, FLUSH * C);
+        }
+        bar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_err = 0;
+    }
+    if (warp == W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sptr(&s_tmem)), "n"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    stage_x<NC, PG>(a, xs, first, tile0, tiles);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_before();
+    if (C > 1) cluster_sync();  // (others arrive at this block's barriers)
+    else __syncthreads();
+    fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+
+    if (warp < UNPACK) {
+        int slot = 0;
+        for (int u = warp >> 2; u < units; u += 2) {
+            issue();
+            wait_copies(a.depth - 1);
+            __syncwarp();  // (a row comes by four lanes' copies)
+            uint32_t r[32];
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                const uint4 w = lds16(ring + slot * 2048 + lane * 64 + ((t + (lane >> 1)) & 3) * 16);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    r[8 * j + 2 * t] = (v[j] >> 3) & 0x0f0f0f0fu;
+                    r[8 * j + 2 * t + 1] = __funnelshift_r(v[j], v[j], 7) & 0x0f0f0f0fu;
+                }
+            }
+            __syncwarp();  // (before another lane's copy into this slot)
+            slot = slot + 1 == a.depth ? 0 : slot + 1;
+            const int s = u % SA;
+            if (u >= SA) wait(a_empty + 8 * s, (u / SA - 1) & 1, err, a.waits);
+            fence_after();
+            tm_store(tmem + 32 * s + (uint32_t(32 * q) << 16), r);
+            tm_store_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(a_full + 8 * s);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else if (warp == W_MMA) {
+        Units at(tiles, rb0, clusters, 0);
+        int d = 0;
+        for (int u = 0; u < units; u++, at.next(1)) {
+            const int s = u % SA;
+            wait(a_full + 8 * s, (u / SA) & 1, err, a.waits);
+            const uint64_t b = desc_sw128(xs.operand + at.kt * (N * 128));
+#pragma unroll
+            for (int p = 0; p < PG; p++, d++) {
+                const int i = d % SD;
+                if (d >= SD) wait(d_empty + 8 * i, (d / SD - 1) & 1, err, a.waits);
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < 4 / PG; k++)
+                    mma_f8(tmem + TM_D + i * N, tmem + 32 * s + 8 * (p * (4 / PG) + k), b + 2 * (p * (4 / PG) + k), IDESC<N>, k != 0);
+                commit(d_full + 8 * i);
+            }
+            commit(a_empty + 8 * s);
+        }
+    } else {
+        const int row = 32 * q + lane;  // of the row block
+        uint64_t tot[NC / 2];
+        Units at(tiles, rb0, clusters, 0), next = at;
+        uint32_t par[2][PG];
+        auto fetch = [&](uint32_t (&p)[PG]) {  // (lo, step) of the row in the groups of a unit to come
+            const int64_t tile = int64_t(min(next.rb * 8 + row / 16, a.RT - 1)) * a.KT + tile0 + next.kt;
+#pragma unroll
+            for (int g = 0; g < PG; g++) p[g] = __ldg(reinterpret_cast<const uint32_t *>(a.params) + (tile * PG + g) * 16 + row % 16);
+            next.next(1);
+        };
+        fetch(par[0]);
+        if (units > 1) fetch(par[1]);
+        int d = 0, done = 0;
+#pragma unroll
+        for (int i = 0; i < NC / 2; i++) tot[i] = 0;
+        auto unit = [&](int u, uint32_t (&mine)[PG]) {
+#pragma unroll
+            for (int g = 0; g < PG; g++, d++) {
+                const int i = d % SD;
+                const float2 p = __half22float2(kvq_h2(mine[g]));
+                const uint64_t lo = kvq_pair(p.x, p.x), step = kvq_pair(p.y * 512.f, p.y * 512.f);
+                const uint32_t sc = xs.scale + at.kt * (NC * 4), sum = xs.sum + (at.kt * PG + g) * (NC * 4);
+                wait(d_full + 8 * i, (d / SD) & 1, err, a.waits);
+                fence_after();
+                const uint32_t from = tmem + TM_D + i * N + (uint32_t(32 * q) << 16);
+                uint32_t v[2][8];
+                tm_load8(from, v[0]);
+#pragma unroll
+                for (int c = 0; c < NC; c += 8) {
+                    uint32_t (&w)[8] = v[c / 8 % 2];
+                    tm_wait8(w);
+                    if (c + 8 < NC) {
+                        tm_load8(from + c + 8, v[(c / 8 + 1) % 2]);
+                    } else {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(d_empty + 8 * i);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const ulonglong2 f = lds_two_pairs(sc + 4 * (c + e)), s = lds_two_pairs(sum + 4 * (c + e));
+                        uint64_t &t0 = tot[(c + e) / 2], &t1 = tot[(c + e) / 2 + 1];
+                        t0 = kvq_fma2(kvq_mul2(step, f.x), kvq_pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), kvq_fma2(lo, s.x, t0));
+                        t1 = kvq_fma2(kvq_mul2(step, f.y), kvq_pair(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])), kvq_fma2(lo, s.y, t1));
+                    }
+                }
+            }
+            if (u + 2 < units) fetch(mine);
+            if (at.kt + 1 == tiles) {  // the row block's end
+                const int64_t out = int64_t(at.rb) * 128 + row;
+                const int half = done & 1;
+                const uint32_t share = shares + half * (a.tokens * 512) + row * 4;
+                if (C > 1 && done >= 2) wait_cluster(freed + 8 * half, (done / 2 - 1) & 1, err, a.waits.timeout_ns);
+                const bool lost = *err;
+                auto put = [&](int token, float y) {
+                    if (lost) y = __uint_as_float(0x7fffffffu);
+                    if (token >= held) return;
+                    if (C > 1) asm volatile("st.shared.f32 [%0], %1;" ::"r"(share + token * 512), "f"(y) : "memory");
+                    else if (out < a.rows) store_y(a, out, first + token, y);
+                };
+#pragma unroll
+                for (int c = 0; c < NC; c += 4) {
+                    float y[4];
+                    kvq_split(tot[c / 2], y[0], y[1]);
+                    kvq_split(tot[c / 2 + 1], y[2], y[3]);
+                    tot[c / 2] = tot[c / 2 + 1] = 0;
+                    if (a.terms == 1) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++) put(c + e, y[e]);
+                    } else if (a.terms == 2) {
+                        put(c / 2, y[0] + y[1]);
+                        put(c / 2 + 1, y[2] + y[3]);
+                    } else {
+                        put(c / 4, (y[0] + y[1]) + (y[2] + y[3]));
+                    }
+                }
+                if (C > 1) {
+                    __syncwarp();
+                    if (lane < C) arrive_in(ready + 8 * half, lane);
+                    wait_cluster(ready + 8 * half, (done / 2) & 1, err, a.waits.timeout_ns);
+                    for (int token = rank; token < held; token += C) {
+                        float y = 0.f;
+                        for (int b = 0; b < C; b++) y += load_in(share + token * 512, b);
+                        if (*err) y = __uint_as_float(0x7fffffffu);
+                        if (out < a.rows) store_y(a, out, first + token, y);
+                    }
+                    __syncwarp();
+                    if (lane < C) arrive_in(freed + 8 * half, lane);
+                }
+                done++;
+            }
+            at.next(1);
+        };
+        for (int u = 0; u < units; u += 2) {
+            unit(u, par[0]);
+            if (u + 1 < units) unit(u + 1, par[1]);
+        }
+        fence_before();
+    }
+    if (C > 1) cluster_sync();  // (no block ends while others read its shares)
+    __syncthreads();
+    if (*err) {  // a wait has run out: products in flight end before their memory goes
+        if (warp == W_MMA) {
+            commit(drained);
+            bar_wait_long(drained, 0, KVQ_DRAIN_NS);
+        }
+        __syncthreads();
+    }
+    if (warp == W_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+template <int NC, int PG>
+int smem_bytes(int slice, int depth, int cluster, int tokens) {
+    return 1024 + (XSlice<NC, PG>::bytes(slice) + 15) / 16 * 16 + UNPACK * depth * 2048 + (cluster > 1 ? 2 * tokens * 512 : 0);
+}
+
+// Clusters of c blocks, one an SM, that the device holds at a time (c = 8: fewer than SMs / 8, by the SMs of a GPC).
+int clusters_of(const void *kernel, int c, int nsm) {
+    static std::atomic<int> known[4];  // (of 1, 2, 4, 8; every device here is alike)
+    const int at = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
+    if (c == 1) return nsm;
+    int n = known[at].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nsm / c * c);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = MAX_SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(c), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return nsm / c;
+    }
+    known[at].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int NC, int PG>
+int launch(const TcArgs &in, int nsm, cudaStream_t st) {
+    const void *kernel = reinterpret_cast<const void *>(k_qmat_tc<NC, PG>);
+    if (!allow_smem(kernel, MAX_SMEM)) return LL_ERR_CUDA;
+    // Blocks that share the columns, by the units of the busiest block: what fits, then the fewest steps, with
+    // 2 for a row block's end, 4 where shares meet.
+    TcArgs a = in;
+    a.cluster = 0;
+    int at_once = 0;
+    const int RB = (in.RT + 7) / 8;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= MAX_CLUSTER; c *= 2) {
+        const int slice = (in.KT + c - 1) / c;
+        if ((c - 1) * slice >= in.KT) break;  // (a block without a tile)
+        int depth = 8;
+        while (depth > 2 && smem_bytes<NC, PG>(slice, depth, c, in.tokens) > MAX_SMEM) depth--;
+        if (smem_bytes<NC, PG>(slice, depth, c, in.tokens) > MAX_SMEM) continue;
+        const int held = clusters_of(kernel, c, nsm);
+        const int64_t rounds = (RB + held - 1) / held, steps = rounds * (slice + (c > 1 ? 4 : 2)) + (depth < 4 ? slice : 0);
+        if (steps < best) {
+            best = steps;
+            a.cluster = c;
+            a.slice = slice;
+            a.depth = depth;
+            at_once = held;
+        }
+    }
+    if (!a.cluster) return LL_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(RB, at_once) * a.cluster, (a.n + a.tokens - 1) / a.tokens);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<NC, PG>(a.slice, a.depth, a.cluster, a.tokens);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {unsigned(a.cluster), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_qmat_tc<NC, PG>, a) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+template <int NC>
+int launch_pg(const TcArgs &a, int pg, int nsm, cudaStream_t st) {
+    return pg == 1 ? launch<NC, 1>(a, nsm, st) : pg == 2 ? launch<NC, 2>(a, nsm, st) : launch<NC, 4>(a, nsm, st);
+}
+
+}  // namespace
+
+// LL_ERR_SHAPE: x does not fit into shared memory (nothing was launched).
+int launch_qmat_tc(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st) {
+    TcArgs a = {};
+    a.codes = reinterpret_cast<const uint4 *>(m.codes);
+    a.params = reinterpret_cast<const uint4 *>(m.params);
+    a.rows = m.rows;
+    a.cols = m.cols;
+    a.KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;
+    a.RT = (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS;
+    a.x = x.data;
+    a.x_type = x.type;
+    a.x_stride = n > 1 ? x.stride : 0;
+    a.scale = x.scale;
+    a.scale_row = x.group ? a.KT : 1;
+    a.scale_step = x.group ? 1 : 0;
+    const int size = x.type == LL_F32 ? 4 : x.type == LL_BF16 ? 2 : 1, wide = size == 1 ? 8 : 16;
+    a.vec = reinterpret_cast<uintptr_t>(x.data) % wide == 0 && (a.x_stride * size) % wide == 0;
+    a.add = add ? add->data : nullptr;
+    a.add_stride = add ? add->stride : 0;
+    a.y = y.data;
+    a.y_stride = y.stride;
+    a.y_f32 = y.type == LL_F32;
+    a.n = n;
+    a.terms = x.type == LL_F32 ? 4 : x.type == LL_BF16 ? 2 : 1;
+    const int pg = QM_TILE_COLS / m.group;
+    // As many columns of x a pass as there are, up to 64; fewer where they do not fit.
+    for (int nc = n * a.terms <= 8 ? 8 : n * a.terms <= 16 ? 16 : n * a.terms <= 32 ? 32 : 64; nc >= 8; nc /= 2) {
+        a.tokens = nc / a.terms;
+        const int rc = nc == 64 ? launch_pg<64>(a, pg, nsm, st) : nc == 32 ? launch_pg<32>(a, pg, nsm, st)
+                     : nc == 16 ? launch_pg<16>(a, pg, nsm, st) : launch_pg<8>(a, pg, nsm, st);
+        if (rc != LL_ERR_SHAPE) return rc;
+    }
+    return LL_ERR_SHAPE;
+}
+
+}  // namespace ll
