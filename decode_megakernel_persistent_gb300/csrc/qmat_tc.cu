@@ -10,11 +10,17 @@
 // 128 (what is lost below is 2^-22 of it at most), four hold 20 bits of fp32. Products are exact, sums fp32; lo, step and
 // the scales meet them in fp32, once a group.
 //
-// A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Eight warps, in two sets that
+// That is for fp32 outputs, or fp32 x. bf16 outputs of bf16 or e4m3 x (HALF) take W's values themselves, rounded to fp16
+// (2^-12 of a value at most), and x in fp16, scaled by a power of two a row (bf16's 8 bits exactly down to 2^-28 of the
+// largest; e4m3 times its scale rounded to 11 bits): three times the instructions a code, but one sum over all columns, where
+// taking the sums of 64 columns of x a group of 128 from tensor memory cost more. The roundings add 2e-4 of the
+// outputs' norm to the 1.6e-3 of their own.
+//
+// A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Sixteen warps, in four sets that
 // take units in turn, unpack 32 rows each from a ring of their own (cp.async) into tensor memory, the products' A operand,
-// a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products of a group into one
-// of several sums in tensor memory; four warps, a row to a thread, take them from there and join them in registers with
-// the group's parameters. Blocks of a cluster share the columns: each row's shares then meet through shared memory.
+// a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products; four warps, a row
+// to a thread, take the sums from tensor memory (a group's, joined in registers with its parameters, or HALF a row
+// block's). Blocks of a cluster share the columns: each row's shares then meet through shared memory.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,24 +59,25 @@ struct TcArgs {
     int depth;              // units of a warp in flight
 };
 
-constexpr int UNPACK = 8, FLUSH = 4, W_MMA = UNPACK + FLUSH, THREADS = 32 * (W_MMA + 1);
-constexpr int SA = 8;                     // A stages, 32 columns of tensor memory each
+constexpr int SETS = 4, UNPACK = 4 * SETS, FLUSH = 4, W_MMA = UNPACK + FLUSH, THREADS = 32 * (W_MMA + 1);
 constexpr int MAX_SMEM = 232448 - 2048, MAX_CLUSTER = 8;
 
 // What a block keeps of x, by bytes from `base` on (a 1,024-byte border):
-//   operand  [slice][N][128]      K-major rows of a tile's columns, in the 128-byte swizzle
+//   operand  [slice][N][128]      K-major rows of a tile's columns in e4m3, in the 128-byte swizzle
 //   scale    [slice][NC] floats   of a tile's column
 //   sum      [slice][PG][NC]      of a group's x (in the column of its first term)
-template <int NC, int PG>
-struct XSlice {
-    static constexpr int N = NC < 16 ? 16 : NC;  // columns of a product: 16 at least
-    uint32_t operand, scale, sum;
-    __device__ __forceinline__ XSlice(uint32_t base, int slice) {
-        operand = base;
-        scale = operand + slice * N * 128;
-        sum = scale + slice * NC * 4;
-    }
-    static __host__ __device__ int bytes(int slice) { return slice * (N * 128 + NC * 4 * (1 + PG)); }
+// or HALF
+//   operand  [slice][2][N][128]   the same in fp16, 64 columns after 64
+//   scale    [NC] floats          of a token; then the largest of each, as bits
+template <int NC, int PG, bool HALF>
+struct Shape {
+    static constexpr int N = NC < 16 ? 16 : NC;                  // columns of a product: 16 at least
+    static constexpr int TILE = N * (HALF ? 256 : 128);
+    static constexpr int A_COLS = HALF ? 64 : 32;                // of tensor memory: a stage of A
+    static constexpr int SD = HALF ? 2 : N <= 32 ? 8 : 4;        // sums
+    static constexpr int TM_A = SD * N, SA = (512 - TM_A) / A_COLS < 8 ? (512 - TM_A) / A_COLS : 8;
+    static constexpr int SLOT = 2048 + (HALF ? 128 * PG : 0);    // a warp's unit in its ring: codes, parameters
+    static __host__ __device__ int x_bytes(int slice) { return slice * TILE + (HALF ? 2 * NC * 4 : slice * NC * 4 * (1 + PG)); }
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
@@ -114,12 +121,19 @@ __device__ __forceinline__ float2 from_e4m3(uint32_t two) {
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
     return uint64_t((addr >> 4) & 0x3fffu) | uint64_t(1u) << 16 | uint64_t(1024u >> 4) << 32 | uint64_t(1u) << 46 | uint64_t(2u) << 61;
 }
-// kind::f8f6f4: e4m3 A and B, fp32 sums, M = 128.
+// e4m3 (kind::f8f6f4) or fp16 (kind::f16) A and B, fp32 sums, M = 128.
 template <int N>
 constexpr uint32_t IDESC = (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(128 >> 4) << 24);
 // (by a whole warp, of which one elected lane, the same at every call, carries it out)
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile(
+template <bool HALF>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    if (HALF)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(add)
+            : "memory");
+    else asm volatile(
         "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
@@ -216,65 +230,154 @@ __device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <int NC, int PG>
-__device__ __forceinline__ void stage_x(const TcArgs &a, const XSlice<NC, PG> &xs, int first, int tile0, int tiles) {
-    const int u = threadIdx.x % 16;
-    const int held = min(a.tokens, a.n - first);
-    for (int e = threadIdx.x / 16; e < tiles * held; e += blockDim.x / 16) {
-        const int kt = e / held, token = e % held;  // (16 threads alike)
-        const int k = (tile0 + kt) * QM_TILE_COLS + 8 * u;
-        const int64_t row = int64_t(first + token) * a.x_stride;
-        float v[8];
-        uint32_t raw[2] = {0, 0};  // e4m3: the codes as they are
-        const bool whole = a.vec && k + 8 <= a.cols;
-        if (a.x_type == LL_BF16) {
-            const uint16_t *p = static_cast<const uint16_t *>(a.x) + row + k;
-            if (whole) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-                const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = __uint_as_float(i & 1 ? q[i / 2] & 0xffff0000u : q[i / 2] << 16);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = k + i < a.cols ? __uint_as_float(uint32_t(p[i]) << 16) : 0.f;
-            }
-        } else if (a.x_type == LL_F32) {
-            const float *p = static_cast<const float *>(a.x) + row + k;
-            if (whole) {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(p)), z = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-                v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w; v[4] = z.x; v[5] = z.y; v[6] = z.z; v[7] = z.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = k + i < a.cols ? p[i] : 0.f;
-            }
+// 8 values of a row of x from column k on, as they lie in memory, zeros past the end.
+__device__ __forceinline__ void load_raw(const TcArgs &a, int64_t row, int k, uint4 (&raw)[2]) {
+    const int size = a.x_type == LL_F32 ? 4 : a.x_type == LL_BF16 ? 2 : 1;
+    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
+    if (k >= a.cols) return;
+    const char *p = static_cast<const char *>(a.x) + (row * a.x_stride + k) * size;
+    if (a.vec && k + 8 <= a.cols) {
+        if (size == 1) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+            raw[0].x = w.x;
+            raw[0].y = w.y;
         } else {
-            const uint8_t *p = static_cast<const uint8_t *>(a.x) + row + k;
-            if (whole) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-                raw[0] = w.x;
-                raw[1] = w.y;
-            } else {
+            raw[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+            if (size == 4) raw[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+        }
+    } else {
+        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 8; i++) raw[i / 4] |= (k + i < a.cols ? uint32_t(p[i]) : 0u) << (8 * (i % 4));
+        for (int j = 0; j < 8; j++) {
+            if (k + j >= a.cols) continue;
+            if (size == 4) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+            else if (size == 2) w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t *>(p)[j]) << (16 * (j % 2));
+            else w[j / 4] |= uint32_t(reinterpret_cast<const uint8_t *>(p)[j]) << (8 * (j % 4));
+        }
+        raw[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        raw[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+__device__ __forceinline__ void widen(const TcArgs &a, const uint4 (&r)[2], float (&v)[8]) {
+    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
+    if (a.x_type == LL_BF16) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    } else if (a.x_type == LL_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = from_e4m3(w[j / 2] >> (16 * (j % 2)));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+constexpr int BATCH = 4;  // tokens' tiles of a thread on their way at once
+
+// HALF: a token's columns in fp16, largest values of the block's columns to [2^14, 2^15). First the largest of each
+// token go round (a token's tile to 16 threads), then the values are rounded.
+template <int NC, int PG>
+__device__ __forceinline__ void stage_half(const TcArgs &a, uint32_t operand, int first, int tile0, int tiles) {
+    using S = Shape<NC, PG, true>;
+    const uint32_t scales = operand + a.slice * S::TILE, tops = scales + NC * 4;
+    const int u = threadIdx.x % 16, step = THREADS / 16;
+    const int held = min(a.tokens, a.n - first), items = tiles * held;
+    const unsigned mates = 0xffffu << (threadIdx.x & 16);
+    for (int i = threadIdx.x; i < NC; i += THREADS) asm volatile("st.shared.u32 [%0], %1;" ::"r"(tops + 4 * i), "r"(0) : "memory");
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < 2; pass++) {
+#pragma unroll 1
+        for (int e0 = threadIdx.x / 16; e0 < items; e0 += BATCH * step) {
+            uint4 raws[BATCH][2];
+            float factor[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; i++) {
+                const int e = min(e0 + i * step, items - 1), kt = e / held, token = e % held;
+                load_raw(a, first + token, (tile0 + kt) * QM_TILE_COLS + 8 * u, raws[i]);
+                factor[i] = a.x_type == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float2 f = from_e4m3(raw[i / 2] >> (16 * (i % 2)));
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
+            for (int i = 0; i < BATCH; i++) {
+                const int e = e0 + i * step;
+                if (e >= items) break;  // (16 threads alike)
+                const int kt = e / held, token = e % held;
+                float v[8];
+                widen(a, raws[i], v);
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j] *= factor[i];
+                if (pass == 0) {
+                    uint32_t top = 0;  // of finite values
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const uint32_t bits = __float_as_uint(v[j]) & 0x7fffffffu;
+                        top = max(top, bits < 0x7f800000u ? bits : 0u);
+                    }
+                    top = __reduce_max_sync(mates, top);
+                    if (u == 0) asm volatile("red.shared.max.u32 [%0], %1;" ::"r"(tops + 4 * token), "r"(top) : "memory");
+                } else {
+                    uint32_t top;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(top) : "r"(tops + 4 * token) : "memory");
+                    // by 2^(141 - top), held to normal numbers (a largest value below 2^-106: zeros)
+                    const int up = 268 - int(max(top >> 23, 21u));
+                    const float f = __uint_as_float(uint32_t(up) << 23);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        // (a value that is not finite becomes a NaN: infinities would meet zeros and other signs)
+                        const float p = isfinite(v[2 * j]) ? v[2 * j] * f : __uint_as_float(0x7fffffffu);
+                        const float r = isfinite(v[2 * j + 1]) ? v[2 * j + 1] * f : __uint_as_float(0x7fffffffu);
+                        h[j] = kvq_u32(__floats2half2_rn(p, r));
+                    }
+                    const uint32_t at = operand + kt * S::TILE + (u / 8) * (S::N * 128) + token * 128 + (((u & 7) ^ (token & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+                    if (u == 0 && kt == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + 4 * token), "f"(__uint_as_float(uint32_t(254 - up) << 23)) : "memory");
+                }
             }
         }
+        __syncthreads();
+    }
+}
+
+// 16 threads turn a token's 128 columns of a tile into the operand: thread u has columns 8 u .. 8 u + 7, 8 bytes of a row of 128 (the
+// order of a word's codes as they are unpacked: columns 0, 4, 1, 5 and 2, 6, 3, 7 of the 8).
+template <int NC, int PG>
+__device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int first, int tile0, int tiles) {
+    using S = Shape<NC, PG, false>;
+    const uint32_t scales = operand + a.slice * S::TILE, sums = scales + a.slice * NC * 4;
+    const int u = threadIdx.x % 16, step = THREADS / 16;
+    const int held = min(a.tokens, a.n - first), items = tiles * held;
+#pragma unroll 1
+    for (int e0 = threadIdx.x / 16; e0 < items; e0 += BATCH * step) {
+    uint4 raws[BATCH][2];
+    float factor[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; i++) {
+        const int e = min(e0 + i * step, items - 1), kt = e / held, token = e % held;
+        load_raw(a, first + token, (tile0 + kt) * QM_TILE_COLS + 8 * u, raws[i]);
+        factor[i] = a.x_type == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; i++) {
+        const int e = e0 + i * step;
+        if (e >= items) break;  // (16 threads alike)
+        const int kt = e / held, token = e % held;
+        float v[8];
+        widen(a, raws[i], v);
         const unsigned mates = 0xffffu << (threadIdx.x & 16);
         float scale, sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         const int col0 = token * a.terms;
-        const uint32_t tile = xs.operand + kt * (XSlice<NC, PG>::N * 128);
+        const uint32_t tile = operand + kt * S::TILE;
         auto store = [&](int col, uint32_t w0, uint32_t w1) {  // codes of columns 0..3 and 4..7
             const uint32_t at = tile + col * 128 + ((u / 2 ^ (col & 7)) << 4) + u % 2 * 8;  // (the 128-byte swizzle)
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(__byte_perm(w0, w1, 0x5140)), "r"(__byte_perm(w0, w1, 0x7362)) : "memory");
         };
         if (a.x_type == LL_E4M3) {
-            scale = __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step);
-            store(col0, raw[0], raw[1]);
+            scale = factor[i];
+            store(col0, raws[i][0].x, raws[i][0].y);
             sum *= scale;
         } else {
             uint32_t top = 0;  // the largest exponent of finite values
@@ -302,18 +405,19 @@ __device__ __forceinline__ void stage_x(const TcArgs &a, const XSlice<NC, PG> &x
                     v[2 * i + 1] = (v[2 * i + 1] - b.y) * 32.f;
                 }
                 store(col0 + term, h[0] | h[1] << 16, h[2] | h[3] << 16);
-                if (u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xs.scale + (kt * NC + col0 + term) * 4), "f"(s) : "memory");
+                if (u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + (kt * NC + col0 + term) * 4), "f"(s) : "memory");
                 s *= 1.f / 32;
             }
         }
 #pragma unroll
         for (int o = 1; o < 16 / PG; o *= 2) sum += __shfl_xor_sync(mates, sum, o);
-        if (a.x_type == LL_E4M3 && u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xs.scale + (kt * NC + col0) * 4), "f"(scale) : "memory");
+        if (a.x_type == LL_E4M3 && u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + (kt * NC + col0) * 4), "f"(scale) : "memory");
         if (u % (16 / PG) == 0) {
-            const uint32_t at = xs.sum + ((kt * PG + u / (16 / PG)) * NC + col0) * 4;
+            const uint32_t at = sums + ((kt * PG + u / (16 / PG)) * NC + col0) * 4;
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sum) : "memory");
             for (int term = 1; term < a.terms; term++) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * term), "f"(0.f) : "memory");
         }
+    }
     }
 }
 
@@ -341,11 +445,27 @@ struct Units {
     }
 };
 
+// Pairs of codes of a word as fp16 values lo + step c. In bits 6..9 of a half, alone, a code is the subnormal number c 2^-18, so that
+// with step 2^18 (while that is finite: WIDE) one operation has the value; otherwise the code becomes a number first.
+template <bool WIDE>
+__device__ __forceinline__ void values(uint32_t w, __half2 lo, __half2 step, uint32_t *r) {
+    const uint32_t v[4] = {w << 3, w >> 1, w >> 5, __funnelshift_r(w, w, 9)};
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+        if (WIDE) {
+            r[p] = kvq_u32(__hfma2(step, kvq_h2(v[p] & 0x03c003c0u), lo));
+        } else {
+            const __half2 c = __hsub2(kvq_h2((v[p] & 0x03c003c0u) | 0x4c004c00u), __float2half2_rn(16.f));
+            r[p] = kvq_u32(__hfma2(step, c, lo));
+        }
+    }
+}
+
 // NC columns of x's operand, PG parameter groups of a tile.
-template <int NC, int PG>
+template <int NC, int PG, bool HALF>
 __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ TcArgs a) {
-    constexpr int N = XSlice<NC, PG>::N, SD = N <= 32 ? 8 : 4;  // (256 columns of sums at most)
-    constexpr uint32_t TM_D = 32 * SA;
+    using S = Shape<NC, PG, HALF>;
+    constexpr int N = S::N, SD = S::SD, SA = S::SA;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[2 * SA + 2 * SD + 5];
     __shared__ uint32_t s_tmem;
@@ -359,31 +479,39 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
     const int RB = (a.RT + 7) / 8, rb0 = int(blockIdx.x) / C, blocks = (RB - rb0 + clusters - 1) / clusters;
     const int units = blocks * tiles;
     const int held = min(a.tokens, a.n - first);
-    const uint32_t base = (sptr(raw) + 1023u) & ~1023u;
-    const XSlice<NC, PG> xs(base, a.slice);
-    const uint32_t rings = base + (XSlice<NC, PG>::bytes(a.slice) + 15) / 16 * 16, shares = rings + UNPACK * a.depth * 2048;
+    const uint32_t operand = (sptr(raw) + 1023u) & ~1023u, scales = operand + a.slice * S::TILE, sums = scales + a.slice * NC * 4;
+    const uint32_t rings = operand + (S::x_bytes(a.slice) + 15) / 16 * 16, shares = rings + UNPACK * a.depth * S::SLOT;
 
     // the unpacking warps' copies
-    const int q = warp & 3;
-    const uint32_t ring = rings + warp * (a.depth * 2048);
-    Units ahead(tiles, rb0, clusters, warp >> 2);
-    int ahead_u = warp >> 2, ahead_slot = 0;
+    const int q = warp & 3, set = warp >> 2;
+    const uint32_t ring = rings + warp * (a.depth * S::SLOT);
+    Units ahead(tiles, rb0, clusters, set);
+    int ahead_u = set, ahead_slot = 0, aimed = -1;
+    int64_t tiles_at[2];  // of the two row tiles: their first tile of the block's columns
     auto issue = [&]() {
         if (ahead_u < units) {
+            if (aimed != ahead.rb) {
+                aimed = ahead.rb;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                // 16 bytes a lane: row (i * 32 + lane) / 4 of the warp's, piece lane % 4 of it, turned by the row so that a row's
-                // reader meets no bank twice
-                const int64_t tile = int64_t(min(ahead.rb * 8 + 2 * q + i / 2, a.RT - 1)) * a.KT + tile0 + ahead.kt;  // (rows past the end: not stored)
-                const int row = 8 * i + lane / 4;
-                copy16(ring + ahead_slot * 2048 + row * 64 + (((lane & 3) + (row >> 1)) & 3) * 16, a.codes + tile * 64 + (i & 1) * 32 + lane);
+                for (int r = 0; r < 2; r++) tiles_at[r] = int64_t(min(aimed * 8 + 2 * q + r, a.RT - 1)) * a.KT + tile0;  // (rows past the end: not stored)
             }
-            if (lane < 4 * PG) {  // (the parameters, for the joining warps)
-                const int64_t tile = int64_t(min(ahead.rb * 8 + 2 * q + lane / (2 * PG), a.RT - 1)) * a.KT + tile0 + ahead.kt;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.params + tile * (4 * PG) + lane % (2 * PG) * 2));
+            const uint32_t to = ring + ahead_slot * S::SLOT;
+            // 16 bytes a lane: row 8 i + lane / 4 of the warp's, piece lane % 4 of it, turned by the row so that a row's
+            // reader meets no bank twice
+            const uint32_t turned = to + lane / 4 * 64 + (((lane & 3) + (lane >> 3)) & 3) * 16;
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const uint4 *from = a.codes + (tiles_at[r] + ahead.kt) * 64 + lane;
+                copy16(turned + r * 1024, from);
+                copy16(turned + r * 1024 + 512, from + 32);
             }
-            ahead.next(2);
-            ahead_u += 2;
+            if (HALF) {
+                if (lane < 8 * PG) copy16(to + 2048 + 16 * lane, a.params + (tiles_at[lane / (4 * PG)] + ahead.kt) * (4 * PG) + lane % (4 * PG));
+            } else if (lane < 4 * PG) {  // (for the joining warps)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.params + (tiles_at[lane / (2 * PG)] + ahead.kt) * (4 * PG) + lane % (2 * PG) * 2));
+            }
+            ahead.next(SETS);
+            ahead_u += SETS;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         ahead_slot = ahead_slot + 1 == a.depth ? 0 : ahead_slot + 1;
@@ -412,37 +540,81 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sptr(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    stage_x<NC, PG>(a, xs, first, tile0, tiles);
+    if constexpr (HALF) stage_half<NC, PG>(a, operand, first, tile0, tiles);
+    else stage_x<NC, PG>(a, operand, first, tile0, tiles);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     fence_before();
     if (C > 1) cluster_sync();  // (others arrive at this block's barriers)
     else __syncthreads();
     fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0), tmem_a = tmem + S::TM_A;
 
     if (warp < UNPACK) {
         int slot = 0;
-        for (int u = warp >> 2; u < units; u += 2) {
+        for (int u = set; u < units; u += SETS) {
             issue();
             wait_copies(a.depth - 1);
             __syncwarp();  // (a row comes by four lanes' copies)
-            uint32_t r[32];
+            const uint32_t at = ring + slot * S::SLOT;
+            uint32_t w[4][4];  // [t][j]
 #pragma unroll
             for (int t = 0; t < 4; t++) {
-                const uint4 w = lds16(ring + slot * 2048 + lane * 64 + ((t + (lane >> 1)) & 3) * 16);
-                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    r[8 * j + 2 * t] = (v[j] >> 3) & 0x0f0f0f0fu;
-                    r[8 * j + 2 * t + 1] = __funnelshift_r(v[j], v[j], 7) & 0x0f0f0f0fu;
-                }
+                const uint4 v = lds16(at + lane * 64 + ((t + (lane >> 1)) & 3) * 16);
+                w[t][0] = v.x; w[t][1] = v.y; w[t][2] = v.z; w[t][3] = v.w;
             }
-            __syncwarp();  // (before another lane's copy into this slot)
-            slot = slot + 1 == a.depth ? 0 : slot + 1;
             const int s = u % SA;
-            if (u >= SA) wait(a_empty + 8 * s, (u / SA - 1) & 1, err, a.waits);
-            fence_after();
-            tm_store(tmem + 32 * s + (uint32_t(32 * q) << 16), r);
+            const uint32_t to = tmem_a + S::A_COLS * s + (uint32_t(32 * q) << 16);
+            if constexpr (HALF) {
+                uint32_t par[PG];
+#pragma unroll
+                for (int g = 0; g < PG; g++)
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(par[g]) : "r"(at + 2048 + (lane / 16 * PG + g) * 64 + lane % 16 * 4) : "memory");
+                bool wide = true;
+                __half2 lo[PG], step[PG], step18[PG];
+#pragma unroll
+                for (int g = 0; g < PG; g++) {
+                    lo[g] = kvq_h2(kvq_prmt(par[g], 0, 0x1010));
+                    step[g] = kvq_h2(kvq_prmt(par[g], 0, 0x3232));
+                    step18[g] = __hmul2(__hmul2(step[g], __float2half2_rn(512.f)), __float2half2_rn(512.f));
+                    wide = wide && (kvq_u32(step18[g]) & 0x7c00u) != 0x7c00u;
+                }
+                wide = __all_sync(0xffffffffu, wide);
+                __syncwarp();  // (before another lane's copy into this slot)
+                if (u >= SA) wait(a_empty + 8 * s, (u / SA - 1) & 1, err, a.waits);
+                fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    uint32_t r[32];
+                    if (wide) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const int j = 2 * h + e / 4, t = e % 4, g = j * PG / 4;
+                            values<true>(w[t][j], lo[g], step18[g], r + 4 * e);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const int j = 2 * h + e / 4, t = e % 4, g = j * PG / 4;
+                            values<false>(w[t][j], lo[g], step[g], r + 4 * e);
+                        }
+                    }
+                    tm_store(to + 32 * h, r);
+                }
+            } else {
+                uint32_t r[32];
+#pragma unroll
+                for (int t = 0; t < 4; t++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        r[8 * j + 2 * t] = (w[t][j] >> 3) & 0x0f0f0f0fu;
+                        r[8 * j + 2 * t + 1] = __funnelshift_r(w[t][j], w[t][j], 7) & 0x0f0f0f0fu;
+                    }
+                __syncwarp();
+                if (u >= SA) wait(a_empty + 8 * s, (u / SA - 1) & 1, err, a.waits);
+                fence_after();
+                tm_store(to, r);
+            }
+            slot = slot + 1 == a.depth ? 0 : slot + 1;
             tm_store_wait();
             fence_before();
             __syncwarp();
@@ -455,45 +627,87 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
         for (int u = 0; u < units; u++, at.next(1)) {
             const int s = u % SA;
             wait(a_full + 8 * s, (u / SA) & 1, err, a.waits);
-            const uint64_t b = desc_sw128(xs.operand + at.kt * (N * 128));
-#pragma unroll
-            for (int p = 0; p < PG; p++, d++) {
+            const uint32_t b = operand + at.kt * S::TILE;
+            if constexpr (HALF) {
                 const int i = d % SD;
-                if (d >= SD) wait(d_empty + 8 * i, (d / SD - 1) & 1, err, a.waits);
+                if (at.kt == 0 && d >= SD) wait(d_empty + 8 * i, (d / SD - 1) & 1, err, a.waits);
                 fence_after();
 #pragma unroll
-                for (int k = 0; k < 4 / PG; k++)
-                    mma_f8(tmem + TM_D + i * N, tmem + 32 * s + 8 * (p * (4 / PG) + k), b + 2 * (p * (4 / PG) + k), IDESC<N>, k != 0);
-                commit(d_full + 8 * i);
+                for (int k = 0; k < 8; k++)
+                    mma<true>(tmem + i * N, tmem_a + S::A_COLS * s + 8 * k, desc_sw128(b + k / 4 * (N * 128)) + 2 * (k % 4), IDESC<N>, (at.kt | k) != 0);
+                commit(a_empty + 8 * s);
+                if (at.kt + 1 == tiles) {
+                    commit(d_full + 8 * i);
+                    d++;
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < PG; p++, d++) {
+                    const int i = d % SD;
+                    if (d >= SD) wait(d_empty + 8 * i, (d / SD - 1) & 1, err, a.waits);
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4 / PG; k++)
+                        mma<false>(tmem + i * N, tmem_a + S::A_COLS * s + 8 * (p * (4 / PG) + k), desc_sw128(b) + 2 * (p * (4 / PG) + k), IDESC<N>, k != 0);
+                    commit(d_full + 8 * i);
+                }
+                commit(a_empty + 8 * s);
             }
-            commit(a_empty + 8 * s);
         }
     } else {
         const int row = 32 * q + lane;  // of the row block
-        uint64_t tot[NC / 2];
-        Units at(tiles, rb0, clusters, 0), next = at;
-        uint32_t par[2][PG];
-        auto fetch = [&](uint32_t (&p)[PG]) {  // (lo, step) of the row in the groups of a unit to come
-            const int64_t tile = int64_t(min(next.rb * 8 + row / 16, a.RT - 1)) * a.KT + tile0 + next.kt;
-#pragma unroll
-            for (int g = 0; g < PG; g++) p[g] = __ldg(reinterpret_cast<const uint32_t *>(a.params) + (tile * PG + g) * 16 + row % 16);
-            next.next(1);
+        int done = 0;
+        // y of a row block's tokens, or shares of it: put() for each token, then the row block's end
+        int64_t out = 0;
+        uint32_t share = 0;
+        bool lost = false;
+        auto begin = [&](int rb) {
+            const int half = done & 1;
+            out = int64_t(rb) * 128 + row;
+            share = shares + half * (a.tokens * 512) + row * 4;
+            if (C > 1 && done >= 2) wait_cluster(freed + 8 * half, (done / 2 - 1) & 1, err, a.waits.timeout_ns);
+            lost = *err;
         };
-        fetch(par[0]);
-        if (units > 1) fetch(par[1]);
-        int d = 0, done = 0;
+        auto put = [&](int token, float y) {
+            if (lost) y = __uint_as_float(0x7fffffffu);
+            if (token >= held) return;
+            if (C > 1) asm volatile("st.shared.f32 [%0], %1;" ::"r"(share + token * 512), "f"(y) : "memory");
+            else if (out < a.rows) store_y(a, out, first + token, y);
+        };
+        auto end = [&]() {
+            const int half = done & 1;
+            if (C > 1) {
+                __syncwarp();
+                if (lane < C) arrive_in(ready + 8 * half, lane);
+                wait_cluster(ready + 8 * half, (done / 2) & 1, err, a.waits.timeout_ns);
+                lost = *err;
+                for (int t0 = rank; t0 < held; t0 += 2 * C) {  // (two tokens' shares on their way at once)
+                    float v[2][MAX_CLUSTER];
 #pragma unroll
-        for (int i = 0; i < NC / 2; i++) tot[i] = 0;
-        auto unit = [&](int u, uint32_t (&mine)[PG]) {
+                    for (int i = 0; i < 2; i++)
 #pragma unroll
-            for (int g = 0; g < PG; g++, d++) {
-                const int i = d % SD;
-                const float2 p = __half22float2(kvq_h2(mine[g]));
-                const uint64_t lo = kvq_pair(p.x, p.x), step = kvq_pair(p.y * 512.f, p.y * 512.f);
-                const uint32_t sc = xs.scale + at.kt * (NC * 4), sum = xs.sum + (at.kt * PG + g) * (NC * 4);
-                wait(d_full + 8 * i, (d / SD) & 1, err, a.waits);
+                        for (int b = 0; b < MAX_CLUSTER; b++) v[i][b] = b < C && t0 + i * C < held ? load_in(share + (t0 + i * C) * 512, b) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        float y = 0.f;
+#pragma unroll
+                        for (int b = 0; b < MAX_CLUSTER; b++) y += v[i][b];
+                        if (lost) y = __uint_as_float(0x7fffffffu);
+                        if (t0 + i * C < held && out < a.rows) store_y(a, out, first + t0 + i * C, y);
+                    }
+                }
+                __syncwarp();
+                if (lane < C) arrive_in(freed + 8 * half, lane);
+            }
+            done++;
+        };
+        if constexpr (HALF) {
+            for (int rb = rb0; rb < RB; rb += clusters) {
+                const int i = done % SD;
+                wait(d_full + 8 * i, (done / SD) & 1, err, a.waits);
                 fence_after();
-                const uint32_t from = tmem + TM_D + i * N + (uint32_t(32 * q) << 16);
+                begin(rb);
+                const uint32_t from = tmem + i * N + (uint32_t(32 * q) << 16);
                 uint32_t v[2][8];
                 tm_load8(from, v[0]);
 #pragma unroll
@@ -508,63 +722,88 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
                         if (lane == 0) arrive(d_empty + 8 * i);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        const ulonglong2 f = lds_two_pairs(sc + 4 * (c + e)), s = lds_two_pairs(sum + 4 * (c + e));
-                        uint64_t &t0 = tot[(c + e) / 2], &t1 = tot[(c + e) / 2 + 1];
-                        t0 = kvq_fma2(kvq_mul2(step, f.x), kvq_pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), kvq_fma2(lo, s.x, t0));
-                        t1 = kvq_fma2(kvq_mul2(step, f.y), kvq_pair(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])), kvq_fma2(lo, s.y, t1));
+                    for (int e = 0; e < 8; e++) {
+                        float f;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(scales + 4 * (c + e)) : "memory");
+                        put(c + e, __uint_as_float(w[e]) * f);
                     }
                 }
+                end();
             }
-            if (u + 2 < units) fetch(mine);
-            if (at.kt + 1 == tiles) {  // the row block's end
-                const int64_t out = int64_t(at.rb) * 128 + row;
-                const int half = done & 1;
-                const uint32_t share = shares + half * (a.tokens * 512) + row * 4;
-                if (C > 1 && done >= 2) wait_cluster(freed + 8 * half, (done / 2 - 1) & 1, err, a.waits.timeout_ns);
-                const bool lost = *err;
-                auto put = [&](int token, float y) {
-                    if (lost) y = __uint_as_float(0x7fffffffu);
-                    if (token >= held) return;
-                    if (C > 1) asm volatile("st.shared.f32 [%0], %1;" ::"r"(share + token * 512), "f"(y) : "memory");
-                    else if (out < a.rows) store_y(a, out, first + token, y);
-                };
+        } else {
+            uint64_t tot[NC / 2];
+            Units at(tiles, rb0, clusters, 0), next = at;
+            uint32_t par[2][PG];
+            auto fetch = [&](uint32_t (&p)[PG]) {  // (lo, step) of the row in the groups of a unit to come
+                const int64_t tile = int64_t(min(next.rb * 8 + row / 16, a.RT - 1)) * a.KT + tile0 + next.kt;
 #pragma unroll
-                for (int c = 0; c < NC; c += 4) {
-                    float y[4];
-                    kvq_split(tot[c / 2], y[0], y[1]);
-                    kvq_split(tot[c / 2 + 1], y[2], y[3]);
-                    tot[c / 2] = tot[c / 2 + 1] = 0;
-                    if (a.terms == 1) {
+                for (int g = 0; g < PG; g++) p[g] = __ldg(reinterpret_cast<const uint32_t *>(a.params) + (tile * PG + g) * 16 + row % 16);
+                next.next(1);
+            };
+            fetch(par[0]);
+            if (units > 1) fetch(par[1]);
+            int d = 0;
 #pragma unroll
-                        for (int e = 0; e < 4; e++) put(c + e, y[e]);
-                    } else if (a.terms == 2) {
-                        put(c / 2, y[0] + y[1]);
-                        put(c / 2 + 1, y[2] + y[3]);
-                    } else {
-                        put(c / 4, (y[0] + y[1]) + (y[2] + y[3]));
+            for (int i = 0; i < NC / 2; i++) tot[i] = 0;
+            auto unit = [&](int u, uint32_t (&mine)[PG]) {
+#pragma unroll
+                for (int g = 0; g < PG; g++, d++) {
+                    const int i = d % SD;
+                    const float2 p = __half22float2(kvq_h2(mine[g]));
+                    const uint64_t lo = kvq_pair(p.x, p.x), step = kvq_pair(p.y * 512.f, p.y * 512.f);
+                    const uint32_t sc = scales + at.kt * (NC * 4), sum = sums + (at.kt * PG + g) * (NC * 4);
+                    wait(d_full + 8 * i, (d / SD) & 1, err, a.waits);
+                    fence_after();
+                    const uint32_t from = tmem + i * N + (uint32_t(32 * q) << 16);
+                    uint32_t v[2][8];
+                    tm_load8(from, v[0]);
+#pragma unroll
+                    for (int c = 0; c < NC; c += 8) {
+                        uint32_t (&w)[8] = v[c / 8 % 2];
+                        tm_wait8(w);
+                        if (c + 8 < NC) {
+                            tm_load8(from + c + 8, v[(c / 8 + 1) % 2]);
+                        } else {
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive(d_empty + 8 * i);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const ulonglong2 f = lds_two_pairs(sc + 4 * (c + e)), x = lds_two_pairs(sum + 4 * (c + e));
+                            uint64_t &t0 = tot[(c + e) / 2], &t1 = tot[(c + e) / 2 + 1];
+                            t0 = kvq_fma2(kvq_mul2(step, f.x), kvq_pair(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), kvq_fma2(lo, x.x, t0));
+                            t1 = kvq_fma2(kvq_mul2(step, f.y), kvq_pair(__uint_as_float(w[e + 2]), __uint_as_float(w[e + 3])), kvq_fma2(lo, x.y, t1));
+                        }
                     }
                 }
-                if (C > 1) {
-                    __syncwarp();
-                    if (lane < C) arrive_in(ready + 8 * half, lane);
-                    wait_cluster(ready + 8 * half, (done / 2) & 1, err, a.waits.timeout_ns);
-                    for (int token = rank; token < held; token += C) {
-                        float y = 0.f;
-                        for (int b = 0; b < C; b++) y += load_in(share + token * 512, b);
-                        if (*err) y = __uint_as_float(0x7fffffffu);
-                        if (out < a.rows) store_y(a, out, first + token, y);
+                if (u + 2 < units) fetch(mine);
+                if (at.kt + 1 == tiles) {
+                    begin(at.rb);
+#pragma unroll
+                    for (int c = 0; c < NC; c += 4) {
+                        float y[4];
+                        kvq_split(tot[c / 2], y[0], y[1]);
+                        kvq_split(tot[c / 2 + 1], y[2], y[3]);
+                        tot[c / 2] = tot[c / 2 + 1] = 0;
+                        if (a.terms == 1) {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) put(c + e, y[e]);
+                        } else if (a.terms == 2) {
+                            put(c / 2, y[0] + y[1]);
+                            put(c / 2 + 1, y[2] + y[3]);
+                        } else {
+                            put(c / 4, (y[0] + y[1]) + (y[2] + y[3]));
+                        }
                     }
-                    __syncwarp();
-                    if (lane < C) arrive_in(freed + 8 * half, lane);
+                    end();
                 }
-                done++;
+                at.next(1);
+            };
+            for (int u = 0; u < units; u += 2) {
+                unit(u, par[0]);
+                if (u + 1 < units) unit(u + 1, par[1]);
             }
-            at.next(1);
-        };
-        for (int u = 0; u < units; u += 2) {
-            unit(u, par[0]);
-            if (u + 1 < units) unit(u + 1, par[1]);
         }
         fence_before();
     }
@@ -580,14 +819,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
     if (warp == W_MMA) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
 }
 
-template <int NC, int PG>
+template <int NC, int PG, bool HALF>
 int smem_bytes(int slice, int depth, int cluster, int tokens) {
-    return 1024 + (XSlice<NC, PG>::bytes(slice) + 15) / 16 * 16 + UNPACK * depth * 2048 + (cluster > 1 ? 2 * tokens * 512 : 0);
+    using S = Shape<NC, PG, HALF>;
+    return 1024 + (S::x_bytes(slice) + 15) / 16 * 16 + UNPACK * depth * S::SLOT + (cluster > 1 ? 2 * tokens * 512 : 0);
 }
 
 // Clusters of c blocks, one an SM, that the device holds at a time (c = 8: fewer than SMs / 8, by the SMs of a GPC).
 int clusters_of(const void *kernel, int c, int nsm) {
-    static std::atomic<int> known[4];  // (of 1, 2, 4, 8; every device here is alike)
+    static std::atomic<int> known[4];  // (of 1, 2, 4, 8; every device is alike)
     const int at = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : 3;
     if (c == 1) return nsm;
     int n = known[at].load(std::memory_order_relaxed);
@@ -609,9 +849,9 @@ int clusters_of(const void *kernel, int c, int nsm) {
     return n;
 }
 
-template <int NC, int PG>
+template <int NC, int PG, bool HALF>
 int launch(const TcArgs &in, int nsm, cudaStream_t st) {
-    const void *kernel = reinterpret_cast<const void *>(k_qmat_tc<NC, PG>);
+    const void *kernel = reinterpret_cast<const void *>(k_qmat_tc<NC, PG, HALF>);
     if (!allow_smem(kernel, MAX_SMEM)) return LL_ERR_CUDA;
     // Blocks that share the columns, by the units of the busiest block: what fits, then the fewest steps, with
     // 2 for a row block's end, 4 where shares meet.
@@ -624,8 +864,8 @@ int launch(const TcArgs &in, int nsm, cudaStream_t st) {
         const int slice = (in.KT + c - 1) / c;
         if ((c - 1) * slice >= in.KT) break;  // (a block without a tile)
         int depth = 8;
-        while (depth > 2 && smem_bytes<NC, PG>(slice, depth, c, in.tokens) > MAX_SMEM) depth--;
-        if (smem_bytes<NC, PG>(slice, depth, c, in.tokens) > MAX_SMEM) continue;
+        while (depth > 2 && smem_bytes<NC, PG, HALF>(slice, depth, c, in.tokens) > MAX_SMEM) depth--;
+        if (smem_bytes<NC, PG, HALF>(slice, depth, c, in.tokens) > MAX_SMEM) continue;
         const int held = clusters_of(kernel, c, nsm);
         const int64_t rounds = (RB + held - 1) / held, steps = rounds * (slice + (c > 1 ? 4 : 2)) + (depth < 4 ? slice : 0);
         if (steps < best) {
@@ -640,19 +880,23 @@ int launch(const TcArgs &in, int nsm, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(RB, at_once) * a.cluster, (a.n + a.tokens - 1) / a.tokens);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = smem_bytes<NC, PG>(a.slice, a.depth, a.cluster, a.tokens);
+    cfg.dynamicSmemBytes = smem_bytes<NC, PG, HALF>(a.slice, a.depth, a.cluster, a.tokens);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {unsigned(a.cluster), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_qmat_tc<NC, PG>, a) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k_qmat_tc<NC, PG, HALF>, a) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
-template <int NC>
+template <int NC, bool HALF>
 int launch_pg(const TcArgs &a, int pg, int nsm, cudaStream_t st) {
-    return pg == 1 ? launch<NC, 1>(a, nsm, st) : pg == 2 ? launch<NC, 2>(a, nsm, st) : launch<NC, 4>(a, nsm, st);
+    return pg == 1 ? launch<NC, 1, HALF>(a, nsm, st) : pg == 2 ? launch<NC, 2, HALF>(a, nsm, st) : launch<NC, 4, HALF>(a, nsm, st);
+}
+template <bool HALF>
+int launch_nc(const TcArgs &a, int nc, int pg, int nsm, cudaStream_t st) {
+    return nc == 64 ? launch_pg<64, HALF>(a, pg, nsm, st) : nc == 32 ? launch_pg<32, HALF>(a, pg, nsm, st) : launch_pg<16, HALF>(a, pg, nsm, st);
 }
 
 }  // namespace
@@ -680,13 +924,13 @@ int launch_qmat_tc(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add
     a.y_stride = y.stride;
     a.y_f32 = y.type == LL_F32;
     a.n = n;
-    a.terms = x.type == LL_F32 ? 4 : x.type == LL_BF16 ? 2 : 1;
+    const bool half = !a.y_f32 && x.type != LL_F32;
+    a.terms = half ? 1 : x.type == LL_F32 ? 4 : x.type == LL_BF16 ? 2 : 1;
     const int pg = QM_TILE_COLS / m.group;
     // As many columns of x a pass as there are, up to 64; fewer where they do not fit.
-    for (int nc = n * a.terms <= 8 ? 8 : n * a.terms <= 16 ? 16 : n * a.terms <= 32 ? 32 : 64; nc >= 8; nc /= 2) {
+    for (int nc = n * a.terms <= 16 ? 16 : n * a.terms <= 32 ? 32 : 64; nc >= 16; nc /= 2) {
         a.tokens = nc / a.terms;
-        const int rc = nc == 64 ? launch_pg<64>(a, pg, nsm, st) : nc == 32 ? launch_pg<32>(a, pg, nsm, st)
-                     : nc == 16 ? launch_pg<16>(a, pg, nsm, st) : launch_pg<8>(a, pg, nsm, st);
+        const int rc = half ? launch_nc<true>(a, nc, pg, nsm, st) : launch_nc<false>(a, nc, pg, nsm, st);
         if (rc != LL_ERR_SHAPE) return rc;
     }
     return LL_ERR_SHAPE;

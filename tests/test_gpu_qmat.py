@@ -119,6 +119,7 @@ def test_integers_are_exact(rows, cols, n, kind):
     assert float((wide.abs() @ (lo.abs() + step * code + 16 * step).t()).max()) < 2 ** 24
     got = m.matvec(xs, scale=scale, out_dtype=torch.float32)
     assert torch.equal(got.cpu().double(), want)
+    assert torch.equal(m.matvec(xs, scale=scale).cpu(), want.float().bfloat16())  # (one rounding of the exact sum)
     add = torch.randint(-9, 9, (n, rows), generator=g).double()
     got = m.matvec(xs, scale=scale, add=add.float().cuda())
     assert torch.equal(got.cpu().double(), want + add)
