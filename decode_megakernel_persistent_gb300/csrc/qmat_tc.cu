@@ -194,9 +194,9 @@ __device__ __forceinline__ uint32_t in_block(uint32_t at, int rank) {  // a shar
 __device__ __forceinline__ void arrive_in(uint32_t bar, int rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_block(bar, rank)) : "memory");
 }
-__device__ __forceinline__ float load_in(uint32_t at, int rank) {
+__device__ __forceinline__ float load_in(uint32_t at) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(in_block(at, rank)) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
     return v;
 }
 __device__ __forceinline__ void cluster_sync() {  // (by whole warps)
@@ -231,60 +231,73 @@ __device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t *r) {
 __device__ __forceinline__ void tm_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 8 values of a row of x from column k on, as they lie in memory, zeros past the end.
-__device__ __forceinline__ void load_raw(const TcArgs &a, int64_t row, int k, uint4 (&raw)[2]) {
-    const int size = a.x_type == LL_F32 ? 4 : a.x_type == LL_BF16 ? 2 : 1;
-    raw[0] = raw[1] = make_uint4(0, 0, 0, 0);
-    if (k >= a.cols) return;
-    const char *p = static_cast<const char *>(a.x) + (row * a.x_stride + k) * size;
-    if (a.vec && k + 8 <= a.cols) {
-        if (size == 1) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-            raw[0].x = w.x;
-            raw[0].y = w.y;
+template <int XT>
+struct Raw {
+    static constexpr int SIZE = XT == LL_F32 ? 4 : XT == LL_BF16 ? 2 : 1, WORDS = 2 * SIZE;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void widen(float (&v)[8]) const {
+        if constexpr (XT == LL_BF16) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+        } else if constexpr (XT == LL_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
         } else {
-            raw[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-            if (size == 4) raw[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-        }
-    } else {
-        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            if (k + j >= a.cols) continue;
-            if (size == 4) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
-            else if (size == 2) w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t *>(p)[j]) << (16 * (j % 2));
-            else w[j / 4] |= uint32_t(reinterpret_cast<const uint8_t *>(p)[j]) << (8 * (j % 4));
-        }
-        raw[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        raw[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-__device__ __forceinline__ void widen(const TcArgs &a, const uint4 (&r)[2], float (&v)[8]) {
-    const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-    if (a.x_type == LL_BF16) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-    } else if (a.x_type == LL_F32) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = __uint_as_float(w[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = from_e4m3(w[j / 2] >> (16 * (j % 2)));
-            v[2 * j] = f.x;
-            v[2 * j + 1] = f.y;
+            for (int j = 0; j < 4; j++) {
+                const float2 f = from_e4m3(w[j / 2] >> (16 * (j % 2)));
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
+            }
         }
     }
+};
+template <int XT>
+__device__ __noinline__ Raw<XT> load_edge(const char *p, int n) {  // (rows that are not aligned, a row's end)
+    Raw<XT> r;
+#pragma unroll
+    for (int j = 0; j < Raw<XT>::WORDS; j++) r.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        if (j >= n) continue;
+        if constexpr (XT == LL_F32) r.w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+        else if constexpr (XT == LL_BF16) r.w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t *>(p)[j]) << (16 * (j % 2));
+        else r.w[j / 4] |= uint32_t(reinterpret_cast<const uint8_t *>(p)[j]) << (8 * (j % 4));
+    }
+    return r;
 }
+template <int XT>
+__device__ __forceinline__ void load_raw(const TcArgs &a, int64_t row, int k, Raw<XT> &r) {
+    const char *p = static_cast<const char *>(a.x) + (row * a.x_stride + k) * Raw<XT>::SIZE;
+    if (a.vec && k + 8 <= a.cols) {
+        if constexpr (XT == LL_E4M3) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            r.w[0] = u.x;
+            r.w[1] = u.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < Raw<XT>::SIZE / 2; j++) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + j);
+                r.w[4 * j] = u.x; r.w[4 * j + 1] = u.y; r.w[4 * j + 2] = u.z; r.w[4 * j + 3] = u.w;
+            }
+        }
+    } else {
+        r = load_edge<XT>(p, a.cols - k);
+    }
+}
+// e / d by 1 / d in fp32: exact for the sizes here (e below 2^16: (e + 1/2) / d is 1 / (2 d) away from any integer).
+__device__ __forceinline__ int quotient(int e, float per) { return int((float(e) + 0.5f) * per); }
 constexpr int BATCH = 4;  // tokens' tiles of a thread on their way at once
 
 // HALF: a token's columns in fp16, largest values of the block's columns to [2^14, 2^15). First the largest of each
 // token go round (a token's tile to 16 threads), then the values are rounded.
-template <int NC, int PG>
+template <int XT, int NC, int PG>
 __device__ __forceinline__ void stage_half(const TcArgs &a, uint32_t operand, int first, int tile0, int tiles) {
     using S = Shape<NC, PG, true>;
     const uint32_t scales = operand + a.slice * S::TILE, tops = scales + NC * 4;
     const int u = threadIdx.x % 16, step = THREADS / 16;
     const int held = min(a.tokens, a.n - first), items = tiles * held;
+    const float per = 1.f / float(tiles);
     const unsigned mates = 0xffffu << (threadIdx.x & 16);
     for (int i = threadIdx.x; i < NC; i += THREADS) asm volatile("st.shared.u32 [%0], %1;" ::"r"(tops + 4 * i), "r"(0) : "memory");
     __syncthreads();
@@ -292,21 +305,21 @@ __device__ __forceinline__ void stage_half(const TcArgs &a, uint32_t operand, in
     for (int pass = 0; pass < 2; pass++) {
 #pragma unroll 1
         for (int e0 = threadIdx.x / 16; e0 < items; e0 += BATCH * step) {
-            uint4 raws[BATCH][2];
+            Raw<XT> raws[BATCH];
             float factor[BATCH];
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
-                const int e = min(e0 + i * step, items - 1), kt = e / held, token = e % held;
+                const int e = min(e0 + i * step, items - 1), token = quotient(e, per), kt = e - token * tiles;
                 load_raw(a, first + token, (tile0 + kt) * QM_TILE_COLS + 8 * u, raws[i]);
-                factor[i] = a.x_type == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
+                factor[i] = XT == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
             }
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
                 const int e = e0 + i * step;
                 if (e >= items) break;  // (16 threads alike)
-                const int kt = e / held, token = e % held;
+                const int token = quotient(e, per), kt = e - token * tiles;
                 float v[8];
-                widen(a, raws[i], v);
+                raws[i].widen(v);
 #pragma unroll
                 for (int j = 0; j < 8; j++) v[j] *= factor[i];
                 if (pass == 0) {
@@ -344,29 +357,30 @@ __device__ __forceinline__ void stage_half(const TcArgs &a, uint32_t operand, in
 
 // 16 threads turn a token's 128 columns of a tile into the operand: thread u has columns 8 u .. 8 u + 7, 8 bytes of a row of 128 (the
 // order of a word's codes as they are unpacked: columns 0, 4, 1, 5 and 2, 6, 3, 7 of the 8).
-template <int NC, int PG>
+template <int XT, int NC, int PG>
 __device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int first, int tile0, int tiles) {
     using S = Shape<NC, PG, false>;
     const uint32_t scales = operand + a.slice * S::TILE, sums = scales + a.slice * NC * 4;
     const int u = threadIdx.x % 16, step = THREADS / 16;
     const int held = min(a.tokens, a.n - first), items = tiles * held;
+    const float per = 1.f / float(tiles);
 #pragma unroll 1
     for (int e0 = threadIdx.x / 16; e0 < items; e0 += BATCH * step) {
-    uint4 raws[BATCH][2];
+    Raw<XT> raws[BATCH];
     float factor[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; i++) {
-        const int e = min(e0 + i * step, items - 1), kt = e / held, token = e % held;
+        const int e = min(e0 + i * step, items - 1), token = quotient(e, per), kt = e - token * tiles;
         load_raw(a, first + token, (tile0 + kt) * QM_TILE_COLS + 8 * u, raws[i]);
-        factor[i] = a.x_type == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
+        factor[i] = XT == LL_E4M3 ? __ldg(a.scale + int64_t(first + token) * a.scale_row + (tile0 + kt) * a.scale_step) : 1.f;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; i++) {
         const int e = e0 + i * step;
         if (e >= items) break;  // (16 threads alike)
-        const int kt = e / held, token = e % held;
+        const int token = quotient(e, per), kt = e - token * tiles;
         float v[8];
-        widen(a, raws[i], v);
+        raws[i].widen(v);
         const unsigned mates = 0xffffu << (threadIdx.x & 16);
         float scale, sum = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         const int col0 = token * a.terms;
@@ -375,9 +389,9 @@ __device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int f
             const uint32_t at = tile + col * 128 + ((u / 2 ^ (col & 7)) << 4) + u % 2 * 8;  // (the 128-byte swizzle)
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(__byte_perm(w0, w1, 0x5140)), "r"(__byte_perm(w0, w1, 0x7362)) : "memory");
         };
-        if (a.x_type == LL_E4M3) {
+        if constexpr (XT == LL_E4M3) {
             scale = factor[i];
-            store(col0, raws[i][0].x, raws[i][0].y);
+            store(col0, raws[i].w[0], raws[i].w[1]);
             sum *= scale;
         } else {
             uint32_t top = 0;  // the largest exponent of finite values
@@ -411,7 +425,7 @@ __device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int f
         }
 #pragma unroll
         for (int o = 1; o < 16 / PG; o *= 2) sum += __shfl_xor_sync(mates, sum, o);
-        if (a.x_type == LL_E4M3 && u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + (kt * NC + col0) * 4), "f"(scale) : "memory");
+        if (XT == LL_E4M3 && u == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales + (kt * NC + col0) * 4), "f"(scale) : "memory");
         if (u % (16 / PG) == 0) {
             const uint32_t at = sums + ((kt * PG + u / (16 / PG)) * NC + col0) * 4;
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(sum) : "memory");
@@ -421,14 +435,25 @@ __device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int f
     }
 }
 
-__device__ __forceinline__ void store_y(const TcArgs &a, int64_t row, int token, float y) {
-    const int64_t at = token * a.y_stride + row, from = token * a.add_stride + row;
-    if (a.y_f32) {
-        if (a.add) y += static_cast<const float *>(a.add)[from];
-        static_cast<float *>(a.y)[at] = y;
-    } else {
-        if (a.add) y += __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[from]);
-        static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(y);
+// y of a row for up to 8 tokens, n of them held.
+__device__ __forceinline__ void store_8(const TcArgs &a, int64_t row, int token, int n, const uint32_t (&y)[8]) {
+    if (row >= a.rows) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = __uint_as_float(y[e]);
+    if (a.add) {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int64_t from = int64_t(token + min(e, n - 1)) * a.add_stride + row;
+            v[e] += a.y_f32 ? static_cast<const float *>(a.add)[from] : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.add)[from]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        const int64_t at = int64_t(token + e) * a.y_stride + row;
+        if (e >= n) continue;
+        if (a.y_f32) static_cast<float *>(a.y)[at] = v[e];
+        else static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v[e]);
     }
 }
 
@@ -540,8 +565,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sptr(&s_tmem)), "n"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if constexpr (HALF) stage_half<NC, PG>(a, operand, first, tile0, tiles);
-    else stage_x<NC, PG>(a, operand, first, tile0, tiles);
+    if constexpr (HALF) {
+        if (a.x_type == LL_BF16) stage_half<LL_BF16, NC, PG>(a, operand, first, tile0, tiles);
+        else stage_half<LL_E4M3, NC, PG>(a, operand, first, tile0, tiles);
+    } else {
+        if (a.x_type == LL_BF16) stage_x<LL_BF16, NC, PG>(a, operand, first, tile0, tiles);
+        else if (a.x_type == LL_F32) stage_x<LL_F32, NC, PG>(a, operand, first, tile0, tiles);
+        else stage_x<LL_E4M3, NC, PG>(a, operand, first, tile0, tiles);
+    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     fence_before();
     if (C > 1) cluster_sync();  // (others arrive at this block's barriers)
@@ -657,22 +688,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
     } else {
         const int row = 32 * q + lane;  // of the row block
         int done = 0;
-        // y of a row block's tokens, or shares of it: put() for each token, then the row block's end
+        // a row block's outputs, or shares of them: begin(), put() for each token (HALF: as they come), then end()
         int64_t out = 0;
         uint32_t share = 0;
         bool lost = false;
         auto begin = [&](int rb) {
             const int half = done & 1;
             out = int64_t(rb) * 128 + row;
-            share = shares + half * (a.tokens * 512) + row * 4;
+            share = shares + half * (a.tokens * 512) + row * 4;  // (columns past the last token: nobody's)
             if (C > 1 && done >= 2) wait_cluster(freed + 8 * half, (done / 2 - 1) & 1, err, a.waits.timeout_ns);
             lost = *err;
         };
         auto put = [&](int token, float y) {
             if (lost) y = __uint_as_float(0x7fffffffu);
-            if (token >= held) return;
-            if (C > 1) asm volatile("st.shared.f32 [%0], %1;" ::"r"(share + token * 512), "f"(y) : "memory");
-            else if (out < a.rows) store_y(a, out, first + token, y);
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(share + token * 512), "f"(y) : "memory");
         };
         auto end = [&]() {
             const int half = done & 1;
@@ -681,23 +710,33 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
                 if (lane < C) arrive_in(ready + 8 * half, lane);
                 wait_cluster(ready + 8 * half, (done / 2) & 1, err, a.waits.timeout_ns);
                 lost = *err;
-                for (int t0 = rank; t0 < held; t0 += 2 * C) {  // (two tokens' shares on their way at once)
-                    float v[2][MAX_CLUSTER];
+                // this block's eighth (or so) of the tokens, 8 on their way at once
+                const int mine = (held + C - 1) / C, t1 = min(held, (rank + 1) * mine);
+#pragma unroll 1
+                for (int t0 = rank * mine; t0 < t1; t0 += 8) {
+                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int b = 0; b < C; b++) {
+                        const uint32_t at = in_block(share + t0 * 512, b);
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
-#pragma unroll
-                        for (int b = 0; b < MAX_CLUSTER; b++) v[i][b] = b < C && t0 + i * C < held ? load_in(share + (t0 + i * C) * 512, b) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        float y = 0.f;
-#pragma unroll
-                        for (int b = 0; b < MAX_CLUSTER; b++) y += v[i][b];
-                        if (lost) y = __uint_as_float(0x7fffffffu);
-                        if (t0 + i * C < held && out < a.rows) store_y(a, out, first + t0 + i * C, y);
+                        for (int i = 0; i < 8; i++) y[i] += load_in(at + min(i, t1 - 1 - t0) * 512);
                     }
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) w[i] = lost ? 0x7fffffffu : __float_as_uint(y[i]);
+                    store_8(a, out, first + t0, t1 - t0, w);
                 }
                 __syncwarp();
                 if (lane < C) arrive_in(freed + 8 * half, lane);
+            } else if (!HALF) {  // (a thread's own row)
+#pragma unroll 1
+                for (int t0 = 0; t0 < held; t0 += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[e]) : "r"(share + min(t0 + e, held - 1) * 512) : "memory");
+                    store_8(a, out, first + t0, held - t0, w);
+                }
             }
             done++;
         };
@@ -708,26 +747,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
                 fence_after();
                 begin(rb);
                 const uint32_t from = tmem + i * N + (uint32_t(32 * q) << 16);
-                uint32_t v[2][8];
-                tm_load8(from, v[0]);
-#pragma unroll
+                // (a loop and not NC / 8 copies of it: code that runs once a row block comes slower than it runs)
+#pragma unroll 1
                 for (int c = 0; c < NC; c += 8) {
-                    uint32_t (&w)[8] = v[c / 8 % 2];
+                    uint32_t w[8];
+                    tm_load8(from + c, w);
                     tm_wait8(w);
-                    if (c + 8 < NC) {
-                        tm_load8(from + c + 8, v[(c / 8 + 1) % 2]);
-                    } else {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive(d_empty + 8 * i);
-                    }
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         float f;
                         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(scales + 4 * (c + e)) : "memory");
-                        put(c + e, __uint_as_float(w[e]) * f);
+                        w[e] = __float_as_uint(lost ? __uint_as_float(0x7fffffffu) : __uint_as_float(w[e]) * f);
+                    }
+                    if (C > 1) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++) asm volatile("st.shared.u32 [%0], %1;" ::"r"(share + (c + e) * 512), "r"(w[e]) : "memory");
+                    } else {
+                        store_8(a, out, first + c, held - c, w);
                     }
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(d_empty + 8 * i);
                 end();
             }
         } else {
@@ -822,7 +863,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
 template <int NC, int PG, bool HALF>
 int smem_bytes(int slice, int depth, int cluster, int tokens) {
     using S = Shape<NC, PG, HALF>;
-    return 1024 + (S::x_bytes(slice) + 15) / 16 * 16 + UNPACK * depth * S::SLOT + (cluster > 1 ? 2 * tokens * 512 : 0);
+    return 1024 + (S::x_bytes(slice) + 15) / 16 * 16 + UNPACK * depth * S::SLOT + (cluster > 1 || !HALF ? 2 * tokens * 512 : 0);
 }
 
 // Clusters of c blocks, one an SM, that the device holds at a time (c = 8: fewer than SMs / 8, by the SMs of a GPC).
