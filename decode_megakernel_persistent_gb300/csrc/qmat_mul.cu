@@ -33,7 +33,7 @@ struct MvArgs {
     int64_t y_stride;
     bool y_f32;
     int n;
-    int splits;             // warps that share a row tile's columns, a divisor of MV_WARPS
+    int log_splits;         // 2^this warps share a row tile's columns, a divisor of MV_WARPS
 };
 
 constexpr int MV_WARPS = 8;
@@ -50,6 +50,18 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// D = A B: the first product of a group.
+template <bool HALF>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
@@ -78,9 +90,10 @@ struct Column {
         term = c % TERMS;
         row = static_cast<const char *>(a.x) + int64_t(min(first + c / TERMS, a.n - 1)) * a.x_stride * SIZE + 8 * t * SIZE;
     }
+    __device__ __forceinline__ Column() {}
     // The lane's 8 values of word j of the tile from column k0 on, as four pairs.
-    __device__ __forceinline__ void load(const MvArgs &a, int k0, int j, int t, bool whole, uint32_t (&b)[4]) const {
-        const char *p = row + (k0 + 32 * j) * SIZE;
+    __device__ __forceinline__ void load(const MvArgs &a, const char *at, int k0, int j, int t, bool whole, uint32_t (&b)[4]) const {
+        const char *p = at + 32 * j * SIZE;
         uint32_t w[2 * SIZE];
         if (whole) {
             if constexpr (SIZE == 1) {
@@ -151,10 +164,10 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
     extern __shared__ __align__(16) uint8_t ring[];  // [warp][DEPTH][R][STAGE]
     __shared__ float part[2][MV_WARPS][ROWS][8 * NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int ks = warp % a.splits, team = warp / a.splits, teams = MV_WARPS / a.splits;
+    const int splits = 1 << a.log_splits, ks = warp & (splits - 1), team = warp >> a.log_splits, teams = MV_WARPS >> a.log_splits;
     const int groups = (a.RT + R - 1) / R, stride = gridDim.x * teams;
     const int first = blockIdx.y * TOKENS;
-    const int own = (a.KT - ks + a.splits - 1) / a.splits;  // (splits <= KT: 1 at least)
+    const int own = (a.KT - ks + splits - 1) >> a.log_splits;  // (splits <= KT: 1 at least)
     const uint32_t stages = uint32_t(__cvta_generic_to_shared(ring)) + warp * (DEPTH * R * STAGE);
     uint32_t magic;
     asm volatile("mov.b32 %0, %1;" : "=r"(magic) : "n"(HALF ? 0x4c004c00 : 0x41804180));
@@ -180,8 +193,8 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
                 copy16(to, code_at[r]);
                 copy16(to + 512, code_at[r] + 32);
                 if (lane < 4 * PG) copy16(to + 1024, param_at[r]);
-                code_at[r] += 64 * a.splits;
-                param_at[r] += 4 * PG * a.splits;
+                code_at[r] += 64 * splits;
+                param_at[r] += 4 * PG * splits;
             }
             if (++next_k == own) {
                 next_k = 0;
@@ -197,7 +210,14 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
     for (int i = 0; i < DEPTH - 1; i++) issue();
 
     int stage = 0, parity = 0;
+    Column<XT> col[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) col[nt] = Column<XT>(a, nt * 8 + g, first, t);
+    const bool all_whole = a.vec && a.cols % QM_TILE_COLS == 0;
     for (int group = g0; group < groups; group += stride) {
+        const char *at_x[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) at_x[nt] = col[nt].row + ks * QM_TILE_COLS * Column<XT>::SIZE;
         float tot[R][NT][4];
 #pragma unroll
         for (int r = 0; r < R; r++)
@@ -207,14 +227,14 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
                 for (int i = 0; i < 4; i++) tot[r][nt][i] = 0.f;
 #pragma unroll 1
         for (int k = 0; k < own; k++) {
-            const int kt = ks + k * a.splits, k0 = kt * QM_TILE_COLS;
+            const int kt = ks + k * splits, k0 = kt * QM_TILE_COLS;
             uint32_t b[NT][4][4];
-            const bool whole = a.vec && k0 + QM_TILE_COLS <= a.cols;
+            const bool whole = all_whole || (a.vec && k0 + QM_TILE_COLS <= a.cols);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                const Column<XT> col(a, nt * 8 + g, first, t);
 #pragma unroll
-                for (int j = 0; j < 4; j++) col.load(a, k0, j, t, whole, b[nt][j]);
+                for (int j = 0; j < 4; j++) col[nt].load(a, at_x[nt], k0, j, t, whole, b[nt][j]);
+                at_x[nt] += splits * (QM_TILE_COLS * Column<XT>::SIZE);
             }
             issue();
             asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
@@ -229,27 +249,24 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
             float acc[R][NT][4], ones[NT][4];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                if ((j * PG) % 4 == 0) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            ones[nt][i] = 0.f;
-#pragma unroll
-                            for (int r = 0; r < R; r++) acc[r][nt][i] = 0.f;
-                        }
-                }
 #pragma unroll
                 for (int m = 0; m < 2; m++) {
+                    const bool begins = (j * PG) % 4 == 0 && m == 0;
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) mma<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                    for (int nt = 0; nt < NT; nt++) {
+                        if (begins) mma_first<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][0], b[nt][j][1]);
+                        else mma<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                    }
 #pragma unroll
                     for (int r = 0; r < R; r++) {
                         const uint32_t lo = (&c[r][0].x)[j], hi = (&c[r][1].x)[j];
                         const uint32_t a0 = qm_codes<HALF, EXACT>(lo, 2 * m, magic), a1 = qm_codes<HALF, EXACT>(hi, 2 * m, magic);
                         const uint32_t a2 = qm_codes<HALF, EXACT>(lo, 2 * m + 1, magic), a3 = qm_codes<HALF, EXACT>(hi, 2 * m + 1, magic);
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++) mma<HALF>(acc[r][nt], a0, a1, a2, a3, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                        for (int nt = 0; nt < NT; nt++) {
+                            if (begins) mma_first<HALF>(acc[r][nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+                            else mma<HALF>(acc[r][nt], a0, a1, a2, a3, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                        }
                     }
                 }
                 if (((j + 1) * PG) % 4 != 0) continue;
@@ -294,16 +311,16 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
 #pragma unroll
                 for (int i = 0; i < 4; i++) part[parity][warp][r * QM_TILE_ROWS + g + 8 * (i / 2)][nt * 8 + 2 * t + (i & 1)] = tot[r][nt][i];
         // (the shares of the group before last lie in the other half: one barrier a group)
-        if (a.splits == 1) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * a.splits) : "memory");
-        for (int e = ks * 32 + lane; e < ROWS * min(TOKENS, a.n - first); e += 32 * a.splits) {
+        if (splits == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * splits) : "memory");
+        for (int e = ks * 32 + lane; e < ROWS * min(TOKENS, a.n - first); e += 32 * splits) {
             const int in = e % ROWS, token = e / ROWS;
             const int64_t row = int64_t(group) * ROWS + in;
             if (row >= a.rows) continue;
             float y = 0.f;
-            for (int s = 0; s < a.splits; s++)
+            for (int s = 0; s < splits; s++)
 #pragma unroll
-                for (int u = TERMS - 1; u >= 0; u--) y += part[parity][team * a.splits + s][in][token * TERMS + u];
+                for (int u = TERMS - 1; u >= 0; u--) y += part[parity][team * splits + s][in][token * TERMS + u];
             const int64_t to = int64_t(first + token) * a.y_stride + row, from = int64_t(first + token) * a.add_stride + row;
             if (a.y_f32) {
                 if (a.add) y += static_cast<const float *>(a.add)[from];
@@ -326,12 +343,13 @@ int launch_mv(const MvArgs &a, int nsm, cudaStream_t st) {
     // splits by the steps of the busiest warp: its tiles, and 2 a group for the shares' barrier
     const int tiles = (a.RT + R - 1) / R, blocks = MvGeo<NT>::BLOCKS * nsm;
     int64_t best = INT64_MAX;
-    for (int splits = 1; splits <= MV_WARPS && splits <= a.KT; splits *= 2) {
+    for (int log = 0; 1 << log <= MV_WARPS && 1 << log <= a.KT; log++) {
+        const int splits = 1 << log;
         const int64_t slots = int64_t(blocks) * (MV_WARPS / splits), rounds = (tiles + slots - 1) / slots;
         const int64_t steps = rounds * ((a.KT + splits - 1) / splits * R + (splits > 1 ? 2 : 1));
         if (steps < best) {
             best = steps;
-            b.splits = splits;
+            b.log_splits = log;
         }
     }
     // (fewer groups than slots: one a block before two in one)

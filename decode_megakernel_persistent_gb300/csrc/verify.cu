@@ -26,8 +26,11 @@ namespace {
 
 constexpr int VF_THREADS = 512, VF_WARPS = VF_THREADS / 32;
 constexpr int VF_CLUSTER = 16;
+constexpr int VF_ROWS = 8;               // rows of a step, at most
+constexpr int VF_PIECES = 8 * 24;        // pieces of a step: of 1024 places, or 512 of a single row's
 constexpr int VF_STEP = 4;               // neighbouring logits of a lane
 constexpr int VF_MAX_VOCAB = 393216;     // a slice's weights (8 bytes each) fit in shared memory
+constexpr int VF_WINDOWS = VF_MAX_VOCAB / VF_CLUSTER / VF_WARPS / 128;
 constexpr double LN2 = 0.693147180559945309417232, LOG2E = 1.442695040888963407359925;
 
 struct VfArgs {
@@ -38,7 +41,8 @@ struct VfArgs {
     int64_t probs_seq, probs_row;
     const float *u, *temperature;
     int32_t n_draft, vocab, slice;  // slice: a multiple of VF_STEP
-    bool vec;                       // rows take whole-step loads
+    int32_t log_rows, piece;        // 2^this rows a step; places of a warp's piece of one
+    bool vec, vec_probs;            // rows take whole-step loads
     int32_t *tokens, *accepted;
 };
 
@@ -58,19 +62,24 @@ __device__ __forceinline__ Two mul(Two a, Two b) {
     return {p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi)};
 }
 
-// 2^(j / 32), j < 32, by the series of e^(j ln 2 / 32).
-__device__ Two root_of_two(int j) {
-    constexpr float H = float(LN2 / 32), L = float(LN2 / 32 - double(H));
-    const Two z = mul({float(j), 0.f}, {H, L});
-    Two sum = {1.f, 0.f};
-    for (int k = 24; k > 0; k--) {  // 1 + z / k (1 + z / (k + 1) (...)): z^24 / 24! is below 2^-90
-        const float inv = 1.f / float(k);
-        const Two t = mul(mul(z, sum), {inv, fmaf(-float(k), inv, 1.f) * inv});
-        const Two s = two_sum(1.f, t.hi);
-        sum = fast_two_sum(s.hi, s.lo + t.lo);
+// 2^(j / 32), j < 32, by the series of e^(j ln 2 / 32) in 64 bits, as two fp32.
+struct Roots {
+    float hi[32], lo[32];
+};
+constexpr Roots make_roots() {
+    Roots r = {};
+    for (int j = 0; j < 32; j++) {
+        double term = 1, sum = 1;
+        for (int k = 1; k < 24; k++) {  // z^24 / 24! is below 2^-90
+            term *= LN2 / 32 * j / k;
+            sum += term;
+        }
+        r.hi[j] = float(sum);
+        r.lo[j] = float(sum - double(r.hi[j]));
     }
-    return sum;
+    return r;
 }
+__constant__ const Roots ROOTS = make_roots();
 
 // e^((l - m) / T) for l <= m, c = log2(e) / T, off by some 2^-45 of itself: 2^(k + j / 32) from the table times
 // e^z, |z| <= ln 2 / 64, of which 1, z and z^2 / 2 are held in two fp32. Below 2^-50: 0.
@@ -132,38 +141,45 @@ struct Stat {
     float m, sum;
     int at;
 };
+__device__ __forceinline__ Stat nothing() { return {-INFINITY, 0.f, 0x7fffffff}; }
 __device__ __forceinline__ float weight(float l, float m, float c) { return l == m ? 1.f : exp2f((l - m) * c); }
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
-    if (b.m > a.m || (b.m == a.m && b.at < a.at)) {
-        const Stat t = a;
-        a = b;
-        b = t;
-    }
-    if (b.m > -INFINITY) a.sum += b.sum * weight(b.m, a.m, c);
-    return a;
+// The largest of a warp's numbers (no NaN): as integers of the same order.
+__device__ __forceinline__ float warp_max(float x) {
+    const int b = __float_as_int(x), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
+    return __int_as_float(m ^ (m >> 31 & 0x7fffffff));
 }
-__device__ __forceinline__ Stat warp_join(Stat a, float c) {
+__device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        const Stat b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.sum, o), __shfl_xor_sync(0xffffffffu, a.at, o)};
-        a = join(a, b, c);
-    }
-    return a;
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+// The lanes' as one.
+__device__ __forceinline__ Stat warp_join(Stat a, float c) {
+    const float m = warp_max(a.m);
+    return {m, warp_sum(a.m > -INFINITY ? a.sum * weight(a.m, m, c) : 0.f), __reduce_min_sync(0xffffffffu, a.m == m ? a.at : 0x7fffffff)};
 }
 
 struct Shared {
-    Stat warp_stat[VF_WARPS];
-    Stat stats[2][VF_CLUSTER];      // of a row, by block (rows take turns)
-    int64_t warp_sum[VF_WARPS];
-    int64_t sums[2][VF_CLUSTER];    // of all weights, then of the residual's, by block
+    Stat piece[VF_PIECES];               // of a step's rows, by pieces of the slice
+    Stat stats[2][VF_ROWS][VF_CLUSTER];  // by block (steps take turns)
+    Stat row[VF_ROWS];                   // of whole rows, and whether their drafts stand
+    int stands[VF_ROWS];
+    int64_t window[2][VF_WARPS][VF_WINDOWS];  // sums of all weights, then of the residual's, by 128 places
+    int64_t warp_sum[2][VF_WARPS];
+    int64_t sums[2][VF_CLUSTER];         // by block
     float2 roots[32];
 };
 
 // Block b of a sequence's cluster has slice b of the vocabulary, and in step 2 a warp one run of it, so that sums over
-// blocks and warps are sums over the vocabulary in order.
+// blocks, warps and windows of 128 places are sums over the vocabulary in order.
 template <typename T>
 __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
-    extern __shared__ int64_t weights[];
+    extern __shared__ __align__(16) int64_t weights[];  // [slice]
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
@@ -176,56 +192,108 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     const bool greedy = !(given > 0x1p-100f);
     const float inv = 1.f / temp;
     const Two c = greedy ? Two{0.f, 0.f} : mul({inv, fmaf(-inv, temp, 1.f) * inv}, {float(LOG2E), float(LOG2E - double(float(LOG2E)))});
-    if (warp == 0) {
-        const Two r = root_of_two(lane);
-        sh.roots[lane] = make_float2(r.hi, r.lo);
-    }
+    if (warp == 0) sh.roots[lane] = make_float2(ROOTS.hi[lane], ROOTS.lo[lane]);
     const T *rows = static_cast<const T *>(a.logits) + s * a.logits_seq;
 
+    // 1. Steps of one row or several: several where few sequences leave the device waiting for memory, one where the
+    // rows behind a rejection are better not read. A warp takes pieces of a row's slice.
+    constexpr int U = 8;  // loads on their way: a piece is 128 times as many places, or half of them
+    const int rows_step = 1 << a.log_rows, used = a.piece / 128, pieces = (a.slice + a.piece - 1) / a.piece;
     int row = 0;
     Stat all;
-    for (;; row++) {
-        const T *l = rows + row * a.logits_row;
-        Stat st = {-INFINITY, 0.f, 0x7fffffff};
-        for (int i = first + VF_STEP * tid; i < end; i += VF_STEP * VF_THREADS) {
-            float x[VF_STEP];
-            load_step(l, i, end, a.vec, -INFINITY, x);
+    bool more = true;
+    for (int step = 0; more; step++) {
+        const int row0 = step << a.log_rows;
+        // what warp r decides row r by
+        int x = -1;
+        float lx = -INFINITY, q = 1.f, uj = 0.f;
+        if (warp < rows_step && row0 + warp < n) {
+            const int j = row0 + warp;
+            x = a.draft[int64_t(s) * D + j];
+            uj = a.u[int64_t(s) * (D + 1) + j];
+            if (x >= 0 && x < V) {
+                lx = logit(float(rows[j * a.logits_row + x]));
+                if (a.probs) q = a.probs[s * a.probs_seq + j * a.probs_row + x];
+            }
+        }
+#pragma unroll 1
+        for (int t = warp; t < pieces << a.log_rows; t += VF_WARPS) {
+            const int r = t / pieces, i0 = first + (t - r * pieces) * a.piece + VF_STEP * lane;
+            const T *l = rows + (row0 + r) * a.logits_row;
+            Stat st = nothing();
+            if (row0 + r <= n) {
+                float v[U][VF_STEP];
 #pragma unroll
-            for (int e = 0; e < VF_STEP; e++) {
-                x[e] = logit(x[e]);
-                if (x[e] > st.m) {
-                    st.sum *= exp2f((st.m - x[e]) * c.hi);
-                    st.m = x[e];
-                    st.at = i + e;
+                for (int u = 0; u < U; u++)
+                    if (u < used) load_step(l, i0 + u * 128, end, a.vec, -INFINITY, v[u]);
+                float top = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (u < used)
+#pragma unroll
+                        for (int e = 0; e < VF_STEP; e++) top = fmaxf(top, v[u][e]);  // (a NaN is passed over)
+                st.m = warp_max(top);
+                if (st.m > -INFINITY) {
+                    float sum = 0.f;
+                    int at = 0x7fffffff;
+#pragma unroll
+                    for (int u = U - 1; u >= 0; u--)
+                        if (u < used)
+#pragma unroll
+                            for (int e = VF_STEP - 1; e >= 0; e--) {
+                                if (greedy) at = v[u][e] == st.m ? i0 + u * 128 + e : at;
+                                else sum += weight(logit(v[u][e]), st.m, c.hi);
+                            }
+                    if (greedy) st.at = __reduce_min_sync(0xffffffffu, at);
+                    else st.sum = warp_sum(sum);
                 }
             }
-            if (st.m > -INFINITY)
-#pragma unroll
-                for (int e = 0; e < VF_STEP; e++) st.sum += weight(x[e], st.m, c.hi);
+            if (lane == 0) sh.piece[t] = st;
         }
-        st = warp_join(st, c.hi);
-        if (lane == 0) sh.warp_stat[warp] = st;
         __syncthreads();
-        if (row == 0) cluster.barrier_wait(std::move(begun));
-        if (warp == 0) {
-            st = lane < VF_WARPS ? sh.warp_stat[lane] : Stat{-INFINITY, 0.f, 0x7fffffff};
+        if (step == 0) cluster.barrier_wait(std::move(begun));
+        if (warp < rows_step) {
+            Stat st;
+            // (at most 64 pieces: two a lane)
+            if (pieces > 32) {
+                const Stat u = lane < pieces ? sh.piece[warp * pieces + lane] : nothing();
+                const Stat w = 32 + lane < pieces ? sh.piece[warp * pieces + 32 + lane] : nothing();
+                const Stat ju = warp_join(u, c.hi), jw = warp_join(w, c.hi);
+                st = lane == 0 ? ju : lane == 1 ? jw : nothing();
+            } else {
+                st = lane < pieces ? sh.piece[warp * pieces + lane] : nothing();
+            }
             st = warp_join(st, c.hi);
-            if (lane < blocks) cluster.map_shared_rank(&sh, lane)->stats[row & 1][rank] = st;
+            if (lane < blocks) cluster.map_shared_rank(&sh, lane)->stats[step & 1][warp][rank] = st;
         }
         cluster.sync();
-        all = lane < blocks ? sh.stats[row & 1][lane] : Stat{-INFINITY, 0.f, 0x7fffffff};
-        all = warp_join(all, c.hi);
-        if (row >= n || !(all.m > -INFINITY)) break;
-        const int x = a.draft[int64_t(s) * D + row];
-        bool ok = false;
-        if (greedy) {
-            ok = x == all.at;
-        } else if (x >= 0 && x < V) {
-            const float q = a.probs ? a.probs[s * a.probs_seq + row * a.probs_row + x] : 1.f;
-            const Two e = exp_two(logit(float(l[x])), all.m, c, sh.roots);
-            ok = double(a.u[int64_t(s) * (D + 1) + row]) * double(q) * double(all.sum) < double(e.hi) + double(e.lo);
+        if (warp < rows_step) {
+            const Stat st = warp_join(lane < blocks ? sh.stats[step & 1][warp][lane] : nothing(), c.hi);
+            bool stands = false;
+            if (row0 + warp < n && st.m > -INFINITY) {
+                if (greedy) {
+                    stands = x == st.at;
+                } else if (x >= 0 && x < V) {
+                    // u q sum < e, all but the sum exact to some 2^-45 (by fp32 pairs: 64-bit operations are few a cycle)
+                    const float uq = __fmul_rn(uj, q);
+                    const Two left = mul({uq, fmaf(uj, q, -uq)}, {st.sum, 0.f});
+                    const Two e = exp_two(lx, st.m, c, sh.roots);
+                    stands = (left.hi - e.hi) + (left.lo - e.lo) < 0.f;
+                }
+            }
+            if (lane == 0) {
+                sh.row[warp] = st;
+                sh.stands[warp] = stands;
+            }
         }
-        if (!ok) break;
+        __syncthreads();
+#pragma unroll 1
+        for (int r = 0; r < rows_step; r++) {
+            row = row0 + r;
+            all = sh.row[r];
+            more = sh.stands[r];
+            if (!more) break;
+        }
     }
     const bool none = !(all.m > -INFINITY);  // no logit to draw
     int32_t *tokens = a.tokens + int64_t(s) * (D + 1);
@@ -237,99 +305,124 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     }
     if (none || greedy) return;  // (every block of the cluster; none reads another's memory any more)
 
+    // 2. The draw. A warp's run of the slice, in windows of 128 places, four to a lane.
     const T *l = rows + row * a.logits_row;
     const bool residual = row < n;
     const float *q = residual && a.probs ? a.probs + s * a.probs_seq + row * a.probs_row : nullptr;
     const int draft = residual ? a.draft[int64_t(s) * D + row] : -1;
-    // a warp's run of the slice, in windows of 32 steps
-    const int run = ((a.slice + VF_WARPS - 1) / VF_WARPS + 32 * VF_STEP - 1) / (32 * VF_STEP) * (32 * VF_STEP);
-    const int from = min(end, first + warp * run), to = min(end, from + run);
-    int64_t sum = 0;
-    for (int i = from + VF_STEP * lane; i < to; i += 32 * VF_STEP) {
-        float x[VF_STEP];
-        load_step(l, i, end, a.vec, -INFINITY, x);
+    const float ud = a.u[int64_t(s) * (D + 1) + D];
+    const int windows = (a.slice + VF_WARPS * 128 - 1) / (VF_WARPS * 128), from = first + warp * windows * 128 + VF_STEP * lane;
+    longlong2 *const mine = reinterpret_cast<longlong2 *>(weights + warp * windows * 128 + VF_STEP * lane);  // (a lane's own)
+    constexpr int W = 4;  // windows on their way
+#pragma unroll 1
+    for (int k0 = 0; k0 < windows; k0 += W) {
+        float v[W][VF_STEP];
 #pragma unroll
-        for (int e = 0; e < VF_STEP; e++) {
-            const int64_t w = i + e < to ? fixed(exp_two(logit(x[e]), all.m, c, sh.roots)) : 0;
-            if (i + e < to) weights[i + e - first] = w;
-            sum += w;
+        for (int k = 0; k < W; k++) load_step(l, from + (k0 + k) * 128, k0 + k < windows ? end : 0, a.vec, -INFINITY, v[k]);
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+            if (k0 + k >= windows) break;
+            int64_t w[VF_STEP];
+#pragma unroll
+            for (int e = 0; e < VF_STEP; e++) w[e] = fixed(exp_two(logit(v[k][e]), all.m, c, sh.roots));
+            mine[(k0 + k) * 64] = make_longlong2(w[0], w[1]);
+            mine[(k0 + k) * 64 + 1] = make_longlong2(w[2], w[3]);
+            const int64_t sum = warp_sum((w[0] + w[1]) + (w[2] + w[3]));
+            if (lane == 0) sh.window[0][warp][k0 + k] = sum;
         }
     }
     // sums of the warps, then of the blocks, for everyone
-    auto total_of = [&](int64_t v, int which) {
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-        __syncthreads();
-        if (lane == 0) sh.warp_sum[warp] = v;
+    auto total_of = [&](int which) {
+        if (lane == 0) {
+            int64_t sum = 0;
+            for (int k = 0; k < windows; k++) sum += sh.window[which][warp][k];
+            sh.warp_sum[which][warp] = sum;
+        }
         __syncthreads();
         if (warp == 0) {
-            int64_t t = lane < VF_WARPS ? sh.warp_sum[lane] : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+            const int64_t t = warp_sum(lane < VF_WARPS ? sh.warp_sum[which][lane] : int64_t(0));
             if (lane < blocks) cluster.map_shared_rank(&sh, lane)->sums[which][rank] = t;
         }
         cluster.sync();
-        int64_t t = 0;
-        for (int b = 0; b < blocks; b++) t += sh.sums[which][b];
-        return t;
+        return warp_sum(lane < blocks ? sh.sums[which][lane] : int64_t(0));
     };
-    int64_t total = total_of(sum, 0);
-    int which = 0;
-    const double z = double(total) * 0x1p-43;
-    const Two Z = {float(z), float(z - double(float(z)))};
+    int64_t total = total_of(0);
+    const float zh = __ll2float_rn(total), zl = __ll2float_rn(total - __float2ll_rn(zh));
+    const Two Z = {zh * 0x1p-43f, zl * 0x1p-43f};
     // the residual's weight of a place
-    auto left = [&](int i, int64_t w) -> int64_t {
+    auto left = [&](int i, int64_t w, float p) -> int64_t {
         if (!q) return i == draft ? 0 : w;
-        const float p = q[i], h = __fmul_rn(p, Z.hi);
+        const float h = __fmul_rn(p, Z.hi);
         if (!(h < 1.5f)) return h >= 1.5f ? 0 : w;  // (a NaN takes nothing away)
         const int64_t d = w - (h > 0.f ? fixed({h, fmaf(p, Z.hi, -h) + p * Z.lo}) : 0);
         return d > 0 ? d : 0;
     };
-    bool reduced = false;
+    int which = 0;
     if (residual) {
-        sum = 0;
-        for (int i = from + lane; i < to; i += 32) sum += left(i, weights[i - first]);
-        const int64_t own = sh.warp_sum[warp];
-        const int64_t t = total_of(sum, 1);
-        if (t > 0) {
+#pragma unroll 1
+        for (int k0 = 0; k0 < windows; k0 += W) {
+            float p[W][VF_STEP];
+            if (q)
+#pragma unroll
+                for (int k = 0; k < W; k++) load_step(q, from + (k0 + k) * 128, k0 + k < windows ? end : 0, a.vec_probs, 0.f, p[k]);
+#pragma unroll
+            for (int k = 0; k < W; k++) {
+                if (k0 + k >= windows) break;
+                const longlong2 u0 = mine[(k0 + k) * 64], u1 = mine[(k0 + k) * 64 + 1];
+                const int i = from + (k0 + k) * 128;
+                const int64_t sum = warp_sum((left(i, u0.x, p[k][0]) + left(i + 1, u0.y, p[k][1])) + (left(i + 2, u1.x, p[k][2]) + left(i + 3, u1.y, p[k][3])));
+                if (lane == 0) sh.window[1][warp][k0 + k] = sum;
+            }
+        }
+        const int64_t t = total_of(1);
+        if (t > 0) {  // (0: nothing left, and p itself)
             total = t;
             which = 1;
-            reduced = true;
-        } else {  // nothing left: p itself, whose warps' sums come back
-            __syncthreads();
-            if (lane == 0) sh.warp_sum[warp] = own;
-            __syncthreads();
         }
     }
-    int64_t target = int64_t(double(a.u[int64_t(s) * (D + 1) + D]) * double(total));
-    target = max(int64_t(0), min(target, total - 1));
+    // floor(u total), u as 24 bits and an exponent
+    int64_t target = 0;
+    if (ud > 0x1p-64f) {
+        const uint32_t bits = __float_as_uint(ud), mant = (bits & 0x7fffffu) | 0x800000u, shift = 150 - (bits >> 23);  // u = mant / 2^shift
+        const uint64_t hi = __umul64hi(uint64_t(total), mant), lo = uint64_t(total) * mant;
+        target = shift >= 64 ? int64_t(hi >> (shift - 64)) : int64_t(hi << (64 - shift) | lo >> shift);
+    }
+    target = min(target, total - 1);
     for (int b = 0; b < rank; b++) target -= sh.sums[which][b];
     if (target < 0 || target >= sh.sums[which][rank]) return;
-    for (int w = 0; w < warp; w++) target -= sh.warp_sum[w];
-    if (target < 0 || target >= sh.warp_sum[warp]) return;
-    for (int base = from; base < to; base += 32) {
-        const int i = base + lane;
-        int64_t w = i < to ? weights[i - first] : 0;
-        if (reduced && i < to) w = left(i, w);
-        int64_t upto = w;
+    for (int w = 0; w < warp; w++) target -= sh.warp_sum[which][w];
+    if (target < 0 || target >= sh.warp_sum[which][warp]) return;
+    int k = 0;
+    for (; k + 1 < windows && target >= sh.window[which][warp][k]; k++) target -= sh.window[which][warp][k];
+    const longlong2 u0 = mine[k * 64], u1 = mine[k * 64 + 1];
+    int64_t w[VF_STEP] = {u0.x, u0.y, u1.x, u1.y};
+    const int i = from + k * 128;
+    if (which) {
+        float p[VF_STEP] = {0.f, 0.f, 0.f, 0.f};
+        if (q) load_step(q, i, end, a.vec_probs, 0.f, p);
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, upto > target);
-        if (past) {
-            if (lane == __ffs(past) - 1) tokens[row] = i;
-            return;
-        }
-        target -= __shfl_sync(0xffffffffu, upto, 31);
+        for (int e = 0; e < VF_STEP; e++) w[e] = left(i + e, w[e], p[e]);
+    }
+    const int64_t own = (w[0] + w[1]) + (w[2] + w[3]);
+    int64_t upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, upto > target);
+    if (past && lane == __ffs(past) - 1) {
+        target -= upto - own;
+        int e = 0;
+        while (e < VF_STEP - 1 && target >= w[e]) target -= w[e++];
+        tokens[row] = i + e;
     }
 }
 
 template <typename T>
 int launch(const VfArgs &a, int n_seq, cudaStream_t st) {
     VfArgs b = a;
-    const int smem = b.slice * int(sizeof(int64_t));
+    const int smem = (b.slice + VF_WARPS * 128 - 1) / (VF_WARPS * 128) * (VF_WARPS * 128) * int(sizeof(int64_t));  // (whole windows)
     // (once a device, of the 64 that check_device knows)
     static std::atomic<uint64_t> allowed{0};
     int dev = 0;
@@ -391,6 +484,9 @@ extern "C" int ll_verify(const void *logits, int32_t type, int64_t logits_seq, i
     a.slice = ((vocab + ll::VF_CLUSTER - 1) / ll::VF_CLUSTER + ll::VF_STEP - 1) / ll::VF_STEP * ll::VF_STEP;
     const int step = ll::VF_STEP * size;
     a.vec = reinterpret_cast<uintptr_t>(logits) % step == 0 && (a.logits_seq * size) % step == 0 && (a.logits_row * size) % step == 0;
+    while (a.log_rows < 3 && 1 << a.log_rows <= n_draft && n_seq * ll::VF_CLUSTER <= nsm) a.log_rows++;
+    a.piece = a.log_rows ? 1024 : 512;
+    a.vec_probs = reinterpret_cast<uintptr_t>(probs) % 16 == 0 && a.probs_seq % 4 == 0 && a.probs_row % 4 == 0;
     a.tokens = tokens;
     a.accepted = accepted;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
