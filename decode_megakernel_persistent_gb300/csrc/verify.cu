@@ -18,6 +18,7 @@
 #include <utility>
 
 #include "call.h"
+#include "kvq.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -27,10 +28,10 @@ namespace {
 constexpr int VF_THREADS = 512, VF_WARPS = VF_THREADS / 32;
 constexpr int VF_CLUSTER = 16;
 constexpr int VF_ROWS = 8;               // rows of a step, at most
-constexpr int VF_PIECES = 8 * 24;        // pieces of a step: of 1024 places, or 512 of a single row's
 constexpr int VF_STEP = 4;               // neighbouring logits of a lane
-constexpr int VF_MAX_VOCAB = 393216;     // a slice's weights (8 bytes each) fit in shared memory
-constexpr int VF_WINDOWS = VF_MAX_VOCAB / VF_CLUSTER / VF_WARPS / 128;
+constexpr int VF_MAX_VOCAB = 393216;
+constexpr int VF_PIECES = VF_ROWS * (VF_MAX_VOCAB / VF_CLUSTER / 1024);  // of 1024 places: of a step of several rows
+constexpr int VF_WINDOWS = 16;           // parts of a warp's run
 constexpr double LN2 = 0.693147180559945309417232, LOG2E = 1.442695040888963407359925;
 
 struct VfArgs {
@@ -41,7 +42,8 @@ struct VfArgs {
     int64_t probs_seq, probs_row;
     const float *u, *temperature;
     int32_t n_draft, vocab, slice;  // slice: a multiple of VF_STEP
-    int32_t log_rows, piece;        // 2^this rows a step; places of a warp's piece of one
+    int32_t log_rows, piece;        // 2^this rows a step; places of a warp's piece of one (512 or 1024)
+    int32_t window;                 // places of a part of a warp's run, a multiple of 128
     bool vec, vec_probs;            // rows take whole-step loads
     int32_t *tokens, *accepted;
 };
@@ -49,29 +51,29 @@ struct VfArgs {
 struct Two {  // hi + lo, |lo| at most half a unit in hi's last place (or near it)
     float hi, lo;
 };
-__device__ __forceinline__ Two two_sum(float a, float b) {
-    const float s = a + b, bb = s - a;
-    return {s, (a - (s - bb)) + (b - bb)};
-}
-__device__ __forceinline__ Two fast_two_sum(float a, float b) {  // |a| >= |b|
-    const float s = a + b;
-    return {s, b - (s - a)};
-}
 __device__ __forceinline__ Two mul(Two a, Two b) {
     const float p = __fmul_rn(a.hi, b.hi);
     return {p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi)};
 }
 
-// 2^(j / 32), j < 32, by the series of e^(j ln 2 / 32) in 64 bits, as two fp32.
+// Two numbers of two fp32 each, for fp32 operations on two at once.
+struct Pair {
+    uint64_t hi, lo;
+};
+__device__ __forceinline__ uint64_t both(float x) { return kvq_pair(x, x); }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) { return kvq_fma2(b, both(-1.f), a); }  // (exact product)
+
+// 2^(j / 256), j < 256, by the series of e^(j ln 2 / 256) in 64 bits, as two fp32.
+constexpr int ROOTS = 256;
 struct Roots {
-    float hi[32], lo[32];
+    float hi[ROOTS], lo[ROOTS];
 };
 constexpr Roots make_roots() {
     Roots r = {};
-    for (int j = 0; j < 32; j++) {
+    for (int j = 0; j < ROOTS; j++) {
         double term = 1, sum = 1;
-        for (int k = 1; k < 24; k++) {  // z^24 / 24! is below 2^-90
-            term *= LN2 / 32 * j / k;
+        for (int k = 1; k < 20; k++) {  // (z^20 / 20! is below 2^-70)
+            term *= LN2 / ROOTS * j / k;
             sum += term;
         }
         r.hi[j] = float(sum);
@@ -79,42 +81,65 @@ constexpr Roots make_roots() {
     }
     return r;
 }
-__constant__ const Roots ROOTS = make_roots();
+__device__ const Roots g_roots = make_roots();
 
-// e^((l - m) / T) for l <= m, c = log2(e) / T, off by some 2^-45 of itself: 2^(k + j / 32) from the table times
-// e^z, |z| <= ln 2 / 64, of which 1, z and z^2 / 2 are held in two fp32. Below 2^-50: 0.
-__device__ __forceinline__ Two exp_two(float l, float m, Two c, const float2 *roots) {
-    if (l == m) return {1.f, 0.f};  // (infinities, too)
-    const Two d = two_sum(l, -m);
-    const float yh = __fmul_rn(d.hi, c.hi);
-    if (!(yh > -50.f)) return {0.f, 0.f};
-    const float yl = fmaf(d.hi, c.hi, -yh) + fmaf(d.hi, c.lo, d.lo * c.hi);
-    const float r = yh + 393216.f;  // 1.5 * 2^18: to multiples of 1 / 32
-    const int n = __float_as_int(r) - __float_as_int(393216.f);  // 32 k + j
-    const float fh = yh - (r - 393216.f);
-    constexpr float LH = float(LN2), LL = float(LN2 - double(LH));
-    const float zh = __fmul_rn(fh, LH), zl = fmaf(fh, LH, -zh) + fmaf(fh, LL, yl * LH);
-    const float sh = 0.5f * zh, qh = __fmul_rn(sh, zh), ql = fmaf(sh, zh, -qh) + zh * zl;
-    const float t = zh * zh * zh * fmaf(zh, fmaf(zh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f);
-    const Two p = fast_two_sum(zh, qh);
-    const float pl = p.lo + (zl + (ql + t));
-    const float2 w = roots[n & 31];
-    const float g = __fmul_rn(w.x, p.hi);
-    const Two s = fast_two_sum(w.x, g);
-    const float lo = s.lo + (fmaf(w.x, p.hi, -g) + fmaf(w.x, pl, fmaf(w.y, p.hi, w.y)));
-    const float scale = __int_as_float(((n >> 5) + 127) << 23);
-    return {s.hi * scale, lo * scale};
+// x cut to its upper 10 bits: a 14-bit integer times it is exact in fp32.
+constexpr double upper10(double x) {
+    double unit = 1;
+    while (unit > x) unit /= 2;
+    unit /= 512;
+    return double(static_cast<long long>(x / unit)) * unit;
+}
+constexpr double STEP = LN2 / ROOTS, STEP1 = upper10(STEP), STEP2 = upper10(STEP - STEP1), STEP3 = STEP - STEP1 - STEP2;
+
+// e^((l - m) / T) of two logits l <= m, m finite, off by some 2^-45 of the larger of itself and 2^-10: 2^(k + j / 256)
+// from the table times e^z, |z| <= ln 2 / 512. The difference and its quotient are two fp32; z is what is left of
+// it after n steps of ln 2 / 256, in three parts of which the first two are taken off exactly; of e^z - 1, z is held
+// in two fp32 and the rest, below 2^-20, in one. A logit
+// further than -lim (64 T) below m, or a NaN, counts as that far: less than any weight's unit.
+__device__ __forceinline__ Pair exp_two(float l0, float l1, float m, float lim, Two inv, bool scaled, const float2 *roots) {
+    const uint64_t l = kvq_pair(l0, l1), nm = both(-m);
+    uint64_t ah = kvq_add2(l, nm), al;
+    {
+        const uint64_t bb = sub2(ah, l);  // (the sum's error, whichever is larger)
+        al = kvq_add2(sub2(l, sub2(ah, bb)), sub2(nm, bb));
+        float a0, a1, b0, b1;
+        kvq_split(ah, a0, a1);
+        kvq_split(al, b0, b1);
+        const bool near0 = a0 >= lim, near1 = a1 >= lim;
+        ah = kvq_pair(near0 ? a0 : lim, near1 ? a1 : lim);
+        al = kvq_pair(near0 ? b0 : 0.f, near1 ? b1 : 0.f);
+    }
+    if (scaled) {
+        const uint64_t p = kvq_mul2(ah, both(inv.hi)), e = kvq_fma2(ah, both(inv.hi), kvq_mul2(ah, both(-inv.hi)));
+        al = kvq_add2(e, kvq_fma2(ah, both(inv.lo), kvq_mul2(al, both(inv.hi))));
+        ah = p;
+    }
+    const uint64_t r = kvq_fma2(ah, both(float(1 / STEP)), both(12582912.f)), n = kvq_add2(r, both(-12582912.f));  // (1.5 * 2^23)
+    const uint64_t zh = kvq_fma2(n, both(float(-STEP2)), kvq_fma2(n, both(float(-STEP1)), ah)), zl = kvq_fma2(n, both(float(-STEP3)), al);
+    const uint64_t rest = kvq_fma2(kvq_mul2(zh, zh), kvq_fma2(zh, kvq_fma2(zh, both(1.f / 24), both(1.f / 6)), both(0.5f)), zl);
+    float r0, r1;
+    kvq_split(r, r0, r1);
+    const int n0 = __float_as_int(r0) - 0x4b400000, n1 = __float_as_int(r1) - 0x4b400000;
+    const float2 w0 = roots[n0 & (ROOTS - 1)], w1 = roots[n1 & (ROOTS - 1)];
+    const uint64_t w = kvq_pair(w0.x, w1.x), wl = kvq_pair(w0.y, w1.y);
+    const uint64_t g = kvq_mul2(w, zh), ge = kvq_fma2(w, zh, kvq_mul2(w, kvq_mul2(zh, both(-1.f))));
+    const uint64_t s = kvq_add2(w, g), sl = sub2(g, sub2(s, w));
+    const uint64_t lo = kvq_add2(kvq_add2(sl, ge), kvq_fma2(w, rest, kvq_fma2(wl, zh, wl)));
+    const uint64_t scale = kvq_pair(__int_as_float(((n0 >> 8) + 127) << 23), __int_as_float(((n1 >> 8) + 127) << 23));
+    return {kvq_mul2(s, scale), kvq_mul2(lo, scale)};
 }
 
-// A number in [0, 1.5] in units of 2^-43, to the nearest: its upper part in units of 2^-21 and the rest, each
+// Numbers in [0, 1.5] in units of 2^-43, to the nearest: their upper parts in units of 2^-21 and the rest, each
 // rounded by the addition of 1.5 * 2^23 of its units.
-__device__ __forceinline__ int64_t fixed(Two v) {
-    const float a = v.hi + 6.f;
-    const int h = __float_as_int(a) - __float_as_int(6.f);
-    const float rest = (v.hi - (a - 6.f)) + v.lo;
+__device__ __forceinline__ void fixed(Pair v, int64_t &i0, int64_t &i1) {
     constexpr float UNIT = 1.430511474609375e-06f;  // 1.5 * 2^23 * 2^-43
-    const float b = rest + UNIT;
-    return (int64_t(h) << 22) + (__float_as_int(b) - __float_as_int(UNIT));
+    const uint64_t a = kvq_add2(v.hi, both(6.f)), b = kvq_add2(kvq_add2(sub2(v.hi, kvq_add2(a, both(-6.f))), v.lo), both(UNIT));
+    float a0, a1, b0, b1;
+    kvq_split(a, a0, a1);
+    kvq_split(b, b0, b1);
+    i0 = (int64_t(__float_as_int(a0) - __float_as_int(6.f)) << 22) + (__float_as_int(b0) - __float_as_int(UNIT));
+    i1 = (int64_t(__float_as_int(a1) - __float_as_int(6.f)) << 22) + (__float_as_int(b1) - __float_as_int(UNIT));
 }
 
 template <typename T>
@@ -133,8 +158,13 @@ __device__ __forceinline__ void load_step(const T *row, int i, int end, bool vec
         for (int e = 0; e < VF_STEP; e++) x[e] = i + e < end ? float(row[i + e]) : none;
     }
 }
-// A logit as it counts: NaN as -infinity.
-__device__ __forceinline__ float logit(float x) { return fmaxf(x, -INFINITY); }
+// A logit as the weights take it: where the largest is infinite, infinities as 0 (as m is then), others as -infinity.
+__device__ __forceinline__ float logit(float x, bool infinite) { return !infinite ? x : x == INFINITY ? 0.f : -INFINITY; }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // The largest logit of some, the lowest place of it, and the sum of exp((l - m) / T).
 struct Stat {
@@ -142,7 +172,7 @@ struct Stat {
     int at;
 };
 __device__ __forceinline__ Stat nothing() { return {-INFINITY, 0.f, 0x7fffffff}; }
-__device__ __forceinline__ float weight(float l, float m, float c) { return l == m ? 1.f : exp2f((l - m) * c); }
+__device__ __forceinline__ float weight(float l, float m, float c) { return l == m ? 1.f : ex2((l - m) * c); }
 // The largest of a warp's numbers (no NaN): as integers of the same order.
 __device__ __forceinline__ float warp_max(float x) {
     const int b = __float_as_int(x), m = __reduce_max_sync(0xffffffffu, b ^ (b >> 31 & 0x7fffffff));
@@ -172,14 +202,15 @@ struct Shared {
     int64_t window[2][VF_WARPS][VF_WINDOWS];  // sums of all weights, then of the residual's, by 128 places
     int64_t warp_sum[2][VF_WARPS];
     int64_t sums[2][VF_CLUSTER];         // by block
-    float2 roots[32];
+    float2 roots[ROOTS];
 };
 
 // Block b of a sequence's cluster has slice b of the vocabulary, and in step 2 a warp one run of it, so that sums over
-// blocks, warps and windows of 128 places are sums over the vocabulary in order.
-template <typename T>
-__global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
-    extern __shared__ __align__(16) int64_t weights[];  // [slice]
+// blocks, warps and windows are sums over the vocabulary in order. (Weights are not kept: a second exponential costs less
+// than the shared memory that would leave fewer blocks an SM.)
+// FEW: one block an SM, with more registers and more loads on their way, for sequences that leave SMs free.
+template <typename T, bool FEW>
+__global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs a) {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
@@ -191,8 +222,11 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     const float given = a.temperature ? a.temperature[s] : 1.f, temp = fminf(given, 0x1p100f);
     const bool greedy = !(given > 0x1p-100f);
     const float inv = 1.f / temp;
-    const Two c = greedy ? Two{0.f, 0.f} : mul({inv, fmaf(-inv, temp, 1.f) * inv}, {float(LOG2E), float(LOG2E - double(float(LOG2E)))});
-    if (warp == 0) sh.roots[lane] = make_float2(ROOTS.hi[lane], ROOTS.lo[lane]);
+    const Two it = {inv, fmaf(-inv, temp, 1.f) * inv};
+    const float c = greedy ? 0.f : inv * float(LOG2E);
+    const bool scaled = temp != 1.f;
+    const float lim = -64.f * temp;
+    if (tid < ROOTS) sh.roots[tid] = make_float2(g_roots.hi[tid], g_roots.lo[tid]);
     const T *rows = static_cast<const T *>(a.logits) + s * a.logits_seq;
 
     // 1. Steps of one row or several: several where few sequences leave the device waiting for memory, one where the
@@ -212,10 +246,11 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
             x = a.draft[int64_t(s) * D + j];
             uj = a.u[int64_t(s) * (D + 1) + j];
             if (x >= 0 && x < V) {
-                lx = logit(float(rows[j * a.logits_row + x]));
+                lx = float(rows[j * a.logits_row + x]);
                 if (a.probs) q = a.probs[s * a.probs_seq + j * a.probs_row + x];
             }
         }
+        Stat mine = nothing();  // of a single row's pieces
 #pragma unroll 1
         for (int t = warp; t < pieces << a.log_rows; t += VF_WARPS) {
             const int r = t / pieces, i0 = first + (t - r * pieces) * a.piece + VF_STEP * lane;
@@ -234,41 +269,47 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
                         for (int e = 0; e < VF_STEP; e++) top = fmaxf(top, v[u][e]);  // (a NaN is passed over)
                 st.m = warp_max(top);
                 if (st.m > -INFINITY) {
-                    float sum = 0.f;
-                    int at = 0x7fffffff;
+                    if (greedy) {
+                        int at = 0x7fffffff;
 #pragma unroll
-                    for (int u = U - 1; u >= 0; u--)
-                        if (u < used)
+                        for (int u = U - 1; u >= 0; u--)
+                            if (u < used)
 #pragma unroll
-                            for (int e = VF_STEP - 1; e >= 0; e--) {
-                                if (greedy) at = v[u][e] == st.m ? i0 + u * 128 + e : at;
-                                else sum += weight(logit(v[u][e]), st.m, c.hi);
-                            }
-                    if (greedy) st.at = __reduce_min_sync(0xffffffffu, at);
-                    else st.sum = warp_sum(sum);
+                                for (int e = VF_STEP - 1; e >= 0; e--) at = v[u][e] == st.m ? i0 + u * 128 + e : at;
+                        st.at = __reduce_min_sync(0xffffffffu, at);
+                    } else {
+                        const bool infinite = st.m == INFINITY;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int u = 0; u < U; u++)
+                            if (u < used)
+#pragma unroll
+                                for (int e = 0; e < VF_STEP; e++)
+                                    sum += infinite ? float(v[u][e] == INFINITY) : ex2((fmaxf(v[u][e], -INFINITY) - st.m) * c);
+                        st.sum = warp_sum(sum);
+                    }
                 }
             }
-            if (lane == 0) sh.piece[t] = st;
+            if (a.log_rows) {
+                if (lane == 0) sh.piece[t] = st;
+            } else if (st.m > -INFINITY) {
+                const float m = fmaxf(mine.m, st.m);
+                mine = {m, (mine.m > -INFINITY ? mine.sum * weight(mine.m, m, c) : 0.f) + st.sum * weight(st.m, m, c),
+                        mine.m == m && (st.m < m || mine.at < st.at) ? mine.at : st.at};
+            }
         }
+        if (!a.log_rows && lane == 0) sh.piece[warp] = mine;
         __syncthreads();
         if (step == 0) cluster.barrier_wait(std::move(begun));
         if (warp < rows_step) {
-            Stat st;
-            // (at most 64 pieces: two a lane)
-            if (pieces > 32) {
-                const Stat u = lane < pieces ? sh.piece[warp * pieces + lane] : nothing();
-                const Stat w = 32 + lane < pieces ? sh.piece[warp * pieces + 32 + lane] : nothing();
-                const Stat ju = warp_join(u, c.hi), jw = warp_join(w, c.hi);
-                st = lane == 0 ? ju : lane == 1 ? jw : nothing();
-            } else {
-                st = lane < pieces ? sh.piece[warp * pieces + lane] : nothing();
-            }
-            st = warp_join(st, c.hi);
+            const int held = a.log_rows ? pieces : VF_WARPS;  // (24 at most)
+            Stat st = lane < held ? sh.piece[warp * held + lane] : nothing();
+            st = warp_join(st, c);
             if (lane < blocks) cluster.map_shared_rank(&sh, lane)->stats[step & 1][warp][rank] = st;
         }
         cluster.sync();
         if (warp < rows_step) {
-            const Stat st = warp_join(lane < blocks ? sh.stats[step & 1][warp][lane] : nothing(), c.hi);
+            const Stat st = warp_join(lane < blocks ? sh.stats[step & 1][warp][lane] : nothing(), c);
             bool stands = false;
             if (row0 + warp < n && st.m > -INFINITY) {
                 if (greedy) {
@@ -277,8 +318,13 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
                     // u q sum < e, all but the sum exact to some 2^-45 (by fp32 pairs: 64-bit operations are few a cycle)
                     const float uq = __fmul_rn(uj, q);
                     const Two left = mul({uq, fmaf(uj, q, -uq)}, {st.sum, 0.f});
-                    const Two e = exp_two(lx, st.m, c, sh.roots);
-                    stands = (left.hi - e.hi) + (left.lo - e.lo) < 0.f;
+                    const bool infinite = st.m == INFINITY;
+                    const float l = logit(lx, infinite);
+                    const Pair e = exp_two(l, l, infinite ? 0.f : st.m, lim, it, scaled, sh.roots);
+                    float eh, el, unused;
+                    kvq_split(e.hi, eh, unused);
+                    kvq_split(e.lo, el, unused);
+                    stands = l > -INFINITY && (left.hi - eh) + (left.lo - el) < 0.f;
                 }
             }
             if (lane == 0) {
@@ -305,39 +351,79 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     }
     if (none || greedy) return;  // (every block of the cluster; none reads another's memory any more)
 
-    // 2. The draw. A warp's run of the slice, in windows of 128 places, four to a lane.
+    // 2. The draw. A warp's run of the slice, in windows, four neighbouring places to a lane.
     const T *l = rows + row * a.logits_row;
     const bool residual = row < n;
     const float *q = residual && a.probs ? a.probs + s * a.probs_seq + row * a.probs_row : nullptr;
     const int draft = residual ? a.draft[int64_t(s) * D + row] : -1;
     const float ud = a.u[int64_t(s) * (D + 1) + D];
-    const int windows = (a.slice + VF_WARPS * 128 - 1) / (VF_WARPS * 128), from = first + warp * windows * 128 + VF_STEP * lane;
-    longlong2 *const mine = reinterpret_cast<longlong2 *>(weights + warp * windows * 128 + VF_STEP * lane);  // (a lane's own)
-    constexpr int W = 4;  // windows on their way
-#pragma unroll 1
-    for (int k0 = 0; k0 < windows; k0 += W) {
-        float v[W][VF_STEP];
+    const int run = (a.slice + VF_WARPS * a.window - 1) / (VF_WARPS * a.window) * a.window;
+    const int from = min(end, first + warp * run), to = min(end, from + run);
+    const bool infinite = all.m == INFINITY;
+    const float m = infinite ? 0.f : all.m;
+    Two Z = {0.f, 0.f};
+    // the weights of four places, and what the residual leaves of them
+    auto weights = [&](const float (&v)[VF_STEP], int64_t (&w)[VF_STEP]) {
 #pragma unroll
-        for (int k = 0; k < W; k++) load_step(l, from + (k0 + k) * 128, k0 + k < windows ? end : 0, a.vec, -INFINITY, v[k]);
+        for (int e = 0; e < VF_STEP; e += 2) fixed(exp_two(logit(v[e], infinite), logit(v[e + 1], infinite), m, lim, it, scaled, sh.roots), w[e], w[e + 1]);
+    };
+    auto left = [&](int i, int64_t (&w)[VF_STEP], const float (&p)[VF_STEP]) {
 #pragma unroll
-        for (int k = 0; k < W; k++) {
-            if (k0 + k >= windows) break;
-            int64_t w[VF_STEP];
-#pragma unroll
-            for (int e = 0; e < VF_STEP; e++) w[e] = fixed(exp_two(logit(v[k][e]), all.m, c, sh.roots));
-            mine[(k0 + k) * 64] = make_longlong2(w[0], w[1]);
-            mine[(k0 + k) * 64 + 1] = make_longlong2(w[2], w[3]);
-            const int64_t sum = warp_sum((w[0] + w[1]) + (w[2] + w[3]));
-            if (lane == 0) sh.window[0][warp][k0 + k] = sum;
+        for (int e = 0; e < VF_STEP; e += 2) {
+            if (!q) {
+                w[e] = i + e == draft ? 0 : w[e];
+                w[e + 1] = i + e + 1 == draft ? 0 : w[e + 1];
+                continue;
+            }
+            // q Z, as far as a weight goes (a NaN or less than 0 takes nothing away)
+            const uint64_t x = kvq_pair(fmaxf(p[e], 0.f), fmaxf(p[e + 1], 0.f));
+            const uint64_t h = kvq_mul2(x, both(Z.hi)), lo = kvq_fma2(x, both(Z.lo), kvq_fma2(x, both(Z.hi), kvq_mul2(x, both(-Z.hi))));
+            float h0, h1, l0, l1;
+            kvq_split(h, h0, h1);
+            kvq_split(lo, l0, l1);
+            int64_t t0, t1;
+            fixed({kvq_pair(fminf(h0, 1.5f), fminf(h1, 1.5f)), kvq_pair(h0 < 1.5f ? l0 : 0.f, h1 < 1.5f ? l1 : 0.f)}, t0, t1);
+            w[e] = max(w[e] - t0, int64_t(0));
+            w[e + 1] = max(w[e + 1] - t1, int64_t(0));
         }
-    }
+    };
+    // The sums of the run's windows, W steps of 128 places on their way.
+    constexpr int W = FEW ? 4 : 2;
+    auto sums_of = [&](int which) {
+        int64_t sum = 0;
+        int window = 0, upto = from + a.window;
+#pragma unroll 1
+        for (int b0 = from; b0 < to; b0 += W * 128) {
+            float v[W][VF_STEP], p[W][VF_STEP];
+#pragma unroll
+            for (int k = 0; k < W; k++) {
+                load_step(l, b0 + k * 128 + VF_STEP * lane, to, a.vec, -INFINITY, v[k]);
+                if (which && q) load_step(q, b0 + k * 128 + VF_STEP * lane, to, a.vec_probs, 0.f, p[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < W; k++) {
+                int64_t w[VF_STEP];
+                weights(v[k], w);
+                if (which) left(b0 + k * 128 + VF_STEP * lane, w, p[k]);
+                sum += (w[0] + w[1]) + (w[2] + w[3]);
+            }
+            if (b0 + W * 128 >= upto || b0 + W * 128 >= to) {  // (a window is a multiple of W steps, or the run)
+                sum = warp_sum(sum);
+                if (lane == 0) sh.window[which][warp][window] = sum;
+                sum = 0;
+                window++;
+                upto += a.window;
+            }
+        }
+        for (; window < VF_WINDOWS; window++)
+            if (lane == 0) sh.window[which][warp][window] = 0;
+        __syncwarp();
+    };
+    sums_of(0);
     // sums of the warps, then of the blocks, for everyone
     auto total_of = [&](int which) {
-        if (lane == 0) {
-            int64_t sum = 0;
-            for (int k = 0; k < windows; k++) sum += sh.window[which][warp][k];
-            sh.warp_sum[which][warp] = sum;
-        }
+        const int64_t sum = warp_sum(lane < VF_WINDOWS ? sh.window[which][warp][lane] : int64_t(0));
+        if (lane == 0) sh.warp_sum[which][warp] = sum;
         __syncthreads();
         if (warp == 0) {
             const int64_t t = warp_sum(lane < VF_WARPS ? sh.warp_sum[which][lane] : int64_t(0));
@@ -348,32 +434,10 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     };
     int64_t total = total_of(0);
     const float zh = __ll2float_rn(total), zl = __ll2float_rn(total - __float2ll_rn(zh));
-    const Two Z = {zh * 0x1p-43f, zl * 0x1p-43f};
-    // the residual's weight of a place
-    auto left = [&](int i, int64_t w, float p) -> int64_t {
-        if (!q) return i == draft ? 0 : w;
-        const float h = __fmul_rn(p, Z.hi);
-        if (!(h < 1.5f)) return h >= 1.5f ? 0 : w;  // (a NaN takes nothing away)
-        const int64_t d = w - (h > 0.f ? fixed({h, fmaf(p, Z.hi, -h) + p * Z.lo}) : 0);
-        return d > 0 ? d : 0;
-    };
+    Z = {zh * 0x1p-43f, zl * 0x1p-43f};
     int which = 0;
     if (residual) {
-#pragma unroll 1
-        for (int k0 = 0; k0 < windows; k0 += W) {
-            float p[W][VF_STEP];
-            if (q)
-#pragma unroll
-                for (int k = 0; k < W; k++) load_step(q, from + (k0 + k) * 128, k0 + k < windows ? end : 0, a.vec_probs, 0.f, p[k]);
-#pragma unroll
-            for (int k = 0; k < W; k++) {
-                if (k0 + k >= windows) break;
-                const longlong2 u0 = mine[(k0 + k) * 64], u1 = mine[(k0 + k) * 64 + 1];
-                const int i = from + (k0 + k) * 128;
-                const int64_t sum = warp_sum((left(i, u0.x, p[k][0]) + left(i + 1, u0.y, p[k][1])) + (left(i + 2, u1.x, p[k][2]) + left(i + 3, u1.y, p[k][3])));
-                if (lane == 0) sh.window[1][warp][k0 + k] = sum;
-            }
-        }
+        sums_of(1);
         const int64_t t = total_of(1);
         if (t > 0) {  // (0: nothing left, and p itself)
             total = t;
@@ -393,57 +457,61 @@ __global__ void __launch_bounds__(VF_THREADS) k_verify(const VfArgs a) {
     for (int w = 0; w < warp; w++) target -= sh.warp_sum[which][w];
     if (target < 0 || target >= sh.warp_sum[which][warp]) return;
     int k = 0;
-    for (; k + 1 < windows && target >= sh.window[which][warp][k]; k++) target -= sh.window[which][warp][k];
-    const longlong2 u0 = mine[k * 64], u1 = mine[k * 64 + 1];
-    int64_t w[VF_STEP] = {u0.x, u0.y, u1.x, u1.y};
-    const int i = from + k * 128;
-    if (which) {
-        float p[VF_STEP] = {0.f, 0.f, 0.f, 0.f};
-        if (q) load_step(q, i, end, a.vec_probs, 0.f, p);
+    while (k + 1 < VF_WINDOWS && target >= sh.window[which][warp][k]) target -= sh.window[which][warp][k++];
+    // the window again, 128 places at a time
+    const int last = min(to, from + (k + 1) * a.window);
+#pragma unroll 1
+    for (int b0 = from + k * a.window; b0 < last; b0 += 128) {
+        const int i = b0 + VF_STEP * lane;
+        float v[VF_STEP], p[VF_STEP];
+        load_step(l, i, to, a.vec, -INFINITY, v);
+        int64_t w[VF_STEP];
+        weights(v, w);
+        if (which) {
+            if (q) load_step(q, i, to, a.vec_probs, 0.f, p);
+            left(i, w, p);
+        }
+        const int64_t own = (w[0] + w[1]) + (w[2] + w[3]);
+        int64_t upto = own;
 #pragma unroll
-        for (int e = 0; e < VF_STEP; e++) w[e] = left(i + e, w[e], p[e]);
-    }
-    const int64_t own = (w[0] + w[1]) + (w[2] + w[3]);
-    int64_t upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, upto > target);
-    if (past && lane == __ffs(past) - 1) {
-        target -= upto - own;
-        int e = 0;
-        while (e < VF_STEP - 1 && target >= w[e]) target -= w[e++];
-        tokens[row] = i + e;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, upto > target);
+        if (past) {
+            if (lane == __ffs(past) - 1) {
+                target -= upto - own;
+                int e = 0;
+                while (e < VF_STEP - 1 && target >= w[e]) target -= w[e++];
+                tokens[row] = i + e;
+            }
+            return;
+        }
+        target -= __shfl_sync(0xffffffffu, upto, 31);
     }
 }
 
-template <typename T>
-int launch(const VfArgs &a, int n_seq, cudaStream_t st) {
-    VfArgs b = a;
-    const int smem = (b.slice + VF_WARPS * 128 - 1) / (VF_WARPS * 128) * (VF_WARPS * 128) * int(sizeof(int64_t));  // (whole windows)
+template <typename T, bool FEW>
+int launch(const VfArgs &a, int n_seq, int cluster, cudaStream_t st) {
     // (once a device, of the 64 that check_device knows)
     static std::atomic<uint64_t> allowed{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LL_ERR_CUDA;
     if (!(allowed.load(std::memory_order_acquire) >> dev & 1)) {
-        if (cudaFuncSetAttribute(k_verify<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaFuncSetAttribute(k_verify<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, VF_MAX_VOCAB / VF_CLUSTER * int(sizeof(int64_t))) != cudaSuccess)
-            return LL_ERR_CUDA;
+        if (cudaFuncSetAttribute(k_verify<T, FEW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return LL_ERR_CUDA;
         allowed.fetch_or(1ull << dev, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(n_seq) * VF_CLUSTER);
+    cfg.gridDim = dim3(unsigned(n_seq) * cluster);
     cfg.blockDim = dim3(VF_THREADS);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {VF_CLUSTER, 1, 1};
+    attr[0].val.clusterDim = {unsigned(cluster), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_verify<T>, b) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k_verify<T, FEW>, a) == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
 }  // namespace
@@ -481,14 +549,23 @@ extern "C" int ll_verify(const void *logits, int32_t type, int64_t logits_seq, i
     a.temperature = temperature;
     a.n_draft = n_draft;
     a.vocab = vocab;
-    a.slice = ((vocab + ll::VF_CLUSTER - 1) / ll::VF_CLUSTER + ll::VF_STEP - 1) / ll::VF_STEP * ll::VF_STEP;
+    // As many blocks a sequence as the device holds at a time, two an SM, but no fewer than a block's pieces pay for.
+    int cluster = ll::VF_CLUSTER;
+    while (cluster > 1 && int64_t(n_seq) * cluster > 2 * nsm) cluster /= 2;
+    a.slice = ((vocab + cluster - 1) / cluster + ll::VF_STEP - 1) / ll::VF_STEP * ll::VF_STEP;
     const int step = ll::VF_STEP * size;
     a.vec = reinterpret_cast<uintptr_t>(logits) % step == 0 && (a.logits_seq * size) % step == 0 && (a.logits_row * size) % step == 0;
-    while (a.log_rows < 3 && 1 << a.log_rows <= n_draft && n_seq * ll::VF_CLUSTER <= nsm) a.log_rows++;
-    a.piece = a.log_rows ? 1024 : 512;
+    const bool few = n_seq * ll::VF_CLUSTER <= nsm;
+    while (few && a.log_rows < 3 && 1 << a.log_rows <= n_draft) a.log_rows++;
+    a.piece = a.log_rows || a.slice >= ll::VF_WARPS * 1024 ? 1024 : 512;
+    const int run = (a.slice + ll::VF_WARPS - 1) / ll::VF_WARPS;
+    a.window = ((run + ll::VF_WINDOWS - 1) / ll::VF_WINDOWS + 511) / 512 * 512;
     a.vec_probs = reinterpret_cast<uintptr_t>(probs) % 16 == 0 && a.probs_seq % 4 == 0 && a.probs_row % 4 == 0;
     a.tokens = tokens;
     a.accepted = accepted;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return ll::finish(type == LL_F32 ? ll::launch<float>(a, n_seq, st) : ll::launch<__nv_bfloat16>(a, n_seq, st), err, err_len);
+    const int rc = type == LL_F32 ? few ? ll::launch<float, true>(a, n_seq, cluster, st) : ll::launch<float, false>(a, n_seq, cluster, st)
+                 : few            ? ll::launch<__nv_bfloat16, true>(a, n_seq, cluster, st)
+                                  : ll::launch<__nv_bfloat16, false>(a, n_seq, cluster, st);
+    return ll::finish(rc, err, err_len);
 }
