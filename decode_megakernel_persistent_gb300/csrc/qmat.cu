@@ -8,6 +8,7 @@
 #include "kvq.h"
 #include "qmat.cuh"
 #include "qmat.h"
+#include "rows.cuh"
 
 namespace ll {
 namespace {
@@ -24,28 +25,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
-}
-
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// 8 values of a row from column k on, those past the matrix as `none`.
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int64_t k, int64_t cols, bool vec, float none, float (&x)[8]) {
-    if (vec && k + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(row + k), b = *reinterpret_cast<const float4 *>(row + k + 4);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(row + k);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = k + i < cols ? widen(row[k + i]) : none;
-    }
 }
 
 // Quantise. A lane is row g or g + 8 of a tile and the columns 32 j + 8 t .. + 7 (lane 4 g + t), as the
@@ -65,15 +44,17 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
     float x[4][8];
     float mn[4], mx[4];
     const bool whole = (K + 1) * QM_TILE_COLS <= m.cols;
+    const T *row = w + (held ? r : 0) * stride;
+    const int k0 = int(K) * QM_TILE_COLS + 8 * t, cols = held ? m.cols : 0;
+    if (whole && vec) {  // (the loads go out together)
+        Raw8<T> raw[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const int64_t k = K * QM_TILE_COLS + 32 * j + 8 * t;
-        if (held) {
-            load8(w + r * stride, k, m.cols, vec, 0.f, x[j]);
-        } else {
+        for (int j = 0; j < 4; j++) raw[j].load(row, k0 + 32 * j, cols);
 #pragma unroll
-            for (int i = 0; i < 8; i++) x[j][i] = 0.f;
-        }
+        for (int j = 0; j < 4; j++) raw[j].widen(x[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) load8(row, k0 + 32 * j, cols, false, x[j]);
     }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -160,28 +141,7 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_read(ll_qmat m, T *w, int64
             x[2 * i] = fmaf(p[j / PER].y, __uint_as_float(c << 16) - 16.f, p[j / PER].x);
             x[2 * i + 1] = fmaf(p[j / PER].y, __uint_as_float(c & 0xffff0000u) - 16.f, p[j / PER].x);
         }
-        T *dst = w + r * stride + k;
-        if (vec && k + 8 <= m.cols) {
-            if constexpr (sizeof(T) == 4) {
-                reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-                reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-            } else {
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                    o[i] = *reinterpret_cast<const uint32_t *>(&b);
-                }
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (k + i < m.cols) {
-                    if constexpr (sizeof(T) == 4) dst[i] = x[i];
-                    else dst[i] = __float2bfloat16_rn(x[i]);
-                }
-        }
+        store8(w + r * stride, int(k), m.cols, vec, x);
     }
 }
 

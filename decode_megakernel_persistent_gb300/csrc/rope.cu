@@ -31,22 +31,6 @@ struct RopeArgs {
     bool inverse;
 };
 
-// 8 values as they lie in memory.
-template <typename T>
-struct Unit {
-    uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T *p) {
-#pragma unroll
-        for (int i = 0; i < int(sizeof(T) / 2); i++) w[i] = reinterpret_cast<const uint4 *>(p)[i];
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            x[i] = sizeof(T) == 4 ? __uint_as_float(u[i]) : __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
-    }
-};
-
 // A thread has one unit of one token, its 8 angles in registers, and every slots-th head, BATCH of them on their way at once.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ RopeArgs a) {
@@ -82,14 +66,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
     if constexpr (VEC) {
         const int at0 = a.t.interleaved ? 16 * u : 8 * u, at1 = a.t.interleaved ? 16 * u + 8 : half + 8 * u;
         for (int h0 = slot; h0 < a.heads; h0 += BATCH * a.slots) {
-            Unit<T> r0[BATCH], r1[BATCH];
+            Raw8<T> r0[BATCH], r1[BATCH];
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
                 const int h = h0 + i * a.slots;
                 if (h >= a.heads) break;
                 const T *x = row(a.in, h);
-                r0[i].load(x + at0);
-                r1[i].load(x + at1);
+                r0[i].load(x, at0, at0 + 8);
+                r1[i].load(x, at1, at1 + 8);
             }
 #pragma unroll
             for (int i = 0; i < BATCH; i++) {
@@ -97,8 +81,8 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope(const __grid_constant__ R
                 if (h >= a.heads) break;
                 T *y = row(a.out, h);
                 float p[8], q[8], v[8], w[8];
-                r0[i].get(v);
-                r1[i].get(w);
+                r0[i].widen(v);
+                r1[i].widen(w);
                 if (a.t.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {

@@ -13,15 +13,26 @@ struct e4m3 {
 };
 
 int launch_rmsnorm(const ll_rows &x, const ll_rows *res, const ll_rows *res_out, const uint16_t *gain, float eps, int n, int width,
-                   const ll_rows &out, cudaStream_t st);
+                   const ll_rows &out, int nsm, cudaStream_t st);
 int launch_rope(const ll_rope_table &t, const ll_kvq_rows &q, const ll_kvq_rows &q_out, int nq, const ll_kvq_rows *k, const ll_kvq_rows *k_out,
                 int nk, int type, int n_seq, const KvqLens &l, bool inverse, int nsm, cudaStream_t st);
 
 #ifdef __CUDACC__
+// Columns k..k+7 of a row as they lie in memory, zeros from `width` on, a multiple of 8; 16-byte loads are aligned.
 template <typename T>
-__device__ __forceinline__ float rounded(float x) {
-    return sizeof(T) == 4 ? x : __bfloat162float(__float2bfloat16_rn(x));
-}
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *row, int k, int width) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); i++) w[i] = k < width ? reinterpret_cast<const uint4 *>(row + k)[i] : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void widen(float (&x)[8]) const {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            x[i] = sizeof(T) == 4 ? __uint_as_float(u[i]) : __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    }
+};
 
 // Columns k..k+7 of a row of `width` values, zeros past its end. vec: 16-byte (8-byte for e4m3) accesses are aligned.
 __device__ __forceinline__ void load8(const float *row, int k, int width, bool vec, float (&x)[8]) {
@@ -84,6 +95,25 @@ __device__ __forceinline__ void store8(e4m3 *row, int k, int width, bool vec, co
 #pragma unroll
         for (int i = 0; i < 8; i++)
             if (k + i < width) row[k + i].bits = uint8_t(w[i / 2] >> (8 * (i & 1)));
+    }
+}
+// The same, with the values rounded as they are stored.
+__device__ __forceinline__ void store_rounded8(float *row, int k, int width, bool vec, float (&x)[8]) { store8(row, k, width, vec, x); }
+__device__ __forceinline__ void store_rounded8(__nv_bfloat16 *row, int k, int width, bool vec, float (&x)[8]) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t *>(&b);
+        x[2 * i] = __uint_as_float(o[i] << 16);
+        x[2 * i + 1] = __uint_as_float(o[i] & 0xffff0000u);
+    }
+    if (vec && k + 8 <= width) {
+        *reinterpret_cast<uint4 *>(row + k) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (k + i < width) row[k + i] = __ushort_as_bfloat16(uint16_t(o[i / 2] >> (16 * (i & 1))));
     }
 }
 #endif

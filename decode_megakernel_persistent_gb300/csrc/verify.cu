@@ -14,6 +14,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <utility>
 
@@ -30,7 +31,6 @@ constexpr int VF_CLUSTER = 16;
 constexpr int VF_ROWS = 8;               // rows of a step, at most
 constexpr int VF_STEP = 4;               // neighbouring logits of a lane
 constexpr int VF_MAX_VOCAB = 393216;
-constexpr int VF_PIECES = VF_ROWS * (VF_MAX_VOCAB / VF_CLUSTER / 1024);  // of 1024 places: of a step of several rows
 constexpr int VF_WINDOWS = 16;           // parts of a warp's run
 constexpr double LN2 = 0.693147180559945309417232, LOG2E = 1.442695040888963407359925;
 
@@ -42,7 +42,8 @@ struct VfArgs {
     int64_t probs_seq, probs_row;
     const float *u, *temperature;
     int32_t n_draft, vocab, slice;  // slice: a multiple of VF_STEP
-    int32_t log_rows, piece;        // 2^this rows a step; places of a warp's piece of one (512 or 1024)
+    int32_t rows_step, warps_row;   // rows a step, warps that share one
+    int32_t piece;                  // places of a warp's piece of a row (512 or 1024)
     int32_t window;                 // places of a part of a warp's run, a multiple of 128
     bool vec, vec_probs;            // rows take whole-step loads
     int32_t *tokens, *accepted;
@@ -195,7 +196,7 @@ __device__ __forceinline__ Stat warp_join(Stat a, float c) {
 }
 
 struct Shared {
-    Stat piece[VF_PIECES];               // of a step's rows, by pieces of the slice
+    Stat part[VF_WARPS];                 // of a step's rows, by warp
     Stat stats[2][VF_ROWS][VF_CLUSTER];  // by block (steps take turns)
     Stat row[VF_ROWS];                   // of whole rows, and whether their drafts stand
     int stands[VF_ROWS];
@@ -232,16 +233,16 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
     // 1. Steps of one row or several: several where few sequences leave the device waiting for memory, one where the
     // rows behind a rejection are better not read. A warp takes pieces of a row's slice.
     constexpr int U = 8;  // loads on their way: a piece is 128 times as many places, or half of them
-    const int rows_step = 1 << a.log_rows, used = a.piece / 128, pieces = (a.slice + a.piece - 1) / a.piece;
+    const int used = a.piece / 128, warp_row = warp / a.warps_row;  // (rows_step and past it: a warp without work)
     int row = 0;
     Stat all;
     bool more = true;
     for (int step = 0; more; step++) {
-        const int row0 = step << a.log_rows;
+        const int row0 = step * a.rows_step;
         // what warp r decides row r by
         int x = -1;
         float lx = -INFINITY, q = 1.f, uj = 0.f;
-        if (warp < rows_step && row0 + warp < n) {
+        if (warp < a.rows_step && row0 + warp < n) {
             const int j = row0 + warp;
             x = a.draft[int64_t(s) * D + j];
             uj = a.u[int64_t(s) * (D + 1) + j];
@@ -250,13 +251,14 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
                 if (a.probs) q = a.probs[s * a.probs_seq + j * a.probs_row + x];
             }
         }
-        Stat mine = nothing();  // of a single row's pieces
+        Stat mine = nothing();
+        const T *l = rows + (row0 + warp_row) * a.logits_row;
+        const bool held = warp_row < a.rows_step && row0 + warp_row <= n;
 #pragma unroll 1
-        for (int t = warp; t < pieces << a.log_rows; t += VF_WARPS) {
-            const int r = t / pieces, i0 = first + (t - r * pieces) * a.piece + VF_STEP * lane;
-            const T *l = rows + (row0 + r) * a.logits_row;
+        for (int i1 = first + (warp - warp_row * a.warps_row) * a.piece; held && i1 < end; i1 += a.warps_row * a.piece) {
+            const int i0 = i1 + VF_STEP * lane;
             Stat st = nothing();
-            if (row0 + r <= n) {
+            {
                 float v[U][VF_STEP];
 #pragma unroll
                 for (int u = 0; u < U; u++)
@@ -290,25 +292,22 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
                     }
                 }
             }
-            if (a.log_rows) {
-                if (lane == 0) sh.piece[t] = st;
-            } else if (st.m > -INFINITY) {
+            if (st.m > -INFINITY) {
                 const float m = fmaxf(mine.m, st.m);
                 mine = {m, (mine.m > -INFINITY ? mine.sum * weight(mine.m, m, c) : 0.f) + st.sum * weight(st.m, m, c),
                         mine.m == m && (st.m < m || mine.at < st.at) ? mine.at : st.at};
             }
         }
-        if (!a.log_rows && lane == 0) sh.piece[warp] = mine;
+        if (lane == 0) sh.part[warp] = mine;
         __syncthreads();
         if (step == 0) cluster.barrier_wait(std::move(begun));
-        if (warp < rows_step) {
-            const int held = a.log_rows ? pieces : VF_WARPS;  // (24 at most)
-            Stat st = lane < held ? sh.piece[warp * held + lane] : nothing();
+        if (warp < a.rows_step) {
+            Stat st = lane < a.warps_row ? sh.part[warp * a.warps_row + lane] : nothing();
             st = warp_join(st, c);
             if (lane < blocks) cluster.map_shared_rank(&sh, lane)->stats[step & 1][warp][rank] = st;
         }
         cluster.sync();
-        if (warp < rows_step) {
+        if (warp < a.rows_step) {
             const Stat st = warp_join(lane < blocks ? sh.stats[step & 1][warp][lane] : nothing(), c);
             bool stands = false;
             if (row0 + warp < n && st.m > -INFINITY) {
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
         }
         __syncthreads();
 #pragma unroll 1
-        for (int r = 0; r < rows_step; r++) {
+        for (int r = 0; r < a.rows_step; r++) {
             row = row0 + r;
             all = sh.row[r];
             more = sh.stands[r];
@@ -387,42 +386,66 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
             w[e + 1] = max(w[e + 1] - t1, int64_t(0));
         }
     };
-    // The sums of the run's windows, W steps of 128 places on their way.
-    constexpr int W = FEW ? 4 : 2;
-    auto sums_of = [&](int which) {
+    // Three walks over 128 places at a time, the next ones on their way, by the same code (code that runs for the first time in a
+    // launch comes slower than it runs): the sums of the run's windows, of all weights (0) and of the residual's (1);
+    // then the window of the draw, where the sum passes its target (2).
+    int64_t total = 0, target = 0;
+    int which = 0, lo = from, hi = to;
+#pragma unroll 1
+    for (int walk = 0;; walk++) {
+        float v[VF_STEP], p[VF_STEP] = {0.f, 0.f, 0.f, 0.f};
         int64_t sum = 0;
         int window = 0, upto = from + a.window;
+        load_step(l, lo + VF_STEP * lane, hi, a.vec, -INFINITY, v);
+        if (which && q) load_step(q, lo + VF_STEP * lane, hi, a.vec_probs, 0.f, p);
 #pragma unroll 1
-        for (int b0 = from; b0 < to; b0 += W * 128) {
-            float v[W][VF_STEP], p[W][VF_STEP];
+        for (int b0 = lo; b0 < hi; b0 += 128) {
+            const int i = b0 + VF_STEP * lane;
+            float next_v[VF_STEP], next_p[VF_STEP] = {0.f, 0.f, 0.f, 0.f};
+            load_step(l, i + 128, hi, a.vec, -INFINITY, next_v);
+            if (which && q) load_step(q, i + 128, hi, a.vec_probs, 0.f, next_p);
+            int64_t w[VF_STEP];
+            weights(v, w);
+            if (which) left(i, w, p);
 #pragma unroll
-            for (int k = 0; k < W; k++) {
-                load_step(l, b0 + k * 128 + VF_STEP * lane, to, a.vec, -INFINITY, v[k]);
-                if (which && q) load_step(q, b0 + k * 128 + VF_STEP * lane, to, a.vec_probs, 0.f, p[k]);
+            for (int e = 0; e < VF_STEP; e++) {
+                v[e] = next_v[e];
+                p[e] = next_p[e];
             }
+            const int64_t own = (w[0] + w[1]) + (w[2] + w[3]);
+            sum += own;
+            if (walk < 2) {
+                if (b0 + 128 >= upto || b0 + 128 >= hi) {
+                    sum = warp_sum(sum);
+                    if (lane == 0) sh.window[which][warp][window] = sum;
+                    sum = 0;
+                    window++;
+                    upto += a.window;
+                }
+                continue;
+            }
+            int64_t past = own;  // the sum up to the lane's last place
 #pragma unroll
-            for (int k = 0; k < W; k++) {
-                int64_t w[VF_STEP];
-                weights(v[k], w);
-                if (which) left(b0 + k * 128 + VF_STEP * lane, w, p[k]);
-                sum += (w[0] + w[1]) + (w[2] + w[3]);
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, past, o);
+                if (lane >= o) past += x;
             }
-            if (b0 + W * 128 >= upto || b0 + W * 128 >= to) {  // (a window is a multiple of W steps, or the run)
-                sum = warp_sum(sum);
-                if (lane == 0) sh.window[which][warp][window] = sum;
-                sum = 0;
-                window++;
-                upto += a.window;
+            const unsigned found = __ballot_sync(0xffffffffu, past > target);
+            if (found) {
+                if (lane == __ffs(found) - 1) {
+                    target -= past - own;
+                    int e = 0;
+                    while (e < VF_STEP - 1 && target >= w[e]) target -= w[e++];
+                    tokens[row] = i + e;
+                }
+                return;
             }
+            target -= __shfl_sync(0xffffffffu, past, 31);
         }
-        for (; window < VF_WINDOWS; window++)
-            if (lane == 0) sh.window[which][warp][window] = 0;
+        if (walk == 2) return;  // (not reached: the window's sum passes the target)
+        // sums of the warps, then of the blocks, for everyone
         __syncwarp();
-    };
-    sums_of(0);
-    // sums of the warps, then of the blocks, for everyone
-    auto total_of = [&](int which) {
-        const int64_t sum = warp_sum(lane < VF_WINDOWS ? sh.window[which][warp][lane] : int64_t(0));
+        sum = warp_sum(lane < window ? sh.window[which][warp][lane] : int64_t(0));
         if (lane == 0) sh.warp_sum[which][warp] = sum;
         __syncthreads();
         if (warp == 0) {
@@ -430,65 +453,36 @@ __global__ void __launch_bounds__(VF_THREADS, FEW ? 1 : 2) k_verify(const VfArgs
             if (lane < blocks) cluster.map_shared_rank(&sh, lane)->sums[which][rank] = t;
         }
         cluster.sync();
-        return warp_sum(lane < blocks ? sh.sums[which][lane] : int64_t(0));
-    };
-    int64_t total = total_of(0);
-    const float zh = __ll2float_rn(total), zl = __ll2float_rn(total - __float2ll_rn(zh));
-    Z = {zh * 0x1p-43f, zl * 0x1p-43f};
-    int which = 0;
-    if (residual) {
-        sums_of(1);
-        const int64_t t = total_of(1);
-        if (t > 0) {  // (0: nothing left, and p itself)
+        const int64_t t = warp_sum(lane < blocks ? sh.sums[which][lane] : int64_t(0));
+        if (walk == 0) {
             total = t;
-            which = 1;
-        }
-    }
-    // floor(u total), u as 24 bits and an exponent
-    int64_t target = 0;
-    if (ud > 0x1p-64f) {
-        const uint32_t bits = __float_as_uint(ud), mant = (bits & 0x7fffffu) | 0x800000u, shift = 150 - (bits >> 23);  // u = mant / 2^shift
-        const uint64_t hi = __umul64hi(uint64_t(total), mant), lo = uint64_t(total) * mant;
-        target = shift >= 64 ? int64_t(hi >> (shift - 64)) : int64_t(hi << (64 - shift) | lo >> shift);
-    }
-    target = min(target, total - 1);
-    for (int b = 0; b < rank; b++) target -= sh.sums[which][b];
-    if (target < 0 || target >= sh.sums[which][rank]) return;
-    for (int w = 0; w < warp; w++) target -= sh.warp_sum[which][w];
-    if (target < 0 || target >= sh.warp_sum[which][warp]) return;
-    int k = 0;
-    while (k + 1 < VF_WINDOWS && target >= sh.window[which][warp][k]) target -= sh.window[which][warp][k++];
-    // the window again, 128 places at a time
-    const int last = min(to, from + (k + 1) * a.window);
-#pragma unroll 1
-    for (int b0 = from + k * a.window; b0 < last; b0 += 128) {
-        const int i = b0 + VF_STEP * lane;
-        float v[VF_STEP], p[VF_STEP];
-        load_step(l, i, to, a.vec, -INFINITY, v);
-        int64_t w[VF_STEP];
-        weights(v, w);
-        if (which) {
-            if (q) load_step(q, i, to, a.vec_probs, 0.f, p);
-            left(i, w, p);
-        }
-        const int64_t own = (w[0] + w[1]) + (w[2] + w[3]);
-        int64_t upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, upto > target);
-        if (past) {
-            if (lane == __ffs(past) - 1) {
-                target -= upto - own;
-                int e = 0;
-                while (e < VF_STEP - 1 && target >= w[e]) target -= w[e++];
-                tokens[row] = i + e;
+            if (residual) {
+                const float zh = __ll2float_rn(total), zl = __ll2float_rn(total - __float2ll_rn(zh));
+                Z = {zh * 0x1p-43f, zl * 0x1p-43f};
+                which = 1;
+                continue;
             }
-            return;
+            walk = 1;
+        } else if (t > 0) {
+            total = t;
+        } else {  // (nothing left: p itself)
+            which = 0;
         }
-        target -= __shfl_sync(0xffffffffu, upto, 31);
+        // floor(u total), u as 24 bits and an exponent
+        if (ud > 0x1p-64f) {
+            const uint32_t bits = __float_as_uint(ud), mant = (bits & 0x7fffffu) | 0x800000u, shift = 150 - (bits >> 23);  // u = mant / 2^shift
+            const uint64_t high = __umul64hi(uint64_t(total), mant), low = uint64_t(total) * mant;
+            target = shift >= 64 ? int64_t(high >> (shift - 64)) : int64_t(high << (64 - shift) | low >> shift);
+        }
+        target = min(target, total - 1);
+        // the block, the warp and the window that it falls into
+        const int64_t before = warp_sum(lane < rank ? sh.sums[which][lane] : int64_t(0)) + warp_sum(lane < warp ? sh.warp_sum[which][lane] : int64_t(0));
+        target -= before;
+        if (target < 0 || target >= sh.warp_sum[which][warp]) return;
+        int k = 0;
+        while (k + 1 < VF_WINDOWS && target >= sh.window[which][warp][k]) target -= sh.window[which][warp][k++];
+        lo = from + k * a.window;
+        hi = min(to, lo + a.window);
     }
 }
 
@@ -549,17 +543,23 @@ extern "C" int ll_verify(const void *logits, int32_t type, int64_t logits_seq, i
     a.temperature = temperature;
     a.n_draft = n_draft;
     a.vocab = vocab;
-    // As many blocks a sequence as the device holds at a time, two an SM, but no fewer than a block's pieces pay for.
+    // As many blocks a sequence as the device holds at a time, two an SM, but no fewer than 4 (the longest of a batch's sequences
+    // is what its call waits for). Clusters of 2, 4, 8, 16: 12 sequences of 4 drafts 83, 50, 35, 30 us; 32: 98, 60, 55, 78; 64
+    // of up to 7: 118, 92, 101, 122; 128 of 3: 135, 129, 161, 221.
     int cluster = ll::VF_CLUSTER;
-    while (cluster > 1 && int64_t(n_seq) * cluster > 2 * nsm) cluster /= 2;
+    while (cluster > 4 && int64_t(n_seq) * cluster > 2 * nsm) cluster /= 2;
     a.slice = ((vocab + cluster - 1) / cluster + ll::VF_STEP - 1) / ll::VF_STEP * ll::VF_STEP;
     const int step = ll::VF_STEP * size;
     a.vec = reinterpret_cast<uintptr_t>(logits) % step == 0 && (a.logits_seq * size) % step == 0 && (a.logits_row * size) % step == 0;
     const bool few = n_seq * ll::VF_CLUSTER <= nsm;
-    while (few && a.log_rows < 3 && 1 << a.log_rows <= n_draft) a.log_rows++;
-    a.piece = a.log_rows || a.slice >= ll::VF_WARPS * 1024 ? 1024 : 512;
+    // Rows a step: all of few sequences' (a step is 5 us, most of it waiting); two otherwise, of which one may be read for
+    // nothing (64 sequences, up to 7 drafts: 95.7 us with 1, 94.7 with 2, 93.1 with 4, 106.7 with 8; 128 of 3: 137, 143, 152, 152; 32
+    // of 4: 54.8, 50.1, 51.6, 55.0).
+    a.rows_step = std::min(few ? ll::VF_ROWS : 2, n_draft + 1);
+    a.warps_row = ll::VF_WARPS / a.rows_step;
+    a.piece = a.slice >= a.warps_row * 1024 ? 1024 : 512;
     const int run = (a.slice + ll::VF_WARPS - 1) / ll::VF_WARPS;
-    a.window = ((run + ll::VF_WINDOWS - 1) / ll::VF_WINDOWS + 511) / 512 * 512;
+    a.window = ((run + ll::VF_WINDOWS - 1) / ll::VF_WINDOWS + 127) / 128 * 128;
     a.vec_probs = reinterpret_cast<uintptr_t>(probs) % 16 == 0 && a.probs_seq % 4 == 0 && a.probs_row % 4 == 0;
     a.tokens = tokens;
     a.accepted = accepted;
