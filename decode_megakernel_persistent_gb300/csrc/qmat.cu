@@ -27,65 +27,82 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The range of some values: NaN if any of them is.
+struct Range {
+    float mn, mx;
+};
+__device__ __forceinline__ Range join(Range a, Range b) { return {min_nan(a.mn, b.mn), max_nan(a.mx, b.mx)}; }
+__device__ __forceinline__ Range range8(const Raw8<float> &r) {
+    float x[8];
+    r.widen(x);
+    Range a = {x[0], x[0]};
+#pragma unroll
+    for (int i = 1; i < 8; i++) a = join(a, {x[i], x[i]});
+    return a;
+}
+__device__ __forceinline__ Range range8(const Raw8<__nv_bfloat16> &r) {  // (two values at once)
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(r.w);
+    uint32_t mn = w[0], mx = w[0];
+#pragma unroll
+    for (int i = 1; i < 4; i++) {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(mn) : "r"(w[i]));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(mx) : "r"(w[i]));
+    }
+    return {min_nan(__uint_as_float(mn << 16), __uint_as_float(mn & 0xffff0000u)), max_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u))};
+}
+
 // Quantise. A lane is row g or g + 8 of a tile and the columns 32 j + 8 t .. + 7 (lane 4 g + t), as the
 // products read a tile: four words, 16 bytes a lane, a half warp's rows in one 512-byte store. A group's range
-// goes over the lane's words of the group and the four lanes of a row.
-template <typename T, int GROUP>
-__global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w, int64_t stride, bool vec) {
-    const int KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;
-    const int64_t half = (int64_t(blockIdx.x) * RW_THREADS + threadIdx.x) >> 5;  // (a warp's half tile)
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t tile = half >> 1;
-    const int64_t R = tile / KT, K = tile % KT;
-    if (R >= (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS) return;
+// goes over the lane's words of the group and the four lanes of a row. WHOLE: a tile inside the matrix whose rows are on
+// 16-byte borders.
+template <typename T, int GROUP, bool WHOLE>
+__device__ __forceinline__ void write_half_tile(const ll_qmat &m, const T *w, int64_t stride, int64_t half, int64_t tile, int64_t R, int64_t K, int lane) {
+    const int g = lane >> 2, t = lane & 3;
     const int in_tile = int(half & 1) * 8 + g;
     const int64_t r = R * QM_TILE_ROWS + in_tile;
     const bool held = r < m.rows;
-    float x[4][8];
-    float mn[4], mx[4];
-    const bool whole = (K + 1) * QM_TILE_COLS <= m.cols;
     const T *row = w + (held ? r : 0) * stride;
     const int k0 = int(K) * QM_TILE_COLS + 8 * t, cols = held ? m.cols : 0;
-    if (whole && vec) {  // (the loads go out together)
+    float x[4][8];
+    Range range[4];
+    if constexpr (WHOLE) {
         Raw8<T> raw[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) raw[j].load(row, k0 + 32 * j, cols);
 #pragma unroll
-        for (int j = 0; j < 4; j++) raw[j].widen(x[j]);
+        for (int j = 0; j < 4; j++) {
+            raw[j].widen(x[j]);
+            range[j] = range8(raw[j]);
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; j++) load8(row, k0 + 32 * j, cols, false, x[j]);
-    }
+        for (int j = 0; j < 4; j++) {
+            load8(row, k0 + 32 * j, cols, false, x[j]);
+            range[j] = {INFINITY, -INFINITY};
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        mn[j] = INFINITY;
-        mx[j] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            x[j][i] = min_nan(max_nan(x[j][i], -BOUND), BOUND);
-            if (whole || K * QM_TILE_COLS + 32 * j + 8 * t + i < m.cols) {
-                mn[j] = min_nan(mn[j], x[j][i]);
-                mx[j] = max_nan(mx[j], x[j][i]);
-            }
+            for (int i = 0; i < 8; i++)
+                if (k0 + 32 * j + i < m.cols) range[j] = join(range[j], {x[j][i], x[j][i]});
         }
     }
     constexpr int PER = GROUP / 32;  // words of a group
     uint32_t words[4];
 #pragma unroll
     for (int j0 = 0; j0 < 4; j0 += PER) {
-        float lo = mn[j0], hi = mx[j0];
+        Range a = range[j0];
 #pragma unroll
-        for (int j = j0 + 1; j < j0 + PER; j++) {
-            lo = min_nan(lo, mn[j]);
-            hi = max_nan(hi, mx[j]);
-        }
+        for (int j = j0 + 1; j < j0 + PER; j++) a = join(a, range[j]);
 #pragma unroll
-        for (int o = 1; o < 4; o *= 2) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        for (int o = 1; o < 4; o *= 2) a = join(a, {__shfl_xor_sync(0xffffffffu, a.mn, o), __shfl_xor_sync(0xffffffffu, a.mx, o)});
+        const int first = int(K) * QM_TILE_COLS + 32 * j0;
+        if (!held || (!WHOLE && first >= m.cols)) a = {0.f, 0.f};
+        if (!(a.mn >= -BOUND && a.mx <= BOUND)) {  // (rare: values past the bound, infinities, NaN)
+#pragma unroll
+            for (int j = j0; j < j0 + PER; j++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) x[j][i] = min_nan(max_nan(x[j][i], -BOUND), BOUND);
+            a = {min_nan(max_nan(a.mn, -BOUND), BOUND), min_nan(max_nan(a.mx, -BOUND), BOUND)};
         }
-        const int64_t first = K * QM_TILE_COLS + 32 * j0;
-        if (!held || first >= m.cols) lo = hi = 0.f;
+        const float lo = a.mn, hi = a.mx;
         const __half lo_h = __float2half_rn(lo);
         const float base = __half2float(lo_h);
         const __half step_h = __float2half_rn(fmaxf(__fdiv_rn(hi - base, 15.f), 0.f));  // (lo may round past the largest)
@@ -99,10 +116,12 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const float d = x[j][i] - base, q0 = d * inv, q = fmaf(fmaf(-q0, step, d), inv, q0);
-                // (1.5 * 2^23 added: the nearest integer, ties to even, in the lower bits; NaN: 0, as its group's lo is one)
-                const uint32_t c = __float_as_uint(fminf(fmaxf(q, 0.f), 15.f) + 12582912.f) - 0x4b400000u;
-                word += (whole || first + 32 * (j - j0) + 8 * t + i < m.cols ? c : 0u) << (4 * (i / 2 + 4 * (i % 2)));
+                const float code = fminf(fmaxf(q, 0.f), 15.f) + 12582912.f;
+                // (1.5 * 2^23 added: the nearest integer, ties to even, in the lower bits; NaN: 0, as its group's lo is one. The
+                // sum of the eight goes past 32 bits by what the constants put there, which is taken off behind.)
+                word += (WHOLE || first + 32 * (j - j0) + 8 * t + i < m.cols ? __float_as_uint(code) : 0x4b400000u) << (4 * (i / 2 + 4 * (i % 2)));
             }
+            word -= 0x4b400000u * 0x11111111u;
             words[j] = __funnelshift_l(word, word, 3);
         }
         if (t == 0) {
@@ -111,6 +130,18 @@ __global__ void __launch_bounds__(RW_THREADS) k_qmat_write(ll_qmat m, const T *w
         }
     }
     reinterpret_cast<uint4 *>(m.codes)[half * 32 + lane] = make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(RW_THREADS, 4) k_qmat_write(ll_qmat m, const T *w, int64_t stride, bool vec) {
+    const int KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;
+    const int64_t half = (int64_t(blockIdx.x) * RW_THREADS + threadIdx.x) >> 5;  // (a warp's half tile)
+    const int lane = threadIdx.x & 31;
+    const int64_t tile = half >> 1;
+    const int64_t R = tile / KT, K = tile % KT;
+    if (R >= (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS) return;
+    if (vec && (K + 1) * QM_TILE_COLS <= m.cols) write_half_tile<T, GROUP, true>(m, w, stride, half, tile, R, K, lane);
+    else write_half_tile<T, GROUP, false>(m, w, stride, half, tile, R, K, lane);
 }
 
 // Read back, with k_qmat_write's lanes.
