@@ -9,7 +9,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "call.h"
 #include "qmat.cuh"
@@ -376,8 +375,12 @@ int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
 }  // namespace
 
 int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st) {
-    static const char *force = getenv("QM_TC");
-    if (force && atoi(force)) {
+    // bf16 outputs of more columns than a pass of k_qmat_mv takes, where its products for many row tiles take longer than
+    // unpacking x in every block of the other kernel. us there / here, groups of 128, at 32 and at 64 rows of bf16 x:
+    // 128256 x 2048 61 / 109, 134 / 209; 28672 x 4096 39 / 49, 79 / 92; 17408 x 2048 20 / 18, 28 / 32; 18432 x 8192
+    // 58 / 54, 113 / 102; 4096 x 14336 (not there) 33 / 24, 61 / 46. At 16 rows of fp32: 58 / 419, 34 / 150, 17 / 49, 40 / 272.
+    const int columns = n * (x.type == LL_F32 ? Column<LL_F32>::TERMS : 1);
+    if (y.type == LL_BF16 && columns > 16 && (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS >= 7 * nsm) {
         const int rc = launch_qmat_tc(m, x, n, add, y, nsm, st);
         if (rc != LL_ERR_SHAPE) return rc;
     }

@@ -457,11 +457,12 @@ typedef struct {
 /* y = x W^T (+ add): for each of n rows, y[i][r] = sum_k W[r][k] x[i][k] + add[i][r], one
  * rounding to y's type. x [n][cols]: LL_BF16, LL_F32 or LL_E4M3 with scales (a value is its
  * code times its scale). y and add [n][rows]: LL_BF16 or LL_F32, both of one type; add may
- * be NULL, and may be y itself. n: 1 to 2^19. The codes are multiplied as integers and sums held
- * in fp32; fp32 x enters with all its bits (as three bf16 terms). bf16 y of many rows n of bf16 or
- * e4m3 x may be computed from W and x in fp16's 11 bits (x scaled by a power of two a
- * row). A row of x that holds a NaN or an infinity gives infinities or NaN in its own
- * row of y alone; finite values should be below 2^100 in size. */
+ * be NULL, and may be y itself. n: 1 to 2^19. The codes are multiplied as integers, sums held
+ * in fp32, and fp32 x enters with all its bits (as three bf16 terms). Only bf16 y of many rows
+ * and large matrices may be computed from W and x in fp16's 11 bits (x scaled by a power of
+ * two a row), lo + 15 step then within fp16's range, as ll_qmat_write leaves it. A row of x
+ * that holds a NaN or an infinity gives infinities or NaN in its own row of y alone; finite
+ * values should be below 2^100 in size. */
 int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *add, const ll_rows *y, void *stream, char *err,
                 size_t err_len);
 

@@ -83,17 +83,17 @@ def product(m, x, add, dtype):
     A group of 128 columns is at most 8 matrix instructions with fp32 sums of exact products: each adds
     16 products to a sum, in an order and with a cut that are not documented: 2^-21 of the sum of their sizes
     is allowed. lo and step join in one fp32 operation each, (2 for e4m3 scales), and sums go over the groups,
-    8 warps and 4 terms of fp32 x, and add: a rounding of 2^-24 for each. fp32 x may come as 20 bits (2^-20 of a value,
-    2^-33 of the largest of 128 at least). bf16 outputs may take W and x rounded to fp16's 11 bits (2^-12 of a value; below
-    2^-14 of W, 2^-25)."""
+    8 warps and 3 terms of fp32 x, and add: a rounding of 2^-24 for each. bf16 outputs may take W and x rounded to
+    fp16's 11 bits (half a step is 2^-11 of a value, both (1 + 2^-11)^2 - 1; below 2^-14 of W, 2^-25; of x 2^-39 of its
+    row's largest)."""
     code, lo, step = unpack(m.codes, m.params, m.rows, m.cols)
     y = x @ (lo + step * code).t()
     size = x.abs() @ (step.abs() * (code - 8).abs() + (lo + 8 * step).abs()).t()
     groups = -(-m.cols // 128) * (128 // m.group)
     tol = (8 * 2.0 ** -21 + (2 * groups + 16) * 2.0 ** -24) * size
-    tol = tol + 2.0 ** -20 * size + 2.0 ** -33 * cols_of(x) * (lo.abs() + 15 * step.abs()).sum(1)
     if dtype == torch.bfloat16:
-        tol = tol + 2.0 ** -11 * 1.001 * (x.abs() @ (lo + step * code).abs().t()) + 2.0 ** -25 * x.abs().sum(1, keepdim=True)
+        tol = tol + 2.0 ** -10 * 1.001 * (x.abs() @ (lo + step * code).abs().t()) + 2.0 ** -25 * x.abs().sum(1, keepdim=True)
+        tol = tol + 2.0 ** -39 * x.abs().amax(1, keepdim=True) * (lo.abs() + 15 * step.abs()).sum(1)
     if add is not None:
         y = y + add
         tol = tol + 2.0 ** -24 * (y.abs() + add.abs())

@@ -189,3 +189,98 @@ def test_a_row_that_is_not_finite_stays_alone(n, kind):
         assert not bool(torch.isfinite(got[1:3].float()).any())
         keep = [i for i in range(n) if i not in (1, 2)]
         assert torch.equal(got[keep], want[keep])
+
+
+def large_matrix(rows, cols, group, seed):
+    """Random codes and parameters (zeros past the end), and the values they stand for in 64 bits on the GPU."""
+    g = gen(seed)
+    rt, kt = -(-rows // 16), -(-cols // 128)
+    codes = torch.randint(0, 256, (rt, kt, 1024), generator=g, device="cuda", dtype=torch.uint8)
+    params = torch.empty(rt, kt, 128 // group, 16, 2, device="cuda")
+    params[..., 1] = 0.01 * torch.rand(params.shape[:-1], generator=g, device="cuda")
+    params[..., 0] = -7.5 * params[..., 1] + 0.01 * torch.randn(params.shape[:-1], generator=g, device="cuda")
+    m = ll.Q4Matrix(codes, params.half(), rows, cols)
+    return m, m.read(dtype=torch.float32).double()
+
+
+# (from 16 * 7 * 152 rows on bf16 outputs of more than 16 rows of x, 5 of fp32's, take another kernel: row ends inside and at a
+# border of its 128 rows, columns that one block holds, that 2 and 8 share, and that none do)
+@pytest.mark.parametrize("rows,cols,group", [(17024, 40, 32), (17025, 129, 128), (20000, 1000, 64), (19456, 4096, 128), (17100, 9000, 32), (40000, 2048, 128)])
+@pytest.mark.parametrize("n", [6, 17, 32, 33, 64, 70])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
+def test_large_matrices(rows, cols, group, n, kind):
+    m, w = large_matrix(rows, cols, group, rows)
+    x = torch.randn(n, cols, generator=gen(n), device="cuda")
+    x[:, ::37] *= 30
+    x[n // 2] *= 2.0 ** 60  # rows of very different sizes
+    x[n // 3] *= 2.0 ** -60
+    x[0] = 0
+    scale = None
+    if kind == torch.float8_e4m3fn:
+        tiles = -(-cols // 128)
+        scale = torch.nn.functional.pad(x, (0, tiles * 128 - cols)).unflatten(1, (-1, 128)).abs().amax(2) / 448 + 1e-30
+        each = scale.repeat_interleave(128, 1)[:, :cols]
+        x = (x / each).to(kind)
+        wide = x.double() * each.double()
+    else:
+        x = x.to(kind)
+        wide = x.double()
+    add = torch.randn(n, rows, generator=gen(5), device="cuda").bfloat16() if n % 2 else None
+    y = torch.full((n, rows + 5), 7.0, device="cuda", dtype=torch.bfloat16)
+    m.matvec(x, scale=scale, add=add, out=y[:, :rows])
+    assert bool((y[:, rows:] == 7).all())
+    got = y[:, :rows].double()
+    # as step_ref.product: W rounded to fp32 in `w` (2^-24), W and x each to fp16 (2^-11: both (1 + 2^-11)^2 - 1), and sums of at most cols / 16 instructions
+    size = wide.abs() @ w.abs().t()
+    want = wide @ w.t()
+    tol = (2.0 ** -10 * 1.001 + 2.0 ** -24 + (-(-cols // 16) + 8) * 2.0 ** -21) * size
+    tol += 2.0 ** -25 * wide.abs().sum(1, keepdim=True) + 2.0 ** -39 * wide.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    if add is not None:
+        want = want + add.double()
+        tol += 2.0 ** -24 * (want.abs() + add.double().abs())
+    tol += 2.0 ** -8 * (want.abs() + tol) + 1e-37
+    off = (got - want).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    assert bool((off.norm(dim=1) <= 2.0 ** -8 * want.norm(dim=1) + 1e-37).all())  # (a row in all: as near as one rounding, most of it bf16's)
+    again = m.matvec(x, scale=scale, add=add, out_dtype=torch.bfloat16)
+    assert torch.equal(y[:, :rows], again)
+
+
+@pytest.mark.parametrize("n", [20, 64])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_large_matrices_operands(n, kind):
+    """Rows apart and unaligned, the same for all, a row that is not finite, and the sum written over add."""
+    rows, cols = 17040, 520
+    m, _ = large_matrix(rows, cols, 64, 3)
+    x = torch.randn(n, cols, generator=gen(2), device="cuda").to(kind)
+    want = m.matvec(x)
+    for pad, shift in ((8, 0), (3, 1), (1, 5)):
+        store = torch.full((n, cols + pad + shift), float("nan"), dtype=kind, device="cuda")
+        view = store[:, shift:shift + cols]
+        view.copy_(x)
+        assert torch.equal(m.matvec(view), want)
+    assert torch.equal(m.matvec(x[:1].expand(n, cols)), want[:1].expand(n, rows))
+    add = torch.randn(n, rows, generator=gen(3), device="cuda").bfloat16()
+    both = m.matvec(x, add=add)
+    own = add.clone()
+    m.matvec(x, add=own, out=own)
+    assert torch.equal(own, both)
+    x[1, 17], x[2, 519] = float("nan"), float("-inf")
+    got = m.matvec(x)
+    assert not bool(torch.isfinite(got[1:3].float()).any())
+    keep = [i for i in range(n) if i not in (1, 2)]
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_steps_past_fp16s_quarter():
+    """Steps so large that 2^18 of them passes fp16's largest (0.25 and up)."""
+    rows, cols, n = 17040, 256, 24
+    m, _ = large_matrix(rows, cols, 128, 4)
+    pairs = m.params.view(-1, 2)
+    pairs[::3, 1] = 4000.0
+    pairs[::3, 0] = -30000.0
+    w = m.read(dtype=torch.float32).double()
+    x = torch.randn(n, cols, generator=gen(2), device="cuda").bfloat16()
+    got, want = m.matvec(x).double(), x.double() @ w.t()
+    tol = 2.0 ** -11 * 1.01 * (x.double().abs() @ w.abs().t())
+    assert bool(((got - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all())
