@@ -440,51 +440,67 @@ def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=No
     return out
 
 
-def _device_call(fn, device, *args) -> None:
-    """One call without a handle on torch's current stream of `device`."""
-    import torch
-    index = device.index
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _device_call(fn, device, *args)
-    err = _kvq_thread.err
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(index), err, 256)
-    if rc != LL_OK:
-        raise LLError(rc, err.value.decode())
-
-
 class _Types:
-    """torch's dtypes by the library's, looked up once."""
+    """torch's dtypes by the library's, and what every call looks up, found once."""
     codes = None
 
     @classmethod
     def get(cls) -> dict:
         if cls.codes is None:
             import torch
-            cls.codes = {torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float8_e4m3fn: LL_E4M3}
             cls.bf16, cls.f32, cls.e4m3, cls.int32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+            cls.torch, cls.c, cls.lib = torch, torch._C, lib()
+            cls.codes = {torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float8_e4m3fn: LL_E4M3}
         return cls.codes
 
 
-def _matrix_rows(t, name: str, shape, device, written: bool = False, scale=None, group: int = 0):
-    """t [n, width] as an ll_rows' bytes (the library checks types and strides, which it sees)."""
-    if getattr(t, "device", None) != device or device.type != "cuda":
-        raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor" + (f" on {device}" if device is not None and device.type == "cuda" else ""))
-    code = _Types.get().get(t.dtype)
-    if code is None:
+def _device_call(fn, index: int, *args) -> None:
+    """One call without a handle on torch's current stream of device `index`."""
+    c = _Types.c
+    if index != c._cuda_getDevice():
+        with _Types.torch.cuda.device(index):
+            return _device_call(fn, index, *args)
+    err = _kvq_thread.err
+    rc = fn(*args, c._cuda_getCurrentRawStream(index), err, 256)
+    if rc:
+        raise LLError(rc, err.value.decode())
+
+
+def _matrix_rows(t, name: str, shape, index: int, scale: int = 0, group: int = 0) -> bytes:
+    """t (of this shape [n, width], on device `index`) as an ll_rows' bytes. (The library checks types and
+    strides, which it sees. A small call's GPU work takes two microseconds, so what is right is passed by as few lookups
+    as show it; the rest finds the reason.)"""
+    try:
+        code = _Types.codes[t.dtype]
+        if t.get_device() == index and t.shape == shape:
+            stride, last = t.stride()
+            if last == 1 or shape[1] <= 1:
+                return _matrix_rows_bytes(t.data_ptr(), stride, code, group, scale)
+    except (AttributeError, KeyError):
+        pass
+    if not getattr(t, "is_cuda", False) or t.get_device() != index:
+        raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index >= 0 else ""))
+    if t.dtype not in _Types.codes:
         raise LLError(LL_ERR_ARG, f"{name} must not be {t.dtype}")
     if t.shape != shape:
         raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {list(shape)}")
-    stride, last = t.stride()
-    if last != 1 and shape[1] > 1:
-        raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
-    return _matrix_rows_bytes(t.data_ptr(), stride, code, group, 0 if scale is None else scale.data_ptr())
+    raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
 
 
-def _scales(scale, name: str, n: int, width: int, device):
+def _array(t, name: str, dtype, shape, index: int) -> int:
+    """The address of a contiguous tensor of this type and shape on device `index`."""
+    try:
+        if t.get_device() == index and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise LLError(LL_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda" + (f":{index}" if index >= 0 else ""))
+
+
+def _scales(scale, name: str, n: int, width: int, index: int):
     """The group (0: the row) that the scales [n, groups] of e4m3 rows stand for."""
-    if getattr(scale, "device", None) != device or scale.dtype != _Types.f32 or scale.dim() != 2 or not scale.is_contiguous():
-        raise LLError(LL_ERR_ARG, f"{name} must be a contiguous float32 tensor [{n}, groups] on {device}")
+    if not getattr(scale, "is_cuda", False) or scale.get_device() != index or scale.dtype != _Types.f32 or scale.dim() != 2 or not scale.is_contiguous():
+        raise LLError(LL_ERR_ARG, f"{name} must be a contiguous float32 tensor [{n}, groups] on cuda:{index}")
     tiles = (width + 127) // 128
     if scale.shape not in ((n, 1), (n, tiles)):
         raise LLError(LL_ERR_ARG, f"{name} is {tuple(scale.shape)}, the call needs [{n}, 1] or [{n}, {tiles}]")
@@ -493,16 +509,15 @@ def _scales(scale, name: str, n: int, width: int, device):
 
 def ll_qmat_write(m: "Q4Matrix", w) -> None:
     """Quantise w [rows, cols] (bf16 or fp32) into the matrix."""
-    _matrix_rows(w, "w", (m.rows, m.cols), m.device)
+    _matrix_rows(w, "w", (m.rows, m.cols), m.index)
     _kvq_call(m.lib.ll_qmat_write, m, w.data_ptr(), _Types.codes[w.dtype], w.stride(0))
 
 
 def ll_qmat_read(m: "Q4Matrix", out=None, dtype=None):
     """The matrix's values [rows, cols], each rounded once to bf16 (or fp32)."""
     if out is None:
-        import torch
-        out = torch.empty(m.rows, m.cols, dtype=dtype or torch.bfloat16, device=m.device)
-    _matrix_rows(out, "out", (m.rows, m.cols), m.device, True)
+        out = _Types.torch.empty(m.rows, m.cols, dtype=dtype or _Types.bf16, device=m.device)
+    _matrix_rows(out, "out", (m.rows, m.cols), m.index)
     _kvq_call(m.lib.ll_qmat_read, m, out.data_ptr(), _Types.codes[out.dtype], out.stride(0))
     return out
 
@@ -511,26 +526,25 @@ def ll_qmat_mul(m: "Q4Matrix", x, scale=None, add=None, out=None, out_dtype=None
     """x [n, cols] times the matrix's transpose (+ add [n, rows]): [n, rows]. x is bf16, fp32, or
     float8_e4m3fn with ``scale`` (fp32 [n, 1] or [n, ceil(cols / 128)]); out like add, or of
     ``out_dtype`` (bf16 if None). out may be add."""
-    device = m.device
+    index = m.index
     if getattr(x, "ndim", 0) != 2:
         raise LLError(LL_ERR_ARG, "x must be [n, cols]")
-    n = x.shape[0]
-    types = _Types.get()
-    group = 0
+    n, cols = x.shape
     if x.dtype == _Types.e4m3:
         if scale is None:
             raise LLError(LL_ERR_ARG, "x in float8_e4m3fn needs its scales")
-        group = _scales(scale, "scale", n, m.cols, device)
+        group = _scales(scale, "scale", n, m.cols, index)
+        xr = _matrix_rows(x, "x", (n, m.cols), index, scale.data_ptr(), group)
     elif scale is not None:
         raise LLError(LL_ERR_ARG, f"x in {x.dtype} has no scales")
-    xr = _matrix_rows(x, "x", (n, m.cols), device, False, scale, group)
+    else:
+        xr = _matrix_rows(x, "x", (n, m.cols), index)
     shape = (n, m.rows)
     if out is None:
-        import torch
-        out = torch.empty(shape, dtype=out_dtype or (add.dtype if add is not None else torch.bfloat16), device=device)
-    yr = _matrix_rows(out, "out", shape, device, True)
-    ar = _matrix_rows(add, "add", shape, device) if add is not None else None
-    if types[out.dtype] == LL_E4M3:
+        out = _Types.torch.empty(shape, dtype=out_dtype or (add.dtype if add is not None else _Types.bf16), device=m.device)
+    yr = _matrix_rows(out, "out", shape, index)
+    ar = None if add is None else _matrix_rows(add, "add", shape, index)
+    if out.dtype == _Types.e4m3:
         raise LLError(LL_ERR_ARG, "out must be bfloat16 or float32")
     _kvq_call(m.lib.ll_qmat_mul, m, xr, n, ar, yr)
     return out
@@ -540,35 +554,36 @@ def ll_rmsnorm(x, gain, eps: float = 1e-5, residual=None, residual_out=None, out
     """RMS norm of the rows of x [n, width], with the residual's addition in front if there is
     one (residual_out: where the sum goes, residual itself if None). Returns out (of x's type, or
     ``out_dtype``); for float8_e4m3fn (out, scale), a scale for each row (group 0) or 128 columns."""
-    if getattr(x, "ndim", 0) != 2:
-        raise LLError(LL_ERR_ARG, "x must be [n, width]")
-    import torch
-    shape, device = x.shape, x.device
+    if not getattr(x, "is_cuda", False) or x.ndim != 2:
+        raise LLError(LL_ERR_ARG, "x must be a CUDA tensor [n, width]")
+    types = _Types
+    if types.codes is None:
+        types.get()
+    shape, index = x.shape, x.get_device()
     n, width = shape
+    xr = _matrix_rows(x, "x", shape, index)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
-    xr = _matrix_rows(x, "x", shape, device)
-    e4m3 = out.dtype == _Types.e4m3
+        out = types.torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    e4m3 = getattr(out, "dtype", None) == types.e4m3
+    at = 0
     if group not in (0, 128) or (group and not e4m3):
         raise LLError(LL_ERR_ARG, "group is 0, or 128 for float8_e4m3fn")
     if e4m3:
         groups = (n, (width + 127) // 128 if group else 1)
         if scale is None:
-            scale = torch.empty(groups, dtype=torch.float32, device=device)
-        elif getattr(scale, "device", None) != device or scale.dtype != torch.float32 or scale.shape != groups or not scale.is_contiguous():
-            raise LLError(LL_ERR_ARG, f"scale must be a contiguous float32 tensor {list(groups)} on {device}")
+            scale = types.torch.empty(groups, dtype=types.f32, device=x.device)
+        at = _array(scale, "scale", types.f32, groups, index)
     elif scale is not None:
         raise LLError(LL_ERR_ARG, f"out in {out.dtype} has no scales")
-    outr = _matrix_rows(out, "out", shape, device, True, scale, group)
-    if getattr(gain, "device", None) != device or gain.dtype != torch.bfloat16 or gain.shape != (width,) or not gain.is_contiguous():
-        raise LLError(LL_ERR_ARG, f"gain must be a contiguous bfloat16 tensor [{width}] on {device}")
+    outr = _matrix_rows(out, "out", shape, index, at, group)
+    gp = _array(gain, "gain", types.bf16, (width,), index)
     rr = ro = None
     if residual is not None:
-        rr = _matrix_rows(residual, "residual", shape, device)
-        ro = rr if residual_out is None else _matrix_rows(residual_out, "residual_out", shape, device, True)
+        rr = _matrix_rows(residual, "residual", shape, index)
+        ro = rr if residual_out is None else _matrix_rows(residual_out, "residual_out", shape, index)
     elif residual_out is not None:
         raise LLError(LL_ERR_ARG, "residual_out needs a residual")
-    _device_call(lib().ll_rmsnorm, device, xr, rr, ro, gain.data_ptr(), eps, n, width, outr)
+    _device_call(types.lib.ll_rmsnorm, index, xr, rr, ro, gp, eps, n, width, outr)
     return (out, scale) if e4m3 else out
 
 
@@ -578,37 +593,34 @@ def ll_verify(logits, drafts, u, probs=None, n_drafts=None, temperature=None, to
     probs [n_seq, n_draft, vocab]: the drafts' own distribution, or None; n_drafts int32 [n_seq] and
     temperature fp32 [n_seq], or None. Returns tokens int32 [n_seq, n_draft + 1] (accepted drafts, the new
     token, then -1) and accepted int32 [n_seq]."""
-    if getattr(logits, "ndim", 0) != 3 or not logits.is_cuda:
+    if not getattr(logits, "is_cuda", False) or logits.ndim != 3:
         raise LLError(LL_ERR_ARG, "logits must be a CUDA tensor [n_seq, n_draft + 1, vocab]")
-    device = logits.device
+    types = _Types
+    if types.codes is None:
+        types.get()
+    index = logits.get_device()
     S, rows, V = logits.shape
     D = rows - 1
-    code = _Types.get().get(logits.dtype)
-    f32, int32 = _Types.f32, _Types.int32
+    code = types.codes.get(logits.dtype)
+    f32, int32 = types.f32, types.int32
     ls, lr, last = logits.stride()
     if code not in (LL_BF16, LL_F32) or (last != 1 and V > 1):
         raise LLError(LL_ERR_ARG, "logits must be bfloat16 or float32, contiguous in the last dim")
-    if tokens is None or accepted is None:
-        import torch
-        tokens = torch.empty((S, rows), dtype=int32, device=device) if tokens is None else tokens
-        accepted = torch.empty((S,), dtype=int32, device=device) if accepted is None else accepted
-
-    def need(t, name, dtype, shape):
-        if getattr(t, "device", None) != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise LLError(LL_ERR_ARG, f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
-        return t.data_ptr()
-
-    dp = need(drafts, "drafts", int32, (S, D)) if D or drafts is not None else None
-    up = need(u, "u", f32, (S, rows))
-    tp, ap = need(tokens, "tokens", int32, (S, rows)), need(accepted, "accepted", int32, (S,))
-    np_ = need(n_drafts, "n_drafts", int32, (S,)) if n_drafts is not None else None
-    temp = need(temperature, "temperature", f32, (S,)) if temperature is not None else None
+    if tokens is None:
+        tokens = types.torch.empty((S, rows), dtype=int32, device=logits.device)
+    if accepted is None:
+        accepted = types.torch.empty((S,), dtype=int32, device=logits.device)
+    dp = _array(drafts, "drafts", int32, (S, D), index) if D or drafts is not None else None
+    up = _array(u, "u", f32, (S, rows), index)
+    tp, ap = _array(tokens, "tokens", int32, (S, rows), index), _array(accepted, "accepted", int32, (S,), index)
+    np_ = _array(n_drafts, "n_drafts", int32, (S,), index) if n_drafts is not None else None
+    temp = _array(temperature, "temperature", f32, (S,), index) if temperature is not None else None
     pp, ps, pr = None, 0, 0
     if probs is not None:
-        if getattr(probs, "device", None) != device or probs.dtype != f32 or probs.shape != (S, D, V) or (V > 1 and probs.stride(2) != 1):
-            raise LLError(LL_ERR_ARG, f"probs must be a float32 tensor {[S, D, V]} on {device}, contiguous in the last dim")
+        if not getattr(probs, "is_cuda", False) or probs.get_device() != index or probs.dtype != f32 or probs.shape != (S, D, V) or (V > 1 and probs.stride(2) != 1):
+            raise LLError(LL_ERR_ARG, f"probs must be a float32 tensor {[S, D, V]} on cuda:{index}, contiguous in the last dim")
         pp, ps, pr = probs.data_ptr(), probs.stride(0), probs.stride(1)
-    _device_call(lib().ll_verify, device, logits.data_ptr(), code, ls, lr, dp, np_, pp, ps, pr, up, temp, S, D, V, tp, ap)
+    _device_call(types.lib.ll_verify, index, logits.data_ptr(), code, ls, lr, dp, np_, pp, ps, pr, up, temp, S, D, V, tp, ap)
     return tokens, accepted
 
 
@@ -1007,6 +1019,7 @@ class Rope:
         self.table = ll_rope_table()
         self.ref = ctypes.byref(self.table)
         self.lib, self.head_dim = lib(), head_dim
+        self.codes = {t: code for t, code in _Types.get().items() if code != LL_E4M3}
         err = ctypes.create_string_buffer(256)
         rc = self.lib.ll_rope_plan(self.ref, head_dim, head_dim if rot_dims is None else rot_dims, int(interleaved), theta,
                                    list(keys).index(kind), s.get("factor", 1.0), s.get("low", 0.0), s.get("high", 0.0),
@@ -1014,48 +1027,54 @@ class Rope:
         if rc != LL_OK:
             raise LLError(rc, err.value.decode())
 
-    def _rows(self, t, name: str, like, heads: int, written: bool):
-        if getattr(t, "device", None) != like.device or t.dtype != like.dtype:
-            raise LLError(LL_ERR_ARG, f"{name} must be {like.dtype} on {like.device}, as q")
-        if t.shape != (like.shape[0], like.shape[1], heads, self.head_dim):
-            raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {[*like.shape[:2], heads, self.head_dim]}")
-        seq, token, head, last = t.stride()
+    def _rows(self, t, name: str, shape, dtype, index: int, written: bool) -> bytes:
+        try:
+            if t.get_device() == index and t.dtype == dtype and t.shape == shape:
+                seq, token, head, last = t.stride()
+                if last == 1 and (not written or t.is_contiguous()):
+                    return _rows_bytes(t.data_ptr(), seq, token, head)
+        except AttributeError:
+            pass
+        if not getattr(t, "is_cuda", False) or t.get_device() != index or t.dtype != dtype:
+            raise LLError(LL_ERR_ARG, f"{name} must be {dtype} on cuda:{index}, as q")
+        if t.shape != shape:
+            raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {list(shape)}")
         if last != 1:
             raise LLError(LL_ERR_ARG, f"{name}'s last dim must be contiguous")
-        if written and not t.is_contiguous():  # no two rows of an output may share memory
-            reach = self.head_dim
-            for stride, size in sorted(((seq, t.shape[0]), (token, t.shape[1]), (head, heads))):
-                if size > 1:
-                    if stride < reach:
-                        raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
-                    reach += stride * (size - 1)
+        reach = self.head_dim  # (no two rows of an output may share memory)
+        for stride, size in sorted(((seq, shape[0]), (token, shape[1]), (head, shape[2]))):
+            if size > 1:
+                if stride < reach:
+                    raise LLError(LL_ERR_ARG, f"{name} is written and its rows overlap")
+                reach += stride * (size - 1)
         return _rows_bytes(t.data_ptr(), seq, token, head)
 
     def apply(self, q, k, lens, n_toks=None, q_out=None, k_out=None, inverse: bool = False):
         """Turn the last tokens' q [n_seq, n_tok, n_q_heads, head_dim] and k [n_seq, n_tok, n_k_heads, head_dim]
         (or None), bf16 or fp32, into q_out and k_out (in place where None). Rows of padded
         tokens keep what they hold."""
-        if getattr(q, "ndim", 0) != 4 or not q.is_cuda:
+        if not getattr(q, "is_cuda", False) or q.ndim != 4:
             raise LLError(LL_ERR_ARG, "q must be a CUDA tensor [n_seq, n_tok, n_q_heads, head_dim]")
-        code = _Types.get().get(q.dtype)
-        if code not in (LL_BF16, LL_F32):
-            raise LLError(LL_ERR_ARG, f"q must be bfloat16 or float32, not {q.dtype}")
-        S, n_tok, heads, _ = q.shape
-        qo = q if q_out is None else q_out
-        qr, qor = self._rows(q, "q", q, heads, q_out is None), self._rows(qo, "q_out", q, heads, True)
+        dtype, index, shape = q.dtype, q.get_device(), q.shape
+        code = self.codes.get(dtype)
+        if code is None:
+            raise LLError(LL_ERR_ARG, f"q must be bfloat16 or float32, not {dtype}")
+        S, n_tok, heads, width = shape
+        if width != self.head_dim:
+            raise LLError(LL_ERR_ARG, f"q's heads are {width} wide, not {self.head_dim}")
+        qr = self._rows(q, "q", shape, dtype, index, q_out is None)
+        qor = qr if q_out is None else self._rows(q_out, "q_out", shape, dtype, index, True)
         kr = kor = None
         k_heads = 0
         if k is not None:
             k_heads = k.shape[2] if getattr(k, "ndim", 0) == 4 else 0
-            kr = self._rows(k, "k", q, k_heads, k_out is None)
-            kor = kr if k_out is None else self._rows(k_out, "k_out", q, k_heads, True)
+            shape = (S, n_tok, k_heads, width)
+            kr = self._rows(k, "k", shape, dtype, index, k_out is None)
+            kor = kr if k_out is None else self._rows(k_out, "k_out", shape, dtype, index, True)
         elif k_out is not None:
             raise LLError(LL_ERR_ARG, "k_out needs a k")
-        for t, name in ((lens, "lens"), (n_toks, "n_toks")):
-            if t is None and name == "n_toks":
-                continue
-            if getattr(t, "device", None) != q.device or t.dtype != _Types.int32 or t.shape != (S,) or not t.is_contiguous():
-                raise LLError(LL_ERR_ARG, f"{name} must be a contiguous int32 tensor [{S}] on {q.device}")
-        _device_call(self.lib.ll_rope, q.device, self.ref, qr, qor, heads, kr, kor, k_heads, code, S, n_tok, lens.data_ptr(),
-                     n_toks.data_ptr() if n_toks is not None else None, int(inverse))
-        return qo, (k if k_out is None else k_out)
+        int32 = _Types.int32
+        lp = _array(lens, "lens", int32, (S,), index)
+        np_ = None if n_toks is None else _array(n_toks, "n_toks", int32, (S,), index)
+        _device_call(self.lib.ll_rope, index, self.ref, qr, qor, heads, kr, kor, k_heads, code, S, n_tok, lp, np_, 1 if inverse else 0)
+        return q if q_out is None else q_out, (k if k_out is None else k_out)
