@@ -263,7 +263,7 @@ __device__ __forceinline__ int quotient(int e, float per) { return int((float(e)
 template <int XT, int NC, int PG>
 __device__ __forceinline__ void stage_x(const TcArgs &a, uint32_t operand, int first, int tile0, int tiles) {
     using S = Shape<NC, PG>;
-    constexpr int BATCH = XT == LL_F32 ? 4 : 8;  // tokens' tiles of a thread on their way at once
+    constexpr int BATCH = 4;  // tokens' tiles of a thread on their way at once (8: more code, which runs once a launch, and 2 us more at 64)
     const uint32_t scales = operand + a.slice * S::TILE, tops = scales + NC * 4;
     const int u = threadIdx.x % 16, step = THREADS / 16;
     const int held = min(a.tokens, a.n - first), items = tiles * held;
