@@ -275,7 +275,7 @@ int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *ad
                 size_t err_len) {
     if (int rc = check_matrix(m, err, err_len)) return rc;
     if (n < 1) return report(err, err_len, LL_ERR_ARG, "n must be at least 1");
-    if (n > 1 << 19) return report(err, err_len, LL_ERR_SHAPE, "n must be at most 2^19");
+    if (n > 1 << 18) return report(err, err_len, LL_ERR_SHAPE, "n must be at most 2^18");
     if (int rc = ll::check_matrix_rows(x, "x", n, m->cols, true, false, err, err_len)) return rc;
     if (int rc = ll::check_matrix_rows(y, "y", n, m->rows, false, true, err, err_len)) return rc;
     if (add) {

@@ -221,6 +221,7 @@ extern "C" int ll_rmsnorm(const ll_rows *x, const ll_rows *residual, const ll_ro
     using ll::report;
     if (err && err_len) err[0] = '\0';
     if (n < 1) return report(err, err_len, LL_ERR_ARG, "n must be at least 1");
+    if (n > 1 << 30) return report(err, err_len, LL_ERR_SHAPE, "n must be at most 2^30");
     if (width < 1 || width > 32768) return report(err, err_len, LL_ERR_SHAPE, "width must be 1 to 32768");
     if (!(eps >= 0.f) || !isfinite(eps)) return report(err, err_len, LL_ERR_ARG, "eps must be finite and not negative");
     if (!gain || reinterpret_cast<uintptr_t>(gain) % 2) return report(err, err_len, LL_ERR_ARG, "gain is NULL or not aligned to its type");

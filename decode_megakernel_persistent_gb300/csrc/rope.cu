@@ -214,6 +214,7 @@ int ll_rope(const ll_rope_table *r, const ll_kvq_rows *q, const ll_kvq_rows *q_o
     if (type != LL_BF16 && type != LL_F32) return report(err, err_len, LL_ERR_ARG, "type must be LL_BF16 or LL_F32");
     if (n_seq < 1 || n_seq > 65535) return report(err, err_len, LL_ERR_SHAPE, "n_seq must be 1 to 65535");
     if (n_tok < 1) return report(err, err_len, LL_ERR_ARG, "n_tok must be at least 1");
+    if (n_tok > 1 << 30) return report(err, err_len, LL_ERR_SHAPE, "n_tok must be at most 2^30");
     if (n_q_heads < 1 || n_q_heads > 32767 || (k && (n_k_heads < 1 || n_k_heads > 32767)))
         return report(err, err_len, LL_ERR_SHAPE, "heads must be 1 to 32767");
     if (!k != !k_out) return report(err, err_len, LL_ERR_ARG, "k and k_out go together");

@@ -79,7 +79,7 @@ def test_products_that_are_refused(lib):
     def mul(x=None, n=3, add=None, y=None):
         return answer(lib.ll_qmat_mul, mat(), x or rows(), n, add, y or rows(data=131072))
     A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
-    for kw, code in ((dict(n=0), A), (dict(n=-1), A), (dict(n=(1 << 19) + 1), S), (dict(x=rows(data=None)), A), (dict(x=rows(data=65537)), A),
+    for kw, code in ((dict(n=0), A), (dict(n=-1), A), (dict(n=(1 << 18) + 1), S), (dict(x=rows(data=None)), A), (dict(x=rows(data=65537)), A),
                      (dict(x=rows(data=65538, type=1)), A), (dict(x=rows(type=3)), A), (dict(x=rows(type=2)), A), (dict(x=rows(type=2, scale=4098)), A),
                      (dict(x=rows(type=2, scale=4096, group=64)), A), (dict(y=rows(type=2, scale=4096)), A), (dict(y=rows(stride=63)), A),
                      (dict(y=rows(stride=0)), A), (dict(y=rows(data=None)), A), (dict(add=rows(type=1)), A), (dict(add=rows(data=None)), A)):
@@ -93,7 +93,7 @@ def test_norms_that_are_refused(lib):
         return answer(lib.ll_rmsnorm, x or rows(), res, res_out, gain, eps, n, width, out or rows(data=131072))
     A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
     r = rows(data=1 << 18)
-    for kw, code in ((dict(n=0), A), (dict(width=0), S), (dict(width=32769), S), (dict(eps=-1.0), A), (dict(eps=NAN), A), (dict(eps=INF), A), (dict(gain=None), A),
+    for kw, code in ((dict(n=0), A), (dict(n=(1 << 30) + 1), S), (dict(width=0), S), (dict(width=32769), S), (dict(eps=-1.0), A), (dict(eps=NAN), A), (dict(eps=INF), A), (dict(gain=None), A),
                      (dict(gain=4097), A), (dict(x=rows(type=2, scale=4096)), A), (dict(out=rows(type=2)), A), (dict(out=rows(type=2, scale=4096, group=32)), A),
                      (dict(out=rows(stride=255)), A), (dict(res=r), A), (dict(res_out=r), A), (dict(res=r, res_out=rows(data=1 << 18, type=1)), A),
                      (dict(res=r, res_out=rows(data=131072)), A), (dict(res=r, res_out=rows(data=1 << 18, stride=3)), A), (dict(x=rows(data=None)), A)):
@@ -145,7 +145,7 @@ def test_rotary_calls_that_are_refused(lib):
     k = kvq_rows(data=1 << 18)
     for kw, code in ((dict(t=None), A), (dict(t=ctypes.byref(bad)), A), (dict(q=kvq_rows(data=None)), A), (dict(q=kvq_rows(data=65544)), A),
                      (dict(qo=kvq_rows(token=4)), A), (dict(qo=kvq_rows(token=0)), A), (dict(nq=0), S), (dict(nq=40000), S), (dict(k=k), A), (dict(ko=k), A),
-                     (dict(k=k, ko=k, nk=0), S), (dict(k=k, ko=kvq_rows()), A), (dict(kind=2), A), (dict(S=0), S), (dict(S=65536), S), (dict(n=0), A),
+                     (dict(k=k, ko=k, nk=0), S), (dict(k=k, ko=kvq_rows()), A), (dict(kind=2), A), (dict(S=0), S), (dict(S=65536), S), (dict(n=0), A), (dict(n=(1 << 30) + 1), S),
                      (dict(lens=None), A), (dict(lens=66), A), (dict(n_toks=65), A)):
         rc, msg = rope(**kw)
         assert rc == code and msg, kw
