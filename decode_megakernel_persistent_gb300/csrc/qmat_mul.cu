@@ -144,9 +144,11 @@ struct Column {
     }
 };
 
-template <int NT>
+template <int NT, int R, int PG>
 struct MvGeo {
-    static constexpr int UNITS = 6, BLOCKS = NT == 1 ? 3 : 2;  // tiles of a warp in flight, blocks of an SM
+    static constexpr int UNITS = R == 4 ? 8 : 6, BLOCKS = NT == 1 && R < 4 ? 3 : 2;  // tiles of a warp in flight, blocks of an SM
+    static constexpr int PARTS = NT * R < 8 ? 2 : 1, PART = R * QM_TILE_ROWS * (8 * NT + 1);  // shares of two groups or one; floats of a warp's
+    static constexpr int RING = MV_WARPS * UNITS * (1024 + 64 * PG), SMEM = RING + PARTS * MV_WARPS * PART * 4;
 };
 
 // A few rows x: up to 8 NT columns. A warp takes R row tiles at a time and, of `splits` warps that share them, every
@@ -155,13 +157,13 @@ struct MvGeo {
 // EXACT: the codes as c - 8; otherwise as 16 + c, a subtraction a pair less, whose sums are some six times as large, and
 // so are their roundings.
 template <int XT, int NT, int R, int PG, bool EXACT>
-__global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const MvArgs a) {
+__global__ void __launch_bounds__(MV_THREADS, MvGeo<NT, R, PG>::BLOCKS) k_qmat_mv(const MvArgs a) {
     constexpr bool HALF = XT == LL_E4M3;
-    constexpr int TERMS = Column<XT>::TERMS, TOKENS = 8 * NT / TERMS, DEPTH = MvGeo<NT>::UNITS / R, STAGE = 1024 + 64 * PG;
+    constexpr int TERMS = Column<XT>::TERMS, TOKENS = 8 * NT / TERMS, DEPTH = MvGeo<NT, R, PG>::UNITS / R, STAGE = 1024 + 64 * PG;
     constexpr int ROWS = R * QM_TILE_ROWS;
     constexpr uint32_t ONE = HALF ? 0x3c003c00u : 0x3f803f80u;
     extern __shared__ __align__(16) uint8_t ring[];  // [warp][DEPTH][R][STAGE]
-    __shared__ float part[2][MV_WARPS][ROWS][8 * NT + 1];
+    using Geo = MvGeo<NT, R, PG>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int splits = 1 << a.log_splits, ks = warp & (splits - 1), team = warp >> a.log_splits, teams = MV_WARPS >> a.log_splits;
     const int groups = (a.RT + R - 1) / R, stride = gridDim.x * teams;
@@ -208,6 +210,7 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; i++) issue();
 
+    float *part = reinterpret_cast<float *>(ring + Geo::RING);  // [PARTS][warp][row][column]
     int stage = 0, parity = 0;
     Column<XT> col[NT];
 #pragma unroll
@@ -239,50 +242,52 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
             asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
             __syncwarp();  // (parameters come by other lanes' copies)
             const uint32_t at = stages + stage * (R * STAGE);
-            uint4 c[R][2];
+            float sc[NT][2];
+            if constexpr (XT == LL_E4M3) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int token = min(first + nt * 8 + 2 * t + e, a.n - 1);
+                        sc[nt][e] = __ldg(a.scale + int64_t(token) * a.scale_row + kt * a.scale_step);
+                    }
+            }
+            float sums[PG][NT][2];  // of a group's x
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                c[r][0] = lds16(at + r * STAGE + 16 * lane);
-                c[r][1] = lds16(at + r * STAGE + 512 + 16 * lane);
-            }
-            float acc[R][NT][4], ones[NT][4];
+                const uint4 c0 = lds16(at + r * STAGE + 16 * lane), c1 = lds16(at + r * STAGE + 512 + 16 * lane);
+                float acc[NT][4], ones[NT][4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t lo = (&c0.x)[j], hi = (&c1.x)[j];
 #pragma unroll
-                for (int m = 0; m < 2; m++) {
-                    const bool begins = (j * PG) % 4 == 0 && m == 0;
+                    for (int m = 0; m < 2; m++) {
+                        const bool begins = (j * PG) % 4 == 0 && m == 0;
+                        if (r == 0) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        if (begins) mma_first<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][0], b[nt][j][1]);
-                        else mma<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < R; r++) {
-                        const uint32_t lo = (&c[r][0].x)[j], hi = (&c[r][1].x)[j];
+                            for (int nt = 0; nt < NT; nt++) {
+                                if (begins) mma_first<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][0], b[nt][j][1]);
+                                else mma<HALF>(ones[nt], ONE, ONE, ONE, ONE, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                            }
+                        }
                         const uint32_t a0 = qm_codes<HALF, EXACT>(lo, 2 * m, magic), a1 = qm_codes<HALF, EXACT>(hi, 2 * m, magic);
                         const uint32_t a2 = qm_codes<HALF, EXACT>(lo, 2 * m + 1, magic), a3 = qm_codes<HALF, EXACT>(hi, 2 * m + 1, magic);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
-                            if (begins) mma_first<HALF>(acc[r][nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
-                            else mma<HALF>(acc[r][nt], a0, a1, a2, a3, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
+                            if (begins) mma_first<HALF>(acc[nt], a0, a1, a2, a3, b[nt][j][0], b[nt][j][1]);
+                            else mma<HALF>(acc[nt], a0, a1, a2, a3, b[nt][j][2 * m], b[nt][j][2 * m + 1]);
                         }
                     }
-                }
-                if (((j + 1) * PG) % 4 != 0) continue;
-                // the group's end: its sums meet their parameters
-                const int s = j * PG / 4;
-                float sc[NT][2];
-                if constexpr (XT == LL_E4M3) {
+                    if (((j + 1) * PG) % 4 != 0) continue;
+                    // the group's end: its sums meet their parameters
+                    const int s = j * PG / 4;
+                    if (r == 0) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int token = min(first + nt * 8 + 2 * t + e, a.n - 1);
-                            sc[nt][e] = __ldg(a.scale + int64_t(token) * a.scale_row + kt * a.scale_step);
+                        for (int nt = 0; nt < NT; nt++) {
+                            sums[s][nt][0] = ones[nt][0];
+                            sums[s][nt][1] = ones[nt][1];
                         }
-                }
-#pragma unroll
-                for (int r = 0; r < R; r++) {
+                    }
                     const uint32_t p = at + r * STAGE + 1024 + (s * QM_TILE_ROWS + g) * 4;
                     const float2 p0 = lds_pair(p), p1 = lds_pair(p + 32);
                     constexpr float ZERO = EXACT ? 8.f : -16.f;
@@ -293,9 +298,9 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
                         for (int i = 0; i < 4; i++) {
                             const float step = i < 2 ? p0.y : p1.y, z = i < 2 ? z0 : z1;
                             if constexpr (XT == LL_E4M3)
-                                tot[r][nt][i] = fmaf(fmaf(step, acc[r][nt][i], z * ones[nt][i & 1]), sc[nt][i & 1], tot[r][nt][i]);
+                                tot[r][nt][i] = fmaf(fmaf(step, acc[nt][i], z * sums[s][nt][i & 1]), sc[nt][i & 1], tot[r][nt][i]);
                             else
-                                tot[r][nt][i] = fmaf(step, acc[r][nt][i], fmaf(z, ones[nt][i & 1], tot[r][nt][i]));
+                                tot[r][nt][i] = fmaf(step, acc[nt][i], fmaf(z, sums[s][nt][i & 1], tot[r][nt][i]));
                         }
                 }
             }
@@ -308,8 +313,9 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) part[parity][warp][r * QM_TILE_ROWS + g + 8 * (i / 2)][nt * 8 + 2 * t + (i & 1)] = tot[r][nt][i];
-        // (the shares of the group before last lie in the other half: one barrier a group)
+                for (int i = 0; i < 4; i++)
+                    part[(parity * MV_WARPS + warp) * Geo::PART + (r * QM_TILE_ROWS + g + 8 * (i / 2)) * (8 * NT + 1) + nt * 8 + 2 * t + (i & 1)] = tot[r][nt][i];
+        // (with room for two, the shares of the group before last lie in the other half: one barrier a group)
         if (splits == 1) __syncwarp();
         else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * splits) : "memory");
         for (int e = ks * 32 + lane; e < ROWS * min(TOKENS, a.n - first); e += 32 * splits) {
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
             float y = 0.f;
             for (int s = 0; s < splits; s++)
 #pragma unroll
-                for (int u = TERMS - 1; u >= 0; u--) y += part[parity][team * splits + s][in][token * TERMS + u];
+                for (int u = TERMS - 1; u >= 0; u--) y += part[(parity * MV_WARPS + team * splits + s) * Geo::PART + in * (8 * NT + 1) + token * TERMS + u];
             const int64_t to = int64_t(first + token) * a.y_stride + row, from = int64_t(first + token) * a.add_stride + row;
             if (a.y_f32) {
                 if (a.add) y += static_cast<const float *>(a.add)[from];
@@ -329,47 +335,67 @@ __global__ void __launch_bounds__(MV_THREADS, MvGeo<NT>::BLOCKS) k_qmat_mv(const
                 static_cast<__nv_bfloat16 *>(a.y)[to] = __float2bfloat16_rn(y);
             }
         }
-        parity ^= 1;
+        if (Geo::PARTS == 2) parity ^= 1;
+        else if (splits == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * splits) : "memory");
     }
 }
 
-template <int XT, int NT, int R, int PG, bool EXACT>
-int launch_mv(const MvArgs &a, int nsm, cudaStream_t st) {
-    constexpr int TOKENS = 8 * NT / Column<XT>::TERMS, SMEM = MV_WARPS * MvGeo<NT>::UNITS * (1024 + 64 * PG);
-    const auto kernel = k_qmat_mv<XT, NT, R, PG, EXACT>;
-    if (!allow_smem(reinterpret_cast<const void *>(kernel), SMEM)) return LL_ERR_CUDA;
-    MvArgs b = a;
-    // splits by the steps of the busiest warp: its tiles, and 2 a group for the shares' barrier
-    const int tiles = (a.RT + R - 1) / R, blocks = MvGeo<NT>::BLOCKS * nsm;
-    int64_t best = INT64_MAX;
+// How the warps share the matrix, by the steps of the busiest warp: its tiles, and 2 a group for the shares' barrier.
+struct MvPlan {
+    int log_splits;
+    int64_t steps;
+    dim3 grid;
+};
+template <int NT, int R>
+MvPlan plan_mv(const MvArgs &a, int tokens, int nsm) {
+    const int tiles = (a.RT + R - 1) / R, blocks = MvGeo<NT, R, 1>::BLOCKS * nsm, passes = (a.n + tokens - 1) / tokens;
+    // (fewer groups than slots: one a block before two in one)
+    MvPlan p = {0, INT64_MAX, dim3(tiles < blocks ? tiles : blocks, passes)};
+    const int64_t waves = (int64_t(p.grid.x) * passes + blocks - 1) / blocks;
     for (int log = 0; 1 << log <= MV_WARPS && 1 << log <= a.KT; log++) {
         const int splits = 1 << log;
         const int64_t slots = int64_t(blocks) * (MV_WARPS / splits), rounds = (tiles + slots - 1) / slots;
-        const int64_t steps = rounds * ((a.KT + splits - 1) / splits * R + (splits > 1 ? 2 : 1));
-        if (steps < best) {
-            best = steps;
-            b.log_splits = log;
+        const int64_t steps = waves * rounds * ((a.KT + splits - 1) / splits * R + (splits > 1 ? 2 : 1));
+        if (steps < p.steps) {
+            p.steps = steps;
+            p.log_splits = log;
         }
     }
-    // (fewer groups than slots: one a block before two in one)
-    const dim3 grid(tiles < blocks ? tiles : blocks, (a.n + TOKENS - 1) / TOKENS);
-    kernel<<<grid, MV_THREADS, SMEM, st>>>(b);
+    return p;
+}
+
+template <int XT, int NT, int R, int PG, bool EXACT>
+int launch_mv(const MvArgs &a, const MvPlan &p, cudaStream_t st) {
+    constexpr int SMEM = MvGeo<NT, R, PG>::SMEM;
+    const auto kernel = k_qmat_mv<XT, NT, R, PG, EXACT>;
+    if (!allow_smem(reinterpret_cast<const void *>(kernel), SMEM)) return LL_ERR_CUDA;
+    MvArgs b = a;
+    b.log_splits = p.log_splits;
+    kernel<<<p.grid, MV_THREADS, SMEM, st>>>(b);
     return launched();
 }
 
-template <int XT, int NT, int R, bool EXACT>
-int launch_mv_pg(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
-    return pg == 1 ? launch_mv<XT, NT, R, 1, EXACT>(a, nsm, st) : pg == 2 ? launch_mv<XT, NT, R, 2, EXACT>(a, nsm, st) : launch_mv<XT, NT, R, 4, EXACT>(a, nsm, st);
+template <int XT, int NT, int R>
+int launch_mv_rows(const MvArgs &a, int pg, const MvPlan &p, cudaStream_t st) {
+    if (a.y_f32) return pg == 1 ? launch_mv<XT, NT, R, 1, true>(a, p, st) : pg == 2 ? launch_mv<XT, NT, R, 2, true>(a, p, st) : launch_mv<XT, NT, R, 4, true>(a, p, st);
+    return pg == 1 ? launch_mv<XT, NT, R, 1, false>(a, p, st) : pg == 2 ? launch_mv<XT, NT, R, 2, false>(a, p, st) : launch_mv<XT, NT, R, 4, false>(a, p, st);
 }
 
+// Row tiles of a warp (R), which share x's fragments and the products with ones: as many as leave every block some. us with
+// 1 / 2 / 4, one bf16 row x: 512 x 2048 2.5 / - / 3.7, 6144 x 4096 5.8 / 6.5 / 6.3, 19456 x 4096 - / 14.2 / 11.3, 28672 x 4096 19.6 / 17.6 /
+// 17.7 (of 8 rows in groups of 32 - / 27.0 / 23.1), 128256 x 2048 40.6 / 35.8 / 33.1. For more columns by the steps, of which those of 4 take nine tenths:
+// 2 / 4, 4096 x 14336 with 64 e4m3 rows 53.0 / 46.7, with 32 25.1 / 32.8; 28672 x 4096 with 16 26.3 / 28.4; 128256 x 2048 with 16 66.3 / 59.1.
 template <int XT>
 int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
-    const int columns = a.n * Column<XT>::TERMS;
-    // two row tiles a warp share x's fragments; one where that leaves SMs without any
-    const bool two = a.RT >= 4 * nsm;
-    if (columns > 8) return a.y_f32 ? launch_mv_pg<XT, 2, 2, true>(a, pg, nsm, st) : launch_mv_pg<XT, 2, 2, false>(a, pg, nsm, st);
-    if (a.y_f32) return two ? launch_mv_pg<XT, 1, 2, true>(a, pg, nsm, st) : launch_mv_pg<XT, 1, 1, true>(a, pg, nsm, st);
-    return two ? launch_mv_pg<XT, 1, 2, false>(a, pg, nsm, st) : launch_mv_pg<XT, 1, 1, false>(a, pg, nsm, st);
+    constexpr int TERMS = Column<XT>::TERMS;
+    if (a.n * TERMS > 8) {
+        const MvPlan two = plan_mv<2, 2>(a, 16 / TERMS, nsm), four = plan_mv<2, 4>(a, 16 / TERMS, nsm);
+        return four.steps * 9 < two.steps * 10 ? launch_mv_rows<XT, 2, 4>(a, pg, four, st) : launch_mv_rows<XT, 2, 2>(a, pg, two, st);
+    }
+    if (a.RT >= 8 * nsm) return launch_mv_rows<XT, 1, 4>(a, pg, plan_mv<1, 4>(a, 8 / TERMS, nsm), st);
+    if (a.RT >= 4 * nsm) return launch_mv_rows<XT, 1, 2>(a, pg, plan_mv<1, 2>(a, 8 / TERMS, nsm), st);
+    return launch_mv_rows<XT, 1, 1>(a, pg, plan_mv<1, 1>(a, 8 / TERMS, nsm), st);
 }
 
 }  // namespace
