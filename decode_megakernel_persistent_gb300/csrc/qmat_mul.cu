@@ -376,22 +376,29 @@ int launch_mv(const MvArgs &a, const MvPlan &p, cudaStream_t st) {
     return launched();
 }
 
+template <int XT, int NT, int R, int PG>
+int launch_mv_exact(const MvArgs &a, const MvPlan &p, cudaStream_t st) {
+    return a.y_f32 ? launch_mv<XT, NT, R, PG, true>(a, p, st) : launch_mv<XT, NT, R, PG, false>(a, p, st);
+}
 template <int XT, int NT, int R>
 int launch_mv_rows(const MvArgs &a, int pg, const MvPlan &p, cudaStream_t st) {
-    if (a.y_f32) return pg == 1 ? launch_mv<XT, NT, R, 1, true>(a, p, st) : pg == 2 ? launch_mv<XT, NT, R, 2, true>(a, p, st) : launch_mv<XT, NT, R, 4, true>(a, p, st);
-    return pg == 1 ? launch_mv<XT, NT, R, 1, false>(a, p, st) : pg == 2 ? launch_mv<XT, NT, R, 2, false>(a, p, st) : launch_mv<XT, NT, R, 4, false>(a, p, st);
+    if (pg == 1) return launch_mv_exact<XT, NT, R, 1>(a, p, st);
+    if (pg == 2) return launch_mv_exact<XT, NT, R, 2>(a, p, st);
+    if constexpr (NT * R < 8) return launch_mv_exact<XT, NT, R, 4>(a, p, st);
+    return LL_ERR_SHAPE;  // (not asked for)
 }
 
 // Row tiles of a warp (R), which share x's fragments and the products with ones: as many as leave every block some. us with
 // 1 / 2 / 4, one bf16 row x: 512 x 2048 2.5 / - / 3.7, 6144 x 4096 5.8 / 6.5 / 6.3, 19456 x 4096 - / 14.2 / 11.3, 28672 x 4096 19.6 / 17.6 /
 // 17.7 (of 8 rows in groups of 32 - / 27.0 / 23.1), 128256 x 2048 40.6 / 35.8 / 33.1. For more columns by the steps, of which those of 4 take nine tenths:
-// 2 / 4, 4096 x 14336 with 64 e4m3 rows 53.0 / 46.7, with 32 25.1 / 32.8; 28672 x 4096 with 16 26.3 / 28.4; 128256 x 2048 with 16 66.3 / 59.1.
+// 2 / 4, 4096 x 14336 with 64 e4m3 rows 53.0 / 46.7, with 32 25.1 / 32.8; 28672 x 4096 with 16 26.3 / 28.4; 128256 x 2048 with 16 66.3 / 59.1. Not in
+// groups of 32, whose sums then do not fit the registers (128256 x 2048 with 16 76.1 / 87.5).
 template <int XT>
 int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
     constexpr int TERMS = Column<XT>::TERMS;
     if (a.n * TERMS > 8) {
         const MvPlan two = plan_mv<2, 2>(a, 16 / TERMS, nsm), four = plan_mv<2, 4>(a, 16 / TERMS, nsm);
-        return four.steps * 9 < two.steps * 10 ? launch_mv_rows<XT, 2, 4>(a, pg, four, st) : launch_mv_rows<XT, 2, 2>(a, pg, two, st);
+        return pg < 4 && four.steps * 9 < two.steps * 10 ? launch_mv_rows<XT, 2, 4>(a, pg, four, st) : launch_mv_rows<XT, 2, 2>(a, pg, two, st);
     }
     if (a.RT >= 8 * nsm) return launch_mv_rows<XT, 1, 4>(a, pg, plan_mv<1, 4>(a, 8 / TERMS, nsm), st);
     if (a.RT >= 4 * nsm) return launch_mv_rows<XT, 1, 2>(a, pg, plan_mv<1, 2>(a, 8 / TERMS, nsm), st);
@@ -402,11 +409,12 @@ int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
 
 int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st) {
     // bf16 outputs of more columns than a pass of k_qmat_mv takes, where its products for many row tiles take longer than
-    // unpacking x in every block of the other kernel. us there / here, groups of 128, at 32 and at 64 rows of bf16 x:
-    // 128256 x 2048 61 / 109, 134 / 209; 28672 x 4096 39 / 49, 79 / 92; 17408 x 2048 20 / 18, 28 / 32; 18432 x 8192
-    // 58 / 54, 113 / 102; 4096 x 14336 (not there) 33 / 24, 61 / 46. At 16 rows of fp32: 58 / 419, 34 / 150, 17 / 49, 40 / 272.
+    // unpacking x in every block of the other kernel (and, but for fp32, than joining what its blocks have of long rows). us there /
+    // here, groups of 128, at 32 and at 64 rows of bf16 x: 128256 x 2048 60 / 106, 131 / 201; 28672 x 4096 39 / 48, 76 / 90; 32768 x
+    // 2048 28 / 31, 45 / 56; 17408 x 2048 20 / 19, 27 / 34; not there: 18432 x 8192 57 / 52, 111 / 97; 4096 x 14336 33 / 25, 61 / 46. At 16
+    // rows of fp32: 57 / 325, 34 / 145, 25 / 88, 17 / 39; 18432 x 8192 40 / 153.
     const int columns = n * (x.type == LL_F32 ? Column<LL_F32>::TERMS : 1);
-    if (y.type == LL_BF16 && columns > 16 && (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS >= 7 * nsm) {
+    if (y.type == LL_BF16 && columns > 16 && (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS >= 7 * nsm && (x.type == LL_F32 || m.cols <= 6144)) {
         const int rc = launch_qmat_tc(m, x, n, add, y, nsm, st);
         if (rc != LL_ERR_SHAPE) return rc;
     }
