@@ -146,7 +146,7 @@ struct Column {
 
 template <int NT, int R, int PG>
 struct MvGeo {
-    static constexpr int UNITS = R == 4 ? 8 : 6, BLOCKS = NT == 1 && R < 4 ? 3 : 2;  // tiles of a warp in flight, blocks of an SM
+    static constexpr int UNITS = R == 4 ? 8 : R == 3 ? 9 : 6, BLOCKS = NT == 1 && R < 3 ? 3 : 2;  // tiles of a warp in flight, blocks of an SM
     static constexpr int PARTS = NT * R < 8 ? 2 : 1, PART = R * QM_TILE_ROWS * (8 * NT + 1);  // shares of two groups or one; floats of a warp's
     static constexpr int RING = MV_WARPS * UNITS * (1024 + 64 * PG), SMEM = RING + PARTS * MV_WARPS * PART * 4;
 };
@@ -388,11 +388,12 @@ int launch_mv_rows(const MvArgs &a, int pg, const MvPlan &p, cudaStream_t st) {
     return LL_ERR_SHAPE;  // (not asked for)
 }
 
-// Row tiles of a warp (R), which share x's fragments and the products with ones: as many as leave every block some. us with
-// 1 / 2 / 4, one bf16 row x: 512 x 2048 2.5 / - / 3.7, 6144 x 4096 5.8 / 6.5 / 6.3, 19456 x 4096 - / 14.2 / 11.3, 28672 x 4096 19.6 / 17.6 /
-// 17.7 (of 8 rows in groups of 32 - / 27.0 / 23.1), 128256 x 2048 40.6 / 35.8 / 33.1. For more columns by the steps, of which those of 4 take nine tenths:
-// 2 / 4, 4096 x 14336 with 64 e4m3 rows 53.0 / 46.7, with 32 25.1 / 32.8; 28672 x 4096 with 16 26.3 / 28.4; 128256 x 2048 with 16 66.3 / 59.1. Not in
-// groups of 32, whose sums then do not fit the registers (128256 x 2048 with 16 76.1 / 87.5).
+// Row tiles of a warp (R), which share x's fragments and the products with ones: by the steps of the busiest warp, and what a
+// step takes with the warps that an SM then holds. us with 1 / 3 / 4, one bf16 row x in groups of 128: 512 x 2048 2.5 / - / 3.7, 6144 x 4096
+// 5.8 / 6.6 / 6.3, 11008 x 4096 - / 7.8 / 9.5, 19456 x 4096 - / 12.5 / 11.3, 28672 x 4096 19.6 / 15.6 / 17.7, 128256 x 4096 in groups of 64 into
+// fp32 - / 66.3 / 62.5 (28672 and 128256 with 2: 17.1, 69.3). More columns, with 2 / 4: 4096 x 14336 with 64 e4m3 rows 53.0 / 46.7, with 32
+// 25.1 / 32.8; 28672 x 4096 with 16 26.3 / 28.4; 128256 x 2048 with 16 66.3 / 59.1; 4 not in groups of 32, whose sums then do not fit the registers
+// (128256 x 2048 with 16 76.1 / 87.5).
 template <int XT>
 int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
     constexpr int TERMS = Column<XT>::TERMS;
@@ -400,9 +401,10 @@ int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
         const MvPlan two = plan_mv<2, 2>(a, 16 / TERMS, nsm), four = plan_mv<2, 4>(a, 16 / TERMS, nsm);
         return pg < 4 && four.steps * 9 < two.steps * 10 ? launch_mv_rows<XT, 2, 4>(a, pg, four, st) : launch_mv_rows<XT, 2, 2>(a, pg, two, st);
     }
-    if (a.RT >= 8 * nsm) return launch_mv_rows<XT, 1, 4>(a, pg, plan_mv<1, 4>(a, 8 / TERMS, nsm), st);
-    if (a.RT >= 4 * nsm) return launch_mv_rows<XT, 1, 2>(a, pg, plan_mv<1, 2>(a, 8 / TERMS, nsm), st);
-    return launch_mv_rows<XT, 1, 1>(a, pg, plan_mv<1, 1>(a, 8 / TERMS, nsm), st);
+    const MvPlan one = plan_mv<1, 1>(a, 8 / TERMS, nsm), three = plan_mv<1, 3>(a, 8 / TERMS, nsm), four = plan_mv<1, 4>(a, 8 / TERMS, nsm);
+    const int64_t cost1 = one.steps * 33, cost3 = three.steps * 18, cost4 = four.steps * 17;
+    if (cost4 <= cost3 && cost4 <= cost1) return launch_mv_rows<XT, 1, 4>(a, pg, four, st);
+    return cost3 <= cost1 ? launch_mv_rows<XT, 1, 3>(a, pg, three, st) : launch_mv_rows<XT, 1, 1>(a, pg, one, st);
 }
 
 }  // namespace
