@@ -54,7 +54,9 @@ __device__ __forceinline__ Range range8(const Raw8<__nv_bfloat16> &r) {  // (two
 // Quantise. A lane is row g or g + 8 of a tile and the columns 32 j + 8 t .. + 7 (lane 4 g + t), as the
 // products read a tile: four words, 16 bytes a lane, a half warp's rows in one 512-byte store. A group's range
 // goes over the lane's words of the group and the four lanes of a row. WHOLE: a tile inside the matrix whose rows are on
-// 16-byte borders.
+// 16-byte borders. Bounded by its instructions, 16 a value, and by waiting for its rows: 64 registers, which spill up to 96 bytes a
+// thread, let an SM hold four blocks where 90 let it hold two, and writing and reading 14336 x 4096 (bf16, groups of 128) went
+// from 74 us to 60 (37 of them written in); with three blocks 66.
 template <typename T, int GROUP, bool WHOLE>
 __device__ __forceinline__ void write_half_tile(const ll_qmat &m, const T *w, int64_t stride, int64_t half, int64_t tile, int64_t R, int64_t K, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -144,7 +146,7 @@ __global__ void __launch_bounds__(RW_THREADS, 4) k_qmat_write(ll_qmat m, const T
     else write_half_tile<T, GROUP, false>(m, w, stride, half, tile, R, K, lane);
 }
 
-// Read back, with k_qmat_write's lanes.
+// Read back, with k_qmat_write's lanes: bounded by the memory it writes.
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(RW_THREADS) k_qmat_read(ll_qmat m, T *w, int64_t stride, bool vec) {
     const int KT = (m.cols + QM_TILE_COLS - 1) / QM_TILE_COLS;

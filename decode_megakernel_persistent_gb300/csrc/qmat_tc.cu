@@ -10,8 +10,12 @@
 // A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Sixteen warps, in four sets that
 // take units in turn, unpack 32 rows each from a ring of their own (cp.async) into tensor memory, the products' A operand,
 // a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products; four warps, a row
-// to a thread, take a row block's sums from tensor memory
-// and scale them. Blocks of a cluster share the columns: each row's shares then meet through shared memory.
+// to a thread, take a row block's sums from tensor memory and scale them. Blocks of a cluster share the columns: each
+// row's shares then meet through shared memory.
+//
+// 128256 x 2048, 32 rows, 60 us (2.3 TB/s): a unit takes some 820 cycles where its bytes would take 360. Without the products it
+// took 44 us, without the unpacking's arithmetic 48, without storing the outputs 55, with one more unit in flight no less: what the warps
+// wait for is each other, and no one part bounds it. x's staging is 3 to 7 us of a call.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

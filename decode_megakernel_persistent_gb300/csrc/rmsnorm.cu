@@ -3,7 +3,8 @@
 //   r = round(x + residual),   out = r / sqrt(mean(r^2) + eps) * gain,   e4m3: out / scale, scale = max|out| / 448
 //
 // One pass: a row's values stay in the registers of the threads that loaded them (units of 8, one 16-byte
-// load of bf16) while its sum of squares goes round.
+// load of bf16) while its sum of squares goes round. What has to move is each row once in and once out, which bounds many
+// rows (8192 of 4096 at 81 % of a copy's rate); one row of 2048 is its launch and a round trip to memory (1.7 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
