@@ -84,6 +84,17 @@ int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t wid
     return LL_OK;
 }
 
+int check_in_place(const ll_rows *in, const char *in_name, const ll_rows *out, const char *out_name, int64_t n, char *err, size_t err_len) {
+    if (in->data != out->data || (in->type == out->type && (n <= 1 || in->stride == out->stride))) return LL_OK;
+    return report(err, err_len, LL_ERR_ARG, "%s begins where %s does, with another type or stride", out_name, in_name);
+}
+
+int check_in_place(const ll_kvq_rows *in, const ll_kvq_rows *out, const char *name, int64_t n_seq, int64_t n_tok, int64_t heads, char *err, size_t err_len) {
+    if (in->data != out->data) return LL_OK;
+    if ((n_seq <= 1 || in->seq == out->seq) && (n_tok <= 1 || in->token == out->token) && (heads <= 1 || in->head == out->head)) return LL_OK;
+    return report(err, err_len, LL_ERR_ARG, "%s_out begins where %s does, with other strides", name, name);
+}
+
 bool allow_smem(const void *kernel, int bytes) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;

@@ -26,6 +26,10 @@ int check_rows(const ll_kvq_rows *r, const char *name, int64_t n_seq, int64_t n_
 int check_matrix_rows(const ll_rows *r, const char *name, int64_t n, int64_t width, bool e4m3, bool written, char *err,
                       size_t err_len);
 
+// Outputs that begin where an input does must be its very rows (of one type, strides alike).
+int check_in_place(const ll_rows *in, const char *in_name, const ll_rows *out, const char *out_name, int64_t n, char *err, size_t err_len);
+int check_in_place(const ll_kvq_rows *in, const ll_kvq_rows *out, const char *name, int64_t n_seq, int64_t n_tok, int64_t heads, char *err, size_t err_len);
+
 // rc, with CUDA's reason where a launch failed.
 int finish(int rc, char *err, size_t err_len);
 

@@ -79,7 +79,7 @@ __device__ __forceinline__ void write_half_tile(const ll_qmat &m, const T *w, in
     } else {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            load8(row, k0 + 32 * j, cols, false, x[j]);
+            load8(row, k0 + 32 * j, cols, x[j]);
             range[j] = {INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -283,7 +283,9 @@ int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *ad
     if (add) {
         if (int rc = ll::check_matrix_rows(add, "add", n, m->rows, false, false, err, err_len)) return rc;
         if (add->type != y->type) return report(err, err_len, LL_ERR_ARG, "add must be of y's type");
+        if (int rc = ll::check_in_place(add, "add", y, "y", n, err, err_len)) return rc;
     }
+    if (y->data == x->data) return report(err, err_len, LL_ERR_ARG, "y is x");
     int nsm = 0;
     if (int rc = check_device(nsm, err, err_len)) return rc;
     return finish(ll::launch_qmat_mul(*m, *x, n, add, *y, nsm, static_cast<cudaStream_t>(stream)), err, err_len);

@@ -86,10 +86,10 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) k_rmsnorm_rows(const 
     } else {
 #pragma unroll
         for (int u = 0; u < UNITS; u++) {
-            load8(x, 8 * (in + u * TEAM), width, false, v[u]);
+            load8(x, 8 * (in + u * TEAM), width, v[u]);
             if constexpr (RES) {
                 float w[8];
-                load8(static_cast<const TR *>(a.res) + at * a.res_stride, 8 * (in + u * TEAM), width, false, w);
+                load8(static_cast<const TR *>(a.res) + at * a.res_stride, 8 * (in + u * TEAM), width, w);
 #pragma unroll
                 for (int i = 0; i < 8; i++) v[u][i] += w[i];
             }
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) k_rmsnorm_rows(const 
     for (int u = 0; u < UNITS; u++) {
         float gain[8];
         if constexpr (VEC) rg[u].widen(gain);
-        else load8(a.gain, 8 * (in + u * TEAM), a.width, false, gain);
+        else load8(a.gain, 8 * (in + u * TEAM), a.width, gain);
 #pragma unroll
         for (int i = 0; i < 8; i++) v[u][i] = v[u][i] * r * gain[i];
     }
@@ -229,10 +229,14 @@ extern "C" int ll_rmsnorm(const ll_rows *x, const ll_rows *residual, const ll_ro
     if (int rc = ll::check_matrix_rows(x, "x", n, width, false, false, err, err_len)) return rc;
     if (int rc = ll::check_matrix_rows(out, "out", n, width, true, true, err, err_len)) return rc;
     if (!residual != !residual_out) return report(err, err_len, LL_ERR_ARG, "residual and residual_out go together");
+    if (int rc = ll::check_in_place(x, "x", out, "out", n, err, err_len)) return rc;
     if (residual) {
         if (int rc = ll::check_matrix_rows(residual, "residual", n, width, false, false, err, err_len)) return rc;
         if (int rc = ll::check_matrix_rows(residual_out, "residual_out", n, width, false, true, err, err_len)) return rc;
         if (residual->type != residual_out->type) return report(err, err_len, LL_ERR_ARG, "residual_out must be of residual's type");
+        if (int rc = ll::check_in_place(residual, "residual", residual_out, "residual_out", n, err, err_len)) return rc;
+        if (int rc = ll::check_in_place(x, "x", residual_out, "residual_out", n, err, err_len)) return rc;
+        if (int rc = ll::check_in_place(residual, "residual", out, "out", n, err, err_len)) return rc;
         if (residual_out->data == out->data) return report(err, err_len, LL_ERR_ARG, "out and residual_out are the same rows");
     }
     int nsm = 0;

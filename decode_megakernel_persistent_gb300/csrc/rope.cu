@@ -227,9 +227,11 @@ int ll_rope(const ll_rope_table *r, const ll_kvq_rows *q, const ll_kvq_rows *q_o
     const int size = type == LL_F32 ? 4 : 2;
     if (int rc = check_rows(q, "q", n_seq, n_tok, n_q_heads, size, false, err, err_len)) return rc;
     if (int rc = check_rows(q_out, "q_out", n_seq, n_tok, n_q_heads, size, true, err, err_len)) return rc;
+    if (int rc = ll::check_in_place(q, q_out, "q", n_seq, n_tok, n_q_heads, err, err_len)) return rc;
     if (k) {
         if (int rc = check_rows(k, "k", n_seq, n_tok, n_k_heads, size, false, err, err_len)) return rc;
         if (int rc = check_rows(k_out, "k_out", n_seq, n_tok, n_k_heads, size, true, err, err_len)) return rc;
+        if (int rc = ll::check_in_place(k, k_out, "k", n_seq, n_tok, n_k_heads, err, err_len)) return rc;
         if (k_out->data == q_out->data) return report(err, err_len, LL_ERR_ARG, "q_out and k_out are the same rows");
     }
     int nsm = 0;

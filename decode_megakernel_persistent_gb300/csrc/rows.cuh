@@ -34,28 +34,17 @@ struct Raw8 {
     }
 };
 
-// Columns k..k+7 of a row of `width` values, zeros past its end. vec: 16-byte (8-byte for e4m3) accesses are aligned.
-__device__ __forceinline__ void load8(const float *row, int k, int width, bool vec, float (&x)[8]) {
-    if (vec && k + 8 <= width) {
-        const float4 a = *reinterpret_cast<const float4 *>(row + k), b = *reinterpret_cast<const float4 *>(row + k + 4);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
+// Columns k..k+7 of a row of `width` values, zeros past its end, of any alignment.
+__device__ __forceinline__ void load8(const float *row, int k, int width, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = k + i < width ? row[k + i] : 0.f;
-    }
+    for (int i = 0; i < 8; i++) x[i] = k + i < width ? row[k + i] : 0.f;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int k, int width, bool vec, float (&x)[8]) {
-    if (vec && k + 8 <= width) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(row + k);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int k, int width, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = k + i < width ? __bfloat162float(row[k + i]) : 0.f;
-    }
+    for (int i = 0; i < 8; i++) x[i] = k + i < width ? __bfloat162float(row[k + i]) : 0.f;
 }
 
+// Stored to there. vec: 16-byte (8-byte for e4m3) accesses are aligned.
 __device__ __forceinline__ void store8(float *row, int k, int width, bool vec, const float (&x)[8]) {
     if (vec && k + 8 <= width) {
         reinterpret_cast<float4 *>(row + k)[0] = make_float4(x[0], x[1], x[2], x[3]);

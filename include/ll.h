@@ -411,7 +411,8 @@ int ll_init_kvq(const ll_config *cfg, const ll_weights *w, const ll_kvq_cache *c
  * graphs, and return LL_OK, LL_ERR_ARG / LL_ERR_SHAPE (nothing was launched),
  * LL_ERR_DEVICE or LL_ERR_CUDA with a one-line reason in err. Repeated on the same
  * data, a call gives the same bits. Outputs must not overlap inputs or each other
- * unless a call says so. */
+ * unless a call says so; where they may, they are the same rows (strides alike). What
+ * begins at the same place against this is refused. */
 #define LL_E4M3 2 /* 8-bit floats: 1 sign, 4 exponent, 3 mantissa bits, no infinities */
 
 /* A matrix of rows x cols values in 4 bits. Each row is cut into groups of `group`

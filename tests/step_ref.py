@@ -73,11 +73,6 @@ def quantised(w, group):
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11}
 
 
-def cols_of(x):
-    """The largest of each row's values, [n, 1]."""
-    return x.abs().amax(1, keepdim=True)
-
-
 def product(m, x, add, dtype):
     """x W^T + add in 64 bits and how far a kernel's may be off. x [n, cols] in 64 bits (on the CPU).
     A group of 128 columns is at most 8 matrix instructions with fp32 sums of exact products: each adds

@@ -82,7 +82,8 @@ def test_products_that_are_refused(lib):
     for kw, code in ((dict(n=0), A), (dict(n=-1), A), (dict(n=(1 << 18) + 1), S), (dict(x=rows(data=None)), A), (dict(x=rows(data=65537)), A),
                      (dict(x=rows(data=65538, type=1)), A), (dict(x=rows(type=3)), A), (dict(x=rows(type=2)), A), (dict(x=rows(type=2, scale=4098)), A),
                      (dict(x=rows(type=2, scale=4096, group=64)), A), (dict(y=rows(type=2, scale=4096)), A), (dict(y=rows(stride=63)), A),
-                     (dict(y=rows(stride=0)), A), (dict(y=rows(data=None)), A), (dict(add=rows(type=1)), A), (dict(add=rows(data=None)), A)):
+                     (dict(y=rows(stride=0)), A), (dict(y=rows(data=None)), A), (dict(add=rows(type=1)), A), (dict(add=rows(data=None)), A), (dict(y=rows()), A),
+                     (dict(add=rows(data=131072, stride=256)), A)):
         rc, msg = mul(**kw)
         assert rc == code and msg, kw
     assert lib.ll_qmat_mul(mat(), rows(), 0, None, rows(), None, None, 0) == A  # (no place for a reason)
@@ -96,7 +97,9 @@ def test_norms_that_are_refused(lib):
     for kw, code in ((dict(n=0), A), (dict(n=(1 << 30) + 1), S), (dict(width=0), S), (dict(width=32769), S), (dict(eps=-1.0), A), (dict(eps=NAN), A), (dict(eps=INF), A), (dict(gain=None), A),
                      (dict(gain=4097), A), (dict(x=rows(type=2, scale=4096)), A), (dict(out=rows(type=2)), A), (dict(out=rows(type=2, scale=4096, group=32)), A),
                      (dict(out=rows(stride=255)), A), (dict(res=r), A), (dict(res_out=r), A), (dict(res=r, res_out=rows(data=1 << 18, type=1)), A),
-                     (dict(res=r, res_out=rows(data=131072)), A), (dict(res=r, res_out=rows(data=1 << 18, stride=3)), A), (dict(x=rows(data=None)), A)):
+                     (dict(res=r, res_out=rows(data=131072)), A), (dict(res=r, res_out=rows(data=1 << 18, stride=3)), A), (dict(x=rows(data=None)), A), (dict(out=rows(stride=300)), A), (dict(out=rows(type=2, scale=4096)), A),
+                     (dict(x=rows(type=1), out=rows()), A), (dict(res=r, res_out=rows(data=1 << 18, stride=300)), A), (dict(res=rows(type=1), res_out=rows(type=1)), A),
+                     (dict(res=r, res_out=rows(data=1 << 20), out=rows(data=1 << 18, stride=300)), A)):
         rc, msg = norm(**kw)
         assert rc == code and msg, kw
 
@@ -146,7 +149,7 @@ def test_rotary_calls_that_are_refused(lib):
     for kw, code in ((dict(t=None), A), (dict(t=ctypes.byref(bad)), A), (dict(q=kvq_rows(data=None)), A), (dict(q=kvq_rows(data=65544)), A),
                      (dict(qo=kvq_rows(token=4)), A), (dict(qo=kvq_rows(token=0)), A), (dict(nq=0), S), (dict(nq=40000), S), (dict(k=k), A), (dict(ko=k), A),
                      (dict(k=k, ko=k, nk=0), S), (dict(k=k, ko=kvq_rows()), A), (dict(kind=2), A), (dict(S=0), S), (dict(S=65536), S), (dict(n=0), A), (dict(n=(1 << 30) + 1), S),
-                     (dict(lens=None), A), (dict(lens=66), A), (dict(n_toks=65), A)):
+                     (dict(lens=None), A), (dict(qo=kvq_rows(token=1024)), A), (dict(k=k, ko=kvq_rows(data=1 << 18, head=128)), A), (dict(lens=66), A), (dict(n_toks=65), A)):
         rc, msg = rope(**kw)
         assert rc == code and msg, kw
 
@@ -154,11 +157,11 @@ def test_rotary_calls_that_are_refused(lib):
 def test_verifications_that_are_refused(lib):
     A, S = ll.LL_ERR_ARG, ll.LL_ERR_SHAPE
 
-    def verify(logits=65536, kind=1, draft=64, nd=None, probs=None, u=64, temp=None, S=2, D=3, V=100, tokens=64, accepted=64):
+    def verify(logits=65536, kind=1, draft=64, nd=None, probs=None, u=64, temp=None, S=2, D=3, V=100, tokens=192, accepted=64):
         return answer(lib.ll_verify, logits, kind, 400, 100, draft, nd, probs, 300, 100, u, temp, S, D, V, tokens, accepted)
     for kw, code in ((dict(logits=None), A), (dict(logits=65538), A), (dict(logits=65537, kind=0), A), (dict(kind=2), A), (dict(draft=None), A), (dict(draft=65), A),
                      (dict(nd=66), A), (dict(probs=66), A), (dict(u=None), A), (dict(u=66), A), (dict(temp=66), A), (dict(S=0), S), (dict(S=65536), S), (dict(D=-1), S),
-                     (dict(D=(1 << 20) + 1), S), (dict(V=0), S), (dict(V=393217), S), (dict(tokens=None), A), (dict(accepted=None), A), (dict(accepted=65), A)):
+                     (dict(D=(1 << 20) + 1), S), (dict(V=0), S), (dict(V=393217), S), (dict(tokens=None), A), (dict(accepted=None), A), (dict(accepted=65), A), (dict(draft=128, tokens=128), A)):
         rc, msg = verify(**kw)
         assert rc == code and msg, kw
 
