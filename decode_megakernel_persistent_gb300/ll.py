@@ -440,28 +440,31 @@ def ll_kvq_attention(cache: "KVQCache", q, lens, n_toks=None, out=None, scale=No
     return out
 
 
+_codes = {}  # torch's dtypes by the library's
+
+
 class _Types:
-    """torch's dtypes by the library's, and what every call looks up, found once."""
-    codes = None
+    """torch's dtypes, and what every call looks up, found once."""
 
     @classmethod
     def get(cls) -> dict:
-        if cls.codes is None:
+        if not _codes:
             import torch
             cls.bf16, cls.f32, cls.e4m3, cls.int32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
-            cls.torch, cls.c, cls.lib = torch, torch._C, lib()
-            cls.codes = {torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float8_e4m3fn: LL_E4M3}
-        return cls.codes
+            cls.torch, cls.lib = torch, lib()
+            cls.device, cls.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+            _codes.update({torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float8_e4m3fn: LL_E4M3})
+        return _codes
 
 
 def _device_call(fn, index: int, *args) -> None:
     """One call without a handle on torch's current stream of device `index`."""
-    c = _Types.c
-    if index != c._cuda_getDevice():
-        with _Types.torch.cuda.device(index):
+    types = _Types
+    if index != types.device():
+        with types.torch.cuda.device(index):
             return _device_call(fn, index, *args)
     err = _kvq_thread.err
-    rc = fn(*args, c._cuda_getCurrentRawStream(index), err, 256)
+    rc = fn(*args, types.stream(index), err, 256)
     if rc:
         raise LLError(rc, err.value.decode())
 
@@ -471,16 +474,15 @@ def _matrix_rows(t, name: str, shape, index: int, scale: int = 0, group: int = 0
     strides, which it sees. A small call's GPU work takes two microseconds, so what is right is passed by as few lookups
     as show it; the rest finds the reason.)"""
     try:
-        code = _Types.codes[t.dtype]
         if t.get_device() == index and t.shape == shape:
             stride, last = t.stride()
             if last == 1 or shape[1] <= 1:
-                return _matrix_rows_bytes(t.data_ptr(), stride, code, group, scale)
+                return _matrix_rows_bytes(t.data_ptr(), stride, _codes[t.dtype], group, scale)
     except (AttributeError, KeyError):
         pass
     if not getattr(t, "is_cuda", False) or t.get_device() != index:
         raise LLError(LL_ERR_ARG, f"{name} must be a CUDA tensor" + (f" on cuda:{index}" if index >= 0 else ""))
-    if t.dtype not in _Types.codes:
+    if t.dtype not in _codes:
         raise LLError(LL_ERR_ARG, f"{name} must not be {t.dtype}")
     if t.shape != shape:
         raise LLError(LL_ERR_ARG, f"{name} is {tuple(t.shape)}, the call needs {list(shape)}")
@@ -510,7 +512,7 @@ def _scales(scale, name: str, n: int, width: int, index: int):
 def ll_qmat_write(m: "Q4Matrix", w) -> None:
     """Quantise w [rows, cols] (bf16 or fp32) into the matrix."""
     _matrix_rows(w, "w", (m.rows, m.cols), m.index)
-    _kvq_call(m.lib.ll_qmat_write, m, w.data_ptr(), _Types.codes[w.dtype], w.stride(0))
+    _kvq_call(m.lib.ll_qmat_write, m, w.data_ptr(), _codes[w.dtype], w.stride(0))
 
 
 def ll_qmat_read(m: "Q4Matrix", out=None, dtype=None):
@@ -518,7 +520,7 @@ def ll_qmat_read(m: "Q4Matrix", out=None, dtype=None):
     if out is None:
         out = _Types.torch.empty(m.rows, m.cols, dtype=dtype or _Types.bf16, device=m.device)
     _matrix_rows(out, "out", (m.rows, m.cols), m.index)
-    _kvq_call(m.lib.ll_qmat_read, m, out.data_ptr(), _Types.codes[out.dtype], out.stride(0))
+    _kvq_call(m.lib.ll_qmat_read, m, out.data_ptr(), _codes[out.dtype], out.stride(0))
     return out
 
 
@@ -557,7 +559,7 @@ def ll_rmsnorm(x, gain, eps: float = 1e-5, residual=None, residual_out=None, out
     if not getattr(x, "is_cuda", False) or x.ndim != 2:
         raise LLError(LL_ERR_ARG, "x must be a CUDA tensor [n, width]")
     types = _Types
-    if types.codes is None:
+    if not _codes:
         types.get()
     shape, index = x.shape, x.get_device()
     n, width = shape
@@ -596,12 +598,12 @@ def ll_verify(logits, drafts, u, probs=None, n_drafts=None, temperature=None, to
     if not getattr(logits, "is_cuda", False) or logits.ndim != 3:
         raise LLError(LL_ERR_ARG, "logits must be a CUDA tensor [n_seq, n_draft + 1, vocab]")
     types = _Types
-    if types.codes is None:
+    if not _codes:
         types.get()
     index = logits.get_device()
     S, rows, V = logits.shape
     D = rows - 1
-    code = types.codes.get(logits.dtype)
+    code = _codes.get(logits.dtype)
     f32, int32 = types.f32, types.int32
     ls, lr, last = logits.stride()
     if code not in (LL_BF16, LL_F32) or (last != 1 and V > 1):
