@@ -16,7 +16,6 @@
 // 128256 x 2048, 32 rows, 60 us (2.3 TB/s): a unit takes some 820 cycles where its bytes would take 360. Without the products it
 // took 44 us, without the unpacking's arithmetic 48, without storing the outputs 55, with one more unit in flight no less: what the warps
 // wait for is each other, and no one part bounds it. x's staging is 3 to 7 us of a call.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

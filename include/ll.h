@@ -463,7 +463,8 @@ typedef struct {
  * and large matrices may be computed from W and x in fp16's 11 bits (x scaled by a power of
  * two a row), lo + 15 step then within fp16's range, as ll_qmat_write leaves it. A row of x
  * that holds a NaN or an infinity gives infinities or NaN in its own row of y alone; finite
- * values should be below 2^100 in size. */
+ * values should be below 2^100 in size. Waits inside are for blocks that run at the same
+ * time and end after a second at most; the rows concerned are NaN then. */
 int ll_qmat_mul(const ll_qmat *m, const ll_rows *x, int32_t n, const ll_rows *add, const ll_rows *y, void *stream, char *err,
                 size_t err_len);
 
