@@ -458,7 +458,8 @@ typedef struct {
 /* y = x W^T (+ add): for each of n rows, y[i][r] = sum_k W[r][k] x[i][k] + add[i][r], one
  * rounding to y's type. x [n][cols]: LL_BF16, LL_F32 or LL_E4M3 with scales (a value is its
  * code times its scale). y and add [n][rows]: LL_BF16 or LL_F32, both of one type; add may
- * be NULL, and may be y itself. n: 1 to 2^18. The codes are multiplied as integers, sums held
+ * be NULL, and may be y itself. n: 1 to 2^18, made for up to some 100 (a pass takes 64 rows; reading the
+ * matrix back once and a product of bf16 are faster for a prompt). The codes are multiplied as integers, sums held
  * in fp32, and fp32 x enters with all its bits (as three bf16 terms). Only bf16 y of many rows
  * and large matrices may be computed from W and x in fp16's 11 bits (x scaled by a power of
  * two a row), lo + 15 step then within fp16's range, as ll_qmat_write leaves it. A row of x

@@ -204,7 +204,7 @@ def large_matrix(rows, cols, group, seed):
 
 
 # (from 16 * 7 * 152 rows on bf16 outputs of more than 16 rows of x, 5 of fp32's, take another kernel: row ends inside and at a
-# border of its 128 rows, columns that one block holds, that 2 and 8 share, and that none do)
+# border of its 128 rows, columns that one block holds, that 2 and, of fp32, 8 share)
 @pytest.mark.parametrize("rows,cols,group", [(17024, 40, 32), (17025, 129, 128), (20000, 1000, 64), (19456, 4096, 128), (17100, 9000, 32), (40000, 2048, 128)])
 @pytest.mark.parametrize("n", [6, 17, 32, 33, 64, 70])
 @pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
@@ -244,6 +244,11 @@ def test_large_matrices(rows, cols, group, n, kind):
     assert bool((off.norm(dim=1) <= 2.0 ** -8 * want.norm(dim=1) + 1e-37).all())  # (a row in all: as near as one rounding, most of it bf16's)
     again = m.matvec(x, scale=scale, add=add, out_dtype=torch.bfloat16)
     assert torch.equal(y[:, :rows], again)
+
+
+def test_columns_past_shared_memory():
+    """fp32 rows so long that no cluster holds them: the first kernel again."""
+    test_large_matrices(17024, 60000, 128, 6, torch.float32)
 
 
 @pytest.mark.parametrize("n", [20, 64])
