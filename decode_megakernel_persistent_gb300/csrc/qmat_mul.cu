@@ -415,12 +415,12 @@ int launch_mv_type(const MvArgs &a, int pg, int nsm, cudaStream_t st) {
 
 int launch_qmat_mul(const ll_qmat &m, const ll_rows &x, int n, const ll_rows *add, const ll_rows &y, int nsm, cudaStream_t st) {
     // bf16 outputs of more columns than a pass of k_qmat_mv takes, where its products for many row tiles take longer than
-    // unpacking x in every block of the other kernel (and, but for fp32, than joining what its blocks have of long rows). us there /
-    // here, groups of 128, at 32 and at 64 rows of bf16 x: 128256 x 2048 60 / 106, 131 / 201; 28672 x 4096 39 / 48, 76 / 90; 32768 x
-    // 2048 28 / 31, 45 / 56; 17408 x 2048 20 / 19, 27 / 34; not there: 18432 x 8192 57 / 52, 111 / 97; 4096 x 14336 33 / 25, 61 / 46. At 16
-    // rows of fp32: 57 / 325, 34 / 145, 25 / 88, 17 / 39; 18432 x 8192 40 / 153.
+    // unpacking x in every block of the other kernel. us there / here, groups of 128, at 32 and at 64 rows of bf16 x: 128256 x 2048 61 /
+    // 106, 110 / 202; 28672 x 4096 36 / 48, 73 / 90; 18432 x 8192 43 / 52, 83 / 97; 17408 x 2048 19 / 19, 25 / 34; 12288 x 4096 23 / 24, 40 / 43;
+    // not there: 8192 x 8192 29 / 27, 57 / 50; 4096 x 14336 33 / 25, 59 / 42. fp32, three columns a row, from smaller matrices on: 16 rows of
+    // 28672 x 4096 34 / 145, 4096 x 14336 31 / 74.
     const int columns = n * (x.type == LL_F32 ? Column<LL_F32>::TERMS : 1);
-    if (y.type == LL_BF16 && columns > 16 && (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS >= 7 * nsm && (x.type == LL_F32 || m.cols <= 6144)) {
+    if (y.type == LL_BF16 && columns > 16 && (m.rows + QM_TILE_ROWS - 1) / QM_TILE_ROWS >= (x.type == LL_F32 ? 1 : 5) * nsm) {
         const int rc = launch_qmat_tc(m, x, n, add, y, nsm, st);
         if (rc != LL_ERR_SHAPE) return rc;
     }

@@ -7,15 +7,16 @@
 // taking the sums of 64 columns of x a group of 128 from tensor memory cost more than these three instructions a code. The
 // roundings add 2e-4 of the outputs' norm to the 1.6e-3 of bf16's own.
 //
-// A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Sixteen warps, in four sets that
+// A block takes 128 rows at a time and walks their columns in tiles of 128, a unit each. Twelve warps, in three sets that
 // take units in turn, unpack 32 rows each from a ring of their own (cp.async) into tensor memory, the products' A operand,
-// a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products; four warps, a row
-// to a thread, take a row block's sums from tensor memory and scale them. Blocks of a cluster share the columns: each
-// row's shares then meet through shared memory.
+// a row to a lane; x stays in shared memory, unpacked once a block, as B. One warp issues the products; eight warps, a row
+// and every other 8 columns to a thread, take a row block's sums from tensor memory and scale them. Blocks of a cluster share
+// the columns: each row's shares then meet through shared memory.
 //
-// 128256 x 2048, 32 rows, 60 us (2.3 TB/s): a unit takes some 820 cycles where its bytes would take 360. Without the products it
-// took 44 us, without the unpacking's arithmetic 48, without storing the outputs 55, with one more unit in flight no less: what the warps
-// wait for is each other, and no one part bounds it. x's staging is 3 to 7 us of a call.
+// 128256 x 2048, 32 rows, 61 us (2.3 TB/s), 64 rows, in clusters of 2, 110: a unit takes some 820 cycles where its bytes would
+// take 360. Without the products it took 44 us, without the unpacking's arithmetic 48, without storing the outputs 55, with one more
+// unit in flight no less: what the warps wait for is each other. The numbers of unpacking sets and of last warps, at 64 rows: 4 and 4
+// 131 us, 4 and 8 115, 3 and 8 110, 3 and 12 114, 2 and 8 111 (at 17 rows 55, 56, 56, 56, 58).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -52,7 +53,7 @@ struct TcArgs {
     int depth;              // units of a warp in flight
 };
 
-constexpr int SETS = 4, UNPACK = 4 * SETS, FLUSH = 4, W_MMA = UNPACK + FLUSH, THREADS = 32 * (W_MMA + 1);
+constexpr int SETS = 3, UNPACK = 4 * SETS, FLUSH = 8, W_MMA = UNPACK + FLUSH, THREADS = 32 * (W_MMA + 1);
 constexpr int MAX_SMEM = 232448 - 2048, MAX_CLUSTER = 8;
 
 // What a block keeps of x, by bytes from `base` on (a 1,024-byte border):
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
             }
         }
     } else {
-        const int row = 32 * q + lane;  // of the row block
+        const int row = 32 * q + lane, part = (warp - UNPACK) / 4;  // of the row block; which of the two warps of these rows
         int done = 0;
         // a row block's outputs, or shares of them, from begin() to end()
         int64_t out = 0;
@@ -580,21 +581,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
                 // this block's eighth (or so) of the tokens, 8 on their way at once
                 const int mine = (held + C - 1) / C, t1 = min(held, (rank + 1) * mine);
 #pragma unroll 1
-                for (int t0 = rank * mine; t0 < t1; t0 += 8) {
+                for (int t0 = rank * mine + 8 * part; t0 < t1; t0 += 2 * FLUSH) {
                     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                     for (int b0 = 0; b0 < C; b0 += 4) {
-                        float part[4][8];
+                        float sh[4][8];
 #pragma unroll
                         for (int b = 0; b < 4; b++) {
                             const uint32_t at = in_block(share + t0 * 512, min(b0 + b, C - 1));
 #pragma unroll
-                            for (int i = 0; i < 8; i++) part[b][i] = load_in(at + min(i, t1 - 1 - t0) * 512);
+                            for (int i = 0; i < 8; i++) sh[b][i] = load_in(at + min(i, t1 - 1 - t0) * 512);
                         }
 #pragma unroll
                         for (int b = 0; b < 4; b++)
 #pragma unroll
-                            for (int i = 0; i < 8; i++) y[i] += b0 + b < C ? part[b][i] : 0.f;
+                            for (int i = 0; i < 8; i++) y[i] += b0 + b < C ? sh[b][i] : 0.f;
                     }
                     uint32_t w[8];
 #pragma unroll
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qmat_tc(const __grid_constant__ 
             const uint32_t from = tmem + i * N + (uint32_t(32 * q) << 16);
             // (a loop and not NC / 8 copies of it: code that runs once a row block comes slower than it runs)
 #pragma unroll 1
-            for (int c = 0; c < NC; c += 8) {
+            for (int c = 8 * part; c < NC; c += 2 * FLUSH) {
                 uint32_t w[8];
                 tm_load8(from + c, w);
                 tm_wait8(w);

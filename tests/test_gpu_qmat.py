@@ -203,7 +203,7 @@ def large_matrix(rows, cols, group, seed):
     return m, m.read(dtype=torch.float32).double()
 
 
-# (from 16 * 7 * 152 rows on bf16 outputs of more than 16 rows of x, 5 of fp32's, take another kernel: row ends inside and at a
+# (from 16 * 5 * 152 rows on bf16 outputs of more than 16 rows of x, 5 of fp32's, take another kernel: row ends inside and at a
 # border of its 128 rows, columns that one block holds, that 2 and, of fp32, 8 share)
 @pytest.mark.parametrize("rows,cols,group", [(17024, 40, 32), (17025, 129, 128), (20000, 1000, 64), (19456, 4096, 128), (17100, 9000, 32), (40000, 2048, 128)])
 @pytest.mark.parametrize("n", [6, 17, 32, 33, 64, 70])
